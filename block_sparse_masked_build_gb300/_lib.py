@@ -70,6 +70,13 @@ class TensorView(ctypes.Structure):
     """bsm_tensor: device data pointer and batch/head/sequence strides."""
     _fields_ = [("data", ctypes.c_void_p), ("strides", ctypes.c_int64 * 3)]
 
+
+class ScoreMod(ctypes.Structure):
+    """bsm_score_mod: cap and per-head slopes of the softmax scores."""
+    _fields_ = [("softcap", ctypes.c_float),
+                ("alibi_slopes", ctypes.c_void_p)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -92,6 +99,13 @@ def _declare(lib):
         c.POINTER(MaskInfoStruct), c.c_void_p, c.c_void_p, c.c_float,
         c.c_int32, c.c_void_p, c.c_void_p, c.c_void_p, c.c_size_t,
         c.c_void_p]
+    lib.bsm_splash_fwd_mod.restype = c.c_int
+    lib.bsm_splash_fwd_mod.argtypes = [
+        c.c_void_p, c.c_void_p, c.c_void_p, I64x3, I64x3, I64x3, I64x3,
+        c.c_int32, c.c_int32, c.c_int32, c.c_int32, c.c_int32, c.c_int32,
+        c.POINTER(MaskInfoStruct), c.c_void_p, c.c_void_p, c.c_float,
+        c.c_int32, c.POINTER(ScoreMod), c.c_void_p, c.c_void_p, c.c_void_p,
+        c.c_size_t, c.c_void_p]
     lib.bsm_splash_fwd_host_bytes.restype = c.c_size_t
     lib.bsm_splash_fwd_host_bytes.argtypes = [
         c.POINTER(MaskSpec), c.c_int32, c.c_int32, c.c_int32, c.c_int32,
@@ -120,6 +134,12 @@ def _declare(lib):
         c.c_int32, c.c_int32, c.c_int32, c.POINTER(MaskInfoStruct),
         c.c_void_p, c.c_void_p, c.c_float, c.c_int32, tv, tv, tv, c.c_void_p,
         c.c_size_t, c.c_void_p]
+    lib.bsm_splash_bwd_mod.restype = c.c_int
+    lib.bsm_splash_bwd_mod.argtypes = [
+        tv, tv, tv, tv, c.c_void_p, tv, c.c_int32, c.c_int32, c.c_int32,
+        c.c_int32, c.c_int32, c.c_int32, c.POINTER(MaskInfoStruct),
+        c.c_void_p, c.c_void_p, c.c_float, c.c_int32, c.POINTER(ScoreMod), tv,
+        tv, tv, c.c_void_p, c.c_size_t, c.c_void_p]
     lib.bsm_pack_dense_mask.restype = c.c_int
     lib.bsm_pack_dense_mask.argtypes = [c.c_void_p, c.c_int64, c.c_int32,
                                         c.c_int32, c.c_void_p, c.c_int32,

@@ -15,7 +15,8 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import MaskInfoStruct, MaskSpec, I64x3, TensorView
+from ._lib import (MaskInfoStruct, MaskSpec, I64x3, ScoreMod,
+                   TensorView)
 
 MASK_CAUSAL = 1
 MASK_LOCAL = 2
@@ -191,20 +192,38 @@ def _default_workspace(device, stream_handle):
     return ws
 
 
+def _score_mod(softcap: float, alibi_slopes, H: int, device):
+    """bsm_score_mod of a cap and per-head slopes, or None for neither."""
+    if alibi_slopes is not None:
+        if (alibi_slopes.dtype != torch.float32
+                or tuple(alibi_slopes.shape) != (H,)
+                or not alibi_slopes.is_contiguous()
+                or alibi_slopes.device != device):
+            raise ValueError("alibi_slopes must be a contiguous float32 "
+                             f"tensor [{H}] on {device}")
+    elif softcap == 0:
+        return None
+    return ScoreMod(float(softcap), _ptr(alibi_slopes))
+
+
 def bsm_splash_fwd(q, k, v, mask_info: MaskInfo, q_segment_ids,
                    kv_segment_ids, scale: float, score: int, out,
-                   lse=None, stream=None, workspace=None) -> None:
-    """q [B,H,Sq,D], k/v [B,H_kv,Skv,D], out [B,H,Sq,D] (bf16, CUDA)."""
+                   lse=None, stream=None, workspace=None,
+                   softcap: float = 0.0, alibi_slopes=None) -> None:
+    """q [B,H,Sq,D], k/v [B,H_kv,Skv,D], out [B,H,Sq,D] (bf16, CUDA).
+    softcap, alibi_slopes: modified softmax scores (bsm_splash_fwd_mod)."""
     B, H, Sq, D = q.shape
     H_kv, Skv = k.shape[1], k.shape[2]
     sh = _stream_handle(stream)
+    mod = _score_mod(softcap, alibi_slopes, H, q.device)
     if workspace is None:
         workspace = _default_workspace(q.device, sh)
-    _check(_lib.lib().bsm_splash_fwd(
+    _check(_lib.lib().bsm_splash_fwd_mod(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), _strides3(q), _strides3(k),
         _strides3(v), _strides3(out), B, H, H_kv, Sq, Skv, D,
         ctypes.byref(mask_info.struct), _ptr(q_segment_ids),
-        _ptr(kv_segment_ids), float(scale), int(score), out.data_ptr(),
+        _ptr(kv_segment_ids), float(scale), int(score),
+        None if mod is None else ctypes.byref(mod), out.data_ptr(),
         _ptr(lse), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), sh))
 
@@ -268,21 +287,25 @@ def bsm_splash_bwd_workspace_bytes(B: int, H: int, Sq: int,
 
 def bsm_splash_bwd(q, k, v, out, lse, dout, mask_info: MaskInfo,
                    q_segment_ids, kv_segment_ids, scale: float, score: int,
-                   dq, dk, dv, stream=None, workspace=None) -> None:
+                   dq, dk, dv, stream=None, workspace=None,
+                   softcap: float = 0.0, alibi_slopes=None) -> None:
     """Gradients of sum(dout * out): dq [B,H,Sq,D], dk/dv [B,H_kv,Skv,D]
-    (bf16, CUDA), from the forward's q, k, v and (softmax) out and lse."""
+    (bf16, CUDA), from the forward's q, k, v and (softmax) out and lse.
+    softcap, alibi_slopes: as given to the forward."""
     B, H, Sq, D = q.shape
     H_kv, Skv = k.shape[1], k.shape[2]
     sh = _stream_handle(stream)
+    mod = _score_mod(softcap, alibi_slopes, H, q.device)
     need = bsm_splash_bwd_workspace_bytes(B, H, Sq, score)
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     views = [_view(t) for t in (q, k, v, out, dout, dq, dk, dv)]
     refs = [None if x is None else ctypes.byref(x) for x in views]
-    _check(_lib.lib().bsm_splash_bwd(
+    _check(_lib.lib().bsm_splash_bwd_mod(
         refs[0], refs[1], refs[2], refs[3], _ptr(lse), refs[4], B, H, H_kv,
         Sq, Skv, D, ctypes.byref(mask_info.struct), _ptr(q_segment_ids),
-        _ptr(kv_segment_ids), float(scale), int(score), refs[5], refs[6],
+        _ptr(kv_segment_ids), float(scale), int(score),
+        None if mod is None else ctypes.byref(mod), refs[5], refs[6],
         refs[7], _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(),
         sh))
@@ -394,11 +417,13 @@ def splash_attention_bwd(q, k, v, out, lse, dout, *,
                          score: int = SCORE_SOFTMAX, block_q: int = 128,
                          block_kv: int = 128,
                          mask_info: MaskInfo | None = None, stream=None,
-                         dense_mask=None):
+                         dense_mask=None, softcap: float = 0.0,
+                         alibi_slopes=None):
     """Backward of :func:`splash_attention` on CUDA tensors: returns
     (dq, dk, dv) for the gradient ``dout`` of the output.  ``out`` and
     ``lse`` are the forward's (softmax path; ignored for the pointwise
-    path)."""
+    path); ``softcap`` and ``alibi_slopes`` as given to it (the slopes are
+    constants and get no gradient)."""
     B, H, Sq, D = q.shape
     Skv = k.shape[2]
     if scale is None:
@@ -417,7 +442,7 @@ def splash_attention_bwd(q, k, v, out, lse, dout, *,
     sm = score == SCORE_SOFTMAX
     bsm_splash_bwd(q, k, v, out if sm else None, lse if sm else None, dout,
                    mask_info, q_segment_ids, kv_segment_ids, scale, score, dq,
-                   dk, dv, stream)
+                   dk, dv, stream, softcap=softcap, alibi_slopes=alibi_slopes)
     return dq, dk, dv
 
 
@@ -470,7 +495,8 @@ def splash_attention(q, k, v, *, mask_flags: int = MASK_CAUSAL,
                      block_q: int = 128, block_kv: int = 128,
                      mask_info: MaskInfo | None = None,
                      return_lse: bool = True, out=None, lse=None,
-                     stream=None, dense_mask=None):
+                     stream=None, dense_mask=None, softcap: float = 0.0,
+                     alibi_slopes=None):
     """Block-sparse masked attention forward, q/k/v [B, H, S, D] bf16.
 
     Defaults follow hstu_ops ``pointwise_splash_attention``: scale =
@@ -482,6 +508,11 @@ def splash_attention(q, k, v, *, mask_flags: int = MASK_CAUSAL,
     ``return_lse`` is False.  ``dense_mask`` (with MASK_DENSE) is a boolean
     [Sq, Skv] tensor, an arbitrary mask shared by every batch row and head;
     it is bit-packed on the device here.
+
+    Modified softmax scores: with x = scale * q.k, ``softcap`` = c > 0 makes
+    the score c * tanh(x / c), and ``alibi_slopes`` (float32 [H], contiguous,
+    on the compute device, or on the host with host inputs) subtracts
+    slopes[h] * |q - k|; the mask comes after both.
     """
     B, H, Sq, D = q.shape
     Skv = k.shape[2]
@@ -491,8 +522,10 @@ def splash_attention(q, k, v, *, mask_flags: int = MASK_CAUSAL,
     dev = torch.device("cuda", torch.cuda.current_device()) if host \
         else q.device
     want_lse = return_lse and score == SCORE_SOFTMAX
-    if host and _can_pipeline(q, k, v, out, lse, q_segment_ids,
-                              kv_segment_ids, stream, mask_info, dense_mask):
+    modified = softcap != 0 or alibi_slopes is not None
+    if host and not modified and _can_pipeline(
+            q, k, v, out, lse, q_segment_ids, kv_segment_ids, stream,
+            mask_info, dense_mask):
         return _splash_host_pipelined(
             q, k, v, mask_flags, window, q_segment_ids, kv_segment_ids,
             scale, score, block_q, block_kv, want_lse, out, lse, stream, dev)
@@ -505,6 +538,8 @@ def splash_attention(q, k, v, *, mask_flags: int = MASK_CAUSAL,
             q_segment_ids.to(dev, non_blocking=nb)
         ks = None if kv_segment_ids is None else \
             kv_segment_ids.to(dev, non_blocking=nb)
+        if alibi_slopes is not None:
+            alibi_slopes = alibi_slopes.to(dev)
     else:
         qd, kd, vd, qs, ks = q, k, v, q_segment_ids, kv_segment_ids
     if mask_info is None:
@@ -521,7 +556,7 @@ def splash_attention(q, k, v, *, mask_flags: int = MASK_CAUSAL,
         ld = torch.empty((B, H, Sq), dtype=torch.float32, device=dev) \
             if (host or lse is None) else lse
     bsm_splash_fwd(qd, kd, vd, mask_info, qs, ks, scale, score, od, ld,
-                   stream)
+                   stream, softcap=softcap, alibi_slopes=alibi_slopes)
     if not host:
         return od, ld
     if out is None:

@@ -188,6 +188,37 @@ bool aligned16(const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
+// The kernels' form of a caller's score modification (mod may be NULL).
+bsm_status check_mod(const bsm_score_mod* mod, float scale, int32_t score,
+                     bsm::ScoreMod* out) {
+  out->kind = 0;
+  out->cap_e = out->cap_log2 = 0.f;
+  out->slopes = nullptr;
+  if (mod == nullptr) return BSM_OK;
+  if (!(mod->softcap >= 0.f) || !std::isfinite(mod->softcap))
+    return fail(BSM_ERR_INVALID_ARG, "softcap must be finite and >= 0");
+  const double log2e = 1.4426950408889634;
+  if (mod->softcap > 0.f) {
+    out->kind |= bsm::kModCap;
+    out->cap_e = static_cast<float>(2.0 * log2e * static_cast<double>(scale) /
+                                    static_cast<double>(mod->softcap));
+    out->cap_log2 =
+        static_cast<float>(static_cast<double>(mod->softcap) * log2e);
+    if (!std::isfinite(out->cap_e) || !std::isfinite(out->cap_log2 * 2.f))
+      return fail(BSM_ERR_INVALID_ARG, "softcap out of range for this scale");
+  }
+  if (mod->alibi_slopes != nullptr) {
+    out->kind |= bsm::kModBias;
+    out->slopes = mod->alibi_slopes;
+  }
+  if (out->kind != 0 && score != BSM_SCORE_SOFTMAX)
+    return fail(BSM_ERR_INVALID_ARG,
+                "softcap and slopes modify softmax scores only");
+  if ((reinterpret_cast<uintptr_t>(mod->alibi_slopes) & 3u) != 0)
+    return fail(BSM_ERR_INVALID_ARG, "alibi_slopes must be 4-byte aligned");
+  return BSM_OK;
+}
+
 // A new epoch for every mask-info build (40 bits, never 0), starting at a
 // value that differs between processes, so that a ticket word left in a
 // reused buffer by an earlier build never matches.
@@ -337,6 +368,25 @@ bsm_status bsm_splash_fwd(const void* q, const void* k, const void* v,
                           int32_t score, void* out, float* lse,
                           void* workspace, size_t workspace_bytes,
                           void* stream) {
+  return bsm_splash_fwd_mod(q, k, v, q_strides, k_strides, v_strides,
+                            o_strides, B, H, H_kv, Sq, Skv, D, info,
+                            q_segment_ids, kv_segment_ids, scale, score,
+                            nullptr, out, lse, workspace, workspace_bytes,
+                            stream);
+}
+
+bsm_status bsm_splash_fwd_mod(const void* q, const void* k, const void* v,
+                              const int64_t q_strides[3],
+                              const int64_t k_strides[3],
+                              const int64_t v_strides[3],
+                              const int64_t o_strides[3], int32_t B, int32_t H,
+                              int32_t H_kv, int32_t Sq, int32_t Skv, int32_t D,
+                              const bsm_mask_info* info,
+                              const int32_t* q_segment_ids,
+                              const int32_t* kv_segment_ids, float scale,
+                              int32_t score, const bsm_score_mod* mod,
+                              void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, void* stream) {
   g_last_error.clear();
   if (B < 0 || H < 0 || H_kv < 0 || Sq < 0 || Skv < 0)
     return fail(BSM_ERR_INVALID_ARG, "negative size");
@@ -352,6 +402,9 @@ bsm_status bsm_splash_fwd(const void* q, const void* k, const void* v,
     return fail(BSM_ERR_INVALID_ARG,
                 "the pointwise score path has no logsumexp; pass lse = NULL");
   if (!std::isfinite(scale)) return fail(BSM_ERR_INVALID_ARG, "scale not finite");
+  bsm::ScoreMod sm_mod;
+  if (const bsm_status ms = check_mod(mod, scale, score, &sm_mod); ms != BSM_OK)
+    return ms;
   if (info == nullptr) return fail(BSM_ERR_INVALID_ARG, "mask info is NULL");
   if (info->Sq != Sq || info->Skv != Skv)
     return fail(BSM_ERR_INVALID_ARG,
@@ -446,6 +499,7 @@ bsm_status bsm_splash_fwd(const void* q, const void* k, const void* v,
   p.dense = (info->flags & BSM_MASK_DENSE) ? info->dense_bits : nullptr;
   p.dense_words = info->dense_row_words;
   p.score = score;
+  p.mod = sm_mod;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.scale = scale;
   p.inv_sq = Sq > 0 ? static_cast<float>(1.0 / static_cast<double>(Sq)) : 0.f;
@@ -535,6 +589,24 @@ bsm_status bsm_splash_bwd(const bsm_tensor* q, const bsm_tensor* k,
                           const bsm_tensor* dk, const bsm_tensor* dv,
                           void* workspace, size_t workspace_bytes,
                           void* stream) {
+  return bsm_splash_bwd_mod(q, k, v, out, lse, dout, B, H, H_kv, Sq, Skv, D,
+                            info, q_segment_ids, kv_segment_ids, scale, score,
+                            nullptr, dq, dk, dv, workspace, workspace_bytes,
+                            stream);
+}
+
+bsm_status bsm_splash_bwd_mod(const bsm_tensor* q, const bsm_tensor* k,
+                              const bsm_tensor* v, const bsm_tensor* out,
+                              const float* lse, const bsm_tensor* dout,
+                              int32_t B, int32_t H, int32_t H_kv, int32_t Sq,
+                              int32_t Skv, int32_t D,
+                              const bsm_mask_info* info,
+                              const int32_t* q_segment_ids,
+                              const int32_t* kv_segment_ids, float scale,
+                              int32_t score, const bsm_score_mod* mod,
+                              const bsm_tensor* dq, const bsm_tensor* dk,
+                              const bsm_tensor* dv, void* workspace,
+                              size_t workspace_bytes, void* stream) {
   g_last_error.clear();
   if (B < 0 || H < 0 || H_kv < 0 || Sq < 0 || Skv < 0)
     return fail(BSM_ERR_INVALID_ARG, "negative size");
@@ -547,6 +619,9 @@ bsm_status bsm_splash_bwd(const bsm_tensor* q, const bsm_tensor* k,
   if (score != BSM_SCORE_SOFTMAX && score != BSM_SCORE_POINTWISE)
     return fail(BSM_ERR_INVALID_ARG, "unknown score path");
   if (!std::isfinite(scale)) return fail(BSM_ERR_INVALID_ARG, "scale not finite");
+  bsm::ScoreMod sm_mod;
+  if (const bsm_status ms = check_mod(mod, scale, score, &sm_mod); ms != BSM_OK)
+    return ms;
   const bool sm = score == BSM_SCORE_SOFTMAX;
   if (q == nullptr || k == nullptr || v == nullptr || dout == nullptr ||
       dq == nullptr || dk == nullptr || dv == nullptr || (sm && out == nullptr))
@@ -646,6 +721,7 @@ bsm_status bsm_splash_bwd(const bsm_tensor* q, const bsm_tensor* k,
   p.dense = (info->flags & BSM_MASK_DENSE) ? info->dense_bits : nullptr;
   p.dense_words = info->dense_row_words;
   p.score = score;
+  p.mod = sm_mod;
   p.scale = scale;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.inv_sq = Sq > 0 ? static_cast<float>(1.0 / static_cast<double>(Sq)) : 0.f;

@@ -11,6 +11,9 @@
 // with x = scale * q.k, sig = logistic(x), p = x sig / Sq (0 where masked),
 //     dV = p^T dO,  dS = (dO V^T) sig (1 + x (1 - sig)) / Sq,
 //     dQ = scale dS K,  dK = scale dS^T Q.
+// Modified softmax scores (ScoreMod): s = cap tanh(x / cap) - slope |q - k|
+// with x = scale * q.k; P and D_q as above, and dS gains the cap's
+// derivative: dS = P * (dO V^T - D_q) * (1 - tanh^2(x / cap)).
 // As in hstu_ops' backward, p (and dS) are rounded to the input type (bf16)
 // for the products; accumulation is f32 in TMEM.
 //
@@ -405,7 +408,7 @@ __device__ __forceinline__ void bwd_mma_role(const BwdParams& p, uint8_t* smem,
 // columns [64, 128).  The packed P and dS of the second half go over
 // columns [32, 64), which the first half reads: the second half writes only
 // after the first half has read (h0_read).
-template <int D, int SCORE, bool DKDV>
+template <int D, int SCORE, int MOD, bool DKDV>
 __device__ __forceinline__ void bwd_elem_role(const BwdParams& p,
                                               BwdBars* bars,
                                               const uint16_t* list,
@@ -482,6 +485,14 @@ __device__ __forceinline__ void bwd_elem_role(const BwdParams& p,
     tc_fence_before();
     if (!DKDV) mbar_arrive(&bars->p_ready);  // S read: the next S may go in
     else if (half == 0) mbar_arrive(&bars->h0_s);
+    // signed distance of the row to the half's first column; the head's
+    // slope (dK/dV: the step's query head)
+    float dist0 = 0.f, slope2 = 0.f;
+    if (MOD & kModBias) {
+      dist0 = static_cast<float>(col0 - row);
+      slope2 = p.mod.slopes[DKDV ? hq_or_hkv * G + it / n_list : hq_or_hkv] *
+               kLog2e;
+    }
     // P, and the per-element factor dS needs: softmax dS = P (dP - D_q),
     // pointwise dS = dP sig (1 + x (1 - sig)) / Sq
     float f[64];
@@ -497,9 +508,30 @@ __device__ __forceinline__ void bwd_elem_role(const BwdParams& p,
         if (SCORE == BSM_SCORE_SOFTMAX) {
           const float l2 = DKDV ? __shfl_sync(0xffffffffu, lse2_c[c], jj)
                                 : lse2_row;
-          const float pr = v ? ex2_approx(fmaf(sv, p.scale_log2, -l2)) : 0.f;
+          float x = 0.f, slope_x = 1.f;
+          if (MOD == 0) {
+            x = fmaf(sv, p.scale_log2, -l2);
+          } else {
+            // the forward's modified score, in log2 units.  With E =
+            // e^(-2 |y|) and r = 1 / (1 + E): |tanh y| = (1 - E) r, and the
+            // cap multiplies dS by its derivative 1 - tanh^2 y = 4 E r^2,
+            // which keeps its relative precision where tanh saturates
+            // (1 - t * t would cancel)
+            if (MOD & kModCap) {
+              const float ee = ex2_approx(-fabsf(sv * p.mod.cap_e));
+              const float r = rcp_approx(1.f + ee);
+              const float t = copysignf((1.f - ee) * r, sv * p.mod.cap_e);
+              x = fmaf(t, p.mod.cap_log2, -l2);
+              slope_x = 4.f * ee * r * r;
+            } else {
+              x = fmaf(sv, p.scale_log2, -l2);
+            }
+            if (MOD & kModBias)
+              x = fmaf(-slope2, fabsf(dist0 + static_cast<float>(j + u)), x);
+          }
+          const float pr = v ? ex2_approx(x) : 0.f;
           pv[u] = pr;
-          f[j + u] = pr;
+          f[j + u] = (MOD & kModCap) ? (v ? pr * slope_x : 0.f) : pr;
         } else {
           const float x = sv * p.scale;
           const float sig = fmaf(0.5f, tanh_approx(0.5f * x), 0.5f);
@@ -623,7 +655,7 @@ __device__ __forceinline__ void bwd_elem_role(const BwdParams& p,
   }
 }
 
-template <int D, int SCORE, bool DKDV>
+template <int D, int SCORE, int MOD, bool DKDV>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     splash_bwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
@@ -707,7 +739,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   } else if (warp == 1) {
     if (n_iter > 0) bwd_mma_role<D, DKDV>(p, smem, bars, tmem, n_iter);
   } else {
-    bwd_elem_role<D, SCORE, DKDV>(p, bars, list, tmem, b, head, fixed_tile,
+    bwd_elem_role<D, SCORE, MOD, DKDV>(p, bars, list, tmem, b, head, fixed_tile,
                                   n_iter);
   }
 
@@ -761,12 +793,12 @@ __global__ void __launch_bounds__(256) bwd_delta_kernel(const BwdParams p) {
   }
 }
 
-template <int D, int SCORE, bool DKDV>
+template <int D, int SCORE, int MOD, bool DKDV>
 cudaError_t launch_bwd_one(const BwdParams& p, const CUtensorMap& tq,
                            const CUtensorMap& tk, const CUtensorMap& tv,
                            const CUtensorMap& tdo, cudaStream_t stream) {
   using C = BwdCfg<D>;
-  auto kern = splash_bwd_kernel<D, SCORE, DKDV>;
+  auto kern = splash_bwd_kernel<D, SCORE, MOD, DKDV>;
   cudaError_t e = cudaFuncSetAttribute(
       kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -792,15 +824,26 @@ cudaError_t launch_bwd_one(const BwdParams& p, const CUtensorMap& tq,
   return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, tdo, p);
 }
 
-template <int D, int SCORE>
+template <int D, int SCORE, int MOD>
 cudaError_t launch_bwd_d(const BwdParams& p, const CUtensorMap& tq,
                          const CUtensorMap& tk, const CUtensorMap& tv,
                          const CUtensorMap& tdo, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
-  if (p.Skv > 0) e = launch_bwd_one<D, SCORE, true>(p, tq, tk, tv, tdo, stream);
+  if (p.Skv > 0) e = launch_bwd_one<D, SCORE, MOD, true>(p, tq, tk, tv, tdo, stream);
   if (e != cudaSuccess) return e;
-  if (p.Sq > 0) e = launch_bwd_one<D, SCORE, false>(p, tq, tk, tv, tdo, stream);
+  if (p.Sq > 0) e = launch_bwd_one<D, SCORE, MOD, false>(p, tq, tk, tv, tdo, stream);
   return e;
+}
+
+template <int SCORE, int MOD>
+cudaError_t launch_bwd_score(const BwdParams& p, const CUtensorMap& tq,
+                             const CUtensorMap& tk, const CUtensorMap& tv,
+                             const CUtensorMap& tdo, cudaStream_t stream) {
+  if (p.D == 128)
+    return launch_bwd_d<128, SCORE, MOD>(p, tq, tk, tv, tdo, stream);
+  if (p.D == 64)
+    return launch_bwd_d<64, SCORE, MOD>(p, tq, tk, tv, tdo, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -823,13 +866,21 @@ cudaError_t launch_splash_bwd(const BwdParams& p, const CUtensorMap& tq,
       if (e != cudaSuccess) return e;
     }
   }
-  const bool pw = p.score == BSM_SCORE_POINTWISE;
-  if (p.D == 128)
-    return pw ? launch_bwd_d<128, BSM_SCORE_POINTWISE>(p, tq, tk, tv, tdo, stream)
-              : launch_bwd_d<128, BSM_SCORE_SOFTMAX>(p, tq, tk, tv, tdo, stream);
-  if (p.D == 64)
-    return pw ? launch_bwd_d<64, BSM_SCORE_POINTWISE>(p, tq, tk, tv, tdo, stream)
-              : launch_bwd_d<64, BSM_SCORE_SOFTMAX>(p, tq, tk, tv, tdo, stream);
+  if (p.score == BSM_SCORE_POINTWISE)
+    return launch_bwd_score<BSM_SCORE_POINTWISE, 0>(p, tq, tk, tv, tdo, stream);
+  switch (p.mod.kind) {
+    case 0:
+      return launch_bwd_score<BSM_SCORE_SOFTMAX, 0>(p, tq, tk, tv, tdo, stream);
+    case kModCap:
+      return launch_bwd_score<BSM_SCORE_SOFTMAX, kModCap>(p, tq, tk, tv, tdo,
+                                                          stream);
+    case kModBias:
+      return launch_bwd_score<BSM_SCORE_SOFTMAX, kModBias>(p, tq, tk, tv, tdo,
+                                                           stream);
+    case kModCap | kModBias:
+      return launch_bwd_score<BSM_SCORE_SOFTMAX, kModCap | kModBias>(
+          p, tq, tk, tv, tdo, stream);
+  }
   return cudaErrorInvalidValue;
 }
 

@@ -641,10 +641,35 @@ __device__ __forceinline__ void mask_tile(float* s, int lo_c, int hi_c,
   }
 }
 
+// Modified scores of one row's 128 columns, in place and in log2 units: from
+// S = q.k to cap * tanh(scale S / cap) (kModCap) or scale S, minus slope *
+// |q - k| (kModBias; slope2 = slope * log2(e)).  tanh(y) = 1 - 2 / (1 +
+// e^(2 y)): exact to a few units of 2^-24 of the cap for every y (tanh.approx
+// is off by up to 2^-11 of its value, which the logsumexp would show), at its
+// limits without a clamp, and NaN stays NaN.
+template <int MOD>
+__device__ __forceinline__ void modify_tile(float* s, const FwdParams& p,
+                                            int kbase, int qrow,
+                                            float slope2) {
+  const float d0 = static_cast<float>(kbase - qrow);
+#pragma unroll
+  for (int c = 0; c < kTileN; ++c) {
+    float x;
+    if (MOD & kModCap)
+      x = fmaf(-2.f * p.mod.cap_log2,
+               rcp_approx(ex2_approx(s[c] * p.mod.cap_e) + 1.f),
+               p.mod.cap_log2);
+    else
+      x = s[c] * p.scale_log2;
+    if (MOD & kModBias) x = fmaf(-slope2, fabsf(d0 + c), x);
+    s[c] = x;
+  }
+}
+
 // KEEP: partial tiles also carry per-element "keep" bits -- from segment ids
 // compared element by element (some key-id row is not sorted) and/or from
 // an arbitrary bit-packed mask; otherwise every mask is a key range per row.
-template <int D, int SCORE, bool KEEP, bool PINGPONG>
+template <int D, int SCORE, int MOD, bool KEEP, bool PINGPONG>
 __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
                                            const uint16_t* lists,
                                            uint32_t tmem) {
@@ -701,6 +726,8 @@ __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
     const int32_t* segk_b =
         seg_elem ? p.kv_seg + static_cast<int64_t>(uc.b) * p.Skv : nullptr;
     float m_used = NEG_INF, l_sum = 0.f;
+    const float slope2 =
+        (MOD & kModBias) ? p.mod.slopes[uc.h] * 1.4426950408889634f : 0.f;
     uint32_t unit_pv = 0;
     bool ok = true;
     for (int e = 0; e < n_ent; ++e) {
@@ -757,6 +784,7 @@ __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
         tmem_ld32(s_addr + q * 32, sraw + q * 32);
       tmem_ld_wait();
       float* s = reinterpret_cast<float*>(sraw);
+      if (MOD != 0) modify_tile<MOD>(s, p, kbase, qrow, slope2);
       if (cls == 1) mask_tile(s, rlo - kbase, rhi - kbase, keep, KEEP);
 
       uint32_t pk[16];
@@ -772,7 +800,7 @@ __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
           mx3 = fmax3(mx3, s[c + 6], s[c + 7]);
         }
         const float mx = fmax3(mx0, mx1, fmaxf(mx2, mx3));
-        const float m_blk = mx * p.scale_log2;
+        const float m_blk = MOD != 0 ? mx : mx * p.scale_log2;
         bool rescale = false;
         float alpha = 1.f;
         if (m_blk > m_used + kRescaleLog2) {
@@ -791,8 +819,13 @@ __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
           for (int c = 32 * q; c < 32 * q + 32; c += 4) {
             // paired f32 FMA/add: the same roundings as one element at a time
             float x0, x1, x2, x3;
-            ffma2(x0, x1, s[c], s[c + 1], p.scale_log2, neg_m);
-            ffma2(x2, x3, s[c + 2], s[c + 3], p.scale_log2, neg_m);
+            if (MOD != 0) {  // already in log2 units
+              fadd2(x0, x1, s[c], s[c + 1], neg_m, neg_m);
+              fadd2(x2, x3, s[c + 2], s[c + 3], neg_m, neg_m);
+            } else {
+              ffma2(x0, x1, s[c], s[c + 1], p.scale_log2, neg_m);
+              ffma2(x2, x3, s[c + 2], s[c + 3], p.scale_log2, neg_m);
+            }
             const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
             const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
             fadd2(ls0, ls1, ls0, ls1, p0, p1);
@@ -930,7 +963,7 @@ __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
   }
 }
 
-template <int D, int SCORE, bool PINGPONG>
+template <int D, int SCORE, int MOD, bool PINGPONG>
 __global__ void __launch_bounds__(kThreads, 1)
     splash_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
@@ -996,9 +1029,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // thread).  The alternating-turn instance is never launched for either.
     if (!PINGPONG && (((p.flags & BSM_MASK_SEGMENT) && (*p.seg_flags & 1) != 0) ||
                       p.dense != nullptr))
-      score_role<D, SCORE, !PINGPONG, PINGPONG>(p, bars, lists, tmem);
+      score_role<D, SCORE, MOD, !PINGPONG, PINGPONG>(p, bars, lists, tmem);
     else
-      score_role<D, SCORE, false, PINGPONG>(p, bars, lists, tmem);
+      score_role<D, SCORE, MOD, false, PINGPONG>(p, bars, lists, tmem);
   }
 
   tc_fence_before();
@@ -1360,7 +1393,7 @@ __device__ __forceinline__ void dt_mma_role(const FwdParams& p, uint8_t* smem,
   __syncwarp();
 }
 
-template <int SCORE, bool KEEP, bool TRACE>
+template <int SCORE, int MOD, bool KEEP, bool TRACE>
 __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
                                               const uint16_t* lists,
                                               uint32_t tmem, const int t) {
@@ -1412,6 +1445,8 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
     const int32_t* segk_b =
         seg_elem ? p.kv_seg + static_cast<int64_t>(uc.b) * p.Skv : nullptr;
     float m_used = NEG_INF, l_sum = 0.f;
+    const float slope2 =
+        (MOD & kModBias) ? p.mod.slopes[uc.h] * 1.4426950408889634f : 0.f;
     uint32_t unit_pv = 0;
     bool ok = true;
     for (int e = 0; e < n_ent; ++e) {
@@ -1448,6 +1483,7 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
         tmem_ld32(s_addr + q * 32, sraw + q * 32);
       tmem_ld_wait();
       float* s = reinterpret_cast<float*>(sraw);
+      if (MOD != 0) modify_tile<MOD>(s, p, kbase, qrow, slope2);
       if (cls == 1) mask_tile(s, rlo - kbase, rhi - kbase, keep, KEEP);
 
       uint32_t pk[16];
@@ -1463,7 +1499,7 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
           mx3 = fmax3(mx3, s[c + 6], s[c + 7]);
         }
         const float mx = fmax3(mx0, mx1, fmaxf(mx2, mx3));
-        const float m_blk = mx * p.scale_log2;
+        const float m_blk = MOD != 0 ? mx : mx * p.scale_log2;
         bool rescale = false;
         float alpha = 1.f;
         if (m_blk > m_used + kRescaleLog2) {
@@ -1482,8 +1518,13 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
           for (int c = 32 * q; c < 32 * q + 32; c += 4) {
             // paired f32 FMA/add: the same roundings as one element at a time
             float x0, x1, x2, x3;
-            ffma2(x0, x1, s[c], s[c + 1], p.scale_log2, neg_m);
-            ffma2(x2, x3, s[c + 2], s[c + 3], p.scale_log2, neg_m);
+            if (MOD != 0) {  // already in log2 units
+              fadd2(x0, x1, s[c], s[c + 1], neg_m, neg_m);
+              fadd2(x2, x3, s[c + 2], s[c + 3], neg_m, neg_m);
+            } else {
+              ffma2(x0, x1, s[c], s[c + 1], p.scale_log2, neg_m);
+              ffma2(x2, x3, s[c + 2], s[c + 3], p.scale_log2, neg_m);
+            }
             const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
             const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
             fadd2(ls0, ls1, ls0, ls1, p0, p1);
@@ -1618,7 +1659,7 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
 }
 
 
-template <int SCORE, bool TRACE>
+template <int SCORE, int MOD, bool TRACE>
 __global__ void __launch_bounds__(kDtThreads, 1)
     splash_fwd_dt_kernel(const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k,
@@ -1683,9 +1724,9 @@ __global__ void __launch_bounds__(kDtThreads, 1)
     // arbitrary mask is given (read once; the same for every thread)
     if (((p.flags & BSM_MASK_SEGMENT) && (*p.seg_flags & 1) != 0) ||
         p.dense != nullptr)
-      dt_score_role<SCORE, true, TRACE>(p, bars, lt, tmem, t);
+      dt_score_role<SCORE, MOD, true, TRACE>(p, bars, lt, tmem, t);
     else
-      dt_score_role<SCORE, false, TRACE>(p, bars, lt, tmem, t);
+      dt_score_role<SCORE, MOD, false, TRACE>(p, bars, lt, tmem, t);
   }
 
   tc_fence_before();
@@ -1701,13 +1742,13 @@ __global__ void __launch_bounds__(kDtThreads, 1)
   }
 }
 
-template <int SCORE>
+template <int SCORE, int MOD>
 cudaError_t launch_dt(const FwdParams& p, const CUtensorMap& tq,
                       const CUtensorMap& tk, const CUtensorMap& tv, int grid,
                       cudaStream_t stream) {
   // the instance that records the event trace is launched only with one
-  auto kern = p.trace != nullptr ? splash_fwd_dt_kernel<SCORE, true>
-                                 : splash_fwd_dt_kernel<SCORE, false>;
+  auto kern = p.trace != nullptr ? splash_fwd_dt_kernel<SCORE, MOD, true>
+                                 : splash_fwd_dt_kernel<SCORE, MOD, false>;
   cudaFuncAttributes attr;
   cudaError_t e = cudaFuncGetAttributes(&attr, kern);
   if (e != cudaSuccess) return e;
@@ -1719,12 +1760,12 @@ cudaError_t launch_dt(const FwdParams& p, const CUtensorMap& tq,
   return cudaGetLastError();
 }
 
-template <int D, int SCORE, bool PINGPONG>
+template <int D, int SCORE, int MOD, bool PINGPONG>
 cudaError_t launch_one(const FwdParams& p, const CUtensorMap& tq,
                        const CUtensorMap& tk, const CUtensorMap& tv,
                        int grid, cudaStream_t stream) {
   using C = Cfg<D>;
-  auto kern = splash_fwd_kernel<D, SCORE, PINGPONG>;
+  auto kern = splash_fwd_kernel<D, SCORE, MOD, PINGPONG>;
   cudaFuncAttributes attr;
   cudaError_t e = cudaFuncGetAttributes(&attr, kern);
   if (e != cudaSuccess) return e;
@@ -1736,6 +1777,35 @@ cudaError_t launch_one(const FwdParams& p, const CUtensorMap& tq,
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
+}
+
+// The instances of one score path (SCORE and, for the softmax, the kind of
+// modified scores MOD).
+template <int SCORE, int MOD>
+cudaError_t launch_score(const FwdParams& p, const CUtensorMap& tq,
+                         const CUtensorMap& tk, const CUtensorMap& tv,
+                         int grid, cudaStream_t stream) {
+  // Softmax turns alternate between the tiles only where work units are
+  // long: no segment ids and at least 4096 keys.  Packed sequences and
+  // short sequences give short units, where the alternation costs more
+  // than it saves.  Arbitrary masks take the other instance too, which
+  // keeps the alternating one free of per-element keep bits; head dim 64
+  // is built without it.
+  const bool pp = (p.flags & BSM_MASK_SEGMENT) == 0 && p.Skv >= 4096 &&
+                  p.dense == nullptr && p.D == 128;
+  // Packed sequences (segment ids, no arbitrary mask) at head dim 128 take
+  // the kernel with decoupled query tiles, and so do the other masks below
+  // 4096 keys (causal S=2048: 11 % faster there; from 4096 keys on, the
+  // lockstep kernel's shared K/V stream is 2-6 % faster).
+  const bool dt = p.dense == nullptr && p.D == 128 &&
+                  ((p.flags & BSM_MASK_SEGMENT) != 0 || p.Skv < 4096);
+  if (dt) return launch_dt<SCORE, MOD>(p, tq, tk, tv, grid, stream);
+  if (p.D == 128)
+    return pp ? launch_one<128, SCORE, MOD, true>(p, tq, tk, tv, grid, stream)
+              : launch_one<128, SCORE, MOD, false>(p, tq, tk, tv, grid, stream);
+  if (p.D == 64)  // head dim 64 uses the instance without alternation
+    return launch_one<64, SCORE, MOD, false>(p, tq, tk, tv, grid, stream);
+  return cudaErrorInvalidValue;
 }
 
 // Self test of the bounded wait: nothing ever arrives on this barrier.
@@ -1764,34 +1834,20 @@ cudaError_t launch_splash_fwd(const FwdParams& p, const CUtensorMap& tq,
                               const CUtensorMap& tk, const CUtensorMap& tv,
                               int num_sms, cudaStream_t stream) {
   const int grid = fwd_grid_size(p, num_sms);
-  const bool pw = p.score == BSM_SCORE_POINTWISE;
-  // Softmax turns alternate between the tiles only where work units are
-  // long: no segment ids and at least 4096 keys.  Packed sequences and
-  // short sequences give short units, where the alternation costs more
-  // than it saves.  Arbitrary masks take the other instance too, which
-  // keeps the alternating one free of per-element keep bits; head dim 64
-  // is built without it.
-  const bool pp = (p.flags & BSM_MASK_SEGMENT) == 0 && p.Skv >= 4096 &&
-                  p.dense == nullptr && p.D == 128;
-  // Packed sequences (segment ids, no arbitrary mask) at head dim 128 take
-  // the kernel with decoupled query tiles, and so do the other masks below
-  // 4096 keys (causal S=2048: 11 % faster there; from 4096 keys on, the
-  // lockstep kernel's shared K/V stream is 2-6 % faster).
-  const bool dt = p.dense == nullptr && p.D == 128 &&
-                  ((p.flags & BSM_MASK_SEGMENT) != 0 || p.Skv < 4096);
-  if (dt)
-    return pw ? launch_dt<BSM_SCORE_POINTWISE>(p, tq, tk, tv, grid, stream)
-              : launch_dt<BSM_SCORE_SOFTMAX>(p, tq, tk, tv, grid, stream);
-  if (p.D == 128) {
-    if (pw)
-      return pp ? launch_one<128, BSM_SCORE_POINTWISE, true>(p, tq, tk, tv, grid, stream)
-                : launch_one<128, BSM_SCORE_POINTWISE, false>(p, tq, tk, tv, grid, stream);
-    return pp ? launch_one<128, BSM_SCORE_SOFTMAX, true>(p, tq, tk, tv, grid, stream)
-              : launch_one<128, BSM_SCORE_SOFTMAX, false>(p, tq, tk, tv, grid, stream);
-  }
-  if (p.D == 64) {  // head dim 64 uses the instance without alternation
-    return pw ? launch_one<64, BSM_SCORE_POINTWISE, false>(p, tq, tk, tv, grid, stream)
-              : launch_one<64, BSM_SCORE_SOFTMAX, false>(p, tq, tk, tv, grid, stream);
+  if (p.score == BSM_SCORE_POINTWISE)
+    return launch_score<BSM_SCORE_POINTWISE, 0>(p, tq, tk, tv, grid, stream);
+  switch (p.mod.kind) {
+    case 0:
+      return launch_score<BSM_SCORE_SOFTMAX, 0>(p, tq, tk, tv, grid, stream);
+    case kModCap:
+      return launch_score<BSM_SCORE_SOFTMAX, kModCap>(p, tq, tk, tv, grid,
+                                                      stream);
+    case kModBias:
+      return launch_score<BSM_SCORE_SOFTMAX, kModBias>(p, tq, tk, tv, grid,
+                                                       stream);
+    case kModCap | kModBias:
+      return launch_score<BSM_SCORE_SOFTMAX, kModCap | kModBias>(
+          p, tq, tk, tv, grid, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -53,6 +53,16 @@ struct MaskInfoParams {
   unsigned long long epoch;  // 1 .. 2^40 - 1, new for every build
 };
 
+// Modified softmax scores: with x = scale * q.k, z = cap * tanh(x / cap) (or
+// x), minus slope_h * |q - k|.  All in log2 units, as the kernels use them.
+constexpr int kModCap = 1, kModBias = 2;
+struct ScoreMod {
+  int32_t kind;         // kModCap | kModBias; 0 = unmodified scores
+  float cap_e;          // 2 log2(e) scale / cap: tanh from exp2(cap_e * q.k)
+  float cap_log2;       // cap * log2(e)
+  const float* slopes;  // [H], or null
+};
+
 struct FwdParams {
   int32_t B, H, Hkv, Sq, Skv, D;
   int32_t n_super;    // ceil(Sq / 256)
@@ -77,6 +87,7 @@ struct FwdParams {
   float inv_sq;      // pointwise: 1 / Sq
   float pw_half;     // pointwise: scale / 2
   float pw_g;        // pointwise: scale / (2 Sq)
+  ScoreMod mod;      // softmax: cap and distance bias
   // outputs
   uint16_t* out;  // bf16 bits
   int64_t o_sb, o_sh, o_ss;
@@ -104,6 +115,7 @@ struct BwdParams {
   // scores
   int32_t score;
   float scale, scale_log2, inv_sq;
+  ScoreMod mod;      // softmax: cap and distance bias
   const float* lse;  // forward logsumexp [B][H][Sq] (softmax)
   float* delta;      // workspace: D_q = sum_d dO * out, [B][H][Sq] (softmax)
   const uint16_t* out;   // forward output (softmax), bf16

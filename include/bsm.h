@@ -210,6 +210,40 @@ bsm_status bsm_splash_fwd(const void* q, const void* k, const void* v,
                           void* workspace, size_t workspace_bytes,
                           void* stream);
 
+/* Modified softmax scores: with x = scale * q.k, the logit of a visible key is
+ *     z = softcap * tanh(x / softcap)   (softcap > 0; else z = x)
+ *     z -= alibi_slopes[h] * |q - k|    (alibi_slopes != NULL)
+ * with q, k the row's and the key's positions and h the query head.  The mask
+ * is applied after both.  These scores have no counterpart on the pages.
+ *   softcap       0 (no cap) or positive, with scale / softcap finite in f32
+ *   alibi_slopes  device f32 [H], contiguous, finite, of any sign, or NULL;
+ *                 read by the kernels (not checked).  Constants: the backward
+ *                 gives them no gradient
+ * tanh is computed as 1 - 2 / (1 + e^(2 x / softcap)) in f32, and the bias is
+ * added in f32: a logit carries about 2^-24 of softcap and of the bias. */
+typedef struct bsm_score_mod {
+  float softcap;
+  const float* alibi_slopes;
+} bsm_score_mod;
+
+/* bsm_splash_fwd with modified softmax scores: the same arguments, checks and
+ * kernels, plus `mod` (NULL, or with softcap 0 and no slopes: exactly
+ * bsm_splash_fwd).  A NaN or negative softcap, an overflowing scale / softcap,
+ * or a modification on the pointwise score path returns
+ * BSM_ERR_INVALID_ARG. */
+bsm_status bsm_splash_fwd_mod(const void* q, const void* k, const void* v,
+                              const int64_t q_strides[3],
+                              const int64_t k_strides[3],
+                              const int64_t v_strides[3],
+                              const int64_t o_strides[3], int32_t B, int32_t H,
+                              int32_t H_kv, int32_t Sq, int32_t Skv, int32_t D,
+                              const bsm_mask_info* info,
+                              const int32_t* q_segment_ids,
+                              const int32_t* kv_segment_ids, float scale,
+                              int32_t score, const bsm_score_mod* mod,
+                              void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* Bytes of the forward's device workspace (about 6 MiB): the work-unit
  * counter and each CTA's lists of the KV tiles of its next units.  The
  * counter is zeroed on `stream` before each launch; the launch overwrites
@@ -351,6 +385,25 @@ bsm_status bsm_splash_bwd(const bsm_tensor* q, const bsm_tensor* k,
                           void* workspace, size_t workspace_bytes,
                           void* stream);
 
+/* bsm_splash_bwd with modified softmax scores (see bsm_score_mod): the same
+ * arguments and checks plus the `mod` given to the forward.  With
+ * t = tanh(x / softcap), P = exp(z - lse) over the visible keys and D_q as
+ * above: dV = P^T dout, dS = P * (dout V^T - D_q) * (1 - t^2) (no factor
+ * without a cap), dQ = scale dS K, dK = scale dS^T Q.  The slopes get no
+ * gradient. */
+bsm_status bsm_splash_bwd_mod(const bsm_tensor* q, const bsm_tensor* k,
+                              const bsm_tensor* v, const bsm_tensor* out,
+                              const float* lse, const bsm_tensor* dout,
+                              int32_t B, int32_t H, int32_t H_kv, int32_t Sq,
+                              int32_t Skv, int32_t D,
+                              const bsm_mask_info* info,
+                              const int32_t* q_segment_ids,
+                              const int32_t* kv_segment_ids, float scale,
+                              int32_t score, const bsm_score_mod* mod,
+                              const bsm_tensor* dq, const bsm_tensor* dk,
+                              const bsm_tensor* dv, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* Synchronise `stream` and report whether a kernel of this library gave up
  * on a bounded wait since the last call (then BSM_ERR_DEVICE_TIMEOUT; the
  * affected outputs are undefined, the CUDA context stays usable).  If
@@ -383,7 +436,9 @@ const char* bsm_last_error(void);
 /* ABI version (major*10000 + minor*100 + patch): 302 = 0.3.2, adding
  * bsm_splash_fwd_host and bsm_splash_fwd_host_bytes to 0.3.1 (which added
  * bsm_pack_dense_mask to 0.3.0: the backward entry points and bsm_tensor
- * added to 0.2.0's forward, mask spec and mask info). */
+ * added to 0.2.0's forward, mask spec and mask info).  Entry points added
+ * since, with structs of their own, leave the number as it is: callers of
+ * 302 are served unchanged. */
 int32_t bsm_version(void);
 
 #ifdef __cplusplus
