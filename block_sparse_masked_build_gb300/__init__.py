@@ -14,12 +14,16 @@ from .api import (  # noqa: F401
     SCORE_POINTWISE,
     SCORE_SOFTMAX,
     BsmError,
+    KVCache,
     MaskInfo,
     bsm_build_mask_info,
     bsm_device_status,
+    bsm_kv_append,
     bsm_last_error,
     bsm_mask_info_bytes,
     bsm_pack_dense_mask,
+    bsm_paged_attention,
+    bsm_paged_attention_workspace_bytes,
     bsm_selftest_wait_timeout,
     bsm_splash_bwd,
     bsm_splash_bwd_workspace_bytes,
@@ -29,7 +33,9 @@ from .api import (  # noqa: F401
     bsm_splash_fwd_workspace_bytes,
     bsm_version,
     build_mask_info,
+    kv_append,
     pack_dense_mask,
+    paged_attention,
     splash_attention,
     splash_attention_bwd,
 )

@@ -77,6 +77,14 @@ class ScoreMod(ctypes.Structure):
                 ("alibi_slopes", ctypes.c_void_p)]
 
 
+class KVCacheStruct(ctypes.Structure):
+    """bsm_kv_cache: pages of e4m3 codes and their scales."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("D", ctypes.c_int32)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -144,6 +152,18 @@ def _declare(lib):
     lib.bsm_pack_dense_mask.argtypes = [c.c_void_p, c.c_int64, c.c_int32,
                                         c.c_int32, c.c_void_p, c.c_int32,
                                         c.c_void_p]
+    kc = c.POINTER(KVCacheStruct)
+    lib.bsm_kv_append.restype = c.c_int
+    lib.bsm_kv_append.argtypes = [
+        kc, c.c_void_p, c.c_int64, c.c_int32, c.c_void_p, c.c_void_p, tv, tv,
+        c.c_int32, c.c_int32, c.c_void_p]
+    lib.bsm_paged_attention_workspace_bytes.restype = c.c_size_t
+    lib.bsm_paged_attention_workspace_bytes.argtypes = [c.c_int32] * 5
+    lib.bsm_paged_attention.restype = c.c_int
+    lib.bsm_paged_attention.argtypes = [
+        tv, kc, c.c_void_p, c.c_int64, c.c_int32, c.c_void_p, c.c_int32,
+        c.c_int32, c.c_int32, c.c_float, c.c_int32, c.POINTER(ScoreMod), tv,
+        c.c_void_p, c.c_void_p, c.c_size_t, c.c_void_p]
     lib.bsm_device_status.restype = c.c_int
     lib.bsm_device_status.argtypes = [c.c_void_p, c.POINTER(c.c_int32)]
     lib.bsm_selftest_wait_timeout.restype = c.c_int

@@ -8,6 +8,7 @@ torch for device memory, pinned host memory and streams.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from dataclasses import dataclass
@@ -15,7 +16,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import (MaskInfoStruct, MaskSpec, I64x3, ScoreMod,
+from ._lib import (I64x3, KVCacheStruct, MaskInfoStruct, MaskSpec, ScoreMod,
                    TensorView)
 
 MASK_CAUSAL = 1
@@ -45,6 +46,14 @@ def _stream_handle(stream) -> int | None:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _on_device(dev):
+    """Makes dev the current device for a call (CUDA's launches and the
+    current stream go by it); nothing to do where it is already."""
+    if dev.type != "cuda" or dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
 
 
 def _ptr(t) -> int | None:
@@ -311,6 +320,135 @@ def bsm_splash_bwd(q, k, v, out, lse, dout, mask_info: MaskInfo,
         sh))
 
 
+class KVCache:
+    """A paged 8-bit key/value cache over four CUDA tensors, which it keeps:
+    k_pages, v_pages [num_pages, H_kv, page_size, D] (float8_e4m3fn) and
+    k_scale, v_scale [num_pages, H_kv] (float32), all contiguous.  An element
+    is its code times the scale of its page and head."""
+
+    __slots__ = ("k_pages", "v_pages", "k_scale", "v_scale", "struct")
+
+    def __init__(self, k_pages, v_pages, k_scale, v_scale):
+        n, H_kv, P, D = k_pages.shape
+        for t in (k_pages, v_pages):
+            if (t.dtype != torch.float8_e4m3fn or t.shape != (n, H_kv, P, D)
+                    or not t.is_contiguous()
+                    or t.device != k_pages.device):
+                raise ValueError("k_pages and v_pages must be contiguous "
+                                 "float8_e4m3fn tensors of one shape "
+                                 "[num_pages, H_kv, page_size, D] on one "
+                                 "device")
+        for t in (k_scale, v_scale):
+            if (t.dtype != torch.float32 or t.shape != (n, H_kv)
+                    or not t.is_contiguous()
+                    or t.device != k_pages.device):
+                raise ValueError("k_scale and v_scale must be contiguous "
+                                 "float32 tensors [num_pages, H_kv] beside "
+                                 "the pages")
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.struct = KVCacheStruct(k_pages.data_ptr(), v_pages.data_ptr(),
+                                    k_scale.data_ptr(), v_scale.data_ptr(),
+                                    n, H_kv, P, D)
+
+    @classmethod
+    def empty(cls, num_pages: int, H_kv: int, page_size: int, D: int,
+              device="cuda") -> "KVCache":
+        """A cache of unwritten pages."""
+        pages = [torch.empty((num_pages, H_kv, page_size, D),
+                             dtype=torch.float8_e4m3fn, device=device)
+                 for _ in range(2)]
+        scales = [torch.ones((num_pages, H_kv), device=device)
+                  for _ in range(2)]
+        return cls(*pages, *scales)
+
+
+def _check_table(cache: KVCache, page_table, B: int, **ints) -> None:
+    dev = cache.k_pages.device
+    if (page_table.dtype != torch.int32 or page_table.dim() != 2
+            or page_table.shape[0] != B or page_table.device != dev
+            or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+        raise ValueError("page_table must be an int32 tensor [B, max_pages] "
+                         "with contiguous rows, beside the cache")
+    for name, t in ints.items():
+        if t is not None and (t.dtype != torch.int32 or t.shape != (B,)
+                              or not t.is_contiguous() or t.device != dev):
+            raise ValueError(f"{name} must be a contiguous int32 tensor [B] "
+                             "beside the cache")
+
+
+def _check_tokens(t, shape, dev, name: str):
+    if t.dtype != torch.bfloat16 or t.shape != shape or t.device != dev:
+        raise ValueError(f"{name} must be a bfloat16 tensor "
+                         f"{list(shape)} beside the cache")
+    return TensorView(t.data_ptr(), _strides3(t))
+
+
+def bsm_kv_append(cache: KVCache, page_table, lens, k_new, v_new, n_new=None,
+                  stream=None) -> None:
+    """Append k_new, v_new [B,H_kv,T,D] (bf16, any strides that are multiples
+    of 8) to sequences of lens [B] tokens, n_new [B] of them each (None: T).
+    page_table int32 [B, max_pages]; lens is left as it is."""
+    s = cache.struct
+    if k_new.dim() != 4:
+        raise ValueError("k_new must be [B, H_kv, T, D]")
+    B, T = k_new.shape[0], k_new.shape[2]
+    dev = cache.k_pages.device
+    _check_table(cache, page_table, B, lens=lens, n_new=n_new)
+    shape = (B, s.H_kv, T, s.D)
+    kt = _check_tokens(k_new, shape, dev, "k_new")
+    vt = _check_tokens(v_new, shape, dev, "v_new")
+    with _on_device(dev):
+        _check(_lib.lib().bsm_kv_append(
+            ctypes.byref(s), page_table.data_ptr(), page_table.stride(0),
+            page_table.shape[1], lens.data_ptr(), _ptr(n_new),
+            ctypes.byref(kt), ctypes.byref(vt), B, T,
+            _stream_handle(stream)))
+
+
+def bsm_paged_attention_workspace_bytes(B: int, H: int, H_kv: int, T: int,
+                                        D: int) -> int:
+    return int(_lib.lib().bsm_paged_attention_workspace_bytes(B, H, H_kv, T,
+                                                              D))
+
+
+def bsm_paged_attention(q, cache: KVCache, page_table, lens, scale: float,
+                        out, lse=None, window: int = 0, softcap: float = 0.0,
+                        alibi_slopes=None, stream=None,
+                        workspace=None) -> None:
+    """q, out [B,H,T,D] (bf16): the last T of each sequence's lens [B]
+    tokens attend to the cache; lse [B,H,T] (f32, contiguous) or None."""
+    s = cache.struct
+    if q.dim() != 4:
+        raise ValueError("q must be [B, H, T, D]")
+    B, H, T, D = q.shape
+    dev = cache.k_pages.device
+    _check_table(cache, page_table, B, lens=lens)
+    shape = (B, H, T, s.D)
+    qt = _check_tokens(q, shape, dev, "q")
+    ot = _check_tokens(out, shape, dev, "out")
+    if lse is not None and (lse.dtype != torch.float32
+                            or lse.shape != (B, H, T) or lse.device != dev
+                            or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 tensor [B, H, T] "
+                         "beside the cache")
+    mod = _score_mod(softcap, alibi_slopes, H, dev)
+    with _on_device(dev):
+        sh = _stream_handle(stream)
+        if workspace is None:
+            need = bsm_paged_attention_workspace_bytes(B, H, s.H_kv, T, D)
+            if need > 0:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        _check(_lib.lib().bsm_paged_attention(
+            ctypes.byref(qt), ctypes.byref(s), page_table.data_ptr(),
+            page_table.stride(0), page_table.shape[1], lens.data_ptr(), B, H,
+            T, float(scale), int(window),
+            None if mod is None else ctypes.byref(mod), ctypes.byref(ot),
+            _ptr(lse), _ptr(workspace),
+            0 if workspace is None
+            else workspace.numel() * workspace.element_size(), sh))
+
+
 def bsm_device_status(stream=None) -> tuple[int, list[int]]:
     detail = (ctypes.c_int32 * 4)()
     st = _lib.lib().bsm_device_status(_stream_handle(stream), detail)
@@ -408,6 +546,40 @@ def pack_dense_mask(mask: torch.Tensor, stream=None) -> torch.Tensor:
                         device=mask.device)
     bsm_pack_dense_mask(mask, words, stream)
     return words
+
+
+def kv_append(cache: KVCache, page_table, lens, k_new, v_new, *, n_new=None,
+              stream=None) -> None:
+    """Append new tokens' keys and values (bf16 [B, H_kv, T, D]) to the 8-bit
+    cache: sequence b, which holds lens[b] tokens, gets its first n_new[b]
+    (None: all T).  One scale per page and head, a power of two; a page that
+    already holds tokens keeps or raises its scale (include/bsm.h has the
+    rule).  ``lens`` is not changed: advance it before attending."""
+    bsm_kv_append(cache, page_table, lens, k_new, v_new, n_new, stream)
+
+
+def paged_attention(q, cache: KVCache, page_table, lens, *,
+                    scale: float | None = None, window: int = 0,
+                    softcap: float = 0.0, alibi_slopes=None,
+                    return_lse: bool = True, out=None, lse=None, stream=None):
+    """Causal attention of q [B, H, T, D] (bf16), the last T tokens of each
+    sequence, over the cache's lens[b] tokens (the queries' own among them).
+
+    ``window`` > 0 keeps the last ``window`` keys of each query; scale,
+    ``softcap`` and ``alibi_slopes`` as in :func:`splash_attention`.  Rows
+    that see no key are 0 with logsumexp -inf.  Returns (out, lse)."""
+    B, H, T, D = q.shape
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty((B, H, T, D), dtype=torch.bfloat16, device=q.device)
+    if not return_lse:
+        lse = None
+    elif lse is None:
+        lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
+    bsm_paged_attention(q, cache, page_table, lens, scale, out, lse, window,
+                        softcap, alibi_slopes, stream)
+    return out, lse
 
 
 def splash_attention_bwd(q, k, v, out, lse, dout, *,

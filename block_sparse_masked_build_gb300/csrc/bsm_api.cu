@@ -219,6 +219,61 @@ bsm_status check_mod(const bsm_score_mod* mod, float scale, int32_t score,
   return BSM_OK;
 }
 
+// Shape of a cache, its page table and a batch of B sequences with T tokens.
+bsm_status check_cache(const bsm_kv_cache* c, int64_t table_stride,
+                       int32_t max_pages, int32_t B, int32_t T) {
+  if (c == nullptr) return fail(BSM_ERR_INVALID_ARG, "cache is NULL");
+  if (B < 0 || T < 0 || max_pages < 0 || c->num_pages < 0 || c->H_kv < 0)
+    return fail(BSM_ERR_INVALID_ARG, "negative size");
+  if (c->D != 64 && c->D != 128)
+    return fail(BSM_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 &&
+      c->page_size != 128)
+    return fail(BSM_ERR_UNSUPPORTED, "page_size must be 16, 32, 64 or 128");
+  if (B > 65535 || c->H_kv > 32767)
+    return fail(BSM_ERR_UNSUPPORTED, "too many sequences or heads");
+  if (T > (1 << 24) ||
+      static_cast<int64_t>(max_pages) * c->page_size > (1 << 30))
+    return fail(BSM_ERR_UNSUPPORTED, "more than 2^30 tokens per sequence");
+  if (B > 1 && table_stride < max_pages)
+    return fail(BSM_ERR_INVALID_ARG, "table_stride must be >= max_pages");
+  return BSM_OK;
+}
+
+bsm_status check_cache_memory(const bsm_kv_cache* c, const int32_t* table,
+                              int32_t max_pages, const int32_t* lens) {
+  if (lens == nullptr || (reinterpret_cast<uintptr_t>(lens) & 3u) != 0)
+    return fail(BSM_ERR_INVALID_ARG, "lens must be non-NULL, 4-byte aligned");
+  if ((table == nullptr && max_pages > 0) ||
+      (reinterpret_cast<uintptr_t>(table) & 3u) != 0)
+    return fail(BSM_ERR_INVALID_ARG,
+                "page_table must be non-NULL, 4-byte aligned");
+  if (c->k == nullptr || c->v == nullptr || !aligned16(c->k) || !aligned16(c->v))
+    return fail(BSM_ERR_INVALID_ARG,
+                "the cache's pages must be non-NULL and 16-byte aligned");
+  if (c->k_scale == nullptr || c->v_scale == nullptr ||
+      (reinterpret_cast<uintptr_t>(c->k_scale) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(c->v_scale) & 3u) != 0)
+    return fail(BSM_ERR_INVALID_ARG,
+                "the cache's scales must be non-NULL, 4-byte aligned");
+  return BSM_OK;
+}
+
+// A [B][heads][S][D] view: aligned data, positive strides, multiples of 8.
+bsm_status check_view(const bsm_tensor* t, int64_t B, int64_t heads, int64_t S,
+                      const char* name) {
+  if (t->data == nullptr || !aligned16(t->data))
+    return fail(BSM_ERR_INVALID_ARG,
+                std::string(name) + " must be non-NULL and 16-byte aligned");
+  const int64_t sizes[3] = {B, heads, S};
+  for (int d = 0; d < 3; ++d)
+    if (sizes[d] > 1 && (t->strides[d] <= 0 || t->strides[d] % 8 != 0))
+      return fail(BSM_ERR_INVALID_ARG,
+                  std::string(name) +
+                      " strides must be positive multiples of 8");
+  return BSM_OK;
+}
+
 // A new epoch for every mask-info build (40 bits, never 0), starting at a
 // value that differs between processes, so that a ticket word left in a
 // reused buffer by an earlier build never matches.
@@ -754,14 +809,160 @@ bsm_status bsm_splash_bwd_mod(const bsm_tensor* q, const bsm_tensor* k,
   return BSM_OK;
 }
 
+bsm_status bsm_kv_append(const bsm_kv_cache* cache, const int32_t* page_table,
+                         int64_t table_stride, int32_t max_pages,
+                         const int32_t* lens, const int32_t* n_new,
+                         const bsm_tensor* k_new, const bsm_tensor* v_new,
+                         int32_t B, int32_t T, void* stream) {
+  g_last_error.clear();
+  bsm_status s = check_cache(cache, table_stride, max_pages, B, T);
+  if (s != BSM_OK) return s;
+  if (k_new == nullptr || v_new == nullptr)
+    return fail(BSM_ERR_INVALID_ARG, "NULL tensor view");
+  if (B == 0 || T == 0 || cache->H_kv == 0) return BSM_OK;
+  s = check_cache_memory(cache, page_table, max_pages, lens);
+  if (s != BSM_OK) return s;
+  if ((reinterpret_cast<uintptr_t>(n_new) & 3u) != 0)
+    return fail(BSM_ERR_INVALID_ARG, "n_new must be 4-byte aligned");
+  s = check_view(k_new, B, cache->H_kv, T, "k_new");
+  if (s == BSM_OK) s = check_view(v_new, B, cache->H_kv, T, "v_new");
+  if (s == BSM_OK) s = check_device(nullptr);
+  if (s != BSM_OK) return s;
+  bsm::AppendParams p;
+  p.k = static_cast<uint8_t*>(cache->k);
+  p.v = static_cast<uint8_t*>(cache->v);
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.num_pages = cache->num_pages;
+  p.H_kv = cache->H_kv;
+  p.page_size = cache->page_size;
+  p.D = cache->D;
+  p.table = page_table;
+  p.table_stride = table_stride;
+  p.max_pages = max_pages;
+  p.lens = lens;
+  p.n_new = n_new;
+  p.B = B;
+  p.T = T;
+  p.k_new = static_cast<const uint16_t*>(k_new->data);
+  p.v_new = static_cast<const uint16_t*>(v_new->data);
+  p.k_sb = k_new->strides[0];
+  p.k_sh = k_new->strides[1];
+  p.k_ss = k_new->strides[2];
+  p.v_sb = v_new->strides[0];
+  p.v_sh = v_new->strides[1];
+  p.v_ss = v_new->strides[2];
+  const cudaError_t e =
+      bsm::launch_kv_append(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
+  return BSM_OK;
+}
+
+size_t bsm_paged_attention_workspace_bytes(int32_t B, int32_t H, int32_t H_kv,
+                                           int32_t T, int32_t D) {
+  if (B < 0 || H < 0 || H_kv < 1 || T < 0 || H % H_kv != 0) return 0;
+  (void)D;
+  return 0;
+}
+
+bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
+                               const int32_t* page_table, int64_t table_stride,
+                               int32_t max_pages, const int32_t* lens,
+                               int32_t B, int32_t H, int32_t T, float scale,
+                               int32_t window, const bsm_score_mod* mod,
+                               const bsm_tensor* out, float* lse,
+                               void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  g_last_error.clear();
+  bsm_status s = check_cache(cache, table_stride, max_pages, B, T);
+  if (s != BSM_OK) return s;
+  if (H < 0 || (cache->H_kv == 0 ? H != 0 : H % cache->H_kv != 0))
+    return fail(BSM_ERR_INVALID_ARG, "H must be a multiple of H_kv");
+  if (!std::isfinite(scale)) return fail(BSM_ERR_INVALID_ARG, "scale not finite");
+  if (window < 0) return fail(BSM_ERR_INVALID_ARG, "window must be >= 0");
+  if (q == nullptr || out == nullptr)
+    return fail(BSM_ERR_INVALID_ARG, "NULL tensor view");
+  bsm::PagedParams p;
+  s = check_mod(mod, scale, BSM_SCORE_SOFTMAX, &p.mod);
+  if (s != BSM_OK) return s;
+  p.cap_x = p.mod.kind & bsm::kModCap
+                ? static_cast<float>(2.0 * 1.4426950408889634 /
+                                     static_cast<double>(mod->softcap))
+                : 0.f;
+  if (!std::isfinite(p.cap_x))
+    return fail(BSM_ERR_INVALID_ARG, "softcap out of range");
+  if (B == 0 || T == 0 || H == 0) return BSM_OK;
+  s = check_cache_memory(cache, page_table, max_pages, lens);
+  if (s == BSM_OK) s = check_view(q, B, H, T, "q");
+  if (s == BSM_OK) s = check_view(out, B, H, T, "out");
+  if (s != BSM_OK) return s;
+  const int64_t rows = static_cast<int64_t>(H / cache->H_kv) * T;
+  if (rows > (1 << 20))
+    return fail(BSM_ERR_UNSUPPORTED, "too many query rows per K/V head");
+  if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+    return fail(BSM_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+  const size_t need =
+      bsm_paged_attention_workspace_bytes(B, H, cache->H_kv, T, cache->D);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need ||
+                   !aligned16(workspace)))
+    return fail(BSM_ERR_INVALID_ARG,
+                "workspace must be >= bsm_paged_attention_workspace_bytes() "
+                "bytes, 16-byte aligned");
+  int num_sms = 0;
+  s = check_device(&num_sms);
+  if (s != BSM_OK) return s;
+  p.k = static_cast<const uint8_t*>(cache->k);
+  p.v = static_cast<const uint8_t*>(cache->v);
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.num_pages = cache->num_pages;
+  p.H_kv = cache->H_kv;
+  p.page_size = cache->page_size;
+  p.D = cache->D;
+  p.table = page_table;
+  p.table_stride = table_stride;
+  p.max_pages = max_pages;
+  p.lens = lens;
+  p.B = B;
+  p.H = H;
+  p.T = T;
+  p.window = window;
+  p.scale = scale;
+  p.q = static_cast<const uint16_t*>(q->data);
+  p.q_sb = q->strides[0];
+  p.q_sh = q->strides[1];
+  p.q_ss = q->strides[2];
+  p.out = static_cast<uint16_t*>(out->data);
+  p.o_sb = out->strides[0];
+  p.o_sh = out->strides[1];
+  p.o_ss = out->strides[2];
+  p.lse = lse;
+  const cudaError_t e =
+      bsm::launch_paged_attention(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged_attention launch");
+  return BSM_OK;
+}
+
 bsm_status bsm_device_status(void* stream, int32_t* detail) {
   g_last_error.clear();
   int32_t rec[4] = {0, 0, 0, 0}, brec[4] = {0, 0, 0, 0};
+  int32_t crec[4] = {0, 0, 0, 0};
   cudaError_t e = bsm::read_device_error(rec, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "device status");
   e = bsm::read_bwd_error(brec);
   if (e != cudaSuccess) return cuda_fail(e, "device status");
+  e = bsm::read_cache_error(crec);
+  if (e != cudaSuccess) return cuda_fail(e, "device status");
   if (rec[0] == 0 && brec[0] != 0) std::memcpy(rec, brec, sizeof(rec));
+  if (rec[0] == 0 && crec[0] != 0) {
+    if (detail != nullptr) std::memcpy(detail, crec, sizeof(crec));
+    return fail(BSM_ERR_INVALID_ARG,
+                (crec[2] < 0 ? "a length is out of range (sequence "
+                             : "a page is out of range (sequence ") +
+                    std::to_string(crec[1]) +
+                    (crec[2] < 0 ? "" : ", slot " + std::to_string(crec[2])) +
+                    ", value " + std::to_string(crec[3]) + ")");
+  }
   if (detail != nullptr) std::memcpy(detail, rec, sizeof(rec));
   if (rec[0] != 0)
     return fail(BSM_ERR_DEVICE_TIMEOUT,

@@ -132,7 +132,45 @@ struct BwdParams {
   uint64_t timeout_ns;
 };
 
+struct AppendParams {
+  uint8_t *k, *v;  // pages [num_pages][H_kv][page_size][D], e4m3
+  float *k_scale, *v_scale;  // [num_pages][H_kv]
+  int32_t num_pages, H_kv, page_size, D;
+  const int32_t* table;  // [B][table_stride], max_pages entries per sequence
+  int64_t table_stride;
+  int32_t max_pages;
+  const int32_t* lens;   // [B] tokens before the call
+  const int32_t* n_new;  // [B] or null (T each)
+  int32_t B, T;
+  const uint16_t *k_new, *v_new;  // bf16 [B][H_kv][T][D]
+  int64_t k_sb, k_sh, k_ss, v_sb, v_sh, v_ss;
+};
+
+struct PagedParams {
+  const uint8_t *k, *v;
+  const float *k_scale, *v_scale;
+  int32_t num_pages, H_kv, page_size, D;
+  const int32_t* table;
+  int64_t table_stride;
+  int32_t max_pages;
+  const int32_t* lens;  // [B] tokens, the queries' own among them
+  int32_t B, H, T;
+  int32_t window;  // 0 = none
+  float scale;
+  ScoreMod mod;
+  float cap_x;  // 2 log2(e) / cap
+  const uint16_t* q;  // bf16 [B][H][T][D]
+  int64_t q_sb, q_sh, q_ss;
+  uint16_t* out;
+  int64_t o_sb, o_sh, o_ss;
+  float* lse;  // [B][H][T] or null
+};
+
 // Launchers (return a cudaError_t from the launch).
+cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
+cudaError_t launch_paged_attention(const PagedParams& p, cudaStream_t stream);
+// Reads and clears the device error record of the cache kernels.
+cudaError_t read_cache_error(int32_t out[4]);
 cudaError_t launch_mask_info(const MaskInfoParams& p, cudaStream_t stream);
 cudaError_t launch_pack_dense(const uint8_t* mask, int64_t stride, int32_t Sq,
                               int32_t Skv, uint32_t* words, int32_t row_words,

@@ -404,10 +404,88 @@ bsm_status bsm_splash_bwd_mod(const bsm_tensor* q, const bsm_tensor* k,
                               const bsm_tensor* dv, void* workspace,
                               size_t workspace_bytes, void* stream);
 
+/* A paged cache of keys and values in 8-bit floating point (no counterpart on
+ * the pages; it serves tokens one by one after the prompt's forward).  A page
+ * holds `page_size` consecutive tokens of one sequence for every K/V head:
+ *   k, v              device e4m3 [num_pages][H_kv][page_size][D], contiguous,
+ *                     16-byte aligned
+ *   k_scale, v_scale  device f32 [num_pages][H_kv], contiguous: an element is
+ *                     its code times its page's and head's scale; finite and
+ *                     positive wherever a page holds tokens
+ *   page_size         16, 32, 64 or 128; D 64 or 128
+ * The memory is the caller's.  A sequence's tokens are found through a page
+ * table: entry j of its row is the page of tokens [j page_size, (j + 1)
+ * page_size); entries past its last token are never read. */
+typedef struct bsm_kv_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t num_pages, H_kv, page_size, D;
+} bsm_kv_cache;
+
+/* Append tokens to the cache: sequence b, which holds lens[b] tokens, gets
+ * n_new[b] more, k_new[b][:][0 .. n_new[b]) and v_new likewise.  Per page and
+ * head, with amax the largest finite magnitude among the new tokens there and
+ * e the smallest integer in [-40, 40] with amax <= 448 * 2^e: a page without
+ * tokens takes the scale 2^e; one that holds some keeps the larger of its
+ * scale and 2^e, and where its scale grows its old codes are rounded again.
+ * Codes are element / scale rounded to the nearest e4m3 value (ties to even);
+ * magnitudes above 448 scales (infinities among them) become 448 scales, NaN
+ * stays NaN.  Nothing else of the cache is written: not the page's tokens
+ * behind the new ones, nor pages that get none.  `lens` is not changed.
+ *   page_table  device int32, row b at page_table + b * table_stride, with
+ *               max_pages entries; the rows must hold the new tokens' pages
+ *   lens, n_new device int32 [B]; n_new NULL = T new tokens each
+ *   k_new, v_new  device bf16 [B][H_kv][T][D] (head_dim contiguous, strides
+ *               multiples of 8, 16-byte aligned)
+ * A page that gets tokens must belong to one sequence only (copy a shared
+ * last page first).  On the device, lens[b] < 0, n_new[b] outside [0, T],
+ * more tokens than max_pages pages hold, or a page outside [0, num_pages)
+ * leave that sequence (or page) unwritten and are reported by
+ * bsm_device_status as BSM_ERR_INVALID_ARG.  One launch on `stream`. */
+bsm_status bsm_kv_append(const bsm_kv_cache* cache, const int32_t* page_table,
+                         int64_t table_stride, int32_t max_pages,
+                         const int32_t* lens, const int32_t* n_new,
+                         const bsm_tensor* k_new, const bsm_tensor* v_new,
+                         int32_t B, int32_t T, void* stream);
+
+/* Attention over the cache.  The T queries of sequence b are its last tokens:
+ * query t is at position p = lens[b] - T + t and sees the keys j <= p of its
+ * sequence, with window > 0 only those with p - j < window.  Scores as in
+ * bsm_splash_fwd_mod (softmax; `mod` may be NULL, its bias is slope (p - j)).
+ *   q, out      device bf16 [B][H][T][D], strides as above; H a multiple of
+ *               the cache's H_kv (query head h reads head h / (H / H_kv))
+ *   lens        device int32 [B]: tokens in the cache, the queries' own
+ *               among them (append first); 0 is allowed
+ *   lse         device f32 [B][H][T], contiguous, or NULL: natural-log
+ *               logsumexp of the visible logits
+ *   workspace   device, >= bsm_paged_attention_workspace_bytes(...) bytes,
+ *               16-byte aligned (NULL where that is 0); its contents do not
+ *               matter.  Two calls that may run at once need separate ones
+ * A row that sees no key (lens[b] = 0, or T > lens[b]) gets out = 0 and lse =
+ * -inf.  On the device, a length outside [0, max_pages * page_size] is cut to
+ * it, tokens of a page outside [0, num_pages) count as masked, and both are
+ * reported by bsm_device_status as BSM_ERR_INVALID_ARG. */
+bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
+                               const int32_t* page_table, int64_t table_stride,
+                               int32_t max_pages, const int32_t* lens,
+                               int32_t B, int32_t H, int32_t T, float scale,
+                               int32_t window, const bsm_score_mod* mod,
+                               const bsm_tensor* out, float* lse,
+                               void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* Bytes of bsm_paged_attention's device workspace (0 on bad sizes). */
+size_t bsm_paged_attention_workspace_bytes(int32_t B, int32_t H, int32_t H_kv,
+                                           int32_t T, int32_t D);
+
 /* Synchronise `stream` and report whether a kernel of this library gave up
  * on a bounded wait since the last call (then BSM_ERR_DEVICE_TIMEOUT; the
- * affected outputs are undefined, the CUDA context stays usable).  If
- * `detail` is non-NULL it receives 4 ints: code, block, role, phase. */
+ * affected outputs are undefined, the CUDA context stays usable), or a cache
+ * kernel met a length or page out of range (BSM_ERR_INVALID_ARG).  If
+ * `detail` is non-NULL it receives 4 ints: code, block, role, phase; for the
+ * cache kernels 2, the sequence, the page slot (-1: a length) and the value. */
 bsm_status bsm_device_status(void* stream, int32_t* detail);
 
 /* Failure-detection self test: enqueue one tiny kernel that waits on an
