@@ -860,9 +860,10 @@ bsm_status bsm_kv_append(const bsm_kv_cache* cache, const int32_t* page_table,
 
 size_t bsm_paged_attention_workspace_bytes(int32_t B, int32_t H, int32_t H_kv,
                                            int32_t T, int32_t D) {
-  if (B < 0 || H < 0 || H_kv < 1 || T < 0 || H % H_kv != 0) return 0;
-  (void)D;
-  return 0;
+  if (B < 0 || H < 0 || H_kv < 1 || T < 0 || H % H_kv != 0 ||
+      (D != 64 && D != 128))
+    return 0;
+  return bsm::paged_workspace_bytes(static_cast<int64_t>(H / H_kv) * T, D);
 }
 
 bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
@@ -897,8 +898,8 @@ bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
   if (s == BSM_OK) s = check_view(out, B, H, T, "out");
   if (s != BSM_OK) return s;
   const int64_t rows = static_cast<int64_t>(H / cache->H_kv) * T;
-  if (rows > (1 << 20))
-    return fail(BSM_ERR_UNSUPPORTED, "too many query rows per K/V head");
+  if (rows * cache->H_kv > 8 * 65535)
+    return fail(BSM_ERR_UNSUPPORTED, "too many query rows");
   if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
     return fail(BSM_ERR_INVALID_ARG, "lse must be 4-byte aligned");
   const size_t need =
@@ -911,6 +912,9 @@ bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
   int num_sms = 0;
   s = check_device(&num_sms);
   if (s != BSM_OK) return s;
+  if (num_sms > bsm::kPaMaxSms)
+    return fail(BSM_ERR_UNSUPPORTED, "more than 256 SMs");
+  p.parts = static_cast<float*>(workspace);
   p.k = static_cast<const uint8_t*>(cache->k);
   p.v = static_cast<const uint8_t*>(cache->v);
   p.k_scale = cache->k_scale;
@@ -938,7 +942,7 @@ bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
   p.o_ss = out->strides[2];
   p.lse = lse;
   const cudaError_t e =
-      bsm::launch_paged_attention(p, static_cast<cudaStream_t>(stream));
+      bsm::launch_paged_attention(p, num_sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged_attention launch");
   return BSM_OK;
 }

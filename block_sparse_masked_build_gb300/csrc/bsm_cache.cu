@@ -328,34 +328,151 @@ __device__ __forceinline__ void load_group(const PagedParams& p,
               ok);
 }
 
-// One CTA: query rows [row0, row0 + 8 NT) of one (sequence, key/value head).
-// Warp w takes groups w, w + 4, ... of 16 tokens.  Per group, with the group
-// as the 16-row operand so that 8 query rows fill the other one:
+// Writes N elements of one result row from dim d on: x / sum in bf16 and, with
+// d = 0, the logsumexp of base + log2(sum).  sum = 0: the row saw no key.
+template <int N>
+__device__ __forceinline__ void write_row(const PagedParams& p, int b,
+                                          int head, int t, int d, float base,
+                                          float sum, const float* x) {
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  uint16_t* dst = p.out + b * p.o_sb + head * p.o_sh + t * p.o_ss + d;
+#pragma unroll
+  for (int i = 0; i < N; i += 2)
+    *reinterpret_cast<uint32_t*>(dst + i) =
+        pack_bf16x2(x[i] * inv, x[i + 1] * inv);
+  if (d == 0 && p.lse != nullptr)
+    p.lse[(static_cast<int64_t>(b) * p.H + head) * p.T + t] =
+        sum != 0.f ? (base + log2f(sum)) * 0.6931471805599453f
+                   : __int_as_float(0xff800000);
+}
+
+// How the tokens are dealt out.  An item is (sequence, key/value head, tile of
+// 8 NT query rows); its work is its sequence's visible tokens in units of 64
+// (a group of 16 for each warp).  All units of all items, in order, are cut
+// into equal runs, one per CTA, so that unequal lengths and few long
+// sequences load every SM alike.  A CTA may start and end inside an item;
+// then it leaves its part (o, m, l) in the workspace and the join kernel adds
+// the parts up.  The cut depends on the lengths alone, which both kernels
+// read.
+struct PaPlan {
+  int len, lo;      // of one sequence: tokens, first visible one
+  int first_group;  // of 16 tokens
+  int n_groups, n_units;
+};
+
+__device__ __forceinline__ PaPlan plan_of(const PagedParams& p, int len) {
+  PaPlan s;
+  s.len = min(max(len, 0), p.max_pages * p.page_size);
+  s.lo = p.window > 0 ? max(0, s.len - p.T - p.window + 1) : 0;
+  s.first_group = s.lo / kPaGroup;
+  s.n_groups = (s.len + kPaGroup - 1) / kPaGroup - s.first_group;
+  s.n_units = (s.n_groups + kPaWarps - 1) / kPaWarps;
+  return s;
+}
+
+// Scans the lengths with the whole block (kPaThreads threads).  Returns the
+// number of units of one item row (heads and row tiles taken once), and, for
+// `seq` >= 0, the units before that sequence in *before.
+__device__ __forceinline__ int64_t scan_units(const PagedParams& p, int seq,
+                                              int64_t* before) {
+  __shared__ long long part[2][kPaWarps];
+  long long all = 0, head = 0;
+  for (int b = threadIdx.x; b < p.B; b += kPaThreads) {
+    const int n = plan_of(p, p.lens[b]).n_units;
+    all += n;
+    if (b < seq) head += n;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) {
+    all += __shfl_xor_sync(0xffffffffu, all, d);
+    head += __shfl_xor_sync(0xffffffffu, head, d);
+  }
+  if (threadIdx.x % 32 == 0) {
+    part[0][threadIdx.x / 32] = all;
+    part[1][threadIdx.x / 32] = head;
+  }
+  __syncthreads();
+  all = head = 0;
+#pragma unroll
+  for (int w = 0; w < kPaWarps; ++w) {
+    all += part[0][w];
+    head += part[1][w];
+  }
+  if (before != nullptr) *before = head;
+  __syncthreads();
+  return all;
+}
+
+// The sequence that holds unit u of one item row times `per` items (whole
+// block): the b with start(b) <= u < start(b + 1), and its start.
+__device__ __forceinline__ int find_sequence(const PagedParams& p, int per,
+                                             int64_t u, int64_t* start) {
+  __shared__ int found;
+  __shared__ long long found_start, warp_sum[kPaWarps];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  long long base = 0;
+  if (threadIdx.x == 0) found = p.B;
+  __syncthreads();
+  for (int b0 = 0; b0 < p.B; b0 += kPaThreads) {
+    const int b = b0 + threadIdx.x;
+    const long long n =
+        b < p.B ? static_cast<long long>(plan_of(p, p.lens[b]).n_units) * per
+                : 0;
+    long long inc = n;  // inclusive scan over the warp
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += v;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    long long at = base + inc - n, total = 0;
+#pragma unroll
+    for (int w = 0; w < kPaWarps; ++w) {
+      if (w < warp) at += warp_sum[w];
+      total += warp_sum[w];
+    }
+    if (n > 0 && at <= u && u < at + n) {
+      found = b;
+      found_start = at;
+    }
+    base += total;
+    __syncthreads();
+    if (found < p.B) break;
+  }
+  *start = found_start;
+  return found;
+}
+
+// CTAs that get work: at least two units each, so that a CTA's first loads
+// and its join are spread over more than one round of groups.
+__device__ __forceinline__ int64_t busy_ctas(int64_t units, int64_t grid) {
+  const int64_t n = (units + 1) / 2;
+  return n < grid ? n : grid;
+}
+
+// One run of units: query rows [row0, row0 + 8 NT) of one (sequence,
+// key/value head), groups [g0, g1) of its plan.  Warp w takes groups g0 + w,
+// g0 + w + 4, ... of 16 tokens.  Per group, with the group as the 16-row
+// operand so that 8 query rows fill the other one:
 //     S^T [16 tokens][8 rows] = K q^T,   O^T [D][8 rows] += V^T P^T.
 // K and V go from shared memory to registers as they lie (16 bytes per lane)
 // and become f16, which holds every e4m3 value, as do P (11 bits; its
 // rounding is 2^-11) and q, scaled by a power of two per row.
+// `part`: where to leave o [row][D], m and l of an item cut across CTAs, or
+// null to write the result.
 template <int D, int NT>
-__global__ void __launch_bounds__(kPaThreads)
-    paged_attention_kernel(const PagedParams p) {
+__device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
+                                           int b, const PaPlan& plan, int hkv,
+                                           int row0, int g0, int g1,
+                                           float* part) {
   using C = PaCfg<D>;
   constexpr int kSteps = D / 16;
-  extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
-  const int b = blockIdx.z, hkv = blockIdx.y, row0 = blockIdx.x * 8 * NT;
   const int G = p.H / p.H_kv, rows = G * p.T;
   const float NEG_INF = __int_as_float(0xff800000);
-
-  int len = p.lens[b];
-  if (len < 0 || len > p.max_pages * p.page_size) {
-    if (threadIdx.x == 0) record_bad_index(b, -1, len);
-    len = min(max(len, 0), p.max_pages * p.page_size);
-  }
-  // tokens any row of the sequence sees: [lo, len)
-  const int lo = p.window > 0 ? max(0, len - p.T - p.window + 1) : 0;
-  const int first_group = lo / kPaGroup;
-  const int n_groups = (len + kPaGroup - 1) / kPaGroup - first_group;
+  const int len = plan.len, lo = plan.lo, first_group = plan.first_group;
 
   // query fragments: row row0 + 8 nt + g, elements 64 h + 16 t .. + 15
   uint32_t qf[NT][kSteps][2];
@@ -437,28 +554,28 @@ __global__ void __launch_bounds__(kPaThreads)
   const uint32_t ring = smem_u32(smem) + warp * kPaStages * C::kStage;
   const uint32_t scales = smem_u32(smem) + C::kOffScale + warp * kPaStages * 8;
   const int* table = p.table + static_cast<int64_t>(b) * p.table_stride;
-  auto issue = [&](int gi) {  // group number gi of the sequence's range
-    if (gi < n_groups) {
+  auto issue = [&](int gi) {  // group number gi of the plan
+    if (gi < g1) {
       const int tok = (first_group + gi) * kPaGroup;
       int pid = table[tok / p.page_size];
       if (pid < 0 || pid >= p.num_pages) {
         if (lane == 0) record_bad_index(b, tok / p.page_size, pid);
         pid = -1;
       }
-      const int st = (gi / kPaWarps) % kPaStages;
+      const int st = ((gi - g0) / kPaWarps) % kPaStages;
       load_group<D>(p, ring + st * C::kStage, scales + st * 8, hkv, pid, tok,
                     lo, len);
     }
     cp_async_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kPaStages - 1; ++i) issue(warp + i * kPaWarps);
+  for (int i = 0; i < kPaStages - 1; ++i) issue(g0 + warp + i * kPaWarps);
 
-  for (int gi = warp; gi < n_groups; gi += kPaWarps) {
+  for (int gi = g0 + warp; gi < g1; gi += kPaWarps) {
     cp_async_wait<kPaStages - 2>();
     __syncwarp();  // the group is in shared memory, and the one before it read
     issue(gi + (kPaStages - 1) * kPaWarps);
-    const int st = (gi / kPaWarps) % kPaStages;
+    const int st = ((gi - g0) / kPaWarps) % kPaStages;
     const uint32_t k_at = ring + st * C::kStage, v_at = k_at + C::kHalf;
     const uint2 sc = lds64(scales + st * 8);
     const float k_scale = __uint_as_float(sc.x);
@@ -694,36 +811,161 @@ __global__ void __launch_bounds__(kPaThreads)
 #pragma unroll
     for (int w = 0; w < kPaWarps; ++w) mx = fmaxf(mx, sm[w * R + r]);
     const float base = mx == NEG_INF ? 0.f : mx;
-    float sum = 0.f, x = 0.f, y = 0.f;
+    float sum = 0.f, xy[2] = {0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < kPaWarps; ++w) {
       const float f = ex2_approx(sm[w * R + r] - base);
       sum = fmaf(sl[w * R + r], f, sum);
       const float2 v = *reinterpret_cast<float2*>(so + (w * R + r) * D + d);
-      x = fmaf(v.x, f, x);
-      y = fmaf(v.y, f, y);
+      xy[0] = fmaf(v.x, f, xy[0]);
+      xy[1] = fmaf(v.y, f, xy[1]);
     }
-    const float inv = sum != 0.f ? 1.f / sum : 0.f;
-    const int head = hkv * G + rr / p.T, tt = rr % p.T;
-    *reinterpret_cast<uint32_t*>(p.out + b * p.o_sb + head * p.o_sh +
-                                 tt * p.o_ss + d) =
-        pack_bf16x2(x * inv, y * inv);
-    if (d == 0 && p.lse != nullptr)
-      p.lse[(static_cast<int64_t>(b) * p.H + head) * p.T + tt] =
-          sum != 0.f ? (base + log2f(sum)) * 0.6931471805599453f : NEG_INF;
+    if (part != nullptr) {
+      *reinterpret_cast<float2*>(part + r * D + d) = make_float2(xy[0], xy[1]);
+      if (d == 0) {
+        part[R * D + r] = mx;
+        part[R * D + R + r] = sum;
+      }
+      continue;
+    }
+    write_row<2>(p, b, hkv * G + rr / p.T, rr % p.T, d, base, sum, xy);
+  }
+  __syncthreads();  // the join area becomes the rings again
+}
+
+// CTAs per SM of the attention kernel: three rings fit an SM's shared memory
+// at head dim 128; registers set the other limits.
+template <int D, int NT>
+constexpr int kPaPerSm = D == 64 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 3 : 2);
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kPaThreads, kPaPerSm<D, NT>)
+    paged_attention_kernel(const PagedParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  // the join kernel may be scheduled once every CTA here runs; it waits for
+  // this grid's end before it reads the parts
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int rows = p.H / p.H_kv * p.T;
+  const int tiles = (rows + 8 * NT - 1) / (8 * NT);
+  const int per = p.H_kv * tiles;
+  const int64_t units = scan_units(p, -1, nullptr) * per;
+  const int64_t busy = busy_ctas(units, gridDim.x);
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < p.B; b += kPaThreads) {
+      const int len = p.lens[b];
+      if (len != plan_of(p, len).len) record_bad_index(b, -1, len);
+    }
+  if (blockIdx.x >= busy) return;
+  int64_t u = blockIdx.x * units / busy;
+  const int64_t end = (blockIdx.x + 1) * units / busy;
+  int64_t start;
+  int b = find_sequence(p, per, u, &start);
+  while (u < end) {
+    const PaPlan plan = plan_of(p, p.lens[b]);
+    const int64_t row_units = static_cast<int64_t>(plan.n_units) * per;
+    if (u >= start + row_units) {
+      start += row_units;
+      ++b;
+      continue;
+    }
+    const int item = static_cast<int>((u - start) / plan.n_units);
+    const int off = static_cast<int>((u - start) % plan.n_units);
+    const int n = static_cast<int>(
+        min(static_cast<int64_t>(plan.n_units - off), end - u));
+    float* part = nullptr;
+    if (n < plan.n_units)  // slot 0: the item began before this CTA's run
+      part = p.parts + (blockIdx.x * 2 + (off > 0 ? 0 : 1)) *
+                           static_cast<int64_t>(8 * NT * (D + 2));
+    attend_run<D, NT>(p, smem, b, plan, item / tiles, item % tiles * 8 * NT,
+                      off * kPaWarps, min((off + n) * kPaWarps, plan.n_groups),
+                      part);
+    u += n;
   }
 }
 
+// Joins the parts of the items that were cut, a warp per query row, and
+// writes the rows of sequences without tokens.
 template <int D, int NT>
-cudaError_t launch_paged(const PagedParams& p, cudaStream_t stream) {
+__global__ void __launch_bounds__(kPaThreads)
+    paged_join_kernel(const PagedParams p, const int grid) {
+  constexpr int R = 8 * NT, kPer = D / 32;
+  const int rows = p.H / p.H_kv * p.T;
+  const int tiles = (rows + R - 1) / R;
+  const int per = p.H_kv * tiles;
+  const int b = blockIdx.z, item = blockIdx.y;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int r = blockIdx.x * kPaWarps + warp;
+  const int rr = item % tiles * R + r;
+  int64_t before;
+  const int64_t units = scan_units(p, b, &before) * per;
+  const int n = plan_of(p, p.lens[b]).n_units;
+  // every block waits for the attention grid, so that work after this kernel
+  // on the stream sees what that grid wrote itself
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (rr >= rows || r >= R) return;
+  const int head = item / tiles * (p.H / p.H_kv) + rr / p.T, t = rr % p.T;
+  float x[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) x[i] = 0.f;
+  if (n == 0) {
+    write_row<kPer>(p, b, head, t, lane * kPer, 0.f, 0.f, x);
+    return;
+  }
+  const int64_t busy = busy_ctas(units, grid);
+  const int64_t u0 = before * per + static_cast<int64_t>(item) * n;
+  // the CTAs that hold its first and last unit
+  const int64_t c0 = ((u0 + 1) * busy - 1) / units;
+  const int64_t c1 = ((u0 + n) * busy - 1) / units;
+  if (c0 == c1) return;  // whole in one CTA, which wrote it
+  const float NEG_INF = __int_as_float(0xff800000);
+  auto part_of = [&](int64_t c) {
+    return p.parts + (c * 2 + (c * units / busy > u0 ? 0 : 1)) *
+                         static_cast<int64_t>(R * (D + 2));
+  };
+  float mx = NEG_INF;
+  for (int64_t c = c0 + lane; c <= c1; c += 32)
+    mx = fmaxf(mx, part_of(c)[R * D + r]);
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2)
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+  const float base = mx == NEG_INF ? 0.f : mx;
+  float sum = 0.f;
+#pragma unroll 4
+  for (int64_t c = c0; c <= c1; ++c) {
+    const float* part = part_of(c);
+    const float f = ex2_approx(part[R * D + r] - base);
+    sum = fmaf(part[R * D + R + r], f, sum);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      x[i] = fmaf(part[r * D + lane * kPer + i], f, x[i]);
+  }
+  write_row<kPer>(p, b, head, t, lane * kPer, base, sum, x);
+}
+
+template <int D, int NT>
+cudaError_t launch_paged(const PagedParams& p, int num_sms,
+                         cudaStream_t stream) {
   auto kern = paged_attention_kernel<D, NT>;
-  const cudaError_t e = cudaFuncSetAttribute(
+  cudaError_t e = cudaFuncSetAttribute(
       kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PaCfg<D>::kSmem);
   if (e != cudaSuccess) return e;
   const int rows = p.H / p.H_kv * p.T;
-  const dim3 grid((rows + 8 * NT - 1) / (8 * NT), p.H_kv, p.B);
+  const int tiles = (rows + 8 * NT - 1) / (8 * NT);
+  const int grid = num_sms * kPaPerSm<D, NT>;
   kern<<<grid, kPaThreads, PaCfg<D>::kSmem, stream>>>(p);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((min(rows, 8 * NT) + kPaWarps - 1) / kPaWarps,
+                     p.H_kv * tiles, p.B);
+  cfg.blockDim = dim3(kPaThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, NT>, p, grid);
 }
 
 }  // namespace
@@ -742,13 +984,25 @@ cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_paged_attention(const PagedParams& p, cudaStream_t stream) {
-  // one tile of 8 query rows, or two where the group and the tokens fill them
-  const bool two = p.H / p.H_kv * p.T > 8;
+// Query rows of an item: one tile of 8, or two where the group and the tokens
+// fill them.
+static bool two_tiles(int64_t rows) { return rows > 8; }
+
+size_t paged_workspace_bytes(int64_t rows, int D) {
+  // two parts per CTA: o, m and l of an item's rows
+  return static_cast<size_t>(kPaMaxSms) * 4 * 2 * (two_tiles(rows) ? 16 : 8) *
+         (D + 2) * sizeof(float);
+}
+
+cudaError_t launch_paged_attention(const PagedParams& p, int num_sms,
+                                   cudaStream_t stream) {
+  const bool two = two_tiles(static_cast<int64_t>(p.H / p.H_kv) * p.T);
   if (p.D == 128)
-    return two ? launch_paged<128, 2>(p, stream) : launch_paged<128, 1>(p, stream);
+    return two ? launch_paged<128, 2>(p, num_sms, stream)
+               : launch_paged<128, 1>(p, num_sms, stream);
   if (p.D == 64)
-    return two ? launch_paged<64, 2>(p, stream) : launch_paged<64, 1>(p, stream);
+    return two ? launch_paged<64, 2>(p, num_sms, stream)
+               : launch_paged<64, 1>(p, num_sms, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -164,11 +164,15 @@ struct PagedParams {
   uint16_t* out;
   int64_t o_sb, o_sh, o_ss;
   float* lse;  // [B][H][T] or null
+  float* parts;  // workspace: parts of the items cut across CTAs
 };
+constexpr int kPaMaxSms = 256;  // the workspace's size is for up to so many
 
 // Launchers (return a cudaError_t from the launch).
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
-cudaError_t launch_paged_attention(const PagedParams& p, cudaStream_t stream);
+cudaError_t launch_paged_attention(const PagedParams& p, int num_sms,
+                                   cudaStream_t stream);
+size_t paged_workspace_bytes(int64_t rows, int D);
 // Reads and clears the device error record of the cache kernels.
 cudaError_t read_cache_error(int32_t out[4]);
 cudaError_t launch_mask_info(const MaskInfoParams& p, cudaStream_t stream);
