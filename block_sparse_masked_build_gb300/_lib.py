@@ -108,12 +108,12 @@ def _declare(lib):
         c.c_int32, c.c_void_p, c.c_void_p, c.c_void_p, c.c_size_t,
         c.c_void_p]
     lib.bsm_splash_fwd_mod.restype = c.c_int
+    # strides and tensor views go by address (arrays or structs by byref)
+    vp = c.c_void_p
     lib.bsm_splash_fwd_mod.argtypes = [
-        c.c_void_p, c.c_void_p, c.c_void_p, I64x3, I64x3, I64x3, I64x3,
-        c.c_int32, c.c_int32, c.c_int32, c.c_int32, c.c_int32, c.c_int32,
-        c.POINTER(MaskInfoStruct), c.c_void_p, c.c_void_p, c.c_float,
-        c.c_int32, c.POINTER(ScoreMod), c.c_void_p, c.c_void_p, c.c_void_p,
-        c.c_size_t, c.c_void_p]
+        vp, vp, vp, vp, vp, vp, vp, c.c_int32, c.c_int32, c.c_int32,
+        c.c_int32, c.c_int32, c.c_int32, c.POINTER(MaskInfoStruct), vp, vp,
+        c.c_float, c.c_int32, c.POINTER(ScoreMod), vp, vp, vp, c.c_size_t, vp]
     lib.bsm_splash_fwd_host_bytes.restype = c.c_size_t
     lib.bsm_splash_fwd_host_bytes.argtypes = [
         c.POINTER(MaskSpec), c.c_int32, c.c_int32, c.c_int32, c.c_int32,
@@ -144,26 +144,23 @@ def _declare(lib):
         c.c_size_t, c.c_void_p]
     lib.bsm_splash_bwd_mod.restype = c.c_int
     lib.bsm_splash_bwd_mod.argtypes = [
-        tv, tv, tv, tv, c.c_void_p, tv, c.c_int32, c.c_int32, c.c_int32,
-        c.c_int32, c.c_int32, c.c_int32, c.POINTER(MaskInfoStruct),
-        c.c_void_p, c.c_void_p, c.c_float, c.c_int32, c.POINTER(ScoreMod), tv,
-        tv, tv, c.c_void_p, c.c_size_t, c.c_void_p]
+        vp, vp, vp, vp, vp, vp, c.c_int32, c.c_int32, c.c_int32, c.c_int32,
+        c.c_int32, c.c_int32, c.POINTER(MaskInfoStruct), vp, vp, c.c_float,
+        c.c_int32, c.POINTER(ScoreMod), vp, vp, vp, vp, c.c_size_t, vp]
     lib.bsm_pack_dense_mask.restype = c.c_int
     lib.bsm_pack_dense_mask.argtypes = [c.c_void_p, c.c_int64, c.c_int32,
                                         c.c_int32, c.c_void_p, c.c_int32,
                                         c.c_void_p]
     kc = c.POINTER(KVCacheStruct)
     lib.bsm_kv_append.restype = c.c_int
-    lib.bsm_kv_append.argtypes = [
-        kc, c.c_void_p, c.c_int64, c.c_int32, c.c_void_p, c.c_void_p, tv, tv,
-        c.c_int32, c.c_int32, c.c_void_p]
+    lib.bsm_kv_append.argtypes = [kc, vp, c.c_int64, c.c_int32, vp, vp, vp,
+                                  vp, c.c_int32, c.c_int32, vp]
     lib.bsm_paged_attention_workspace_bytes.restype = c.c_size_t
-    lib.bsm_paged_attention_workspace_bytes.argtypes = [c.c_int32] * 5
+    lib.bsm_paged_attention_workspace_bytes.argtypes = []
     lib.bsm_paged_attention.restype = c.c_int
     lib.bsm_paged_attention.argtypes = [
-        tv, kc, c.c_void_p, c.c_int64, c.c_int32, c.c_void_p, c.c_int32,
-        c.c_int32, c.c_int32, c.c_float, c.c_int32, c.POINTER(ScoreMod), tv,
-        c.c_void_p, c.c_void_p, c.c_size_t, c.c_void_p]
+        vp, kc, vp, c.c_int64, c.c_int32, vp, c.c_int32, c.c_int32, c.c_int32,
+        c.c_float, c.c_int32, c.POINTER(ScoreMod), vp, vp, vp, c.c_size_t, vp]
     lib.bsm_device_status.restype = c.c_int
     lib.bsm_device_status.argtypes = [c.c_void_p, c.POINTER(c.c_int32)]
     lib.bsm_selftest_wait_timeout.restype = c.c_int

@@ -8,16 +8,15 @@ torch for device memory, pinned host memory and streams.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 from dataclasses import dataclass
 
 import torch
 
 from . import _lib
-from ._lib import (I64x3, KVCacheStruct, MaskInfoStruct, MaskSpec, ScoreMod,
-                   TensorView)
+from ._lib import I64x3, KVCacheStruct, MaskInfoStruct, MaskSpec, ScoreMod
 
 MASK_CAUSAL = 1
 MASK_LOCAL = 2
@@ -40,20 +39,27 @@ def _check(status: int) -> None:
         raise BsmError(status, _lib.last_error())
 
 
+# The current device and its current stream as plain numbers (making a
+# torch.cuda.Stream object costs several microseconds of every call).
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_handle(stream) -> int | None:
     if stream is None:
+        if _current_stream is not None and torch.cuda.is_initialized():
+            return _current_stream(_current_device())
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
 
 
-def _on_device(dev):
-    """Makes dev the current device for a call (CUDA's launches and the
-    current stream go by it); nothing to do where it is already."""
-    if dev.type != "cuda" or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+def _elsewhere(dev) -> bool:
+    """Whether dev is a CUDA device other than the current one (launches and
+    the current stream go by that one)."""
+    return dev.index is not None and dev.type == "cuda" and \
+        dev.index != torch.cuda.current_device()
 
 
 def _ptr(t) -> int | None:
@@ -176,10 +182,11 @@ def bsm_build_mask_info(flags: int, window: int, q_segment_ids, kv_segment_ids,
 
 
 def _strides3(t: torch.Tensor):
-    if t.dim() != 4 or t.stride(3) != 1:
+    st = t.stride()
+    if len(st) != 4 or st[3] != 1:
         raise ValueError("tensors must be 4-D [B, H, S, D] views with a "
                          "contiguous head dimension")
-    return I64x3(t.stride(0), t.stride(1), t.stride(2))
+    return I64x3(st[0], st[1], st[2])
 
 
 def bsm_splash_fwd_workspace_bytes() -> int:
@@ -205,7 +212,7 @@ def _score_mod(softcap: float, alibi_slopes, H: int, device):
     """bsm_score_mod of a cap and per-head slopes, or None for neither."""
     if alibi_slopes is not None:
         if (alibi_slopes.dtype != torch.float32
-                or tuple(alibi_slopes.shape) != (H,)
+                or alibi_slopes.shape != (H,)
                 or not alibi_slopes.is_contiguous()
                 or alibi_slopes.device != device):
             raise ValueError("alibi_slopes must be a contiguous float32 "
@@ -227,13 +234,12 @@ def bsm_splash_fwd(q, k, v, mask_info: MaskInfo, q_segment_ids,
     mod = _score_mod(softcap, alibi_slopes, H, q.device)
     if workspace is None:
         workspace = _default_workspace(q.device, sh)
+    views, at = _views(q, k, v, out)  # strides are behind the pointers
     _check(_lib.lib().bsm_splash_fwd_mod(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), _strides3(q), _strides3(k),
-        _strides3(v), _strides3(out), B, H, H_kv, Sq, Skv, D,
-        ctypes.byref(mask_info.struct), _ptr(q_segment_ids),
-        _ptr(kv_segment_ids), float(scale), int(score),
-        None if mod is None else ctypes.byref(mod), out.data_ptr(),
-        _ptr(lse), workspace.data_ptr(),
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), at + 8, at + 40, at + 72,
+        at + 104, B, H, H_kv, Sq, Skv, D, mask_info.struct,
+        _ptr(q_segment_ids), _ptr(kv_segment_ids), float(scale), int(score),
+        mod, out.data_ptr(), _ptr(lse), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), sh))
 
 
@@ -281,12 +287,26 @@ def bsm_splash_fwd_noalloc(q, k, v, mask_info: MaskInfo, q_segment_ids,
         _ptr(lse), _stream_handle(stream)))
 
 
-def _view(t):
-    """bsm_tensor of a 4-D [B, heads, S, D] CUDA tensor view (or None)."""
-    if t is None:
-        return None
-    st = _strides3(t)
-    return TensorView(t.data_ptr(), st)
+def _views(*tensors):
+    """bsm_tensor structs (32 bytes each) of 4-D [B, heads, S, D] tensor
+    views, in one array: (array, its address); None leaves zeros."""
+    flat = []
+    for t in tensors:
+        if t is None:
+            flat += (0, 0, 0, 0)
+            continue
+        st = t.stride()
+        if len(st) != 4 or st[3] != 1:
+            raise ValueError("tensors must be 4-D [B, H, S, D] views with a "
+                             "contiguous head dimension")
+        flat += (t.data_ptr(), st[0], st[1], st[2])
+    array = _views_type(len(flat))(*flat)
+    return array, ctypes.addressof(array)
+
+
+@functools.lru_cache(maxsize=None)
+def _views_type(n: int):
+    return ctypes.c_int64 * n
 
 
 def bsm_splash_bwd_workspace_bytes(B: int, H: int, Sq: int,
@@ -308,14 +328,12 @@ def bsm_splash_bwd(q, k, v, out, lse, dout, mask_info: MaskInfo,
     need = bsm_splash_bwd_workspace_bytes(B, H, Sq, score)
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    views = [_view(t) for t in (q, k, v, out, dout, dq, dk, dv)]
-    refs = [None if x is None else ctypes.byref(x) for x in views]
+    views, at = _views(q, k, v, out, dout, dq, dk, dv)
     _check(_lib.lib().bsm_splash_bwd_mod(
-        refs[0], refs[1], refs[2], refs[3], _ptr(lse), refs[4], B, H, H_kv,
-        Sq, Skv, D, ctypes.byref(mask_info.struct), _ptr(q_segment_ids),
-        _ptr(kv_segment_ids), float(scale), int(score),
-        None if mod is None else ctypes.byref(mod), refs[5], refs[6],
-        refs[7], _ptr(workspace),
+        at, at + 32, at + 64, None if out is None else at + 96, _ptr(lse),
+        at + 128, B, H, H_kv, Sq, Skv, D, mask_info.struct,
+        _ptr(q_segment_ids), _ptr(kv_segment_ids), float(scale), int(score),
+        mod, at + 160, at + 192, at + 224, _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(),
         sh))
 
@@ -326,30 +344,31 @@ class KVCache:
     k_scale, v_scale [num_pages, H_kv] (float32), all contiguous.  An element
     is its code times the scale of its page and head."""
 
-    __slots__ = ("k_pages", "v_pages", "k_scale", "v_scale", "struct")
+    __slots__ = ("k_pages", "v_pages", "k_scale", "v_scale", "device",
+                 "struct")
 
     def __init__(self, k_pages, v_pages, k_scale, v_scale):
-        n, H_kv, P, D = k_pages.shape
+        shape, dev = k_pages.shape, k_pages.device
         for t in (k_pages, v_pages):
-            if (t.dtype != torch.float8_e4m3fn or t.shape != (n, H_kv, P, D)
-                    or not t.is_contiguous()
-                    or t.device != k_pages.device):
+            if (t.dtype != torch.float8_e4m3fn or t.dim() != 4
+                    or t.shape != shape or not t.is_contiguous()
+                    or t.device != dev):
                 raise ValueError("k_pages and v_pages must be contiguous "
                                  "float8_e4m3fn tensors of one shape "
                                  "[num_pages, H_kv, page_size, D] on one "
                                  "device")
         for t in (k_scale, v_scale):
-            if (t.dtype != torch.float32 or t.shape != (n, H_kv)
-                    or not t.is_contiguous()
-                    or t.device != k_pages.device):
+            if (t.dtype != torch.float32 or t.shape != shape[:2]
+                    or not t.is_contiguous() or t.device != dev):
                 raise ValueError("k_scale and v_scale must be contiguous "
                                  "float32 tensors [num_pages, H_kv] beside "
                                  "the pages")
         self.k_pages, self.v_pages = k_pages, v_pages
         self.k_scale, self.v_scale = k_scale, v_scale
+        self.device = dev
         self.struct = KVCacheStruct(k_pages.data_ptr(), v_pages.data_ptr(),
                                     k_scale.data_ptr(), v_scale.data_ptr(),
-                                    n, H_kv, P, D)
+                                    *shape)
 
     @classmethod
     def empty(cls, num_pages: int, H_kv: int, page_size: int, D: int,
@@ -363,25 +382,24 @@ class KVCache:
         return cls(*pages, *scales)
 
 
-def _check_table(cache: KVCache, page_table, B: int, **ints) -> None:
-    dev = cache.k_pages.device
+def _check_table(dev, page_table, B: int, lens, n_new=None) -> None:
     if (page_table.dtype != torch.int32 or page_table.dim() != 2
             or page_table.shape[0] != B or page_table.device != dev
             or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
         raise ValueError("page_table must be an int32 tensor [B, max_pages] "
                          "with contiguous rows, beside the cache")
-    for name, t in ints.items():
+    for name, t in (("lens", lens), ("n_new", n_new)):
         if t is not None and (t.dtype != torch.int32 or t.shape != (B,)
                               or not t.is_contiguous() or t.device != dev):
             raise ValueError(f"{name} must be a contiguous int32 tensor [B] "
                              "beside the cache")
 
 
-def _check_tokens(t, shape, dev, name: str):
-    if t.dtype != torch.bfloat16 or t.shape != shape or t.device != dev:
-        raise ValueError(f"{name} must be a bfloat16 tensor "
-                         f"{list(shape)} beside the cache")
-    return TensorView(t.data_ptr(), _strides3(t))
+def _check_tokens(t, shape, dev, name: str) -> None:
+    if (t.dtype != torch.bfloat16 or t.shape != shape or t.device != dev
+            or t.stride(3) != 1):
+        raise ValueError(f"{name} must be a bfloat16 tensor {list(shape)} "
+                         "with a contiguous head dimension, beside the cache")
 
 
 def bsm_kv_append(cache: KVCache, page_table, lens, k_new, v_new, n_new=None,
@@ -389,27 +407,47 @@ def bsm_kv_append(cache: KVCache, page_table, lens, k_new, v_new, n_new=None,
     """Append k_new, v_new [B,H_kv,T,D] (bf16, any strides that are multiples
     of 8) to sequences of lens [B] tokens, n_new [B] of them each (None: T).
     page_table int32 [B, max_pages]; lens is left as it is."""
+    dev = cache.device
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return bsm_kv_append(cache, page_table, lens, k_new, v_new, n_new,
+                                 stream)
     s = cache.struct
     if k_new.dim() != 4:
         raise ValueError("k_new must be [B, H_kv, T, D]")
-    B, T = k_new.shape[0], k_new.shape[2]
-    dev = cache.k_pages.device
-    _check_table(cache, page_table, B, lens=lens, n_new=n_new)
+    B, _, T, _ = k_new.shape
+    _check_table(dev, page_table, B, lens, n_new)
     shape = (B, s.H_kv, T, s.D)
-    kt = _check_tokens(k_new, shape, dev, "k_new")
-    vt = _check_tokens(v_new, shape, dev, "v_new")
-    with _on_device(dev):
-        _check(_lib.lib().bsm_kv_append(
-            ctypes.byref(s), page_table.data_ptr(), page_table.stride(0),
-            page_table.shape[1], lens.data_ptr(), _ptr(n_new),
-            ctypes.byref(kt), ctypes.byref(vt), B, T,
-            _stream_handle(stream)))
+    _check_tokens(k_new, shape, dev, "k_new")
+    _check_tokens(v_new, shape, dev, "v_new")
+    views, at = _views(k_new, v_new)
+    _check(_lib.lib().bsm_kv_append(
+        s, page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
+        lens.data_ptr(), None if n_new is None else n_new.data_ptr(), at,
+        at + 32, B, T, _stream_handle(stream)))
 
 
-def bsm_paged_attention_workspace_bytes(B: int, H: int, H_kv: int, T: int,
-                                        D: int) -> int:
-    return int(_lib.lib().bsm_paged_attention_workspace_bytes(B, H, H_kv, T,
-                                                              D))
+def bsm_paged_attention_workspace_bytes() -> int:
+    return int(_lib.lib().bsm_paged_attention_workspace_bytes())
+
+
+_paged_workspaces: dict = {}
+
+
+def _paged_workspace(dev, stream_handle):
+    """paged_attention's workspace: one per (device, stream), as calls on one
+    stream run in order.  A captured call gets one of its own, from the
+    graph's memory: graphs captured on one stream may run at once."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(bsm_paged_attention_workspace_bytes(),
+                           dtype=torch.uint8, device=dev)
+    key = (dev, stream_handle)
+    ws = _paged_workspaces.get(key)
+    if ws is None:
+        ws = torch.empty(bsm_paged_attention_workspace_bytes(),
+                         dtype=torch.uint8, device=dev)
+        _paged_workspaces[key] = ws
+    return ws
 
 
 def bsm_paged_attention(q, cache: KVCache, page_table, lens, scale: float,
@@ -418,35 +456,36 @@ def bsm_paged_attention(q, cache: KVCache, page_table, lens, scale: float,
                         workspace=None) -> None:
     """q, out [B,H,T,D] (bf16): the last T of each sequence's lens [B]
     tokens attend to the cache; lse [B,H,T] (f32, contiguous) or None."""
+    dev = cache.device
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return bsm_paged_attention(q, cache, page_table, lens, scale, out,
+                                       lse, window, softcap, alibi_slopes,
+                                       stream, workspace)
     s = cache.struct
     if q.dim() != 4:
         raise ValueError("q must be [B, H, T, D]")
     B, H, T, D = q.shape
-    dev = cache.k_pages.device
-    _check_table(cache, page_table, B, lens=lens)
+    _check_table(dev, page_table, B, lens)
     shape = (B, H, T, s.D)
-    qt = _check_tokens(q, shape, dev, "q")
-    ot = _check_tokens(out, shape, dev, "out")
+    _check_tokens(q, shape, dev, "q")
+    _check_tokens(out, shape, dev, "out")
     if lse is not None and (lse.dtype != torch.float32
                             or lse.shape != (B, H, T) or lse.device != dev
                             or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 tensor [B, H, T] "
                          "beside the cache")
     mod = _score_mod(softcap, alibi_slopes, H, dev)
-    with _on_device(dev):
-        sh = _stream_handle(stream)
-        if workspace is None:
-            need = bsm_paged_attention_workspace_bytes(B, H, s.H_kv, T, D)
-            if need > 0:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        _check(_lib.lib().bsm_paged_attention(
-            ctypes.byref(qt), ctypes.byref(s), page_table.data_ptr(),
-            page_table.stride(0), page_table.shape[1], lens.data_ptr(), B, H,
-            T, float(scale), int(window),
-            None if mod is None else ctypes.byref(mod), ctypes.byref(ot),
-            _ptr(lse), _ptr(workspace),
-            0 if workspace is None
-            else workspace.numel() * workspace.element_size(), sh))
+    sh = _stream_handle(stream)
+    if workspace is None:
+        workspace = _paged_workspace(dev, sh)
+    views, at = _views(q, out)
+    _check(_lib.lib().bsm_paged_attention(
+        at, s, page_table.data_ptr(), page_table.stride(0),
+        page_table.shape[1], lens.data_ptr(), B, H, T, scale, window, mod,
+        at + 32, None if lse is None else lse.data_ptr(),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        sh))
 
 
 def bsm_device_status(stream=None) -> tuple[int, list[int]]:
@@ -498,6 +537,9 @@ def decode_trace(buffer, grid: int):
 
 # ------------------------------------------------------------ conveniences
 
+_CUDA = torch.device("cuda")
+
+
 def build_mask_info(flags: int, B: int, Sq: int, Skv: int, block_q: int = 128,
                     block_kv: int = 128, window: int = 0, q_segment_ids=None,
                     kv_segment_ids=None, device=None, stream=None,
@@ -508,7 +550,7 @@ def build_mask_info(flags: int, B: int, Sq: int, Skv: int, block_q: int = 128,
         raise BsmError(_lib.BSM_ERR_INVALID_ARG, bsm_last_error())
     if device is None:
         device = (q_segment_ids.device if q_segment_ids is not None
-                  else torch.device("cuda"))
+                  else _CUDA)
     buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return bsm_build_mask_info(flags, window, q_segment_ids, kv_segment_ids, B,
                                Sq, Skv, block_q, block_kv, buf, stream,

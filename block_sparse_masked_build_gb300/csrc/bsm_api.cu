@@ -858,12 +858,8 @@ bsm_status bsm_kv_append(const bsm_kv_cache* cache, const int32_t* page_table,
   return BSM_OK;
 }
 
-size_t bsm_paged_attention_workspace_bytes(int32_t B, int32_t H, int32_t H_kv,
-                                           int32_t T, int32_t D) {
-  if (B < 0 || H < 0 || H_kv < 1 || T < 0 || H % H_kv != 0 ||
-      (D != 64 && D != 128))
-    return 0;
-  return bsm::paged_workspace_bytes(static_cast<int64_t>(H / H_kv) * T, D);
+size_t bsm_paged_attention_workspace_bytes(void) {
+  return bsm::kPaWorkspaceBytes;
 }
 
 bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
@@ -902,10 +898,8 @@ bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
     return fail(BSM_ERR_UNSUPPORTED, "too many query rows");
   if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
     return fail(BSM_ERR_INVALID_ARG, "lse must be 4-byte aligned");
-  const size_t need =
-      bsm_paged_attention_workspace_bytes(B, H, cache->H_kv, T, cache->D);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need ||
-                   !aligned16(workspace)))
+  if (workspace == nullptr || workspace_bytes < bsm::kPaWorkspaceBytes ||
+      !aligned16(workspace))
     return fail(BSM_ERR_INVALID_ARG,
                 "workspace must be >= bsm_paged_attention_workspace_bytes() "
                 "bytes, 16-byte aligned");

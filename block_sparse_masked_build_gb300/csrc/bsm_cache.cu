@@ -838,6 +838,8 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
 template <int D, int NT>
 constexpr int kPaPerSm = D == 64 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 3 : 2);
 
+static_assert(kPaPerSm<64, 1> <= kPaMaxPerSm, "workspace");
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kPaThreads, kPaPerSm<D, NT>)
     paged_attention_kernel(const PagedParams p) {
@@ -984,19 +986,10 @@ cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// Query rows of an item: one tile of 8, or two where the group and the tokens
-// fill them.
-static bool two_tiles(int64_t rows) { return rows > 8; }
-
-size_t paged_workspace_bytes(int64_t rows, int D) {
-  // two parts per CTA: o, m and l of an item's rows
-  return static_cast<size_t>(kPaMaxSms) * 4 * 2 * (two_tiles(rows) ? 16 : 8) *
-         (D + 2) * sizeof(float);
-}
-
 cudaError_t launch_paged_attention(const PagedParams& p, int num_sms,
                                    cudaStream_t stream) {
-  const bool two = two_tiles(static_cast<int64_t>(p.H / p.H_kv) * p.T);
+  // one tile of 8 query rows, or two where the group and the tokens fill them
+  const bool two = static_cast<int64_t>(p.H / p.H_kv) * p.T > 8;
   if (p.D == 128)
     return two ? launch_paged<128, 2>(p, num_sms, stream)
                : launch_paged<128, 1>(p, num_sms, stream);

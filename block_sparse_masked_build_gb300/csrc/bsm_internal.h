@@ -166,13 +166,16 @@ struct PagedParams {
   float* lse;  // [B][H][T] or null
   float* parts;  // workspace: parts of the items cut across CTAs
 };
-constexpr int kPaMaxSms = 256;  // the workspace's size is for up to so many
+// The workspace: for up to kPaMaxSms SMs with kPaMaxPerSm CTAs each, two parts
+// per CTA: o, m and l of up to 16 query rows.
+constexpr int kPaMaxSms = 256, kPaMaxPerSm = 4;
+constexpr size_t kPaWorkspaceBytes = static_cast<size_t>(kPaMaxSms) *
+                                     kPaMaxPerSm * 2 * 16 * (128 + 2) * 4;
 
 // Launchers (return a cudaError_t from the launch).
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_paged_attention(const PagedParams& p, int num_sms,
                                    cudaStream_t stream);
-size_t paged_workspace_bytes(int64_t rows, int D);
 // Reads and clears the device error record of the cache kernels.
 cudaError_t read_cache_error(int32_t out[4]);
 cudaError_t launch_mask_info(const MaskInfoParams& p, cudaStream_t stream);

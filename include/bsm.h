@@ -460,9 +460,9 @@ bsm_status bsm_kv_append(const bsm_kv_cache* cache, const int32_t* page_table,
  *               among them (append first); 0 is allowed
  *   lse         device f32 [B][H][T], contiguous, or NULL: natural-log
  *               logsumexp of the visible logits
- *   workspace   device, >= bsm_paged_attention_workspace_bytes(...) bytes,
- *               16-byte aligned (NULL where that is 0); its contents do not
- *               matter.  Two calls that may run at once need separate ones
+ *   workspace   device, >= bsm_paged_attention_workspace_bytes() bytes,
+ *               16-byte aligned; its contents do not matter.  Two calls that
+ *               may run at once need separate ones
  * A row that sees no key (lens[b] = 0, or T > lens[b]) gets out = 0 and lse =
  * -inf.  On the device, a length outside [0, max_pages * page_size] is cut to
  * it, tokens of a page outside [0, num_pages) count as masked, and both are
@@ -476,9 +476,9 @@ bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
                                void* workspace, size_t workspace_bytes,
                                void* stream);
 
-/* Bytes of bsm_paged_attention's device workspace (0 on bad sizes). */
-size_t bsm_paged_attention_workspace_bytes(int32_t B, int32_t H, int32_t H_kv,
-                                           int32_t T, int32_t D);
+/* Bytes of bsm_paged_attention's device workspace (16 MiB and a little): the
+ * parts of rows whose keys are split over several CTAs. */
+size_t bsm_paged_attention_workspace_bytes(void);
 
 /* Synchronise `stream` and report whether a kernel of this library gave up
  * on a bounded wait since the last call (then BSM_ERR_DEVICE_TIMEOUT; the
