@@ -69,8 +69,13 @@ struct BwdCfg {
   static constexpr int kOffList = kOffT + 4 * kTileBytes;
   static constexpr int kOffBar = kOffList + kMaxKvTiles * 2;
   static constexpr int kSmemBytes = kOffBar + 256 + 1024;
+  // modified scores, dK/dV: per elementwise warp, the lse and D_q of the
+  // step's 64 columns of its half
+  static constexpr int kOffStat = kOffBar + 256;
+  static constexpr int kStatBytes = 8 * 128 * 4;
 };
-static_assert(BwdCfg<128>::kSmemBytes <= 232448, "shared memory budget");
+static_assert(BwdCfg<128>::kSmemBytes + BwdCfg<128>::kStatBytes <= 232448,
+              "shared memory budget");
 
 struct BwdBars {
   uint64_t f_full;
@@ -403,6 +408,165 @@ __device__ __forceinline__ void bwd_mma_role(const BwdParams& p, uint8_t* smem,
   __syncwarp();
 }
 
+__device__ __forceinline__ void load4(const float* at, float r[4]) {
+  const float4 v = *reinterpret_cast<const float4*>(at);
+  r[0] = v.x;
+  r[1] = v.y;
+  r[2] = v.z;
+  r[3] = v.w;
+}
+
+// Sign of the distance bias's dependence on (column - row) for a half tile of
+// 64 columns from col0 on and the warp's 32 rows from row0 on: -1 where the
+// columns lie after the rows, 1 before, 0 where they mix (then the bias is
+// taken column by column).  Under a causal mask visible queries (dK/dV's
+// columns) lie after the key and visible keys (dQ's) before the query.
+template <bool DKDV>
+__device__ __forceinline__ float bias_side(const BwdParams& p, int col0,
+                                           int row0) {
+  if (p.flags & BSM_MASK_CAUSAL) return DKDV ? -1.f : 1.f;
+  if (col0 >= row0 + 31) return -1.f;
+  return col0 + 63 <= row0 ? 1.f : 0.f;
+}
+
+// P (packed to bf16) and the factor f of dS = f (dP - D_q) for one thread's
+// 64 columns with modified scores, all in log2 units:
+//     x = cap tanh(scale S / cap) or scale S,  P = 2^(x + bias - lse),
+//     f = P (1 - tanh^2) = P (1 - x^2 / cap^2), or P.
+// tanh is the forward's: a polynomial of POLY terms where every |S| of the warp
+// lies within its range, else (POLY = 0), with E = e^(-2 |y|) and r = 1 / (1 + E): |tanh y| =
+// (1 - E) r and 1 - tanh^2 y = 4 E r^2, which keeps its relative precision
+// where tanh saturates.  n: dK/dV: the columns' negated lse and bias.
+template <int MOD, bool DKDV, bool MASK, int POLY>
+__device__ __forceinline__ void mod_p_loop(const BwdParams& p,
+                                           const uint32_t* sraw,
+                                           const uint32_t vis[2],
+                                           const float* n, float add,
+                                           const float* pc, float sl8,
+                                           bool split, float slope2,
+                                           float dist0, float* f,
+                                           uint32_t* pw) {
+#pragma unroll
+  for (int j = 0; j < 64; j += 4) {
+    float a[4];  // what is added to x
+    if (DKDV) {
+      load4(n + j, a);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        a[u] = fmaf(sl8, static_cast<float>(j / 8), add);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; u += 2) {
+      const int c = j + u;
+      const float s0 = __uint_as_float(sraw[c]);
+      const float s1 = __uint_as_float(sraw[c + 1]);
+      float x0, x1, b0 = 1.f, b1 = 1.f;
+      if (!(MOD & kModCap)) {
+        if (DKDV)
+          ffma2(x0, x1, s0, s1, p.scale_log2, add);
+        else
+          ffma2v(x0, x1, s0, s1, p.scale_log2, p.scale_log2, pc[c & 7],
+                 pc[(c & 7) + 1]);
+      } else {
+        if (POLY > 0) {
+          float h0, h1;
+          poly_sq2<POLY>(h0, h1, s0, s1, POLY == 4 ? p.mod.poly : p.mod.wide);
+          fmul2v(x0, x1, s0, s1, h0, h1);
+          fmul2v(b0, b1, x0, x1, x0, x1);
+          ffma2(b0, b1, b0, b1, -p.mod.inv_cap2, 1.f);
+        } else {
+          float e0, e1, q0, q1;
+          fmul2(q0, q1, s0, s1, p.mod.cap_e);
+          e0 = ex2_approx(-fabsf(q0));
+          e1 = ex2_approx(-fabsf(q1));
+          float d0, d1;
+          fadd2(d0, d1, e0, e1, 1.f, 1.f);
+          const float r = rcp_approx(d0 * d1);
+          fmul2(d0, d1, d1, d0, r);  // 1 / (1 + E)
+          x0 = copysignf((1.f - e0) * d0 * p.mod.cap_log2, q0);
+          x1 = copysignf((1.f - e1) * d1 * p.mod.cap_log2, q1);
+          fmul2v(b0, b1, d0, d1, d0, d1);
+          fmul2v(b0, b1, b0, b1, 4.f * e0, 4.f * e1);
+        }
+        if ((MOD & kModBias) && !DKDV)
+          fadd2(a[u], a[u + 1], a[u], a[u + 1], pc[c & 7], pc[(c & 7) + 1]);
+        if ((MOD & kModBias) && DKDV)
+          fadd2(a[u], a[u + 1], a[u], a[u + 1], add, add);
+      }
+      fadd2(x0, x1, x0, x1, a[u], a[u + 1]);
+      if ((MOD & kModBias) && split) {
+        x0 = fmaf(-slope2, fabsf(dist0 + static_cast<float>(c)), x0);
+        x1 = fmaf(-slope2, fabsf(dist0 + static_cast<float>(c + 1)), x1);
+      }
+      float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+      if (MASK) {
+        p0 = (vis[c >> 5] >> (c & 31)) & 1u ? p0 : 0.f;
+        p1 = (vis[c >> 5] >> ((c + 1) & 31)) & 1u ? p1 : 0.f;
+      }
+      pw[c / 2] = pack_bf16x2(p0, p1);
+      if (MOD & kModCap) {
+        fmul2v(f[c], f[c + 1], p0, p1, b0, b1);
+        if (MASK) {  // a masked score may be NaN
+          f[c] = p0 == 0.f ? 0.f : f[c];
+          f[c + 1] = p1 == 0.f ? 0.f : f[c + 1];
+        }
+      } else {
+        f[c] = p0;
+        f[c + 1] = p1;
+      }
+    }
+  }
+}
+
+template <int MOD, bool DKDV>
+__device__ __forceinline__ void mod_p(const BwdParams& p, const uint32_t* sraw,
+                                      const uint32_t vis[2], const float* n,
+                                      int col0, int row, float slope2,
+                                      float lse2_row, float* f, uint32_t* pw) {
+  const int lane = threadIdx.x % 32;
+  const float dist0 = static_cast<float>(col0 - row);
+  float pc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  float sl = 0.f;
+  bool split = false;
+  if (MOD & kModBias) {
+    const float side = bias_side<DKDV>(p, col0, row - lane);
+    split = side == 0.f;
+    sl = side * slope2;
+    if (!DKDV)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) pc[c] = sl * static_cast<float>(c);
+  }
+  const float add = sl * dist0 - (DKDV ? 0.f : lse2_row);
+  const bool full =
+      __all_sync(0xffffffffu, (vis[0] & vis[1]) == 0xffffffffu);
+  bool near = true, wide = true;
+  if (MOD & kModCap) {
+    float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+    for (int c = 0; c < 64; c += 4) {
+      a0 = fmax3_abs(a0, __uint_as_float(sraw[c]), __uint_as_float(sraw[c + 1]));
+      a1 = fmax3_abs(a1, __uint_as_float(sraw[c + 2]),
+                     __uint_as_float(sraw[c + 3]));
+    }
+    a0 = fmaxf(a0, a1);
+    near = __all_sync(0xffffffffu, a0 <= p.mod.poly_max);
+    wide = __all_sync(0xffffffffu, a0 <= p.mod.wide_max);
+  }
+  if (near && full)
+    mod_p_loop<MOD, DKDV, false, 4>(p, sraw, vis, n, add, pc, 8.f * sl, split,
+                                    slope2, dist0, f, pw);
+  else if (!(MOD & kModCap) || near)
+    mod_p_loop<MOD, DKDV, true, 4>(p, sraw, vis, n, add, pc, 8.f * sl, split,
+                                   slope2, dist0, f, pw);
+  else if (wide)
+    mod_p_loop<MOD, DKDV, true, 7>(p, sraw, vis, n, add, pc, 8.f * sl, split,
+                                   slope2, dist0, f, pw);
+  else
+    mod_p_loop<MOD, DKDV, true, 0>(p, sraw, vis, n, add, pc, 8.f * sl, split,
+                                   slope2, dist0, f, pw);
+}
+
 // Elementwise warps: two per TMEM lane quarter (one thread per row of the
 // fixed tiles), warps 2-5 taking columns [0, 64) of S and dP, warps 6-9
 // columns [64, 128).  The packed P and dS of the second half go over
@@ -412,9 +576,9 @@ template <int D, int SCORE, int MOD, bool DKDV>
 __device__ __forceinline__ void bwd_elem_role(const BwdParams& p,
                                               BwdBars* bars,
                                               const uint16_t* list,
-                                              uint32_t tmem, int b,
-                                              int hq_or_hkv, int fixed_tile,
-                                              int n_iter) {
+                                              float* stats, uint32_t tmem,
+                                              int b, int hq_or_hkv,
+                                              int fixed_tile, int n_iter) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int quarter = warp % 4;  // TMEM lanes this warp may access
   const int half = (warp - 2) / 4;  // column half of S and dP
@@ -448,7 +612,9 @@ __device__ __forceinline__ void bwd_elem_role(const BwdParams& p,
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int qc = tile * kTileM + half * 64 + c * 32 + lane;
-      l2[c] = 0.f;
+      // queries past the end: P = 0 (with modified scores; else their zero
+      // dO alone makes them vanish, but a rising bias may overflow P)
+      l2[c] = MOD != 0 ? __int_as_float(0x7f800000) : 0.f;
       dl[c] = 0.f;
       if (qc < p.Sq) {
         const int64_t i = (static_cast<int64_t>(b) * p.H + hd) * p.Sq + qc;
@@ -467,6 +633,24 @@ __device__ __forceinline__ void bwd_elem_role(const BwdParams& p,
     const int col0 = tile * kTileM + half * 64;  // first column of the half
     float lse2_c[2] = {lse2_n[0], lse2_n[1]}, delta_c[2] = {delta_n[0], delta_n[1]};
     if (kStats && it + 1 < n_iter) load_stats(it + 1, lse2_n, delta_n);
+    float slope2 = 0.f;  // dK/dV: of the step's query head
+    if ((MOD & kModBias) && p.mod.slopes != nullptr)
+      slope2 = p.mod.slopes[DKDV ? hq_or_hkv * G + it / n_list : hq_or_hkv] *
+               kLog2e;
+    if (MOD != 0 && DKDV) {
+      // the step's columns, negated, where the warp reads them four at a
+      // time (per-element shuffles took as long as the arithmetic); a bias's
+      // part that depends on the column goes in with the lse
+      const float sl = bias_side<DKDV>(p, col0, row - lane) * slope2;
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        stats[c * 32 + lane] =
+            sl * static_cast<float>(c * 32 + lane) - lse2_c[c];
+        stats[64 + c * 32 + lane] = -delta_c[c];
+      }
+      __syncwarp();
+    }
     ok = bwarp_wait(&bars->s_full, it & 1, abort_flag, p.timeout_ns);
     if (!ok) {
       record_bwd_timeout(kRoleBElem, 0);
@@ -485,18 +669,13 @@ __device__ __forceinline__ void bwd_elem_role(const BwdParams& p,
     tc_fence_before();
     if (!DKDV) mbar_arrive(&bars->p_ready);  // S read: the next S may go in
     else if (half == 0) mbar_arrive(&bars->h0_s);
-    // signed distance of the row to the half's first column; the head's
-    // slope (dK/dV: the step's query head)
-    float dist0 = 0.f, slope2 = 0.f;
-    if (MOD & kModBias) {
-      dist0 = static_cast<float>(col0 - row);
-      slope2 = p.mod.slopes[DKDV ? hq_or_hkv * G + it / n_list : hq_or_hkv] *
-               kLog2e;
-    }
     // P, and the per-element factor dS needs: softmax dS = P (dP - D_q),
     // pointwise dS = dP sig (1 + x (1 - sig)) / Sq
     float f[64];
     uint32_t pw[32];
+    if (MOD != 0)
+      mod_p<MOD, DKDV>(p, sraw, vis, stats, col0, row, slope2, lse2_row, f, pw);
+    else
 #pragma unroll
     for (int j = 0; j < 64; j += 2) {
       float pv[2];
@@ -508,30 +687,9 @@ __device__ __forceinline__ void bwd_elem_role(const BwdParams& p,
         if (SCORE == BSM_SCORE_SOFTMAX) {
           const float l2 = DKDV ? __shfl_sync(0xffffffffu, lse2_c[c], jj)
                                 : lse2_row;
-          float x = 0.f, slope_x = 1.f;
-          if (MOD == 0) {
-            x = fmaf(sv, p.scale_log2, -l2);
-          } else {
-            // the forward's modified score, in log2 units.  With E =
-            // e^(-2 |y|) and r = 1 / (1 + E): |tanh y| = (1 - E) r, and the
-            // cap multiplies dS by its derivative 1 - tanh^2 y = 4 E r^2,
-            // which keeps its relative precision where tanh saturates
-            // (1 - t * t would cancel)
-            if (MOD & kModCap) {
-              const float ee = ex2_approx(-fabsf(sv * p.mod.cap_e));
-              const float r = rcp_approx(1.f + ee);
-              const float t = copysignf((1.f - ee) * r, sv * p.mod.cap_e);
-              x = fmaf(t, p.mod.cap_log2, -l2);
-              slope_x = 4.f * ee * r * r;
-            } else {
-              x = fmaf(sv, p.scale_log2, -l2);
-            }
-            if (MOD & kModBias)
-              x = fmaf(-slope2, fabsf(dist0 + static_cast<float>(j + u)), x);
-          }
-          const float pr = v ? ex2_approx(x) : 0.f;
+          const float pr = v ? ex2_approx(fmaf(sv, p.scale_log2, -l2)) : 0.f;
           pv[u] = pr;
-          f[j + u] = (MOD & kModCap) ? (v ? pr * slope_x : 0.f) : pr;
+          f[j + u] = pr;
         } else {
           const float x = sv * p.scale;
           const float sig = fmaf(0.5f, tanh_approx(0.5f * x), 0.5f);
@@ -572,6 +730,21 @@ __device__ __forceinline__ void bwd_elem_role(const BwdParams& p,
       mbar_arrive(&bars->h0_dp);
     }
     uint32_t dsw[32];
+    if (MOD != 0) {
+#pragma unroll
+      for (int j = 0; j < 64; j += 4) {
+        float d[4] = {-delta_row, -delta_row, -delta_row, -delta_row};
+        if (DKDV) load4(stats + 64 + j, d);
+#pragma unroll
+        for (int u = 0; u < 4; u += 2) {
+          float x0, x1;
+          fadd2(x0, x1, __uint_as_float(dpraw[j + u]),
+                __uint_as_float(dpraw[j + u + 1]), d[u], d[u + 1]);
+          fmul2v(x0, x1, x0, x1, f[j + u], f[j + u + 1]);
+          dsw[(j + u) / 2] = pack_bf16x2(x0, x1);
+        }
+      }
+    } else
 #pragma unroll
     for (int j = 0; j < 64; j += 2) {
       float dsv[2];
@@ -739,8 +912,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   } else if (warp == 1) {
     if (n_iter > 0) bwd_mma_role<D, DKDV>(p, smem, bars, tmem, n_iter);
   } else {
-    bwd_elem_role<D, SCORE, MOD, DKDV>(p, bars, list, tmem, b, head, fixed_tile,
-                                  n_iter);
+    float* stats = reinterpret_cast<float*>(smem + C::kOffStat) +
+                   (warp - 2) * 128;
+    bwd_elem_role<D, SCORE, MOD, DKDV>(p, bars, list, stats, tmem, b, head,
+                                       fixed_tile, n_iter);
   }
 
   tc_fence_before();
@@ -799,13 +974,14 @@ cudaError_t launch_bwd_one(const BwdParams& p, const CUtensorMap& tq,
                            const CUtensorMap& tdo, cudaStream_t stream) {
   using C = BwdCfg<D>;
   auto kern = splash_bwd_kernel<D, SCORE, MOD, DKDV>;
+  constexpr int kSmem = C::kSmemBytes + (MOD != 0 && DKDV ? C::kStatBytes : 0);
   cudaError_t e = cudaFuncSetAttribute(
-      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid = DKDV ? dim3((p.Skv + kTileN - 1) / kTileN, p.Hkv, p.B)
                          : dim3((p.Sq + kTileM - 1) / kTileM, p.H, p.B);
   if (DKDV) {
-    kern<<<grid, kBwdThreads, C::kSmemBytes, stream>>>(tq, tk, tv, tdo, p);
+    kern<<<grid, kBwdThreads, kSmem, stream>>>(tq, tk, tv, tdo, p);
     return cudaGetLastError();
   }
   // dQ: a programmatic dependent of the launch before it (the dK/dV grid,
@@ -814,7 +990,7 @@ cudaError_t launch_bwd_one(const BwdParams& p, const CUtensorMap& tq,
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kBwdThreads);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

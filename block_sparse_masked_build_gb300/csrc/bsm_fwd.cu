@@ -641,29 +641,122 @@ __device__ __forceinline__ void mask_tile(float* s, int lo_c, int hi_c,
   }
 }
 
+// s = s * (c[0] + c[1] s^2 + ...) + the bias of the column's place among eight
+// (kModBias) or + neg_m.
+template <int MOD, int N>
+__device__ __forceinline__ void cap_tile(float* s, const float* c,
+                                         const float* pc, float neg_m) {
+#pragma unroll
+  for (int j = 0; j < kTileN; j += 2) {
+    float h0, h1;
+    poly_sq2<N>(h0, h1, s[j], s[j + 1], c);
+    if (MOD & kModBias)
+      ffma2v(s[j], s[j + 1], s[j], s[j + 1], h0, h1, pc[j & 7],
+             pc[(j & 7) + 1]);
+    else
+      ffma2v(s[j], s[j + 1], s[j], s[j + 1], h0, h1, neg_m, neg_m);
+  }
+}
+
 // Modified scores of one row's 128 columns, in place and in log2 units: from
 // S = q.k to cap * tanh(scale S / cap) (kModCap) or scale S, minus slope *
-// |q - k| (kModBias; slope2 = slope * log2(e)).  tanh(y) = 1 - 2 / (1 +
-// e^(2 y)): exact to a few units of 2^-24 of the cap for every y (tanh.approx
-// is off by up to 2^-11 of its value, which the logsumexp would show), at its
-// limits without a clamp, and NaN stays NaN.
+// |q - k| (kModBias; slope2 = slope * log2(e)).
+//
+// tanh.  Where every |S| of the warp's rows lies within poly_max (|y| <= 0.5),
+// an odd polynomial of degree 7 on the paired f32 pipe, off by 5.5e-7 of its
+// value; no MUFU operation.  (The backward's second polynomial, of degree 13,
+// was no faster here than the exponential.)  Else 1 - 2 / (1 + e^(2 y)), one reciprocal for two
+// columns, to a few 2^-23 of the cap; e^(2 y) is cut at 2^60, where tanh is 1
+// in f32, so that the product of two stays in range.  NaN stays NaN in both.
+// (tanh.approx is off by up to 2^-11 of its value, which the logsumexp would
+// show.)  What bounds it: the f32 pipe and the latency of the softmax, which
+// the tensor core waits for.  Measured on packed S=8192, 2 x 16 heads, against
+// 120 us unmodified: cap 50 183 us with an exponential and a reciprocal per
+// column, 145 us with the polynomial.
+//
+// Bias.  All columns of a tile that lie on one side of the row have bias
+// sl (kbase - qrow + c), sl = +-slope2: column c gets sl (c % 8) here, in the
+// same paired operation that scales S, and *base = sl (kbase - qrow); the
+// caller adds sl 8 (c / 8) + *base per 8 columns.  A tile with columns on both
+// sides that no causal mask cuts takes the bias whole, column by column.
+//
+// kModCap alone: s also has m_fixed subtracted.
 template <int MOD>
 __device__ __forceinline__ void modify_tile(float* s, const FwdParams& p,
-                                            int kbase, int qrow,
-                                            float slope2) {
-  const float d0 = static_cast<float>(kbase - qrow);
+                                            int kbase, int qrow, float slope2,
+                                            float* sl_out, float* base_out) {
+  float pc[8];  // bias of columns 0-7 of a chunk
+  bool split = false;
+  if (MOD & kModBias) {
+    const int lane = threadIdx.x % 32;
+    const int first = qrow - lane;  // the warp's rows: first .. first + 31
+    const bool left =
+        (p.flags & BSM_MASK_CAUSAL) != 0 || kbase + kTileN - 1 <= first;
+    split = !left && kbase < first + 31;  // warp-uniform
+    const float sl = split ? 0.f : left ? slope2 : -slope2;
 #pragma unroll
-  for (int c = 0; c < kTileN; ++c) {
-    float x;
-    if (MOD & kModCap)
-      x = fmaf(-2.f * p.mod.cap_log2,
-               rcp_approx(ex2_approx(s[c] * p.mod.cap_e) + 1.f),
-               p.mod.cap_log2);
-    else
-      x = s[c] * p.scale_log2;
-    if (MOD & kModBias) x = fmaf(-slope2, fabsf(d0 + c), x);
-    s[c] = x;
+    for (int c = 0; c < 8; ++c) pc[c] = sl * static_cast<float>(c);
+    *sl_out = 8.f * sl;
+    *base_out = sl * static_cast<float>(kbase - qrow);
   }
+  if (MOD & kModCap) {
+    float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+#pragma unroll
+    for (int c = 0; c < kTileN; c += 8) {
+      a0 = fmax3_abs(a0, s[c], s[c + 1]);
+      a1 = fmax3_abs(a1, s[c + 2], s[c + 3]);
+      a2 = fmax3_abs(a2, s[c + 4], s[c + 5]);
+      a3 = fmax3_abs(a3, s[c + 6], s[c + 7]);
+    }
+    const float top = fmaxf(fmax3(a0, a1, a2), a3);
+    const float neg_m = MOD == kModCap ? -p.mod.m_fixed : 0.f;
+    if (__all_sync(0xffffffffu, top <= p.mod.poly_max)) {
+      cap_tile<MOD, 4>(s, p.mod.poly, pc, neg_m);
+    } else {
+      const float k2 = -2.f * p.mod.cap_log2, k0 = p.mod.cap_log2 + neg_m;
+#pragma unroll
+      for (int c = 0; c < kTileN; c += 2) {
+        float e0, e1;
+        fmul2(e0, e1, s[c], s[c + 1], p.mod.cap_e);
+        e0 = ex2_approx(fmin_nan(e0, 60.f));
+        e1 = ex2_approx(fmin_nan(e1, 60.f));
+        fadd2(e0, e1, e0, e1, 1.f, 1.f);
+        const float r = rcp_approx(e0 * e1) * k2;
+        if (MOD & kModBias)
+          ffma2v(s[c], s[c + 1], e1, e0, r, r, k0 + pc[c & 7],
+                 k0 + pc[(c & 7) + 1]);
+        else
+          ffma2v(s[c], s[c + 1], e1, e0, r, r, k0, k0);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < kTileN; c += 2)
+      ffma2v(s[c], s[c + 1], s[c], s[c + 1], p.scale_log2, p.scale_log2,
+             pc[c & 7], pc[(c & 7) + 1]);
+  }
+  if ((MOD & kModBias) && split) {
+    const float d0 = static_cast<float>(kbase - qrow);
+#pragma unroll
+    for (int c = 0; c < kTileN; ++c)
+      s[c] = fmaf(-slope2, fabsf(d0 + c), s[c]);
+  }
+}
+
+// Row maximum of a tile whose bias per 8 columns is sl8 (c / 8) + base, to be
+// added to s.
+__device__ __forceinline__ float biased_max(const float* s, float sl8,
+                                            float base) {
+  float mx[2];
+#pragma unroll
+  for (int i = 0; i < kTileN / 8; ++i) {
+    const float* t = s + 8 * i;
+    const float m = fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]),
+                          fmaxf(t[6], t[7])) +
+                    fmaf(sl8, static_cast<float>(i), base);
+    mx[i & 1] = i < 2 ? m : fmaxf(mx[i & 1], m);
+  }
+  return fmaxf(mx[0], mx[1]);
 }
 
 // KEEP: partial tiles also carry per-element "keep" bits -- from segment ids
@@ -725,9 +818,14 @@ __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
     }
     const int32_t* segk_b =
         seg_elem ? p.kv_seg + static_cast<int64_t>(uc.b) * p.Skv : nullptr;
-    float m_used = NEG_INF, l_sum = 0.f;
-    const float slope2 =
-        (MOD & kModBias) ? p.mod.slopes[uc.h] * 1.4426950408889634f : 0.f;
+    // a cap alone bounds the logits to +-cap_log2: no maximum is kept, p is
+    // 2^(x - m_fixed) with m_fixed = max(0, cap_log2 - 52), so p lies within
+    // 2^-121 .. 2^52 for the caps that take this path (cap_log2 <= 87) and
+    // sums of 2^18 of them stay far inside f32
+    float m_used = MOD == kModCap ? p.mod.m_fixed : NEG_INF, l_sum = 0.f;
+    const float slope2 = (MOD & kModBias) && p.mod.slopes != nullptr
+                             ? p.mod.slopes[uc.h] * 1.4426950408889634f
+                             : 0.f;
     uint32_t unit_pv = 0;
     bool ok = true;
     for (int e = 0; e < n_ent; ++e) {
@@ -784,23 +882,31 @@ __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
         tmem_ld32(s_addr + q * 32, sraw + q * 32);
       tmem_ld_wait();
       float* s = reinterpret_cast<float*>(sraw);
-      if (MOD != 0) modify_tile<MOD>(s, p, kbase, qrow, slope2);
+      float sl8 = 0.f, cbase = 0.f;  // bias of each 8 columns (kModBias)
+      if (MOD != 0) modify_tile<MOD>(s, p, kbase, qrow, slope2, &sl8, &cbase);
       if (cls == 1) mask_tile(s, rlo - kbase, rhi - kbase, keep, KEEP);
 
       uint32_t pk[16];
       if (SCORE == BSM_SCORE_SOFTMAX) {
-        // row max: three-input max, four independent chains
-        float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]);
-        float mx2 = fmaxf(s[4], s[5]), mx3 = fmaxf(s[6], s[7]);
+        float m_blk;
+        if (MOD == 0) {
+          // row max: three-input max, four independent chains
+          float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]);
+          float mx2 = fmaxf(s[4], s[5]), mx3 = fmaxf(s[6], s[7]);
 #pragma unroll
-        for (int c = 8; c < kTileN; c += 8) {
-          mx0 = fmax3(mx0, s[c], s[c + 1]);
-          mx1 = fmax3(mx1, s[c + 2], s[c + 3]);
-          mx2 = fmax3(mx2, s[c + 4], s[c + 5]);
-          mx3 = fmax3(mx3, s[c + 6], s[c + 7]);
+          for (int c = 8; c < kTileN; c += 8) {
+            mx0 = fmax3(mx0, s[c], s[c + 1]);
+            mx1 = fmax3(mx1, s[c + 2], s[c + 3]);
+            mx2 = fmax3(mx2, s[c + 4], s[c + 5]);
+            mx3 = fmax3(mx3, s[c + 6], s[c + 7]);
+          }
+          const float mx = fmax3(mx0, mx1, fmaxf(mx2, mx3));
+          m_blk = mx * p.scale_log2;
+        } else if (MOD == kModCap) {
+          m_blk = NEG_INF;  // m_used stays m_fixed
+        } else {
+          m_blk = biased_max(s, sl8, cbase);
         }
-        const float mx = fmax3(mx0, mx1, fmaxf(mx2, mx3));
-        const float m_blk = MOD != 0 ? mx : mx * p.scale_log2;
         bool rescale = false;
         float alpha = 1.f;
         if (m_blk > m_used + kRescaleLog2) {
@@ -819,12 +925,16 @@ __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
           for (int c = 32 * q; c < 32 * q + 32; c += 4) {
             // paired f32 FMA/add: the same roundings as one element at a time
             float x0, x1, x2, x3;
-            if (MOD != 0) {  // already in log2 units
-              fadd2(x0, x1, s[c], s[c + 1], neg_m, neg_m);
-              fadd2(x2, x3, s[c + 2], s[c + 3], neg_m, neg_m);
-            } else {
+            if (MOD == 0) {
               ffma2(x0, x1, s[c], s[c + 1], p.scale_log2, neg_m);
               ffma2(x2, x3, s[c + 2], s[c + 3], p.scale_log2, neg_m);
+            } else if (MOD == kModCap) {  // m_fixed is subtracted already
+              x0 = s[c], x1 = s[c + 1], x2 = s[c + 2], x3 = s[c + 3];
+            } else {
+              const float add =
+                  fmaf(sl8, static_cast<float>(c / 8), cbase + neg_m);
+              fadd2(x0, x1, s[c], s[c + 1], add, add);
+              fadd2(x2, x3, s[c + 2], s[c + 3], add, add);
             }
             const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
             const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
@@ -1444,9 +1554,14 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
     }
     const int32_t* segk_b =
         seg_elem ? p.kv_seg + static_cast<int64_t>(uc.b) * p.Skv : nullptr;
-    float m_used = NEG_INF, l_sum = 0.f;
-    const float slope2 =
-        (MOD & kModBias) ? p.mod.slopes[uc.h] * 1.4426950408889634f : 0.f;
+    // a cap alone bounds the logits to +-cap_log2: no maximum is kept, p is
+    // 2^(x - m_fixed) with m_fixed = max(0, cap_log2 - 52), so p lies within
+    // 2^-121 .. 2^52 for the caps that take this path (cap_log2 <= 87) and
+    // sums of 2^18 of them stay far inside f32
+    float m_used = MOD == kModCap ? p.mod.m_fixed : NEG_INF, l_sum = 0.f;
+    const float slope2 = (MOD & kModBias) && p.mod.slopes != nullptr
+                             ? p.mod.slopes[uc.h] * 1.4426950408889634f
+                             : 0.f;
     uint32_t unit_pv = 0;
     bool ok = true;
     for (int e = 0; e < n_ent; ++e) {
@@ -1483,23 +1598,31 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
         tmem_ld32(s_addr + q * 32, sraw + q * 32);
       tmem_ld_wait();
       float* s = reinterpret_cast<float*>(sraw);
-      if (MOD != 0) modify_tile<MOD>(s, p, kbase, qrow, slope2);
+      float sl8 = 0.f, cbase = 0.f;  // bias of each 8 columns (kModBias)
+      if (MOD != 0) modify_tile<MOD>(s, p, kbase, qrow, slope2, &sl8, &cbase);
       if (cls == 1) mask_tile(s, rlo - kbase, rhi - kbase, keep, KEEP);
 
       uint32_t pk[16];
       if (SCORE == BSM_SCORE_SOFTMAX) {
-        // row max: three-input max, four independent chains
-        float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]);
-        float mx2 = fmaxf(s[4], s[5]), mx3 = fmaxf(s[6], s[7]);
+        float m_blk;
+        if (MOD == 0) {
+          // row max: three-input max, four independent chains
+          float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]);
+          float mx2 = fmaxf(s[4], s[5]), mx3 = fmaxf(s[6], s[7]);
 #pragma unroll
-        for (int c = 8; c < kTileN; c += 8) {
-          mx0 = fmax3(mx0, s[c], s[c + 1]);
-          mx1 = fmax3(mx1, s[c + 2], s[c + 3]);
-          mx2 = fmax3(mx2, s[c + 4], s[c + 5]);
-          mx3 = fmax3(mx3, s[c + 6], s[c + 7]);
+          for (int c = 8; c < kTileN; c += 8) {
+            mx0 = fmax3(mx0, s[c], s[c + 1]);
+            mx1 = fmax3(mx1, s[c + 2], s[c + 3]);
+            mx2 = fmax3(mx2, s[c + 4], s[c + 5]);
+            mx3 = fmax3(mx3, s[c + 6], s[c + 7]);
+          }
+          const float mx = fmax3(mx0, mx1, fmaxf(mx2, mx3));
+          m_blk = mx * p.scale_log2;
+        } else if (MOD == kModCap) {
+          m_blk = NEG_INF;  // m_used stays m_fixed
+        } else {
+          m_blk = biased_max(s, sl8, cbase);
         }
-        const float mx = fmax3(mx0, mx1, fmaxf(mx2, mx3));
-        const float m_blk = MOD != 0 ? mx : mx * p.scale_log2;
         bool rescale = false;
         float alpha = 1.f;
         if (m_blk > m_used + kRescaleLog2) {
@@ -1518,12 +1641,16 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
           for (int c = 32 * q; c < 32 * q + 32; c += 4) {
             // paired f32 FMA/add: the same roundings as one element at a time
             float x0, x1, x2, x3;
-            if (MOD != 0) {  // already in log2 units
-              fadd2(x0, x1, s[c], s[c + 1], neg_m, neg_m);
-              fadd2(x2, x3, s[c + 2], s[c + 3], neg_m, neg_m);
-            } else {
+            if (MOD == 0) {
               ffma2(x0, x1, s[c], s[c + 1], p.scale_log2, neg_m);
               ffma2(x2, x3, s[c + 2], s[c + 3], p.scale_log2, neg_m);
+            } else if (MOD == kModCap) {  // m_fixed is subtracted already
+              x0 = s[c], x1 = s[c + 1], x2 = s[c + 2], x3 = s[c + 3];
+            } else {
+              const float add =
+                  fmaf(sl8, static_cast<float>(c / 8), cbase + neg_m);
+              fadd2(x0, x1, s[c], s[c + 1], add, add);
+              fadd2(x2, x3, s[c + 2], s[c + 3], add, add);
             }
             const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
             const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
@@ -1797,12 +1924,20 @@ cudaError_t launch_score(const FwdParams& p, const CUtensorMap& tq,
   // the kernel with decoupled query tiles, and so do the other masks below
   // 4096 keys (causal S=2048: 11 % faster there; from 4096 keys on, the
   // lockstep kernel's shared K/V stream is 2-6 % faster).
+  // Modified scores take it at every length: their softmax, not the tensor
+  // core, sets the pace, and its turns in the lockstep kernel leave half the
+  // score warps waiting (causal S=8192, 32/8 heads: cap 50 672 us there, 623
+  // here; bias 618 and 524; both 1049 and 757).
   const bool dt = p.dense == nullptr && p.D == 128 &&
-                  ((p.flags & BSM_MASK_SEGMENT) != 0 || p.Skv < 4096);
+                  (MOD != 0 || (p.flags & BSM_MASK_SEGMENT) != 0 ||
+                   p.Skv < 4096);
   if (dt) return launch_dt<SCORE, MOD>(p, tq, tk, tv, grid, stream);
+  if constexpr (MOD == 0) {
+    if (p.D == 128 && pp)
+      return launch_one<128, SCORE, MOD, true>(p, tq, tk, tv, grid, stream);
+  }
   if (p.D == 128)
-    return pp ? launch_one<128, SCORE, MOD, true>(p, tq, tk, tv, grid, stream)
-              : launch_one<128, SCORE, MOD, false>(p, tq, tk, tv, grid, stream);
+    return launch_one<128, SCORE, MOD, false>(p, tq, tk, tv, grid, stream);
   if (p.D == 64)  // head dim 64 uses the instance without alternation
     return launch_one<64, SCORE, MOD, false>(p, tq, tk, tv, grid, stream);
   return cudaErrorInvalidValue;
@@ -1836,7 +1971,12 @@ cudaError_t launch_splash_fwd(const FwdParams& p, const CUtensorMap& tq,
   const int grid = fwd_grid_size(p, num_sms);
   if (p.score == BSM_SCORE_POINTWISE)
     return launch_score<BSM_SCORE_POINTWISE, 0>(p, tq, tk, tv, grid, stream);
-  switch (p.mod.kind) {
+  // a cap too large for a fixed reference (see score_role) takes the instance
+  // with a running maximum, with slopes of zero
+  const int kind = p.mod.kind == kModCap && p.mod.cap_log2 > 87.f
+                       ? kModCap | kModBias
+                       : p.mod.kind;
+  switch (kind) {
     case 0:
       return launch_score<BSM_SCORE_SOFTMAX, 0>(p, tq, tk, tv, grid, stream);
     case kModCap:

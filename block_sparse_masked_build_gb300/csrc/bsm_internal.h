@@ -60,6 +60,12 @@ struct ScoreMod {
   int32_t kind;         // kModCap | kModBias; 0 = unmodified scores
   float cap_e;          // 2 log2(e) scale / cap: tanh from exp2(cap_e * q.k)
   float cap_log2;       // cap * log2(e)
+  // cap_log2 * tanh(scale S / cap) = S * (poly[0] + poly[1] S^2 + ...) for
+  // |S| <= poly_max (negative: nowhere), and with wide[] for |S| <= wide_max
+  float poly[4], poly_max;
+  float wide[7], wide_max;
+  float m_fixed;        // see kModCap's softmax in bsm_fwd.cu
+  float inv_cap2;       // 1 / cap_log2^2
   const float* slopes;  // [H], or null
 };
 

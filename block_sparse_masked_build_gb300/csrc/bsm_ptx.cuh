@@ -364,6 +364,42 @@ __device__ __forceinline__ void fadd2(float& d0, float& d1, float a0, float a1,
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
+// (d0, d1) = (a0 * b0, a1 * b1) on the paired f32 pipe.
+__device__ __forceinline__ void fmul2v(float& d0, float& d1, float a0,
+                                       float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// (d0, d1) = c[0] + c[1] v + ... + c[N - 1] v^(N - 1) at v = (a0^2, a1^2), on
+// the paired f32 pipe.
+template <int N>
+__device__ __forceinline__ void poly_sq2(float& d0, float& d1, float a0,
+                                         float a1, const float* c) {
+  float v0, v1;
+  fmul2v(v0, v1, a0, a1, a0, a1);
+  ffma2(d0, d1, v0, v1, c[N - 1], c[N - 2]);
+#pragma unroll
+  for (int i = N - 3; i >= 0; --i) ffma2v(d0, d1, d0, d1, v0, v1, c[i], c[i]);
+}
+
+// max(|a|, |b|, |c|) (sm_100 and later).
+__device__ __forceinline__ float fmax3_abs(float a, float b, float c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// min(a, b), NaN if either is.
+__device__ __forceinline__ float fmin_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // 32-byte store of eight words; `p` must be 32-byte aligned.
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t w[8]) {
   asm volatile(

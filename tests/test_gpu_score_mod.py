@@ -176,6 +176,15 @@ def test_negative_and_zero_slopes():
     run(q, k, v, do, 0, slopes=torch.tensor([-0.02, 0.0]))
 
 
+def test_rising_bias_past_the_last_query():
+    # a bias that grows with the distance, no mask, a ragged end: queries past
+    # the last one, whose bias alone would overflow, must not reach dK and dV
+    q, k, v, do = inputs("rise", 1, 1, 1, 200, 333, 128)
+    run(q, k, v, do, 0, slopes=torch.tensor([-2.0]))
+    q, k, v, do = inputs("rise2", 1, 1, 1, 20, 2000, 128)
+    run(q, k, v, do, 0, slopes=torch.tensor([-1.0]))
+
+
 def test_no_modification_is_the_unmodified_call():
     q, k, v, do = (t.cuda() for t in inputs("none", 1, 2, 2, 300, 300, 128))
     a = bsm.splash_attention(q, k, v)
