@@ -7,6 +7,7 @@ library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -196,6 +197,40 @@ def lib():
                     f"expects {ABI_VERSION}: rebuild the library")
             _lib = loaded
     return _lib
+
+
+_fast = None
+_FAST_NAMES = ("bsm_mask_info_bytes", "bsm_build_mask_info",
+               "bsm_splash_fwd_mod", "bsm_splash_bwd_mod",
+               "bsm_splash_bwd_workspace_bytes", "bsm_kv_append",
+               "bsm_paged_attention", "bsm_splash_fwd_workspace_bytes",
+               "bsm_paged_attention_workspace_bytes")
+
+
+def fast(on_status):
+    """_bsm_torch, the library's calls from torch tensors, bound to the loaded
+    library; False where it has not been built (ctypes then serves alone).
+    on_status: raises for a failing status."""
+    global _fast
+    if _fast is None:
+        loaded = lib()
+        with _lock:
+            if _fast is None:
+                _fast = _load_fast(loaded, on_status)
+    return _fast
+
+
+def _load_fast(loaded, on_status):
+    path = os.path.join(HERE, "_bsm_torch.so")
+    if not os.path.exists(path):
+        return False
+    spec = importlib.util.spec_from_file_location("_bsm_torch", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.bind(on_status, {
+        n: ctypes.cast(getattr(loaded, n), ctypes.c_void_p).value
+        for n in _FAST_NAMES})
+    return module
 
 
 def last_error() -> str:

@@ -62,6 +62,17 @@ def _elsewhere(dev) -> bool:
         dev.index != torch.cuda.current_device()
 
 
+def _fast():
+    """The module that calls the library straight from tensors, or False."""
+    return _lib._fast or _lib.fast(_check)
+
+
+def _fast_stream(stream) -> int | None:
+    """A given stream's handle; None leaves the choice (the tensors' device's
+    current stream) to the call."""
+    return None if stream is None else _stream_handle(stream)
+
+
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -545,6 +556,21 @@ def build_mask_info(flags: int, B: int, Sq: int, Skv: int, block_q: int = 128,
                     kv_segment_ids=None, device=None, stream=None,
                     dense_bits=None) -> MaskInfo:
     """Allocate the mask-info buffer with torch and build the tables."""
+    fast = _fast()
+    if fast:
+        if device is None:
+            index = None if q_segment_ids is None else \
+                q_segment_ids.device.index
+        else:
+            index = torch.device(device).index
+        info = MaskInfoStruct()
+        buf = fast.build_mask_info(
+            ctypes.addressof(info), flags, window, q_segment_ids,
+            kv_segment_ids, B, Sq, Skv, block_q, block_kv, index, dense_bits,
+            _fast_stream(stream))
+        if buf is None:
+            raise BsmError(_lib.BSM_ERR_INVALID_ARG, bsm_last_error())
+        return MaskInfo(info, buf, dense_bits)
     nbytes = bsm_mask_info_bytes(flags, window, B, Sq, Skv, block_q, block_kv)
     if nbytes == 0:
         raise BsmError(_lib.BSM_ERR_INVALID_ARG, bsm_last_error())
@@ -597,6 +623,11 @@ def kv_append(cache: KVCache, page_table, lens, k_new, v_new, *, n_new=None,
     (None: all T).  One scale per page and head, a power of two; a page that
     already holds tokens keeps or raises its scale (include/bsm.h has the
     rule).  ``lens`` is not changed: advance it before attending."""
+    fast = _fast()
+    if fast:
+        return fast.kv_append(
+            cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale,
+            page_table, lens, k_new, v_new, n_new, _fast_stream(stream))
     bsm_kv_append(cache, page_table, lens, k_new, v_new, n_new, stream)
 
 
@@ -610,6 +641,14 @@ def paged_attention(q, cache: KVCache, page_table, lens, *,
     ``window`` > 0 keeps the last ``window`` keys of each query; scale,
     ``softcap`` and ``alibi_slopes`` as in :func:`splash_attention`.  Rows
     that see no key are 0 with logsumexp -inf.  Returns (out, lse)."""
+    fast = _fast()
+    if fast:
+        return fast.paged_attention(
+            cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale,
+            page_table, lens, q, scale, window, softcap, alibi_slopes, out,
+            lse, return_lse, _fast_stream(stream))
+    if q.dim() != 4:
+        raise ValueError("q must be [B, H, T, D]")
     B, H, T, D = q.shape
     if scale is None:
         scale = 1.0 / math.sqrt(D)
@@ -650,10 +689,16 @@ def splash_attention_bwd(q, k, v, out, lse, dout, *,
                                     window, q_segment_ids, kv_segment_ids,
                                     device=q.device, stream=stream,
                                     dense_bits=bits)
+    sm = score == SCORE_SOFTMAX
+    fast = _fast()
+    if fast:
+        return fast.splash_bwd(
+            q, k, v, out if sm else None, lse if sm else None, dout,
+            ctypes.addressof(mask_info.struct), q_segment_ids, kv_segment_ids,
+            scale, score, softcap, alibi_slopes, _fast_stream(stream))
     dq = torch.empty_like(q)
     dk = torch.empty_like(k)
     dv = torch.empty_like(v)
-    sm = score == SCORE_SOFTMAX
     bsm_splash_bwd(q, k, v, out if sm else None, lse if sm else None, dout,
                    mask_info, q_segment_ids, kv_segment_ids, scale, score, dq,
                    dk, dv, stream, softcap=softcap, alibi_slopes=alibi_slopes)
@@ -732,7 +777,7 @@ def splash_attention(q, k, v, *, mask_flags: int = MASK_CAUSAL,
     Skv = k.shape[2]
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    host = q.device.type == "cpu"
+    host = q.is_cpu
     dev = torch.device("cuda", torch.cuda.current_device()) if host \
         else q.device
     want_lse = return_lse and score == SCORE_SOFTMAX
@@ -763,6 +808,11 @@ def splash_attention(q, k, v, *, mask_flags: int = MASK_CAUSAL,
         mask_info = build_mask_info(mask_flags, B, Sq, Skv, block_q, block_kv,
                                     window, qs, ks, device=dev, stream=stream,
                                     dense_bits=bits)
+    fast = _fast()
+    if fast and not host:
+        return fast.splash_fwd(
+            q, k, v, ctypes.addressof(mask_info.struct), qs, ks, scale, score,
+            softcap, alibi_slopes, out, lse, want_lse, _fast_stream(stream))
     od = torch.empty((B, H, Sq, D), dtype=torch.bfloat16, device=dev) \
         if (host or out is None) else out
     ld = None

@@ -115,7 +115,13 @@ def test_attention_refusals(lib):
     assert "workspace" in _lib.last_error()
 
 
-def test_python_checks():
+@pytest.mark.parametrize("binding", ["tensors", "ctypes"])
+def test_python_checks(binding, lib, monkeypatch):
+    # the module that calls the library from tensors, and ctypes alone
+    if binding == "ctypes":
+        monkeypatch.setattr(bsm.api, "_fast", lambda: False)
+    else:
+        assert bsm.api._fast()
     k, v, ks, vs = ref.random_cache(3, 2, 16, 64, 1)
     cache = bsm.KVCache(k, v, ks, vs)
     assert cache.struct.num_pages == 3 and cache.struct.page_size == 16
@@ -152,6 +158,15 @@ def test_python_checks():
     with pytest.raises(ValueError):
         bsm.paged_attention(q, cache, table, lens,
                             lse=torch.zeros(1, 4, 1, dtype=torch.float64))
+    if binding == "ctypes":
+        return  # the library's own checks come after a CUDA workspace there
+    for softcap in (-1.0, float("nan")):
+        with pytest.raises(bsm.BsmError, match="softcap"):
+            bsm.paged_attention(q, cache, table, lens, softcap=softcap)
+    with pytest.raises(bsm.BsmError, match="window"):
+        bsm.paged_attention(q, cache, table, lens, window=-1)
+    with pytest.raises(bsm.BsmError, match="multiple"):
+        bsm.paged_attention(q[:, :3], cache, table, lens)
 
 
 def test_reference_rounding():
