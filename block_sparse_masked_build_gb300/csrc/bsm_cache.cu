@@ -118,7 +118,7 @@ __device__ __forceinline__ float block_scale(float amax) {
 // Bound by memory for prompts and by latency for single tokens (a load, a
 // block maximum, a store).
 template <int NCH>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, NCH <= 8 ? 8 : 4)
     kv_append_kernel(const AppendParams p) {
   const int b = blockIdx.z;
   const int h = blockIdx.y >> 1;
@@ -370,78 +370,85 @@ __device__ __forceinline__ PaPlan plan_of(const PagedParams& p, int len) {
   return s;
 }
 
-// Scans the lengths with the whole block (kPaThreads threads).  Returns the
-// number of units of one item row (heads and row tiles taken once), and, for
-// `seq` >= 0, the units before that sequence in *before.
-__device__ __forceinline__ int64_t scan_units(const PagedParams& p, int seq,
-                                              int64_t* before) {
-  __shared__ long long part[2][kPaWarps];
-  long long all = 0, head = 0;
-  for (int b = threadIdx.x; b < p.B; b += kPaThreads) {
-    const int n = plan_of(p, p.lens[b]).n_units;
-    all += n;
-    if (b < seq) head += n;
+// a * b / c, in 32 bits where that is enough (a 64-bit division takes some
+// hundred instructions, and small calls are bound by latency).
+__device__ __forceinline__ int64_t mul_div(int64_t a, int64_t b, int64_t c) {
+  if (((a | b) < (1 << 15) || (a < 1024 && b < (1 << 21))) &&
+      c < (int64_t{1} << 31))
+    return static_cast<uint32_t>(a) * static_cast<uint32_t>(b) /
+           static_cast<uint32_t>(c);
+  return a * b / c;
+}
+
+// Where the units of an item row (one head and row tile) lie: the sum over all
+// sequences, and of those before one of them.
+struct PaScan {
+  int64_t all, before;
+};
+
+// One warp's scan of the lengths, every warp on its own (no barrier): lane i
+// takes `chunk` sequences in order.  n: its sequences' units.
+__device__ __forceinline__ int lane_units(const PagedParams& p, int chunk,
+                                          int64_t* n) {
+  const int b0 = (threadIdx.x % 32) * chunk;
+  int64_t sum = 0;
+  for (int i = 0; i < chunk; ++i)
+    if (b0 + i < p.B) sum += plan_of(p, p.lens[b0 + i]).n_units;
+  *n = sum;
+  return b0;
+}
+
+__device__ __forceinline__ PaScan scan_before(const PagedParams& p, int seq) {
+  const int chunk = (p.B + 31) / 32;
+  int64_t all = 0, head = 0;
+  // interleaved: both sums, whatever the order
+  for (int i = 0; i < chunk; ++i) {
+    const int b = i * 32 + threadIdx.x % 32;
+    if (b < p.B) {
+      const int n = plan_of(p, p.lens[b]).n_units;
+      all += n;
+      if (b < seq) head += n;
+    }
   }
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) {
     all += __shfl_xor_sync(0xffffffffu, all, d);
     head += __shfl_xor_sync(0xffffffffu, head, d);
   }
-  if (threadIdx.x % 32 == 0) {
-    part[0][threadIdx.x / 32] = all;
-    part[1][threadIdx.x / 32] = head;
-  }
-  __syncthreads();
-  all = head = 0;
-#pragma unroll
-  for (int w = 0; w < kPaWarps; ++w) {
-    all += part[0][w];
-    head += part[1][w];
-  }
-  if (before != nullptr) *before = head;
-  __syncthreads();
-  return all;
+  return PaScan{all, head};
 }
 
-// The sequence that holds unit u of one item row times `per` items (whole
-// block): the b with start(b) <= u < start(b + 1), and its start.
+// Sums all units (of one item row) and finds the sequence that holds the unit
+// `u_of(total)` of `per` item rows per sequence: the b with start(b) <= u <
+// start(b + 1).  Whole warps; the same in every one.
+template <class F>
 __device__ __forceinline__ int find_sequence(const PagedParams& p, int per,
-                                             int64_t u, int64_t* start) {
-  __shared__ int found;
-  __shared__ long long found_start, warp_sum[kPaWarps];
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  long long base = 0;
-  if (threadIdx.x == 0) found = p.B;
-  __syncthreads();
-  for (int b0 = 0; b0 < p.B; b0 += kPaThreads) {
-    const int b = b0 + threadIdx.x;
-    const long long n =
-        b < p.B ? static_cast<long long>(plan_of(p, p.lens[b]).n_units) * per
-                : 0;
-    long long inc = n;  // inclusive scan over the warp
+                                             F&& u_of, int64_t* start) {
+  const int lane = threadIdx.x % 32;
+  const int chunk = (p.B + 31) / 32;
+  int64_t n;
+  int b = lane_units(p, chunk, &n);
+  int64_t inc = n;
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += v;
-    }
-    if (lane == 31) warp_sum[warp] = inc;
-    __syncthreads();
-    long long at = base + inc - n, total = 0;
-#pragma unroll
-    for (int w = 0; w < kPaWarps; ++w) {
-      if (w < warp) at += warp_sum[w];
-      total += warp_sum[w];
-    }
-    if (n > 0 && at <= u && u < at + n) {
-      found = b;
-      found_start = at;
-    }
-    base += total;
-    __syncthreads();
-    if (found < p.B) break;
+  for (int d = 1; d < 32; d *= 2) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += v;
   }
-  *start = found_start;
-  return found;
+  const int64_t u = u_of(__shfl_sync(0xffffffffu, inc, 31));
+  int64_t at = (inc - n) * per;
+  const unsigned has =
+      __ballot_sync(0xffffffffu, u >= 0 && n > 0 && at <= u && u < inc * per);
+  if (has == 0) return -1;
+  const int owner = __ffs(has) - 1;
+  if (lane == owner)
+    for (;; ++b) {
+      const int64_t m =
+          static_cast<int64_t>(plan_of(p, p.lens[b]).n_units) * per;
+      if (u < at + m) break;
+      at += m;
+    }
+  *start = __shfl_sync(0xffffffffu, at, owner);
+  return __shfl_sync(0xffffffffu, b, owner);
 }
 
 // CTAs that get work: at least two units each, so that a CTA's first loads
@@ -850,18 +857,25 @@ __global__ void __launch_bounds__(kPaThreads, kPaPerSm<D, NT>)
   const int rows = p.H / p.H_kv * p.T;
   const int tiles = (rows + 8 * NT - 1) / (8 * NT);
   const int per = p.H_kv * tiles;
-  const int64_t units = scan_units(p, -1, nullptr) * per;
-  const int64_t busy = busy_ctas(units, gridDim.x);
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < p.B; b += kPaThreads) {
       const int len = p.lens[b];
       if (len != plan_of(p, len).len) record_bad_index(b, -1, len);
     }
-  if (blockIdx.x >= busy) return;
-  int64_t u = blockIdx.x * units / busy;
-  const int64_t end = (blockIdx.x + 1) * units / busy;
-  int64_t start;
-  int b = find_sequence(p, per, u, &start);
+  int64_t u = -1, end = -1, start;
+  int b = find_sequence(
+      p, per,
+      [&](int64_t all) {
+        const int64_t units = all * per;
+        const int64_t busy = busy_ctas(units, gridDim.x);
+        if (blockIdx.x < busy) {
+          u = mul_div(blockIdx.x, units, busy);
+          end = mul_div(blockIdx.x + 1, units, busy);
+        }
+        return u;
+      },
+      &start);
+  if (b < 0) return;
   while (u < end) {
     const PaPlan plan = plan_of(p, p.lens[b]);
     const int64_t row_units = static_cast<int64_t>(plan.n_units) * per;
@@ -898,8 +912,8 @@ __global__ void __launch_bounds__(kPaThreads)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int r = blockIdx.x * kPaWarps + warp;
   const int rr = item % tiles * R + r;
-  int64_t before;
-  const int64_t units = scan_units(p, b, &before) * per;
+  const PaScan scan = scan_before(p, b);
+  const int64_t units = scan.all * per;
   const int n = plan_of(p, p.lens[b]).n_units;
   // every block waits for the attention grid, so that work after this kernel
   // on the stream sees what that grid wrote itself
@@ -914,15 +928,18 @@ __global__ void __launch_bounds__(kPaThreads)
     return;
   }
   const int64_t busy = busy_ctas(units, grid);
-  const int64_t u0 = before * per + static_cast<int64_t>(item) * n;
+  const int64_t u0 = scan.before * per + static_cast<int64_t>(item) * n;
   // the CTAs that hold its first and last unit
-  const int64_t c0 = ((u0 + 1) * busy - 1) / units;
-  const int64_t c1 = ((u0 + n) * busy - 1) / units;
+  const int64_t c0 = mul_div(u0 + 1, busy, units) -
+                     (mul_div(u0 + 1, busy, units) * units == (u0 + 1) * busy);
+  const int64_t c1 = mul_div(u0 + n, busy, units) -
+                     (mul_div(u0 + n, busy, units) * units == (u0 + n) * busy);
   if (c0 == c1) return;  // whole in one CTA, which wrote it
   const float NEG_INF = __int_as_float(0xff800000);
+  // the item begins within the first CTA's run and before every other's
+  constexpr int64_t kPart = R * (D + 2);
   auto part_of = [&](int64_t c) {
-    return p.parts + (c * 2 + (c * units / busy > u0 ? 0 : 1)) *
-                         static_cast<int64_t>(R * (D + 2));
+    return p.parts + (c * 2 + (c == c0 ? 1 : 0)) * kPart;
   };
   float mx = NEG_INF;
   for (int64_t c = c0 + lane; c <= c1; c += 32)
@@ -932,15 +949,37 @@ __global__ void __launch_bounds__(kPaThreads)
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
   const float base = mx == NEG_INF ? 0.f : mx;
   float sum = 0.f;
-#pragma unroll 4
-  for (int64_t c = c0; c <= c1; ++c) {
-    const float* part = part_of(c);
-    const float f = ex2_approx(part[R * D + r] - base);
-    sum = fmaf(part[R * D + R + r], f, sum);
+  for (int64_t c = c0; c <= c1; c += 32) {
+    // lane i: the weight of part c + i
+    float f = 0.f;
+    if (c + lane <= c1) {
+      const float* part = part_of(c + lane) + R * D + r;
+      f = ex2_approx(part[0] - base);
+      sum = fmaf(part[R], f, sum);
+    }
+    const int m = static_cast<int>(min(c1 - c + 1, static_cast<int64_t>(32)));
+#pragma unroll 8
+    for (int i = 0; i < m; ++i) {
+      const float w = __shfl_sync(0xffffffffu, f, i);
+      const float* o = part_of(c + i) + r * D + lane * kPer;
+      float v[kPer];
+      if (kPer == 4) {
+        const float4 q = *reinterpret_cast<const float4*>(o);
+        v[0] = q.x;
+        v[1] = q.y;
+        v[kPer - 2] = q.z;
+        v[kPer - 1] = q.w;
+      } else {
+        const float2 q = *reinterpret_cast<const float2*>(o);
+        v[0] = q.x;
+        v[1] = q.y;
+      }
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      x[i] = fmaf(part[r * D + lane * kPer + i], f, x[i]);
+      for (int j = 0; j < kPer; ++j) x[j] = fmaf(v[j], w, x[j]);
+    }
   }
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   write_row<kPer>(p, b, head, t, lane * kPer, base, sum, x);
 }
 
