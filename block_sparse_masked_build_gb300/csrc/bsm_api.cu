@@ -902,12 +902,10 @@ bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
   bsm::PagedParams p;
   s = check_mod(mod, scale, BSM_SCORE_SOFTMAX, &p.mod);
   if (s != BSM_OK) return s;
-  p.cap_x = p.mod.kind & bsm::kModCap
-                ? static_cast<float>(2.0 * 1.4426950408889634 /
-                                     static_cast<double>(mod->softcap))
-                : 0.f;
-  if (!std::isfinite(p.cap_x))
-    return fail(BSM_ERR_INVALID_ARG, "softcap out of range");
+  p.scale_x = p.mod.kind & bsm::kModCap
+                  ? p.mod.cap_e
+                  : static_cast<float>(static_cast<double>(scale) *
+                                       1.4426950408889634);
   if (B == 0 || T == 0 || H == 0) return BSM_OK;
   s = check_cache_memory(cache, page_table, max_pages, lens);
   if (s == BSM_OK) s = check_view(q, B, H, T, "q");
@@ -936,6 +934,7 @@ bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
   p.num_pages = cache->num_pages;
   p.H_kv = cache->H_kv;
   p.page_size = cache->page_size;
+  for (p.page_shift = 4; (1 << p.page_shift) < p.page_size;) ++p.page_shift;
   p.D = cache->D;
   p.table = page_table;
   p.table_stride = table_stride;
@@ -945,7 +944,6 @@ bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
   p.H = H;
   p.T = T;
   p.window = window;
-  p.scale = scale;
   p.q = static_cast<const uint16_t*>(q->data);
   p.q_sb = q->strides[0];
   p.q_sh = q->strides[1];

@@ -218,14 +218,17 @@ constexpr int kPaWarps = 4;
 constexpr int kPaThreads = 32 * kPaWarps;
 constexpr int kPaGroup = 16;  // tokens a warp works on at a time
 constexpr int kPaStages = 4;  // groups a warp keeps in flight
+constexpr int kPaRunCost = 4; // see PaPlan
 constexpr float kPUp = 512.f; // p's factor before it becomes f16
 
-template <int D>
+template <int D, int NT>
 struct PaCfg {
   static constexpr int kHalf = kPaGroup * D;  // bytes of a group's K or V
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kOffScale = kPaWarps * kPaStages * kStage;
-  static constexpr int kSmem = kOffScale + kPaWarps * kPaStages * 8;
+  // two row tiles: their query fragments
+  static constexpr int kOffQ = kOffScale + kPaWarps * kPaStages * 8;
+  static constexpr int kSmem = kOffQ + (NT > 1 ? NT * D / 32 * 512 : 0);
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src,
@@ -254,6 +257,12 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
                : "r"(a)
                : "memory");
   return r;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y,
+                                       uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x),
+               "r"(y), "r"(z), "r"(w)
+               : "memory");
 }
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 r;
@@ -299,29 +308,29 @@ __device__ __forceinline__ uint32_t piece_at(int tr, int c) {
          (((((tr & 1) << 2) | c) ^ (((tr >> 1) & 3) << 1)) << 4);
 }
 
-// Starts the copy of one group of 16 tokens into a stage (whole warp).
-// Tokens outside [lo, hi) and pages out of range are filled with zeros; a
-// scale of zero marks the latter.
+// Starts the copy of one group of 16 tokens from `tok` on into a stage (whole
+// warp).  Tokens outside [lo, hi) and pages out of range (pid < 0) are filled
+// with zeros; a scale of zero marks the latter.
 template <int D>
 __device__ __forceinline__ void load_group(const PagedParams& p,
                                            uint32_t stage, uint32_t scale_at,
-                                           int64_t head_block, int pid,
-                                           int tok, int lo, int hi) {
+                                           int head, int pid, int tok, int lo,
+                                           int hi) {
   const int lane = threadIdx.x % 32;
   const bool ok = pid >= 0;
-  const int64_t block = (ok ? pid : 0) * static_cast<int64_t>(p.H_kv) +
-                        head_block;
+  const int64_t block = static_cast<int64_t>(ok ? pid : 0) * p.H_kv + head;
   const int64_t off =
-      (block * p.page_size + (tok & (p.page_size - 1))) * D;
+      ((block << p.page_shift) + (tok & (p.page_size - 1))) * D + lane * 16;
   constexpr int kPieces = kPaGroup * D / 16;
+  const bool whole = ok && tok >= lo && tok + kPaGroup <= hi;
 #pragma unroll
   for (int i = 0; i < kPieces / 32; ++i) {
     const int c = i * 32 + lane;
     const int tr = c / (D / 16);
-    const bool keep = ok && tok + tr >= lo && tok + tr < hi;
+    const bool keep = whole || (ok && tok + tr >= lo && tok + tr < hi);
     const uint32_t at = piece_at<D>(tr, c % (D / 16));
-    cp_async16(stage + at, p.k + off + c * 16, keep);
-    cp_async16(stage + PaCfg<D>::kHalf + at, p.v + off + c * 16, keep);
+    cp_async16(stage + at, p.k + off + i * 512, keep);
+    cp_async16(stage + kPaGroup * D + at, p.v + off + i * 512, keep);
   }
   if (lane < 2)
     cp_async4(scale_at + lane * 4, (lane == 0 ? p.k_scale : p.v_scale) + block,
@@ -350,7 +359,9 @@ __device__ __forceinline__ void write_row(const PagedParams& p, int b,
 // 8 NT query rows); its work is its sequence's visible tokens in units of 64
 // (a group of 16 for each warp).  All units of all items, in order, are cut
 // into equal runs, one per CTA, so that unequal lengths and few long
-// sequences load every SM alike.  A CTA may start and end inside an item;
+// sequences load every SM alike.  An item counts kPaRunCost units more than
+// it has, before its first: what starting and ending a run costs (64
+// sequences of 300-12000 tokens: 160 us without, 140 with).  A CTA may start and end inside an item;
 // then it leaves its part (o, m, l) in the workspace and the join kernel adds
 // the parts up.  The cut depends on the lengths alone, which both kernels
 // read.
@@ -358,6 +369,7 @@ struct PaPlan {
   int len, lo;      // of one sequence: tokens, first visible one
   int first_group;  // of 16 tokens
   int n_groups, n_units;
+  int n_cost;  // n_units + kPaRunCost, or 0 without units
 };
 
 __device__ __forceinline__ PaPlan plan_of(const PagedParams& p, int len) {
@@ -367,6 +379,7 @@ __device__ __forceinline__ PaPlan plan_of(const PagedParams& p, int len) {
   s.first_group = s.lo / kPaGroup;
   s.n_groups = (s.len + kPaGroup - 1) / kPaGroup - s.first_group;
   s.n_units = (s.n_groups + kPaWarps - 1) / kPaWarps;
+  s.n_cost = s.n_units > 0 ? s.n_units + kPaRunCost : 0;
   return s;
 }
 
@@ -393,7 +406,7 @@ __device__ __forceinline__ int lane_units(const PagedParams& p, int chunk,
   const int b0 = (threadIdx.x % 32) * chunk;
   int64_t sum = 0;
   for (int i = 0; i < chunk; ++i)
-    if (b0 + i < p.B) sum += plan_of(p, p.lens[b0 + i]).n_units;
+    if (b0 + i < p.B) sum += plan_of(p, p.lens[b0 + i]).n_cost;
   *n = sum;
   return b0;
 }
@@ -405,7 +418,7 @@ __device__ __forceinline__ PaScan scan_before(const PagedParams& p, int seq) {
   for (int i = 0; i < chunk; ++i) {
     const int b = i * 32 + threadIdx.x % 32;
     if (b < p.B) {
-      const int n = plan_of(p, p.lens[b]).n_units;
+      const int n = plan_of(p, p.lens[b]).n_cost;
       all += n;
       if (b < seq) head += n;
     }
@@ -443,7 +456,7 @@ __device__ __forceinline__ int find_sequence(const PagedParams& p, int per,
   if (lane == owner)
     for (;; ++b) {
       const int64_t m =
-          static_cast<int64_t>(plan_of(p, p.lens[b]).n_units) * per;
+          static_cast<int64_t>(plan_of(p, p.lens[b]).n_cost) * per;
       if (u < at + m) break;
       at += m;
     }
@@ -473,7 +486,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
                                            int b, const PaPlan& plan, int hkv,
                                            int row0, int g0, int g1,
                                            float* part) {
-  using C = PaCfg<D>;
+  using C = PaCfg<D, NT>;
   constexpr int kSteps = D / 16;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
@@ -481,9 +494,15 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
   const float NEG_INF = __int_as_float(0xff800000);
   const int len = plan.len, lo = plan.lo, first_group = plan.first_group;
 
-  // query fragments: row row0 + 8 nt + g, elements 64 h + 16 t .. + 15
+  // query fragments: row row0 + 8 nt + g, elements 64 h + 16 t .. + 15.  One
+  // tile's stay in registers; two tiles' (32 registers at D = 128, which the
+  // third CTA of an SM would not get) are read from shared memory, where the
+  // four warps, which hold the same ones, leave them
   uint32_t qf[NT][kSteps][2];
-  float q_mul[NT][2];  // of rows 8 nt + 2 t, + 1: scale * 2^(row's exponent)
+  const uint32_t q_at = smem_u32(smem) + C::kOffQ + lane * 16;
+  // of rows 8 nt + 2 t, + 1: 2^(row's exponent) times what makes q.k the
+  // exponent of e^(2 x / cap), or x, in log2 units
+  float q_mul[NT][2];
   float slope2[NT][2];
   int pos[NT][2];  // positions of those rows; -1 for rows that do not exist
 #pragma unroll
@@ -525,13 +544,20 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
       for (int i = 0; i < 2; ++i)
         qf[nt][s][i] = pack_f16x2(bf16_lo(w[s][i]) * down,
                                   bf16_hi(w[s][i]) * down);
+    if (NT > 1) {
+#pragma unroll
+      for (int s = 0; s < kSteps; s += 2)
+        if (warp == nt * 2 + (s / 2 & 1))
+          sts128(q_at + (nt * (kSteps / 2) + s / 2) * 512, qf[nt][s][0],
+                 qf[nt][s][1], qf[nt][s + 1][0], qf[nt][s + 1][1]);
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       // lane (2 t + i) * 4 holds row 2 t + i's factor
       const float u = __shfl_sync(0xffffffffu, up, (2 * t + i) * 4);
       const int rr = row0 + nt * 8 + 2 * t + i;
       const bool live = rr < rows;
-      q_mul[nt][i] = u * p.scale;
+      q_mul[nt][i] = u * p.scale_x;
       pos[nt][i] = live ? len - p.T + rr % p.T : -1;
       slope2[nt][i] = (p.mod.kind & kModBias) && live
                           ? p.mod.slopes[hkv * G + rr / p.T] *
@@ -539,6 +565,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
                           : 0.f;
     }
   }
+  if (NT > 1) __syncthreads();
   // a group none of whose tokens any live row masks
   const int pos_min = len - p.T, pos_max = len - 1;
 
@@ -561,32 +588,62 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
   const uint32_t ring = smem_u32(smem) + warp * kPaStages * C::kStage;
   const uint32_t scales = smem_u32(smem) + C::kOffScale + warp * kPaStages * 8;
   const int* table = p.table + static_cast<int64_t>(b) * p.table_stride;
-  auto issue = [&](int gi) {  // group number gi of the plan
-    if (gi < g1) {
-      const int tok = (first_group + gi) * kPaGroup;
-      int pid = table[tok / p.page_size];
-      if (pid < 0 || pid >= p.num_pages) {
-        if (lane == 0) record_bad_index(b, tok / p.page_size, pid);
-        pid = -1;
-      }
-      const int st = ((gi - g0) / kPaWarps) % kPaStages;
-      load_group<D>(p, ring + st * C::kStage, scales + st * 8, hkv, pid, tok,
-                    lo, len);
-    }
+  // the page of a group; -1 past the run's end and for a page out of range
+  auto page_of = [&](int gi) {
+    if (gi >= g1) return -1;
+    const int slot = (first_group + gi) >> (p.page_shift - 4);
+    const int pid = table[slot];
+    if (static_cast<uint32_t>(pid) < static_cast<uint32_t>(p.num_pages))
+      return pid;
+    if (lane == 0) record_bad_index(b, slot, pid);
+    return -1;
+  };
+  auto issue = [&](int gi, int st, int pid) {
+    if (gi < g1)
+      load_group<D>(p, ring + st * C::kStage, scales + st * 8, hkv, pid,
+                    (first_group + gi) * kPaGroup, lo, len);
     cp_async_commit();
   };
+  // the ring's first groups, their pages looked up together; from then on a
+  // group's page is looked up one turn before its copy starts
+  int pid[kPaStages];
 #pragma unroll
-  for (int i = 0; i < kPaStages - 1; ++i) issue(g0 + warp + i * kPaWarps);
+  for (int i = 0; i < kPaStages; ++i) pid[i] = page_of(g0 + warp + i * kPaWarps);
+#pragma unroll
+  for (int i = 0; i < kPaStages - 1; ++i)
+    issue(g0 + warp + i * kPaWarps, i, pid[i]);
+  int next_pid = pid[kPaStages - 1];
+  // distance of the lane's first token to the rows' positions (negative),
+  // kept as it moves on: exact in f32
+  float dist[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      dist[nt][c] = static_cast<float>(
+          (first_group + g0 + warp) * kPaGroup + g - pos[nt][c]);
 
-  for (int gi = g0 + warp; gi < g1; gi += kPaWarps) {
+  int st = 0;
+  float v_inv = 1.f;  // 1 / v_ref
+  for (int gi = g0 + warp; gi < g1;
+       gi += kPaWarps, st = st + 1 == kPaStages ? 0 : st + 1) {
     cp_async_wait<kPaStages - 2>();
     __syncwarp();  // the group is in shared memory, and the one before it read
-    issue(gi + (kPaStages - 1) * kPaWarps);
-    const int st = ((gi - g0) / kPaWarps) % kPaStages;
+    issue(gi + (kPaStages - 1) * kPaWarps, st == 0 ? kPaStages - 1 : st - 1,
+          next_pid);
+    next_pid = page_of(gi + kPaStages * kPaWarps);
     const uint32_t k_at = ring + st * C::kStage, v_at = k_at + C::kHalf;
     const uint2 sc = lds64(scales + st * 8);
     const float k_scale = __uint_as_float(sc.x);
     const float v_scale = __uint_as_float(sc.y);
+    float d[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        d[nt][c] = dist[nt][c];
+        dist[nt][c] += static_cast<float>(kPaGroup * kPaWarps);
+      }
     if (k_scale == 0.f) continue;  // a page that is not there (whole warp)
     const int tok = (first_group + gi) * kPaGroup;
 
@@ -596,6 +653,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+    uint4 qs[NT];
 #pragma unroll
     for (int h = 0; h < D / 64; ++h) {
       const uint4 x = lds128(k_at + piece_at<D>(g, 4 * h + t));
@@ -606,10 +664,19 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
       for (int j = 0; j < 4; ++j) {
         const uint32_t a0 = e4m3x2_to_f16x2(xw[j]), a2 = e4m3x2_to_f16x2_hi(xw[j]);
         const uint32_t a1 = e4m3x2_to_f16x2(yw[j]), a3 = e4m3x2_to_f16x2_hi(yw[j]);
+        if (NT == 1) {
+          mma16816(s[0], a0, a1, a2, a3, qf[0][4 * h + j][0],
+                   qf[0][4 * h + j][1]);
+        } else {
+          if ((j & 1) == 0)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma16816(s[nt], a0, a1, a2, a3, qf[nt][4 * h + j][0],
-                   qf[nt][4 * h + j][1]);
+            for (int nt = 0; nt < NT; ++nt)
+              qs[nt] = lds128(q_at + (nt * (kSteps / 2) + 2 * h + j / 2) * 512);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(s[nt], a0, a1, a2, a3, (j & 1) ? qs[nt].z : qs[nt].x,
+                     (j & 1) ? qs[nt].w : qs[nt].y);
+        }
       }
     }
 
@@ -624,12 +691,10 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
         const int c = i & 1, j = tok + g + (i >> 1) * 8;
         float x = s[nt][i] * (q_mul[nt][c] * k_scale);
         if (p.mod.kind & kModCap)
-          x = fmaf(-2.f * p.mod.cap_log2,
-                   rcp_approx(ex2_approx(x * p.cap_x) + 1.f), p.mod.cap_log2);
-        else
-          x *= 1.4426950408889634f;
+          x = fmaf(-2.f * p.mod.cap_log2, rcp_approx(ex2_approx(x) + 1.f),
+                   p.mod.cap_log2);
         if (p.mod.kind & kModBias)
-          x = fmaf(slope2[nt][c], static_cast<float>(j - pos[nt][c]), x);
+          x = fmaf(slope2[nt][c], d[nt][c] + (i >> 1) * 8.f, x);
         if (!inner &&
             (j > pos[nt][c] || (p.window > 0 && pos[nt][c] - j >= p.window)))
           x = NEG_INF;
@@ -662,7 +727,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
     // moves to the new unit.  p <= 1, so p * kPUp * 2^6 <= 2^15 fits f16, and
     // what f16 flushes to zero is p below 2^-27: 2^18 such keys together
     // weigh less than the 2^-8 of the output's own rounding
-    float v_mul = v_scale / v_ref;
+    float v_mul = v_scale * v_inv;
     if (!(v_mul >= 0.015625f && v_mul <= 64.f)) {
       const float r = v_ref / v_scale;
 #pragma unroll
@@ -672,6 +737,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[nt][d][i] *= r;
       v_ref = v_scale;
+      v_inv = 1.f / v_scale;
       v_mul = 1.f;
     }
     v_mul *= kPUp;
@@ -843,7 +909,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
 // CTAs per SM of the attention kernel: three rings fit an SM's shared memory
 // at head dim 128; registers set the other limits.
 template <int D, int NT>
-constexpr int kPaPerSm = D == 64 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 3 : 2);
+constexpr int kPaPerSm = D == 64 && NT == 1 ? 4 : 3;
 
 static_assert(kPaPerSm<64, 1> <= kPaMaxPerSm, "workspace");
 
@@ -878,23 +944,31 @@ __global__ void __launch_bounds__(kPaThreads, kPaPerSm<D, NT>)
   if (b < 0) return;
   while (u < end) {
     const PaPlan plan = plan_of(p, p.lens[b]);
-    const int64_t row_units = static_cast<int64_t>(plan.n_units) * per;
-    if (u >= start + row_units) {
-      start += row_units;
+    const int64_t row_cost = static_cast<int64_t>(plan.n_cost) * per;
+    if (u >= start + row_cost) {
+      start += row_cost;
       ++b;
       continue;
     }
-    const int item = static_cast<int>((u - start) / plan.n_units);
-    const int off = static_cast<int>((u - start) % plan.n_units);
+    const int64_t within = u - start;
+    const int item = within < (int64_t{1} << 31)
+                         ? static_cast<int>(static_cast<uint32_t>(within) /
+                                            static_cast<uint32_t>(plan.n_cost))
+                         : static_cast<int>(within / plan.n_cost);
+    const int off =
+        static_cast<int>(within - static_cast<int64_t>(item) * plan.n_cost);
     const int n = static_cast<int>(
-        min(static_cast<int64_t>(plan.n_units - off), end - u));
-    float* part = nullptr;
-    if (n < plan.n_units)  // slot 0: the item began before this CTA's run
-      part = p.parts + (blockIdx.x * 2 + (off > 0 ? 0 : 1)) *
-                           static_cast<int64_t>(8 * NT * (D + 2));
-    attend_run<D, NT>(p, smem, b, plan, item / tiles, item % tiles * 8 * NT,
-                      off * kPaWarps, min((off + n) * kPaWarps, plan.n_groups),
-                      part);
+        min(static_cast<int64_t>(plan.n_cost - off), end - u));
+    // units [r0, r1) of the item
+    const int r0 = max(off - kPaRunCost, 0), r1 = off + n - kPaRunCost;
+    if (r1 > r0) {
+      float* part = nullptr;
+      if (r0 > 0 || r1 < plan.n_units)  // slot 0: an earlier CTA has the start
+        part = p.parts + (blockIdx.x * 2 + (r0 > 0 ? 0 : 1)) *
+                             static_cast<int64_t>(8 * NT * (D + 2));
+      attend_run<D, NT>(p, smem, b, plan, item / tiles, item % tiles * 8 * NT,
+                        r0 * kPaWarps, min(r1 * kPaWarps, plan.n_groups), part);
+    }
     u += n;
   }
 }
@@ -928,15 +1002,17 @@ __global__ void __launch_bounds__(kPaThreads)
     return;
   }
   const int64_t busy = busy_ctas(units, grid);
-  const int64_t u0 = scan.before * per + static_cast<int64_t>(item) * n;
   // the CTAs that hold its first and last unit
-  const int64_t c0 = mul_div(u0 + 1, busy, units) -
-                     (mul_div(u0 + 1, busy, units) * units == (u0 + 1) * busy);
-  const int64_t c1 = mul_div(u0 + n, busy, units) -
-                     (mul_div(u0 + n, busy, units) * units == (u0 + n) * busy);
+  const int64_t u0 = scan.before * per +
+                     static_cast<int64_t>(item) * (n + kPaRunCost) + kPaRunCost;
+  auto cta_of = [&](int64_t u) {  // the last c with c * units / busy <= u
+    const int64_t c = mul_div(u + 1, busy, units);
+    return c - (c * units == (u + 1) * busy);
+  };
+  const int64_t c0 = cta_of(u0), c1 = cta_of(u0 + n - 1);
   if (c0 == c1) return;  // whole in one CTA, which wrote it
   const float NEG_INF = __int_as_float(0xff800000);
-  // the item begins within the first CTA's run and before every other's
+  // the item's first unit is in the first CTA, which leaves its part in slot 1
   constexpr int64_t kPart = R * (D + 2);
   auto part_of = [&](int64_t c) {
     return p.parts + (c * 2 + (c == c0 ? 1 : 0)) * kPart;
@@ -988,12 +1064,12 @@ cudaError_t launch_paged(const PagedParams& p, int num_sms,
                          cudaStream_t stream) {
   auto kern = paged_attention_kernel<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(
-      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PaCfg<D>::kSmem);
+      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PaCfg<D, NT>::kSmem);
   if (e != cudaSuccess) return e;
   const int rows = p.H / p.H_kv * p.T;
   const int tiles = (rows + 8 * NT - 1) / (8 * NT);
   const int grid = num_sms * kPaPerSm<D, NT>;
-  kern<<<grid, kPaThreads, PaCfg<D>::kSmem, stream>>>(p);
+  kern<<<grid, kPaThreads, PaCfg<D, NT>::kSmem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

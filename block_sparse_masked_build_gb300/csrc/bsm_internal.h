@@ -162,9 +162,9 @@ struct PagedParams {
   const int32_t* lens;  // [B] tokens, the queries' own among them
   int32_t B, H, T;
   int32_t window;  // 0 = none
-  float scale;
+  int32_t page_shift;  // log2(page_size)
   ScoreMod mod;
-  float cap_x;  // 2 log2(e) / cap
+  float scale_x;  // scale * log2(e), or with a cap 2 scale log2(e) / cap
   const uint16_t* q;  // bf16 [B][H][T][D]
   int64_t q_sb, q_sh, q_ss;
   uint16_t* out;

@@ -102,7 +102,7 @@ def test_attention_refusals(lib):
     assert _attend(lib, window=-1) == INVALID
     assert _attend(lib, mod=ScoreMod(-1.0, None)) == INVALID
     assert _attend(lib, mod=ScoreMod(float("nan"), None)) == INVALID
-    assert _attend(lib, mod=ScoreMod(1e-39, None), scale=0.0) == INVALID
+    assert _attend(lib, mod=ScoreMod(1e-30, None), scale=1e20) == INVALID
     assert _attend(lib, mod=ScoreMod(0.0, 0x1002)) == INVALID
     assert _attend(lib, q=_view(0x500002)) == INVALID
     assert _attend(lib, out=_view(None)) == INVALID
