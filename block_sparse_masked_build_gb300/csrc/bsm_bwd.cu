@@ -70,9 +70,9 @@ struct BwdCfg {
   static constexpr int kOffBar = kOffList + kMaxKvTiles * 2;
   static constexpr int kSmemBytes = kOffBar + 256 + 1024;
   // modified scores, dK/dV: per elementwise warp, the lse and D_q of the
-  // step's 64 columns of its half
+  // step's 32 columns
   static constexpr int kOffStat = kOffBar + 256;
-  static constexpr int kStatBytes = 8 * 128 * 4;
+  static constexpr int kStatBytes = 16 * 64 * 4;
 };
 static_assert(BwdCfg<128>::kSmemBytes + BwdCfg<128>::kStatBytes <= 232448,
               "shared memory budget");
@@ -416,8 +416,8 @@ __device__ __forceinline__ void load4(const float* at, float r[4]) {
   r[3] = v.w;
 }
 
-// Sign of the distance bias's dependence on (column - row) for a half tile of
-// 64 columns from col0 on and the warp's 32 rows from row0 on: -1 where the
+// Sign of the distance bias's dependence on (column - row) for the 32
+// columns from col0 on and the warp's 32 rows from row0 on: -1 where the
 // columns lie after the rows, 1 before, 0 where they mix (then the bias is
 // taken column by column).  Under a causal mask visible queries (dK/dV's
 // columns) lie after the key and visible keys (dQ's) before the query.
@@ -426,11 +426,11 @@ __device__ __forceinline__ float bias_side(const BwdParams& p, int col0,
                                            int row0) {
   if (p.flags & BSM_MASK_CAUSAL) return DKDV ? -1.f : 1.f;
   if (col0 >= row0 + 31) return -1.f;
-  return col0 + 63 <= row0 ? 1.f : 0.f;
+  return col0 + 31 <= row0 ? 1.f : 0.f;
 }
 
 // P (packed to bf16) and the factor f of dS = f (dP - D_q) for one thread's
-// 64 columns with modified scores, all in log2 units:
+// 32 columns with modified scores, all in log2 units:
 //     x = cap tanh(scale S / cap) or scale S,  P = 2^(x + bias - lse),
 //     f = P (1 - tanh^2) = P (1 - x^2 / cap^2), or P.
 // tanh is the forward's: a polynomial of POLY terms where every |S| of the warp
@@ -440,14 +440,14 @@ __device__ __forceinline__ float bias_side(const BwdParams& p, int col0,
 template <int MOD, bool DKDV, bool MASK, int POLY>
 __device__ __forceinline__ void mod_p_loop(const BwdParams& p,
                                            const uint32_t* sraw,
-                                           const uint32_t vis[2],
+                                           const uint32_t vis,
                                            const float* n, float add,
                                            const float* pc, float sl8,
                                            bool split, float slope2,
                                            float dist0, float* f,
                                            uint32_t* pw) {
 #pragma unroll
-  for (int j = 0; j < 64; j += 4) {
+  for (int j = 0; j < 32; j += 4) {
     float a[4];  // what is added to x
     if (DKDV) {
       load4(n + j, a);
@@ -501,8 +501,8 @@ __device__ __forceinline__ void mod_p_loop(const BwdParams& p,
       }
       float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
       if (MASK) {
-        p0 = (vis[c >> 5] >> (c & 31)) & 1u ? p0 : 0.f;
-        p1 = (vis[c >> 5] >> ((c + 1) & 31)) & 1u ? p1 : 0.f;
+        p0 = (vis >> c) & 1u ? p0 : 0.f;
+        p1 = (vis >> (c + 1)) & 1u ? p1 : 0.f;
       }
       pw[c / 2] = pack_bf16x2(p0, p1);
       if (MOD & kModCap) {
@@ -521,7 +521,7 @@ __device__ __forceinline__ void mod_p_loop(const BwdParams& p,
 
 template <int MOD, bool DKDV>
 __device__ __forceinline__ void mod_p(const BwdParams& p, const uint32_t* sraw,
-                                      const uint32_t vis[2], const float* n,
+                                      const uint32_t vis, const float* n,
                                       int col0, int row, float slope2,
                                       float lse2_row, float* f, uint32_t* pw) {
   const int lane = threadIdx.x % 32;
@@ -538,13 +538,12 @@ __device__ __forceinline__ void mod_p(const BwdParams& p, const uint32_t* sraw,
       for (int c = 0; c < 8; ++c) pc[c] = sl * static_cast<float>(c);
   }
   const float add = sl * dist0 - (DKDV ? 0.f : lse2_row);
-  const bool full =
-      __all_sync(0xffffffffu, (vis[0] & vis[1]) == 0xffffffffu);
+  const bool full = __all_sync(0xffffffffu, vis == 0xffffffffu);
   bool near = true, wide = true;
   if (MOD & kModCap) {
     float a0 = 0.f, a1 = 0.f;
 #pragma unroll
-    for (int c = 0; c < 64; c += 4) {
+    for (int c = 0; c < 32; c += 4) {
       a0 = fmax3_abs(a0, __uint_as_float(sraw[c]), __uint_as_float(sraw[c + 1]));
       a1 = fmax3_abs(a1, __uint_as_float(sraw[c + 2]),
                      __uint_as_float(sraw[c + 3]));
@@ -572,13 +571,13 @@ __device__ __forceinline__ void mod_p(const BwdParams& p, const uint32_t* sraw,
 // columns [64, 128).  The packed P and dS of the second half go over
 // columns [32, 64), which the first half reads: the second half writes only
 // after the first half has read (h0_read).
-template <int D, int SCORE, int MOD, bool DKDV>
+template <int D, int SCORE, bool DKDV>
 __device__ __forceinline__ void bwd_elem_role(const BwdParams& p,
                                               BwdBars* bars,
                                               const uint16_t* list,
-                                              float* stats, uint32_t tmem,
-                                              int b, int hq_or_hkv,
-                                              int fixed_tile, int n_iter) {
+                                              uint32_t tmem, int b,
+                                              int hq_or_hkv, int fixed_tile,
+                                              int n_iter) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int quarter = warp % 4;  // TMEM lanes this warp may access
   const int half = (warp - 2) / 4;  // column half of S and dP
@@ -612,9 +611,7 @@ __device__ __forceinline__ void bwd_elem_role(const BwdParams& p,
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int qc = tile * kTileM + half * 64 + c * 32 + lane;
-      // queries past the end: P = 0 (with modified scores; else their zero
-      // dO alone makes them vanish, but a rising bias may overflow P)
-      l2[c] = MOD != 0 ? __int_as_float(0x7f800000) : 0.f;
+      l2[c] = 0.f;
       dl[c] = 0.f;
       if (qc < p.Sq) {
         const int64_t i = (static_cast<int64_t>(b) * p.H + hd) * p.Sq + qc;
@@ -633,24 +630,6 @@ __device__ __forceinline__ void bwd_elem_role(const BwdParams& p,
     const int col0 = tile * kTileM + half * 64;  // first column of the half
     float lse2_c[2] = {lse2_n[0], lse2_n[1]}, delta_c[2] = {delta_n[0], delta_n[1]};
     if (kStats && it + 1 < n_iter) load_stats(it + 1, lse2_n, delta_n);
-    float slope2 = 0.f;  // dK/dV: of the step's query head
-    if ((MOD & kModBias) && p.mod.slopes != nullptr)
-      slope2 = p.mod.slopes[DKDV ? hq_or_hkv * G + it / n_list : hq_or_hkv] *
-               kLog2e;
-    if (MOD != 0 && DKDV) {
-      // the step's columns, negated, where the warp reads them four at a
-      // time (per-element shuffles took as long as the arithmetic); a bias's
-      // part that depends on the column goes in with the lse
-      const float sl = bias_side<DKDV>(p, col0, row - lane) * slope2;
-      __syncwarp();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        stats[c * 32 + lane] =
-            sl * static_cast<float>(c * 32 + lane) - lse2_c[c];
-        stats[64 + c * 32 + lane] = -delta_c[c];
-      }
-      __syncwarp();
-    }
     ok = bwarp_wait(&bars->s_full, it & 1, abort_flag, p.timeout_ns);
     if (!ok) {
       record_bwd_timeout(kRoleBElem, 0);
@@ -673,9 +652,6 @@ __device__ __forceinline__ void bwd_elem_role(const BwdParams& p,
     // pointwise dS = dP sig (1 + x (1 - sig)) / Sq
     float f[64];
     uint32_t pw[32];
-    if (MOD != 0)
-      mod_p<MOD, DKDV>(p, sraw, vis, stats, col0, row, slope2, lse2_row, f, pw);
-    else
 #pragma unroll
     for (int j = 0; j < 64; j += 2) {
       float pv[2];
@@ -730,21 +706,6 @@ __device__ __forceinline__ void bwd_elem_role(const BwdParams& p,
       mbar_arrive(&bars->h0_dp);
     }
     uint32_t dsw[32];
-    if (MOD != 0) {
-#pragma unroll
-      for (int j = 0; j < 64; j += 4) {
-        float d[4] = {-delta_row, -delta_row, -delta_row, -delta_row};
-        if (DKDV) load4(stats + 64 + j, d);
-#pragma unroll
-        for (int u = 0; u < 4; u += 2) {
-          float x0, x1;
-          fadd2(x0, x1, __uint_as_float(dpraw[j + u]),
-                __uint_as_float(dpraw[j + u + 1]), d[u], d[u + 1]);
-          fmul2v(x0, x1, x0, x1, f[j + u], f[j + u + 1]);
-          dsw[(j + u) / 2] = pack_bf16x2(x0, x1);
-        }
-      }
-    } else
 #pragma unroll
     for (int j = 0; j < 64; j += 2) {
       float dsv[2];
@@ -828,8 +789,206 @@ __device__ __forceinline__ void bwd_elem_role(const BwdParams& p,
   }
 }
 
+// Elementwise warps with modified scores: four per TMEM lane quarter, each on
+// 32 columns of S and dP (warps 2-5 on [0, 32), 6-9 on [32, 64) and so on):
+// the arithmetic per column is about twice the unmodified role's, and the
+// tensor core waits for it twice a step, so it is spread over twice the warps
+// (two warps per quarter: 390 us on causal S=2048, 4 x 16 heads, cap 50; four:
+// 344).  The packed P and dS of columns
+// [32 k, 32 k + 32) go over columns [16 k, 16 k + 16), which the warps of the
+// first half (k < 2) read: the others write only after both have read.
+template <int D, int MOD, bool DKDV>
+__device__ __forceinline__ void bwd_elem_mod_role(
+    const BwdParams& p, BwdBars* bars, const uint16_t* list, float* stats,
+    uint32_t tmem, int b, int hq_or_hkv, int fixed_tile, int n_iter) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int quarter = warp % 4;     // TMEM lanes this warp may access
+  const int part = (warp - 2) / 4;  // columns [32 part, 32 part + 32)
+  const int r = quarter * 32 + lane;
+  const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+  const uint32_t t_s = tmem + lane_off, t_dp = tmem + lane_off + 128;
+  volatile int* abort_flag = &bars->abort;
+  const int G = p.H / p.Hkv;
+  const int n_list = bars->n_list;
+  const float kLog2e = 1.4426950408889634f;
+  // the thread's row: a key (dK/dV) or a query (dQ), and its segment id
+  const int row = fixed_tile * kTileM + r;
+  int row_seg = 0;
+  if ((p.flags & BSM_MASK_SEGMENT) && (DKDV ? row < p.Skv : row < p.Sq))
+    row_seg = DKDV ? p.kv_seg[static_cast<int64_t>(b) * p.Skv + row]
+                   : p.q_seg[static_cast<int64_t>(b) * p.Sq + row];
+  // dQ: the row's lse (log2 units) and D_q are fixed
+  float lse2_row = 0.f, delta_row = 0.f;
+  if (!DKDV && row < p.Sq) {
+    const int64_t i = (static_cast<int64_t>(b) * p.H + hq_or_hkv) * p.Sq + row;
+    lse2_row = p.lse[i] * kLog2e;
+    delta_row = p.delta[i];
+  }
+  // dK/dV: the lse (log2 units) and D_q of this lane's query column and the
+  // query head's slope, loaded a step ahead.  A column past the last query
+  // gets lse = inf, so P = 0 (its zero dO alone makes it vanish unless a rising
+  // bias overflows P)
+  auto load_stats = [&](int it, float& l2, float& dl, float& slope) {
+    const int qc = (list[it % n_list] >> 2) * kTileM + part * 32 + lane;
+    const int hd = hq_or_hkv * G + it / n_list;
+    l2 = __int_as_float(0x7f800000);
+    dl = 0.f;
+    if (qc < p.Sq) {
+      const int64_t i = (static_cast<int64_t>(b) * p.H + hd) * p.Sq + qc;
+      l2 = p.lse[i] * kLog2e;
+      dl = p.delta[i];
+    }
+    if ((MOD & kModBias) && p.mod.slopes != nullptr)
+      slope = p.mod.slopes[hd] * kLog2e;
+  };
+  float lse2_n = 0.f, delta_n = 0.f, slope_n = 0.f;
+  if (DKDV) {
+    if (n_iter > 0) load_stats(0, lse2_n, delta_n, slope_n);
+  } else if ((MOD & kModBias) && p.mod.slopes != nullptr) {
+    slope_n = p.mod.slopes[hq_or_hkv] * kLog2e;
+  }
+  bool ok = true;
+  for (int it = 0; it < n_iter; ++it) {
+    const int e = it % n_list;
+    const int tile = list[e] >> 2, cls = list[e] & 3;
+    const int col0 = tile * kTileM + part * 32;
+    const float slope2 = slope_n;
+    if (DKDV) {
+      // the step's columns, negated, where the warp reads them four at a time
+      // (per-element shuffles took as long as the arithmetic); a bias's part
+      // that depends on the column goes in with the lse
+      const float sl = bias_side<DKDV>(p, col0, row - lane) * slope2;
+      __syncwarp();
+      stats[lane] = sl * static_cast<float>(lane) - lse2_n;
+      stats[32 + lane] = -delta_n;
+      __syncwarp();
+      if (it + 1 < n_iter) load_stats(it + 1, lse2_n, delta_n, slope_n);
+    }
+    ok = bwarp_wait(&bars->s_full, it & 1, abort_flag, p.timeout_ns);
+    if (!ok) {
+      record_bwd_timeout(kRoleBElem, 0);
+      break;
+    }
+    tc_fence_after();
+    uint32_t sraw[32];
+    tmem_ld32(t_s + part * 32, sraw);
+    uint32_t vis = 0xffffffffu;
+    if (cls == 1) vis = chunk_visible<DKDV>(p, b, row, row_seg, col0);
+    tmem_ld_wait();
+    tc_fence_before();
+    if (!DKDV) mbar_arrive(&bars->p_ready);  // S read: the next S may go in
+    else if (part < 2) mbar_arrive(&bars->h0_s);
+    float f[32];
+    uint32_t pw[16];
+    mod_p<MOD, DKDV>(p, sraw, vis, stats, col0, row, slope2, lse2_row, f, pw);
+    if (DKDV) {
+      if (part > 0) {
+        if (!bwarp_wait(&bars->h0_s, it & 1, abort_flag, p.timeout_ns)) {
+          record_bwd_timeout(kRoleBElem, 2);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+      }
+      tmem_st16(t_s + part * 16, pw);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&bars->p_ready);
+    }
+    ok = bwarp_wait(&bars->dp_full, it & 1, abort_flag, p.timeout_ns);
+    if (!ok) {
+      record_bwd_timeout(kRoleBElem, 3);
+      break;
+    }
+    tc_fence_after();
+    tmem_ld32(t_dp + part * 32, sraw);
+    tmem_ld_wait();
+    if (part < 2) {
+      tc_fence_before();
+      mbar_arrive(&bars->h0_dp);
+    }
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      float d[4] = {-delta_row, -delta_row, -delta_row, -delta_row};
+      if (DKDV) load4(stats + 32 + j, d);
+#pragma unroll
+      for (int u = 0; u < 4; u += 2) {
+        float x0, x1;
+        fadd2(x0, x1, __uint_as_float(sraw[j + u]),
+              __uint_as_float(sraw[j + u + 1]), d[u], d[u + 1]);
+        fmul2v(x0, x1, x0, x1, f[j + u], f[j + u + 1]);
+        pw[(j + u) / 2] = pack_bf16x2(x0, x1);
+      }
+    }
+    if (part > 0) {
+      if (!bwarp_wait(&bars->h0_dp, it & 1, abort_flag, p.timeout_ns)) {
+        record_bwd_timeout(kRoleBElem, 2);
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+    }
+    tmem_st16(t_dp + part * 16, pw);
+    tmem_st_wait();
+    tc_fence_before();
+    mbar_arrive(&bars->ds_ready);
+  }
+  if (!ok) return;
+  // ---- results: dK/dV rows (keys) or dQ rows, bf16; dK and dQ scaled; each
+  // warp stores 32 of the D columns
+  const bool row_ok = DKDV ? row < p.Skv : row < p.Sq;
+  if (n_iter > 0) {
+    if (!bwarp_wait(&bars->acc_done, 0, abort_flag, p.timeout_ns)) {
+      record_bwd_timeout(kRoleBElem, 1);
+      return;
+    }
+    tc_fence_after();
+  }
+  if (part >= D / 32) return;
+#pragma unroll 1
+  for (int a = 0; a < (DKDV ? 2 : 1); ++a) {
+    // dK/dV: a = 0 is dV (TMEM 256), a = 1 dK (TMEM 384); dQ: a = 0
+    uint16_t* dst;
+    float mul;
+    if (DKDV) {
+      dst = (a == 0 ? p.dv : p.dk) +
+            static_cast<int64_t>(b) * (a == 0 ? p.dv_sb : p.dk_sb) +
+            static_cast<int64_t>(hq_or_hkv) * (a == 0 ? p.dv_sh : p.dk_sh) +
+            static_cast<int64_t>(row) * (a == 0 ? p.dv_ss : p.dk_ss);
+      mul = a == 0 ? 1.f : p.scale;
+    } else {
+      dst = p.dq + static_cast<int64_t>(b) * p.dq_sb +
+            static_cast<int64_t>(hq_or_hkv) * p.dq_sh +
+            static_cast<int64_t>(row) * p.dq_ss;
+      mul = p.scale;
+    }
+    uint32_t o[32];
+    if (n_iter > 0) {
+      tmem_ld32(tmem + lane_off + 256 + a * 128 + part * 32, o);
+      tmem_ld_wait();
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = 0u;
+    }
+    if (row_ok) {
+      uint32_t w[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        w[j] = pack_bf16x2(__uint_as_float(o[2 * j]) * mul,
+                           __uint_as_float(o[2 * j + 1]) * mul);
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        st_global_v4(dst + part * 32 + v * 8, w[4 * v], w[4 * v + 1],
+                     w[4 * v + 2], w[4 * v + 3]);
+    }
+  }
+}
+
+// Threads of a kernel: two role warps and the elementwise ones.
+constexpr int bwd_threads(int mod) { return mod != 0 ? 64 + 512 : kBwdThreads; }
+
 template <int D, int SCORE, int MOD, bool DKDV>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(bwd_threads(MOD), 1)
     splash_bwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v,
@@ -878,10 +1037,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     mbar_init(&bars->s_full, 1);
     mbar_init(&bars->dp_full, 1);
-    mbar_init(&bars->p_ready, 256);
-    mbar_init(&bars->ds_ready, 256);
-    mbar_init(&bars->h0_s, 128);
-    mbar_init(&bars->h0_dp, 128);
+    mbar_init(&bars->p_ready, bwd_threads(MOD) - 64);
+    mbar_init(&bars->ds_ready, bwd_threads(MOD) - 64);
+    mbar_init(&bars->h0_s, (bwd_threads(MOD) - 64) / 2);
+    mbar_init(&bars->h0_dp, (bwd_threads(MOD) - 64) / 2);
     mbar_init(&bars->acc_done, 1);
     mbar_init(&bars->mma_done, 1);
     bars->abort = 0;
@@ -912,10 +1071,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   } else if (warp == 1) {
     if (n_iter > 0) bwd_mma_role<D, DKDV>(p, smem, bars, tmem, n_iter);
   } else {
-    float* stats = reinterpret_cast<float*>(smem + C::kOffStat) +
-                   (warp - 2) * 128;
-    bwd_elem_role<D, SCORE, MOD, DKDV>(p, bars, list, stats, tmem, b, head,
-                                       fixed_tile, n_iter);
+    if constexpr (MOD != 0) {
+      float* stats = reinterpret_cast<float*>(smem + C::kOffStat) +
+                     (warp - 2) * 64;
+      bwd_elem_mod_role<D, MOD, DKDV>(p, bars, list, stats, tmem, b, head,
+                                      fixed_tile, n_iter);
+    } else {
+      bwd_elem_role<D, SCORE, DKDV>(p, bars, list, tmem, b, head, fixed_tile,
+                                    n_iter);
+    }
   }
 
   tc_fence_before();
@@ -981,7 +1145,7 @@ cudaError_t launch_bwd_one(const BwdParams& p, const CUtensorMap& tq,
   const dim3 grid = DKDV ? dim3((p.Skv + kTileN - 1) / kTileN, p.Hkv, p.B)
                          : dim3((p.Sq + kTileM - 1) / kTileM, p.H, p.B);
   if (DKDV) {
-    kern<<<grid, kBwdThreads, kSmem, stream>>>(tq, tk, tv, tdo, p);
+    kern<<<grid, bwd_threads(MOD), kSmem, stream>>>(tq, tk, tv, tdo, p);
     return cudaGetLastError();
   }
   // dQ: a programmatic dependent of the launch before it (the dK/dV grid,
@@ -989,7 +1153,7 @@ cudaError_t launch_bwd_one(const BwdParams& p, const CUtensorMap& tq,
   // after it as usual)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kBwdThreads);
+  cfg.blockDim = dim3(bwd_threads(MOD));
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
