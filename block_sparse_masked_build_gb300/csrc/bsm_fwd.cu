@@ -581,13 +581,14 @@ __device__ __forceinline__ void mma_role(const FwdParams& p, uint8_t* smem,
 // "Same segment" bits of the 128 keys of a tile for one row (unsorted
 // segment ids), one 32-bit word per 32 keys.  Computed before S is loaded
 // from TMEM, so the loads never compete with S for registers.
+template <int NC = kTileN>
 __device__ __forceinline__ void segment_bits(uint32_t keep[4],
                                              const int32_t* segk, int nvalid,
                                              int segq) {
   const bool vec =
-      nvalid == kTileN && (reinterpret_cast<uintptr_t>(segk) & 15u) == 0;
+      nvalid == NC && (reinterpret_cast<uintptr_t>(segk) & 15u) == 0;
 #pragma unroll 1
-  for (int w = 0; w < kTileN / 32; ++w) {
+  for (int w = 0; w < NC / 32; ++w) {
     uint32_t bits = 0;
     if (vec) {
       const int4* s4 = reinterpret_cast<const int4*>(segk + 32 * w);
@@ -620,12 +621,13 @@ __device__ __forceinline__ void segment_bits(uint32_t keep[4],
 // whole (a warp-uniform test) is left alone, the others cost one bit test
 // and one select per column.  Under causal and packed-segment masks most
 // chunks of a partial tile are whole for the warp.
+template <int NC = kTileN>
 __device__ __forceinline__ void mask_tile(float* s, int lo_c, int hi_c,
-                                          const uint32_t keep[4],
+                                          const uint32_t* keep,
                                           bool use_keep) {
   const float NEG_INF = __int_as_float(0xff800000);
 #pragma unroll
-  for (int q = 0; q < kTileN / 32; ++q) {
+  for (int q = 0; q < NC / 32; ++q) {
     const int c0 = 32 * q;
     // visible columns of this chunk as bits: [lo_c, hi_c] cut to the chunk
     const int lb = min(max(lo_c - c0, 0), 32), hb = min(max(hi_c - c0 + 1, 0), 32);
@@ -643,11 +645,11 @@ __device__ __forceinline__ void mask_tile(float* s, int lo_c, int hi_c,
 
 // s = s * (c[0] + c[1] s^2 + ...) + the bias of the column's place among eight
 // (kModBias) or + neg_m.
-template <int MOD, int N>
+template <int MOD, int NC, int N>
 __device__ __forceinline__ void cap_tile(float* s, const float* c,
                                          const float* pc, float neg_m) {
 #pragma unroll
-  for (int j = 0; j < kTileN; j += 2) {
+  for (int j = 0; j < NC; j += 2) {
     float h0, h1;
     poly_sq2<N>(h0, h1, s[j], s[j + 1], c);
     if (MOD & kModBias)
@@ -658,7 +660,7 @@ __device__ __forceinline__ void cap_tile(float* s, const float* c,
   }
 }
 
-// Modified scores of one row's 128 columns, in place and in log2 units: from
+// Modified scores of one row's NC columns, in place and in log2 units: from
 // S = q.k to cap * tanh(scale S / cap) (kModCap) or scale S, minus slope *
 // |q - k| (kModBias; slope2 = slope * log2(e)).
 //
@@ -681,7 +683,7 @@ __device__ __forceinline__ void cap_tile(float* s, const float* c,
 // sides that no causal mask cuts takes the bias whole, column by column.
 //
 // kModCap alone: s also has m_fixed subtracted.
-template <int MOD>
+template <int MOD, int NC>
 __device__ __forceinline__ void modify_tile(float* s, const FwdParams& p,
                                             int kbase, int qrow, float slope2,
                                             float* sl_out, float* base_out) {
@@ -691,7 +693,7 @@ __device__ __forceinline__ void modify_tile(float* s, const FwdParams& p,
     const int lane = threadIdx.x % 32;
     const int first = qrow - lane;  // the warp's rows: first .. first + 31
     const bool left =
-        (p.flags & BSM_MASK_CAUSAL) != 0 || kbase + kTileN - 1 <= first;
+        (p.flags & BSM_MASK_CAUSAL) != 0 || kbase + NC - 1 <= first;
     split = !left && kbase < first + 31;  // warp-uniform
     const float sl = split ? 0.f : left ? slope2 : -slope2;
 #pragma unroll
@@ -702,7 +704,7 @@ __device__ __forceinline__ void modify_tile(float* s, const FwdParams& p,
   if (MOD & kModCap) {
     float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
 #pragma unroll
-    for (int c = 0; c < kTileN; c += 8) {
+    for (int c = 0; c < NC; c += 8) {
       a0 = fmax3_abs(a0, s[c], s[c + 1]);
       a1 = fmax3_abs(a1, s[c + 2], s[c + 3]);
       a2 = fmax3_abs(a2, s[c + 4], s[c + 5]);
@@ -711,11 +713,11 @@ __device__ __forceinline__ void modify_tile(float* s, const FwdParams& p,
     const float top = fmaxf(fmax3(a0, a1, a2), a3);
     const float neg_m = MOD == kModCap ? -p.mod.m_fixed : 0.f;
     if (__all_sync(0xffffffffu, top <= p.mod.poly_max)) {
-      cap_tile<MOD, 4>(s, p.mod.poly, pc, neg_m);
+      cap_tile<MOD, NC, 4>(s, p.mod.poly, pc, neg_m);
     } else {
       const float k2 = -2.f * p.mod.cap_log2, k0 = p.mod.cap_log2 + neg_m;
 #pragma unroll
-      for (int c = 0; c < kTileN; c += 2) {
+      for (int c = 0; c < NC; c += 2) {
         float e0, e1;
         fmul2(e0, e1, s[c], s[c + 1], p.mod.cap_e);
         e0 = ex2_approx(fmin_nan(e0, 60.f));
@@ -731,25 +733,26 @@ __device__ __forceinline__ void modify_tile(float* s, const FwdParams& p,
     }
   } else {
 #pragma unroll
-    for (int c = 0; c < kTileN; c += 2)
+    for (int c = 0; c < NC; c += 2)
       ffma2v(s[c], s[c + 1], s[c], s[c + 1], p.scale_log2, p.scale_log2,
              pc[c & 7], pc[(c & 7) + 1]);
   }
   if ((MOD & kModBias) && split) {
     const float d0 = static_cast<float>(kbase - qrow);
 #pragma unroll
-    for (int c = 0; c < kTileN; ++c)
+    for (int c = 0; c < NC; ++c)
       s[c] = fmaf(-slope2, fabsf(d0 + c), s[c]);
   }
 }
 
 // Row maximum of a tile whose bias per 8 columns is sl8 (c / 8) + base, to be
 // added to s.
+template <int NC>
 __device__ __forceinline__ float biased_max(const float* s, float sl8,
                                             float base) {
   float mx[2];
 #pragma unroll
-  for (int i = 0; i < kTileN / 8; ++i) {
+  for (int i = 0; i < NC / 8; ++i) {
     const float* t = s + 8 * i;
     const float m = fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]),
                           fmaxf(t[6], t[7])) +
@@ -883,7 +886,7 @@ __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
       tmem_ld_wait();
       float* s = reinterpret_cast<float*>(sraw);
       float sl8 = 0.f, cbase = 0.f;  // bias of each 8 columns (kModBias)
-      if (MOD != 0) modify_tile<MOD>(s, p, kbase, qrow, slope2, &sl8, &cbase);
+      if (MOD != 0) modify_tile<MOD, kTileN>(s, p, kbase, qrow, slope2, &sl8, &cbase);
       if (cls == 1) mask_tile(s, rlo - kbase, rhi - kbase, keep, KEEP);
 
       uint32_t pk[16];
@@ -905,7 +908,7 @@ __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
         } else if (MOD == kModCap) {
           m_blk = NEG_INF;  // m_used stays m_fixed
         } else {
-          m_blk = biased_max(s, sl8, cbase);
+          m_blk = biased_max<kTileN>(s, sl8, cbase);
         }
         bool rescale = false;
         float alpha = 1.f;
@@ -1195,12 +1198,29 @@ struct DtBars {
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[2][2], kv_empty[2][2];  // [pipeline][slot]: K, V
   uint64_t s_full[2], p_full[2], pv_done[2], o_free[2], mma_done[2];
+  // two threads per row: the two score warps of a pipeline and lane quarter,
+  // on every entry and at a unit's end
+  uint64_t meet[2][4], meet_sum[2][4];
   uint32_t tmem_base;
   int abort;
   uint32_t trace_n[6];
   DtMeta meta[2][kListBufs];
 };
 static_assert(sizeof(DtBars) <= 1024, "barrier block");
+
+// Two threads per row: their sums by pipeline and half.  A unit's sums
+// alternate between two places: a thread writes the next unit's while its
+// partner may still read this one's, but the one after that only once the
+// partner has arrived with the next.
+struct DtPair {
+  float sum[2][2][2][kTileM];
+};
+constexpr int kDtOffPair = kDtOffBar + 1024;
+static_assert(kDtSmemBytes + sizeof(DtPair) <= 232448, "shared memory budget");
+
+// Score threads of one pipeline, and threads of the kernel.
+constexpr int dt_score_threads(int mod) { return mod == kModCap ? 256 : 128; }
+constexpr int dt_threads(int mod) { return 128 + 2 * dt_score_threads(mod); }
 
 // Optional event trace, in the layout of `trace` above; the six recording
 // threads are: loader 0, MMA 0, score 0, score 1, loader 1, MMA 1.
@@ -1599,7 +1619,7 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
       tmem_ld_wait();
       float* s = reinterpret_cast<float*>(sraw);
       float sl8 = 0.f, cbase = 0.f;  // bias of each 8 columns (kModBias)
-      if (MOD != 0) modify_tile<MOD>(s, p, kbase, qrow, slope2, &sl8, &cbase);
+      if (MOD != 0) modify_tile<MOD, kTileN>(s, p, kbase, qrow, slope2, &sl8, &cbase);
       if (cls == 1) mask_tile(s, rlo - kbase, rhi - kbase, keep, KEEP);
 
       uint32_t pk[16];
@@ -1621,7 +1641,7 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
         } else if (MOD == kModCap) {
           m_blk = NEG_INF;  // m_used stays m_fixed
         } else {
-          m_blk = biased_max(s, sl8, cbase);
+          m_blk = biased_max<kTileN>(s, sl8, cbase);
         }
         bool rescale = false;
         float alpha = 1.f;
@@ -1785,9 +1805,210 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
   }
 }
 
+// Score warps of pipeline t for capped softmax scores without a bias
+// (kModCap): eight instead of four, two threads per query row, each with one
+// 64-key half of the tile.  The arithmetic per score is about twice the
+// unmodified one's and the tensor core waits for it on every entry, so a row's
+// latency is halved.  No maximum is kept, so the threads of a row share only
+// their sums, in the epilogue; and half 1, whose P goes over columns [32, 64)
+// of S (half 0's scores), writes after half 0 has read.  Measured against one
+// thread per row (us): packed S=8192, 2 x 16 heads: cap 50 136 and 145, cap 20
+// 155 and 186; causal S=8192, 32/8 heads, cap 20: 571 and 690.  With a bias,
+// whose running maximum the two threads would have to exchange on every entry,
+// it was 1 to 7 % slower instead.
+template <bool KEEP, bool TRACE>
+__device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
+                                                  DtBars* bars, DtPair* pair,
+                                                  const uint16_t* lists,
+                                                  uint32_t tmem, const int t,
+                                                  const int hf) {
+  constexpr int D = 128, NC = kTileN / 2;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int quarter = warp % 4;  // TMEM lane quarter this warp may access
+  const int r = quarter * 32 + lane;
+  const bool tracer = r == 0 && hf == 0;
+  const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+  const uint32_t s_addr = tmem + lane_off + t * 128;
+  const uint32_t o_addr = tmem + lane_off + 256 + t * 128 + hf * (D / 2);
+  volatile int* abort_flag = &bars->abort;
+  const float NEG_INF = __int_as_float(0xff800000);
+  const bool seg = (p.flags & BSM_MASK_SEGMENT) != 0;
+  const bool seg_elem = KEEP && seg;
+  uint64_t* meet = &bars->meet[t][quarter];
+  uint32_t s_cnt = 0, pv_cnt = 0, meets = 0, sums = 0;
+  for (int ui = 0;; ++ui) {
+    const int buf = ui % kListBufs;
+    if (!warp_wait(&bars->list_full[t][buf], (ui / kListBufs) & 1, abort_flag,
+                   p.timeout_ns)) {
+      record_timeout(kRoleScore, 0);
+      break;
+    }
+    const int unit = bars->meta[t][buf].unit;
+    if (unit < 0) break;
+    const int n_ent = bars->meta[t][buf].n;
+    const UnitCoord uc{bars->meta[t][buf].b, bars->meta[t][buf].h, 0};
+    const uint16_t* list = lists + buf * kMaxKvTiles;
+    const int qrow = bars->meta[t][buf].qt * kTileM + r;
+    const bool row_ok = qrow < p.Sq;
+    // visible keys of this row form [rlo, rhi] (plus the element compare of
+    // unsorted segment ids)
+    int rlo = 0, rhi = p.Skv - 1;
+    if (p.flags & BSM_MASK_CAUSAL) rhi = min(rhi, qrow);
+    if (p.flags & BSM_MASK_LOCAL) rlo = max(rlo, qrow - p.window + 1);
+    if (p.flags & BSM_MASK_BAND) rhi = min(rhi, qrow + p.window - 1);
+    int segq = 0;
+    if (seg && row_ok) {
+      const int64_t qi = static_cast<int64_t>(uc.b) * p.Sq + qrow;
+      if (seg_elem) {
+        segq = p.q_seg[qi];
+      } else {
+        const int2 sr = reinterpret_cast<const int2*>(p.seg_range)[qi];
+        rlo = max(rlo, sr.x);
+        rhi = min(rhi, sr.y);
+      }
+    }
+    const int32_t* segk_b =
+        seg_elem ? p.kv_seg + static_cast<int64_t>(uc.b) * p.Skv : nullptr;
+    // the cap bounds the logits to +-cap_log2: no maximum is kept, p is
+    // 2^(x - m_fixed) with m_fixed = max(0, cap_log2 - 52), so p lies within
+    // 2^-121 .. 2^52 for the caps that take this path (cap_log2 <= 87) and
+    // sums of 2^18 of them stay far inside f32
+    float l_sum = 0.f;
+    uint32_t unit_pv = 0;
+    bool ok = true;
+    for (int e = 0; e < n_ent; ++e) {
+      const uint32_t ent = list[e];
+      const int cls = static_cast<int>(ent & 3u);
+      const int jt = static_cast<int>(ent >> 2);
+      const int kbase = jt * kTileN + hf * NC;
+      uint32_t keep[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+      if (KEEP && cls == 1)
+        segment_bits<NC>(keep, segk_b + kbase,
+                         min(max(p.Skv - kbase, 0), NC), segq);
+      ok = warp_wait(&bars->s_full[t], s_cnt & 1, abort_flag, p.timeout_ns);
+      if (!ok) {
+        record_timeout(kRoleScore, 1);
+        break;
+      }
+      ++s_cnt;
+      if (tracer) dt_trace<TRACE>(p, bars, kRoleScore, kEvSFull, t, e, unit);
+      tc_fence_after();
+      uint32_t sraw[NC];
+#pragma unroll
+      for (int q = 0; q < NC / 32; ++q)
+        tmem_ld32(s_addr + hf * NC + q * 32, sraw + q * 32);
+      tmem_ld_wait();
+      float* s = reinterpret_cast<float*>(sraw);
+      if (hf == 0) {  // half 1 may write over S
+        tc_fence_before();
+        mbar_arrive(meet);
+      }
+      float unused;
+      modify_tile<kModCap, NC>(s, p, kbase, qrow, 0.f, &unused, &unused);
+      if (cls == 1) mask_tile<NC>(s, rlo - kbase, rhi - kbase, keep, KEEP);
+
+      float ls0 = 0.f, ls1 = 0.f, ls2 = 0.f, ls3 = 0.f;
+#pragma unroll
+      for (int q = 0; q < NC / 32; ++q) {  // 32 columns at a time
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 32 * q; c < 32 * q + 32; c += 4) {
+          const float p0 = ex2_approx(s[c]), p1 = ex2_approx(s[c + 1]);
+          const float p2 = ex2_approx(s[c + 2]), p3 = ex2_approx(s[c + 3]);
+          fadd2(ls0, ls1, ls0, ls1, p0, p1);
+          fadd2(ls2, ls3, ls2, ls3, p2, p3);
+          pk[(c & 31) / 2] = pack_bf16x2(p0, p1);
+          pk[(c & 31) / 2 + 1] = pack_bf16x2(p2, p3);
+        }
+        if (hf == 1 && q == 0) {
+          ok = warp_wait(meet, meets & 1, abort_flag, p.timeout_ns);
+          tc_fence_after();
+        }
+        tmem_st16(s_addr + hf * 32 + q * 16, pk);
+      }
+      ++meets;
+      if (!ok) {
+        record_timeout(kRoleScore, 6);
+        break;
+      }
+      l_sum += (ls0 + ls1) + (ls2 + ls3);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&bars->p_full[t]);
+      if (tracer) dt_trace<TRACE>(p, bars, kRoleScore, kEvPFull, t, e, unit);
+      ++pv_cnt;
+      ++unit_pv;
+    }
+    if (!ok) break;
+
+    // ---- epilogue: out = O / l, bf16; each thread half of the row
+    if (tracer) dt_trace<TRACE>(p, bars, kRoleScore, kEvEpiBegin, t, 0, unit);
+    uint16_t* orow = p.out + static_cast<int64_t>(uc.b) * p.o_sb +
+                     static_cast<int64_t>(uc.h) * p.o_sh +
+                     static_cast<int64_t>(qrow) * p.o_ss + hf * (D / 2);
+    if (unit_pv > 0) {
+      // the two halves' sums
+      pair->sum[sums & 1][t][hf][r] = l_sum;
+      mbar_arrive(&bars->meet_sum[t][quarter]);
+      if (!warp_wait(&bars->meet_sum[t][quarter], sums & 1, abort_flag,
+                     p.timeout_ns)) {
+        record_timeout(kRoleScore, 7);
+        break;
+      }
+      l_sum = pair->sum[sums & 1][t][0][r] + pair->sum[sums & 1][t][1][r];
+      ++sums;
+      if (!warp_wait(&bars->pv_done[t], (pv_cnt - 1) & 1, abort_flag,
+                     p.timeout_ns)) {
+        record_timeout(kRoleScore, 3);
+        break;
+      }
+      tc_fence_after();
+      uint32_t o[D / 2];
+#pragma unroll
+      for (int q = 0; q < D / 64; ++q) tmem_ld32(o_addr + q * 32, o + q * 32);
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(&bars->o_free[t]);
+      const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
+      if (row_ok) {
+        const bool v8 = p.o_vec8 != 0;
+#pragma unroll
+        for (int v = 0; v < D / 32; ++v) {
+          uint32_t w[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            w[c] = pack_bf16x2(__uint_as_float(o[16 * v + 2 * c]) * inv,
+                               __uint_as_float(o[16 * v + 2 * c + 1]) * inv);
+          if (v8) {
+            st_global_v8(orow + v * 16, w);
+          } else {
+            st_global_v4(orow + v * 16, w[0], w[1], w[2], w[3]);
+            st_global_v4(orow + v * 16 + 8, w[4], w[5], w[6], w[7]);
+          }
+        }
+      }
+    } else {
+      if (row_ok) {
+#pragma unroll
+        for (int v = 0; v < D / 16; ++v)
+          st_global_v4(orow + v * 8, 0u, 0u, 0u, 0u);
+      }
+      tc_fence_before();
+      mbar_arrive(&bars->o_free[t]);
+    }
+    if (hf == 0 && p.lse != nullptr && row_ok) {
+      const float lse = l_sum > 0.f
+                            ? (p.mod.m_fixed + log2f(l_sum)) * 0.6931471805599453f
+                            : NEG_INF;
+      p.lse[(static_cast<int64_t>(uc.b) * p.H + uc.h) * p.Sq + qrow] = lse;
+    }
+    mbar_arrive(&bars->list_free[t][buf]);
+    if (tracer) dt_trace<TRACE>(p, bars, kRoleScore, kEvEpiEnd, t, 0, unit);
+  }
+}
 
 template <int SCORE, int MOD, bool TRACE>
-__global__ void __launch_bounds__(kDtThreads, 1)
+__global__ void __launch_bounds__(dt_threads(MOD), 1)
     splash_fwd_dt_kernel(const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v,
@@ -1805,7 +2026,8 @@ __global__ void __launch_bounds__(kDtThreads, 1)
     for (int t = 0; t < 2; ++t) {
       for (int i = 0; i < kListBufs; ++i) {
         mbar_init(&bars->list_full[t][i], 1);
-        mbar_init(&bars->list_free[t][i], 2 + kTileM);  // load, MMA, score
+        // load, MMA, score
+        mbar_init(&bars->list_free[t][i], 2 + dt_score_threads(MOD));
       }
       mbar_init(&bars->q_full[t], 1);
       mbar_init(&bars->q_empty[t], 1);
@@ -1814,10 +2036,14 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         mbar_init(&bars->kv_empty[t][s], 1);
       }
       mbar_init(&bars->s_full[t], 1);
-      mbar_init(&bars->p_full[t], kTileM);
+      mbar_init(&bars->p_full[t], dt_score_threads(MOD));
       mbar_init(&bars->pv_done[t], 1);
-      mbar_init(&bars->o_free[t], kTileM);
+      mbar_init(&bars->o_free[t], dt_score_threads(MOD));
       mbar_init(&bars->mma_done[t], 1);
+      for (int q = 0; q < 4; ++q) {
+        mbar_init(&bars->meet[t][q], 32);  // half 0 tells half 1
+        mbar_init(&bars->meet_sum[t][q], 64);
+      }
     }
     bars->abort = 0;
     for (int i = 0; i < 6; ++i) bars->trace_n[i] = 0;
@@ -1836,7 +2062,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
   const uint32_t tmem = bars->tmem_base;
 
   if (warp < 4) {
-    setmaxnreg_dec<kRegsLight>();
+    if (MOD != kModCap) setmaxnreg_dec<kRegsLight>();
     const int t = warp & 1;
     uint16_t* lt = lists + t * kListBufs * kMaxKvTiles;
     if (warp < 2)
@@ -1844,16 +2070,27 @@ __global__ void __launch_bounds__(kDtThreads, 1)
     else
       dt_mma_role<SCORE, TRACE>(p, smem, bars, tmem, t);
   } else {
-    setmaxnreg_inc<kRegsScore>();
-    const int t = (warp - 4) / 4;
-    const uint16_t* lt = lists + t * kListBufs * kMaxKvTiles;
     // per-element keep bits only when segment ids are unsorted or an
     // arbitrary mask is given (read once; the same for every thread)
-    if (((p.flags & BSM_MASK_SEGMENT) && (*p.seg_flags & 1) != 0) ||
-        p.dense != nullptr)
-      dt_score_role<SCORE, MOD, true, TRACE>(p, bars, lt, tmem, t);
-    else
-      dt_score_role<SCORE, MOD, false, TRACE>(p, bars, lt, tmem, t);
+    if constexpr (MOD != kModCap) {
+      setmaxnreg_inc<kRegsScore>();
+      const int t = (warp - 4) / 4;
+      const uint16_t* lt = lists + t * kListBufs * kMaxKvTiles;
+      if (((p.flags & BSM_MASK_SEGMENT) && (*p.seg_flags & 1) != 0) ||
+          p.dense != nullptr)
+        dt_score_role<SCORE, MOD, true, TRACE>(p, bars, lt, tmem, t);
+      else
+        dt_score_role<SCORE, MOD, false, TRACE>(p, bars, lt, tmem, t);
+    } else {
+      const int t = (warp - 4) / 8, hf = (warp - 4) / 4 & 1;
+      const uint16_t* lt = lists + t * kListBufs * kMaxKvTiles;
+      DtPair* pair = reinterpret_cast<DtPair*>(smem + kDtOffPair);
+      // (an arbitrary mask with modified scores takes the lockstep kernel)
+      if ((p.flags & BSM_MASK_SEGMENT) && (*p.seg_flags & 1) != 0)
+        dt_score_cap_role<true, TRACE>(p, bars, pair, lt, tmem, t, hf);
+      else
+        dt_score_cap_role<false, TRACE>(p, bars, pair, lt, tmem, t, hf);
+    }
   }
 
   tc_fence_before();
@@ -1879,11 +2116,13 @@ cudaError_t launch_dt(const FwdParams& p, const CUtensorMap& tq,
   cudaFuncAttributes attr;
   cudaError_t e = cudaFuncGetAttributes(&attr, kern);
   if (e != cudaSuccess) return e;
-  if (attr.numRegs * kDtThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
+  if (MOD != kModCap && attr.numRegs * kDtThreads < kRegsNeeded)
+    return cudaErrorInvalidConfiguration;
+  constexpr int kSmem = kDtSmemBytes + (MOD == kModCap ? sizeof(DtPair) : 0);
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kDtSmemBytes);
+                           kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kDtThreads, kDtSmemBytes, stream>>>(tq, tk, tv, p);
+  kern<<<grid, dt_threads(MOD), kSmem, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
 }
 
