@@ -137,32 +137,32 @@ __global__ void __launch_bounds__(kAppendThreads, NCH <= 8 ? 8 : 4)
   const int lo = max(len, tok0) - tok0;  // new tokens [lo, hi) of the page
   const int hi = min(len + n - tok0, p.page_size);
   if (lo >= hi) return;
+  // the new elements and, beside them, the page: neither waits for the other
   const int pid = p.table[static_cast<int64_t>(b) * p.table_stride + slot];
-  if (pid < 0 || pid >= p.num_pages) {
-    if (threadIdx.x == 0) record_bad_index(b, slot, pid);
-    return;
-  }
-  const int per = p.D / 8;  // pieces per token
+  const int per_shift = p.D == 128 ? 4 : 3;  // log2 of the pieces per token
   const uint16_t* src = is_v ? p.v_new : p.k_new;
   const int64_t sb = is_v ? p.v_sb : p.k_sb, sh = is_v ? p.v_sh : p.k_sh,
                 ss = is_v ? p.v_ss : p.k_ss;
   src += b * sb + h * sh;
-  const int64_t block = static_cast<int64_t>(pid) * p.H_kv + h;
-  uint8_t* dst = (is_v ? p.v : p.k) + block * p.page_size * p.D;
-  float* scale_at = (is_v ? p.v_scale : p.k_scale) + block;
-  const float was = lo > 0 ? *scale_at : 0.f;
-
   uint4 x[NCH];
   uint32_t top = 0;  // two running maxima of |bits|, finite elements only
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int c = threadIdx.x + i * kAppendThreads;
-    const int tok = c / per;
+    const int tok = c >> per_shift;
     x[i] = make_uint4(0u, 0u, 0u, 0u);
     if (tok >= lo && tok < hi)
       x[i] = *reinterpret_cast<const uint4*>(
-          src + (tok0 + tok - len) * ss + (c % per) * 8);
+          src + (tok0 + tok - len) * ss + (c & ((1 << per_shift) - 1)) * 8);
   }
+  if (pid < 0 || pid >= p.num_pages) {
+    if (threadIdx.x == 0) record_bad_index(b, slot, pid);
+    return;
+  }
+  const int64_t block = static_cast<int64_t>(pid) * p.H_kv + h;
+  uint8_t* dst = (is_v ? p.v : p.k) + block * p.page_size * p.D;
+  float* scale_at = (is_v ? p.v_scale : p.k_scale) + block;
+  const float was = lo > 0 ? *scale_at : 0.f;
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kAppendThreads, NCH <= 8 ? 8 : 4)
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int c = threadIdx.x + i * kAppendThreads;
-    const int tok = c / per;
+    const int tok = c >> per_shift;
     if (tok >= lo && tok < hi) {
       const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
       uint2 q;
@@ -217,12 +217,15 @@ __global__ void __launch_bounds__(kAppendThreads, NCH <= 8 ? 8 : 4)
 constexpr int kPaWarps = 4;
 constexpr int kPaThreads = 32 * kPaWarps;
 constexpr int kPaGroup = 16;  // tokens a warp works on at a time
-constexpr int kPaStages = 4;  // groups a warp keeps in flight
 constexpr int kPaRunCost = 4; // see PaPlan
 constexpr float kPUp = 512.f; // p's factor before it becomes f16
 
 template <int D, int NT>
 struct PaCfg {
+  // groups of a warp's ring, one of them being read: what three CTAs of an SM
+  // have room for at D = 128.  (At 64, where six fit, they were no faster: 94
+  // us on 64 sequences of 300-12000 tokens, with four 91.)
+  static constexpr int kPaStages = 4;
   static constexpr int kHalf = kPaGroup * D;  // bytes of a group's K or V
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kOffScale = kPaWarps * kPaStages * kStage;
@@ -472,8 +475,8 @@ __device__ __forceinline__ int64_t busy_ctas(int64_t units, int64_t grid) {
 }
 
 // One run of units: query rows [row0, row0 + 8 NT) of one (sequence,
-// key/value head), groups [g0, g1) of its plan.  Warp w takes groups g0 + w,
-// g0 + w + 4, ... of 16 tokens.  Per group, with the group as the 16-row
+// key/value head), groups [g0, g1) of its plan.  Warp w takes groups
+// g1 - 1 - w, g1 - 5 - w, ... of 16 tokens.  Per group, with the group as the 16-row
 // operand so that 8 query rows fill the other one:
 //     S^T [16 tokens][8 rows] = K q^T,   O^T [D][8 rows] += V^T P^T.
 // K and V go from shared memory to registers as they lie (16 bytes per lane)
@@ -487,12 +490,49 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
                                            int row0, int g0, int g1,
                                            float* part) {
   using C = PaCfg<D, NT>;
-  constexpr int kSteps = D / 16;
+  constexpr int kSteps = D / 16, kPaStages = C::kPaStages;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, t = lane % 4;
   const int G = p.H / p.H_kv, rows = G * p.T;
   const float NEG_INF = __int_as_float(0xff800000);
   const int len = plan.len, lo = plan.lo, first_group = plan.first_group;
+
+  // the copies start first; the queries are loaded while they run
+  const uint32_t ring = smem_u32(smem) + warp * kPaStages * C::kStage;
+  const uint32_t scales = smem_u32(smem) + C::kOffScale + warp * kPaStages * 8;
+  const int* table = p.table + static_cast<int64_t>(b) * p.table_stride;
+  // the run's groups from the last to the first: with a bias that falls with
+  // the distance the maximum is then met early and o is seldom rescaled (64
+  // sequences of 300-12000 tokens with a bias: 158 us in rising order, 137 in
+  // this one)
+  const int n = g1 - g0;
+  auto group_of = [&](int k) { return first_group + g1 - 1 - k; };
+  // the page of the run's k-th group; -1 past its end and for a page out of
+  // range
+  auto page_of = [&](int k) {
+    if (k >= n) return -1;
+    const int slot = group_of(k) >> (p.page_shift - 4);
+    const int pid = table[slot];
+    if (static_cast<uint32_t>(pid) < static_cast<uint32_t>(p.num_pages))
+      return pid;
+    if (lane == 0) record_bad_index(b, slot, pid);
+    return -1;
+  };
+  auto issue = [&](int k, int st, int pid) {
+    if (k < n)
+      load_group<D>(p, ring + st * C::kStage, scales + st * 8, hkv, pid,
+                    group_of(k) * kPaGroup, lo, len);
+    cp_async_commit();
+  };
+  // the ring's first groups, their pages looked up together; from then on a
+  // group's page is looked up one turn before its copy starts
+  int pid[kPaStages];
+#pragma unroll
+  for (int i = 0; i < kPaStages; ++i) pid[i] = page_of(warp + i * kPaWarps);
+#pragma unroll
+  for (int i = 0; i < kPaStages - 1; ++i)
+    issue(warp + i * kPaWarps, i, pid[i]);
+  int next_pid = pid[kPaStages - 1];
 
   // query fragments: row row0 + 8 nt + g, elements 64 h + 16 t .. + 15.  One
   // tile's stay in registers; two tiles' (32 registers at D = 128, which the
@@ -585,34 +625,6 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
   }
   float v_ref = 1.f;  // o is in units of this value scale
 
-  const uint32_t ring = smem_u32(smem) + warp * kPaStages * C::kStage;
-  const uint32_t scales = smem_u32(smem) + C::kOffScale + warp * kPaStages * 8;
-  const int* table = p.table + static_cast<int64_t>(b) * p.table_stride;
-  // the page of a group; -1 past the run's end and for a page out of range
-  auto page_of = [&](int gi) {
-    if (gi >= g1) return -1;
-    const int slot = (first_group + gi) >> (p.page_shift - 4);
-    const int pid = table[slot];
-    if (static_cast<uint32_t>(pid) < static_cast<uint32_t>(p.num_pages))
-      return pid;
-    if (lane == 0) record_bad_index(b, slot, pid);
-    return -1;
-  };
-  auto issue = [&](int gi, int st, int pid) {
-    if (gi < g1)
-      load_group<D>(p, ring + st * C::kStage, scales + st * 8, hkv, pid,
-                    (first_group + gi) * kPaGroup, lo, len);
-    cp_async_commit();
-  };
-  // the ring's first groups, their pages looked up together; from then on a
-  // group's page is looked up one turn before its copy starts
-  int pid[kPaStages];
-#pragma unroll
-  for (int i = 0; i < kPaStages; ++i) pid[i] = page_of(g0 + warp + i * kPaWarps);
-#pragma unroll
-  for (int i = 0; i < kPaStages - 1; ++i)
-    issue(g0 + warp + i * kPaWarps, i, pid[i]);
-  int next_pid = pid[kPaStages - 1];
   // distance of the lane's first token to the rows' positions (negative),
   // kept as it moves on: exact in f32
   float dist[NT][2];
@@ -620,18 +632,18 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      dist[nt][c] = static_cast<float>(
-          (first_group + g0 + warp) * kPaGroup + g - pos[nt][c]);
+      dist[nt][c] =
+          static_cast<float>(group_of(warp) * kPaGroup + g - pos[nt][c]);
 
   int st = 0;
   float v_inv = 1.f;  // 1 / v_ref
-  for (int gi = g0 + warp; gi < g1;
-       gi += kPaWarps, st = st + 1 == kPaStages ? 0 : st + 1) {
+  for (int k = warp; k < n;
+       k += kPaWarps, st = st + 1 == kPaStages ? 0 : st + 1) {
     cp_async_wait<kPaStages - 2>();
     __syncwarp();  // the group is in shared memory, and the one before it read
-    issue(gi + (kPaStages - 1) * kPaWarps, st == 0 ? kPaStages - 1 : st - 1,
+    issue(k + (kPaStages - 1) * kPaWarps, st == 0 ? kPaStages - 1 : st - 1,
           next_pid);
-    next_pid = page_of(gi + kPaStages * kPaWarps);
+    next_pid = page_of(k + kPaStages * kPaWarps);
     const uint32_t k_at = ring + st * C::kStage, v_at = k_at + C::kHalf;
     const uint2 sc = lds64(scales + st * 8);
     const float k_scale = __uint_as_float(sc.x);
@@ -642,17 +654,18 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         d[nt][c] = dist[nt][c];
-        dist[nt][c] += static_cast<float>(kPaGroup * kPaWarps);
+        dist[nt][c] -= static_cast<float>(kPaGroup * kPaWarps);
       }
     if (k_scale == 0.f) continue;  // a page that is not there (whole warp)
-    const int tok = (first_group + gi) * kPaGroup;
+    const int tok = group_of(k) * kPaGroup;
 
     // ---- S^T = K q^T
-    float s[NT][4];
+    // (in two chains of accumulation, as each product waits for the one before)
+    float s[NT][4], s1[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+      for (int i = 0; i < 4; ++i) s[nt][i] = s1[nt][i] = 0.f;
     uint4 qs[NT];
 #pragma unroll
     for (int h = 0; h < D / 64; ++h) {
@@ -665,8 +678,8 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
         const uint32_t a0 = e4m3x2_to_f16x2(xw[j]), a2 = e4m3x2_to_f16x2_hi(xw[j]);
         const uint32_t a1 = e4m3x2_to_f16x2(yw[j]), a3 = e4m3x2_to_f16x2_hi(yw[j]);
         if (NT == 1) {
-          mma16816(s[0], a0, a1, a2, a3, qf[0][4 * h + j][0],
-                   qf[0][4 * h + j][1]);
+          mma16816((j & 1) ? s1[0] : s[0], a0, a1, a2, a3,
+                   qf[0][4 * h + j][0], qf[0][4 * h + j][1]);
         } else {
           if ((j & 1) == 0)
 #pragma unroll
@@ -674,7 +687,8 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
               qs[nt] = lds128(q_at + (nt * (kSteps / 2) + 2 * h + j / 2) * 512);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            mma16816(s[nt], a0, a1, a2, a3, (j & 1) ? qs[nt].z : qs[nt].x,
+            mma16816((j & 1) ? s1[nt] : s[nt], a0, a1, a2, a3,
+                     (j & 1) ? qs[nt].z : qs[nt].x,
                      (j & 1) ? qs[nt].w : qs[nt].y);
         }
       }
@@ -689,7 +703,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int c = i & 1, j = tok + g + (i >> 1) * 8;
-        float x = s[nt][i] * (q_mul[nt][c] * k_scale);
+        float x = (s[nt][i] + s1[nt][i]) * (q_mul[nt][c] * k_scale);
         if (p.mod.kind & kModCap)
           x = fmaf(-2.f * p.mod.cap_log2, rcp_approx(ex2_approx(x) + 1.f),
                    p.mod.cap_log2);
@@ -973,9 +987,10 @@ __global__ void __launch_bounds__(kPaThreads, kPaPerSm<D, NT>)
   }
 }
 
-// Joins the parts of the items that were cut, a warp per query row, and
-// writes the rows of sequences without tokens.
-template <int D, int NT>
+// Joins the parts of the items that were cut and writes the rows of sequences
+// without tokens: a warp per query row, or (WIDE) a block, whose warps share
+// the parts.
+template <int D, int NT, bool WIDE>
 __global__ void __launch_bounds__(kPaThreads)
     paged_join_kernel(const PagedParams p, const int grid) {
   constexpr int R = 8 * NT, kPer = D / 32;
@@ -984,7 +999,7 @@ __global__ void __launch_bounds__(kPaThreads)
   const int per = p.H_kv * tiles;
   const int b = blockIdx.z, item = blockIdx.y;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int r = blockIdx.x * kPaWarps + warp;
+  const int r = WIDE ? blockIdx.x : blockIdx.x * kPaWarps + warp;
   const int rr = item % tiles * R + r;
   const PaScan scan = scan_before(p, b);
   const int64_t units = scan.all * per;
@@ -1025,19 +1040,22 @@ __global__ void __launch_bounds__(kPaThreads)
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
   const float base = mx == NEG_INF ? 0.f : mx;
   float sum = 0.f;
-  for (int64_t c = c0; c <= c1; c += 32) {
-    // lane i: the weight of part c + i
+  constexpr int kStep = WIDE ? kPaWarps : 1;
+  const int64_t first = c0 + (WIDE ? warp : 0);
+  for (int64_t c = first; c <= c1; c += 32 * kStep) {
+    // lane i: the weight of part c + i kStep
     float f = 0.f;
-    if (c + lane <= c1) {
-      const float* part = part_of(c + lane) + R * D + r;
+    if (c + lane * kStep <= c1) {
+      const float* part = part_of(c + lane * kStep) + R * D + r;
       f = ex2_approx(part[0] - base);
       sum = fmaf(part[R], f, sum);
     }
-    const int m = static_cast<int>(min(c1 - c + 1, static_cast<int64_t>(32)));
+    const int m = static_cast<int>(
+        min((c1 - c) / kStep + 1, static_cast<int64_t>(32)));
 #pragma unroll 8
     for (int i = 0; i < m; ++i) {
       const float w = __shfl_sync(0xffffffffu, f, i);
-      const float* o = part_of(c + i) + r * D + lane * kPer;
+      const float* o = part_of(c + i * kStep) + r * D + lane * kPer;
       float v[kPer];
       if (kPer == 4) {
         const float4 q = *reinterpret_cast<const float4*>(o);
@@ -1056,6 +1074,23 @@ __global__ void __launch_bounds__(kPaThreads)
   }
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if (WIDE) {  // (all warps of the block come here, or none: one row)
+    __shared__ float shared_x[kPaWarps][D], shared_sum[kPaWarps];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) shared_x[warp][lane * kPer + i] = x[i];
+    if (lane == 0) shared_sum[warp] = sum;
+    __syncthreads();
+    if (warp > 0) return;
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kPaWarps; ++w) {
+      sum += shared_sum[w];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) x[i] += shared_x[w][lane * kPer + i];
+    }
+  }
   write_row<kPer>(p, b, head, t, lane * kPer, base, sum, x);
 }
 
@@ -1073,7 +1108,12 @@ cudaError_t launch_paged(const PagedParams& p, int num_sms,
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((min(rows, 8 * NT) + kPaWarps - 1) / kPaWarps,
+  // few rows, which may each have many parts: a block per row (one sequence of
+  // 8000 tokens and one K/V head: 20 us with a warp per row, 12.4 so)
+  const int tile_rows = min(rows, 8 * NT);
+  const bool wide =
+      static_cast<int64_t>(p.B) * p.H_kv * tiles * tile_rows <= 4 * num_sms;
+  cfg.gridDim = dim3(wide ? tile_rows : (tile_rows + kPaWarps - 1) / kPaWarps,
                      p.H_kv * tiles, p.B);
   cfg.blockDim = dim3(kPaThreads);
   cfg.stream = stream;
@@ -1082,7 +1122,10 @@ cudaError_t launch_paged(const PagedParams& p, int num_sms,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, NT>, p, grid);
+  return wide
+             ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, NT, true>, p, grid)
+             : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, NT, false>, p,
+                                  grid);
 }
 
 }  // namespace
