@@ -26,6 +26,7 @@ from .api import (  # noqa: F401
     bsm_paged_attention_workspace_bytes,
     bsm_selftest_wait_timeout,
     bsm_splash_bwd,
+    bsm_splash_bwd_mod_workspace_bytes,
     bsm_splash_bwd_workspace_bytes,
     bsm_splash_fwd,
     bsm_splash_fwd_host,

@@ -143,6 +143,8 @@ def _declare(lib):
         c.c_int32, c.c_int32, c.c_int32, c.POINTER(MaskInfoStruct),
         c.c_void_p, c.c_void_p, c.c_float, c.c_int32, tv, tv, tv, c.c_void_p,
         c.c_size_t, c.c_void_p]
+    lib.bsm_splash_bwd_mod_workspace_bytes.restype = c.c_size_t
+    lib.bsm_splash_bwd_mod_workspace_bytes.argtypes = [c.c_int32] * 6
     lib.bsm_splash_bwd_mod.restype = c.c_int
     lib.bsm_splash_bwd_mod.argtypes = [
         vp, vp, vp, vp, vp, vp, c.c_int32, c.c_int32, c.c_int32, c.c_int32,
@@ -202,7 +204,8 @@ def lib():
 _fast = None
 _FAST_NAMES = ("bsm_mask_info_bytes", "bsm_build_mask_info",
                "bsm_splash_fwd_mod", "bsm_splash_bwd_mod",
-               "bsm_splash_bwd_workspace_bytes", "bsm_kv_append",
+               "bsm_splash_bwd_workspace_bytes",
+               "bsm_splash_bwd_mod_workspace_bytes", "bsm_kv_append",
                "bsm_paged_attention", "bsm_splash_fwd_workspace_bytes",
                "bsm_paged_attention_workspace_bytes")
 

@@ -325,6 +325,12 @@ def bsm_splash_bwd_workspace_bytes(B: int, H: int, Sq: int,
     return int(_lib.lib().bsm_splash_bwd_workspace_bytes(B, H, Sq, score))
 
 
+def bsm_splash_bwd_mod_workspace_bytes(B: int, H: int, H_kv: int, Sq: int,
+                                       Skv: int, D: int) -> int:
+    return int(_lib.lib().bsm_splash_bwd_mod_workspace_bytes(B, H, H_kv, Sq,
+                                                             Skv, D))
+
+
 def bsm_splash_bwd(q, k, v, out, lse, dout, mask_info: MaskInfo,
                    q_segment_ids, kv_segment_ids, scale: float, score: int,
                    dq, dk, dv, stream=None, workspace=None,
@@ -336,7 +342,8 @@ def bsm_splash_bwd(q, k, v, out, lse, dout, mask_info: MaskInfo,
     H_kv, Skv = k.shape[1], k.shape[2]
     sh = _stream_handle(stream)
     mod = _score_mod(softcap, alibi_slopes, H, q.device)
-    need = bsm_splash_bwd_workspace_bytes(B, H, Sq, score)
+    need = bsm_splash_bwd_workspace_bytes(B, H, Sq, score) if mod is None \
+        else bsm_splash_bwd_mod_workspace_bytes(B, H, H_kv, Sq, Skv, D)
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     views, at = _views(q, k, v, out, dout, dq, dk, dv)

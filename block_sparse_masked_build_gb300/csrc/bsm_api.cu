@@ -653,6 +653,18 @@ size_t bsm_splash_bwd_workspace_bytes(int32_t B, int32_t H, int32_t Sq,
   return align_up(static_cast<size_t>(B) * H * Sq * sizeof(float), 256);
 }
 
+size_t bsm_splash_bwd_mod_workspace_bytes(int32_t B, int32_t H, int32_t H_kv,
+                                          int32_t Sq, int32_t Skv, int32_t D) {
+  const size_t base = bsm_splash_bwd_workspace_bytes(B, H, Sq,
+                                                     BSM_SCORE_SOFTMAX);
+  if (B < 0 || H < 0 || H_kv < 1 || H % H_kv != 0 || Sq < 0 || Skv < 0 || D < 0)
+    return base;
+  const size_t parts = bsm::bwd_parts(B, H, H_kv, Sq, Skv);
+  return parts < 2 ? base
+                   : base + parts * 2 * sizeof(float) * static_cast<size_t>(B) *
+                                H_kv * Skv * D;
+}
+
 bsm_status bsm_splash_bwd(const bsm_tensor* q, const bsm_tensor* k,
                           const bsm_tensor* v, const bsm_tensor* out,
                           const float* lse, const bsm_tensor* dout, int32_t B,
@@ -822,6 +834,15 @@ bsm_status bsm_splash_bwd_mod(const bsm_tensor* q, const bsm_tensor* k,
   p.dv_sb = dv->strides[0];
   p.dv_sh = dv->strides[1];
   p.dv_ss = dv->strides[2];
+  p.parts = 1;
+  p.part_sums = nullptr;
+  if (sm_mod.kind != 0 &&
+      workspace_bytes >=
+          bsm_splash_bwd_mod_workspace_bytes(B, H, H_kv, Sq, Skv, D)) {
+    p.parts = bsm::bwd_parts(B, H, H_kv, Sq, Skv);
+    p.part_sums =
+        reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws_need);
+  }
   p.timeout_ns = wait_timeout_ns();
   cudaError_t e = bsm::launch_splash_bwd(p, tq, tk, tv, tdo,
                                          static_cast<cudaStream_t>(stream));

@@ -235,7 +235,7 @@ __device__ __forceinline__ void bwd_load_role(
     const BwdParams& p, const CUtensorMap* tq, const CUtensorMap* tk,
     const CUtensorMap* tv, const CUtensorMap* tdo, uint8_t* smem,
     BwdBars* bars, const uint16_t* list, int b, int hq_or_hkv, int fixed_tile,
-    int n_iter) {
+    int it0, int n_iter) {
   using C = BwdCfg<D>;
   const int lane = threadIdx.x % 32;
   volatile int* abort_flag = &bars->abort;
@@ -268,11 +268,12 @@ __device__ __forceinline__ void bwd_load_role(
       break;
     }
     if (lane == 0) {
-      const int e = it % n_list;
+      const int e = (it0 + it) % n_list;
       const int tile = list[e] >> 2;
-      // dK/dV: Q and dO of query head hkv * G + it / n_list; dQ: K and V
+      // dK/dV: Q and dO of query head hkv * G + step / n_list; dQ: K and V
       // of the query head's K/V head
-      const int head = DKDV ? hq_or_hkv * G + it / n_list : hq_or_hkv / G;
+      const int head =
+          DKDV ? hq_or_hkv * G + (it0 + it) / n_list : hq_or_hkv / G;
       uint8_t* dst = smem + C::kOffT + s * 2 * C::kTileBytes;
       mbar_arrive_expect_tx(&bars->t_full[s], 2 * C::kTileBytes);
       for (int kb = 0; kb < C::kKBlocks; ++kb) {
@@ -800,7 +801,8 @@ __device__ __forceinline__ void bwd_elem_role(const BwdParams& p,
 template <int D, int MOD, bool DKDV>
 __device__ __forceinline__ void bwd_elem_mod_role(
     const BwdParams& p, BwdBars* bars, const uint16_t* list, float* stats,
-    uint32_t tmem, int b, int hq_or_hkv, int fixed_tile, int n_iter) {
+    uint32_t tmem, int b, int hq_or_hkv, int fixed_tile, int it0, int n_iter,
+    int cut) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int quarter = warp % 4;     // TMEM lanes this warp may access
   const int part = (warp - 2) / 4;  // columns [32 part, 32 part + 32)
@@ -829,8 +831,9 @@ __device__ __forceinline__ void bwd_elem_mod_role(
   // gets lse = inf, so P = 0 (its zero dO alone makes it vanish unless a rising
   // bias overflows P)
   auto load_stats = [&](int it, float& l2, float& dl, float& slope) {
-    const int qc = (list[it % n_list] >> 2) * kTileM + part * 32 + lane;
-    const int hd = hq_or_hkv * G + it / n_list;
+    const int step = it0 + it;
+    const int qc = (list[step % n_list] >> 2) * kTileM + part * 32 + lane;
+    const int hd = hq_or_hkv * G + step / n_list;
     l2 = __int_as_float(0x7f800000);
     dl = 0.f;
     if (qc < p.Sq) {
@@ -849,7 +852,7 @@ __device__ __forceinline__ void bwd_elem_mod_role(
   }
   bool ok = true;
   for (int it = 0; it < n_iter; ++it) {
-    const int e = it % n_list;
+    const int e = (it0 + it) % n_list;
     const int tile = list[e] >> 2, cls = list[e] & 3;
     const int col0 = tile * kTileM + part * 32;
     const float slope2 = slope_n;
@@ -970,7 +973,18 @@ __device__ __forceinline__ void bwd_elem_mod_role(
 #pragma unroll
       for (int j = 0; j < 32; ++j) o[j] = 0u;
     }
-    if (row_ok) {
+    if (DKDV && p.parts > 1) {
+      // one part of the walk: f32 sums for the kernel that adds them up
+      if (row_ok) {
+        float* at = p.part_sums +
+                    ((((static_cast<int64_t>(cut) * 2 + a) * p.B + b) * p.Hkv +
+                      hq_or_hkv) * p.Skv + row) * D + part * 32;
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+          st_global_v4(at + v * 4, o[4 * v], o[4 * v + 1], o[4 * v + 2],
+                       o[4 * v + 3]);
+      }
+    } else if (row_ok) {
       uint32_t w[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j)
@@ -1022,6 +1036,11 @@ __global__ void __launch_bounds__(bwd_threads(MOD), 1)
     head = g % gridDim.y;
     b = g / gridDim.y;
   }
+  int cut = 0;  // part of the walk (dK/dV with modified scores)
+  if (MOD != 0 && DKDV) {
+    cut = b % p.parts;
+    b /= p.parts;
+  }
   const int table = (p.flags & BSM_MASK_SEGMENT) ? b : 0;
   // The dQ grid reads nothing the dK/dV grid writes, so it is launched as
   // its programmatic dependent: once every dK/dV CTA has started, dQ CTAs
@@ -1062,12 +1081,18 @@ __global__ void __launch_bounds__(bwd_threads(MOD), 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  const int n_iter = bars->n_list * (DKDV ? p.H / p.Hkv : 1);
+  int it0 = 0;
+  int n_iter = bars->n_list * (DKDV ? p.H / p.Hkv : 1);
+  if (MOD != 0 && DKDV) {  // (a walk has less than 2^24 steps, parts are 8)
+    const int end = n_iter * (cut + 1) / p.parts;
+    it0 = n_iter * cut / p.parts;
+    n_iter = end - it0;
+  }
 
   if (warp == 0) {
     if (n_iter > 0)
       bwd_load_role<D, DKDV>(p, &tm_q, &tm_k, &tm_v, &tm_do, smem, bars, list,
-                             b, head, fixed_tile, n_iter);
+                             b, head, fixed_tile, it0, n_iter);
   } else if (warp == 1) {
     if (n_iter > 0) bwd_mma_role<D, DKDV>(p, smem, bars, tmem, n_iter);
   } else {
@@ -1075,7 +1100,7 @@ __global__ void __launch_bounds__(bwd_threads(MOD), 1)
       float* stats = reinterpret_cast<float*>(smem + C::kOffStat) +
                      (warp - 2) * 64;
       bwd_elem_mod_role<D, MOD, DKDV>(p, bars, list, stats, tmem, b, head,
-                                      fixed_tile, n_iter);
+                                      fixed_tile, it0, n_iter, cut);
     } else {
       bwd_elem_role<D, SCORE, DKDV>(p, bars, list, tmem, b, head, fixed_tile,
                                     n_iter);
@@ -1142,7 +1167,8 @@ cudaError_t launch_bwd_one(const BwdParams& p, const CUtensorMap& tq,
   cudaError_t e = cudaFuncSetAttribute(
       kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  const dim3 grid = DKDV ? dim3((p.Skv + kTileN - 1) / kTileN, p.Hkv, p.B)
+  const int cuts = MOD != 0 ? p.parts : 1;
+  const dim3 grid = DKDV ? dim3((p.Skv + kTileN - 1) / kTileN, p.Hkv, p.B * cuts)
                          : dim3((p.Sq + kTileM - 1) / kTileM, p.H, p.B);
   if (DKDV) {
     kern<<<grid, bwd_threads(MOD), kSmem, stream>>>(tq, tk, tv, tdo, p);
@@ -1164,6 +1190,35 @@ cudaError_t launch_bwd_one(const BwdParams& p, const CUtensorMap& tq,
   return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, tdo, p);
 }
 
+// Adds up the parts of dK and dV in order: a thread per four elements.
+__global__ void __launch_bounds__(256) bwd_sum_kernel(const BwdParams p) {
+  const int64_t n = static_cast<int64_t>(p.B) * p.Hkv * p.Skv * p.D;
+  const int64_t i =
+      (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * 4;
+  if (i >= n) return;
+  const bool is_dk = blockIdx.y == 1;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = 0; c < p.parts; ++c) {
+    const float4 v = *reinterpret_cast<const float4*>(
+        p.part_sums + (static_cast<int64_t>(c) * 2 + is_dk) * n + i);
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  const float mul = is_dk ? p.scale : 1.f;
+  const int d = static_cast<int>(i % p.D);
+  const int64_t row = i / p.D;
+  const int64_t k = row % p.Skv, bh = row / p.Skv;
+  const int64_t h = bh % p.Hkv, b = bh / p.Hkv;
+  uint16_t* dst = is_dk ? p.dk + b * p.dk_sb + h * p.dk_sh + k * p.dk_ss
+                        : p.dv + b * p.dv_sb + h * p.dv_sh + k * p.dv_ss;
+  *reinterpret_cast<uint2*>(dst + d) =
+      make_uint2(pack_bf16x2(s.x * mul, s.y * mul),
+                 pack_bf16x2(s.z * mul, s.w * mul));
+}
+
 template <int D, int SCORE, int MOD>
 cudaError_t launch_bwd_d(const BwdParams& p, const CUtensorMap& tq,
                          const CUtensorMap& tk, const CUtensorMap& tv,
@@ -1172,6 +1227,13 @@ cudaError_t launch_bwd_d(const BwdParams& p, const CUtensorMap& tq,
   if (p.Skv > 0) e = launch_bwd_one<D, SCORE, MOD, true>(p, tq, tk, tv, tdo, stream);
   if (e != cudaSuccess) return e;
   if (p.Sq > 0) e = launch_bwd_one<D, SCORE, MOD, false>(p, tq, tk, tv, tdo, stream);
+  if (e == cudaSuccess && MOD != 0 && p.parts > 1) {
+    // (after the dQ grid, which ends after the dK/dV grid)
+    const int64_t n = static_cast<int64_t>(p.B) * p.Hkv * p.Skv * D;
+    bwd_sum_kernel<<<dim3(static_cast<unsigned>((n / 4 + 255) / 256), 2), 256,
+                     0, stream>>>(p);
+    e = cudaGetLastError();
+  }
   return e;
 }
 
@@ -1187,6 +1249,24 @@ cudaError_t launch_bwd_score(const BwdParams& p, const CUtensorMap& tq,
 }
 
 }  // namespace
+
+// With few key tiles (short sequences, few K/V heads) the dK/dV grid leaves
+// most SMs idle while each CTA walks every query head of its group, one step
+// after another; the walks are then cut into up to eight parts, as far as the
+// grid stays within one CTA per SM of 152 and a part has six steps.  Cap 50:
+// causal S=1024, 8/1 heads 146 us uncut, 40 in eight parts; S=1000, B=2, 16/4
+// heads 103 uncut, 82 in two, 88 in four; S=512, 8/8 heads (walks of four
+// steps) 24 uncut, 30 in two parts: the kernel that adds them up costs 5.
+int bwd_parts(int64_t B, int64_t H, int64_t Hkv, int64_t Sq, int64_t Skv) {
+  constexpr int64_t kBwdCtas = 152, kMaxParts = 8, kMinSteps = 6;
+  if (B * Hkv * Skv * Sq == 0) return 1;
+  const int64_t walks = (Skv + kTileN - 1) / kTileN * Hkv * B;
+  const int64_t steps = (Sq + kTileM - 1) / kTileM * (H / Hkv);
+  int64_t n = kBwdCtas / walks;
+  if (n > kMaxParts) n = kMaxParts;
+  if (n > steps / kMinSteps) n = steps / kMinSteps;
+  return n < 1 ? 1 : static_cast<int>(n);
+}
 
 cudaError_t launch_splash_bwd(const BwdParams& p, const CUtensorMap& tq,
                               const CUtensorMap& tk, const CUtensorMap& tv,

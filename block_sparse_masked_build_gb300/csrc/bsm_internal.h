@@ -135,8 +135,14 @@ struct BwdParams {
   int64_t dk_sb, dk_sh, dk_ss;
   uint16_t* dv;
   int64_t dv_sb, dv_sh, dv_ss;
+  // modified scores: the dK/dV walks cut into this many parts, and where they
+  // leave f32 sums: [part][dV, dK][B][Hkv][Skv][D]
+  int32_t parts;
+  float* part_sums;
   uint64_t timeout_ns;
 };
+// Parts of a dK/dV walk (a function of the sizes alone).
+int bwd_parts(int64_t B, int64_t H, int64_t Hkv, int64_t Sq, int64_t Skv);
 
 struct AppendParams {
   uint8_t *k, *v;  // pages [num_pages][H_kv][page_size][D], e4m3

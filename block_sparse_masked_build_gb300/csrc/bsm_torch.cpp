@@ -36,6 +36,7 @@ decltype(&bsm_kv_append) f_kv_append;
 decltype(&bsm_paged_attention) f_paged_attention;
 size_t fwd_workspace_bytes, paged_workspace_bytes;
 decltype(&bsm_splash_bwd_workspace_bytes) f_bwd_workspace_bytes;
+decltype(&bsm_splash_bwd_mod_workspace_bytes) f_bwd_mod_workspace_bytes;
 PyObject* on_status;  // Python callable that raises for a status
 
 // A Python exception is set.
@@ -315,7 +316,13 @@ PyObject* py_splash_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     OnDevice on(dev, a[13]);
     at::Tensor g[3] = {at::empty_like(q), at::empty_like(k), at::empty_like(v)};
     const bsm_tensor gv[3] = {view(g[0]), view(g[1]), view(g[2])};
-    const size_t need = f_bwd_workspace_bytes(B, H, Sq, score);
+    const bool modified = mod.softcap != 0.f || mod.alibi_slopes != nullptr;
+    const size_t need =
+        modified ? f_bwd_mod_workspace_bytes(
+                       B, H, static_cast<int32_t>(k.size(1)), Sq,
+                       static_cast<int32_t>(k.size(2)),
+                       static_cast<int32_t>(q.size(3)))
+                 : f_bwd_workspace_bytes(B, H, Sq, score);
     at::Tensor ws;
     if (need > 0) ws = empty_on({static_cast<int64_t>(need)}, at::kByte, dev);
     check_status(f_splash_bwd_mod(
@@ -479,6 +486,7 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     set(f_splash_fwd_mod, "bsm_splash_fwd_mod");
     set(f_splash_bwd_mod, "bsm_splash_bwd_mod");
     set(f_bwd_workspace_bytes, "bsm_splash_bwd_workspace_bytes");
+    set(f_bwd_mod_workspace_bytes, "bsm_splash_bwd_mod_workspace_bytes");
     set(f_kv_append, "bsm_kv_append");
     set(f_paged_attention, "bsm_paged_attention");
     decltype(&bsm_splash_fwd_workspace_bytes) f0;

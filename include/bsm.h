@@ -390,7 +390,11 @@ bsm_status bsm_splash_bwd(const bsm_tensor* q, const bsm_tensor* k,
  * t = tanh(x / softcap), P = exp(z - lse) over the visible keys and D_q as
  * above: dV = P^T dout, dS = P * (dout V^T - D_q) * (1 - t^2) (no factor
  * without a cap), dQ = scale dS K, dK = scale dS^T Q.  The slopes get no
- * gradient. */
+ * gradient.
+ *   workspace    as for bsm_splash_bwd; with at least
+ *                bsm_splash_bwd_mod_workspace_bytes(...) bytes, short inputs
+ *                run faster: their dK/dV sums are spread over more CTAs and
+ *                added up in f32 (which rounds in another order) */
 bsm_status bsm_splash_bwd_mod(const bsm_tensor* q, const bsm_tensor* k,
                               const bsm_tensor* v, const bsm_tensor* out,
                               const float* lse, const bsm_tensor* dout,
@@ -403,6 +407,12 @@ bsm_status bsm_splash_bwd_mod(const bsm_tensor* q, const bsm_tensor* k,
                               const bsm_tensor* dq, const bsm_tensor* dk,
                               const bsm_tensor* dv, void* workspace,
                               size_t workspace_bytes, void* stream);
+
+/* Bytes with which bsm_splash_bwd_mod spreads the dK/dV sums of short inputs:
+ * bsm_splash_bwd_workspace_bytes plus f32 partial sums (none for inputs whose
+ * key tiles fill the GPU). */
+size_t bsm_splash_bwd_mod_workspace_bytes(int32_t B, int32_t H, int32_t H_kv,
+                                          int32_t Sq, int32_t Skv, int32_t D);
 
 /* A paged cache of keys and values in 8-bit floating point (no counterpart on
  * the pages; it serves tokens one by one after the prompt's forward).  A page

@@ -185,6 +185,51 @@ def test_rising_bias_past_the_last_query():
     run(q, k, v, do, 0, slopes=torch.tensor([-1.0]))
 
 
+@pytest.mark.parametrize("kind", ["causal", "segments", "full"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_cut_key_walks(kind, D):
+    # few keys and K/V heads under many query heads: dK and dV are summed in
+    # parts, here with walks that do not divide evenly, and with part of the
+    # walks empty; without the larger workspace they are summed in one
+    B, H, Hkv, Sq, Skv = 1, 10, 1, 460, 300
+    assert bsm.bsm_splash_bwd_mod_workspace_bytes(B, H, Hkv, Sq, Skv, D) > \
+        bsm.bsm_splash_bwd_workspace_bytes(B, H, Sq, 0)
+    q, k, v, do = inputs(f"cut{kind}{D}", B, H, Hkv, Sq, Skv, D, 3.0)
+    sq = sk = None
+    flags = 0 if kind == "full" else C
+    if kind == "segments":
+        flags = C | SG
+        sq = wl.random_segment_ids(B, Sq, 30, 90, 5)
+        sk = sq[:, :Skv].copy()
+        sk[:, 128:256] = 99  # a key tile that no query sees
+    _, _, grads = run(q, k, v, do, flags, 0, sq, sk, softcap=6.0,
+                      slopes=slopes_of(H))
+    if kind == "segments":
+        assert (grads[1][:, :, 128:256] == 0).all()
+        assert (grads[2][:, :, 128:256] == 0).all()
+
+
+def test_cut_and_whole_walks_agree():
+    B, H, Hkv, S, D = 1, 8, 1, 300, 128
+    q, k, v, do = (t.cuda() for t in inputs("whole", B, H, Hkv, S, S, D, 2.0))
+    info = bsm.build_mask_info(C, B, S, S)
+    out, lse = bsm.splash_attention(q, k, v, mask_info=info, softcap=9.0)
+    res = []
+    for n in (bsm.bsm_splash_bwd_workspace_bytes(B, H, S, 0),
+              bsm.bsm_splash_bwd_mod_workspace_bytes(B, H, Hkv, S, S, D)):
+        ws = torch.full((n,), 0xff, dtype=torch.uint8).cuda()  # NaN leftovers
+        g = [torch.full_like(t, float("nan")) for t in (q, k, v)]
+        bsm.bsm_splash_bwd(q, k, v, out, lse, do, info, None, None,
+                           1 / math.sqrt(D), 0, *g, workspace=ws, softcap=9.0)
+        res.append(g)
+    assert torch.equal(res[0][0], res[1][0])
+    for a, b in zip(res[0][1:], res[1][1:]):
+        # equal f32 sums up to their order, then one rounding to bf16 each
+        a, b = a.double(), b.double()
+        assert ((a - b).abs() <= HALF * 2.1 * a.abs() + 1e-5 *
+                a.abs().amax()).all()
+
+
 def test_no_modification_is_the_unmodified_call():
     q, k, v, do = (t.cuda() for t in inputs("none", 1, 2, 2, 300, 300, 128))
     a = bsm.splash_attention(q, k, v)
