@@ -438,6 +438,8 @@ def bsm_kv_append(cache: KVCache, page_table, lens, k_new, v_new, n_new=None,
     shape = (B, s.H_kv, T, s.D)
     _check_tokens(k_new, shape, dev, "k_new")
     _check_tokens(v_new, shape, dev, "v_new")
+    if dev.type != "cuda":
+        raise ValueError("the cache must be on a CUDA device")
     views, at = _views(k_new, v_new)
     _check(_lib.lib().bsm_kv_append(
         s, page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
@@ -494,6 +496,10 @@ def bsm_paged_attention(q, cache: KVCache, page_table, lens, scale: float,
         raise ValueError("lse must be a contiguous float32 tensor [B, H, T] "
                          "beside the cache")
     mod = _score_mod(softcap, alibi_slopes, H, dev)
+    if dev.type != "cuda":
+        raise ValueError("the cache must be on a CUDA device")
+    if window >= 2 ** 31:
+        raise ValueError("integer out of range")
     sh = _stream_handle(stream)
     if workspace is None:
         workspace = _paged_workspace(dev, sh)

@@ -215,14 +215,15 @@ bsm_status check_mod(const bsm_score_mod* mod, float scale, int32_t score,
                                     0.1330069738,    -0.05252428411,
                                     0.01868168763,   -0.004920490605,
                                     0.0006554170517};
-    if (std::fabs(c1) >= 0x1p-10 && std::fabs(c1) <= 0x1p6 && cap <= 0x1p12) {
+    if (std::fabs(c1) >= 0x1p-18 && std::fabs(c1) <= 0x1p6 && cap <= 0x1p20) {
       double f = cap * log2e * c1;
       for (int i = 0; i < 7; ++i, f *= c1 * c1) {
         if (i < 4) out->poly[i] = static_cast<float>(kNear[i] * f);
         out->wide[i] = static_cast<float>(kWide[i] * f);
       }
       out->poly_max = static_cast<float>(0.5 / std::fabs(c1));
-      out->wide_max = static_cast<float>(1.2 / std::fabs(c1));
+      if (std::fabs(c1) >= 0x1p-10)
+        out->wide_max = static_cast<float>(1.2 / std::fabs(c1));
     }
     out->m_fixed = std::fmax(0.f, out->cap_log2 - 52.f);
     out->inv_cap2 = 1.f / (out->cap_log2 * out->cap_log2);
@@ -964,7 +965,7 @@ bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
   p.B = B;
   p.H = H;
   p.T = T;
-  p.window = window;
+  p.window = window < (1 << 30) ? window : 1 << 30;  // no sequence is longer
   p.q = static_cast<const uint16_t*>(q->data);
   p.q_sb = q->strides[0];
   p.q_sh = q->strides[1];

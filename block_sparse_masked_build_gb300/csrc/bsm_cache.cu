@@ -704,9 +704,21 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
       for (int i = 0; i < 4; ++i) {
         const int c = i & 1, j = tok + g + (i >> 1) * 8;
         float x = (s[nt][i] + s1[nt][i]) * (q_mul[nt][c] * k_scale);
-        if (p.mod.kind & kModCap)
-          x = fmaf(-2.f * p.mod.cap_log2, rcp_approx(ex2_approx(x) + 1.f),
-                   p.mod.cap_log2);
+        if (p.mod.kind & kModCap) {
+          // tanh(y) = 1 - 2 / (1 + 2^x), x = 2 y log2(e): off by 2^-23 of the
+          // cap.  Above a cap of about 200 that would show in the logits, and
+          // small y take the polynomial of the forward instead
+          const float z = fmaf(-2.f * p.mod.cap_log2,
+                               rcp_approx(ex2_approx(x) + 1.f), p.mod.cap_log2);
+          const float y = x * 0.34657359f, y2 = y * y;
+          x = p.mod.cap_log2 > 300.f && y2 <= 0.25f
+                  ? p.mod.cap_log2 * y *
+                        fmaf(y2, fmaf(y2, fmaf(y2, -0.04439273843f,
+                                               0.1318993943f),
+                                      -0.3332628423f),
+                             0.999999451f)
+                  : z;
+        }
         if (p.mod.kind & kModBias)
           x = fmaf(slope2[nt][c], d[nt][c] + (i >> 1) * 8.f, x);
         if (!inner &&

@@ -160,6 +160,56 @@ bsm_score_mod score_mod(double softcap, const at::Tensor& slopes, int64_t H,
   return m;
 }
 
+// The operands of a forward or backward: bf16 tensors of one CUDA device with
+// the shapes that the pointers will be read with.
+void check_operands(const at::Tensor& q, const at::Tensor& k,
+                    const at::Tensor& v) {
+  const at::Device dev = q.device();
+  if (!dev.is_cuda()) value_error("q must be a CUDA tensor");
+  const std::pair<const char*, const at::Tensor&> all[3] = {
+      {"q", q}, {"k", k}, {"v", v}};
+  for (const auto& [name, t] : all) {
+    if (t.dim() != 4 || t.stride(3) != 1)
+      value_error(
+          "tensors must be 4-D [B, H, S, D] views with a contiguous head "
+          "dimension");
+    if (t.scalar_type() != at::kBFloat16 || t.device() != dev)
+      value_error(std::string(name) + " must be a bfloat16 tensor on " +
+                  device_name(dev));
+  }
+  if (k.sizes() != v.sizes() || k.size(0) != q.size(0) ||
+      k.size(3) != q.size(3))
+    value_error("k and v must be [B, H_kv, Skv, D] for q's B and D");
+}
+
+// A tensor with the shape and device of `like` (bf16).
+void check_like(const at::Tensor& t, const at::Tensor& like, const char* name) {
+  if (t.defined() &&
+      (t.scalar_type() != at::kBFloat16 || t.sizes() != like.sizes() ||
+       t.device() != like.device()))
+    value_error(std::string(name) + " must be a bfloat16 tensor of q's shape "
+                                    "and device");
+}
+
+void check_lse(const at::Tensor& t, const at::Tensor& q) {
+  if (t.defined() &&
+      (t.scalar_type() != at::kFloat || t.dim() != 3 ||
+       t.size(0) != q.size(0) || t.size(1) != q.size(1) ||
+       t.size(2) != q.size(2) || !t.is_contiguous() ||
+       t.device() != q.device()))
+    value_error("lse must be a contiguous float32 tensor [B, H, Sq] on q's "
+                "device");
+}
+
+void check_ids(const at::Tensor& t, int64_t B, int64_t S,
+               const at::Device& dev, const char* name) {
+  if (t.defined() &&
+      (t.scalar_type() != at::kInt || t.dim() != 2 || t.size(0) != B ||
+       t.size(1) != S || !t.is_contiguous() || t.device() != dev))
+    value_error(std::string(name) + " must be a contiguous int32 tensor [B, S] "
+                                    "on " + device_name(dev));
+}
+
 // Makes the tensors' device current for a call, and gives the stream: the
 // one asked for (an integer handle) or that device's current one.
 struct OnDevice {
@@ -237,6 +287,10 @@ PyObject* py_build_mask_info(PyObject*, PyObject* const* a, Py_ssize_t n) {
                          static_cast<c10::DeviceIndex>(
                              a[10] == Py_None ? c10::cuda::current_device()
                                               : integer(a[10])));
+    if ((qs.defined() && !qs.device().is_cuda()) ||
+        (ks.defined() && !ks.device().is_cuda()) ||
+        (bits.defined() && !bits.device().is_cuda()))
+      value_error("segment ids and dense_bits must be CUDA tensors");
     OnDevice on(dev, a[12]);
     at::Tensor buf =
         empty_on({static_cast<int64_t>(bytes)}, at::kByte, dev);
@@ -254,18 +308,23 @@ PyObject* py_splash_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     expect(n, 14);
     const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"),
                      &v = tensor(a[2], "v");
+    check_operands(q, k, v);
     const bsm_tensor qv = view(q), kv = view(k), vv = view(v);
     const at::Tensor qs = tensor_or_none(a[4], "q_segment_ids");
     const at::Tensor ks = tensor_or_none(a[5], "kv_segment_ids");
     const at::Device dev = q.device();
+    check_ids(qs, q.size(0), q.size(2), dev, "q_segment_ids");
+    check_ids(ks, k.size(0), k.size(2), dev, "kv_segment_ids");
     const int64_t B = q.size(0), H = q.size(1), Sq = q.size(2), D = q.size(3);
     const bsm_score_mod mod =
         score_mod(number(a[8]), tensor_or_none(a[9], "alibi_slopes"), H, dev);
     OnDevice on(dev, a[13]);
     at::Tensor out = tensor_or_none(a[10], "out");
+    check_like(out, q, "out");
     if (!out.defined()) out = empty_on({B, H, Sq, D}, at::kBFloat16, dev);
     const bool want_lse = truth(a[12]);
     at::Tensor lse = want_lse ? tensor_or_none(a[11], "lse") : at::Tensor();
+    check_lse(lse, q);
     if (want_lse && !lse.defined())
       lse = empty_on({B, H, Sq}, at::kFloat, dev);
     const bsm_tensor ov = view(out);
@@ -301,12 +360,18 @@ PyObject* py_splash_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      &v = tensor(a[2], "v"), &dout = tensor(a[5], "dout");
     const at::Tensor out = tensor_or_none(a[3], "out");
     const at::Tensor lse = tensor_or_none(a[4], "lse");
+    check_operands(q, k, v);
+    check_like(out, q, "out");
+    check_like(dout, q, "dout");
+    check_lse(lse, q);
     const bsm_tensor qv = view(q), kv = view(k), vv = view(v), dv = view(dout);
     bsm_tensor ov = {};
     if (out.defined()) ov = view(out);
     const at::Tensor qs = tensor_or_none(a[7], "q_segment_ids");
     const at::Tensor ks = tensor_or_none(a[8], "kv_segment_ids");
     const at::Device dev = q.device();
+    check_ids(qs, q.size(0), q.size(2), dev, "q_segment_ids");
+    check_ids(ks, k.size(0), k.size(2), dev, "kv_segment_ids");
     const int32_t score = int32(a[10]);
     const int32_t B = static_cast<int32_t>(q.size(0));
     const int32_t H = static_cast<int32_t>(q.size(1));
@@ -403,6 +468,7 @@ PyObject* py_kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check_table(dev, table, B, lens, n_new);
     const bsm_tensor kt = token_view(k_new, B, c.H_kv, T, c.D, dev, "k_new");
     const bsm_tensor vt = token_view(v_new, B, c.H_kv, T, c.D, dev, "v_new");
+    if (!dev.is_cuda()) value_error("the cache must be on a CUDA device");
     OnDevice on(dev, a[9]);
     check_status(f_kv_append(&c, data<const int32_t>(table), table.stride(0),
                              static_cast<int32_t>(table.size(1)),
@@ -444,6 +510,7 @@ PyObject* py_paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
           "cache");
     const bsm_score_mod mod = score_mod(
         number(a[9]), tensor_or_none(a[10], "alibi_slopes"), H, dev);
+    if (!dev.is_cuda()) value_error("the cache must be on a CUDA device");
     const float scale = static_cast<float>(
         a[7] == Py_None ? 1.0 / std::sqrt(static_cast<double>(c.D))
                         : number(a[7]));

@@ -219,8 +219,10 @@ bsm_status bsm_splash_fwd(const void* q, const void* k, const void* v,
  *   alibi_slopes  device f32 [H], contiguous, finite, of any sign, or NULL;
  *                 read by the kernels (not checked).  Constants: the backward
  *                 gives them no gradient
- * tanh is computed as 1 - 2 / (1 + e^(2 x / softcap)) in f32, and the bias is
- * added in f32: a logit carries about 2^-24 of softcap and of the bias. */
+ * Scores and bias are f32: a logit is off by at most about 6e-7 of its value
+ * (|x| <= softcap / 2, where tanh is a polynomial) or 2^-22 of softcap (beyond,
+ * and everywhere for softcap above 2^18 scale, where it is 1 - 2 / (1 + e^(2 x
+ * / softcap))), and by 2^-23 of the bias. */
 typedef struct bsm_score_mod {
   float softcap;
   const float* alibi_slopes;
@@ -449,8 +451,8 @@ typedef struct bsm_kv_cache {
  *   lens, n_new device int32 [B]; n_new NULL = T new tokens each
  *   k_new, v_new  device bf16 [B][H_kv][T][D] (head_dim contiguous, strides
  *               multiples of 8, 16-byte aligned)
- * A page that gets tokens must belong to one sequence only (copy a shared
- * last page first).  On the device, lens[b] < 0, n_new[b] outside [0, T],
+ * A page that gets tokens must belong to one sequence only, and stand in its
+ * row once (copy a shared last page first).  On the device, lens[b] < 0, n_new[b] outside [0, T],
  * more tokens than max_pages pages hold, or a page outside [0, num_pages)
  * leave that sequence (or page) unwritten and are reported by
  * bsm_device_status as BSM_ERR_INVALID_ARG.  One launch on `stream`. */

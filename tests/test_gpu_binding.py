@@ -118,7 +118,7 @@ def test_errors_are_the_same(both):
         lambda: bsm.splash_attention(q, q, q, alibi_slopes=torch.zeros(2)),
         lambda: bsm.splash_attention(q, q, q, softcap=3.0,
                                      score=bsm.SCORE_POINTWISE),
-        lambda: bsm.splash_attention(q[..., :32], q, q),
+        lambda: bsm.splash_attention(*[q[..., :32]] * 3),
         lambda: bsm.splash_attention(*[wide[..., ::2]] * 3, mask_info=info),
         lambda: bsm.splash_attention_bwd(q, q, q, q, None, q),
     ]

@@ -219,6 +219,20 @@ def test_attention_long(softcap, biased):
     check(out, lse, want)
 
 
+@pytest.mark.parametrize("cap", [0.3, 250.0, 5e4])
+def test_attention_caps(cap):
+    # scores far beyond the cap, and caps that hardly bend them
+    out, lse, want = _attend([300, 77], 16, 64, 2, 3, 2, 79, softcap=cap,
+                             q_sigma=9.0)
+    check(out, lse, want)
+
+
+def test_attention_widest_window():
+    out, lse, want = _attend([100, 3], 16, 64, 1, 2, 3, 80,
+                             window=2 ** 31 - 1)
+    check(out, lse, want)
+
+
 def test_attention_many_sequences():
     g = torch.Generator().manual_seed(3)
     lens = torch.randint(0, 400, (200,), generator=g).tolist()

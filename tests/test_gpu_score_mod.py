@@ -153,7 +153,7 @@ def test_long_rows(mod):
         slopes=slopes_of(2, mod[2]) if mod[2] else None)
 
 
-@pytest.mark.parametrize("cap", [0.5, 5.0, 1000.0])
+@pytest.mark.parametrize("cap", [0.5, 5.0, 70.0, 1000.0, 2e4])
 def test_saturated_and_loose_caps(cap):
     # scores far beyond the cap (most rows at +-cap, where dS vanishes) and
     # a cap that hardly bends them
@@ -238,6 +238,30 @@ def test_no_modification_is_the_unmodified_call():
     ga = bsm.splash_attention_bwd(q, k, v, *a, do)
     gb = bsm.splash_attention_bwd(q, k, v, *a, do, softcap=0.0)
     assert all(torch.equal(x, y) for x, y in zip(ga, gb))
+
+
+def test_operands_are_checked():
+    q = torch.zeros(1, 2, 64, 64, dtype=torch.bfloat16).cuda()
+    info = bsm.build_mask_info(C, 1, 64, 64)
+    lse = torch.zeros(1, 2, 64).cuda()
+    seg = torch.zeros(1, 64, dtype=torch.int32).cuda()
+    for bad in ((q.half(), q, q), (q, q.cpu(), q), (q, q, q.float()),
+                (q, q, q[:, :, :32]), (q, q[..., :32], q[..., :32])):
+        with pytest.raises(ValueError):
+            bsm.splash_attention(*bad, mask_info=info, softcap=5.0)
+        with pytest.raises(ValueError):
+            bsm.splash_attention_bwd(*bad, q, lse, q, mask_info=info,
+                                     softcap=5.0)
+    for kw in (dict(out=q.float()), dict(out=q[:, :1]), dict(lse=lse.double()),
+               dict(lse=lse[:, :, ::2])):
+        with pytest.raises(ValueError):
+            bsm.splash_attention(q, q, q, mask_info=info, **kw)
+    for ids in (seg.long(), seg.cpu(), seg[:, :32]):
+        with pytest.raises((ValueError, bsm.BsmError)):
+            bsm.splash_attention(q, q, q, q_segment_ids=ids,
+                                 kv_segment_ids=ids, mask_info=info)
+    with pytest.raises(ValueError):
+        bsm.splash_attention_bwd(q, q, q, q, lse, q.cpu(), mask_info=info)
 
 
 def test_strided_and_host_tensors():
