@@ -356,37 +356,53 @@ def bsm_splash_bwd(q, k, v, out, lse, dout, mask_info: MaskInfo,
         sh))
 
 
+def _check_cache(k_pages, v_pages, k_scale, v_scale) -> None:
+    shape, dev = k_pages.shape, k_pages.device
+    for t in (k_pages, v_pages):
+        if (t.dtype != torch.float8_e4m3fn or t.dim() != 4
+                or t.shape != shape or not t.is_contiguous()
+                or t.device != dev):
+            raise ValueError("k_pages and v_pages must be contiguous "
+                             "float8_e4m3fn tensors of one shape "
+                             "[num_pages, H_kv, page_size, D] on one device")
+    for t in (k_scale, v_scale):
+        if (t.dtype != torch.float32 or t.shape != shape[:2]
+                or not t.is_contiguous() or t.device != dev):
+            raise ValueError("k_scale and v_scale must be contiguous float32 "
+                             "tensors [num_pages, H_kv] beside the pages")
+
+
 class KVCache:
     """A paged 8-bit key/value cache over four CUDA tensors, which it keeps:
     k_pages, v_pages [num_pages, H_kv, page_size, D] (float8_e4m3fn) and
     k_scale, v_scale [num_pages, H_kv] (float32), all contiguous.  An element
     is its code times the scale of its page and head."""
 
-    __slots__ = ("k_pages", "v_pages", "k_scale", "v_scale", "device",
-                 "struct")
+    __slots__ = ("k_pages", "v_pages", "k_scale", "v_scale", "_struct")
 
     def __init__(self, k_pages, v_pages, k_scale, v_scale):
-        shape, dev = k_pages.shape, k_pages.device
-        for t in (k_pages, v_pages):
-            if (t.dtype != torch.float8_e4m3fn or t.dim() != 4
-                    or t.shape != shape or not t.is_contiguous()
-                    or t.device != dev):
-                raise ValueError("k_pages and v_pages must be contiguous "
-                                 "float8_e4m3fn tensors of one shape "
-                                 "[num_pages, H_kv, page_size, D] on one "
-                                 "device")
-        for t in (k_scale, v_scale):
-            if (t.dtype != torch.float32 or t.shape != shape[:2]
-                    or not t.is_contiguous() or t.device != dev):
-                raise ValueError("k_scale and v_scale must be contiguous "
-                                 "float32 tensors [num_pages, H_kv] beside "
-                                 "the pages")
+        fast = _fast()
+        if fast:
+            fast.check_cache(k_pages, v_pages, k_scale, v_scale)
+        else:
+            _check_cache(k_pages, v_pages, k_scale, v_scale)
         self.k_pages, self.v_pages = k_pages, v_pages
         self.k_scale, self.v_scale = k_scale, v_scale
-        self.device = dev
-        self.struct = KVCacheStruct(k_pages.data_ptr(), v_pages.data_ptr(),
-                                    k_scale.data_ptr(), v_scale.data_ptr(),
-                                    *shape)
+        self._struct = None
+
+    @property
+    def device(self) -> torch.device:
+        return self.k_pages.device
+
+    @property
+    def struct(self) -> KVCacheStruct:
+        """bsm_kv_cache, for the C ABI."""
+        if self._struct is None:
+            self._struct = KVCacheStruct(
+                self.k_pages.data_ptr(), self.v_pages.data_ptr(),
+                self.k_scale.data_ptr(), self.v_scale.data_ptr(),
+                *self.k_pages.shape)
+        return self._struct
 
     @classmethod
     def empty(cls, num_pages: int, H_kv: int, page_size: int, D: int,

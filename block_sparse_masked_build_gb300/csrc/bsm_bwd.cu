@@ -147,7 +147,7 @@ __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int c0) {
 // Causal/local/band and the sequence ends are a range of columns; segment
 // ids and arbitrary-mask words of the 32 columns are loaded one per lane
 // and passed around with shuffles.  Whole warp.
-template <bool DKDV>
+template <bool DKDV, bool QUICK = false>
 __device__ __forceinline__ uint32_t chunk_visible(const BwdParams& p, int b,
                                                   int row, int row_seg,
                                                   int c0) {
@@ -178,9 +178,15 @@ __device__ __forceinline__ uint32_t chunk_visible(const BwdParams& p, int b,
       cs = DKDV ? p.q_seg[static_cast<int64_t>(b) * p.Sq + col]
                 : p.kv_seg[static_cast<int64_t>(b) * p.Skv + col];
     uint32_t same = 0;
+    if (QUICK && __all_sync(0xffffffffu,
+                            cs == __shfl_sync(0xffffffffu, cs, 0))) {
+      // one segment: most chunks of packed sequences
+      same = cs == row_seg ? 0xffffffffu : 0u;
+    } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      same |= (__shfl_sync(0xffffffffu, cs, j) == row_seg ? 1u : 0u) << j;
+      for (int j = 0; j < 32; ++j)
+        same |= (__shfl_sync(0xffffffffu, cs, j) == row_seg ? 1u : 0u) << j;
+    }
     bits &= same;
   }
   if (p.dense != nullptr) {
@@ -867,6 +873,10 @@ __device__ __forceinline__ void bwd_elem_mod_role(
       __syncwarp();
       if (it + 1 < n_iter) load_stats(it + 1, lse2_n, delta_n, slope_n);
     }
+    // (before the wait for S, whose time then covers the ids' loads: packed
+    // S=4096, 32/8 heads, cap 50: FIGURE us after it and id by id, FIGURE so)
+    uint32_t vis = 0xffffffffu;
+    if (cls == 1) vis = chunk_visible<DKDV, true>(p, b, row, row_seg, col0);
     ok = bwarp_wait(&bars->s_full, it & 1, abort_flag, p.timeout_ns);
     if (!ok) {
       record_bwd_timeout(kRoleBElem, 0);
@@ -875,8 +885,6 @@ __device__ __forceinline__ void bwd_elem_mod_role(
     tc_fence_after();
     uint32_t sraw[32];
     tmem_ld32(t_s + part * 32, sraw);
-    uint32_t vis = 0xffffffffu;
-    if (cls == 1) vis = chunk_visible<DKDV>(p, b, row, row_seg, col0);
     tmem_ld_wait();
     tc_fence_before();
     if (!DKDV) mbar_arrive(&bars->p_ready);  // S read: the next S may go in

@@ -406,6 +406,31 @@ PyObject* py_splash_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// check_cache(k_pages, v_pages, k_scale, v_scale)
+PyObject* py_check_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    expect(n, 4);
+    const at::Tensor &k = tensor(a[0], "k_pages"), &v = tensor(a[1], "v_pages"),
+                     &ks = tensor(a[2], "k_scale"),
+                     &vs = tensor(a[3], "v_scale");
+    for (const at::Tensor* t : {&k, &v})
+      if (t->scalar_type() != at::kFloat8_e4m3fn || t->dim() != 4 ||
+          t->sizes() != k.sizes() || !t->is_contiguous() ||
+          t->device() != k.device())
+        value_error(
+            "k_pages and v_pages must be contiguous float8_e4m3fn tensors of "
+            "one shape [num_pages, H_kv, page_size, D] on one device");
+    for (const at::Tensor* t : {&ks, &vs})
+      if (t->scalar_type() != at::kFloat || t->dim() != 2 ||
+          t->size(0) != k.size(0) || t->size(1) != k.size(1) ||
+          !t->is_contiguous() || t->device() != k.device())
+        value_error(
+            "k_scale and v_scale must be contiguous float32 tensors "
+            "[num_pages, H_kv] beside the pages");
+    Py_RETURN_NONE;
+  });
+}
+
 // The cache's four tensors, which KVCache has checked.
 bsm_kv_cache cache_of(PyObject* const* a) {
   const at::Tensor& k = tensor(a[0], "k_pages");
@@ -573,6 +598,7 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {FAST(bind),       FAST(build_mask_info),
                          FAST(splash_fwd), FAST(splash_bwd),
                          FAST(kv_append),  FAST(paged_attention),
+                         FAST(check_cache),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bsm_torch", nullptr, -1,
