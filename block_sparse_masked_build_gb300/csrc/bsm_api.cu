@@ -613,9 +613,16 @@ bsm_status bsm_splash_fwd_mod(const void* q, const void* k, const void* v,
       }
     }
   }
-  cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(int32_t),
-                                  static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "workspace reset");
+  cudaError_t e;
+  if (sm_mod.kind != 0 && p.dense == nullptr && units <= num_sms) {
+    // every unit has a CTA of its own: nothing to count (small calls are bound
+    // by latency, and the reset is a node of its own on the stream)
+    p.unit_counter = nullptr;
+  } else {
+    e = cudaMemsetAsync(workspace, 0, sizeof(int32_t),
+                        static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "workspace reset");
+  }
   e = bsm::launch_splash_fwd(p, tq, tk, tv, num_sms,
                              static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "splash_fwd launch");

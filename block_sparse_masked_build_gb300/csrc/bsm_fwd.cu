@@ -1264,8 +1264,12 @@ __device__ __forceinline__ bool dt_build_list(const FwdParams& p, DtBars* bars,
       return false;
     }
     int unit = 0;
-    if (lane == 0) unit = atomicAdd(p.unit_counter, 1);
-    unit = __shfl_sync(0xffffffffu, unit, 0);
+    if (p.unit_counter == nullptr) {  // a pair of units for each CTA
+      unit = ui == 0 ? static_cast<int>(blockIdx.x) * 2 + t : n_units;
+    } else {
+      if (lane == 0) unit = atomicAdd(p.unit_counter, 1);
+      unit = __shfl_sync(0xffffffffu, unit, 0);
+    }
     DtMeta& mt = bars->meta[t][buf];
     if (unit >= n_units) {
       if (lane == 0) {
@@ -1317,7 +1321,7 @@ __device__ __forceinline__ bool dt_build_list(const FwdParams& p, DtBars* bars,
 // 0, V in slot 1).  The next list is built once this unit's last loads are
 // issued, i.e. while the unit's last entries still run (building it after
 // the first entry's loads measured slower).
-template <bool TRACE>
+template <int D, bool TRACE>
 __device__ __forceinline__ void dt_load_role(const FwdParams& p,
                                              const CUtensorMap* tq,
                                              const CUtensorMap* tk,
@@ -1345,8 +1349,8 @@ __device__ __forceinline__ void dt_load_role(const FwdParams& p,
         break;
       }
       if (lane == 0) {
-        mbar_arrive_expect_tx(&bars->q_full[t], kDtTile);
-        for (int kb = 0; kb < 2; ++kb)
+        mbar_arrive_expect_tx(&bars->q_full[t], kTileM * D * 2);
+        for (int kb = 0; kb < D / 64; ++kb)
           tma_load_4d(tq, &bars->q_full[t],
                       smem + kDtOffQ + t * kDtTile + kb * kTileM * 128,
                       kb * 64, mt.qt * kTileM, mt.h, mt.b, pol_q);
@@ -1368,9 +1372,9 @@ __device__ __forceinline__ void dt_load_role(const FwdParams& p,
           break;
         }
         if (lane == 0) {
-          mbar_arrive_expect_tx(&bars->kv_full[t][which], kDtTile);
+          mbar_arrive_expect_tx(&bars->kv_full[t][which], kTileN * D * 2);
           uint8_t* dst = smem + kDtOffKV + (2 * t + which) * kDtTile;
-          for (int kb = 0; kb < 2; ++kb)
+          for (int kb = 0; kb < D / 64; ++kb)
             tma_load_4d(which == 0 ? tk : tv, &bars->kv_full[t][which],
                         dst + kb * kTileN * 128, kb * 64, jt * kTileN, hkv,
                         mt.b, pol_kv);
@@ -1405,14 +1409,14 @@ __device__ __forceinline__ void dt_load_role(const FwdParams& p,
 // commit goes out from the lane elect.sync picks (the same lane every
 // time: the warp is converged there); issued that way the pipeline's MMAs
 // measured ~5 % faster than from a branch lane 0 takes alone.
-template <int SCORE, bool TRACE>
+template <int D, int SCORE, bool TRACE>
 __device__ __forceinline__ void dt_mma_role(const FwdParams& p, uint8_t* smem,
                                             DtBars* bars, uint32_t tmem,
                                             const int t) {
   const bool leader = (threadIdx.x % 32) == 0;
   volatile int* abort_flag = &bars->abort;
   constexpr uint32_t idesc_s = idesc_bf16_f32(kTileM, kTileN, false);
-  constexpr uint32_t idesc_o = idesc_bf16_f32(kTileM, 128, true);
+  constexpr uint32_t idesc_o = idesc_bf16_f32(kTileM, D, true);
   const uint64_t dq =
       sdesc_sw128(smem_u32(smem + kDtOffQ + t * kDtTile), 16, 1024);
   const uint64_t dk =
@@ -1428,7 +1432,7 @@ __device__ __forceinline__ void dt_mma_role(const FwdParams& p, uint8_t* smem,
   };
   auto issue_s = [&]() {
 #pragma unroll
-    for (int k = 0; k < 128 / 16; ++k) {
+    for (int k = 0; k < D / 16; ++k) {
       const uint32_t off = (k >> 2) * (kTileM * 128 / 16) + (k & 3) * 2;
       mma_ss_elect(s_acc, dq + off, dk + off, idesc_s, k > 0 ? 1u : 0u);
     }
@@ -1523,11 +1527,10 @@ __device__ __forceinline__ void dt_mma_role(const FwdParams& p, uint8_t* smem,
   __syncwarp();
 }
 
-template <int SCORE, int MOD, bool KEEP, bool TRACE>
+template <int D, int SCORE, int MOD, bool KEEP, bool TRACE>
 __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
                                               const uint16_t* lists,
                                               uint32_t tmem, const int t) {
-  constexpr int D = 128;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int quarter = warp % 4;  // TMEM lane quarter this warp may access
   const int r = quarter * 32 + lane;
@@ -1816,13 +1819,13 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
 // 155 and 186; causal S=8192, 32/8 heads, cap 20: 571 and 690.  With a bias,
 // whose running maximum the two threads would have to exchange on every entry,
 // it was 1 to 7 % slower instead.
-template <bool KEEP, bool TRACE>
+template <int D, bool KEEP, bool TRACE>
 __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
                                                   DtBars* bars, DtPair* pair,
                                                   const uint16_t* lists,
                                                   uint32_t tmem, const int t,
                                                   const int hf) {
-  constexpr int D = 128, NC = kTileN / 2;
+  constexpr int NC = kTileN / 2;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int quarter = warp % 4;  // TMEM lane quarter this warp may access
   const int r = quarter * 32 + lane;
@@ -2007,7 +2010,7 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
   }
 }
 
-template <int SCORE, int MOD, bool TRACE>
+template <int D, int SCORE, int MOD, bool TRACE>
 __global__ void __launch_bounds__(dt_threads(MOD), 1)
     splash_fwd_dt_kernel(const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k,
@@ -2066,9 +2069,9 @@ __global__ void __launch_bounds__(dt_threads(MOD), 1)
     const int t = warp & 1;
     uint16_t* lt = lists + t * kListBufs * kMaxKvTiles;
     if (warp < 2)
-      dt_load_role<TRACE>(p, &tm_q, &tm_k, &tm_v, smem, bars, lt, t);
+      dt_load_role<D, TRACE>(p, &tm_q, &tm_k, &tm_v, smem, bars, lt, t);
     else
-      dt_mma_role<SCORE, TRACE>(p, smem, bars, tmem, t);
+      dt_mma_role<D, SCORE, TRACE>(p, smem, bars, tmem, t);
   } else {
     // per-element keep bits only when segment ids are unsorted or an
     // arbitrary mask is given (read once; the same for every thread)
@@ -2078,18 +2081,18 @@ __global__ void __launch_bounds__(dt_threads(MOD), 1)
       const uint16_t* lt = lists + t * kListBufs * kMaxKvTiles;
       if (((p.flags & BSM_MASK_SEGMENT) && (*p.seg_flags & 1) != 0) ||
           p.dense != nullptr)
-        dt_score_role<SCORE, MOD, true, TRACE>(p, bars, lt, tmem, t);
+        dt_score_role<D, SCORE, MOD, true, TRACE>(p, bars, lt, tmem, t);
       else
-        dt_score_role<SCORE, MOD, false, TRACE>(p, bars, lt, tmem, t);
+        dt_score_role<D, SCORE, MOD, false, TRACE>(p, bars, lt, tmem, t);
     } else {
       const int t = (warp - 4) / 8, hf = (warp - 4) / 4 & 1;
       const uint16_t* lt = lists + t * kListBufs * kMaxKvTiles;
       DtPair* pair = reinterpret_cast<DtPair*>(smem + kDtOffPair);
       // (an arbitrary mask with modified scores takes the lockstep kernel)
       if ((p.flags & BSM_MASK_SEGMENT) && (*p.seg_flags & 1) != 0)
-        dt_score_cap_role<true, TRACE>(p, bars, pair, lt, tmem, t, hf);
+        dt_score_cap_role<D, true, TRACE>(p, bars, pair, lt, tmem, t, hf);
       else
-        dt_score_cap_role<false, TRACE>(p, bars, pair, lt, tmem, t, hf);
+        dt_score_cap_role<D, false, TRACE>(p, bars, pair, lt, tmem, t, hf);
     }
   }
 
@@ -2106,13 +2109,13 @@ __global__ void __launch_bounds__(dt_threads(MOD), 1)
   }
 }
 
-template <int SCORE, int MOD>
+template <int D, int SCORE, int MOD>
 cudaError_t launch_dt(const FwdParams& p, const CUtensorMap& tq,
                       const CUtensorMap& tk, const CUtensorMap& tv, int grid,
                       cudaStream_t stream) {
   // the instance that records the event trace is launched only with one
-  auto kern = p.trace != nullptr ? splash_fwd_dt_kernel<SCORE, MOD, true>
-                                 : splash_fwd_dt_kernel<SCORE, MOD, false>;
+  auto kern = p.trace != nullptr ? splash_fwd_dt_kernel<D, SCORE, MOD, true>
+                                 : splash_fwd_dt_kernel<D, SCORE, MOD, false>;
   cudaFuncAttributes attr;
   cudaError_t e = cudaFuncGetAttributes(&attr, kern);
   if (e != cudaSuccess) return e;
@@ -2170,7 +2173,11 @@ cudaError_t launch_score(const FwdParams& p, const CUtensorMap& tq,
   const bool dt = p.dense == nullptr && p.D == 128 &&
                   (MOD != 0 || (p.flags & BSM_MASK_SEGMENT) != 0 ||
                    p.Skv < 4096);
-  if (dt) return launch_dt<SCORE, MOD>(p, tq, tk, tv, grid, stream);
+  if (dt) return launch_dt<128, SCORE, MOD>(p, tq, tk, tv, grid, stream);
+  if constexpr (MOD != 0) {  // and at head dim 64 too
+    if (p.dense == nullptr && p.D == 64)
+      return launch_dt<64, SCORE, MOD>(p, tq, tk, tv, grid, stream);
+  }
   if constexpr (MOD == 0) {
     if (p.D == 128 && pp)
       return launch_one<128, SCORE, MOD, true>(p, tq, tk, tv, grid, stream);
