@@ -97,6 +97,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // ------------------------------------------------------------------ append
 
 constexpr int kAppendThreads = 128;
@@ -145,7 +151,7 @@ __global__ void __launch_bounds__(kAppendThreads, NCH <= 8 ? 8 : 4)
                 ss = is_v ? p.v_ss : p.k_ss;
   src += b * sb + h * sh;
   uint4 x[NCH];
-  uint32_t top = 0;  // two running maxima of |bits|, finite elements only
+  uint32_t top = 0;  // two running maxima, one per half word
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int c = threadIdx.x + i * kAppendThreads;
@@ -163,27 +169,40 @@ __global__ void __launch_bounds__(kAppendThreads, NCH <= 8 ? 8 : 4)
   uint8_t* dst = (is_v ? p.v : p.k) + block * p.page_size * p.D;
   float* scale_at = (is_v ? p.v_scale : p.k_scale) + block;
   const float was = lo > 0 ? *scale_at : 0.f;
+  // the largest |bits| (bf16 magnitudes compare as integers)
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t a = w[j] & 0x7fff7fffu;
-      // bf16 infinities and NaN have magnitudes from 0x7f80 up
-      const uint32_t fin = __vcmpltu2(a, 0x7f807f80u);
-      top = __vmaxu2(top, a & fin);
-    }
+    for (int j = 0; j < 4; ++j) top = max_u16x2(top, w[j] & 0x7fff7fffu);
   }
-  top = max(top & 0xffffu, top >> 16);
-  top = __reduce_max_sync(0xffffffffu, top);
-  __shared__ uint32_t warp_top[kAppendThreads / 32];
-  if (threadIdx.x % 32 == 0) warp_top[threadIdx.x / 32] = top;
-  __syncthreads();  // also: every thread has read the old scale
+  __shared__ uint32_t warp_top[2][kAppendThreads / 32];
+  auto block_max = [&](int which) {
+    top = max(top & 0xffffu, top >> 16);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (threadIdx.x % 32 == 0) warp_top[which][threadIdx.x / 32] = top;
+    __syncthreads();  // (the first: every thread has read the old scale)
 #pragma unroll
-  for (int w = 0; w < kAppendThreads / 32; ++w) top = max(top, warp_top[w]);
+    for (int w = 0; w < kAppendThreads / 32; ++w)
+      top = max(top, warp_top[which][w]);
+  };
+  block_max(0);
+  if (top >= 0x7f80u) {  // an infinity or NaN: once more over the finite ones
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a = w[j] & 0x7fff7fffu;
+        top = max_u16x2(top, a & __vcmpltu2(a, 0x7f807f80u));
+      }
+    }
+    block_max(1);
+  }
   const float want = block_scale(__uint_as_float(top << 16));
   const float scale = lo > 0 ? fmaxf(was, want) : want;
-  const float inv = 1.f / scale;  // exact: a power of two from this kernel
+  const float inv = __frcp_rn(scale);  // exact: a power of two from this kernel
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int c = threadIdx.x + i * kAppendThreads;
@@ -568,7 +587,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) top = __vmaxu2(top, w[s][i] & 0x7fff7fffu);
+      for (int i = 0; i < 2; ++i) top = max_u16x2(top, w[s][i] & 0x7fff7fffu);
     top = max(top & 0xffffu, top >> 16);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
