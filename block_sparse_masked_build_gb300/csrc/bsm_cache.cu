@@ -713,6 +713,39 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
       }
     }
 
+    // ---- the cap: tanh(y) = 1 - 2 / (1 + 2^x), x = 2 y log2(e), off by 2^-23
+    // of the cap; above a cap of about 200 that would show in the logits, and
+    // small y take the forward's polynomial instead
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        s[nt][i] = (s[nt][i] + s1[nt][i]) * (q_mul[nt][i & 1] * k_scale);
+    if (p.mod.kind & kModCap) {
+      if (p.mod.cap_log2 > 300.f) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = s[nt][i], y = x * 0.34657359f, y2 = y * y;
+            const float z = fmaf(-2.f, rcp_approx(ex2_approx(x) + 1.f), 1.f);
+            const float t = fmaf(y2, fmaf(y2, fmaf(y2, -0.04439273843f,
+                                                   0.1318993943f),
+                                          -0.3332628423f),
+                                 0.999999451f);
+            s[nt][i] = p.mod.cap_log2 * (y2 <= 0.25f ? y * t : z);
+          }
+      } else {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            s[nt][i] = fmaf(-2.f * p.mod.cap_log2,
+                            rcp_approx(ex2_approx(s[nt][i]) + 1.f),
+                            p.mod.cap_log2);
+      }
+    }
+
     // ---- logits in log2 units, mask, running maximum
     const bool inner = tok + kPaGroup - 1 <= pos_min &&
                        (p.window <= 0 || pos_max - tok < p.window);
@@ -722,22 +755,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int c = i & 1, j = tok + g + (i >> 1) * 8;
-        float x = (s[nt][i] + s1[nt][i]) * (q_mul[nt][c] * k_scale);
-        if (p.mod.kind & kModCap) {
-          // tanh(y) = 1 - 2 / (1 + 2^x), x = 2 y log2(e): off by 2^-23 of the
-          // cap.  Above a cap of about 200 that would show in the logits, and
-          // small y take the polynomial of the forward instead
-          const float z = fmaf(-2.f * p.mod.cap_log2,
-                               rcp_approx(ex2_approx(x) + 1.f), p.mod.cap_log2);
-          const float y = x * 0.34657359f, y2 = y * y;
-          x = p.mod.cap_log2 > 300.f && y2 <= 0.25f
-                  ? p.mod.cap_log2 * y *
-                        fmaf(y2, fmaf(y2, fmaf(y2, -0.04439273843f,
-                                               0.1318993943f),
-                                      -0.3332628423f),
-                             0.999999451f)
-                  : z;
-        }
+        float x = s[nt][i];
         if (p.mod.kind & kModBias)
           x = fmaf(slope2[nt][c], d[nt][c] + (i >> 1) * 8.f, x);
         if (!inner &&

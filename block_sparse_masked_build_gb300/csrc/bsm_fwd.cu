@@ -1264,8 +1264,13 @@ __device__ __forceinline__ bool dt_build_list(const FwdParams& p, DtBars* bars,
       return false;
     }
     int unit = 0;
-    if (p.unit_counter == nullptr) {  // a pair of units for each CTA
-      unit = ui == 0 ? static_cast<int>(blockIdx.x) * 2 + t : n_units;
+    if (p.unit_counter == nullptr) {
+      // nothing to count: one unit for each pipeline, or, where there are
+      // SMs enough, for each CTA (its other pipeline stays idle)
+      const bool alone = gridDim.x > static_cast<unsigned>(p.num_units);
+      unit = ui > 0 || (alone && t > 0) ? n_units
+             : alone ? static_cast<int>(blockIdx.x)
+                     : static_cast<int>(blockIdx.x) * 2 + t;
     } else {
       if (lane == 0) unit = atomicAdd(p.unit_counter, 1);
       unit = __shfl_sync(0xffffffffu, unit, 0);
@@ -2112,7 +2117,11 @@ __global__ void __launch_bounds__(dt_threads(MOD), 1)
 template <int D, int SCORE, int MOD>
 cudaError_t launch_dt(const FwdParams& p, const CUtensorMap& tq,
                       const CUtensorMap& tk, const CUtensorMap& tv, int grid,
-                      cudaStream_t stream) {
+                      int num_sms, cudaStream_t stream) {
+  // (S=1280, 12/4 heads, no mask, cap 50: FIGURE us with two tiles per CTA,
+  // FIGURE with one)
+  if (p.unit_counter == nullptr && 2 * p.num_units <= num_sms)
+    grid = 2 * p.num_units;
   // the instance that records the event trace is launched only with one
   auto kern = p.trace != nullptr ? splash_fwd_dt_kernel<D, SCORE, MOD, true>
                                  : splash_fwd_dt_kernel<D, SCORE, MOD, false>;
@@ -2153,7 +2162,7 @@ cudaError_t launch_one(const FwdParams& p, const CUtensorMap& tq,
 template <int SCORE, int MOD>
 cudaError_t launch_score(const FwdParams& p, const CUtensorMap& tq,
                          const CUtensorMap& tk, const CUtensorMap& tv,
-                         int grid, cudaStream_t stream) {
+                         int grid, int num_sms, cudaStream_t stream) {
   // Softmax turns alternate between the tiles only where work units are
   // long: no segment ids and at least 4096 keys.  Packed sequences and
   // short sequences give short units, where the alternation costs more
@@ -2173,10 +2182,10 @@ cudaError_t launch_score(const FwdParams& p, const CUtensorMap& tq,
   const bool dt = p.dense == nullptr && p.D == 128 &&
                   (MOD != 0 || (p.flags & BSM_MASK_SEGMENT) != 0 ||
                    p.Skv < 4096);
-  if (dt) return launch_dt<128, SCORE, MOD>(p, tq, tk, tv, grid, stream);
+  if (dt) return launch_dt<128, SCORE, MOD>(p, tq, tk, tv, grid, num_sms, stream);
   if constexpr (MOD != 0) {  // and at head dim 64 too
     if (p.dense == nullptr && p.D == 64)
-      return launch_dt<64, SCORE, MOD>(p, tq, tk, tv, grid, stream);
+      return launch_dt<64, SCORE, MOD>(p, tq, tk, tv, grid, num_sms, stream);
   }
   if constexpr (MOD == 0) {
     if (p.D == 128 && pp)
@@ -2216,7 +2225,7 @@ cudaError_t launch_splash_fwd(const FwdParams& p, const CUtensorMap& tq,
                               int num_sms, cudaStream_t stream) {
   const int grid = fwd_grid_size(p, num_sms);
   if (p.score == BSM_SCORE_POINTWISE)
-    return launch_score<BSM_SCORE_POINTWISE, 0>(p, tq, tk, tv, grid, stream);
+    return launch_score<BSM_SCORE_POINTWISE, 0>(p, tq, tk, tv, grid, num_sms, stream);
   // a cap too large for a fixed reference (see score_role) takes the instance
   // with a running maximum, with slopes of zero
   const int kind = p.mod.kind == kModCap && p.mod.cap_log2 > 87.f
@@ -2224,16 +2233,14 @@ cudaError_t launch_splash_fwd(const FwdParams& p, const CUtensorMap& tq,
                        : p.mod.kind;
   switch (kind) {
     case 0:
-      return launch_score<BSM_SCORE_SOFTMAX, 0>(p, tq, tk, tv, grid, stream);
+      return launch_score<BSM_SCORE_SOFTMAX, 0>(p, tq, tk, tv, grid, num_sms, stream);
     case kModCap:
-      return launch_score<BSM_SCORE_SOFTMAX, kModCap>(p, tq, tk, tv, grid,
-                                                      stream);
+      return launch_score<BSM_SCORE_SOFTMAX, kModCap>(p, tq, tk, tv, grid, num_sms, stream);
     case kModBias:
-      return launch_score<BSM_SCORE_SOFTMAX, kModBias>(p, tq, tk, tv, grid,
-                                                       stream);
+      return launch_score<BSM_SCORE_SOFTMAX, kModBias>(p, tq, tk, tv, grid, num_sms, stream);
     case kModCap | kModBias:
       return launch_score<BSM_SCORE_SOFTMAX, kModCap | kModBias>(
-          p, tq, tk, tv, grid, stream);
+          p, tq, tk, tv, grid, num_sms, stream);
   }
   return cudaErrorInvalidValue;
 }
