@@ -1201,6 +1201,7 @@ struct DtBars {
   // two threads per row: the two score warps of a pipeline and lane quarter,
   // on every entry and at a unit's end
   uint64_t meet[2][4], meet_sum[2][4];
+  uint64_t merge;  // pipelines sharing a tile: pipeline 1's part is there
   uint32_t tmem_base;
   int abort;
   uint32_t trace_n[6];
@@ -1212,9 +1213,15 @@ static_assert(sizeof(DtBars) <= 1024, "barrier block");
 // alternate between two places: a thread writes the next unit's while its
 // partner may still read this one's, but the one after that only once the
 // partner has arrived with the next.
+// Pipelines sharing a tile: pipeline 1's reference and sum of each row.
 struct DtPair {
   float sum[2][2][2][kTileM];
+  float ref[kTileM], total[kTileM];
 };
+// Pipelines sharing a tile: pipeline 1 leaves its O, [D][128] f32, in its own
+// K and V slots, which nothing reads or writes any more.
+constexpr int kDtOffMerge = kDtOffKV + 2 * kDtTile;
+static_assert(kTileM * 128 * 4 <= 2 * kDtTile, "merge area");
 constexpr int kDtOffPair = kDtOffBar + 1024;
 static_assert(kDtSmemBytes + sizeof(DtPair) <= 232448, "shared memory budget");
 
@@ -1245,11 +1252,17 @@ __device__ __forceinline__ void dt_trace(const FwdParams& p, DtBars* bars,
   }
 }
 
+// SHARED (modified scores, at most half as many query tiles as SMs): the two
+// pipelines of a CTA share its tile, each takes every other KV tile and
+// pipeline 0 joins the two results.  (us, one tile per pipeline, one per CTA
+// with an idle pipeline, and shared: S=1280, 12/4 heads, no mask, cap 50: 35.7,
+// 26.4, 24.7; causal S=2048, 4/2 heads, D=64, cap 50: 43.8, 32.3, 26.8.)
+
 // Takes pipeline t's next unit from the counter and writes its KV-tile
 // list (uint16: tile << 2 | class) into buffer ui % kListBufs (whole warp);
 // unit -1 when none is left.  Units are numbered two per 256-row unit of
 // the lockstep kernel's order (its two query tiles), longest first.
-template <bool TRACE>
+template <bool TRACE, bool SHARED>
 __device__ __forceinline__ bool dt_build_list(const FwdParams& p, DtBars* bars,
                                               uint16_t* lists, const int t,
                                               const int ui) {
@@ -1264,13 +1277,10 @@ __device__ __forceinline__ bool dt_build_list(const FwdParams& p, DtBars* bars,
       return false;
     }
     int unit = 0;
-    if (p.unit_counter == nullptr) {
-      // nothing to count: one unit for each pipeline, or, where there are
-      // SMs enough, for each CTA (its other pipeline stays idle)
-      const bool alone = gridDim.x > static_cast<unsigned>(p.num_units);
-      unit = ui > 0 || (alone && t > 0) ? n_units
-             : alone ? static_cast<int>(blockIdx.x)
-                     : static_cast<int>(blockIdx.x) * 2 + t;
+    if (p.unit_counter == nullptr) {  // nothing to count
+      unit = ui > 0 ? n_units
+             : SHARED ? static_cast<int>(blockIdx.x)
+                      : static_cast<int>(blockIdx.x) * 2 + t;
     } else {
       if (lane == 0) unit = atomicAdd(p.unit_counter, 1);
       unit = __shfl_sync(0xffffffffu, unit, 0);
@@ -1301,11 +1311,14 @@ __device__ __forceinline__ bool dt_build_list(const FwdParams& p, DtBars* bars,
       for (int h = 0; h < 2; ++h) {
         const int jt = base + 32 * h + lane;
         const unsigned m = __ballot_sync(0xffffffffu, c[h] != 0);
-        if (c[h]) list[n + __popc(m & ((1u << lane) - 1u))] =
-            static_cast<uint16_t>((jt << 2) | c[h]);
+        const int at = n + __popc(m & ((1u << lane) - 1u));
+        if (c[h] && (!SHARED || (at & 1) == t))
+          list[SHARED ? at >> 1 : at] =
+              static_cast<uint16_t>((jt << 2) | c[h]);
         n += __popc(m);
       }
     }
+    if (SHARED) n = (n + 1 - t) >> 1;  // every other entry
     __syncwarp();
     if (lane == 0) {
       mt.n = n;
@@ -1326,7 +1339,7 @@ __device__ __forceinline__ bool dt_build_list(const FwdParams& p, DtBars* bars,
 // 0, V in slot 1).  The next list is built once this unit's last loads are
 // issued, i.e. while the unit's last entries still run (building it after
 // the first entry's loads measured slower).
-template <int D, bool TRACE>
+template <int D, bool TRACE, bool SHARED>
 __device__ __forceinline__ void dt_load_role(const FwdParams& p,
                                              const CUtensorMap* tq,
                                              const CUtensorMap* tk,
@@ -1341,7 +1354,7 @@ __device__ __forceinline__ void dt_load_role(const FwdParams& p,
   bool ok = true;
   for (int ui = 0; ok; ++ui) {
     const int buf = ui % kListBufs;
-    ok = dt_build_list<TRACE>(p, bars, lists, t, ui);
+    ok = dt_build_list<TRACE, SHARED>(p, bars, lists, t, ui);
     if (!ok) break;
     const DtMeta mt = bars->meta[t][buf];
     if (mt.unit < 0) break;
@@ -1532,8 +1545,9 @@ __device__ __forceinline__ void dt_mma_role(const FwdParams& p, uint8_t* smem,
   __syncwarp();
 }
 
-template <int D, int SCORE, int MOD, bool KEEP, bool TRACE>
+template <int D, int SCORE, int MOD, bool KEEP, bool TRACE, bool SHARED>
 __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
+                                              DtPair* pair, float* merge,
                                               const uint16_t* lists,
                                               uint32_t tmem, const int t) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -1772,6 +1786,34 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
       tmem_ld_wait();
       tc_fence_before();
       mbar_arrive(&bars->o_free[t]);
+      if (SHARED) {
+        if (t == 1) {  // O, reference and sum for pipeline 0
+#pragma unroll
+          for (int c = 0; c < D; ++c)
+            merge[c * kTileM + r] = __uint_as_float(o[c]);
+          pair->ref[r] = m_used;
+          pair->total[r] = l_sum;
+          mbar_arrive(&bars->merge);
+          mbar_arrive(&bars->list_free[t][buf]);
+          continue;
+        }
+        if (!warp_wait(&bars->merge, 0, abort_flag, p.timeout_ns)) {
+          record_timeout(kRoleScore, 8);
+          break;
+        }
+        const float l1 = pair->total[r], m1 = pair->ref[r];
+        const float mm = fmaxf(m_used, m1);
+        const float w0 = m_used == NEG_INF ? 0.f : ex2_approx(m_used - mm);
+        const float w1 = m1 == NEG_INF ? 0.f : ex2_approx(m1 - mm);
+        if (!(l1 == 0.f)) {  // (0: it saw nothing, or had no entry)
+#pragma unroll
+          for (int c = 0; c < D; ++c)
+            o[c] = __float_as_uint(fmaf(merge[c * kTileM + r], w1,
+                                        __uint_as_float(o[c]) * w0));
+          l_sum = fmaf(l1, w1, l_sum * w0);
+          m_used = mm;
+        }
+      }
       float inv = 1.f;
       if (SCORE == BSM_SCORE_SOFTMAX) inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
       if (row_ok) {
@@ -1793,6 +1835,14 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
           }
         }
       }
+    } else if (SHARED && t == 1) {
+      pair->ref[r] = NEG_INF;
+      pair->total[r] = 0.f;
+      tc_fence_before();
+      mbar_arrive(&bars->o_free[t]);
+      mbar_arrive(&bars->merge);
+      mbar_arrive(&bars->list_free[t][buf]);
+      continue;
     } else {
       if (row_ok) {
 #pragma unroll
@@ -1824,9 +1874,10 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
 // 155 and 186; causal S=8192, 32/8 heads, cap 20: 571 and 690.  With a bias,
 // whose running maximum the two threads would have to exchange on every entry,
 // it was 1 to 7 % slower instead.
-template <int D, bool KEEP, bool TRACE>
+template <int D, bool KEEP, bool TRACE, bool SHARED>
 __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
                                                   DtBars* bars, DtPair* pair,
+                                                  float* merge,
                                                   const uint16_t* lists,
                                                   uint32_t tmem, const int t,
                                                   const int hf) {
@@ -1977,6 +2028,29 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
       tmem_ld_wait();
       tc_fence_before();
       mbar_arrive(&bars->o_free[t]);
+      if (SHARED) {
+        float* at = merge + hf * (D / 2) * kTileM + r;
+        if (t == 1) {  // O and sum for pipeline 0 (the reference is the same)
+#pragma unroll
+          for (int c = 0; c < D / 2; ++c)
+            at[c * kTileM] = __uint_as_float(o[c]);
+          if (hf == 0) pair->total[r] = l_sum;
+          mbar_arrive(&bars->merge);
+          mbar_arrive(&bars->list_free[t][buf]);
+          continue;
+        }
+        if (!warp_wait(&bars->merge, 0, abort_flag, p.timeout_ns)) {
+          record_timeout(kRoleScore, 8);
+          break;
+        }
+        const float l1 = pair->total[r];
+        if (!(l1 == 0.f)) {  // (0: it saw nothing, or had no entry)
+#pragma unroll
+          for (int c = 0; c < D / 2; ++c)
+            o[c] = __float_as_uint(__uint_as_float(o[c]) + at[c * kTileM]);
+          l_sum += l1;
+        }
+      }
       const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
       if (row_ok) {
         const bool v8 = p.o_vec8 != 0;
@@ -1995,6 +2069,13 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
           }
         }
       }
+    } else if (SHARED && t == 1) {
+      if (hf == 0) pair->total[r] = 0.f;
+      tc_fence_before();
+      mbar_arrive(&bars->o_free[t]);
+      mbar_arrive(&bars->merge);
+      mbar_arrive(&bars->list_free[t][buf]);
+      continue;
     } else {
       if (row_ok) {
 #pragma unroll
@@ -2015,7 +2096,7 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
   }
 }
 
-template <int D, int SCORE, int MOD, bool TRACE>
+template <int D, int SCORE, int MOD, bool TRACE, bool SHARED>
 __global__ void __launch_bounds__(dt_threads(MOD), 1)
     splash_fwd_dt_kernel(const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k,
@@ -2052,6 +2133,7 @@ __global__ void __launch_bounds__(dt_threads(MOD), 1)
         mbar_init(&bars->meet[t][q], 32);  // half 0 tells half 1
         mbar_init(&bars->meet_sum[t][q], 64);
       }
+      mbar_init(&bars->merge, dt_score_threads(MOD));
     }
     bars->abort = 0;
     for (int i = 0; i < 6; ++i) bars->trace_n[i] = 0;
@@ -2074,30 +2156,35 @@ __global__ void __launch_bounds__(dt_threads(MOD), 1)
     const int t = warp & 1;
     uint16_t* lt = lists + t * kListBufs * kMaxKvTiles;
     if (warp < 2)
-      dt_load_role<D, TRACE>(p, &tm_q, &tm_k, &tm_v, smem, bars, lt, t);
+      dt_load_role<D, TRACE, SHARED>(p, &tm_q, &tm_k, &tm_v, smem, bars, lt, t);
     else
       dt_mma_role<D, SCORE, TRACE>(p, smem, bars, tmem, t);
   } else {
     // per-element keep bits only when segment ids are unsorted or an
     // arbitrary mask is given (read once; the same for every thread)
+    DtPair* pair = reinterpret_cast<DtPair*>(smem + kDtOffPair);
+    float* merge = reinterpret_cast<float*>(smem + kDtOffMerge);
     if constexpr (MOD != kModCap) {
       setmaxnreg_inc<kRegsScore>();
       const int t = (warp - 4) / 4;
       const uint16_t* lt = lists + t * kListBufs * kMaxKvTiles;
       if (((p.flags & BSM_MASK_SEGMENT) && (*p.seg_flags & 1) != 0) ||
           p.dense != nullptr)
-        dt_score_role<D, SCORE, MOD, true, TRACE>(p, bars, lt, tmem, t);
+        dt_score_role<D, SCORE, MOD, true, TRACE, SHARED>(p, bars, pair, merge,
+                                                          lt, tmem, t);
       else
-        dt_score_role<D, SCORE, MOD, false, TRACE>(p, bars, lt, tmem, t);
+        dt_score_role<D, SCORE, MOD, false, TRACE, SHARED>(p, bars, pair, merge,
+                                                           lt, tmem, t);
     } else {
       const int t = (warp - 4) / 8, hf = (warp - 4) / 4 & 1;
       const uint16_t* lt = lists + t * kListBufs * kMaxKvTiles;
-      DtPair* pair = reinterpret_cast<DtPair*>(smem + kDtOffPair);
       // (an arbitrary mask with modified scores takes the lockstep kernel)
       if ((p.flags & BSM_MASK_SEGMENT) && (*p.seg_flags & 1) != 0)
-        dt_score_cap_role<D, true, TRACE>(p, bars, pair, lt, tmem, t, hf);
+        dt_score_cap_role<D, true, TRACE, SHARED>(p, bars, pair, merge, lt,
+                                                  tmem, t, hf);
       else
-        dt_score_cap_role<D, false, TRACE>(p, bars, pair, lt, tmem, t, hf);
+        dt_score_cap_role<D, false, TRACE, SHARED>(p, bars, pair, merge, lt,
+                                                   tmem, t, hf);
     }
   }
 
@@ -2118,19 +2205,24 @@ template <int D, int SCORE, int MOD>
 cudaError_t launch_dt(const FwdParams& p, const CUtensorMap& tq,
                       const CUtensorMap& tk, const CUtensorMap& tv, int grid,
                       int num_sms, cudaStream_t stream) {
-  // (S=1280, 12/4 heads, no mask, cap 50: FIGURE us with two tiles per CTA,
-  // FIGURE with one)
-  if (p.unit_counter == nullptr && 2 * p.num_units <= num_sms)
-    grid = 2 * p.num_units;
   // the instance that records the event trace is launched only with one
-  auto kern = p.trace != nullptr ? splash_fwd_dt_kernel<D, SCORE, MOD, true>
-                                 : splash_fwd_dt_kernel<D, SCORE, MOD, false>;
+  auto kern = p.trace != nullptr
+                  ? splash_fwd_dt_kernel<D, SCORE, MOD, true, false>
+                  : splash_fwd_dt_kernel<D, SCORE, MOD, false, false>;
+  if constexpr (MOD != 0) {
+    // a CTA for every query tile, where there are SMs enough
+    if (p.trace == nullptr && p.unit_counter == nullptr &&
+        2 * p.num_units <= num_sms) {
+      kern = splash_fwd_dt_kernel<D, SCORE, MOD, false, true>;
+      grid = 2 * p.num_units;
+    }
+  }
   cudaFuncAttributes attr;
   cudaError_t e = cudaFuncGetAttributes(&attr, kern);
   if (e != cudaSuccess) return e;
   if (MOD != kModCap && attr.numRegs * kDtThreads < kRegsNeeded)
     return cudaErrorInvalidConfiguration;
-  constexpr int kSmem = kDtSmemBytes + (MOD == kModCap ? sizeof(DtPair) : 0);
+  constexpr int kSmem = kDtSmemBytes + (MOD != 0 ? sizeof(DtPair) : 0);
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kSmem);
   if (e != cudaSuccess) return e;

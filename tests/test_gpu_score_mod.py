@@ -134,6 +134,47 @@ def test_segments(kind, D, mod):
 
 
 @pytest.mark.parametrize("mod", MODS, ids=[m[0] for m in MODS])
+@pytest.mark.parametrize("per_sm", [0.3, 0.8, 1.7])
+@pytest.mark.parametrize("D", [64, 128])
+def test_query_tiles_per_sm(D, per_sm, mod):
+    """Few 256-row units share a CTA's pipelines, more take one pipeline
+    each, and above one per SM they are drawn from a counter."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    S = 400
+    H = int(per_sm * sms / 2)  # two units per head
+    q, k, v, do = inputs(f"units{D}{per_sm}{mod[0]}", 1, H, H, S, S, D, 3.0)
+    run(q, k, v, do, C, softcap=mod[1],
+        slopes=slopes_of(H, mod[2]) if mod[2] else None, bwd=False)
+
+
+@pytest.mark.parametrize("mod", MODS, ids=[m[0] for m in MODS])
+@pytest.mark.parametrize("per_sm", [0.1, 1.3])
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_that_see_nothing(D, per_sm, mod):
+    """A band over fewer keys than queries leaves rows, and whole query
+    tiles, empty; segment ids that no key has leave rows empty inside tiles
+    that are not, in the one or the other half of the keys' tiles."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    Sq, Skv = 640, 300
+    H = max(1, int(per_sm * sms / 3))
+    q, k, v, do = inputs(f"dead{D}{per_sm}{mod[0]}", 1, H, H, Sq, Skv, D, 3.0)
+    sl = slopes_of(H, mod[2]) if mod[2] else None
+    _, lse, _ = run(q, k, v, do, L | BD, 100, softcap=mod[1], slopes=sl,
+                    bwd=False)
+    assert bool(torch.isneginf(lse[..., 400:]).all())
+    rng = np.random.default_rng(77)
+    sq = rng.integers(0, 4, size=(1, Sq)).astype(np.int32)
+    skv = np.repeat(np.array([[0, 1, 2]], np.int32), 128, axis=1)[:, :Skv]
+    # unsorted: element by element
+    skv_mixed = np.array([2, 0, 1], np.int32)[skv]
+    for ids in (skv, skv_mixed):
+        _, lse, _ = run(q, k, v, do, SG, 0, sq, np.ascontiguousarray(ids),
+                        softcap=mod[1], slopes=sl, bwd=False)
+        dead = torch.from_numpy(sq[0] == 3).to(lse.device)
+        assert bool(torch.isneginf(lse[..., dead]).all())
+
+
+@pytest.mark.parametrize("mod", MODS, ids=[m[0] for m in MODS])
 def test_arbitrary_mask_with_empty_rows(mod):
     S, H = 500, 2
     q, k, v, do = inputs("dense" + mod[0], 1, H, H, S, S, 128, 3.0)
