@@ -73,6 +73,50 @@ def _fast_stream(stream) -> int | None:
     return None if stream is None else _stream_handle(stream)
 
 
+def _other_stream(stream, dev):
+    """A given stream that is not dev's current one, as a torch stream; else
+    None."""
+    if stream is None:
+        return None
+    handle = _stream_handle(stream)
+    if handle == torch.cuda.current_stream(dev).cuda_stream:
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return (torch.cuda.ExternalStream(handle, device=dev) if handle
+            else torch.cuda.default_stream(dev))
+
+
+def _run_on(s, call):
+    """call() with stream s current, so that what it allocates is s's memory:
+    scratch is not used again before s has run the call, and the tensors it
+    returns not before the caller's stream, too, is done with them."""
+    caller = torch.cuda.current_stream(s.device)
+    with torch.cuda.stream(s):
+        result = call()
+    for t in result:
+        if t is not None and t.is_cuda:
+            t.record_stream(caller)
+    return result
+
+
+def _scratch(nbytes: int, dev, stream, kept: dict | None = None):
+    """Device memory for a call on `stream` (allocated there: see _run_on).
+    With `kept`, one per (device, stream), as calls on one stream run in
+    order; a captured call gets one of its own, from the graph's memory, as
+    graphs captured on one stream may run at once."""
+    s = _other_stream(stream, dev)
+    if s is not None:
+        with torch.cuda.stream(s):
+            return _scratch(nbytes, dev, None, kept)
+    if kept is None or torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    key = (dev, torch.cuda.current_stream(dev).cuda_stream)
+    if key not in kept:
+        kept[key] = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return kept[key]
+
+
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -207,18 +251,6 @@ def bsm_splash_fwd_workspace_bytes() -> int:
 _workspaces: dict = {}
 
 
-def _default_workspace(device, stream_handle):
-    """One workspace per (device, stream): calls on one stream run in
-    order, so they can share it."""
-    key = (device, stream_handle)
-    ws = _workspaces.get(key)
-    if ws is None:
-        ws = torch.empty(bsm_splash_fwd_workspace_bytes(), dtype=torch.uint8,
-                         device=device)
-        _workspaces[key] = ws
-    return ws
-
-
 def _score_mod(softcap: float, alibi_slopes, H: int, device):
     """bsm_score_mod of a cap and per-head slopes, or None for neither."""
     if alibi_slopes is not None:
@@ -244,7 +276,8 @@ def bsm_splash_fwd(q, k, v, mask_info: MaskInfo, q_segment_ids,
     sh = _stream_handle(stream)
     mod = _score_mod(softcap, alibi_slopes, H, q.device)
     if workspace is None:
-        workspace = _default_workspace(q.device, sh)
+        workspace = _scratch(bsm_splash_fwd_workspace_bytes(), q.device,
+                             stream, _workspaces)
     views, at = _views(q, k, v, out)  # strides are behind the pointers
     _check(_lib.lib().bsm_splash_fwd_mod(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), at + 8, at + 40, at + 72,
@@ -345,7 +378,7 @@ def bsm_splash_bwd(q, k, v, out, lse, dout, mask_info: MaskInfo,
     need = bsm_splash_bwd_workspace_bytes(B, H, Sq, score) if mod is None \
         else bsm_splash_bwd_mod_workspace_bytes(B, H, H_kv, Sq, Skv, D)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, q.device, stream)
     views, at = _views(q, k, v, out, dout, dq, dk, dv)
     _check(_lib.lib().bsm_splash_bwd_mod(
         at, at + 32, at + 64, None if out is None else at + 96, _ptr(lse),
@@ -470,22 +503,6 @@ def bsm_paged_attention_workspace_bytes() -> int:
 _paged_workspaces: dict = {}
 
 
-def _paged_workspace(dev, stream_handle):
-    """paged_attention's workspace: one per (device, stream), as calls on one
-    stream run in order.  A captured call gets one of its own, from the
-    graph's memory: graphs captured on one stream may run at once."""
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(bsm_paged_attention_workspace_bytes(),
-                           dtype=torch.uint8, device=dev)
-    key = (dev, stream_handle)
-    ws = _paged_workspaces.get(key)
-    if ws is None:
-        ws = torch.empty(bsm_paged_attention_workspace_bytes(),
-                         dtype=torch.uint8, device=dev)
-        _paged_workspaces[key] = ws
-    return ws
-
-
 def bsm_paged_attention(q, cache: KVCache, page_table, lens, scale: float,
                         out, lse=None, window: int = 0, softcap: float = 0.0,
                         alibi_slopes=None, stream=None,
@@ -518,7 +535,8 @@ def bsm_paged_attention(q, cache: KVCache, page_table, lens, scale: float,
         raise ValueError("integer out of range")
     sh = _stream_handle(stream)
     if workspace is None:
-        workspace = _paged_workspace(dev, sh)
+        workspace = _scratch(bsm_paged_attention_workspace_bytes(), dev,
+                             stream, _paged_workspaces)
     views, at = _views(q, out)
     _check(_lib.lib().bsm_paged_attention(
         at, s, page_table.data_ptr(), page_table.stride(0),
@@ -585,6 +603,21 @@ def build_mask_info(flags: int, B: int, Sq: int, Skv: int, block_q: int = 128,
                     kv_segment_ids=None, device=None, stream=None,
                     dense_bits=None) -> MaskInfo:
     """Allocate the mask-info buffer with torch and build the tables."""
+    if stream is not None:
+        dev = torch.device(device) if device is not None else \
+            _CUDA if q_segment_ids is None else q_segment_ids.device
+        s = _other_stream(stream, dev) if dev.type == "cuda" else None
+        if s is not None:
+            made = []
+
+            def build():
+                made.append(build_mask_info(
+                    flags, B, Sq, Skv, block_q, block_kv, window,
+                    q_segment_ids, kv_segment_ids, device, None, dense_bits))
+                return [made[0].buffer]
+
+            _run_on(s, build)
+            return made[0]
     fast = _fast()
     if fast:
         if device is None:
@@ -651,7 +684,9 @@ def kv_append(cache: KVCache, page_table, lens, k_new, v_new, *, n_new=None,
     cache: sequence b, which holds lens[b] tokens, gets its first n_new[b]
     (None: all T).  One scale per page and head, a power of two; a page that
     already holds tokens keeps or raises its scale (include/bsm.h has the
-    rule).  ``lens`` is not changed: advance it before attending."""
+    rule).  A page that the call writes belongs to one sequence only; pages
+    that sequences share are full ones.  ``lens`` is not changed: advance it
+    before attending."""
     fast = _fast()
     if fast:
         return fast.kv_append(
@@ -670,6 +705,13 @@ def paged_attention(q, cache: KVCache, page_table, lens, *,
     ``window`` > 0 keeps the last ``window`` keys of each query; scale,
     ``softcap`` and ``alibi_slopes`` as in :func:`splash_attention`.  Rows
     that see no key are 0 with logsumexp -inf.  Returns (out, lse)."""
+    s = _other_stream(stream, cache.device) \
+        if cache.device.type == "cuda" else None
+    if s is not None:
+        return _run_on(s, lambda: paged_attention(
+            q, cache, page_table, lens, scale=scale, window=window,
+            softcap=softcap, alibi_slopes=alibi_slopes, return_lse=return_lse,
+            out=out, lse=lse))
     fast = _fast()
     if fast:
         return fast.paged_attention(
@@ -706,6 +748,14 @@ def splash_attention_bwd(q, k, v, out, lse, dout, *,
     ``lse`` are the forward's (softmax path; ignored for the pointwise
     path); ``softcap`` and ``alibi_slopes`` as given to it (the slopes are
     constants and get no gradient)."""
+    s = _other_stream(stream, q.device) if q.is_cuda else None
+    if s is not None:
+        return _run_on(s, lambda: splash_attention_bwd(
+            q, k, v, out, lse, dout, mask_flags=mask_flags, window=window,
+            q_segment_ids=q_segment_ids, kv_segment_ids=kv_segment_ids,
+            scale=scale, score=score, block_q=block_q, block_kv=block_kv,
+            mask_info=mask_info, dense_mask=dense_mask, softcap=softcap,
+            alibi_slopes=alibi_slopes))
     B, H, Sq, D = q.shape
     Skv = k.shape[2]
     if scale is None:
@@ -817,6 +867,15 @@ def splash_attention(q, k, v, *, mask_flags: int = MASK_CAUSAL,
         return _splash_host_pipelined(
             q, k, v, mask_flags, window, q_segment_ids, kv_segment_ids,
             scale, score, block_q, block_kv, want_lse, out, lse, stream, dev)
+    s = _other_stream(stream, dev)
+    if s is not None:
+        return _run_on(s, lambda: splash_attention(
+            q, k, v, mask_flags=mask_flags, window=window,
+            q_segment_ids=q_segment_ids, kv_segment_ids=kv_segment_ids,
+            scale=scale, score=score, block_q=block_q, block_kv=block_kv,
+            mask_info=mask_info, return_lse=return_lse, out=out, lse=lse,
+            dense_mask=dense_mask, softcap=softcap,
+            alibi_slopes=alibi_slopes))
     if host:
         nb = q.is_pinned()
         qd = q.to(dev, non_blocking=nb)

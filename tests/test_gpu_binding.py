@@ -69,6 +69,53 @@ def test_splash(both, kind):
         same(r, a)
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_side_stream_beside_a_busy_one(both, handle):
+    """Scratch and mask infos of calls on another stream are not given out
+    again on the caller's before that stream has run the calls."""
+    B, H, S, D = 1, 4, 700, 64
+    g = torch.Generator().manual_seed(6)
+    q, k, v, do = (torch.randn(B, H, S, D, generator=g).bfloat16().cuda()
+                   for _ in range(4))
+    kw = dict(mask_flags=bsm.MASK_CAUSAL, softcap=9.0)
+    out, lse = bsm.splash_attention(q, k, v, **kw)
+    want = (out, lse) + tuple(
+        bsm.splash_attention_bwd(q, k, v, out, lse, do, **kw))
+    sizes = {B * H * S * 4, B * H * S * 64, 1 << 12, 1 << 14, 1 << 16}
+
+    def run():
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        s = side.cuda_stream if handle else side
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2_000_000)
+        got = []
+        for _ in range(10):
+            o, l = bsm.splash_attention(q, k, v, stream=s, **kw)
+            got.append((o, l) + tuple(bsm.splash_attention_bwd(
+                q, k, v, o, l, do, stream=s, **kw)))
+            for n in sizes:  # would take memory freed too early, and spoil it
+                for _ in range(4):
+                    torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+        side.synchronize()
+        return [t for r in got for t in r]
+
+    for r in both(run):
+        same(r, list(want) * 10)
+
+
+def test_host_tensors_on_a_side_stream(both):
+    B, H, S, D = 1, 2, 200, 64
+    g = torch.Generator().manual_seed(7)
+    q, k, v = (torch.randn(B, H, S, D, generator=g).bfloat16()
+               for _ in range(3))
+    want = bsm.splash_attention(q.cuda(), k.cuda(), v.cuda(), softcap=9.0)
+    side = torch.cuda.Stream()
+    for r in both(lambda: bsm.splash_attention(q, k, v, softcap=9.0,
+                                               stream=side)):
+        same([t.cuda() for t in r], want)
+
+
 def test_mask_info(both):
     a, b = both(lambda: bsm.build_mask_info(
         bsm.MASK_CAUSAL | bsm.MASK_LOCAL, 1, 700, 500, 64, 128, window=90))
