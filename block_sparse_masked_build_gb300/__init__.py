@@ -1,5 +1,6 @@
 """GB300-native block-sparse masked attention (Splash-style): forward and
-backward.
+backward, with a tanh cap and a distance bias of the scores where wanted, and
+a paged 8-bit key/value cache with the attention that reads it.
 
 The compute runs in libbsm.so (hand-written CUDA for sm_103a) behind the C
 ABI of ``include/bsm.h``; this package is its Python binding.

@@ -40,6 +40,10 @@
 //     dK/dV: dV += P T1, dK += dS T0 (A from TMEM, B = the streamed tile
 //            read MN-major) -> TMEM [256, 256 + D), [384, 384 + D)
 //     dQ:    dQ += dS T0 -> TMEM [256, 256 + D)
+// With modified scores sixteen warps do the elementwise work (576 threads, 32
+// columns each; see bwd_elem_mod_role), and where there are few key tiles the
+// dK/dV walks are cut into parts that leave f32 partial sums in the workspace,
+// which a small kernel adds up in order (see bwd_parts).
 // Every mbarrier wait is bounded; a role that gives up records the error
 // (read by bsm_device_status) and every role stops.
 #include <cstdint>

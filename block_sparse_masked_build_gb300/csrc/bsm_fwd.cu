@@ -1,8 +1,9 @@
 // Block-sparse masked attention forward for sm_103a (GB300).  Two kernels:
-// the lockstep one described here, and, at head dim 128 for packed
-// sequences (segment ids) and for any mask below 4096 keys, a variant whose
-// two query tiles run as independent pipelines (see "Decoupled query
-// tiles" below).
+// the lockstep one described here, and a variant whose two query tiles run as
+// independent pipelines (see "Decoupled query tiles" below): at head dim 128
+// for packed sequences (segment ids) and for any mask below 4096 keys, and for
+// modified softmax scores (tanh cap, distance bias; see modify_tile) at both
+// head dims, all but those with an arbitrary mask.
 //
 // One persistent CTA per SM takes work units of (batch, head, 256 query
 // rows) from a counter in the caller's workspace, longest units first.  A
@@ -1161,7 +1162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Decoupled query tiles, for packed sequences (segment ids).  There the
+// Decoupled query tiles, made for packed sequences (segment ids).  There the
 // units are short and the two query tiles of a unit often need different KV
 // tiles, so the lockstep pipeline above spends much of its time at unit
 // boundaries and on entries one tile skips.  Here the two 128-row query
@@ -1170,14 +1171,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 // and has its own Q buffer and two-slot K/V ring, so one pipeline's unit
 // boundary overlaps the other's work on the tensor core.  K/V tiles are not
 // shared between the tiles (L2 carries the reuse).  Masks without segment
-// ids take this kernel too below 4096 keys, where units are short as well.
+// ids take this kernel too below 4096 keys, where units are short as well,
+// and modified scores at any length (see launch_score).
 //
 // Warp roles (384 threads, three warpgroups, registers split as above):
 // warps 0/1 take pipeline 0/1's units, build their lists and load their
 // tiles; warps 2/3 issue its MMAs (warp 2 also owns the TMEM); warps 4-7
-// and 8-11 are the score warpgroups of pipeline 0 and 1.  TMEM as above:
-// S_t/P_t at [128 t, +128), O_t at [256 + 128 t, +128).  Head dim 128,
-// softmax or pointwise.
+// and 8-11 are the score warpgroups of pipeline 0 and 1.  With a cap alone
+// each pipeline has two score warpgroups (640 threads without a register
+// split; see dt_score_cap_role).  TMEM as above: S_t/P_t at [128 t, +128),
+// O_t at [256 + 128 t, +D).  Head dim 128, softmax or pointwise; head dim 64
+// with modified scores only.
 constexpr int kDtThreads = 384;
 constexpr int kDtTile = kTileM * 128 * 2;  // one 128 x 128 bf16 tile
 constexpr int kDtOffQ = 0;                 // Q of pipeline t at t tiles
