@@ -411,7 +411,7 @@ class KVCache:
     k_scale, v_scale [num_pages, H_kv] (float32), all contiguous.  An element
     is its code times the scale of its page and head."""
 
-    __slots__ = ("k_pages", "v_pages", "k_scale", "v_scale", "_struct")
+    __slots__ = ("_tensors",)
 
     def __init__(self, k_pages, v_pages, k_scale, v_scale):
         fast = _fast()
@@ -419,23 +419,23 @@ class KVCache:
             fast.check_cache(k_pages, v_pages, k_scale, v_scale)
         else:
             _check_cache(k_pages, v_pages, k_scale, v_scale)
-        self.k_pages, self.v_pages = k_pages, v_pages
-        self.k_scale, self.v_scale = k_scale, v_scale
-        self._struct = None
+        self._tensors = (k_pages, v_pages, k_scale, v_scale)
+
+    # read only: calls rely on the checks made above
+    k_pages = property(lambda self: self._tensors[0])
+    v_pages = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
 
     @property
     def device(self) -> torch.device:
-        return self.k_pages.device
+        return self._tensors[0].device
 
     @property
     def struct(self) -> KVCacheStruct:
         """bsm_kv_cache, for the C ABI."""
-        if self._struct is None:
-            self._struct = KVCacheStruct(
-                self.k_pages.data_ptr(), self.v_pages.data_ptr(),
-                self.k_scale.data_ptr(), self.v_scale.data_ptr(),
-                *self.k_pages.shape)
-        return self._struct
+        return KVCacheStruct(*[t.data_ptr() for t in self._tensors],
+                             *self.k_pages.shape)
 
     @classmethod
     def empty(cls, num_pages: int, H_kv: int, page_size: int, D: int,
@@ -690,8 +690,8 @@ def kv_append(cache: KVCache, page_table, lens, k_new, v_new, *, n_new=None,
     fast = _fast()
     if fast:
         return fast.kv_append(
-            cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale,
-            page_table, lens, k_new, v_new, n_new, _fast_stream(stream))
+            *cache._tensors, page_table, lens, k_new, v_new, n_new,
+            _fast_stream(stream))
     bsm_kv_append(cache, page_table, lens, k_new, v_new, n_new, stream)
 
 
@@ -715,9 +715,8 @@ def paged_attention(q, cache: KVCache, page_table, lens, *,
     fast = _fast()
     if fast:
         return fast.paged_attention(
-            cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale,
-            page_table, lens, q, scale, window, softcap, alibi_slopes, out,
-            lse, return_lse, _fast_stream(stream))
+            *cache._tensors, page_table, lens, q, scale, window, softcap,
+            alibi_slopes, out, lse, return_lse, _fast_stream(stream))
     if q.dim() != 4:
         raise ValueError("q must be [B, H, T, D]")
     B, H, T, D = q.shape

@@ -165,6 +165,13 @@ def test_python_checks(binding, lib, monkeypatch):
         bsm.kv_append(cache, table, lens, new, new)
 
 
+def test_a_cache_keeps_the_tensors_it_checked():
+    cache = bsm.KVCache(*ref.random_cache(3, 2, 16, 64, 1))
+    for name in ("k_pages", "v_pages", "k_scale", "v_scale"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, getattr(cache, name))
+
+
 def test_reference_rounding():
     # every e4m3 value is itself; midpoints go to the even neighbour
     codes = torch.arange(0, 0x7f, dtype=torch.uint8)
