@@ -259,6 +259,10 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src,
                "l"(src), "r"(keep ? 16 : 0)
                : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src)
+               : "memory");
+}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src,
                                           bool keep) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst),
@@ -344,15 +348,29 @@ __device__ __forceinline__ void load_group(const PagedParams& p,
   const int64_t off =
       ((block << p.page_shift) + (tok & (p.page_size - 1))) * D + lane * 16;
   constexpr int kPieces = kPaGroup * D / 16;
-  const bool whole = ok && tok >= lo && tok + kPaGroup <= hi;
+  // piece i * 32 + lane lies at first + i * 512 but for the exchange, which
+  // differs in one bit between odd and even i (D = 128).  (Groups that end
+  // inside take the other branch: with the tests in one loop 64 sequences of
+  // 300-12000 tokens took 135 us, so 131; of four query tokens 206 and 198.)
+  const uint32_t first = stage + piece_at<D>(lane / (D / 16), lane % (D / 16));
+  const uint8_t* k = p.k + off;
+  const uint8_t* v = p.v + off;
+  if (ok && tok >= lo && tok + kPaGroup <= hi) {  // whole (warp-uniform)
 #pragma unroll
-  for (int i = 0; i < kPieces / 32; ++i) {
-    const int c = i * 32 + lane;
-    const int tr = c / (D / 16);
-    const bool keep = whole || (ok && tok + tr >= lo && tok + tr < hi);
-    const uint32_t at = piece_at<D>(tr, c % (D / 16));
-    cp_async16(stage + at, p.k + off + i * 512, keep);
-    cp_async16(stage + kPaGroup * D + at, p.v + off + i * 512, keep);
+    for (int i = 0; i < kPieces / 32; ++i) {
+      const uint32_t at = (D == 128 && (i & 1) ? first ^ 32u : first) + i * 512;
+      cp_async16(at, k + i * 512);
+      cp_async16(at + kPaGroup * D, v + i * 512);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPieces / 32; ++i) {
+      const int t = tok + i * (512 / D) + lane / (D / 16);
+      const bool keep = ok && t >= lo && t < hi;
+      const uint32_t at = (D == 128 && (i & 1) ? first ^ 32u : first) + i * 512;
+      cp_async16(at, k + i * 512, keep);
+      cp_async16(at + kPaGroup * D, v + i * 512, keep);
+    }
   }
   if (lane < 2)
     cp_async4(scale_at + lane * 4, (lane == 0 ? p.k_scale : p.v_scale) + block,
@@ -514,6 +532,9 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
   const int g = lane / 4, t = lane % 4;
   const int G = p.H / p.H_kv, rows = G * p.T;
   const float NEG_INF = __int_as_float(0xff800000);
+  // a row's maximum before it has seen a key: the lowest finite value, from
+  // which -inf - m and m - m need no special case
+  const float kLowest = __int_as_float(0xff7fffff);
   const int len = plan.len, lo = plan.lo, first_group = plan.first_group;
 
   // the copies start first; the queries are loaded while they run
@@ -638,7 +659,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
       for (int i = 0; i < 4; ++i) o[nt][s][i] = 0.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      m[nt][i] = NEG_INF;
+      m[nt][i] = kLowest;
       l[nt][i] = 0.f;
     }
   }
@@ -812,8 +833,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
       float pr[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float mm = m[nt][i & 1];
-        pr[i] = ex2_approx(s[nt][i] - (mm == NEG_INF ? 0.f : mm));
+        pr[i] = ex2_approx(s[nt][i] - m[nt][i & 1]);
         l[nt][i & 1] += pr[i];
         pr[i] *= v_mul;
       }
@@ -943,10 +963,9 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
     const int r = i / (D / 2), d = i % (D / 2) * 2;
     const int rr = row0 + r;
     if (rr >= rows) break;
-    float mx = NEG_INF;
+    float base = kLowest;
 #pragma unroll
-    for (int w = 0; w < kPaWarps; ++w) mx = fmaxf(mx, sm[w * R + r]);
-    const float base = mx == NEG_INF ? 0.f : mx;
+    for (int w = 0; w < kPaWarps; ++w) base = fmaxf(base, sm[w * R + r]);
     float sum = 0.f, xy[2] = {0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < kPaWarps; ++w) {
@@ -959,7 +978,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
     if (part != nullptr) {
       *reinterpret_cast<float2*>(part + r * D + d) = make_float2(xy[0], xy[1]);
       if (d == 0) {
-        part[R * D + r] = mx;
+        part[R * D + r] = base;
         part[R * D + R + r] = sum;
       }
       continue;
@@ -970,11 +989,12 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
 }
 
 // CTAs per SM of the attention kernel: three rings fit an SM's shared memory
-// at head dim 128; registers set the other limits.
+// at head dim 128.  At 64 four fit its registers (64 sequences of 300-12000
+// tokens, one row tile: 86 us, with five 91; two: 128, with three 131).
 template <int D, int NT>
-constexpr int kPaPerSm = D == 64 && NT == 1 ? 4 : 3;
+constexpr int kPaPerSm = D == 64 ? 4 : 3;
 
-static_assert(kPaPerSm<64, 1> <= kPaMaxPerSm, "workspace");
+static_assert(kPaPerSm<64, 2> <= kPaMaxPerSm, "workspace");
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kPaThreads, kPaPerSm<D, NT>)
@@ -1075,19 +1095,17 @@ __global__ void __launch_bounds__(kPaThreads)
   };
   const int64_t c0 = cta_of(u0), c1 = cta_of(u0 + n - 1);
   if (c0 == c1) return;  // whole in one CTA, which wrote it
-  const float NEG_INF = __int_as_float(0xff800000);
   // the item's first unit is in the first CTA, which leaves its part in slot 1
   constexpr int64_t kPart = R * (D + 2);
   auto part_of = [&](int64_t c) {
     return p.parts + (c * 2 + (c == c0 ? 1 : 0)) * kPart;
   };
-  float mx = NEG_INF;
+  float base = __int_as_float(0xff7fffff);  // as every part's before a key
   for (int64_t c = c0 + lane; c <= c1; c += 32)
-    mx = fmaxf(mx, part_of(c)[R * D + r]);
+    base = fmaxf(base, part_of(c)[R * D + r]);
 #pragma unroll
   for (int d = 16; d > 0; d /= 2)
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-  const float base = mx == NEG_INF ? 0.f : mx;
+    base = fmaxf(base, __shfl_xor_sync(0xffffffffu, base, d));
   float sum = 0.f;
   constexpr int kStep = WIDE ? kPaWarps : 1;
   const int64_t first = c0 + (WIDE ? warp : 0);
