@@ -614,7 +614,7 @@ bsm_status bsm_splash_fwd_mod(const void* q, const void* k, const void* v,
     }
   }
   cudaError_t e;
-  if (sm_mod.kind != 0 && p.dense == nullptr && units <= num_sms) {
+  if (sm_mod.kind != 0 && bsm::fwd_mod_dt(p) && units <= num_sms) {
     // every unit has a CTA of its own: nothing to count (small calls are bound
     // by latency, and the reset is a node of its own on the stream)
     p.unit_counter = nullptr;

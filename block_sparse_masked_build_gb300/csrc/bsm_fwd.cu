@@ -677,7 +677,8 @@ __device__ __forceinline__ void cap_tile(float* s, const float* c,
 // 120 us unmodified: cap 50 183 us with an exponential and a reciprocal per
 // column, 145 us with the polynomial.
 //
-// Bias.  All columns of a tile that lie on one side of the row have bias
+// Bias (where the tensor core does not add it, see kDtOffBias).  All columns of
+// a tile that lie on one side of the row have bias
 // sl (kbase - qrow + c), sl = +-slope2: column c gets sl (c % 8) here, in the
 // same paired operation that scales S, and *base = sl (kbase - qrow); the
 // caller adds sl 8 (c / 8) + *base per 8 columns.  A tile with columns on both
@@ -1229,6 +1230,47 @@ static_assert(kTileM * 128 * 4 <= 2 * kDtTile, "merge area");
 constexpr int kDtOffPair = kDtOffBar + 1024;
 static_assert(kDtSmemBytes + sizeof(DtPair) <= 232448, "shared memory budget");
 
+// A distance bias alone (kModBias) is added by the tensor core: the bias of a
+// tile's columns on one side of the row, in units of S, is +-slope / scale *
+// (c - 64) for column c plus a term per row, so S gets one more step of 16 with
+// A = [1 1 1 0 ..] (negated right of the row) in every row and B row c = the
+// three bf16 parts of slope / scale * (c - 64), whose sum is the f32 value.
+// What is left of the bias is one number per row and tile, which goes into the
+// softmax's reference.  (With the bias added by the score warps, one paired
+// addition per two scores more, causal S=8192, 32/8 heads took 470 us; so 425,
+// and 418 without a bias.)  One 128 x 64 tile (128-byte swizzle) holds it all: columns [0, 16)
+// and [16, 32) B of the pipelines, [32, 48) and [48, 64) A and -A.
+constexpr int kDtOffBias = kDtOffPair + sizeof(DtPair);
+constexpr int kDtBiasBytes = kTileM * 128;
+static_assert(kDtOffBias % 1024 == 0, "swizzle atom");
+static_assert(kDtOffBias + kDtBiasBytes + 1024 <= 232448,
+              "shared memory budget");
+constexpr int kBiasMid = kTileN / 2;
+
+// 16-byte piece `piece` of row `row` of that tile.
+__device__ __forceinline__ uint4* bias_piece(uint8_t* smem, int row, int piece) {
+  return reinterpret_cast<uint4*>(smem + kDtOffBias + row * 128 +
+                                  ((piece ^ (row & 7)) << 4));
+}
+
+// B of pipeline t for a head (whole warp).
+__device__ __forceinline__ void write_bias(uint8_t* smem, int t, float ratio) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int i = 0; i < kTileN / 32; ++i) {
+    const int c = i * 32 + lane;
+    const float v = ratio * static_cast<float>(c - kBiasMid);
+    const uint32_t h = pack_bf16x2(v, 0.f);  // the lower half
+    const float v1 = v - __uint_as_float(h << 16);
+    const uint32_t m = pack_bf16x2(v1, 0.f);
+    const float v2 = v1 - __uint_as_float(m << 16);
+    *bias_piece(smem, c, 2 * t) =
+        make_uint4(h | m << 16, pack_bf16x2(v2, 0.f), 0u, 0u);
+  }
+  fence_proxy_async();
+  __syncwarp();
+}
+
 // Score threads of one pipeline, and threads of the kernel.
 constexpr int dt_score_threads(int mod) { return mod == kModCap ? 256 : 128; }
 constexpr int dt_threads(int mod) { return 128 + 2 * dt_score_threads(mod); }
@@ -1262,11 +1304,39 @@ __device__ __forceinline__ void dt_trace(const FwdParams& p, DtBars* bars,
 // with an idle pipeline, and shared: S=1280, 12/4 heads, no mask, cap 50: 35.7,
 // 26.4, 24.7; causal S=2048, 4/2 heads, D=64, cap 50: 43.8, 32.3, 26.8.)
 
+// The order of a unit's KV tiles under a bias that falls with the distance: the
+// query tile's own, those left of it from near to far, those right of it from
+// near to far.  The first then sets the softmax's reference for good; in
+// rising order a steep head's moves, and O is rescaled, on every entry (us,
+// rising order and this one: causal S=8192, 32/8 heads: 504 and 441, with a cap
+// 630 and 549).  Whole warp.
+template <int MOD>
+__device__ __forceinline__ void dt_order_list(const FwdParams& p,
+                                              uint16_t* list, int n, int qt,
+                                              int head) {
+  if (p.mod.slopes == nullptr || !(p.mod.slopes[head] > 0.f)) return;
+  const int lane = threadIdx.x % 32;
+  int m = 0;  // entries up to the query tile's own
+  if (p.flags & BSM_MASK_CAUSAL) {
+    m = n;
+  } else {
+    for (int i = 0; i < n; i += 32)
+      m += __popc(__ballot_sync(0xffffffffu, i + lane < n &&
+                                                 (list[i + lane] >> 2) <= qt));
+  }
+  for (int i = lane; 2 * i < m - 1; i += 32) {
+    const uint16_t a = list[i];
+    list[i] = list[m - 1 - i];
+    list[m - 1 - i] = a;
+  }
+  __syncwarp();
+}
+
 // Takes pipeline t's next unit from the counter and writes its KV-tile
 // list (uint16: tile << 2 | class) into buffer ui % kListBufs (whole warp);
 // unit -1 when none is left.  Units are numbered two per 256-row unit of
 // the lockstep kernel's order (its two query tiles), longest first.
-template <bool TRACE, bool SHARED>
+template <int MOD, bool TRACE, bool SHARED>
 __device__ __forceinline__ bool dt_build_list(const FwdParams& p, DtBars* bars,
                                               uint16_t* lists, const int t,
                                               const int ui) {
@@ -1324,6 +1394,7 @@ __device__ __forceinline__ bool dt_build_list(const FwdParams& p, DtBars* bars,
     }
     if (SHARED) n = (n + 1 - t) >> 1;  // every other entry
     __syncwarp();
+    if (MOD & kModBias) dt_order_list<MOD>(p, list, n, qt, uc.h);
     if (lane == 0) {
       mt.n = n;
       mt.unit = unit;
@@ -1343,7 +1414,7 @@ __device__ __forceinline__ bool dt_build_list(const FwdParams& p, DtBars* bars,
 // 0, V in slot 1).  The next list is built once this unit's last loads are
 // issued, i.e. while the unit's last entries still run (building it after
 // the first entry's loads measured slower).
-template <int D, bool TRACE, bool SHARED>
+template <int D, int MOD, bool TRACE, bool SHARED>
 __device__ __forceinline__ void dt_load_role(const FwdParams& p,
                                              const CUtensorMap* tq,
                                              const CUtensorMap* tk,
@@ -1358,7 +1429,7 @@ __device__ __forceinline__ void dt_load_role(const FwdParams& p,
   bool ok = true;
   for (int ui = 0; ok; ++ui) {
     const int buf = ui % kListBufs;
-    ok = dt_build_list<TRACE, SHARED>(p, bars, lists, t, ui);
+    ok = dt_build_list<MOD, TRACE, SHARED>(p, bars, lists, t, ui);
     if (!ok) break;
     const DtMeta mt = bars->meta[t][buf];
     if (mt.unit < 0) break;
@@ -1370,6 +1441,8 @@ __device__ __forceinline__ void dt_load_role(const FwdParams& p,
         if (lane == 0) record_timeout(kRoleLoad, 1);
         break;
       }
+      if (MOD == kModBias)  // (the last unit's S, which read it, is complete)
+        write_bias(smem, t, p.mod.slopes[mt.h] / p.scale);
       if (lane == 0) {
         mbar_arrive_expect_tx(&bars->q_full[t], kTileM * D * 2);
         for (int kb = 0; kb < D / 64; ++kb)
@@ -1431,10 +1504,11 @@ __device__ __forceinline__ void dt_load_role(const FwdParams& p,
 // commit goes out from the lane elect.sync picks (the same lane every
 // time: the warp is converged there); issued that way the pipeline's MMAs
 // measured ~5 % faster than from a branch lane 0 takes alone.
-template <int D, int SCORE, bool TRACE>
+template <int D, int SCORE, int MOD, bool TRACE>
 __device__ __forceinline__ void dt_mma_role(const FwdParams& p, uint8_t* smem,
-                                            DtBars* bars, uint32_t tmem,
-                                            const int t) {
+                                            DtBars* bars,
+                                            const uint16_t* lists,
+                                            uint32_t tmem, const int t) {
   const bool leader = (threadIdx.x % 32) == 0;
   volatile int* abort_flag = &bars->abort;
   constexpr uint32_t idesc_s = idesc_bf16_f32(kTileM, kTileN, false);
@@ -1452,12 +1526,15 @@ __device__ __forceinline__ void dt_mma_role(const FwdParams& p, uint8_t* smem,
   auto fail = [&](int where) {
     if (leader) record_timeout(kRoleMma, where);
   };
-  auto issue_s = [&]() {
+  const uint64_t dbias = sdesc_sw128(smem_u32(smem + kDtOffBias), 16, 1024);
+  auto issue_s = [&](bool right) {
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       const uint32_t off = (k >> 2) * (kTileM * 128 / 16) + (k & 3) * 2;
       mma_ss_elect(s_acc, dq + off, dk + off, idesc_s, k > 0 ? 1u : 0u);
     }
+    if (MOD == kModBias)
+      mma_ss_elect(s_acc, dbias + (right ? 6 : 4), dbias + 2 * t, idesc_s, 1u);
     mma_commit_elect(&bars->s_full[t]);
   };
   for (int ui = 0; ok; ++ui) {
@@ -1470,6 +1547,11 @@ __device__ __forceinline__ void dt_mma_role(const FwdParams& p, uint8_t* smem,
     }
     const DtMeta mt = bars->meta[t][buf];
     if (mt.unit < 0) break;
+    const uint16_t* list = lists + buf * kMaxKvTiles;
+    // whether entry e's keys lie right of the query tile
+    auto right = [&](int e) {
+      return MOD == kModBias && static_cast<int>(list[e] >> 2) > mt.qt;
+    };
     const int n = mt.n;
     if (n > 0) {
       ok = warp_wait(&bars->q_full[t], q_it & 1, abort_flag, p.timeout_ns) &&
@@ -1481,7 +1563,7 @@ __device__ __forceinline__ void dt_mma_role(const FwdParams& p, uint8_t* smem,
       ++q_it;
       ++k_it;
       tc_fence_after();
-      issue_s();
+      issue_s(right(0));
       if (leader) dt_trace<TRACE>(p, bars, kRoleMma, kEvSIssued, t, 0, mt.unit);
       if (n == 1) mma_commit_elect(&bars->q_empty[t]);
       mma_commit_elect(&bars->kv_empty[t][0]);
@@ -1530,7 +1612,7 @@ __device__ __forceinline__ void dt_mma_role(const FwdParams& p, uint8_t* smem,
         }
         ++k_it;
         tc_fence_after();
-        issue_s();
+        issue_s(right(e + 1));
         if (leader)
           dt_trace<TRACE>(p, bars, kRoleMma, kEvSIssued, t, e + 1, mt.unit);
         if (e + 1 == n - 1) mma_commit_elect(&bars->q_empty[t]);
@@ -1579,7 +1661,8 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
     const int n_ent = bars->meta[t][buf].n;
     const UnitCoord uc{bars->meta[t][buf].b, bars->meta[t][buf].h, 0};
     const uint16_t* list = lists + buf * kMaxKvTiles;
-    const int qrow = bars->meta[t][buf].qt * kTileM + r;
+    const int qt = bars->meta[t][buf].qt;
+    const int qrow = qt * kTileM + r;
     const bool row_ok = qrow < p.Sq;
     // visible keys of this row form [rlo, rhi] (plus the element compare of
     // unsorted segment ids)
@@ -1638,20 +1721,47 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
       ++s_cnt;
       if (tracer) dt_trace<TRACE>(p, bars, kRoleScore, kEvSFull, t, e, unit);
       tc_fence_after();
+      if (MOD == kModBias && jt == qt && !(p.flags & BSM_MASK_CAUSAL)) {
+        // Keys on both sides of the row: S has the left side's bias, which is
+        // taken twice off the keys on the right.  In TMEM, 32 columns at a
+        // time: code for it over all of the row's registers cost every tile 8 %.
+        const float twice = -2.f * (slope2 / p.scale_log2);
+#pragma unroll 1
+        for (int q = 0; q < kTileN / 32; ++q) {
+          uint32_t x[32];
+          tmem_ld32(s_addr + q * 32, x);
+          tmem_ld_wait();
+          const int d0 = kbase + q * 32 - qrow;
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            x[c] = __float_as_uint(fmaf(twice,
+                                        static_cast<float>(max(d0 + c, 0)),
+                                        __uint_as_float(x[c])));
+          tmem_st32(s_addr + q * 32, x);
+        }
+        tmem_st_wait();
+      }
       uint32_t sraw[kTileN];
 #pragma unroll
       for (int q = 0; q < kTileN / 32; ++q)
         tmem_ld32(s_addr + q * 32, sraw + q * 32);
       tmem_ld_wait();
       float* s = reinterpret_cast<float*>(sraw);
-      float sl8 = 0.f, cbase = 0.f;  // bias of each 8 columns (kModBias)
-      if (MOD != 0) modify_tile<MOD, kTileN>(s, p, kbase, qrow, slope2, &sl8, &cbase);
+      float sl8 = 0.f, cbase = 0.f;  // bias of each 8 columns (cap and bias)
+      float base = 0.f;              // of the row (bias alone)
+      if (MOD == kModBias) {
+        // S has the tile's part already
+        base = (jt > qt ? -slope2 : slope2) *
+               static_cast<float>(kbase + kBiasMid - qrow);
+      } else if (MOD != 0) {
+        modify_tile<MOD, kTileN>(s, p, kbase, qrow, slope2, &sl8, &cbase);
+      }
       if (cls == 1) mask_tile(s, rlo - kbase, rhi - kbase, keep, KEEP);
 
       uint32_t pk[16];
       if (SCORE == BSM_SCORE_SOFTMAX) {
         float m_blk;
-        if (MOD == 0) {
+        if (MOD == 0 || MOD == kModBias) {
           // row max: three-input max, four independent chains
           float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]);
           float mx2 = fmaxf(s[4], s[5]), mx3 = fmaxf(s[6], s[7]);
@@ -1663,7 +1773,7 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
             mx3 = fmax3(mx3, s[c + 6], s[c + 7]);
           }
           const float mx = fmax3(mx0, mx1, fmaxf(mx2, mx3));
-          m_blk = mx * p.scale_log2;
+          m_blk = MOD == 0 ? mx * p.scale_log2 : fmaf(mx, p.scale_log2, base);
         } else if (MOD == kModCap) {
           m_blk = NEG_INF;  // m_used stays m_fixed
         } else {
@@ -1679,7 +1789,8 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
           l_sum *= alpha;
           m_used = m_blk;
         }
-        const float neg_m = (m_used == NEG_INF) ? 0.f : -m_used;
+        float neg_m = (m_used == NEG_INF) ? 0.f : -m_used;
+        if (MOD == kModBias) neg_m += base;
         float ls0 = 0.f, ls1 = 0.f, ls2 = 0.f, ls3 = 0.f;
 #pragma unroll
         for (int q = 0; q < kTileN / 32; ++q) {  // 32 columns at a time
@@ -1687,7 +1798,7 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
           for (int c = 32 * q; c < 32 * q + 32; c += 4) {
             // paired f32 FMA/add: the same roundings as one element at a time
             float x0, x1, x2, x3;
-            if (MOD == 0) {
+            if (MOD == 0 || MOD == kModBias) {
               ffma2(x0, x1, s[c], s[c + 1], p.scale_log2, neg_m);
               ffma2(x2, x3, s[c + 2], s[c + 3], p.scale_log2, neg_m);
             } else if (MOD == kModCap) {  // m_fixed is subtracted already
@@ -2146,6 +2257,13 @@ __global__ void __launch_bounds__(dt_threads(MOD), 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+  if (MOD == kModBias) {  // A, -A and zeros (B comes with each unit)
+    for (int i = threadIdx.x; i < kTileM * 8; i += dt_threads(MOD)) {
+      const uint32_t one = i % 8 == 4 ? 0x3f80u : i % 8 == 6 ? 0xbf80u : 0u;
+      *bias_piece(smem, i / 8, i % 8) = make_uint4(one | one << 16, one, 0u, 0u);
+    }
+    fence_proxy_async();
+  }
   if (warp == 2) {
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
@@ -2160,9 +2278,9 @@ __global__ void __launch_bounds__(dt_threads(MOD), 1)
     const int t = warp & 1;
     uint16_t* lt = lists + t * kListBufs * kMaxKvTiles;
     if (warp < 2)
-      dt_load_role<D, TRACE, SHARED>(p, &tm_q, &tm_k, &tm_v, smem, bars, lt, t);
+      dt_load_role<D, MOD, TRACE, SHARED>(p, &tm_q, &tm_k, &tm_v, smem, bars, lt, t);
     else
-      dt_mma_role<D, SCORE, TRACE>(p, smem, bars, tmem, t);
+      dt_mma_role<D, SCORE, MOD, TRACE>(p, smem, bars, lt, tmem, t);
   } else {
     // per-element keep bits only when segment ids are unsorted or an
     // arbitrary mask is given (read once; the same for every thread)
@@ -2226,7 +2344,8 @@ cudaError_t launch_dt(const FwdParams& p, const CUtensorMap& tq,
   if (e != cudaSuccess) return e;
   if (MOD != kModCap && attr.numRegs * kDtThreads < kRegsNeeded)
     return cudaErrorInvalidConfiguration;
-  constexpr int kSmem = kDtSmemBytes + (MOD != 0 ? sizeof(DtPair) : 0);
+  constexpr int kSmem = kDtSmemBytes + (MOD != 0 ? sizeof(DtPair) : 0) +
+                        (MOD == kModBias ? kDtBiasBytes : 0);
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kSmem);
   if (e != cudaSuccess) return e;
@@ -2273,14 +2392,15 @@ cudaError_t launch_score(const FwdParams& p, const CUtensorMap& tq,
   // lockstep kernel's shared K/V stream is 2-6 % faster).
   // Modified scores take it at every length: their softmax, not the tensor
   // core, sets the pace, and its turns in the lockstep kernel leave half the
-  // score warps waiting (causal S=8192, 32/8 heads: cap 50 672 us there, 623
-  // here; bias 618 and 524; both 1049 and 757).
-  const bool dt = p.dense == nullptr && p.D == 128 &&
-                  (MOD != 0 || (p.flags & BSM_MASK_SEGMENT) != 0 ||
-                   p.Skv < 4096);
+  // score warps waiting (causal S=8192, 32/8 heads, in one form of the scores:
+  // cap 50 672 us there, 623 here; bias 618 and 524; both 1049 and 757).
+  const bool dt = MOD != 0 ? p.D == 128 && fwd_mod_dt(p)
+                           : p.dense == nullptr && p.D == 128 &&
+                                 ((p.flags & BSM_MASK_SEGMENT) != 0 ||
+                                  p.Skv < 4096);
   if (dt) return launch_dt<128, SCORE, MOD>(p, tq, tk, tv, grid, num_sms, stream);
   if constexpr (MOD != 0) {  // and at head dim 64 too
-    if (p.dense == nullptr && p.D == 64)
+    if (p.D == 64 && fwd_mod_dt(p))
       return launch_dt<64, SCORE, MOD>(p, tq, tk, tv, grid, num_sms, stream);
   }
   if constexpr (MOD == 0) {

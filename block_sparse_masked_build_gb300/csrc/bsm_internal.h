@@ -107,6 +107,13 @@ struct FwdParams {
   uint32_t trace_cap;
 };
 
+// Whether a forward with modified scores takes the kernel with decoupled query
+// tiles: not with an arbitrary mask, nor, as it adds a bias alone as slope /
+// scale inside the product, with a scale that is negative or next to nothing.
+inline bool fwd_mod_dt(const FwdParams& p) {
+  return p.dense == nullptr && (p.mod.kind != kModBias || p.scale >= 0x1p-20f);
+}
+
 struct BwdParams {
   int32_t B, H, Hkv, Sq, Skv, D;
   // mask

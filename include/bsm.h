@@ -216,13 +216,16 @@ bsm_status bsm_splash_fwd(const void* q, const void* k, const void* v,
  * with q, k the row's and the key's positions and h the query head.  The mask
  * is applied after both.  These scores have no counterpart on the pages.
  *   softcap       0 (no cap) or positive, with scale / softcap finite in f32
- *   alibi_slopes  device f32 [H], contiguous, finite, of any sign, or NULL;
- *                 read by the kernels (not checked).  Constants: the backward
- *                 gives them no gradient
+ *   alibi_slopes  device f32 [H], contiguous, at most 2^64 in magnitude, of
+ *                 any sign, or NULL; read by the kernels (not checked).
+ *                 Constants: the backward gives them no gradient
  * Scores and bias are f32: a logit is off by at most about 6e-7 of its value
  * (|x| <= softcap / 2, where tanh is a polynomial) or 2^-22 of softcap (beyond,
  * and everywhere for softcap above 2^18 scale, where it is 1 - 2 / (1 + e^(2 x
- * / softcap))), and by 2^-23 of the bias. */
+ * / softcap))), and by 2^-22 of slope times the distance, or times 64 if that
+ * is more.  As without a modification, a key that a row does not see weighs 0,
+ * and 0 times an infinity or NaN in V (in the backward: in any operand) of a
+ * key tile that the row's query tile visits is NaN. */
 typedef struct bsm_score_mod {
   float softcap;
   const float* alibi_slopes;

@@ -211,6 +211,26 @@ def test_scores_beyond_f32_exponentials():
         assert torch.isfinite(g).all()
 
 
+@pytest.mark.parametrize("scale", [-0.09, 0.0, 2.0 ** -22, 2.0 ** -19, 3.0])
+@pytest.mark.parametrize("D", [64, 128])
+def test_bias_with_unusual_scales(D, scale):
+    """A bias alone is added inside the product as slope / scale, but for
+    scales that are negative or next to nothing."""
+    q, k, v, do = inputs(f"scales{D}{scale}", 1, 3, 1, 300, 333, D, 0.5)
+    for flags in (C, 0):
+        run(q, k, v, do, flags, scale=scale, slopes=slopes_of(3))
+
+
+def test_bias_of_many_heads_and_signs():
+    """Every unit brings its own head's slope: far more units than SMs, steep
+    and flat, rising and falling slopes next to one another."""
+    H = 120
+    q, k, v, do = inputs("heads", 2, H, H, 300, 300, 64, 2.0)
+    sl = slopes_of(H) * torch.where(torch.arange(H) % 3 == 0, -0.1, 3.0)
+    for flags in (C, 0):
+        run(q, k, v, do, flags, slopes=sl, bwd=False)
+
+
 def test_negative_and_zero_slopes():
     q, k, v, do = inputs("neg", 1, 2, 2, 300, 300, 128)
     run(q, k, v, do, C, slopes=torch.tensor([-0.02, 0.0]))
