@@ -1178,9 +1178,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Warp roles (384 threads, three warpgroups, registers split as above):
 // warps 0/1 take pipeline 0/1's units, build their lists and load their
 // tiles; warps 2/3 issue its MMAs (warp 2 also owns the TMEM); warps 4-7
-// and 8-11 are the score warpgroups of pipeline 0 and 1.  With a cap alone
-// each pipeline has two score warpgroups (640 threads without a register
-// split; see dt_score_cap_role).  TMEM as above: S_t/P_t at [128 t, +128),
+// and 8-11 are the score warpgroups of pipeline 0 and 1.  With a cap each
+// pipeline has two score warpgroups in most cases (640 threads without a
+// register split; see dt_score_cap_role).  TMEM as above: S_t/P_t at [128 t, +128),
 // O_t at [256 + 128 t, +D).  Head dim 128, softmax or pointwise; head dim 64
 // with modified scores only.
 constexpr int kDtThreads = 384;
@@ -1272,7 +1272,14 @@ __device__ __forceinline__ void write_bias(uint8_t* smem, int t, float ratio) {
 }
 
 // Score threads of one pipeline, and threads of the kernel.
-constexpr int dt_score_threads(int mod) { return mod == kModCap ? 256 : 128; }
+// (kModFixed: cap and bias with a fixed reference, see dt_score_cap_role.)
+constexpr int kModFixed = kModCap | kModBias | 4;
+constexpr bool dt_two_per_row(int mod) {
+  return mod == kModCap || mod == kModFixed;
+}
+constexpr int dt_score_threads(int mod) {
+  return dt_two_per_row(mod) ? 256 : 128;
+}
 constexpr int dt_threads(int mod) { return 128 + 2 * dt_score_threads(mod); }
 
 // Optional event trace, in the layout of `trace` above; the six recording
@@ -1394,7 +1401,8 @@ __device__ __forceinline__ bool dt_build_list(const FwdParams& p, DtBars* bars,
     }
     if (SHARED) n = (n + 1 - t) >> 1;  // every other entry
     __syncwarp();
-    if (MOD & kModBias) dt_order_list<MOD>(p, list, n, qt, uc.h);
+    if ((MOD & kModBias) && MOD != kModFixed)
+      dt_order_list<MOD>(p, list, n, qt, uc.h);
     if (lane == 0) {
       mt.n = n;
       mt.unit = unit;
@@ -1978,18 +1986,18 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
   }
 }
 
-// Score warps of pipeline t for capped softmax scores without a bias
-// (kModCap): eight instead of four, two threads per query row, each with one
-// 64-key half of the tile.  The arithmetic per score is about twice the
-// unmodified one's and the tensor core waits for it on every entry, so a row's
-// latency is halved.  No maximum is kept, so the threads of a row share only
-// their sums, in the epilogue; and half 1, whose P goes over columns [32, 64)
-// of S (half 0's scores), writes after half 0 has read.  Measured against one
-// thread per row (us): packed S=8192, 2 x 16 heads: cap 50 136 and 145, cap 20
-// 155 and 186; causal S=8192, 32/8 heads, cap 20: 571 and 690.  With a bias,
-// whose running maximum the two threads would have to exchange on every entry,
-// it was 1 to 7 % slower instead.
-template <int D, bool KEEP, bool TRACE, bool SHARED>
+// Score warps of pipeline t for softmax scores that a cap bounds (kModCap, and
+// kModFixed with a bias too): eight instead of four, two threads per query row,
+// each with one 64-key half of the tile.  The arithmetic per score is about
+// twice the unmodified one's and the tensor core waits for it on every entry,
+// so a row's latency is halved.  No maximum is kept, so the threads of a row
+// share only their sums, in the epilogue; and half 1, whose P goes over columns
+// [32, 64) of S (half 0's scores), writes after half 0 has read.  Measured
+// against one thread per row (us): packed S=8192, 2 x 16 heads: cap 50 136 and
+// 145, cap 20 155 and 186; causal S=8192, 32/8 heads, cap 20: 571 and 690; with
+// a bias, cap 50: 522 and 560, cap 20: 675 and 798.  What bounds cap 20 is the
+// MUFU pipe (2.5 operations per score: about 540 us at 16 a clock and SM).
+template <int D, int MOD, bool KEEP, bool TRACE, bool SHARED>
 __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
                                                   DtBars* bars, DtPair* pair,
                                                   float* merge,
@@ -2044,10 +2052,20 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
     const int32_t* segk_b =
         seg_elem ? p.kv_seg + static_cast<int64_t>(uc.b) * p.Skv : nullptr;
     // the cap bounds the logits to +-cap_log2: no maximum is kept, p is
-    // 2^(x - m_fixed) with m_fixed = max(0, cap_log2 - 52), so p lies within
+    // 2^(x - ref) with ref = m_fixed = max(0, cap_log2 - 52), so p lies within
     // 2^-121 .. 2^52 for the caps that take this path (cap_log2 <= 87) and
-    // sums of 2^18 of them stay far inside f32
-    float l_sum = 0.f;
+    // sums of 2^18 of them stay far inside f32.  With a bias the key of the
+    // row's interval where it is least bounds them too: ref is lowered by its
+    // bias, that key has a p of 2^-98 at least (cap_log2 <= 75), and what is
+    // flushed to 0, below 2^-126, weighs 2^-28 of it.
+    float ref = p.mod.m_fixed, l_sum = 0.f;
+    float slope2 = 0.f;
+    if (MOD == kModFixed) {
+      slope2 = p.mod.slopes[uc.h] * 1.4426950408889634f;
+      const int near = max(max(qrow - rhi, rlo - qrow), 0);
+      const int far = max(qrow - rlo, rhi - qrow);
+      ref -= slope2 * static_cast<float>(slope2 >= 0.f ? near : far);
+    }
     uint32_t unit_pv = 0;
     bool ok = true;
     for (int e = 0; e < n_ent; ++e) {
@@ -2077,8 +2095,8 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
         tc_fence_before();
         mbar_arrive(meet);
       }
-      float unused;
-      modify_tile<kModCap, NC>(s, p, kbase, qrow, 0.f, &unused, &unused);
+      float sl8, cbase;  // bias of each 8 columns
+      modify_tile<MOD, NC>(s, p, kbase, qrow, slope2, &sl8, &cbase);
       if (cls == 1) mask_tile<NC>(s, rlo - kbase, rhi - kbase, keep, KEEP);
 
       float ls0 = 0.f, ls1 = 0.f, ls2 = 0.f, ls3 = 0.f;
@@ -2087,6 +2105,12 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
         uint32_t pk[16];
 #pragma unroll
         for (int c = 32 * q; c < 32 * q + 32; c += 4) {
+          if (MOD == kModFixed) {
+            const float add =
+                fmaf(sl8, static_cast<float>(c / 8), cbase - ref);
+            fadd2(s[c], s[c + 1], s[c], s[c + 1], add, add);
+            fadd2(s[c + 2], s[c + 3], s[c + 2], s[c + 3], add, add);
+          }
           const float p0 = ex2_approx(s[c]), p1 = ex2_approx(s[c + 1]);
           const float p2 = ex2_approx(s[c + 2]), p3 = ex2_approx(s[c + 3]);
           fadd2(ls0, ls1, ls0, ls1, p0, p1);
@@ -2202,7 +2226,7 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
     }
     if (hf == 0 && p.lse != nullptr && row_ok) {
       const float lse = l_sum > 0.f
-                            ? (p.mod.m_fixed + log2f(l_sum)) * 0.6931471805599453f
+                            ? (ref + log2f(l_sum)) * 0.6931471805599453f
                             : NEG_INF;
       p.lse[(static_cast<int64_t>(uc.b) * p.H + uc.h) * p.Sq + qrow] = lse;
     }
@@ -2274,7 +2298,7 @@ __global__ void __launch_bounds__(dt_threads(MOD), 1)
   const uint32_t tmem = bars->tmem_base;
 
   if (warp < 4) {
-    if (MOD != kModCap) setmaxnreg_dec<kRegsLight>();
+    if (!dt_two_per_row(MOD)) setmaxnreg_dec<kRegsLight>();
     const int t = warp & 1;
     uint16_t* lt = lists + t * kListBufs * kMaxKvTiles;
     if (warp < 2)
@@ -2286,7 +2310,7 @@ __global__ void __launch_bounds__(dt_threads(MOD), 1)
     // arbitrary mask is given (read once; the same for every thread)
     DtPair* pair = reinterpret_cast<DtPair*>(smem + kDtOffPair);
     float* merge = reinterpret_cast<float*>(smem + kDtOffMerge);
-    if constexpr (MOD != kModCap) {
+    if constexpr (!dt_two_per_row(MOD)) {
       setmaxnreg_inc<kRegsScore>();
       const int t = (warp - 4) / 4;
       const uint16_t* lt = lists + t * kListBufs * kMaxKvTiles;
@@ -2300,13 +2324,19 @@ __global__ void __launch_bounds__(dt_threads(MOD), 1)
     } else {
       const int t = (warp - 4) / 8, hf = (warp - 4) / 4 & 1;
       const uint16_t* lt = lists + t * kListBufs * kMaxKvTiles;
-      // (an arbitrary mask with modified scores takes the lockstep kernel)
-      if ((p.flags & BSM_MASK_SEGMENT) && (*p.seg_flags & 1) != 0)
-        dt_score_cap_role<D, true, TRACE, SHARED>(p, bars, pair, merge, lt,
-                                                  tmem, t, hf);
-      else
-        dt_score_cap_role<D, false, TRACE, SHARED>(p, bars, pair, merge, lt,
-                                                   tmem, t, hf);
+      // (an arbitrary mask with modified scores takes the lockstep kernel, and
+      // kModFixed no segment ids)
+      bool keep = false;
+      if constexpr (MOD == kModCap)
+        keep = (p.flags & BSM_MASK_SEGMENT) && (*p.seg_flags & 1) != 0;
+      if constexpr (MOD == kModCap) {
+        if (keep)
+          dt_score_cap_role<D, MOD, true, TRACE, SHARED>(p, bars, pair, merge,
+                                                         lt, tmem, t, hf);
+      }
+      if (!keep)
+        dt_score_cap_role<D, MOD, false, TRACE, SHARED>(p, bars, pair, merge,
+                                                        lt, tmem, t, hf);
     }
   }
 
@@ -2342,7 +2372,7 @@ cudaError_t launch_dt(const FwdParams& p, const CUtensorMap& tq,
   cudaFuncAttributes attr;
   cudaError_t e = cudaFuncGetAttributes(&attr, kern);
   if (e != cudaSuccess) return e;
-  if (MOD != kModCap && attr.numRegs * kDtThreads < kRegsNeeded)
+  if (!dt_two_per_row(MOD) && attr.numRegs * kDtThreads < kRegsNeeded)
     return cudaErrorInvalidConfiguration;
   constexpr int kSmem = kDtSmemBytes + (MOD != 0 ? sizeof(DtPair) : 0) +
                         (MOD == kModBias ? kDtBiasBytes : 0);
@@ -2394,6 +2424,7 @@ cudaError_t launch_score(const FwdParams& p, const CUtensorMap& tq,
   // core, sets the pace, and its turns in the lockstep kernel leave half the
   // score warps waiting (causal S=8192, 32/8 heads, in one form of the scores:
   // cap 50 672 us there, 623 here; bias 618 and 524; both 1049 and 757).
+  // (kModFixed, which only that kernel has, does not come here.)
   const bool dt = MOD != 0 ? p.D == 128 && fwd_mod_dt(p)
                            : p.dense == nullptr && p.D == 128 &&
                                  ((p.flags & BSM_MASK_SEGMENT) != 0 ||
@@ -2447,6 +2478,15 @@ cudaError_t launch_splash_fwd(const FwdParams& p, const CUtensorMap& tq,
   const int kind = p.mod.kind == kModCap && p.mod.cap_log2 > 87.f
                        ? kModCap | kModBias
                        : p.mod.kind;
+  // cap and bias with a fixed reference: the row's visible keys must be an
+  // interval (segment ids may be unsorted), and the cap at most 75 in log2
+  if (kind == (kModCap | kModBias) && p.mod.slopes != nullptr &&
+      p.mod.cap_log2 <= 75.f && fwd_mod_dt(p) &&
+      (p.flags & BSM_MASK_SEGMENT) == 0)
+    return p.D == 128 ? launch_dt<128, BSM_SCORE_SOFTMAX, kModFixed>(
+                            p, tq, tk, tv, grid, num_sms, stream)
+                      : launch_dt<64, BSM_SCORE_SOFTMAX, kModFixed>(
+                            p, tq, tk, tv, grid, num_sms, stream);
   switch (kind) {
     case 0:
       return launch_score<BSM_SCORE_SOFTMAX, 0>(p, tq, tk, tv, grid, num_sms, stream);

@@ -211,6 +211,21 @@ def test_scores_beyond_f32_exponentials():
         assert torch.isfinite(g).all()
 
 
+@pytest.mark.parametrize("cap", [0.5, 20.0, 51.0, 53.0, 61.0, 200.0])
+@pytest.mark.parametrize("kind", ["causal", "full", "far", "band"])
+def test_references_of_cap_and_bias(kind, cap):
+    """Small caps take the row's largest bias for the softmax's reference,
+    larger ones a running maximum: saturated scores, slopes of both signs,
+    rows whose nearest key is far away or that see none."""
+    Sq, Skv = (700, 200) if kind == "far" else (330, 330)
+    flags = {"causal": C, "band": L | BD}.get(kind, 0)
+    H = 6
+    q, k, v, do = inputs(f"ref{kind}{cap}", 1, H, H, Sq, Skv, 64, 6.0)
+    sl = torch.tensor([0.004, 0.3, 2.0, -0.004, -0.02, 0.0])
+    run(q, k, v, do, flags, 90 if kind == "band" else 0, softcap=cap,
+        slopes=sl, scale=1.0 if cap < 1 else None, bwd=False)
+
+
 @pytest.mark.parametrize("scale", [-0.09, 0.0, 2.0 ** -22, 2.0 ** -19, 3.0])
 @pytest.mark.parametrize("D", [64, 128])
 def test_bias_with_unusual_scales(D, scale):
