@@ -1237,9 +1237,10 @@ static_assert(kDtSmemBytes + sizeof(DtPair) <= 232448, "shared memory budget");
 // three bf16 parts of slope / scale * (c - 64), whose sum is the f32 value.
 // What is left of the bias is one number per row and tile, which goes into the
 // softmax's reference.  (With the bias added by the score warps, one paired
-// addition per two scores more, causal S=8192, 32/8 heads took 470 us; so 425,
-// and 418 without a bias.)  One 128 x 64 tile (128-byte swizzle) holds it all: columns [0, 16)
-// and [16, 32) B of the pipelines, [32, 48) and [48, 64) A and -A.
+// addition per two scores more, causal S=8192, 32/8 heads took 527 us; so 466,
+// key tiles in rising order both times; see dt_order_list.)  One 128 x 64 tile
+// (128-byte swizzle) holds it all: columns [0, 16) and [16, 32) B of the
+// pipelines, [32, 48) and [48, 64) A and -A.
 constexpr int kDtOffBias = kDtOffPair + sizeof(DtPair);
 constexpr int kDtBiasBytes = kTileM * 128;
 static_assert(kDtOffBias % 1024 == 0, "swizzle atom");
@@ -1315,8 +1316,8 @@ __device__ __forceinline__ void dt_trace(const FwdParams& p, DtBars* bars,
 // query tile's own, those left of it from near to far, those right of it from
 // near to far.  The first then sets the softmax's reference for good; in
 // rising order a steep head's moves, and O is rescaled, on every entry (us,
-// rising order and this one: causal S=8192, 32/8 heads: 504 and 441, with a cap
-// 630 and 549).  Whole warp.
+// rising order and this one: causal S=8192, 32/8 heads: 466 and 425, with a cap
+// and a running maximum 630 and 560).  Whole warp.
 template <int MOD>
 __device__ __forceinline__ void dt_order_list(const FwdParams& p,
                                               uint16_t* list, int n, int qt,
