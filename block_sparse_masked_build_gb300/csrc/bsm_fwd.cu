@@ -1995,8 +1995,8 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
 // share only their sums, in the epilogue; and half 1, whose P goes over columns
 // [32, 64) of S (half 0's scores), writes after half 0 has read.  Measured
 // against one thread per row (us): packed S=8192, 2 x 16 heads: cap 50 136 and
-// 145, cap 20 155 and 186; causal S=8192, 32/8 heads, cap 20: 571 and 690; with
-// a bias, cap 50: 522 and 560, cap 20: 675 and 798.  What bounds cap 20 is the
+// 145, cap 20 155 and 186, both with a bias 143 and 172, 168 and 211; causal
+// S=8192, 32/8 heads, cap 20: 571 and 690, with a bias 675 and 798.  What bounds cap 20 is the
 // MUFU pipe (2.5 operations per score: about 540 us at 16 a clock and SM).
 template <int D, int MOD, bool KEEP, bool TRACE, bool SHARED>
 __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
@@ -2065,7 +2065,16 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
       slope2 = p.mod.slopes[uc.h] * 1.4426950408889634f;
       const int near = max(max(qrow - rhi, rlo - qrow), 0);
       const int far = max(qrow - rlo, rhi - qrow);
-      ref -= slope2 * static_cast<float>(slope2 >= 0.f ? near : far);
+      int d = slope2 >= 0.f ? near : far;
+      if (KEEP && row_ok && rlo <= rhi) {
+        // unsorted ids: the first key of the row's segment from there on
+        const int end = slope2 >= 0.f ? far : near, step = d < end ? 1 : -1;
+        auto sees = [&](int k) {
+          return k >= rlo && k <= rhi && segk_b[k] == segq;
+        };
+        while (d != end && !sees(qrow - d) && !sees(qrow + d)) d += step;
+      }
+      ref -= slope2 * static_cast<float>(d);
     }
     uint32_t unit_pv = 0;
     bool ok = true;
@@ -2325,17 +2334,11 @@ __global__ void __launch_bounds__(dt_threads(MOD), 1)
     } else {
       const int t = (warp - 4) / 8, hf = (warp - 4) / 4 & 1;
       const uint16_t* lt = lists + t * kListBufs * kMaxKvTiles;
-      // (an arbitrary mask with modified scores takes the lockstep kernel, and
-      // kModFixed no segment ids)
-      bool keep = false;
-      if constexpr (MOD == kModCap)
-        keep = (p.flags & BSM_MASK_SEGMENT) && (*p.seg_flags & 1) != 0;
-      if constexpr (MOD == kModCap) {
-        if (keep)
-          dt_score_cap_role<D, MOD, true, TRACE, SHARED>(p, bars, pair, merge,
-                                                         lt, tmem, t, hf);
-      }
-      if (!keep)
+      // (an arbitrary mask with modified scores takes the lockstep kernel)
+      if ((p.flags & BSM_MASK_SEGMENT) && (*p.seg_flags & 1) != 0)
+        dt_score_cap_role<D, MOD, true, TRACE, SHARED>(p, bars, pair, merge,
+                                                       lt, tmem, t, hf);
+      else
         dt_score_cap_role<D, MOD, false, TRACE, SHARED>(p, bars, pair, merge,
                                                         lt, tmem, t, hf);
     }
@@ -2479,11 +2482,9 @@ cudaError_t launch_splash_fwd(const FwdParams& p, const CUtensorMap& tq,
   const int kind = p.mod.kind == kModCap && p.mod.cap_log2 > 87.f
                        ? kModCap | kModBias
                        : p.mod.kind;
-  // cap and bias with a fixed reference: the row's visible keys must be an
-  // interval (segment ids may be unsorted), and the cap at most 75 in log2
+  // cap and bias with a fixed reference: the cap at most 75 in log2
   if (kind == (kModCap | kModBias) && p.mod.slopes != nullptr &&
-      p.mod.cap_log2 <= 75.f && fwd_mod_dt(p) &&
-      (p.flags & BSM_MASK_SEGMENT) == 0)
+      p.mod.cap_log2 <= 75.f && fwd_mod_dt(p))
     return p.D == 128 ? launch_dt<128, BSM_SCORE_SOFTMAX, kModFixed>(
                             p, tq, tk, tv, grid, num_sms, stream)
                       : launch_dt<64, BSM_SCORE_SOFTMAX, kModFixed>(

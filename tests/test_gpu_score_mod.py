@@ -226,6 +226,24 @@ def test_references_of_cap_and_bias(kind, cap):
         slopes=sl, scale=1.0 if cap < 1 else None, bwd=False)
 
 
+@pytest.mark.parametrize("sign", [1.0, -0.02])
+@pytest.mark.parametrize("flags", [SG, C | SG])
+def test_references_with_unsorted_segments(flags, sign):
+    """Rows whose nearest (farthest) key of their segment is not the nearest
+    (farthest) of the mask's interval, and rows whose id no key has."""
+    S, H = 400, 3
+    q, k, v, do = inputs(f"refseg{flags}{sign}", 2, H, H, S, S, 64, 4.0)
+    ids = np.zeros((2, S), np.int32)
+    ids[:, 300:] = 1      # far from the rows that look for 0
+    ids[1] = np.random.default_rng(5).integers(0, 4, S)
+    ids[1, :40] = 9
+    rows = ids.copy()
+    rows[:, 350:] = 0
+    rows[:, 380:] = 7     # no key has it
+    run(q, k, v, do, flags, 0, rows, ids, softcap=30.0,
+        slopes=sign * torch.tensor([0.01, 1.0, 4.0]), bwd=False)
+
+
 @pytest.mark.parametrize("scale", [-0.09, 0.0, 2.0 ** -22, 2.0 ** -19, 3.0])
 @pytest.mark.parametrize("D", [64, 128])
 def test_bias_with_unusual_scales(D, scale):
