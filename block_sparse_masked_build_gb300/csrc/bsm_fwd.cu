@@ -1996,8 +1996,9 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
 // [32, 64) of S (half 0's scores), writes after half 0 has read.  Measured
 // against one thread per row (us): packed S=8192, 2 x 16 heads: cap 50 136 and
 // 145, cap 20 155 and 186, both with a bias 143 and 172, 168 and 211; causal
-// S=8192, 32/8 heads, cap 20: 571 and 690, with a bias 675 and 798.  What bounds cap 20 is the
-// MUFU pipe (2.5 operations per score: about 540 us at 16 a clock and SM).
+// S=8192, 32/8 heads, cap 20: 571 and 690, with a bias 675 and 798.  What
+// bounds cap 20 is the MUFU pipe (2.5 operations per score: about 540 us at 16
+// a clock and SM).
 template <int D, int MOD, bool KEEP, bool TRACE, bool SHARED>
 __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
                                                   DtBars* bars, DtPair* pair,
