@@ -1402,8 +1402,7 @@ __device__ __forceinline__ bool dt_build_list(const FwdParams& p, DtBars* bars,
     }
     if (SHARED) n = (n + 1 - t) >> 1;  // every other entry
     __syncwarp();
-    if ((MOD & kModBias) && MOD != kModFixed)
-      dt_order_list<MOD>(p, list, n, qt, uc.h);
+    if (MOD & kModBias) dt_order_list<MOD>(p, list, n, qt, uc.h);
     if (lane == 0) {
       mt.n = n;
       mt.unit = unit;
@@ -1991,12 +1990,13 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
 // kModFixed with a bias too): eight instead of four, two threads per query row,
 // each with one 64-key half of the tile.  The arithmetic per score is about
 // twice the unmodified one's and the tensor core waits for it on every entry,
-// so a row's latency is halved.  No maximum is kept, so the threads of a row
-// share only their sums, in the epilogue; and half 1, whose P goes over columns
+// so a row's latency is halved.  No running maximum is kept, so the threads of a
+// row share only their sums, in the epilogue (and with a bias the maximum of the
+// unit's first tile); and half 1, whose P goes over columns
 // [32, 64) of S (half 0's scores), writes after half 0 has read.  Measured
 // against one thread per row (us): packed S=8192, 2 x 16 heads: cap 50 136 and
-// 145, cap 20 155 and 186, both with a bias 143 and 172, 168 and 211; causal
-// S=8192, 32/8 heads, cap 20: 571 and 690, with a bias 675 and 798.  What
+// 145, cap 20 155 and 186, both with a bias 153 and 172, 175 and 211; causal
+// S=8192, 32/8 heads, cap 20: 571 and 690, with a bias 666 and 798.  What
 // bounds cap 20 is the MUFU pipe (2.5 operations per score: about 540 us at 16
 // a clock and SM).
 template <int D, int MOD, bool KEEP, bool TRACE, bool SHARED>
@@ -2056,10 +2056,15 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
     // the cap bounds the logits to +-cap_log2: no maximum is kept, p is
     // 2^(x - ref) with ref = m_fixed = max(0, cap_log2 - 52), so p lies within
     // 2^-121 .. 2^52 for the caps that take this path (cap_log2 <= 87) and
-    // sums of 2^18 of them stay far inside f32.  With a bias the key of the
-    // row's interval where it is least bounds them too: ref is lowered by its
-    // bias, that key has a p of 2^-98 at least (cap_log2 <= 75), and what is
-    // flushed to 0, below 2^-126, weighs 2^-28 of it.
+    // sums of 2^18 of them stay far inside f32.  With a bias the logits of a row
+    // lie within +-cap_log2 of its largest bias, that of its nearest key
+    // (farthest, for a negative slope).  ref is the maximum of the unit's first
+    // tile, where that key is, so that a key that outweighs all others has
+    // p = 1 as with a running maximum (with m_fixed its rounding to bf16 took
+    // the gradients' error from 3.3e-3 to 4.4e-3 on steep slopes); but at least
+    // 90 below the upper bound, so p lies below 2^90 and the row's largest
+    // above 2^-60 (cap_log2 <= 75): what is flushed to 0, below 2^-126, weighs
+    // 2^-66 of it.
     float ref = p.mod.m_fixed, l_sum = 0.f;
     float slope2 = 0.f;
     if (MOD == kModFixed) {
@@ -2075,7 +2080,7 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
         };
         while (d != end && !sees(qrow - d) && !sees(qrow + d)) d += step;
       }
-      ref -= slope2 * static_cast<float>(d);
+      ref = p.mod.cap_log2 - 90.f - slope2 * static_cast<float>(d);
     }
     uint32_t unit_pv = 0;
     bool ok = true;
@@ -2110,6 +2115,19 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
       modify_tile<MOD, NC>(s, p, kbase, qrow, slope2, &sl8, &cbase);
       if (cls == 1) mask_tile<NC>(s, rlo - kbase, rhi - kbase, keep, KEEP);
 
+      if (MOD == kModFixed && unit_pv == 0) {  // the two halves' maxima
+        pair->sum[sums & 1][t][hf][r] = biased_max<NC>(s, sl8, cbase);
+        mbar_arrive(&bars->meet_sum[t][quarter]);
+        ok = warp_wait(&bars->meet_sum[t][quarter], sums & 1, abort_flag,
+                       p.timeout_ns);
+        if (!ok) {
+          record_timeout(kRoleScore, 9);
+          break;
+        }
+        ref = fmax3(ref, pair->sum[sums & 1][t][0][r],
+                    pair->sum[sums & 1][t][1][r]);
+        ++sums;
+      }
       float ls0 = 0.f, ls1 = 0.f, ls2 = 0.f, ls3 = 0.f;
 #pragma unroll
       for (int q = 0; q < NC / 32; ++q) {  // 32 columns at a time
@@ -2180,11 +2198,12 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
       mbar_arrive(&bars->o_free[t]);
       if (SHARED) {
         float* at = merge + hf * (D / 2) * kTileM + r;
-        if (t == 1) {  // O and sum for pipeline 0 (the reference is the same)
+        if (t == 1) {  // O, sum and reference for pipeline 0
 #pragma unroll
           for (int c = 0; c < D / 2; ++c)
             at[c * kTileM] = __uint_as_float(o[c]);
           if (hf == 0) pair->total[r] = l_sum;
+          if (MOD == kModFixed && hf == 0) pair->ref[r] = ref;
           mbar_arrive(&bars->merge);
           mbar_arrive(&bars->list_free[t][buf]);
           continue;
@@ -2195,10 +2214,18 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
         }
         const float l1 = pair->total[r];
         if (!(l1 == 0.f)) {  // (0: it saw nothing, or had no entry)
+          float w0 = 1.f, w1 = 1.f;
+          if (MOD == kModFixed) {
+            const float mm = fmaxf(ref, pair->ref[r]);
+            w0 = ex2_approx(ref - mm);
+            w1 = ex2_approx(pair->ref[r] - mm);
+            ref = mm;
+          }
 #pragma unroll
           for (int c = 0; c < D / 2; ++c)
-            o[c] = __float_as_uint(__uint_as_float(o[c]) + at[c * kTileM]);
-          l_sum += l1;
+            o[c] = __float_as_uint(
+                fmaf(at[c * kTileM], w1, __uint_as_float(o[c]) * w0));
+          l_sum = fmaf(l1, w1, l_sum * w0);
         }
       }
       const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
@@ -2483,7 +2510,7 @@ cudaError_t launch_splash_fwd(const FwdParams& p, const CUtensorMap& tq,
   const int kind = p.mod.kind == kModCap && p.mod.cap_log2 > 87.f
                        ? kModCap | kModBias
                        : p.mod.kind;
-  // cap and bias with a fixed reference: the cap at most 75 in log2
+  // cap and bias with a fixed reference (see dt_score_cap_role)
   if (kind == (kModCap | kModBias) && p.mod.slopes != nullptr &&
       p.mod.cap_log2 <= 75.f && fwd_mod_dt(p))
     return p.D == 128 ? launch_dt<128, BSM_SCORE_SOFTMAX, kModFixed>(
