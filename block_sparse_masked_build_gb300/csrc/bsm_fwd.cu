@@ -684,11 +684,12 @@ __device__ __forceinline__ void cap_tile(float* s, const float* c,
 // caller adds sl 8 (c / 8) + *base per 8 columns.  A tile with columns on both
 // sides that no causal mask cuts takes the bias whole, column by column.
 //
-// kModCap alone: s also has m_fixed subtracted.
+// kModCap alone: neg_m is added to s.
 template <int MOD, int NC>
 __device__ __forceinline__ void modify_tile(float* s, const FwdParams& p,
                                             int kbase, int qrow, float slope2,
-                                            float* sl_out, float* base_out) {
+                                            float* sl_out, float* base_out,
+                                            float neg_m = 0.f) {
   float pc[8];  // bias of columns 0-7 of a chunk
   bool split = false;
   if (MOD & kModBias) {
@@ -713,7 +714,7 @@ __device__ __forceinline__ void modify_tile(float* s, const FwdParams& p,
       a3 = fmax3_abs(a3, s[c + 6], s[c + 7]);
     }
     const float top = fmaxf(fmax3(a0, a1, a2), a3);
-    const float neg_m = MOD == kModCap ? -p.mod.m_fixed : 0.f;
+    if (MOD != kModCap) neg_m = 0.f;
     if (__all_sync(0xffffffffu, top <= p.mod.poly_max)) {
       cap_tile<MOD, NC, 4>(s, p.mod.poly, pc, neg_m);
     } else {
@@ -888,7 +889,9 @@ __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
       tmem_ld_wait();
       float* s = reinterpret_cast<float*>(sraw);
       float sl8 = 0.f, cbase = 0.f;  // bias of each 8 columns (kModBias)
-      if (MOD != 0) modify_tile<MOD, kTileN>(s, p, kbase, qrow, slope2, &sl8, &cbase);
+      if (MOD != 0)
+        modify_tile<MOD, kTileN>(s, p, kbase, qrow, slope2, &sl8, &cbase,
+                                 -p.mod.m_fixed);
       if (cls == 1) mask_tile(s, rlo - kbase, rhi - kbase, keep, KEEP);
 
       uint32_t pk[16];
@@ -1994,11 +1997,11 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
 // row share only their sums, in the epilogue (and with a bias the maximum of the
 // unit's first tile); and half 1, whose P goes over columns
 // [32, 64) of S (half 0's scores), writes after half 0 has read.  Measured
-// against one thread per row (us): packed S=8192, 2 x 16 heads: cap 50 136 and
-// 145, cap 20 155 and 186, both with a bias 153 and 172, 175 and 211; causal
-// S=8192, 32/8 heads, cap 20: 571 and 690, with a bias 666 and 798.  What
-// bounds cap 20 is the MUFU pipe (2.5 operations per score: about 540 us at 16
-// a clock and SM).
+// (us): packed S=8192, 2 x 16 heads: cap 50 148, cap 20 167, with a bias 153 and
+// 175 (one thread per row and a running maximum: 172 and 211); causal S=8192,
+// 32/8 heads: cap 50 504, with a bias 518 (560).  A constant reference would be
+// 6 to 12 % faster with a cap alone, but see ref.  What bounds cap 20 is the
+// MUFU pipe (2.5 operations per score: about 540 us at 16 a clock and SM).
 template <int D, int MOD, bool KEEP, bool TRACE, bool SHARED>
 __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
                                                   DtBars* bars, DtPair* pair,
@@ -2053,19 +2056,17 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
     }
     const int32_t* segk_b =
         seg_elem ? p.kv_seg + static_cast<int64_t>(uc.b) * p.Skv : nullptr;
-    // the cap bounds the logits to +-cap_log2: no maximum is kept, p is
-    // 2^(x - ref) with ref = m_fixed = max(0, cap_log2 - 52), so p lies within
-    // 2^-121 .. 2^52 for the caps that take this path (cap_log2 <= 87) and
-    // sums of 2^18 of them stay far inside f32.  With a bias the logits of a row
-    // lie within +-cap_log2 of its largest bias, that of its nearest key
-    // (farthest, for a negative slope).  ref is the maximum of the unit's first
-    // tile, where that key is, so that a key that outweighs all others has
-    // p = 1 as with a running maximum (with m_fixed its rounding to bf16 took
-    // the gradients' error from 3.3e-3 to 4.4e-3 on steep slopes); but at least
-    // 90 below the upper bound, so p lies below 2^90 and the row's largest
-    // above 2^-60 (cap_log2 <= 75): what is flushed to 0, below 2^-126, weighs
-    // 2^-66 of it.
-    float ref = p.mod.m_fixed, l_sum = 0.f;
+    // No running maximum: the cap bounds the logits to +-cap_log2, with a bias
+    // around the row's largest bias, that of its nearest key (farthest, for a
+    // negative slope).  The reference is the maximum of the unit's first tile
+    // (with a bias the one next to the row), so that a key that outweighs all
+    // others there has p = 1 as with a running maximum; with a constant its
+    // rounding to bf16 reached the gradients (4.4e-3 in norm instead of 3.3e-3
+    // on short rows).  But it is at least 90 below the upper bound, so p lies
+    // below 2^90, where 2^18 of them stay inside f32, and the row's largest
+    // above 2^-84 (cap_log2 <= 87; 75 with a bias): what is flushed to 0, below
+    // 2^-126, weighs 2^-42 of it.
+    float ref = p.mod.cap_log2 - 90.f, l_sum = 0.f;
     float slope2 = 0.f;
     if (MOD == kModFixed) {
       slope2 = p.mod.slopes[uc.h] * 1.4426950408889634f;
@@ -2080,7 +2081,7 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
         };
         while (d != end && !sees(qrow - d) && !sees(qrow + d)) d += step;
       }
-      ref = p.mod.cap_log2 - 90.f - slope2 * static_cast<float>(d);
+      ref -= slope2 * static_cast<float>(d);
     }
     uint32_t unit_pv = 0;
     bool ok = true;
@@ -2113,9 +2114,10 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
       }
       float sl8, cbase;  // bias of each 8 columns
       modify_tile<MOD, NC>(s, p, kbase, qrow, slope2, &sl8, &cbase);
+      if (MOD == kModCap) sl8 = cbase = 0.f;
       if (cls == 1) mask_tile<NC>(s, rlo - kbase, rhi - kbase, keep, KEEP);
 
-      if (MOD == kModFixed && unit_pv == 0) {  // the two halves' maxima
+      if (unit_pv == 0) {  // the two halves' maxima
         pair->sum[sums & 1][t][hf][r] = biased_max<NC>(s, sl8, cbase);
         mbar_arrive(&bars->meet_sum[t][quarter]);
         ok = warp_wait(&bars->meet_sum[t][quarter], sums & 1, abort_flag,
@@ -2134,12 +2136,9 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
         uint32_t pk[16];
 #pragma unroll
         for (int c = 32 * q; c < 32 * q + 32; c += 4) {
-          if (MOD == kModFixed) {
-            const float add =
-                fmaf(sl8, static_cast<float>(c / 8), cbase - ref);
-            fadd2(s[c], s[c + 1], s[c], s[c + 1], add, add);
-            fadd2(s[c + 2], s[c + 3], s[c + 2], s[c + 3], add, add);
-          }
+          const float add = fmaf(sl8, static_cast<float>(c / 8), cbase - ref);
+          fadd2(s[c], s[c + 1], s[c], s[c + 1], add, add);
+          fadd2(s[c + 2], s[c + 3], s[c + 2], s[c + 3], add, add);
           const float p0 = ex2_approx(s[c]), p1 = ex2_approx(s[c + 1]);
           const float p2 = ex2_approx(s[c + 2]), p3 = ex2_approx(s[c + 3]);
           fadd2(ls0, ls1, ls0, ls1, p0, p1);
@@ -2203,7 +2202,7 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
           for (int c = 0; c < D / 2; ++c)
             at[c * kTileM] = __uint_as_float(o[c]);
           if (hf == 0) pair->total[r] = l_sum;
-          if (MOD == kModFixed && hf == 0) pair->ref[r] = ref;
+          if (hf == 0) pair->ref[r] = ref;
           mbar_arrive(&bars->merge);
           mbar_arrive(&bars->list_free[t][buf]);
           continue;
@@ -2214,13 +2213,10 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
         }
         const float l1 = pair->total[r];
         if (!(l1 == 0.f)) {  // (0: it saw nothing, or had no entry)
-          float w0 = 1.f, w1 = 1.f;
-          if (MOD == kModFixed) {
-            const float mm = fmaxf(ref, pair->ref[r]);
-            w0 = ex2_approx(ref - mm);
-            w1 = ex2_approx(pair->ref[r] - mm);
-            ref = mm;
-          }
+          const float mm = fmaxf(ref, pair->ref[r]);
+          const float w0 = ex2_approx(ref - mm);
+          const float w1 = ex2_approx(pair->ref[r] - mm);
+          ref = mm;
 #pragma unroll
           for (int c = 0; c < D / 2; ++c)
             o[c] = __float_as_uint(
