@@ -43,6 +43,7 @@
 // compared element by element and an arbitrary mask contributes its bits
 // (both as per-column keep bits).  Key indices are the tile's true KV
 // position.
+#include <cmath>
 #include <cstdint>
 
 #include "bsm_internal.h"
@@ -621,12 +622,11 @@ __device__ __forceinline__ void segment_bits(uint32_t keep[4],
 // one bit word from the two bounds; a chunk that all 32 rows of the warp see
 // whole (a warp-uniform test) is left alone, the others cost one bit test
 // and one select per column.  Under causal and packed-segment masks most
-// chunks of a partial tile are whole for the warp.
+// chunks of a partial tile are whole for the warp.  (fill: instead of -inf.)
 template <int NC = kTileN>
-__device__ __forceinline__ void mask_tile(float* s, int lo_c, int hi_c,
-                                          const uint32_t* keep,
-                                          bool use_keep) {
-  const float NEG_INF = __int_as_float(0xff800000);
+__device__ __forceinline__ void mask_tile(
+    float* s, int lo_c, int hi_c, const uint32_t* keep, bool use_keep,
+    float fill = -INFINITY) {
 #pragma unroll
   for (int q = 0; q < NC / 32; ++q) {
     const int c0 = 32 * q;
@@ -639,7 +639,7 @@ __device__ __forceinline__ void mask_tile(float* s, int lo_c, int hi_c,
     if (!__all_sync(0xffffffffu, vm == 0xffffffffu)) {
 #pragma unroll
       for (int c = 0; c < 32; ++c)
-        s[c0 + c] = (vm & (1u << c)) ? s[c0 + c] : NEG_INF;
+        s[c0 + c] = (vm & (1u << c)) ? s[c0 + c] : fill;
     }
   }
 }
@@ -670,7 +670,11 @@ __device__ __forceinline__ void cap_tile(float* s, const float* c,
 // value; no MUFU operation.  (The backward's second polynomial, of degree 13,
 // was no faster here than the exponential.)  Else 1 - 2 / (1 + e^(2 y)), one reciprocal for two
 // columns, to a few 2^-23 of the cap; e^(2 y) is cut at 2^60, where tanh is 1
-// in f32, so that the product of two stays in range.  NaN stays NaN in both.
+// in f32, so that the product of two stays in range.  NaN stays NaN in both, and
+// would reach the neighbour through the reciprocal they share: where the warp
+// holds a NaN, the columns that a row of a partial tile does not see, whose
+// score may be anything, are set to 0 before (a NaN that a row sees makes the
+// whole row NaN in any case).
 // (tanh.approx is off by up to 2^-11 of its value, which the logsumexp would
 // show.)  What bounds it: the f32 pipe and the latency of the softmax, which
 // the tensor core waits for.  Measured on packed S=8192, 2 x 16 heads, against
@@ -685,10 +689,16 @@ __device__ __forceinline__ void cap_tile(float* s, const float* c,
 // sides that no causal mask cuts takes the bias whole, column by column.
 //
 // kModCap alone: neg_m is added to s.
+//
+// partial, lo_c, hi_c, keep, use_keep: the row's visible columns, as mask_tile
+// takes them, if the tile is partial.
 template <int MOD, int NC>
 __device__ __forceinline__ void modify_tile(float* s, const FwdParams& p,
-                                            int kbase, int qrow, float slope2,
-                                            float* sl_out, float* base_out,
+                                            int kbase, int qrow, bool partial,
+                                            int lo_c, int hi_c,
+                                            const uint32_t* keep, bool use_keep,
+                                            float slope2, float* sl_out,
+                                            float* base_out,
                                             float neg_m = 0.f) {
   float pc[8];  // bias of columns 0-7 of a chunk
   bool split = false;
@@ -708,16 +718,25 @@ __device__ __forceinline__ void modify_tile(float* s, const FwdParams& p,
     float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
 #pragma unroll
     for (int c = 0; c < NC; c += 8) {
-      a0 = fmax3_abs(a0, s[c], s[c + 1]);
-      a1 = fmax3_abs(a1, s[c + 2], s[c + 3]);
-      a2 = fmax3_abs(a2, s[c + 4], s[c + 5]);
-      a3 = fmax3_abs(a3, s[c + 6], s[c + 7]);
+      a0 = fmax3_abs_nan(a0, s[c], s[c + 1]);
+      a1 = fmax3_abs_nan(a1, s[c + 2], s[c + 3]);
+      a2 = fmax3_abs_nan(a2, s[c + 4], s[c + 5]);
+      a3 = fmax3_abs_nan(a3, s[c + 6], s[c + 7]);
     }
-    const float top = fmaxf(fmax3(a0, a1, a2), a3);
+    float top = fmax3_abs_nan(fmax3_abs_nan(a0, a1, a2), a3, a3);
     if (MOD != kModCap) neg_m = 0.f;
-    if (__all_sync(0xffffffffu, top <= p.mod.poly_max)) {
+    bool near = __all_sync(0xffffffffu, top <= p.mod.poly_max);
+    if (near) {
       cap_tile<MOD, NC, 4>(s, p.mod.poly, pc, neg_m);
-    } else {
+    } else if (__any_sync(0xffffffffu, top != top)) {
+      if (partial) mask_tile<NC>(s, lo_c, hi_c, keep, use_keep, 0.f);
+      top = 0.f;  // of what is no NaN
+#pragma unroll
+      for (int c = 0; c < NC; c += 2) top = fmax3_abs(top, s[c], s[c + 1]);
+      near = __all_sync(0xffffffffu, top <= p.mod.poly_max);
+      if (near) cap_tile<MOD, NC, 4>(s, p.mod.poly, pc, neg_m);
+    }
+    if (!near) {
       const float k2 = -2.f * p.mod.cap_log2, k0 = p.mod.cap_log2 + neg_m;
 #pragma unroll
       for (int c = 0; c < NC; c += 2) {
@@ -890,7 +909,8 @@ __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
       float* s = reinterpret_cast<float*>(sraw);
       float sl8 = 0.f, cbase = 0.f;  // bias of each 8 columns (kModBias)
       if (MOD != 0)
-        modify_tile<MOD, kTileN>(s, p, kbase, qrow, slope2, &sl8, &cbase,
+        modify_tile<MOD, kTileN>(s, p, kbase, qrow, cls == 1, rlo - kbase,
+                                 rhi - kbase, keep, KEEP, slope2, &sl8, &cbase,
                                  -p.mod.m_fixed);
       if (cls == 1) mask_tile(s, rlo - kbase, rhi - kbase, keep, KEEP);
 
@@ -1765,7 +1785,8 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
         base = (jt > qt ? -slope2 : slope2) *
                static_cast<float>(kbase + kBiasMid - qrow);
       } else if (MOD != 0) {
-        modify_tile<MOD, kTileN>(s, p, kbase, qrow, slope2, &sl8, &cbase);
+        modify_tile<MOD, kTileN>(s, p, kbase, qrow, cls == 1, rlo - kbase,
+                                 rhi - kbase, keep, KEEP, slope2, &sl8, &cbase);
       }
       if (cls == 1) mask_tile(s, rlo - kbase, rhi - kbase, keep, KEEP);
 
@@ -2113,7 +2134,8 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
         mbar_arrive(meet);
       }
       float sl8, cbase;  // bias of each 8 columns
-      modify_tile<MOD, NC>(s, p, kbase, qrow, slope2, &sl8, &cbase);
+      modify_tile<MOD, NC>(s, p, kbase, qrow, cls == 1, rlo - kbase,
+                           rhi - kbase, keep, KEEP, slope2, &sl8, &cbase);
       if (MOD == kModCap) sl8 = cbase = 0.f;
       if (cls == 1) mask_tile<NC>(s, rlo - kbase, rhi - kbase, keep, KEEP);
 

@@ -391,6 +391,12 @@ __device__ __forceinline__ void poly_sq2(float& d0, float& d1, float a0,
   for (int i = N - 3; i >= 0; --i) ffma2v(d0, d1, d0, d1, v0, v1, c[i], c[i]);
 }
 
+// max(|a|, |b|, |c|), NaN if any is (sm_100 and later).
+__device__ __forceinline__ float fmax3_abs_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // max(|a|, |b|, |c|) (sm_100 and later).
 __device__ __forceinline__ float fmax3_abs(float a, float b, float c) {
   float d;

@@ -1,0 +1,69 @@
+"""Modified softmax scores at their edges.  Tolerances as in
+test_gpu_score_mod."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_masked_build_gb300 as bsm
+import score_mod_ref as ref
+from gpu_helpers import dense_device_bits
+from test_gpu_score_mod import (BD, C, DN, L, MODS, SG, check_out, inputs,
+                                slopes_of)
+
+pytestmark = pytest.mark.gpu
+
+
+def _masks(S):
+    """name -> (flags, window, segment ids, dense mask, keys for NaN: next to
+    one that a row sees without them)"""
+    i = np.arange(S)
+    mixed = (i % 2)[None].astype(np.int32)  # neighbours never see each other
+    return {
+        "causal": (C, 0, None, None, [79]),
+        "local": (C | L, 40, None, None, [79, 200]),
+        "band": (L | BD, 40, None, None, [79, 200]),
+        "mixed_ids": (SG, 0, mixed, None, [133, 201]),
+        "dense": (DN, 0, None,
+                  (i[None, :] <= i[:, None]) & (i[None, :] % 5 != 1)
+                  | (i[None, :] == i[:, None]), [79]),
+    }
+
+
+@pytest.mark.parametrize("mod", MODS, ids=[m[0] for m in MODS])
+@pytest.mark.parametrize("cap", [1.0, 500.0])  # times the modification's
+@pytest.mark.parametrize("kind", list(_masks(1)))
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_nan_in_keys_that_a_row_does_not_see(D, many, kind, cap, mod):
+    """Keys of NaN leave the rows that do not see them as they are, the
+    neighbouring columns' among them; those that do become NaN."""
+    if cap > 1 and mod[1] == 0:
+        pytest.skip("no cap")
+    S = 300
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    H = sms // 2 + 4 if many else 2  # two 256-row units per head
+    flags, window, seg, dense, bad = _masks(S)[kind]
+    q, k, v, _ = inputs(f"nan{D}{kind}{mod[0]}", 1, H, H, S, S, D, 9.0)
+    slopes = slopes_of(H, mod[2]) if mod[2] else None
+    vis = ref.visible(flags, window, S, S, 1, seg, seg, dense)
+    hit = vis[0][:, bad].any(1)
+    assert bool(hit.any()) and not bool(hit.all())
+    softcap, scale = mod[1] * cap, 1 / math.sqrt(D)
+    want = ref.forward(q, k, v, vis, scale, softcap, slopes)
+    k[:, :, bad] = float("nan")
+    ids = None if seg is None else torch.from_numpy(seg).cuda()
+    bits = None if dense is None else dense_device_bits(dense)
+    info = bsm.build_mask_info(flags, 1, S, S, 128, 128, window, ids, ids,
+                               dense_bits=bits)
+    out, lse = bsm.splash_attention(
+        q.cuda(), k.cuda(), v.cuda(), mask_info=info, q_segment_ids=ids,
+        kv_segment_ids=ids, softcap=softcap,
+        alibi_slopes=None if slopes is None else slopes.cuda())
+    assert bsm.bsm_device_status()[0] == 0
+    out, lse = out.cpu(), lse.cpu()
+    check_out(out[:, :, ~hit], lse[:, :, ~hit],
+              [x[:, :, ~hit] for x in want])
+    assert bool(torch.isnan(out[:, :, hit].float()).all())
