@@ -784,6 +784,13 @@ __device__ __forceinline__ float biased_max(const float* s, float sl8,
   return fmaxf(mx[0], mx[1]);
 }
 
+// Whether a row saw a key.  With modified scores a sum of NaN counts (and the
+// logsumexp becomes NaN); without, such rows have always had -inf.
+template <int MOD>
+__device__ __forceinline__ bool has_sum(float l_sum) {
+  return MOD != 0 ? l_sum != 0.f : l_sum > 0.f;
+}
+
 // KEEP: partial tiles also carry per-element "keep" bits -- from segment ids
 // compared element by element (some key-id row is not sorted) and/or from
 // an arbitrary bit-packed mask; otherwise every mask is a key range per row.
@@ -1061,7 +1068,7 @@ __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
       mbar_arrive(&bars->o_free[t]);
       if (tracer) trace(p, bars, kRoleScore, kEvEpiOLoaded, t, 0, unit);
       float inv = 1.f;
-      if (SCORE == BSM_SCORE_SOFTMAX) inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
+      if (SCORE == BSM_SCORE_SOFTMAX) inv = has_sum<MOD>(l_sum) ? 1.f / l_sum : 0.f;
       if (row_ok) {
         // 32 bytes per store where the row alignment allows: each warp
         // store touches 32 rows, so fewer, wider stores cost fewer requests
@@ -1091,7 +1098,7 @@ __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
       mbar_arrive(&bars->o_free[t]);
     }
     if (SCORE == BSM_SCORE_SOFTMAX && p.lse != nullptr && row_ok) {
-      const float lse = l_sum > 0.f
+      const float lse = has_sum<MOD>(l_sum)
                             ? (m_used + log2f(l_sum)) * 0.6931471805599453f
                             : NEG_INF;
       p.lse[(static_cast<int64_t>(uc.b) * p.H + uc.h) * p.Sq + qrow] = lse;
@@ -1962,7 +1969,7 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
         }
       }
       float inv = 1.f;
-      if (SCORE == BSM_SCORE_SOFTMAX) inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
+      if (SCORE == BSM_SCORE_SOFTMAX) inv = has_sum<MOD>(l_sum) ? 1.f / l_sum : 0.f;
       if (row_ok) {
         // 32 bytes per store where the row alignment allows: each warp
         // store touches 32 rows, so fewer, wider stores cost fewer requests
@@ -2000,7 +2007,7 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
       mbar_arrive(&bars->o_free[t]);
     }
     if (SCORE == BSM_SCORE_SOFTMAX && p.lse != nullptr && row_ok) {
-      const float lse = l_sum > 0.f
+      const float lse = has_sum<MOD>(l_sum)
                             ? (m_used + log2f(l_sum)) * 0.6931471805599453f
                             : NEG_INF;
       p.lse[(static_cast<int64_t>(uc.b) * p.H + uc.h) * p.Sq + qrow] = lse;
@@ -2246,7 +2253,7 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
           l_sum = fmaf(l1, w1, l_sum * w0);
         }
       }
-      const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
+      const float inv = has_sum<MOD>(l_sum) ? 1.f / l_sum : 0.f;
       if (row_ok) {
         const bool v8 = p.o_vec8 != 0;
 #pragma unroll
@@ -2281,7 +2288,7 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
       mbar_arrive(&bars->o_free[t]);
     }
     if (hf == 0 && p.lse != nullptr && row_ok) {
-      const float lse = l_sum > 0.f
+      const float lse = has_sum<MOD>(l_sum)
                             ? (ref + log2f(l_sum)) * 0.6931471805599453f
                             : NEG_INF;
       p.lse[(static_cast<int64_t>(uc.b) * p.H + uc.h) * p.Sq + qrow] = lse;

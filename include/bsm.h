@@ -225,7 +225,8 @@ bsm_status bsm_splash_fwd(const void* q, const void* k, const void* v,
  * / softcap))), and by 2^-22 of slope times the distance, or times 64 if that
  * is more.  As without a modification, a key that a row does not see weighs 0,
  * and 0 times an infinity or NaN in V (in the backward: in any operand) of a
- * key tile that the row's query tile visits is NaN. */
+ * key tile that the row's query tile visits is NaN.  A row that sees a NaN
+ * score gets NaN for its output and logsumexp. */
 typedef struct bsm_score_mod {
   float softcap;
   const float* alibi_slopes;

@@ -67,3 +67,24 @@ def test_nan_in_keys_that_a_row_does_not_see(D, many, kind, cap, mod):
     check_out(out[:, :, ~hit], lse[:, :, ~hit],
               [x[:, :, ~hit] for x in want])
     assert bool(torch.isnan(out[:, :, hit].float()).all())
+
+
+@pytest.mark.parametrize("mod", MODS, ids=[m[0] for m in MODS])
+@pytest.mark.parametrize("kind", ["causal", "dense"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_with_nan_have_a_nan_logsumexp(D, kind, mod):
+    # (-inf would say that the row sees nothing)
+    S, H = 300, 3
+    flags, window, _, dense, _ = _masks(S)[kind]
+    q, k, v, _ = inputs(f"nanlse{D}{kind}{mod[0]}", 1, H, 1, S, S, D, 3.0)
+    q[:, :, 140] = float("nan")
+    bits = None if dense is None else dense_device_bits(dense)
+    info = bsm.build_mask_info(flags, 1, S, S, dense_bits=bits)
+    out, lse = bsm.splash_attention(
+        q.cuda(), k.cuda(), v.cuda(), mask_info=info, softcap=mod[1],
+        alibi_slopes=slopes_of(H).cuda() if mod[2] else None)
+    want = torch.zeros(S, dtype=torch.bool)
+    want[140] = True
+    assert torch.equal(torch.isnan(out.float()).any(-1).cpu(),
+                       want.expand(1, H, S))
+    assert torch.equal(torch.isnan(lse).cpu(), want.expand(1, H, S))
