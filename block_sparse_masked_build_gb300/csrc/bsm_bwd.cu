@@ -447,7 +447,9 @@ __device__ __forceinline__ float bias_side(const BwdParams& p, int col0,
 // tanh is the forward's: a polynomial of POLY terms where every |S| of the warp
 // lies within its range, else (POLY = 0), with E = e^(-2 |y|) and r = 1 / (1 + E): |tanh y| =
 // (1 - E) r and 1 - tanh^2 y = 4 E r^2, which keeps its relative precision
-// where tanh saturates.  n: dK/dV: the columns' negated lse and bias.
+// where tanh saturates.  A NaN is taken for 0 there, as two columns share a
+// reciprocal: if its row does not see it nothing comes of it, and a row that
+// does has a logsumexp of NaN, and with it P.  n: dK/dV: the columns' negated lse and bias.
 template <int MOD, bool DKDV, bool MASK, int POLY>
 __device__ __forceinline__ void mod_p_loop(const BwdParams& p,
                                            const uint32_t* sraw,
@@ -489,8 +491,8 @@ __device__ __forceinline__ void mod_p_loop(const BwdParams& p,
         } else {
           float e0, e1, q0, q1;
           fmul2(q0, q1, s0, s1, p.mod.cap_e);
-          e0 = ex2_approx(-fabsf(q0));
-          e1 = ex2_approx(-fabsf(q1));
+          e0 = ex2_approx(fminf(-fabsf(q0), 0.f));
+          e1 = ex2_approx(fminf(-fabsf(q1), 0.f));
           float d0, d1;
           fadd2(d0, d1, e0, e1, 1.f, 1.f);
           const float r = rcp_approx(d0 * d1);

@@ -88,3 +88,31 @@ def test_rows_with_nan_have_a_nan_logsumexp(D, kind, mod):
     assert torch.equal(torch.isnan(out.float()).any(-1).cpu(),
                        want.expand(1, H, S))
     assert torch.equal(torch.isnan(lse).cpu(), want.expand(1, H, S))
+
+
+@pytest.mark.parametrize("mod", MODS + [("none", 0.0, 0.0)],
+                         ids=[m[0] for m in MODS] + ["none"])
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (8, 1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_nan_in_queries_that_a_key_does_not_serve(D, H, Hkv, mod):
+    """A query of NaN leaves dV of the keys that it does not see as it is:
+    there its weight is 0 and its gradient finite."""
+    S, window = 300, 41
+    q, k, v, do = inputs(f"nanq{D}{H}{mod[0]}", 1, H, Hkv, S, S, D, 9.0)
+    bad = torch.tensor([77, 200, 255])
+    slopes = slopes_of(H, mod[2]) if mod[2] else None
+    vis = ref.visible(C | L, window, S, S, 1)
+    hit = vis[0][bad].any(0)
+    scale = 1 / math.sqrt(D)
+    want, tol = ref.backward(q, k, v, do, vis, scale, mod[1], slopes,
+                             bounds=True)
+    q[:, :, bad] = float("nan")
+    kw = dict(mask_info=bsm.build_mask_info(C | L, 1, S, S, window=window),
+              softcap=mod[1],
+              alibi_slopes=None if slopes is None else slopes.cuda())
+    dev = [t.cuda() for t in (q, k, v)]
+    out, lse = bsm.splash_attention(*dev, **kw)
+    _, _, dv = bsm.splash_attention_bwd(*dev, out, lse, do.cuda(), **kw)
+    assert bsm.bsm_device_status()[0] == 0
+    err = (dv.double().cpu() - want[2]).abs()[:, :, ~hit]
+    assert (err <= tol[2][:, :, ~hit] + 1e-30).all()  # (false for NaN)
