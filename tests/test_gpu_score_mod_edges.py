@@ -11,7 +11,7 @@ import block_sparse_masked_build_gb300 as bsm
 import score_mod_ref as ref
 from gpu_helpers import dense_device_bits
 from test_gpu_score_mod import (BD, C, DN, L, MODS, SG, check_out, inputs,
-                                slopes_of)
+                                run, slopes_of)
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +116,17 @@ def test_nan_in_queries_that_a_key_does_not_serve(D, H, Hkv, mod):
     assert bsm.bsm_device_status()[0] == 0
     err = (dv.double().cpu() - want[2]).abs()[:, :, ~hit]
     assert (err <= tol[2][:, :, ~hit] + 1e-30).all()  # (false for NaN)
+
+
+@pytest.mark.parametrize("mod", [m for m in MODS if m[1]],
+                         ids=[m[0] for m in MODS if m[1]])
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (8, 1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_gradients_of_scores_beyond_f32_exponentials(D, H, Hkv, mod):
+    # |x| / cap in the hundreds: e^(-2 |x| / cap) underflows, tanh is +-1 and
+    # its derivative 0, so dQ and dK nearly vanish and dV does not
+    q, k, v, do = inputs(f"hugebwd{D}{H}{mod[0]}", 1, H, Hkv, 130, 130, D,
+                         200.0)
+    _, _, grads = run(q, k, v, do, C, softcap=1.0,
+                      slopes=slopes_of(H, 1.0) if mod[2] else None)
+    assert len(grads) == 3 and bool((grads[2] != 0).any())
