@@ -225,7 +225,6 @@ bsm_status check_mod(const bsm_score_mod* mod, float scale, int32_t score,
       if (std::fabs(c1) >= 0x1p-10)
         out->wide_max = static_cast<float>(1.2 / std::fabs(c1));
     }
-    out->m_fixed = std::fmax(0.f, out->cap_log2 - 52.f);
     out->inv_cap2 = 1.f / (out->cap_log2 * out->cap_log2);
   }
   if (mod->alibi_slopes != nullptr) {

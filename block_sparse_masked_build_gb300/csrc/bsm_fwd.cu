@@ -644,11 +644,11 @@ __device__ __forceinline__ void mask_tile(
   }
 }
 
-// s = s * (c[0] + c[1] s^2 + ...) + the bias of the column's place among eight
-// (kModBias) or + neg_m.
+// s = s * (c[0] + c[1] s^2 + ...), with kModBias + the bias of the column's
+// place among eight.
 template <int MOD, int NC, int N>
 __device__ __forceinline__ void cap_tile(float* s, const float* c,
-                                         const float* pc, float neg_m) {
+                                         const float* pc) {
 #pragma unroll
   for (int j = 0; j < NC; j += 2) {
     float h0, h1;
@@ -657,7 +657,7 @@ __device__ __forceinline__ void cap_tile(float* s, const float* c,
       ffma2v(s[j], s[j + 1], s[j], s[j + 1], h0, h1, pc[j & 7],
              pc[(j & 7) + 1]);
     else
-      ffma2v(s[j], s[j + 1], s[j], s[j + 1], h0, h1, neg_m, neg_m);
+      fmul2v(s[j], s[j + 1], s[j], s[j + 1], h0, h1);
   }
 }
 
@@ -688,8 +688,6 @@ __device__ __forceinline__ void cap_tile(float* s, const float* c,
 // caller adds sl 8 (c / 8) + *base per 8 columns.  A tile with columns on both
 // sides that no causal mask cuts takes the bias whole, column by column.
 //
-// kModCap alone: neg_m is added to s.
-//
 // partial, lo_c, hi_c, keep, use_keep: the row's visible columns, as mask_tile
 // takes them, if the tile is partial.
 template <int MOD, int NC>
@@ -698,8 +696,7 @@ __device__ __forceinline__ void modify_tile(float* s, const FwdParams& p,
                                             int lo_c, int hi_c,
                                             const uint32_t* keep, bool use_keep,
                                             float slope2, float* sl_out,
-                                            float* base_out,
-                                            float neg_m = 0.f) {
+                                            float* base_out) {
   float pc[8];  // bias of columns 0-7 of a chunk
   bool split = false;
   if (MOD & kModBias) {
@@ -724,20 +721,19 @@ __device__ __forceinline__ void modify_tile(float* s, const FwdParams& p,
       a3 = fmax3_abs_nan(a3, s[c + 6], s[c + 7]);
     }
     float top = fmax3_abs_nan(fmax3_abs_nan(a0, a1, a2), a3, a3);
-    if (MOD != kModCap) neg_m = 0.f;
     bool near = __all_sync(0xffffffffu, top <= p.mod.poly_max);
     if (near) {
-      cap_tile<MOD, NC, 4>(s, p.mod.poly, pc, neg_m);
+      cap_tile<MOD, NC, 4>(s, p.mod.poly, pc);
     } else if (__any_sync(0xffffffffu, top != top)) {
       if (partial) mask_tile<NC>(s, lo_c, hi_c, keep, use_keep, 0.f);
       top = 0.f;  // of what is no NaN
 #pragma unroll
       for (int c = 0; c < NC; c += 2) top = fmax3_abs(top, s[c], s[c + 1]);
       near = __all_sync(0xffffffffu, top <= p.mod.poly_max);
-      if (near) cap_tile<MOD, NC, 4>(s, p.mod.poly, pc, neg_m);
+      if (near) cap_tile<MOD, NC, 4>(s, p.mod.poly, pc);
     }
     if (!near) {
-      const float k2 = -2.f * p.mod.cap_log2, k0 = p.mod.cap_log2 + neg_m;
+      const float k2 = -2.f * p.mod.cap_log2, k0 = p.mod.cap_log2;
 #pragma unroll
       for (int c = 0; c < NC; c += 2) {
         float e0, e1;
@@ -850,11 +846,7 @@ __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
     }
     const int32_t* segk_b =
         seg_elem ? p.kv_seg + static_cast<int64_t>(uc.b) * p.Skv : nullptr;
-    // a cap alone bounds the logits to +-cap_log2: no maximum is kept, p is
-    // 2^(x - m_fixed) with m_fixed = max(0, cap_log2 - 52), so p lies within
-    // 2^-121 .. 2^52 for the caps that take this path (cap_log2 <= 87) and
-    // sums of 2^18 of them stay far inside f32
-    float m_used = MOD == kModCap ? p.mod.m_fixed : NEG_INF, l_sum = 0.f;
+    float m_used = NEG_INF, l_sum = 0.f;
     const float slope2 = (MOD & kModBias) && p.mod.slopes != nullptr
                              ? p.mod.slopes[uc.h] * 1.4426950408889634f
                              : 0.f;
@@ -917,8 +909,7 @@ __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
       float sl8 = 0.f, cbase = 0.f;  // bias of each 8 columns (kModBias)
       if (MOD != 0)
         modify_tile<MOD, kTileN>(s, p, kbase, qrow, cls == 1, rlo - kbase,
-                                 rhi - kbase, keep, KEEP, slope2, &sl8, &cbase,
-                                 -p.mod.m_fixed);
+                                 rhi - kbase, keep, KEEP, slope2, &sl8, &cbase);
       if (cls == 1) mask_tile(s, rlo - kbase, rhi - kbase, keep, KEEP);
 
       uint32_t pk[16];
@@ -937,8 +928,6 @@ __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
           }
           const float mx = fmax3(mx0, mx1, fmaxf(mx2, mx3));
           m_blk = mx * p.scale_log2;
-        } else if (MOD == kModCap) {
-          m_blk = NEG_INF;  // m_used stays m_fixed
         } else {
           m_blk = biased_max<kTileN>(s, sl8, cbase);
         }
@@ -963,8 +952,6 @@ __device__ __forceinline__ void score_role(const FwdParams& p, Bars* bars,
             if (MOD == 0) {
               ffma2(x0, x1, s[c], s[c + 1], p.scale_log2, neg_m);
               ffma2(x2, x3, s[c + 2], s[c + 3], p.scale_log2, neg_m);
-            } else if (MOD == kModCap) {  // m_fixed is subtracted already
-              x0 = s[c], x1 = s[c + 1], x2 = s[c + 2], x3 = s[c + 3];
             } else {
               const float add =
                   fmaf(sl8, static_cast<float>(c / 8), cbase + neg_m);
@@ -1721,11 +1708,7 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
     }
     const int32_t* segk_b =
         seg_elem ? p.kv_seg + static_cast<int64_t>(uc.b) * p.Skv : nullptr;
-    // a cap alone bounds the logits to +-cap_log2: no maximum is kept, p is
-    // 2^(x - m_fixed) with m_fixed = max(0, cap_log2 - 52), so p lies within
-    // 2^-121 .. 2^52 for the caps that take this path (cap_log2 <= 87) and
-    // sums of 2^18 of them stay far inside f32
-    float m_used = MOD == kModCap ? p.mod.m_fixed : NEG_INF, l_sum = 0.f;
+    float m_used = NEG_INF, l_sum = 0.f;
     const float slope2 = (MOD & kModBias) && p.mod.slopes != nullptr
                              ? p.mod.slopes[uc.h] * 1.4426950408889634f
                              : 0.f;
@@ -1813,8 +1796,6 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
           }
           const float mx = fmax3(mx0, mx1, fmaxf(mx2, mx3));
           m_blk = MOD == 0 ? mx * p.scale_log2 : fmaf(mx, p.scale_log2, base);
-        } else if (MOD == kModCap) {
-          m_blk = NEG_INF;  // m_used stays m_fixed
         } else {
           m_blk = biased_max<kTileN>(s, sl8, cbase);
         }
@@ -1840,8 +1821,6 @@ __device__ __forceinline__ void dt_score_role(const FwdParams& p, DtBars* bars,
             if (MOD == 0 || MOD == kModBias) {
               ffma2(x0, x1, s[c], s[c + 1], p.scale_log2, neg_m);
               ffma2(x2, x3, s[c + 2], s[c + 3], p.scale_log2, neg_m);
-            } else if (MOD == kModCap) {  // m_fixed is subtracted already
-              x0 = s[c], x1 = s[c + 1], x2 = s[c + 2], x3 = s[c + 3];
             } else {
               const float add =
                   fmaf(sl8, static_cast<float>(c / 8), cbase + neg_m);
@@ -2481,7 +2460,7 @@ cudaError_t launch_score(const FwdParams& p, const CUtensorMap& tq,
   // core, sets the pace, and its turns in the lockstep kernel leave half the
   // score warps waiting (causal S=8192, 32/8 heads, in one form of the scores:
   // cap 50 672 us there, 623 here; bias 618 and 524; both 1049 and 757).
-  // (kModFixed, which only that kernel has, does not come here.)
+  // (Caps with a fixed reference, which only that kernel has, do not come here.)
   const bool dt = MOD != 0 ? p.D == 128 && fwd_mod_dt(p)
                            : p.dense == nullptr && p.D == 128 &&
                                  ((p.flags & BSM_MASK_SEGMENT) != 0 ||
@@ -2530,14 +2509,14 @@ cudaError_t launch_splash_fwd(const FwdParams& p, const CUtensorMap& tq,
   const int grid = fwd_grid_size(p, num_sms);
   if (p.score == BSM_SCORE_POINTWISE)
     return launch_score<BSM_SCORE_POINTWISE, 0>(p, tq, tk, tv, grid, num_sms, stream);
-  // a cap too large for a fixed reference (see score_role) takes the instance
-  // with a running maximum, with slopes of zero
-  const int kind = p.mod.kind == kModCap && p.mod.cap_log2 > 87.f
-                       ? kModCap | kModBias
-                       : p.mod.kind;
-  // cap and bias with a fixed reference (see dt_score_cap_role)
-  if (kind == (kModCap | kModBias) && p.mod.slopes != nullptr &&
-      p.mod.cap_log2 <= 75.f && fwd_mod_dt(p))
+  // a cap with a fixed reference (see dt_score_cap_role), alone or with a bias
+  const int kind = p.mod.kind;
+  if (kind == kModCap && p.mod.cap_log2 <= 87.f && fwd_mod_dt(p))
+    return p.D == 128 ? launch_dt<128, BSM_SCORE_SOFTMAX, kModCap>(
+                            p, tq, tk, tv, grid, num_sms, stream)
+                      : launch_dt<64, BSM_SCORE_SOFTMAX, kModCap>(
+                            p, tq, tk, tv, grid, num_sms, stream);
+  if (kind == (kModCap | kModBias) && p.mod.cap_log2 <= 75.f && fwd_mod_dt(p))
     return p.D == 128 ? launch_dt<128, BSM_SCORE_SOFTMAX, kModFixed>(
                             p, tq, tk, tv, grid, num_sms, stream)
                       : launch_dt<64, BSM_SCORE_SOFTMAX, kModFixed>(
@@ -2545,10 +2524,11 @@ cudaError_t launch_splash_fwd(const FwdParams& p, const CUtensorMap& tq,
   switch (kind) {
     case 0:
       return launch_score<BSM_SCORE_SOFTMAX, 0>(p, tq, tk, tv, grid, num_sms, stream);
-    case kModCap:
-      return launch_score<BSM_SCORE_SOFTMAX, kModCap>(p, tq, tk, tv, grid, num_sms, stream);
     case kModBias:
       return launch_score<BSM_SCORE_SOFTMAX, kModBias>(p, tq, tk, tv, grid, num_sms, stream);
+    // larger caps and arbitrary masks: a running maximum (and, for a cap
+    // alone, slopes of zero)
+    case kModCap:
     case kModCap | kModBias:
       return launch_score<BSM_SCORE_SOFTMAX, kModCap | kModBias>(
           p, tq, tk, tv, grid, num_sms, stream);

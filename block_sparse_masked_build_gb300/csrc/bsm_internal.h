@@ -64,7 +64,6 @@ struct ScoreMod {
   // |S| <= poly_max (negative: nowhere), and with wide[] for |S| <= wide_max
   float poly[4], poly_max;
   float wide[7], wide_max;
-  float m_fixed;        // see kModCap's softmax in bsm_fwd.cu
   float inv_cap2;       // 1 / cap_log2^2
   const float* slopes;  // [H], or null
 };

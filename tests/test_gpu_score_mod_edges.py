@@ -10,8 +10,8 @@ import torch
 import block_sparse_masked_build_gb300 as bsm
 import score_mod_ref as ref
 from gpu_helpers import dense_device_bits
-from test_gpu_score_mod import (BD, C, DN, L, MODS, SG, check_out, inputs,
-                                run, slopes_of)
+from test_gpu_score_mod import (BD, C, DN, HALF, L, MODS, SG, check_out,
+                                inputs, run, slopes_of)
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +130,36 @@ def test_gradients_of_scores_beyond_f32_exponentials(D, H, Hkv, mod):
     _, _, grads = run(q, k, v, do, C, softcap=1.0,
                       slopes=slopes_of(H, 1.0) if mod[2] else None)
     assert len(grads) == 3 and bool((grads[2] != 0).any())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_key_that_outweighs_all_under_an_arbitrary_mask(D):
+    """Logits of 42 to 47 at a row's own key and 17 or more below that
+    elsewhere: the row is its own key's value to the last bit, as with a
+    running maximum its p is 1 and not rounded, wherever v is not so small
+    that the others show in it (`far` is the exact result's distance from v).
+    A p rounded to bf16 under a sum that is not moves many elements by a
+    step."""
+    S, H = 100, 4
+    g = torch.Generator().manual_seed(D)
+    sign = torch.randint(0, 2, (1, H, S, D), generator=g) * 2.0 - 1.0
+    q = (sign * torch.linspace(5.0, 6.0, S).view(1, 1, S, 1)
+         * math.sqrt(128 / D)).bfloat16()
+    k, v = sign.bfloat16(), torch.randn(1, H, S, D, generator=g).bfloat16()
+    i = np.arange(S)
+    dense = (i[None, :] * 7 + i[:, None] * 3) % 4 != 0
+    dense |= i[None, :] == i[:, None]
+    vis = ref.visible(DN, 0, S, S, 1, dense=dense)
+    scale = 1 / math.sqrt(D)
+    want = ref.forward(q, k, v, vis, scale, 55.0)
+    far = float((want[0] - v.double()).abs().max())
+    assert far < 1e-4
+    info = bsm.build_mask_info(DN, 1, S, S,
+                               dense_bits=dense_device_bits(dense))
+    out, lse = bsm.splash_attention(q.cuda(), k.cuda(), v.cuda(),
+                                    mask_info=info, softcap=55.0)
+    check_out(out, lse, want)
+    # where v is not so small that the others show in its last bit
+    clear = v.float().abs() > 4 * far / HALF
+    assert bool(clear.float().mean() > 0.9)
+    assert torch.equal(out.cpu()[clear], v[clear])
