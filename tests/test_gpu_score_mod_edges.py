@@ -163,3 +163,56 @@ def test_one_key_that_outweighs_all_under_an_arbitrary_mask(D):
     clear = v.float().abs() > 4 * far / HALF
     assert bool(clear.float().mean() > 0.9)
     assert torch.equal(out.cpu()[clear], v[clear])
+
+
+@pytest.mark.parametrize("slope", [0.02, -0.002])
+@pytest.mark.parametrize("flags", [SG, C | SG])
+@pytest.mark.parametrize("rows", ["none", "third", "few"])
+def test_references_with_absent_segments(rows, flags, slope):
+    """Unsorted ids over many key tiles, rows whose id no key has: all of
+    them, every third, those of one warp."""
+    S, H = 1500, 2
+    q, k, v, _ = inputs(f"absent{rows}{flags}{slope}", 1, H, H, S, S, 64, 4.0)
+    rng = np.random.default_rng(11)
+    ids = rng.integers(0, 40, (1, S)).astype(np.int32)
+    want = ids.copy()
+    if rows == "none":
+        want[:] = 77
+    elif rows == "third":
+        want[:, ::3] = 77
+    else:
+        want[:, 700:720] = 77
+    run(q, k, v, v, flags, 0, want, ids, softcap=30.0, bwd=False,
+        slopes=slope * torch.tensor([1.0, 8.0]))
+
+
+@pytest.mark.parametrize("share", [0.5, 1.0])
+def test_absent_segments_cost_no_walk_over_the_keys(share):
+    """Rows whose id no key has: a bias beside the cap needs the distance of
+    each row's nearest key, which is looked for in the unit's tiles alone.
+    (A walk over all keys took 5 to 80 times the cap's own time.)"""
+    S, H, D = 16384, 4, 64
+    q, k, v, _ = (t.cuda() for t in inputs("walk", 1, H, H, S, S, D))
+    g = torch.Generator().manual_seed(3)
+    ids = torch.randint(0, 4, (1, S), generator=g).int()
+    rows = torch.where(torch.rand(1, S, generator=g) < share, 9, ids).int()
+    ids, rows = ids.cuda(), rows.cuda()
+    info = bsm.build_mask_info(C | SG, 1, S, S, q_segment_ids=rows,
+                               kv_segment_ids=ids)
+    kw = dict(mask_info=info, q_segment_ids=rows, kv_segment_ids=ids,
+              softcap=30.0)
+
+    def time(**more):
+        best = math.inf
+        for _ in range(4):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            bsm.splash_attention(q, k, v, **kw, **more)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+
+    alone = time()
+    both = time(alibi_slopes=torch.full((H,), 0.02).cuda())
+    assert both <= 4 * alone + 0.1, (alone, both)
