@@ -995,10 +995,12 @@ bsm_status bsm_device_status(void* stream, int32_t* detail) {
   if (e != cudaSuccess) return cuda_fail(e, "device status");
   e = bsm::read_bwd_error(brec);
   if (e != cudaSuccess) return cuda_fail(e, "device status");
-  e = bsm::read_cache_error(crec);
-  if (e != cudaSuccess) return cuda_fail(e, "device status");
   if (rec[0] == 0 && brec[0] != 0) std::memcpy(rec, brec, sizeof(rec));
-  if (rec[0] == 0 && crec[0] != 0) {
+  // read, and so cleared, only where no timeout is reported before it: else
+  // the next call reports it
+  if (rec[0] == 0) e = bsm::read_cache_error(crec);
+  if (e != cudaSuccess) return cuda_fail(e, "device status");
+  if (crec[0] != 0) {
     if (detail != nullptr) std::memcpy(detail, crec, sizeof(crec));
     return fail(BSM_ERR_INVALID_ARG,
                 (crec[2] < 0 ? "a length is out of range (sequence "

@@ -499,7 +499,8 @@ size_t bsm_paged_attention_workspace_bytes(void);
 /* Synchronise `stream` and report whether a kernel of this library gave up
  * on a bounded wait since the last call (then BSM_ERR_DEVICE_TIMEOUT; the
  * affected outputs are undefined, the CUDA context stays usable), or a cache
- * kernel met a length or page out of range (BSM_ERR_INVALID_ARG).  If
+ * kernel met a length or page out of range (BSM_ERR_INVALID_ARG; with a
+ * timeout pending too, the next call reports it).  If
  * `detail` is non-NULL it receives 4 ints: code, block, role, phase; for the
  * cache kernels 2, the sequence, the page slot (-1: a length) and the value. */
 bsm_status bsm_device_status(void* stream, int32_t* detail);
