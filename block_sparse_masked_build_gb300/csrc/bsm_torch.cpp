@@ -160,8 +160,22 @@ bsm_score_mod score_mod(double softcap, const at::Tensor& slopes, int64_t H,
   return m;
 }
 
-// The operands of a forward or backward: bf16 tensors of one CUDA device with
-// the shapes that the pointers will be read with.
+// bf16, or its bits under a 16-bit integer type.
+bool bf16_bits(const at::Tensor& t) {
+  const at::ScalarType s = t.scalar_type();
+  return s == at::kBFloat16 || s == at::kShort || s == at::kUInt16;
+}
+
+// Whether t covers the first sizes of `like` (a larger buffer may serve).
+bool covers(const at::Tensor& t, const at::Tensor& like) {
+  if (t.dim() != like.dim()) return false;
+  for (int64_t i = 0; i < t.dim(); ++i)
+    if (t.size(i) < like.size(i)) return false;
+  return true;
+}
+
+// The operands of a forward or backward: bf16 tensors of one CUDA device that
+// hold what the pointers will be read with (k's heads and length).
 void check_operands(const at::Tensor& q, const at::Tensor& k,
                     const at::Tensor& v) {
   const at::Device dev = q.device();
@@ -173,41 +187,38 @@ void check_operands(const at::Tensor& q, const at::Tensor& k,
       value_error(
           "tensors must be 4-D [B, H, S, D] views with a contiguous head "
           "dimension");
-    if (t.scalar_type() != at::kBFloat16 || t.device() != dev)
+    if (!bf16_bits(t) || t.device() != dev)
       value_error(std::string(name) + " must be a bfloat16 tensor on " +
                   device_name(dev));
   }
-  if (k.sizes() != v.sizes() || k.size(0) != q.size(0) ||
-      k.size(3) != q.size(3))
+  if (!covers(v, k) || k.size(0) < q.size(0) || k.size(3) < q.size(3))
     value_error("k and v must be [B, H_kv, Skv, D] for q's B and D");
 }
 
 // A tensor with the shape and device of `like` (bf16).
 void check_like(const at::Tensor& t, const at::Tensor& like, const char* name) {
-  if (t.defined() &&
-      (t.scalar_type() != at::kBFloat16 || t.sizes() != like.sizes() ||
-       t.device() != like.device()))
+  if (t.defined() && (!bf16_bits(t) || !covers(t, like) ||
+                      t.device() != like.device()))
     value_error(std::string(name) + " must be a bfloat16 tensor of q's shape "
                                     "and device");
 }
 
 void check_lse(const at::Tensor& t, const at::Tensor& q) {
   if (t.defined() &&
-      (t.scalar_type() != at::kFloat || t.dim() != 3 ||
-       t.size(0) != q.size(0) || t.size(1) != q.size(1) ||
-       t.size(2) != q.size(2) || !t.is_contiguous() ||
+      (t.scalar_type() != at::kFloat ||
+       t.numel() != q.size(0) * q.size(1) * q.size(2) || !t.is_contiguous() ||
        t.device() != q.device()))
-    value_error("lse must be a contiguous float32 tensor [B, H, Sq] on q's "
-                "device");
+    value_error("lse must be a contiguous float32 tensor of B H Sq elements "
+                "on q's device");
 }
 
 void check_ids(const at::Tensor& t, int64_t B, int64_t S,
                const at::Device& dev, const char* name) {
   if (t.defined() &&
-      (t.scalar_type() != at::kInt || t.dim() != 2 || t.size(0) != B ||
-       t.size(1) != S || !t.is_contiguous() || t.device() != dev))
-    value_error(std::string(name) + " must be a contiguous int32 tensor [B, S] "
-                                    "on " + device_name(dev));
+      ((t.scalar_type() != at::kInt && t.scalar_type() != at::kUInt32) ||
+       t.numel() != B * S || !t.is_contiguous() || t.device() != dev))
+    value_error(std::string(name) + " must be a contiguous int32 tensor of "
+                                    "B S elements on " + device_name(dev));
 }
 
 // Makes the tensors' device current for a call, and gives the stream: the
