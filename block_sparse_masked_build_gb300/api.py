@@ -389,6 +389,59 @@ def bsm_splash_bwd(q, k, v, out, lse, dout, mask_info: MaskInfo,
         sh))
 
 
+_BF16_BITS = (torch.bfloat16, torch.int16, torch.uint16)
+_INT32 = (torch.int32, torch.uint32)
+
+
+def _covers(t, sizes) -> bool:
+    """Whether t holds the first `sizes` (a larger buffer may serve)."""
+    return t.dim() == len(sizes) and all(
+        n >= m for n, m in zip(t.shape, sizes))
+
+
+def _check_operands(q, k, v) -> None:
+    """The checks of the tensor binding on a forward's operands, which hold
+    what their pointers will be read with."""
+    dev = q.device
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dim() != 4 or t.stride(3) != 1:
+            raise ValueError("tensors must be 4-D [B, H, S, D] views with a "
+                             "contiguous head dimension")
+        if t.dtype not in _BF16_BITS or t.device != dev:
+            raise ValueError(f"{name} must be a bfloat16 tensor on {dev}")
+    if not _covers(v, k.shape) or k.shape[0] < q.shape[0] \
+            or k.shape[3] < q.shape[3]:
+        raise ValueError("k and v must be [B, H_kv, Skv, D] for q's B and D")
+
+
+def _check_like(t, like, name: str) -> None:
+    if t is not None and (t.dtype not in _BF16_BITS
+                          or not _covers(t, like.shape)
+                          or t.device != like.device):
+        raise ValueError(f"{name} must be a bfloat16 tensor of q's shape and "
+                         "device")
+
+
+def _check_lse(t, q) -> None:
+    if t is not None and (t.dtype != torch.float32
+                          or t.numel() != math.prod(q.shape[:3])
+                          or not t.is_contiguous() or t.device != q.device):
+        raise ValueError("lse must be a contiguous float32 tensor of B H Sq "
+                         "elements on q's device")
+
+
+def _check_ids(t, B: int, S: int, dev, name: str) -> None:
+    if t is not None and (t.dtype not in _INT32 or t.numel() != B * S
+                          or not t.is_contiguous() or t.device != dev):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of B S "
+                         f"elements on {dev}")
+
+
+def _check_both_ids(q_seg, kv_seg, q, k) -> None:
+    _check_ids(q_seg, q.shape[0], q.shape[2], q.device, "q_segment_ids")
+    _check_ids(kv_seg, q.shape[0], k.shape[2], q.device, "kv_segment_ids")
+
+
 def _check_cache(k_pages, v_pages, k_scale, v_scale) -> None:
     shape, dev = k_pages.shape, k_pages.device
     for t in (k_pages, v_pages):
@@ -774,6 +827,13 @@ def splash_attention_bwd(q, k, v, out, lse, dout, *,
             q, k, v, out if sm else None, lse if sm else None, dout,
             ctypes.addressof(mask_info.struct), q_segment_ids, kv_segment_ids,
             scale, score, softcap, alibi_slopes, _fast_stream(stream))
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    _check_operands(q, k, v)
+    _check_like(out if sm else None, q, "out")
+    _check_like(dout, q, "dout")
+    _check_lse(lse if sm else None, q)
+    _check_both_ids(q_segment_ids, kv_segment_ids, q, k)
     dq = torch.empty_like(q)
     dk = torch.empty_like(k)
     dv = torch.empty_like(v)
@@ -900,12 +960,17 @@ def splash_attention(q, k, v, *, mask_flags: int = MASK_CAUSAL,
         return fast.splash_fwd(
             q, k, v, ctypes.addressof(mask_info.struct), qs, ks, scale, score,
             softcap, alibi_slopes, out, lse, want_lse, _fast_stream(stream))
+    _check_operands(qd, kd, vd)
+    _check_both_ids(qs, ks, qd, kd)
+    _score_mod(softcap, alibi_slopes, H, dev)
     od = torch.empty((B, H, Sq, D), dtype=torch.bfloat16, device=dev) \
         if (host or out is None) else out
+    _check_like(od, qd, "out")
     ld = None
     if want_lse:
         ld = torch.empty((B, H, Sq), dtype=torch.float32, device=dev) \
             if (host or lse is None) else lse
+        _check_lse(ld, qd)
     bsm_splash_fwd(qd, kd, vd, mask_info, qs, ks, scale, score, od, ld,
                    stream, softcap=softcap, alibi_slopes=alibi_slopes)
     if not host:

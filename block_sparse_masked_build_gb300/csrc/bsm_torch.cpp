@@ -325,7 +325,7 @@ PyObject* py_splash_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor ks = tensor_or_none(a[5], "kv_segment_ids");
     const at::Device dev = q.device();
     check_ids(qs, q.size(0), q.size(2), dev, "q_segment_ids");
-    check_ids(ks, k.size(0), k.size(2), dev, "kv_segment_ids");
+    check_ids(ks, q.size(0), k.size(2), dev, "kv_segment_ids");
     const int64_t B = q.size(0), H = q.size(1), Sq = q.size(2), D = q.size(3);
     const bsm_score_mod mod =
         score_mod(number(a[8]), tensor_or_none(a[9], "alibi_slopes"), H, dev);
@@ -382,7 +382,7 @@ PyObject* py_splash_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor ks = tensor_or_none(a[8], "kv_segment_ids");
     const at::Device dev = q.device();
     check_ids(qs, q.size(0), q.size(2), dev, "q_segment_ids");
-    check_ids(ks, k.size(0), k.size(2), dev, "kv_segment_ids");
+    check_ids(ks, q.size(0), k.size(2), dev, "kv_segment_ids");
     const int32_t score = int32(a[10]);
     const int32_t B = static_cast<int32_t>(q.size(0));
     const int32_t H = static_cast<int32_t>(q.size(1));

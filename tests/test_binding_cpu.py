@@ -1,0 +1,52 @@
+"""The Python side of the bindings without a GPU: what the checks refuse."""
+
+import pytest
+import torch
+
+from block_sparse_masked_build_gb300 import api
+
+BF = torch.bfloat16
+
+
+def _t(*shape, dtype=BF):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def test_operands():
+    q, k = _t(2, 4, 10, 64), _t(2, 2, 12, 64)
+    api._check_operands(q, k, k)
+    api._check_operands(q, k.view(torch.int16), k.view(torch.uint16))
+    api._check_operands(q, _t(3, 2, 12, 64), _t(3, 2, 30, 64))
+    for bad in ((q.half(), k, k), (q, k.float(), k), (q, k, k[:, :, :11]),
+                (q, k, k[:, :1]), (q, k[:1], k[:1]),
+                (q, k[..., :32], k[..., :32]), (q[0], k, k),
+                (q.transpose(2, 3), k, k), (q, k.to("meta"), k)):
+        with pytest.raises(ValueError):
+            api._check_operands(*bad)
+
+
+def test_outputs():
+    q = _t(2, 4, 10, 64)
+    api._check_like(None, q, "out")
+    api._check_like(_t(2, 4, 20, 64), q, "out")
+    for bad in (q.float(), q[:1], q[:, :, :9], q[..., :8], q[0],
+                q.to("meta")):
+        with pytest.raises(ValueError, match="out must be"):
+            api._check_like(bad, q, "out")
+    api._check_lse(None, q)
+    api._check_lse(_t(8, 10, dtype=torch.float32), q)
+    for bad in (_t(8, 10), _t(8, 9, dtype=torch.float32),
+                _t(8, 20, dtype=torch.float32)[:, ::2]):
+        with pytest.raises(ValueError, match="lse must be"):
+            api._check_lse(bad, q)
+
+
+def test_segment_ids():
+    cpu = torch.device("cpu")
+    good = _t(2, 10, dtype=torch.int32)
+    for t in (None, good, good.view(20), good.view(torch.uint32)):
+        api._check_ids(t, 2, 10, cpu, "q_segment_ids")
+    for bad in (good.long(), good[:, :9], good[:1], good[:1].expand(2, 10),
+                good.to("meta")):
+        with pytest.raises(ValueError, match="q_segment_ids must be"):
+            api._check_ids(bad, 2, 10, cpu, "q_segment_ids")

@@ -67,3 +67,44 @@ def test_larger_buffers(both):  # noqa: F811
         same([got[:1, :2, :200].contiguous(), lse], want)
         assert (got[1:] == 7.0).all() and (got[:, 2:] == 7.0).all()
         assert (got[:, :, 200:] == 7.0).all()
+
+
+def test_refusals_are_the_same(both):  # noqa: F811
+    """Wrong types, devices and shapes: the same error on both ways."""
+    q = torch.zeros(1, 2, 64, 64, dtype=torch.bfloat16).cuda()
+    info = bsm.build_mask_info(bsm.MASK_CAUSAL, 1, 64, 64)
+    lse = torch.zeros(1, 2, 64).cuda()
+    seg = torch.zeros(1, 64, dtype=torch.int32).cuda()
+    bad = [(q.half(), q, q), (q, q.cpu(), q), (q, q, q.float()),
+           (q, q, q[:, :, :32]), (q, q[..., :32], q[..., :32]),
+           (q, q[:, :, :, ::2], q)]
+    calls = [lambda b=b: bsm.splash_attention(*b, mask_info=info, scale=1.0)
+             for b in bad]
+    calls += [lambda b=b: bsm.splash_attention_bwd(*b, q, lse, q, scale=1.0,
+                                                   mask_info=info)
+              for b in bad]
+    calls += [lambda kw=kw: bsm.splash_attention(q, q, q, mask_info=info, **kw)
+              for kw in (dict(out=q.float()), dict(out=q[:, :1]),
+                         dict(out=q.cpu()), dict(lse=lse.double()),
+                         dict(lse=lse[:, :, ::2]), dict(lse=lse.cpu()))]
+    calls += [lambda i=i: bsm.splash_attention(
+        q, q, q, mask_info=info, q_segment_ids=i, kv_segment_ids=i)
+        for i in (seg.long(), seg.cpu(), seg[:, :32])]
+    calls += [lambda: bsm.splash_attention_bwd(q, q, q, q, lse, q.cpu(),
+                                               mask_info=info),
+              lambda: bsm.splash_attention_bwd(q, q, q, q.half(), lse, q,
+                                               mask_info=info),
+              lambda: bsm.splash_attention_bwd(q, q, q, q, lse[:, :1], q,
+                                               mask_info=info),
+              lambda: bsm.splash_attention_bwd(q.cpu(), q, q, q, lse, q,
+                                               mask_info=info)]
+    for f in calls:
+        seen = []
+
+        def call():
+            with pytest.raises((bsm.BsmError, ValueError)) as e:
+                f()
+            seen.append((type(e.value), str(e.value)))
+
+        both(call)
+        assert seen[0] == seen[1]
