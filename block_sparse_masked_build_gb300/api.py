@@ -25,6 +25,7 @@ MASK_BAND = 8  # with MASK_LOCAL: |q - k| < window
 MASK_DENSE = 16  # arbitrary mask, bit-packed uint32 words per query row
 SCORE_SOFTMAX = 0
 SCORE_POINTWISE = 1
+_INT32 = (torch.int32, torch.uint32)  # of segment ids
 
 
 class BsmError(RuntimeError):
@@ -212,6 +213,30 @@ class MaskInfo:
         return idx[:nnz], cls[:nnz]
 
 
+def _check_mask_inputs(flags: int, q_seg, kv_seg, B: int, Sq: int, Skv: int,
+                       dense_bits, dev) -> None:
+    """What the mask-info kernels will read."""
+    if flags & MASK_SEGMENT:
+        for name, t, n in (("q_segment_ids", q_seg, B * Sq),
+                           ("kv_segment_ids", kv_seg, B * Skv)):
+            if t is not None and (t.dtype not in _INT32 or t.numel() < n
+                                  or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous int32 tensor "
+                                 f"of {n} elements or more")
+    if flags & MASK_DENSE and dense_bits is not None and (
+            dense_bits.shape[0] < Sq
+            or dense_bits.shape[1] < (Skv + 31) // 32):
+        raise ValueError("dense_bits must have Sq rows of ceil(Skv / 32) "
+                         "words")
+    given = [t for t in (q_seg, kv_seg, dense_bits) if t is not None]
+    if not all(t.is_cuda for t in given):
+        raise ValueError("segment ids and dense_bits must be CUDA tensors")
+    if dev.type != "cuda":
+        raise ValueError("the mask info must be on a CUDA device")
+    if any(t.device != dev for t in given):
+        raise ValueError(f"segment ids and dense_bits must be on {dev}")
+
+
 def bsm_build_mask_info(flags: int, window: int, q_segment_ids, kv_segment_ids,
                         B: int, Sq: int, Skv: int, block_q: int, block_kv: int,
                         buffer: torch.Tensor, stream=None,
@@ -227,6 +252,8 @@ def bsm_build_mask_info(flags: int, window: int, q_segment_ids, kv_segment_ids,
                              "contiguous rows")
         spec.dense_bits = dense_bits.data_ptr()
         spec.dense_row_words = dense_bits.stride(0)
+    _check_mask_inputs(flags, q_segment_ids, kv_segment_ids, B, Sq, Skv,
+                       dense_bits, buffer.device)
     info = MaskInfoStruct()
     _check(_lib.lib().bsm_build_mask_info(
         ctypes.byref(spec), _ptr(q_segment_ids), _ptr(kv_segment_ids), B, Sq,
@@ -390,7 +417,6 @@ def bsm_splash_bwd(q, k, v, out, lse, dout, mask_info: MaskInfo,
 
 
 _BF16_BITS = (torch.bfloat16, torch.int16, torch.uint16)
-_INT32 = (torch.int32, torch.uint32)
 
 
 def _covers(t, sizes) -> bool:
@@ -424,17 +450,17 @@ def _check_like(t, like, name: str) -> None:
 
 def _check_lse(t, q) -> None:
     if t is not None and (t.dtype != torch.float32
-                          or t.numel() != math.prod(q.shape[:3])
+                          or t.numel() < math.prod(q.shape[:3])
                           or not t.is_contiguous() or t.device != q.device):
         raise ValueError("lse must be a contiguous float32 tensor of B H Sq "
-                         "elements on q's device")
+                         "elements or more on q's device")
 
 
 def _check_ids(t, B: int, S: int, dev, name: str) -> None:
-    if t is not None and (t.dtype not in _INT32 or t.numel() != B * S
+    if t is not None and (t.dtype not in _INT32 or t.numel() < B * S
                           or not t.is_contiguous() or t.device != dev):
         raise ValueError(f"{name} must be a contiguous int32 tensor of B S "
-                         f"elements on {dev}")
+                         f"elements or more on {dev}")
 
 
 def _check_both_ids(q_seg, kv_seg, q, k) -> None:
@@ -671,6 +697,8 @@ def build_mask_info(flags: int, B: int, Sq: int, Skv: int, block_q: int = 128,
 
             _run_on(s, build)
             return made[0]
+    if device is not None and torch.device(device).type != "cuda":
+        raise ValueError("the mask info must be on a CUDA device")
     fast = _fast()
     if fast:
         if device is None:

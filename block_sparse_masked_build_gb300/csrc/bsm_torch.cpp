@@ -206,19 +206,27 @@ void check_like(const at::Tensor& t, const at::Tensor& like, const char* name) {
 void check_lse(const at::Tensor& t, const at::Tensor& q) {
   if (t.defined() &&
       (t.scalar_type() != at::kFloat ||
-       t.numel() != q.size(0) * q.size(1) * q.size(2) || !t.is_contiguous() ||
+       t.numel() < q.size(0) * q.size(1) * q.size(2) || !t.is_contiguous() ||
        t.device() != q.device()))
     value_error("lse must be a contiguous float32 tensor of B H Sq elements "
-                "on q's device");
+                "or more on q's device");
+}
+
+void check_id_size(const at::Tensor& t, int64_t n, const char* name) {
+  if (t.defined() &&
+      ((t.scalar_type() != at::kInt && t.scalar_type() != at::kUInt32) ||
+       t.numel() < n || !t.is_contiguous()))
+    value_error(std::string(name) + " must be a contiguous int32 tensor of " +
+                std::to_string(n) + " elements or more");
 }
 
 void check_ids(const at::Tensor& t, int64_t B, int64_t S,
                const at::Device& dev, const char* name) {
   if (t.defined() &&
       ((t.scalar_type() != at::kInt && t.scalar_type() != at::kUInt32) ||
-       t.numel() != B * S || !t.is_contiguous() || t.device() != dev))
+       t.numel() < B * S || !t.is_contiguous() || t.device() != dev))
     value_error(std::string(name) + " must be a contiguous int32 tensor of "
-                                    "B S elements on " + device_name(dev));
+                                    "B S elements or more on " + device_name(dev));
 }
 
 // Makes the tensors' device current for a call, and gives the stream: the
@@ -294,14 +302,26 @@ PyObject* py_build_mask_info(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const size_t bytes =
         f_mask_info_bytes(&spec, s[0], s[1], s[2], s[3], s[4]);
     if (bytes == 0) Py_RETURN_NONE;
-    const at::Device dev(at::kCUDA,
-                         static_cast<c10::DeviceIndex>(
-                             a[10] == Py_None ? c10::cuda::current_device()
-                                              : integer(a[10])));
+    // what the kernels will read
+    if (spec.flags & BSM_MASK_SEGMENT) {
+      check_id_size(qs, int64_t{s[0]} * s[1], "q_segment_ids");
+      check_id_size(ks, int64_t{s[0]} * s[2], "kv_segment_ids");
+    }
+    if ((spec.flags & BSM_MASK_DENSE) && bits.defined() &&
+        (bits.size(0) < s[1] || bits.size(1) < (int64_t{s[2]} + 31) / 32))
+      value_error("dense_bits must have Sq rows of ceil(Skv / 32) words");
     if ((qs.defined() && !qs.device().is_cuda()) ||
         (ks.defined() && !ks.device().is_cuda()) ||
         (bits.defined() && !bits.device().is_cuda()))
       value_error("segment ids and dense_bits must be CUDA tensors");
+    const at::Device dev(at::kCUDA,
+                         static_cast<c10::DeviceIndex>(
+                             a[10] == Py_None ? c10::cuda::current_device()
+                                              : integer(a[10])));
+    for (const at::Tensor* t : {&qs, &ks, &bits})
+      if (t->defined() && t->device() != dev)
+        value_error("segment ids and dense_bits must be on " +
+                    device_name(dev));
     OnDevice on(dev, a[12]);
     at::Tensor buf =
         empty_on({static_cast<int64_t>(bytes)}, at::kByte, dev);

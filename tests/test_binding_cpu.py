@@ -50,3 +50,32 @@ def test_segment_ids():
                 good.to("meta")):
         with pytest.raises(ValueError, match="q_segment_ids must be"):
             api._check_ids(bad, 2, 10, cpu, "q_segment_ids")
+
+
+@pytest.mark.parametrize("fast", [False, True])
+def test_mask_info_inputs(fast, monkeypatch):
+    """Ids and mask words that the kernels would read past are refused before
+    anything touches a device."""
+    if fast and not api._fast():
+        pytest.skip("the tensor binding is not built")
+    if not fast:
+        monkeypatch.setattr(api, "_fast", lambda: False)
+        # no GPU: the checks come before the buffer's contents matter
+        monkeypatch.setattr(api, "_CUDA", torch.device("cpu"))
+    SEG, DN = api.MASK_SEGMENT, api.MASK_DENSE
+    good = _t(2, 40, dtype=torch.int32)
+    for bad in (good.long(), good[:1], good[:, :39], good[:1].expand(2, 40),
+                good[:, ::2]):
+        for a, b in ((bad, good), (good, bad)):
+            with pytest.raises(ValueError, match="of 80 elements"):
+                api.build_mask_info(SEG, 2, 40, 40, q_segment_ids=a,
+                                    kv_segment_ids=b)
+    words = _t(40, 2, dtype=torch.int32)
+    for bad in (words[:39], words[:, :1]):
+        with pytest.raises(ValueError, match="Sq rows"):
+            api.build_mask_info(DN, 1, 40, 40, dense_bits=bad)
+    with pytest.raises(ValueError, match="must be CUDA tensors"):
+        api.build_mask_info(SEG, 2, 40, 40, q_segment_ids=good,
+                            kv_segment_ids=good)
+    with pytest.raises(ValueError, match="on a CUDA device"):
+        api.build_mask_info(api.MASK_CAUSAL, 1, 40, 40, device="cpu")
