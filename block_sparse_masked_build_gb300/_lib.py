@@ -10,6 +10,7 @@ import ctypes
 import importlib.util
 import os
 import threading
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 # BSM_LIBRARY may point at another build of the same library.
@@ -212,7 +213,8 @@ _FAST_NAMES = ("bsm_mask_info_bytes", "bsm_build_mask_info",
 
 def fast(on_status):
     """_bsm_torch, the library's calls from torch tensors, bound to the loaded
-    library; False where it has not been built (ctypes then serves alone).
+    library; False where it has not been built or does not load (ctypes then
+    serves alone).
     on_status: raises for a failing status."""
     global _fast
     if _fast is None:
@@ -228,8 +230,14 @@ def _load_fast(loaded, on_status):
     if not os.path.exists(path):
         return False
     spec = importlib.util.spec_from_file_location("_bsm_torch", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
+    try:
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except (ImportError, OSError) as e:  # built for another torch or Python
+        warnings.warn(f"{path} does not load ({e}); calls go through ctypes, "
+                      "which is slower: rebuild it", RuntimeWarning,
+                      stacklevel=2)
+        return False
     module.bind(on_status, {
         n: ctypes.cast(getattr(loaded, n), ctypes.c_void_p).value
         for n in _FAST_NAMES})

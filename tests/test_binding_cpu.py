@@ -3,7 +3,8 @@
 import pytest
 import torch
 
-from block_sparse_masked_build_gb300 import api
+from block_sparse_masked_build_gb300 import _lib, api
+from block_sparse_masked_build_gb300 import build as bsm_build
 
 BF = torch.bfloat16
 
@@ -79,3 +80,14 @@ def test_mask_info_inputs(fast, monkeypatch):
                             kv_segment_ids=good)
     with pytest.raises(ValueError, match="on a CUDA device"):
         api.build_mask_info(api.MASK_CAUSAL, 1, 40, 40, device="cpu")
+
+
+def test_a_module_that_does_not_load_leaves_ctypes(monkeypatch, tmp_path):
+    bsm_build.build()
+    _lib.lib()
+    (tmp_path / "_bsm_torch.so").write_bytes(b"built for another machine")
+    monkeypatch.setattr(_lib, "HERE", str(tmp_path))
+    monkeypatch.setattr(_lib, "_fast", None)
+    with pytest.warns(RuntimeWarning, match="does not load"):
+        assert _lib.fast(api._check) is False
+    assert _lib.fast(api._check) is False  # without another attempt
