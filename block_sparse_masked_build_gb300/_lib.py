@@ -192,7 +192,12 @@ def lib():
                     f"{LIB_PATH} is not built: run "
                     "`python -m block_sparse_masked_build_gb300.build` "
                     "(there is no CPU fallback)")
-            loaded = _declare(ctypes.CDLL(LIB_PATH))
+            try:
+                loaded = _declare(ctypes.CDLL(LIB_PATH))
+            except AttributeError as e:  # an older library
+                raise RuntimeError(
+                    f"{LIB_PATH} lacks an entry point of this binding ({e}): "
+                    "rebuild the library") from None
             version = loaded.bsm_version()
             if version != ABI_VERSION:
                 raise RuntimeError(

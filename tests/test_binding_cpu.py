@@ -1,5 +1,7 @@
 """The Python side of the bindings without a GPU: what the checks refuse."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -91,3 +93,12 @@ def test_a_module_that_does_not_load_leaves_ctypes(monkeypatch, tmp_path):
     with pytest.warns(RuntimeWarning, match="does not load"):
         assert _lib.fast(api._check) is False
     assert _lib.fast(api._check) is False  # without another attempt
+
+
+def test_an_older_library_is_named(monkeypatch):
+    bsm_build.build()
+    none = ctypes.CDLL(None)  # has none of the entry points
+    monkeypatch.setattr(_lib, "_lib", None)
+    monkeypatch.setattr(_lib.ctypes, "CDLL", lambda path: none)
+    with pytest.raises(RuntimeError, match="rebuild the library"):
+        _lib.lib()
