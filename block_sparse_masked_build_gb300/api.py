@@ -1012,8 +1012,5 @@ def splash_attention(q, k, v, *, mask_flags: int = MASK_CAUSAL,
             lse = torch.empty((B, H, Sq), dtype=torch.float32,
                               pin_memory=True)
         lse.copy_(ld, non_blocking=True)
-    if stream is None:
-        torch.cuda.current_stream(dev).synchronize()
-    else:
-        stream.synchronize()
+    torch.cuda.current_stream(dev).synchronize()  # (another: see _run_on)
     return out, (lse if want_lse else None)

@@ -108,3 +108,12 @@ def test_refusals_are_the_same(both):  # noqa: F811
 
         both(call)
         assert seen[0] == seen[1]
+
+
+def test_host_tensors_with_the_current_stream_by_handle(both):  # noqa: F811
+    q, k, v, _ = (t.cpu() for t in _tensors())
+    want = bsm.splash_attention(q, k, v, softcap=9.0)
+    for handle in (0, torch.cuda.current_stream().cuda_stream):
+        for r in both(lambda: bsm.splash_attention(q, k, v, softcap=9.0,
+                                                   stream=handle)):
+            same(r, want)
