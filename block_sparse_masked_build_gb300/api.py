@@ -488,7 +488,8 @@ class KVCache:
     """A paged 8-bit key/value cache over four CUDA tensors, which it keeps:
     k_pages, v_pages [num_pages, H_kv, page_size, D] (float8_e4m3fn) and
     k_scale, v_scale [num_pages, H_kv] (float32), all contiguous.  An element
-    is its code times the scale of its page and head."""
+    is its code times the scale of its page and head, which lies between 2^-40
+    and 2^40 wherever a page holds tokens."""
 
     __slots__ = ("_tensors",)
 

@@ -226,7 +226,9 @@ bsm_status bsm_splash_fwd(const void* q, const void* k, const void* v,
  * is more.  As without a modification, a key that a row does not see weighs 0,
  * and 0 times an infinity or NaN in V (in the backward: in any operand) of a
  * key tile that the row's query tile visits is NaN.  A row that sees a NaN
- * score gets NaN for its output and logsumexp. */
+ * score gets NaN for its output and logsumexp.  With a cap a row's weights are
+ * f32 numbers up to 2^90 until they are normalised, and their products with V
+ * are summed in f32: |V| up to 2^20 (about 10^6) is safe at every length. */
 typedef struct bsm_score_mod {
   float softcap;
   const float* alibi_slopes;
@@ -426,8 +428,10 @@ size_t bsm_splash_bwd_mod_workspace_bytes(int32_t B, int32_t H, int32_t H_kv,
  *   k, v              device e4m3 [num_pages][H_kv][page_size][D], contiguous,
  *                     16-byte aligned
  *   k_scale, v_scale  device f32 [num_pages][H_kv], contiguous: an element is
- *                     its code times its page's and head's scale; finite and
- *                     positive wherever a page holds tokens
+ *                     its code times its page's and head's scale; between
+ *                     2^-40 and 2^40 wherever a page holds tokens, as
+ *                     bsm_kv_append leaves them (not checked; the attention
+ *                     joins values whose scales differ by up to 2^80)
  *   page_size         16, 32, 64 or 128; D 64 or 128
  * The memory is the caller's.  A sequence's tokens are found through a page
  * table: entry j of its row is the page of tokens [j page_size, (j + 1)
@@ -446,7 +450,8 @@ typedef struct bsm_kv_cache {
  * e the smallest integer in [-40, 40] with amax <= 448 * 2^e: a page without
  * tokens takes the scale 2^e; one that holds some keeps the larger of its
  * scale and 2^e, and where its scale grows its old codes are rounded again.
- * Codes are element / scale rounded to the nearest e4m3 value (ties to even);
+ * Codes are element / scale rounded to the nearest e4m3 value (ties to even;
+ * a kept scale that is no power of two first makes the quotient an f32);
  * magnitudes above 448 scales (infinities among them) become 448 scales, NaN
  * stays NaN.  Nothing else of the cache is written: not the page's tokens
  * behind the new ones, nor pages that get none.  `lens` is not changed.
