@@ -781,6 +781,11 @@ __device__ __forceinline__ float biased_max(const float* s, float sl8,
   return fmaxf(mx[0], mx[1]);
 }
 
+// Floor of log2(x) for a positive normal x.
+__device__ __forceinline__ float exponent_of(float x) {
+  return static_cast<float>(static_cast<int>(__float_as_uint(x) >> 23) - 127);
+}
+
 // Whether a row saw a key.  With modified scores a sum of NaN counts (and the
 // logsumexp becomes NaN); without, such rows have always had -inf.
 template <int MOD>
@@ -2069,11 +2074,11 @@ __device__ __forceinline__ int segment_distance(const FwdParams& p,
 // each with one 64-key half of the tile.  The arithmetic per score is about
 // twice the unmodified one's and the tensor core waits for it on every entry,
 // so a row's latency is halved.  No running maximum is kept, so the threads of a
-// row share only their sums, in the epilogue (and with a bias the maximum of the
-// unit's first tile); and half 1, whose P goes over columns
+// row share only the maximum of the unit's first tile and, in the epilogue,
+// their sums; and half 1, whose P goes over columns
 // [32, 64) of S (half 0's scores), writes after half 0 has read.  Measured
-// (us): packed S=8192, 2 x 16 heads: cap 50 148, cap 20 167, with a bias 153 and
-// 175 (one thread per row and a running maximum: 172 and 211); causal S=8192,
+// (us): packed S=8192, 2 x 16 heads: cap 50 148, cap 20 171, with a bias 153 and
+// 178 (one thread per row and a running maximum: 172 and 211); causal S=8192,
 // 32/8 heads: cap 50 504, with a bias 518 (560).  A constant reference would be
 // 6 to 12 % faster with a cap alone, but see ref.  What bounds cap 20 is the
 // MUFU pipe (2.5 operations per score: about 540 us at 16 a clock and SM).
@@ -2137,7 +2142,10 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
     // (with a bias the one next to the row), so that a key that outweighs all
     // others there has p = 1 as with a running maximum; with a constant its
     // rounding to bf16 reached the gradients (4.4e-3 in norm instead of 3.3e-3
-    // on short rows).  But it is at least 90 below the upper bound, so p lies
+    // on short rows).  A key that outweighs the others in a later tile has a
+    // rounded p all the same (with a cap alone the first tile is the farthest,
+    // and packed it may hold few of the row's keys: output 2.2e-3 in norm at
+    // S=8192).  The reference is at most 90 below the upper bound, so p lies
     // below 2^90, where 2^18 of them stay inside f32, and the row's largest
     // above 2^-84 (cap_log2 <= 87; 75 with a bias): what is flushed to 0, below
     // 2^-126, weighs 2^-42 of it.
@@ -2284,9 +2292,13 @@ __device__ __forceinline__ void dt_score_cap_role(const FwdParams& p,
         }
         const float l1 = pair->total[r];
         if (!(l1 == 0.f)) {  // (0: it saw nothing, or had no entry)
-          const float mm = fmaxf(ref, pair->ref[r]);
-          const float w0 = ex2_approx(ref - mm);
-          const float w1 = ex2_approx(pair->ref[r] - mm);
+          // by the size of the sums, as the references may lie anywhere below
+          // them (unsorted ids: each pipeline's by the keys of its own tiles)
+          const float r1 = pair->ref[r];
+          const float m0 = l_sum == 0.f ? NEG_INF : ref + exponent_of(l_sum);
+          const float mm = fmaxf(m0, r1 + exponent_of(l1));
+          const float w0 = l_sum == 0.f ? 0.f : ex2_approx(ref - mm);
+          const float w1 = ex2_approx(r1 - mm);
           ref = mm;
 #pragma unroll
           for (int c = 0; c < D / 2; ++c)

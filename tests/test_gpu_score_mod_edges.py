@@ -186,6 +186,29 @@ def test_references_with_absent_segments(rows, flags, slope):
         slopes=slope * torch.tensor([1.0, 8.0]))
 
 
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("slope", [4.0, 0.05, -0.05])
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_whose_keys_lie_in_one_far_tile(D, slope, many):
+    """Unsorted ids; a row's keys all in one KV tile far from it, which one of
+    two pipelines sharing the query tile has, while the other sees none of
+    them and all around the row are keys of another segment."""
+    S = 512
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    H = sms // 2 + 4 if many else 2
+    q, k, v, _ = inputs(f"far{D}{slope}", 1, H, H, S, S, D, 4.0)
+    ids = (np.arange(S, dtype=np.int32) % 2)[None].copy()
+    rows = ids.copy()
+    for j, tile in enumerate((0, 1, 2, 3)):
+        ids[0, 128 * tile + 5:128 * tile + 40:3] = 10 + j
+    rows[0, 3::5] = 10
+    rows[0, 4::5] = 11
+    rows[0, 7::10] = 12
+    rows[0, 9::10] = 13
+    run(q, k, v, v, SG, 0, rows, ids, softcap=30.0, bwd=False,
+        slopes=torch.full((H,), slope))
+
+
 @pytest.mark.parametrize("share", [0.5, 1.0])
 def test_absent_segments_cost_no_walk_over_the_keys(share):
     """Rows whose id no key has: a bias beside the cap needs the distance of
