@@ -1131,10 +1131,12 @@ __global__ void __launch_bounds__(bwd_threads(MOD), 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// D_q = sum_d dO[q, d] * out[q, d]: D / 8 threads per (batch, head, row),
-// each with one 16-byte load of out and of dO (rows and strides are 16-byte
-// aligned), a warp covering 32 / (D / 8) rows per pass of a grid-stride
-// loop.
+// D_q = sum_d dO[q, d] * out[q, d], from the forward's bf16 output: its half
+// step is the larger part of what dQ and dK are off (2.4e-3 in norm of 3.3e-3
+// with modified scores); an f32 output would be twice the bytes to keep.
+// D / 8 threads per (batch, head, row), each with one 16-byte load of out and of
+// dO (rows and strides are 16-byte aligned), a warp covering 32 / (D / 8) rows
+// per pass of a grid-stride loop.
 __global__ void __launch_bounds__(256) bwd_delta_kernel(const BwdParams p) {
   const int gs = p.D / 8;  // threads per row: 16 (D = 128) or 8 (D = 64)
   const int lane = threadIdx.x % 32, sub = lane % gs;
