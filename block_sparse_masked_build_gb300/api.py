@@ -435,8 +435,8 @@ def _check_operands(q, k, v) -> None:
                              "contiguous head dimension")
         if t.dtype not in _BF16_BITS or t.device != dev:
             raise ValueError(f"{name} must be a bfloat16 tensor on {dev}")
-    if not _covers(v, k.shape) or k.shape[0] < q.shape[0] \
-            or k.shape[3] < q.shape[3]:
+    need = (q.shape[0], k.shape[1], k.shape[2], q.shape[3])
+    if not _covers(k, need) or not _covers(v, need):
         raise ValueError("k and v must be [B, H_kv, Skv, D] for q's B and D")
 
 

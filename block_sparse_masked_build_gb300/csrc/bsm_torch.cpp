@@ -166,11 +166,11 @@ bool bf16_bits(const at::Tensor& t) {
   return s == at::kBFloat16 || s == at::kShort || s == at::kUInt16;
 }
 
-// Whether t covers the first sizes of `like` (a larger buffer may serve).
-bool covers(const at::Tensor& t, const at::Tensor& like) {
-  if (t.dim() != like.dim()) return false;
+// Whether t holds the first `sizes` (a larger buffer may serve).
+bool covers(const at::Tensor& t, at::IntArrayRef sizes) {
+  if (t.dim() != static_cast<int64_t>(sizes.size())) return false;
   for (int64_t i = 0; i < t.dim(); ++i)
-    if (t.size(i) < like.size(i)) return false;
+    if (t.size(i) < sizes[i]) return false;
   return true;
 }
 
@@ -191,13 +191,14 @@ void check_operands(const at::Tensor& q, const at::Tensor& k,
       value_error(std::string(name) + " must be a bfloat16 tensor on " +
                   device_name(dev));
   }
-  if (!covers(v, k) || k.size(0) < q.size(0) || k.size(3) < q.size(3))
+  const int64_t need[4] = {q.size(0), k.size(1), k.size(2), q.size(3)};
+  if (!covers(k, need) || !covers(v, need))
     value_error("k and v must be [B, H_kv, Skv, D] for q's B and D");
 }
 
 // A tensor with the shape and device of `like` (bf16).
 void check_like(const at::Tensor& t, const at::Tensor& like, const char* name) {
-  if (t.defined() && (!bf16_bits(t) || !covers(t, like) ||
+  if (t.defined() && (!bf16_bits(t) || !covers(t, like.sizes()) ||
                       t.device() != like.device()))
     value_error(std::string(name) + " must be a bfloat16 tensor of q's shape "
                                     "and device");

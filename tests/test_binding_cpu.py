@@ -19,7 +19,7 @@ def test_operands():
     q, k = _t(2, 4, 10, 64), _t(2, 2, 12, 64)
     api._check_operands(q, k, k)
     api._check_operands(q, k.view(torch.int16), k.view(torch.uint16))
-    api._check_operands(q, _t(3, 2, 12, 64), _t(3, 2, 30, 64))
+    api._check_operands(q, _t(3, 2, 12, 64), _t(2, 2, 30, 64))
     for bad in ((q.half(), k, k), (q, k.float(), k), (q, k, k[:, :, :11]),
                 (q, k, k[:, :1]), (q, k[:1], k[:1]),
                 (q, k[..., :32], k[..., :32]), (q[0], k, k),

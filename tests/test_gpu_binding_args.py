@@ -60,7 +60,7 @@ def test_larger_buffers(both):  # noqa: F811
     q, k, v, _ = _tensors(B=2)
     want = bsm.splash_attention(q[:1], k[:1], v[:1])
     wide = torch.full((2, 3, 300, 64), 7.0, dtype=torch.bfloat16).cuda()
-    longer = torch.cat([v, v], 2)
+    longer = torch.cat([v, v], 2)[:1]
     for got, lse in both(lambda: bsm.splash_attention(q[:1], k, longer,
                                                       out=wide)):
         assert got is wide
