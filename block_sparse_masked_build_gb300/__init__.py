@@ -17,11 +17,16 @@ from .api import (  # noqa: F401
     BsmError,
     KVCache,
     MaskInfo,
+    Rope,
     bsm_build_mask_info,
     bsm_device_status,
     bsm_kv_append,
+    bsm_kv_append_rope,
     bsm_last_error,
     bsm_mask_info_bytes,
+    bsm_norm_rope,
+    bsm_norm_rope_bwd,
+    bsm_norm_rope_bwd_workspace_bytes,
     bsm_pack_dense_mask,
     bsm_paged_attention,
     bsm_paged_attention_workspace_bytes,
@@ -36,6 +41,8 @@ from .api import (  # noqa: F401
     bsm_version,
     build_mask_info,
     kv_append,
+    norm_rope,
+    norm_rope_bwd,
     pack_dense_mask,
     paged_attention,
     splash_attention,

@@ -87,6 +87,24 @@ class KVCacheStruct(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("D", ctypes.c_int32)]
 
 
+class RopeStruct(ctypes.Structure):
+    """bsm_rope: a rotation by position."""
+    _fields_ = [("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("step", ctypes.c_uint64 * 64), ("axis", ctypes.c_uint8 * 64)]
+
+
+class Positions(ctypes.Structure):
+    """bsm_positions: device pointer and axis, batch and token strides."""
+    _fields_ = [("data", ctypes.c_void_p), ("strides", ctypes.c_int64 * 3)]
+
+
+class HeadNorm(ctypes.Structure):
+    """bsm_head_norm: weights of the queries' and keys' norm, and eps."""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("weights_bf16", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -159,6 +177,25 @@ def _declare(lib):
     lib.bsm_kv_append.restype = c.c_int
     lib.bsm_kv_append.argtypes = [kc, vp, c.c_int64, c.c_int32, vp, vp, vp,
                                   vp, c.c_int32, c.c_int32, vp]
+    rp, nm, po = c.POINTER(RopeStruct), c.POINTER(HeadNorm), c.POINTER(
+        Positions)
+    lib.bsm_rope_init.restype = c.c_int
+    lib.bsm_rope_init.argtypes = [rp, c.c_int32, c.c_int32,
+                                  c.POINTER(c.c_double),
+                                  c.POINTER(c.c_int32), c.c_int32]
+    lib.bsm_norm_rope.restype = c.c_int
+    lib.bsm_norm_rope.argtypes = [vp, vp, *[c.c_int32] * 5, nm, rp, po, vp,
+                                  vp, vp]
+    lib.bsm_norm_rope_bwd_workspace_bytes.restype = c.c_size_t
+    lib.bsm_norm_rope_bwd_workspace_bytes.argtypes = []
+    lib.bsm_norm_rope_bwd.restype = c.c_int
+    lib.bsm_norm_rope_bwd.argtypes = [
+        vp, vp, vp, vp, *[c.c_int32] * 5, nm, rp, po, vp, vp, vp, vp, vp,
+        c.c_size_t, vp]
+    lib.bsm_kv_append_rope.restype = c.c_int
+    lib.bsm_kv_append_rope.argtypes = [
+        kc, vp, c.c_int64, c.c_int32, vp, vp, vp, vp, c.c_int32, c.c_int32,
+        nm, rp, po, vp]
     lib.bsm_paged_attention_workspace_bytes.restype = c.c_size_t
     lib.bsm_paged_attention_workspace_bytes.argtypes = []
     lib.bsm_paged_attention.restype = c.c_int
@@ -213,7 +250,9 @@ _FAST_NAMES = ("bsm_mask_info_bytes", "bsm_build_mask_info",
                "bsm_splash_bwd_workspace_bytes",
                "bsm_splash_bwd_mod_workspace_bytes", "bsm_kv_append",
                "bsm_paged_attention", "bsm_splash_fwd_workspace_bytes",
-               "bsm_paged_attention_workspace_bytes")
+               "bsm_paged_attention_workspace_bytes", "bsm_norm_rope",
+               "bsm_norm_rope_bwd", "bsm_norm_rope_bwd_workspace_bytes",
+               "bsm_kv_append_rope")
 
 
 def fast(on_status):

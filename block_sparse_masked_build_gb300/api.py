@@ -16,7 +16,8 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import I64x3, KVCacheStruct, MaskInfoStruct, MaskSpec, ScoreMod
+from ._lib import (HeadNorm, I64x3, KVCacheStruct, MaskInfoStruct, MaskSpec,
+                   Positions, RopeStruct, ScoreMod)
 
 MASK_CAUSAL = 1
 MASK_LOCAL = 2
@@ -554,11 +555,16 @@ def bsm_kv_append(cache: KVCache, page_table, lens, k_new, v_new, n_new=None,
     """Append k_new, v_new [B,H_kv,T,D] (bf16, any strides that are multiples
     of 8) to sequences of lens [B] tokens, n_new [B] of them each (None: T).
     page_table int32 [B, max_pages]; lens is left as it is."""
+    _append(cache, page_table, lens, k_new, v_new, n_new, None, stream)
+
+
+def _append(cache, page_table, lens, k_new, v_new, n_new, turn,
+            stream) -> None:
     dev = cache.device
     if _elsewhere(dev):
         with torch.cuda.device(dev):
-            return bsm_kv_append(cache, page_table, lens, k_new, v_new, n_new,
-                                 stream)
+            return _append(cache, page_table, lens, k_new, v_new, n_new, turn,
+                           stream)
     s = cache.struct
     if k_new.dim() != 4:
         raise ValueError("k_new must be [B, H_kv, T, D]")
@@ -570,10 +576,196 @@ def bsm_kv_append(cache: KVCache, page_table, lens, k_new, v_new, n_new=None,
     if dev.type != "cuda":
         raise ValueError("the cache must be on a CUDA device")
     views, at = _views(k_new, v_new)
-    _check(_lib.lib().bsm_kv_append(
-        s, page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
-        lens.data_ptr(), None if n_new is None else n_new.data_ptr(), at,
-        at + 32, B, T, _stream_handle(stream)))
+    args = (s, page_table.data_ptr(), page_table.stride(0),
+            page_table.shape[1], lens.data_ptr(),
+            None if n_new is None else n_new.data_ptr(), at, at + 32, B, T)
+    if turn is None:
+        _check(_lib.lib().bsm_kv_append(*args, _stream_handle(stream)))
+    else:
+        _check(_lib.lib().bsm_kv_append_rope(
+            *args, *_turn(*turn, B, T, s.D, dev), _stream_handle(stream)))
+
+
+# ------------------------------------------------------ norm and rotation
+
+class Rope:
+    """A rotation of a head's first ``dim`` elements by position: pair i,
+    (x[i], x[i + dim / 2]) or with ``interleaved`` (x[2 i], x[2 i + 1]), turns
+    by position * inv_freq[i], where inv_freq is given ([dim / 2] numbers) or
+    base^(-2 i / dim).  With ``axes`` ([dim / 2] whole numbers from 0 to 3) a
+    position has several numbers, and pair i goes by number axes[i].  Angles
+    are exact however far the position.  Made once and kept; it holds no
+    device memory."""
+
+    __slots__ = ("_struct", "_address")
+
+    def __init__(self, dim: int, base: float = 10000.0, *, inv_freq=None,
+                 axes=None, interleaved: bool = False):
+        dim = int(dim)
+        half = dim // 2
+        if inv_freq is None:
+            inv_freq = [float(base) ** (-2.0 * i / dim) for i in range(half)]
+        freq = [float(f) for f in inv_freq]
+        axis = [0] * half if axes is None else [int(i) for i in axes]
+        if len(freq) != half or len(axis) != half:
+            raise ValueError(f"inv_freq and axes must have dim / 2 = {half} "
+                             "elements")
+        self._struct = RopeStruct()
+        _check(_lib.lib().bsm_rope_init(
+            self._struct, dim, bool(interleaved),
+            (ctypes.c_double * half)(*freq), (ctypes.c_int32 * half)(*axis),
+            max(axis, default=0) + 1))
+        self._address = ctypes.addressof(self._struct)
+
+    dim = property(lambda self: self._struct.dim)
+    axes = property(lambda self: self._struct.axes)
+    interleaved = property(lambda self: bool(self._struct.interleaved))
+
+
+def _rope_address(rope) -> int:
+    if rope is None:
+        return 0
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope")
+    return rope._address
+
+
+def _check_rows(t, shape, dev, name: str) -> None:
+    if (t.dtype != torch.bfloat16 or t.dim() != 4 or t.shape != shape
+            or t.device != dev or t.stride(3) != 1):
+        raise ValueError(f"{name} must be a bfloat16 tensor {list(shape)} "
+                         f"with a contiguous head dimension on {dev}")
+
+
+def _check_rows_of(q, k, names=("q", "k")):
+    """Shape (B, H, S, D, H_kv) and device of queries and keys (or None)."""
+    if q.dim() != 4:
+        raise ValueError(f"{names[0]} must be [B, H, S, D]")
+    B, H, S, D = q.shape
+    _check_rows(q, q.shape, q.device, names[0])
+    Hkv = 0
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError(f"{names[1]} must be [B, H_kv, S, D]")
+        Hkv = k.shape[1]
+        _check_rows(k, (B, Hkv, S, D), q.device, names[1])
+    if not q.is_cuda:
+        raise ValueError(f"{names[0]} must be a CUDA tensor")
+    return B, H, S, D, Hkv
+
+
+def _turn(rope, positions, q_weight, k_weight, eps, B: int, S: int, D: int,
+          dev):
+    """(bsm_head_norm, bsm_rope, bsm_positions), None for what is not there."""
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        if (w.dtype not in (torch.float32, torch.bfloat16)
+                or w.shape != (D,) or not w.is_contiguous()
+                or w.device != dev):
+            raise ValueError(f"{name} must be a contiguous float32 or "
+                             f"bfloat16 tensor [{D}] on {dev}")
+    given = [w for w in (q_weight, k_weight) if w is not None]
+    if eps is None and given:
+        raise ValueError("weights are the norm's: give eps")
+    if len({w.dtype for w in given}) > 1:
+        raise ValueError("q_weight and k_weight must have one type")
+    address = _rope_address(rope)
+    if not address and eps is None:
+        raise ValueError("give a rope, or eps for the norm")
+    norm = None if eps is None else HeadNorm(
+        _ptr(q_weight), _ptr(k_weight),
+        bool(given) and given[0].dtype == torch.bfloat16, float(eps))
+    pos = None
+    if positions is not None:
+        if rope is None:
+            raise ValueError("positions without a rope")
+        p = positions
+        if (p.dtype != torch.int32 or p.device != dev
+                or not (p.shape == (rope.axes, B, S)
+                        or rope.axes == 1 and p.shape == (B, S))):
+            raise ValueError("positions must be an int32 tensor "
+                             f"{[rope.axes, B, S]} (the first 1 may be left "
+                             f"out) on {dev}")
+        st = (0, *p.stride())[-3:]
+        pos = Positions(p.data_ptr(), (ctypes.c_int64 * 3)(*st))
+    return norm, None if rope is None else rope._struct, pos
+
+
+def bsm_norm_rope(q, k, rope, positions, q_weight, k_weight, eps, out, k_out,
+                  stream=None) -> None:
+    """q, out [B,H,S,D] and k, k_out [B,H_kv,S,D] or None (bf16, CUDA); out
+    may be q, k_out k.  rope None: no rotation; eps None: no norm."""
+    if q.is_cuda and _elsewhere(q.device):
+        with torch.cuda.device(q.device):
+            return bsm_norm_rope(q, k, rope, positions, q_weight, k_weight,
+                                 eps, out, k_out, stream)
+    B, H, S, D, Hkv = _check_rows_of(q, k)
+    norm, r, pos = _turn(rope, positions, q_weight, k_weight, eps, B, S, D,
+                         q.device)
+    _check_rows(out, q.shape, q.device, "out")
+    if k is not None:
+        _check_rows(k_out, k.shape, q.device, "k_out")
+    views, at = _views(q, k, out, k_out if k is not None else None)
+    _check(_lib.lib().bsm_norm_rope(at, at + 32, B, H, Hkv, S, D, norm, r, pos,
+                                    at + 64, at + 96, _stream_handle(stream)))
+
+
+def bsm_norm_rope_bwd_workspace_bytes() -> int:
+    return int(_lib.lib().bsm_norm_rope_bwd_workspace_bytes())
+
+
+_rope_workspaces: dict = {}
+
+
+def bsm_norm_rope_bwd(gq, gk, q, k, rope, positions, q_weight, k_weight, eps,
+                      dq, dk, dq_weight=None, dk_weight=None, stream=None,
+                      workspace=None) -> None:
+    """Gradients dq, dk of bsm_norm_rope's q and k for those of its results,
+    and of the weights (f32 [D]) where given.  q and k may be None without a
+    norm; gk, dk where there are no keys."""
+    if gq.is_cuda and _elsewhere(gq.device):
+        with torch.cuda.device(gq.device):
+            return bsm_norm_rope_bwd(gq, gk, q, k, rope, positions, q_weight,
+                                     k_weight, eps, dq, dk, dq_weight,
+                                     dk_weight, stream, workspace)
+    B, H, S, D, Hkv = _check_rows_of(gq, gk, ("gq", "gk"))
+    dev = gq.device
+    norm, r, pos = _turn(rope, positions, q_weight, k_weight, eps, B, S, D,
+                         dev)
+    if norm is not None and (q is None or (gk is not None and k is None)):
+        raise ValueError("the norm's backward needs q and k")
+    for t, like, name in ((q, gq, "q"), (dq, gq, "dq"), (k, gk, "k"),
+                          (dk, gk, "dk")):
+        if t is not None and like is None:
+            raise ValueError(f"{name} without the keys")
+        if t is not None:
+            _check_rows(t, like.shape, dev, name)
+    if dq is None or (gk is not None and dk is None):
+        raise ValueError("dq and dk are written")
+    for t, name in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
+        if t is not None and (t.dtype != torch.float32 or t.shape != (D,)
+                              or not t.is_contiguous() or t.device != dev):
+            raise ValueError(f"{name} must be a contiguous float32 tensor "
+                             f"[{D}] on {dev}")
+    if workspace is None and (dq_weight is not None or dk_weight is not None):
+        workspace = _scratch(bsm_norm_rope_bwd_workspace_bytes(), dev, stream,
+                             _rope_workspaces)
+    views, at = _views(gq, gk, q, k, dq, dk)
+    _check(_lib.lib().bsm_norm_rope_bwd(
+        at, at + 32, at + 64, at + 96, B, H, Hkv, S, D, norm, r, pos, at + 128,
+        at + 160, _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace),
+        0 if workspace is None else
+        workspace.numel() * workspace.element_size(), _stream_handle(stream)))
+
+
+def bsm_kv_append_rope(cache: KVCache, page_table, lens, k_new, v_new,
+                       n_new=None, rope=None, positions=None, k_weight=None,
+                       eps=None, stream=None) -> None:
+    """bsm_kv_append with the keys normalised (eps given) and rotated (rope
+    given) on the way; positions [axes,B,T], or None: lens[b] + t."""
+    _append(cache, page_table, lens, k_new, v_new, n_new,
+            (rope, positions, None, k_weight, eps), stream)
 
 
 def bsm_paged_attention_workspace_bytes() -> int:
@@ -760,21 +952,100 @@ def pack_dense_mask(mask: torch.Tensor, stream=None) -> torch.Tensor:
     return words
 
 
+def norm_rope(q, k=None, *, rope: Rope | None = None, positions=None,
+              q_weight=None, k_weight=None, eps: float | None = None,
+              out=None, k_out=None, stream=None):
+    """Root-mean-square norm and rotation of query and key heads in one pass,
+    ahead of :func:`splash_attention` or :func:`kv_append`: q [B, H, S, D], k
+    [B, H_kv, S, D] or None (bf16, CUDA, D 64 or 128).
+
+    ``eps`` (None: no norm) normalises each row, x / sqrt(mean(x^2) + eps),
+    times ``q_weight`` or ``k_weight`` ([D], float32 or bfloat16; None: ones).
+    Then ``rope`` turns it by the token's position: ``positions`` int32 [B, S],
+    or [axes, B, S] with several axes (any strides; None: 0 .. S - 1).  In f32,
+    rounded once.  ``out`` may be q itself, ``k_out`` k.  Returns (q', k')."""
+    s = _other_stream(stream, q.device) if q.is_cuda else None
+    if s is not None:
+        return _run_on(s, lambda: norm_rope(
+            q, k, rope=rope, positions=positions, q_weight=q_weight,
+            k_weight=k_weight, eps=eps, out=out, k_out=k_out))
+    address = _rope_address(rope)
+    fast = _fast()
+    if fast:
+        return fast.norm_rope(q, k, address, positions, q_weight, k_weight,
+                              eps, out, k_out, _fast_stream(stream))
+    _check_rows_of(q, k)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k is None and k_out is not None:
+        raise ValueError("k_out without the keys")
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    bsm_norm_rope(q, k, rope, positions, q_weight, k_weight, eps, out, k_out,
+                  stream)
+    return out, k_out
+
+
+def norm_rope_bwd(gq, gk=None, q=None, k=None, *, rope: Rope | None = None,
+                  positions=None, q_weight=None, k_weight=None,
+                  eps: float | None = None, stream=None):
+    """Backward of :func:`norm_rope`: for the gradients gq, gk of its results
+    (gk None without keys) and its inputs q and k (needed with a norm alone),
+    (dq, dk, dq_weight, dk_weight); the weights' gradients are float32 [D], None
+    for a weight that is not given."""
+    s = _other_stream(stream, gq.device) if gq.is_cuda else None
+    if s is not None:
+        return _run_on(s, lambda: norm_rope_bwd(
+            gq, gk, q, k, rope=rope, positions=positions, q_weight=q_weight,
+            k_weight=k_weight, eps=eps))
+    address = _rope_address(rope)
+    fast = _fast()
+    if fast:
+        return fast.norm_rope_bwd(gq, gk, q, k, address, positions, q_weight,
+                                  k_weight, eps, _fast_stream(stream))
+    D = _check_rows_of(gq, gk, ("gq", "gk"))[3]
+    if k_weight is not None and gk is None:
+        raise ValueError("k_weight without the keys")
+    dq, dk = (None if g is None else
+              torch.empty(g.shape, dtype=g.dtype, device=g.device)
+              for g in (gq, gk))
+    dqw, dkw = (None if w is None else
+                torch.empty(D, dtype=torch.float32, device=gq.device)
+                for w in (q_weight, k_weight))
+    bsm_norm_rope_bwd(gq, gk, q, k, rope, positions, q_weight, k_weight, eps,
+                      dq, dk, dqw, dkw, stream)
+    return dq, dk, dqw, dkw
+
+
 def kv_append(cache: KVCache, page_table, lens, k_new, v_new, *, n_new=None,
-              stream=None) -> None:
+              rope: Rope | None = None, positions=None, k_weight=None,
+              eps: float | None = None, stream=None) -> None:
     """Append new tokens' keys and values (bf16 [B, H_kv, T, D]) to the 8-bit
     cache: sequence b, which holds lens[b] tokens, gets its first n_new[b]
     (None: all T).  One scale per page and head, a power of two; a page that
     already holds tokens keeps or raises its scale (include/bsm.h has the
     rule).  A page that the call writes belongs to one sequence only; pages
     that sequences share are full ones.  ``lens`` is not changed: advance it
-    before attending."""
+    before attending.
+
+    With ``eps`` or ``rope`` the keys are normalised and rotated on the way, as
+    :func:`norm_rope` does but rounded only once, to the 8 bits; ``positions``
+    int32 [B, T], or [axes, B, T] (None: the tokens' places lens[b] + t)."""
+    turned = eps is not None or rope is not None or positions is not None \
+        or k_weight is not None
     fast = _fast()
     if fast:
-        return fast.kv_append(
-            *cache._tensors, page_table, lens, k_new, v_new, n_new,
-            _fast_stream(stream))
-    bsm_kv_append(cache, page_table, lens, k_new, v_new, n_new, stream)
+        args = (*cache._tensors, page_table, lens, k_new, v_new, n_new,
+                _fast_stream(stream))
+        if not turned:
+            return fast.kv_append(*args)
+        return fast.kv_append(*args, _rope_address(rope), positions, k_weight,
+                              eps)
+    if turned:
+        bsm_kv_append_rope(cache, page_table, lens, k_new, v_new, n_new, rope,
+                           positions, k_weight, eps, stream)
+    else:
+        bsm_kv_append(cache, page_table, lens, k_new, v_new, n_new, stream)
 
 
 def paged_attention(q, cache: KVCache, page_table, lens, *,

@@ -294,6 +294,73 @@ bsm_status check_view(const bsm_tensor* t, int64_t B, int64_t heads, int64_t S,
   return BSM_OK;
 }
 
+// A norm, a rotation and positions of rows of D elements: at least one of the
+// first two.
+bsm_status check_turn(const bsm_head_norm* norm, const bsm_rope* rope,
+                      const bsm_positions* pos, int32_t D,
+                      bsm::TurnParams* t) {
+  *t = bsm::TurnParams{};
+  if (norm == nullptr && rope == nullptr)
+    return fail(BSM_ERR_INVALID_ARG, "neither a norm nor a rotation");
+  if (norm != nullptr) {
+    if (!(norm->eps >= 0.f) || !std::isfinite(norm->eps))
+      return fail(BSM_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    const uintptr_t low = norm->weights_bf16 ? 1u : 3u;
+    for (const void* w : {norm->q_weight, norm->k_weight})
+      if ((reinterpret_cast<uintptr_t>(w) & low) != 0)
+        return fail(BSM_ERR_INVALID_ARG,
+                    "weights must be aligned to their element");
+    t->norm = 1;
+    t->eps = norm->eps;
+    t->q_weight = norm->q_weight;
+    t->k_weight = norm->k_weight;
+    t->weights_bf16 = norm->weights_bf16 != 0;
+  }
+  if (rope == nullptr) {
+    if (pos != nullptr && pos->data != nullptr)
+      return fail(BSM_ERR_INVALID_ARG, "positions without a rotation");
+    return BSM_OK;
+  }
+  if (rope->dim < 16 || rope->dim > 128 || rope->dim % 16 != 0 ||
+      rope->axes < 1 || rope->axes > 4)
+    return fail(BSM_ERR_INVALID_ARG, "a bsm_rope that bsm_rope_init did not fill");
+  if (rope->dim > D)
+    return fail(BSM_ERR_INVALID_ARG, "the rotation is wider than head_dim");
+  for (int i = 0; i < rope->dim / 2; ++i)
+    if (rope->axis[i] >= rope->axes)
+      return fail(BSM_ERR_INVALID_ARG, "a bsm_rope that bsm_rope_init did not fill");
+  t->rope = *rope;
+  if (pos != nullptr && pos->data != nullptr) {
+    if ((reinterpret_cast<uintptr_t>(pos->data) & 3u) != 0)
+      return fail(BSM_ERR_INVALID_ARG, "positions must be 4-byte aligned");
+    t->pos = pos->data;
+    t->pos_sa = pos->strides[0];
+    t->pos_sb = pos->strides[1];
+    t->pos_ss = pos->strides[2];
+  }
+  return BSM_OK;
+}
+
+// The sizes of a norm and rotation; rows are counted in 31 bits.
+bsm_status check_rows(int32_t B, int32_t H, int32_t H_kv, int32_t S,
+                      int32_t D) {
+  if (B < 0 || H < 0 || H_kv < 0 || S < 0)
+    return fail(BSM_ERR_INVALID_ARG, "negative size");
+  if (D != 64 && D != 128)
+    return fail(BSM_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  const double rows = static_cast<double>(B) * S *
+                      (static_cast<double>(H) + H_kv);
+  if (rows > 2147483647.0 || static_cast<double>(B) * S > 2147483647.0)
+    return fail(BSM_ERR_UNSUPPORTED, "more than 2^31 - 1 rows");
+  return BSM_OK;
+}
+
+bsm::RowView row_view(const bsm_tensor* t) {
+  if (t == nullptr) return bsm::RowView{nullptr, 0, 0, 0};
+  return bsm::RowView{static_cast<uint16_t*>(t->data), t->strides[0],
+                      t->strides[1], t->strides[2]};
+}
+
 // A new epoch for every mask-info build (40 bits, never 0), starting at a
 // value that differs between processes, so that a ticket word left in a
 // reused buffer by an earlier build never matches.
@@ -857,12 +924,150 @@ bsm_status bsm_splash_bwd_mod(const bsm_tensor* q, const bsm_tensor* k,
   return BSM_OK;
 }
 
-bsm_status bsm_kv_append(const bsm_kv_cache* cache, const int32_t* page_table,
-                         int64_t table_stride, int32_t max_pages,
-                         const int32_t* lens, const int32_t* n_new,
-                         const bsm_tensor* k_new, const bsm_tensor* v_new,
-                         int32_t B, int32_t T, void* stream) {
+bsm_status bsm_rope_init(bsm_rope* rope, int32_t dim, int32_t interleaved,
+                         const double* inv_freq, const int32_t* axis,
+                         int32_t axes) {
   g_last_error.clear();
+  if (rope == nullptr || inv_freq == nullptr)
+    return fail(BSM_ERR_INVALID_ARG, "NULL rope or inv_freq");
+  if (dim < 16 || dim > 128 || dim % 16 != 0)
+    return fail(BSM_ERR_INVALID_ARG,
+                "a rotation's dim must be a multiple of 16 from 16 to 128");
+  if (axes < 1 || axes > 4)
+    return fail(BSM_ERR_INVALID_ARG, "axes must be from 1 to 4");
+  bsm_rope r = {};
+  r.dim = dim;
+  r.interleaved = interleaved != 0;
+  r.axes = axes;
+  for (int i = 0; i < dim / 2; ++i) {
+    if (!(std::fabs(inv_freq[i]) <= 64.0))
+      return fail(BSM_ERR_INVALID_ARG, "inv_freq must be within [-64, 64]");
+    const int32_t a = axis != nullptr ? axis[i] : 0;
+    if (a < 0 || a >= axes)
+      return fail(BSM_ERR_INVALID_ARG, "axis must be within [0, axes)");
+    r.axis[i] = static_cast<uint8_t>(a);
+    // whole turns dropped, in units of 2^-64 (2^64 itself, which a fraction
+    // next to 1 rounds to, is 0 turns)
+    const double turns = inv_freq[i] * 0.15915494309189535;
+    const double part = std::ldexp(turns - std::floor(turns), 64);
+    r.step[i] = part < 0x1p64 ? static_cast<uint64_t>(part) : 0;
+  }
+  *rope = r;
+  return BSM_OK;
+}
+
+bsm_status bsm_norm_rope(const bsm_tensor* q, const bsm_tensor* k, int32_t B,
+                         int32_t H, int32_t H_kv, int32_t S, int32_t D,
+                         const bsm_head_norm* norm, const bsm_rope* rope,
+                         const bsm_positions* pos, const bsm_tensor* q_out,
+                         const bsm_tensor* k_out, void* stream) {
+  g_last_error.clear();
+  bsm_status s = check_rows(B, H, H_kv, S, D);
+  if (s != BSM_OK) return s;
+  bsm::NormRopeParams p = {};
+  s = check_turn(norm, rope, pos, D, &p.turn);
+  if (s != BSM_OK) return s;
+  if (q == nullptr || q_out == nullptr ||
+      (H_kv > 0 && (k == nullptr || k_out == nullptr)))
+    return fail(BSM_ERR_INVALID_ARG, "NULL tensor view");
+  if (B == 0 || S == 0 || H + static_cast<int64_t>(H_kv) == 0) return BSM_OK;
+  if (H > 0) {
+    s = check_view(q, B, H, S, "q");
+    if (s == BSM_OK) s = check_view(q_out, B, H, S, "q_out");
+  }
+  if (s == BSM_OK && H_kv > 0) {
+    s = check_view(k, B, H_kv, S, "k");
+    if (s == BSM_OK) s = check_view(k_out, B, H_kv, S, "k_out");
+  }
+  int num_sms = 0;
+  if (s == BSM_OK) s = check_device(&num_sms);
+  if (s != BSM_OK) return s;
+  p.B = B;
+  p.S = S;
+  p.D = D;
+  p.heads[0] = H;
+  p.heads[1] = H_kv;
+  p.x[0] = row_view(q);
+  p.x[1] = row_view(k);
+  p.out[0] = row_view(q_out);
+  p.out[1] = row_view(k_out);
+  const cudaError_t e =
+      bsm::launch_norm_rope(p, num_sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "norm_rope launch");
+  return BSM_OK;
+}
+
+size_t bsm_norm_rope_bwd_workspace_bytes(void) {
+  return static_cast<size_t>(bsm::kNormRopeMaxBlocks) * 128 * sizeof(float);
+}
+
+bsm_status bsm_norm_rope_bwd(const bsm_tensor* gq, const bsm_tensor* gk,
+                             const bsm_tensor* q, const bsm_tensor* k,
+                             int32_t B, int32_t H, int32_t H_kv, int32_t S,
+                             int32_t D, const bsm_head_norm* norm,
+                             const bsm_rope* rope, const bsm_positions* pos,
+                             const bsm_tensor* dq, const bsm_tensor* dk,
+                             float* dq_weight, float* dk_weight,
+                             void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  g_last_error.clear();
+  bsm_status s = check_rows(B, H, H_kv, S, D);
+  if (s != BSM_OK) return s;
+  bsm::NormRopeParams p = {};
+  s = check_turn(norm, rope, pos, D, &p.turn);
+  if (s != BSM_OK) return s;
+  const bool keys = H_kv > 0;
+  if (gq == nullptr || dq == nullptr || (keys && (gk == nullptr || dk == nullptr)) ||
+      (norm != nullptr && (q == nullptr || (keys && k == nullptr))))
+    return fail(BSM_ERR_INVALID_ARG, "NULL tensor view");
+  const bool dw = dq_weight != nullptr || dk_weight != nullptr;
+  if (dw && norm == nullptr)
+    return fail(BSM_ERR_INVALID_ARG, "weight gradients without a norm");
+  if (((reinterpret_cast<uintptr_t>(dq_weight) |
+        reinterpret_cast<uintptr_t>(dk_weight)) & 3u) != 0)
+    return fail(BSM_ERR_INVALID_ARG, "weight gradients must be 4-byte aligned");
+  if (dw && (workspace == nullptr || !aligned16(workspace) ||
+             workspace_bytes < bsm_norm_rope_bwd_workspace_bytes()))
+    return fail(BSM_ERR_INVALID_ARG,
+                "workspace must be >= bsm_norm_rope_bwd_workspace_bytes() "
+                "bytes, 16-byte aligned");
+  const bool rows = B > 0 && S > 0 && H + static_cast<int64_t>(H_kv) > 0;
+  if (!rows && !dw) return BSM_OK;
+  const bsm_tensor* views[2][3] = {{gq, dq, q}, {gk, dk, k}};
+  static const char* const names[2][3] = {{"gq", "dq", "q"}, {"gk", "dk", "k"}};
+  for (int i = 0; i < 2 && rows; ++i)
+    for (int j = 0; j < (norm != nullptr ? 3 : 2) && (i ? H_kv : H) > 0; ++j)
+      if (s == BSM_OK)
+        s = check_view(views[i][j], B, i ? H_kv : H, S, names[i][j]);
+  int num_sms = 0;
+  if (s == BSM_OK) s = check_device(&num_sms);
+  if (s != BSM_OK) return s;
+  p.B = B;
+  p.S = S;
+  p.D = D;
+  p.heads[0] = H;
+  p.heads[1] = H_kv;
+  for (int i = 0; i < 2; ++i) {
+    p.g[i] = row_view(views[i][0]);
+    p.out[i] = row_view(views[i][1]);
+    p.x[i] = row_view(views[i][2]);
+  }
+  p.dw[0] = dq_weight;
+  p.dw[1] = dk_weight;
+  p.partial = static_cast<float*>(workspace);
+  const cudaError_t e =
+      bsm::launch_norm_rope_bwd(p, num_sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "norm_rope_bwd launch");
+  return BSM_OK;
+}
+
+namespace {
+// bsm_kv_append, and bsm_kv_append_rope with `turn`.
+bsm_status append(const bsm_kv_cache* cache, const int32_t* page_table,
+                  int64_t table_stride, int32_t max_pages, const int32_t* lens,
+                  const int32_t* n_new, const bsm_tensor* k_new,
+                  const bsm_tensor* v_new, int32_t B, int32_t T,
+                  const bsm::TurnParams* turn, void* stream) {
   bsm_status s = check_cache(cache, table_stride, max_pages, B, T);
   if (s != BSM_OK) return s;
   if (k_new == nullptr || v_new == nullptr)
@@ -900,10 +1105,39 @@ bsm_status bsm_kv_append(const bsm_kv_cache* cache, const int32_t* page_table,
   p.v_sb = v_new->strides[0];
   p.v_sh = v_new->strides[1];
   p.v_ss = v_new->strides[2];
-  const cudaError_t e =
-      bsm::launch_kv_append(p, static_cast<cudaStream_t>(stream));
+  const auto st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = turn != nullptr
+                            ? bsm::launch_kv_append_rope(p, *turn, st)
+                            : bsm::launch_kv_append(p, st);
   if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
   return BSM_OK;
+}
+}  // namespace
+
+bsm_status bsm_kv_append(const bsm_kv_cache* cache, const int32_t* page_table,
+                         int64_t table_stride, int32_t max_pages,
+                         const int32_t* lens, const int32_t* n_new,
+                         const bsm_tensor* k_new, const bsm_tensor* v_new,
+                         int32_t B, int32_t T, void* stream) {
+  g_last_error.clear();
+  return append(cache, page_table, table_stride, max_pages, lens, n_new, k_new,
+                v_new, B, T, nullptr, stream);
+}
+
+bsm_status bsm_kv_append_rope(const bsm_kv_cache* cache,
+                              const int32_t* page_table, int64_t table_stride,
+                              int32_t max_pages, const int32_t* lens,
+                              const int32_t* n_new, const bsm_tensor* k_new,
+                              const bsm_tensor* v_new, int32_t B, int32_t T,
+                              const bsm_head_norm* norm, const bsm_rope* rope,
+                              const bsm_positions* pos, void* stream) {
+  g_last_error.clear();
+  if (cache == nullptr) return fail(BSM_ERR_INVALID_ARG, "cache is NULL");
+  bsm::TurnParams turn;
+  const bsm_status s = check_turn(norm, rope, pos, cache->D, &turn);
+  if (s != BSM_OK) return s;
+  return append(cache, page_table, table_stride, max_pages, lens, n_new, k_new,
+                v_new, B, T, &turn, stream);
 }
 
 size_t bsm_paged_attention_workspace_bytes(void) {

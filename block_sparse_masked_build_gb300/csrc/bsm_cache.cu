@@ -23,6 +23,7 @@
 
 #include "bsm_internal.h"
 #include "bsm_ptx.cuh"
+#include "bsm_rope.cuh"
 
 namespace bsm {
 
@@ -226,6 +227,168 @@ __global__ void __launch_bounds__(kAppendThreads, NCH <= 8 ? 8 : 4)
                              f16_lo(f1) * ratio, f16_hi(f1) * ratio);
       }
       *reinterpret_cast<uint2*>(dst + c * 8) = make_uint2(r[0], r[1]);
+    }
+  }
+  if (threadIdx.x == 0) *scale_at = scale;
+}
+
+// The same with the keys normalised and rotated first, in f32 from the load to
+// the rounding to e4m3.  A token's row lies in D / 8 neighbouring lanes, eight
+// elements each; the partner of a lane's elements is in the lane half a
+// rotation away (or, for neighbouring pairs, in the lane itself), which is the
+// one exchange beside the norm's sum.  A thread's pieces are all of one place
+// in the row, so it reads its weights and frequencies once.
+constexpr int kTurnThreads = 256;
+
+template <int D, int NCH>
+__global__ void __launch_bounds__(kTurnThreads, 2)
+    kv_append_rope_kernel(const AppendParams p,
+                          const __grid_constant__ TurnParams turn) {
+  constexpr int kPer = D / 8;  // pieces of a token's row
+  const int b = blockIdx.z;
+  const int h = blockIdx.y >> 1;
+  const bool is_v = blockIdx.y & 1;
+  const int len = p.lens[b];
+  const int n = p.n_new != nullptr ? p.n_new[b] : p.T;
+  const int capacity = p.max_pages * p.page_size;
+  if (len < 0 || n < 0 || n > p.T || len > capacity - n) {
+    if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0)
+      record_bad_index(b, -1, len < 0 || len > capacity ? len : n);
+    return;  // nothing of such a sequence is written
+  }
+  const int slot = len / p.page_size + blockIdx.x;
+  const int tok0 = slot * p.page_size;
+  const int lo = max(len, tok0) - tok0;  // new tokens [lo, hi) of the page
+  const int hi = min(len + n - tok0, p.page_size);
+  if (lo >= hi) return;
+  const int pid = p.table[static_cast<int64_t>(b) * p.table_stride + slot];
+  const int piece = threadIdx.x % kPer, row0 = threadIdx.x / kPer;
+  constexpr int kRows = kTurnThreads / kPer;  // rows of one step
+  const uint16_t* src = is_v ? p.v_new : p.k_new;
+  const int64_t sb = is_v ? p.v_sb : p.k_sb, sh = is_v ? p.v_sh : p.k_sh,
+                ss = is_v ? p.v_ss : p.k_ss;
+  src += b * sb + h * sh + piece * 8;
+  uint4 raw[NCH];
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int tok = row0 + i * kRows;
+    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tok >= lo && tok < hi)
+      raw[i] = *reinterpret_cast<const uint4*>(src + (tok0 + tok - len) * ss);
+  }
+  // the rotation of this thread's place in the row
+  const bsm_rope& rope = turn.rope;
+  const int half = rope.dim / 16;  // pieces of half a rotation
+  const bool turned = !is_v && piece < 2 * half;
+  const bool pairs = rope.interleaved != 0;
+  const int lane = threadIdx.x % 32;
+  const int partner = turned && !pairs
+                          ? (piece < half ? lane + half : lane - half)
+                          : lane;
+  const int freq = pairs ? piece * 4 : (piece < half ? piece : piece - half) * 8;
+  float w[8];
+  if (!is_v && turn.norm)
+    weights_of(turn.k_weight, turn.weights_bf16, piece * 8, w);
+  if (pid < 0 || pid >= p.num_pages) {
+    if (threadIdx.x == 0) record_bad_index(b, slot, pid);
+    return;
+  }
+  const int64_t block = static_cast<int64_t>(pid) * p.H_kv + h;
+  uint8_t* dst = (is_v ? p.v : p.k) + block * p.page_size * p.D + piece * 8;
+  float* scale_at = (is_v ? p.v_scale : p.k_scale) + block;
+  const float was = lo > 0 ? *scale_at : 0.f;
+  float x[NCH][8];
+  float top = 0.f;  // the largest finite magnitude
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    unpack_bf16x8(raw[i], x[i]);
+    const int tok = row0 + i * kRows;
+    const bool fresh = tok >= lo && tok < hi;
+    // (whole warps: the lanes exchange elements)
+    if (!is_v && __any_sync(0xffffffffu, fresh)) {
+      if (turn.norm) {
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fmaf(x[i][e], x[i][e], sum);
+#pragma unroll
+        for (int d = 1; d < kPer; d *= 2)
+          sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        const float r = rsqrtf(fmaf(sum, 1.f / D, turn.eps));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[i][e] *= r * w[e];
+      }
+      if (rope.dim != 0) {
+        const int t = tok0 + tok - len;
+        const int32_t* pos = turn.pos != nullptr && fresh
+                                 ? turn.pos + b * turn.pos_sb + t * turn.pos_ss
+                                 : nullptr;
+        float c[8], s[8];
+        if (pairs) {
+          if (turned && fresh) {
+            turns_of<4>(rope, rope.step, freq, pos, turn.pos_sa, tok0 + tok, c,
+                        s);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float u = x[i][2 * e], v = x[i][2 * e + 1];
+              x[i][2 * e] = u * c[e] - v * s[e];
+              x[i][2 * e + 1] = v * c[e] + u * s[e];
+            }
+          }
+        } else {
+          float other[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            other[e] = __shfl_sync(0xffffffffu, x[i][e], partner);
+          if (turned && fresh) {
+            turns_of<8>(rope, rope.step, freq, pos, turn.pos_sa, tok0 + tok, c,
+                        s);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              x[i][e] = x[i][e] * c[e] +
+                        other[e] * (piece < half ? -s[e] : s[e]);
+          }
+        }
+      }
+    }
+    if (fresh) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float a = fabsf(x[i][e]);
+        top = fmaxf(top, a < __int_as_float(0x7f800000) ? a : 0.f);
+      }
+    }
+  }
+  __shared__ uint32_t warp_top[kTurnThreads / 32];
+  const uint32_t mine =
+      __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+  if (lane == 0) warp_top[threadIdx.x / 32] = mine;
+  __syncthreads();  // (and every thread has read the old scale)
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < kTurnThreads / 32; ++i) most = max(most, warp_top[i]);
+  const float want = block_scale(__uint_as_float(most));
+  const float scale = lo > 0 ? fmaxf(was, want) : want;
+  const float inv = __frcp_rn(scale);  // exact: a power of two from this kernel
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int tok = row0 + i * kRows;
+    uint2* at = reinterpret_cast<uint2*>(dst + tok * D);
+    if (tok >= lo && tok < hi) {
+      *at = make_uint2(f32x4_to_e4m3(x[i][0] * inv, x[i][1] * inv,
+                                     x[i][2] * inv, x[i][3] * inv),
+                       f32x4_to_e4m3(x[i][4] * inv, x[i][5] * inv,
+                                     x[i][6] * inv, x[i][7] * inv));
+    } else if (tok < lo && scale > was) {
+      const float ratio = was * inv;
+      const uint2 q = *at;
+      uint32_t r[2] = {q.x, q.y};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t f0 = e4m3x2_to_f16x2(r[j]), f1 = e4m3x2_to_f16x2_hi(r[j]);
+        r[j] = f32x4_to_e4m3(f16_lo(f0) * ratio, f16_hi(f0) * ratio,
+                             f16_lo(f1) * ratio, f16_hi(f1) * ratio);
+      }
+      *at = make_uint2(r[0], r[1]);
     }
   }
   if (threadIdx.x == 0) *scale_at = scale;
@@ -1209,6 +1372,29 @@ cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream) {
     default: return cudaErrorInvalidValue;
   }
   return cudaGetLastError();
+}
+
+template <int D>
+static cudaError_t append_rope(const AppendParams& p, const TurnParams& t,
+                               cudaStream_t stream) {
+  const int slots = (p.T + p.page_size - 2) / p.page_size + 1;
+  const dim3 grid(slots, 2 * p.H_kv, p.B);
+  // steps of the block over a page's pieces (half a step: page 16 at D = 64)
+  switch (p.page_size * D / (8 * kTurnThreads)) {
+    case 0:
+    case 1: kv_append_rope_kernel<D, 1><<<grid, kTurnThreads, 0, stream>>>(p, t); break;
+    case 2: kv_append_rope_kernel<D, 2><<<grid, kTurnThreads, 0, stream>>>(p, t); break;
+    case 4: kv_append_rope_kernel<D, 4><<<grid, kTurnThreads, 0, stream>>>(p, t); break;
+    case 8: kv_append_rope_kernel<D, 8><<<grid, kTurnThreads, 0, stream>>>(p, t); break;
+    default: return cudaErrorInvalidValue;
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_append_rope(const AppendParams& p, const TurnParams& t,
+                                  cudaStream_t stream) {
+  return p.D == 128 ? append_rope<128>(p, t, stream)
+                    : append_rope<64>(p, t, stream);
 }
 
 cudaError_t launch_paged_attention(const PagedParams& p, int num_sms,

@@ -164,6 +164,37 @@ struct AppendParams {
   int64_t k_sb, k_sh, k_ss, v_sb, v_sh, v_ss;
 };
 
+// Norm and rotation of rows, as bsm_norm_rope and bsm_kv_append_rope take them.
+struct TurnParams {
+  const void *q_weight, *k_weight;  // [D] or null
+  int32_t weights_bf16;
+  int32_t norm;                     // 0: none
+  float eps;
+  bsm_rope rope;                    // dim 0: none
+  const int32_t* pos;               // or null: token indices
+  int64_t pos_sa, pos_sb, pos_ss;
+};
+
+struct RowView {
+  uint16_t* data;
+  int64_t sb, sh, ss;
+};
+
+struct NormRopeParams {
+  RowView x[2], g[2], out[2];  // queries, keys; g: the backward's gradients
+  int32_t B, S, D;
+  int32_t heads[2];
+  int32_t per[2];     // heads of one token that a group of lanes takes
+  int32_t chunks[2];  // ceil(heads / per)
+  // backward: blocks of the queries and of the keys, weight gradients (or
+  // null) and the blocks' sums [block][D]
+  int32_t blocks[2];
+  float* dw[2];
+  float* partial;
+  TurnParams turn;
+};
+constexpr int kNormRopeMaxBlocks = 1024;  // of the backward
+
 struct PagedParams {
   const uint8_t *k, *v;
   const float *k_scale, *v_scale;
@@ -192,6 +223,12 @@ constexpr size_t kPaWorkspaceBytes = static_cast<size_t>(kPaMaxSms) *
 
 // Launchers (return a cudaError_t from the launch).
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
+cudaError_t launch_kv_append_rope(const AppendParams& p, const TurnParams& t,
+                                  cudaStream_t stream);
+cudaError_t launch_norm_rope(NormRopeParams& p, int num_sms,
+                             cudaStream_t stream);
+cudaError_t launch_norm_rope_bwd(NormRopeParams& p, int num_sms,
+                                 cudaStream_t stream);
 cudaError_t launch_paged_attention(const PagedParams& p, int num_sms,
                                    cudaStream_t stream);
 // Reads and clears the device error record of the cache kernels.

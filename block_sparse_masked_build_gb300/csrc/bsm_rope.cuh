@@ -1,0 +1,69 @@
+// Cosines and sines of a row's position angles, shared by the kernels that
+// rotate rows (bsm_rope.cu, the cache's append).
+#pragma once
+
+#include <cstdint>
+
+#include "bsm_internal.h"
+
+namespace bsm {
+
+// cos and sin of position * step turns.  The product modulo 2^64 drops whole
+// turns exactly; its upper half is a signed fraction of a turn in [-1/2, 1/2),
+// whose angle __sincosf takes within its bound for [-pi, pi] (2^-21.2
+// absolute); with the roundings of the angle itself (3 of 2^-25 of at most pi)
+// that is less than 2^-20, eleven bits below bf16's half step of a result of
+// size 1.
+__device__ __forceinline__ void turn_of(uint64_t step, int32_t position,
+                                        float* c, float* s) {
+  const uint64_t turns =
+      static_cast<uint64_t>(static_cast<int64_t>(position)) * step;
+  const float a = static_cast<float>(static_cast<int32_t>(turns >> 32)) *
+                  1.4629180792671596e-9f;  // 2 pi / 2^32
+  __sincosf(a, s, c);
+}
+
+// Of N frequencies from f on; pos: the token's first axis.
+template <int N>
+__device__ __forceinline__ void turns_of(const bsm_rope& rope,
+                                         const uint64_t* steps, int f,
+                                         const int32_t* pos, int64_t axis_stride,
+                                         int32_t index, float* c, float* s) {
+  if (pos == nullptr || rope.axes == 1) {
+    const int32_t at = pos == nullptr ? index : *pos;
+#pragma unroll
+    for (int i = 0; i < N; ++i) turn_of(steps[f + i], at, &c[i], &s[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      turn_of(steps[f + i], pos[rope.axis[f + i] * axis_stride], &c[i], &s[i]);
+  }
+}
+
+// Eight elements of a norm's weight from `at` on; ones where there is none.
+__device__ __forceinline__ void weights_of(const void* w, int bf16, int at,
+                                           float* out) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = 1.f;
+  } else if (bf16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      out[i] = __uint_as_float(
+          static_cast<uint32_t>(static_cast<const uint16_t*>(w)[at + i]) << 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = static_cast<const float*>(w)[at + i];
+  }
+}
+
+__device__ __forceinline__ void unpack_bf16x8(const uint4& v, float* x) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+}  // namespace bsm

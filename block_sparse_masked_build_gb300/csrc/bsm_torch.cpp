@@ -17,6 +17,7 @@
 #include <cuda_runtime_api.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <array>
 #include <cmath>
 #include <cstring>
 #include <map>
@@ -34,7 +35,10 @@ decltype(&bsm_splash_fwd_mod) f_splash_fwd_mod;
 decltype(&bsm_splash_bwd_mod) f_splash_bwd_mod;
 decltype(&bsm_kv_append) f_kv_append;
 decltype(&bsm_paged_attention) f_paged_attention;
-size_t fwd_workspace_bytes, paged_workspace_bytes;
+decltype(&bsm_kv_append_rope) f_kv_append_rope;
+decltype(&bsm_norm_rope) f_norm_rope;
+decltype(&bsm_norm_rope_bwd) f_norm_rope_bwd;
+size_t fwd_workspace_bytes, paged_workspace_bytes, rope_bwd_workspace_bytes;
 decltype(&bsm_splash_bwd_workspace_bytes) f_bwd_workspace_bytes;
 decltype(&bsm_splash_bwd_mod_workspace_bytes) f_bwd_mod_workspace_bytes;
 PyObject* on_status;  // Python callable that raises for a status
@@ -508,11 +512,194 @@ bsm_tensor token_view(const at::Tensor& t, int64_t B, int64_t heads, int64_t T,
   return view(t);
 }
 
-// kv_append(k_pages, v_pages, k_scale, v_scale, page_table, lens, k_new,
-// v_new, n_new, stream)
-PyObject* py_kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+// A norm, a rotation and positions, as four Python arguments give them: the
+// address of a bsm_rope or 0, positions, eps or None; and the norm's weights.
+struct Turn {
+  bsm_head_norm norm = {};
+  bsm_positions pos = {};
+  const bsm_rope* rope = nullptr;
+  bool normed = false;
+  const bsm_head_norm* norm_or_null() const { return normed ? &norm : nullptr; }
+};
+
+const void* norm_weight(const at::Tensor& w, int64_t D, const at::Device& dev,
+                        const char* name) {
+  if (!w.defined()) return nullptr;
+  if ((w.scalar_type() != at::kFloat && w.scalar_type() != at::kBFloat16) ||
+      w.dim() != 1 || w.size(0) != D || !w.is_contiguous() ||
+      w.device() != dev)
+    value_error(std::string(name) + " must be a contiguous float32 or "
+                                    "bfloat16 tensor [" +
+                std::to_string(D) + "] on " + device_name(dev));
+  return w.const_data_ptr();
+}
+
+Turn turn_of(PyObject* rope, PyObject* positions, PyObject* eps,
+             const at::Tensor& qw, const at::Tensor& kw, int64_t B, int64_t S,
+             int64_t D, const at::Device& dev) {
+  Turn t;
+  t.rope = reinterpret_cast<const bsm_rope*>(
+      static_cast<intptr_t>(integer(rope)));
+  t.normed = eps != Py_None;
+  if (t.normed) t.norm.eps = static_cast<float>(number(eps));
+  t.norm.q_weight = norm_weight(qw, D, dev, "q_weight");
+  t.norm.k_weight = norm_weight(kw, D, dev, "k_weight");
+  if (!t.normed && (qw.defined() || kw.defined()))
+    value_error("weights are the norm's: give eps");
+  if (qw.defined() && kw.defined() && qw.scalar_type() != kw.scalar_type())
+    value_error("q_weight and k_weight must have one type");
+  t.norm.weights_bf16 =
+      (qw.defined() ? qw : kw).defined() &&
+      (qw.defined() ? qw : kw).scalar_type() == at::kBFloat16;
+  if (t.rope == nullptr && !t.normed)
+    value_error("give a rope, or eps for the norm");
+  const at::Tensor p = tensor_or_none(positions, "positions");
+  if (!p.defined()) return t;
+  if (t.rope == nullptr) value_error("positions without a rope");
+  const int64_t axes = t.rope->axes, first = p.dim() - 2;
+  if (p.scalar_type() != at::kInt || p.device() != dev ||
+      !((p.dim() == 2 && axes == 1) || (p.dim() == 3 && p.size(0) == axes)) ||
+      p.size(first) != B || p.size(first + 1) != S)
+    value_error("positions must be an int32 tensor [" + std::to_string(axes) +
+                ", " + std::to_string(B) + ", " + std::to_string(S) +
+                "] (the first 1 may be left out) on " + device_name(dev));
+  t.pos.data = data<const int32_t>(p);
+  t.pos.strides[0] = p.dim() == 3 ? p.stride(0) : 0;
+  t.pos.strides[1] = p.stride(first);
+  t.pos.strides[2] = p.stride(first + 1);
+  return t;
+}
+
+// A bf16 [B, heads, S, D] tensor on dev.
+void check_rows(const at::Tensor& t, at::IntArrayRef sizes,
+                const at::Device& dev, const char* name) {
+  if (t.scalar_type() != at::kBFloat16 || t.dim() != 4 ||
+      t.sizes() != sizes || t.device() != dev || t.stride(3) != 1)
+    value_error(std::string(name) + " must be a bfloat16 tensor [" +
+                std::to_string(sizes[0]) + ", " + std::to_string(sizes[1]) +
+                ", " + std::to_string(sizes[2]) + ", " +
+                std::to_string(sizes[3]) +
+                "] with a contiguous head dimension on " + device_name(dev));
+}
+
+// The queries' and keys' rows of a norm and rotation: k may be missing.
+struct Rows {
+  at::Tensor q, k;
+  at::Device dev;
+  int64_t B, H, S, D, Hkv;
+  Rows(PyObject* a, PyObject* b, const char* qn, const char* kn)
+      : q(tensor(a, qn)), k(tensor_or_none(b, kn)), dev(q.device()) {
+    if (q.dim() != 4) value_error(std::string(qn) + " must be [B, H, S, D]");
+    B = q.size(0), H = q.size(1), S = q.size(2), D = q.size(3);
+    check_rows(q, q.sizes(), dev, qn);
+    if (k.defined() && k.dim() != 4)
+      value_error(std::string(kn) + " must be [B, H_kv, S, D]");
+    Hkv = k.defined() ? k.size(1) : 0;
+    if (k.defined()) check_rows(k, k_sizes(), dev, kn);
+    if (!dev.is_cuda())
+      value_error(std::string(qn) + " must be a CUDA tensor");
+    for (int64_t v : {B, H, S, D, Hkv})
+      if (v > INT32_MAX) value_error("integer out of range");
+  }
+  std::array<int64_t, 4> k_sizes() const { return {B, Hkv, S, D}; }
+  // the tensors that go with q's and k's rows, made where they are missing
+  std::pair<at::Tensor, at::Tensor> like(PyObject* a, PyObject* b,
+                                         const char* qn, const char* kn,
+                                         bool make) const {
+    std::pair<at::Tensor, at::Tensor> r(tensor_or_none(a, qn),
+                                        tensor_or_none(b, kn));
+    if (!r.first.defined() && make)
+      r.first = empty_on({B, H, S, D}, at::kBFloat16, dev);
+    if (!k.defined() && r.second.defined())
+      value_error(std::string(kn) + " without the keys");
+    if (k.defined() && !r.second.defined() && make)
+      r.second = empty_on(k_sizes(), at::kBFloat16, dev);
+    if (r.first.defined()) check_rows(r.first, q.sizes(), dev, qn);
+    if (r.second.defined()) check_rows(r.second, k_sizes(), dev, kn);
+    return r;
+  }
+};
+
+bsm_tensor view_or_none(const at::Tensor& t) {
+  return t.defined() ? view(t) : bsm_tensor{};
+}
+
+PyObject* wrap_or_none(at::Tensor&& t) {
+  if (t.defined()) return THPVariable_Wrap(std::move(t));
+  Py_RETURN_NONE;
+}
+
+// norm_rope(q, k, rope address, positions, q_weight, k_weight, eps, out,
+// k_out, stream) -> (out, k_out)
+PyObject* py_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     expect(n, 10);
+    const Rows r(a[0], a[1], "q", "k");
+    const Turn t = turn_of(a[2], a[3], a[6], tensor_or_none(a[4], "q_weight"),
+                           tensor_or_none(a[5], "k_weight"), r.B, r.S, r.D,
+                           r.dev);
+    OnDevice on(r.dev, a[9]);
+    auto out = r.like(a[7], a[8], "out", "k_out", true);
+    const bsm_tensor qv = view(r.q), kv = view_or_none(r.k),
+                     ov = view(out.first), pv = view_or_none(out.second);
+    check_status(f_norm_rope(
+        &qv, &kv, static_cast<int32_t>(r.B), static_cast<int32_t>(r.H),
+        static_cast<int32_t>(r.Hkv), static_cast<int32_t>(r.S),
+        static_cast<int32_t>(r.D), t.norm_or_null(), t.rope, &t.pos, &ov, &pv,
+        on.stream));
+    PyObject* res = PyTuple_New(2);
+    PyTuple_SET_ITEM(res, 0, wrap_or_none(std::move(out.first)));
+    PyTuple_SET_ITEM(res, 1, wrap_or_none(std::move(out.second)));
+    return res;
+  });
+}
+
+// norm_rope_bwd(gq, gk, q, k, rope address, positions, q_weight, k_weight,
+// eps, stream) -> (dq, dk, dq_weight, dk_weight)
+PyObject* py_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    expect(n, 10);
+    const Rows r(a[0], a[1], "gq", "gk");
+    const at::Tensor qw = tensor_or_none(a[6], "q_weight");
+    const at::Tensor kw = tensor_or_none(a[7], "k_weight");
+    const Turn t = turn_of(a[4], a[5], a[8], qw, kw, r.B, r.S, r.D, r.dev);
+    const auto x = r.like(a[2], a[3], "q", "k", false);
+    if (t.normed && (!x.first.defined() ||
+                     (r.k.defined() && !x.second.defined())))
+      value_error("the norm's backward needs q and k");
+    if (kw.defined() && !r.k.defined())
+      value_error("k_weight without the keys");
+    OnDevice on(r.dev, a[9]);
+    auto d = r.like(Py_None, Py_None, "dq", "dk", true);
+    at::Tensor dw[2], ws;
+    if (qw.defined()) dw[0] = empty_on({r.D}, at::kFloat, r.dev);
+    if (kw.defined()) dw[1] = empty_on({r.D}, at::kFloat, r.dev);
+    if (qw.defined() || kw.defined())
+      ws = workspace(2, rope_bwd_workspace_bytes, r.dev, on.stream);
+    const bsm_tensor gq = view(r.q), gk = view_or_none(r.k),
+                     qv = view_or_none(x.first), kv = view_or_none(x.second),
+                     dq = view(d.first), dk = view_or_none(d.second);
+    check_status(f_norm_rope_bwd(
+        &gq, &gk, &qv, &kv, static_cast<int32_t>(r.B),
+        static_cast<int32_t>(r.H), static_cast<int32_t>(r.Hkv),
+        static_cast<int32_t>(r.S), static_cast<int32_t>(r.D),
+        t.norm_or_null(), t.rope, &t.pos, &dq, &dk, data<float>(dw[0]),
+        data<float>(dw[1]), data<void>(ws), bytes_of(ws), on.stream));
+    PyObject* res = PyTuple_New(4);
+    PyTuple_SET_ITEM(res, 0, wrap_or_none(std::move(d.first)));
+    PyTuple_SET_ITEM(res, 1, wrap_or_none(std::move(d.second)));
+    PyTuple_SET_ITEM(res, 2, wrap_or_none(std::move(dw[0])));
+    PyTuple_SET_ITEM(res, 3, wrap_or_none(std::move(dw[1])));
+    return res;
+  });
+}
+
+// kv_append(k_pages, v_pages, k_scale, v_scale, page_table, lens, k_new,
+// v_new, n_new, stream), and behind them, for keys normalised and rotated on
+// the way: rope address, positions, k_weight, eps
+PyObject* py_kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 14) expect(n, 10);
     const bsm_kv_cache c = cache_of(a);
     const at::Device dev = tensor(a[0], "k_pages").device();
     const at::Tensor &table = tensor(a[4], "page_table"),
@@ -527,6 +714,17 @@ PyObject* py_kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const bsm_tensor vt = token_view(v_new, B, c.H_kv, T, c.D, dev, "v_new");
     if (!dev.is_cuda()) value_error("the cache must be on a CUDA device");
     OnDevice on(dev, a[9]);
+    if (n == 14) {
+      const Turn t = turn_of(a[10], a[11], a[13], at::Tensor(),
+                             tensor_or_none(a[12], "k_weight"), B, T, c.D, dev);
+      check_status(f_kv_append_rope(
+          &c, data<const int32_t>(table), table.stride(0),
+          static_cast<int32_t>(table.size(1)), data<const int32_t>(lens),
+          data<const int32_t>(n_new), &kt, &vt, static_cast<int32_t>(B),
+          static_cast<int32_t>(T), t.norm_or_null(), t.rope, &t.pos,
+          on.stream));
+      Py_RETURN_NONE;
+    }
     check_status(f_kv_append(&c, data<const int32_t>(table), table.stride(0),
                              static_cast<int32_t>(table.size(1)),
                              data<const int32_t>(lens),
@@ -613,7 +811,13 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     set(f_bwd_mod_workspace_bytes, "bsm_splash_bwd_mod_workspace_bytes");
     set(f_kv_append, "bsm_kv_append");
     set(f_paged_attention, "bsm_paged_attention");
+    set(f_kv_append_rope, "bsm_kv_append_rope");
+    set(f_norm_rope, "bsm_norm_rope");
+    set(f_norm_rope_bwd, "bsm_norm_rope_bwd");
     decltype(&bsm_splash_fwd_workspace_bytes) f0;
+    decltype(&bsm_norm_rope_bwd_workspace_bytes) f2;
+    set(f2, "bsm_norm_rope_bwd_workspace_bytes");
+    rope_bwd_workspace_bytes = f2();
     decltype(&bsm_paged_attention_workspace_bytes) f1;
     set(f0, "bsm_splash_fwd_workspace_bytes");
     set(f1, "bsm_paged_attention_workspace_bytes");
@@ -630,7 +834,8 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {FAST(bind),       FAST(build_mask_info),
                          FAST(splash_fwd), FAST(splash_bwd),
                          FAST(kv_append),  FAST(paged_attention),
-                         FAST(check_cache),
+                         FAST(check_cache), FAST(norm_rope),
+                         FAST(norm_rope_bwd),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bsm_torch", nullptr, -1,

@@ -501,6 +501,101 @@ bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
  * parts of rows whose keys are split over several CTAs. */
 size_t bsm_paged_attention_workspace_bytes(void);
 
+/* Rotation of a head's row by its position (no counterpart on the pages): of
+ * the row's first `dim` elements the pairs (x[i], x[i + dim / 2]), or with
+ * `interleaved` (x[2 i], x[2 i + 1]), i < dim / 2, turn by the angle
+ * a_i = position[axis[i]] * inv_freq[i]:
+ *     (u, v) -> (u cos a_i - v sin a_i, v cos a_i + u sin a_i);
+ * the elements behind them stay as they are.  A position has `axes` numbers
+ * (time, height, width, ...); frequency i goes by the one axis[i] names.
+ * Filled by bsm_rope_init, plain data, copied by the calls that take it.
+ * step[i] is inv_freq[i] / (2 pi) turns in units of 2^-64, so that position *
+ * step[i] modulo 2^64 is the angle without its whole turns, however far the
+ * position: cosines and sines are off by less than 2^-20. */
+typedef struct bsm_rope {
+  int32_t dim, interleaved, axes, reserved;
+  uint64_t step[64];
+  uint8_t axis[64];
+} bsm_rope;
+
+/* Fills `rope` (host only): dim a multiple of 16 from 16 to 128, inv_freq
+ * [dim / 2] of magnitude at most 64, axis [dim / 2] with values in [0, axes)
+ * or NULL for all 0, axes from 1 to 4. */
+bsm_status bsm_rope_init(bsm_rope* rope, int32_t dim, int32_t interleaved,
+                         const double* inv_freq, const int32_t* axis,
+                         int32_t axes);
+
+/* Positions [axes][B][S] in device memory, int32, with element strides of the
+ * axis, batch and token (0 repeats); data NULL: each token's position is its
+ * index, on every axis. */
+typedef struct bsm_positions {
+  const int32_t* data;
+  int64_t strides[3];
+} bsm_positions;
+
+/* Root-mean-square norm of each head's row: x -> w x / sqrt(mean(x^2) + eps),
+ * w of the queries' rows and of the keys' ([D], device, f32, or bf16 with
+ * weights_bf16; NULL = ones); eps >= 0.  Sums are f32: |x| up to 2^59. */
+typedef struct bsm_head_norm {
+  const void* q_weight;
+  const void* k_weight;
+  int32_t weights_bf16;
+  float eps;
+} bsm_head_norm;
+
+/* Norm and rotation of every query and key row in one pass, as an attention
+ * layer needs them ahead of bsm_splash_fwd or bsm_kv_append: first the norm
+ * (norm NULL: none), then the rotation (rope NULL: none; one of the two is
+ * given).  Computed in f32 and rounded to bf16 once.
+ *   q, q_out  device bf16 [B][H][S][D]; k, k_out [B][H_kv][S][D], or both NULL
+ *             with H_kv = 0; D 64 or 128, rope->dim <= D.  q_out may be q
+ *             itself (the same memory and strides), and k_out k; no other
+ *             overlap is allowed
+ *   pos       NULL: token indices
+ * One launch on `stream`. */
+bsm_status bsm_norm_rope(const bsm_tensor* q, const bsm_tensor* k, int32_t B,
+                         int32_t H, int32_t H_kv, int32_t S, int32_t D,
+                         const bsm_head_norm* norm, const bsm_rope* rope,
+                         const bsm_positions* pos, const bsm_tensor* q_out,
+                         const bsm_tensor* k_out, void* stream);
+
+/* Backward of bsm_norm_rope.  With g the gradient of a row's result, g' = g
+ * turned back by the row's angles, r = 1 / sqrt(mean(x^2) + eps), n = r x:
+ *     dx = r (w g' - n mean(w g' n)),   dw = sum over the rows of g' n
+ * (without the norm dx = g', and x is not read).
+ *   gq, gk    gradients of q_out and k_out; dq, dk those of q and k, written
+ *             (dq may be gq itself, and dk gk)
+ *   q, k      as given to the forward; may be NULL without a norm
+ *   dq_weight, dk_weight  device f32 [D], written, or NULL.  The sums' order
+ *             depends on the sizes alone
+ *   workspace device, >= bsm_norm_rope_bwd_workspace_bytes() bytes, 16-byte
+ *             aligned; NULL where neither weight gradient is asked for */
+bsm_status bsm_norm_rope_bwd(const bsm_tensor* gq, const bsm_tensor* gk,
+                             const bsm_tensor* q, const bsm_tensor* k,
+                             int32_t B, int32_t H, int32_t H_kv, int32_t S,
+                             int32_t D, const bsm_head_norm* norm,
+                             const bsm_rope* rope, const bsm_positions* pos,
+                             const bsm_tensor* dq, const bsm_tensor* dk,
+                             float* dq_weight, float* dk_weight,
+                             void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+size_t bsm_norm_rope_bwd_workspace_bytes(void);
+
+/* bsm_kv_append with the keys normalised (norm's k_weight) and rotated on the
+ * way, in f32 and rounded once, to the cache's 8 bits; the scale's largest
+ * magnitude is that of the rotated keys.  Values are appended as they are.
+ *   pos       [axes][B][T]; NULL: the tokens' places in the sequence, lens[b]
+ *             + t, on every axis
+ * One of norm and rope is given; everything else as in bsm_kv_append. */
+bsm_status bsm_kv_append_rope(const bsm_kv_cache* cache,
+                              const int32_t* page_table, int64_t table_stride,
+                              int32_t max_pages, const int32_t* lens,
+                              const int32_t* n_new, const bsm_tensor* k_new,
+                              const bsm_tensor* v_new, int32_t B, int32_t T,
+                              const bsm_head_norm* norm, const bsm_rope* rope,
+                              const bsm_positions* pos, void* stream);
+
 /* Synchronise `stream` and report whether a kernel of this library gave up
  * on a bounded wait since the last call (then BSM_ERR_DEVICE_TIMEOUT; the
  * affected outputs are undefined, the CUDA context stays usable), or a cache
