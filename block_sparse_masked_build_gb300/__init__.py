@@ -29,6 +29,8 @@ from .api import (  # noqa: F401
     bsm_norm_rope_bwd_workspace_bytes,
     bsm_pack_dense_mask,
     bsm_paged_attention,
+    bsm_paged_attention_tree,
+    bsm_paged_attention_tree_workspace_bytes,
     bsm_paged_attention_workspace_bytes,
     bsm_selftest_wait_timeout,
     bsm_splash_bwd,

@@ -202,6 +202,13 @@ def _declare(lib):
     lib.bsm_paged_attention.argtypes = [
         vp, kc, vp, c.c_int64, c.c_int32, vp, c.c_int32, c.c_int32, c.c_int32,
         c.c_float, c.c_int32, c.POINTER(ScoreMod), vp, vp, vp, c.c_size_t, vp]
+    lib.bsm_paged_attention_tree_workspace_bytes.restype = c.c_size_t
+    lib.bsm_paged_attention_tree_workspace_bytes.argtypes = [c.c_int32] * 4
+    lib.bsm_paged_attention_tree.restype = c.c_int
+    lib.bsm_paged_attention_tree.argtypes = [
+        vp, kc, vp, c.c_int64, c.c_int32, vp, vp, vp, c.c_int64, c.c_int64,
+        c.c_int32, c.c_int32, c.c_int32, c.c_float, c.c_int32,
+        c.POINTER(ScoreMod), vp, vp, vp, c.c_size_t, vp]
     lib.bsm_device_status.restype = c.c_int
     lib.bsm_device_status.argtypes = [c.c_void_p, c.POINTER(c.c_int32)]
     lib.bsm_selftest_wait_timeout.restype = c.c_int
@@ -252,7 +259,8 @@ _FAST_NAMES = ("bsm_mask_info_bytes", "bsm_build_mask_info",
                "bsm_paged_attention", "bsm_splash_fwd_workspace_bytes",
                "bsm_paged_attention_workspace_bytes", "bsm_norm_rope",
                "bsm_norm_rope_bwd", "bsm_norm_rope_bwd_workspace_bytes",
-               "bsm_kv_append_rope")
+               "bsm_kv_append_rope", "bsm_paged_attention_tree",
+               "bsm_paged_attention_tree_workspace_bytes")
 
 
 def fast(on_status):

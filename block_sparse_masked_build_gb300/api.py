@@ -114,7 +114,7 @@ def _scratch(nbytes: int, dev, stream, kept: dict | None = None):
     if kept is None or torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)
     key = (dev, torch.cuda.current_stream(dev).cuda_stream)
-    if key not in kept:
+    if key not in kept or kept[key].numel() < nbytes:
         kept[key] = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     return kept[key]
 
@@ -773,6 +773,7 @@ def bsm_paged_attention_workspace_bytes() -> int:
 
 
 _paged_workspaces: dict = {}
+_tree_workspaces: dict = {}
 
 
 def bsm_paged_attention(q, cache: KVCache, page_table, lens, scale: float,
@@ -781,17 +782,54 @@ def bsm_paged_attention(q, cache: KVCache, page_table, lens, scale: float,
                         workspace=None) -> None:
     """q, out [B,H,T,D] (bf16): the last T of each sequence's lens [B]
     tokens attend to the cache; lse [B,H,T] (f32, contiguous) or None."""
+    _paged(q, cache, page_table, lens, scale, out, lse, window, softcap,
+           alibi_slopes, stream, workspace, None)
+
+
+def bsm_paged_attention_tree_workspace_bytes(H: int, H_kv: int, T: int,
+                                             D: int) -> int:
+    return int(_lib.lib().bsm_paged_attention_tree_workspace_bytes(H, H_kv, T,
+                                                                   D))
+
+
+def bsm_paged_attention_tree(q, cache: KVCache, page_table, lens, tree, n_new,
+                             scale: float, out, lse=None, window: int = 0,
+                             softcap: float = 0.0, alibi_slopes=None,
+                             stream=None, workspace=None) -> None:
+    """bsm_paged_attention of drafted tokens: the last n_new [B] (None: T) of
+    each sequence's tokens, each with the drafts that it sees as bits in tree
+    (int32 words [B,T,W] or [T,W], W >= ceil(T / 32); None: those up to
+    itself)."""
+    _paged(q, cache, page_table, lens, scale, out, lse, window, softcap,
+           alibi_slopes, stream, workspace, (tree, n_new))
+
+
+def _check_tree(tree, B: int, T: int, dev) -> None:
+    words = (T + 31) // 32
+    if tree is not None and (
+            tree.dtype not in _INT32 or tree.dim() not in (2, 3)
+            or (tree.dim() == 3 and tree.shape[0] != B)
+            or tree.shape[-2] != T or tree.shape[-1] < words
+            or (words > 1 and tree.stride(-1) != 1) or tree.device != dev):
+        raise ValueError(f"tree must be an int32 tensor {[B, T, words]} (the "
+                         "batch may be left out) with contiguous rows, beside "
+                         "the cache")
+
+
+def _paged(q, cache, page_table, lens, scale, out, lse, window, softcap,
+           alibi_slopes, stream, workspace, drafts) -> None:
     dev = cache.device
     if _elsewhere(dev):
         with torch.cuda.device(dev):
-            return bsm_paged_attention(q, cache, page_table, lens, scale, out,
-                                       lse, window, softcap, alibi_slopes,
-                                       stream, workspace)
+            return _paged(q, cache, page_table, lens, scale, out, lse, window,
+                          softcap, alibi_slopes, stream, workspace, drafts)
     s = cache.struct
     if q.dim() != 4:
         raise ValueError("q must be [B, H, T, D]")
     B, H, T, D = q.shape
-    _check_table(dev, page_table, B, lens)
+    tree, n_new = drafts or (None, None)
+    _check_table(dev, page_table, B, lens, n_new)
+    _check_tree(tree, B, T, dev)
     shape = (B, H, T, s.D)
     _check_tokens(q, shape, dev, "q")
     _check_tokens(out, shape, dev, "out")
@@ -807,15 +845,25 @@ def bsm_paged_attention(q, cache: KVCache, page_table, lens, scale: float,
         raise ValueError("integer out of range")
     sh = _stream_handle(stream)
     if workspace is None:
-        workspace = _scratch(bsm_paged_attention_workspace_bytes(), dev,
-                             stream, _paged_workspaces)
+        need, kept = (
+            (bsm_paged_attention_workspace_bytes(), _paged_workspaces)
+            if drafts is None else
+            (bsm_paged_attention_tree_workspace_bytes(H, s.H_kv, T, s.D),
+             _tree_workspaces))
+        workspace = _scratch(need, dev, stream, kept)
     views, at = _views(q, out)
-    _check(_lib.lib().bsm_paged_attention(
-        at, s, page_table.data_ptr(), page_table.stride(0),
-        page_table.shape[1], lens.data_ptr(), B, H, T, scale, window, mod,
-        at + 32, None if lse is None else lse.data_ptr(),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        sh))
+    args = (at, s, page_table.data_ptr(), page_table.stride(0),
+            page_table.shape[1], lens.data_ptr())
+    more = (B, H, T, scale, window, mod, at + 32,
+            None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), sh)
+    if drafts is None:
+        _check(_lib.lib().bsm_paged_attention(*args, *more))
+    else:
+        _check(_lib.lib().bsm_paged_attention_tree(
+            *args, _ptr(n_new), _ptr(tree),
+            0 if tree is None or tree.dim() == 2 else tree.stride(0),
+            0 if tree is None else tree.stride(-2), *more))
 
 
 def bsm_device_status(stream=None) -> tuple[int, list[int]]:
@@ -1051,25 +1099,36 @@ def kv_append(cache: KVCache, page_table, lens, k_new, v_new, *, n_new=None,
 def paged_attention(q, cache: KVCache, page_table, lens, *,
                     scale: float | None = None, window: int = 0,
                     softcap: float = 0.0, alibi_slopes=None,
-                    return_lse: bool = True, out=None, lse=None, stream=None):
+                    return_lse: bool = True, out=None, lse=None, stream=None,
+                    tree=None, n_new=None):
     """Causal attention of q [B, H, T, D] (bf16), the last T tokens of each
     sequence, over the cache's lens[b] tokens (the queries' own among them).
 
     ``window`` > 0 keeps the last ``window`` keys of each query; scale,
     ``softcap`` and ``alibi_slopes`` as in :func:`splash_attention`.  Rows
-    that see no key are 0 with logsumexp -inf.  Returns (out, lse)."""
+    that see no key are 0 with logsumexp -inf.  Returns (out, lse).
+
+    Drafted tokens: with ``n_new`` (int32 [B], at most T and lens[b]) the
+    queries are a sequence's last n_new[b] tokens and the rows behind them are
+    empty.  ``tree`` (int32 words [B, T, W], or [T, W] for all; bit j of row t:
+    draft t sees draft j, W >= ceil(T / 32) as :func:`pack_dense_mask` packs
+    them) makes them a tree: draft t sees the tokens before the drafts and the
+    drafts of its row, its ancestors' and itself, and stands as many places
+    behind those tokens as its row has bits, less one."""
+    drafts = tree is not None or n_new is not None
     s = _other_stream(stream, cache.device) \
         if cache.device.type == "cuda" else None
     if s is not None:
         return _run_on(s, lambda: paged_attention(
             q, cache, page_table, lens, scale=scale, window=window,
             softcap=softcap, alibi_slopes=alibi_slopes, return_lse=return_lse,
-            out=out, lse=lse))
+            out=out, lse=lse, tree=tree, n_new=n_new))
     fast = _fast()
     if fast:
-        return fast.paged_attention(
-            *cache._tensors, page_table, lens, q, scale, window, softcap,
-            alibi_slopes, out, lse, return_lse, _fast_stream(stream))
+        args = (*cache._tensors, page_table, lens, q, scale, window, softcap,
+                alibi_slopes, out, lse, return_lse, _fast_stream(stream))
+        return fast.paged_attention(*args, tree, n_new) if drafts else \
+            fast.paged_attention(*args)
     if q.dim() != 4:
         raise ValueError("q must be [B, H, T, D]")
     B, H, T, D = q.shape
@@ -1081,8 +1140,8 @@ def paged_attention(q, cache: KVCache, page_table, lens, *,
         lse = None
     elif lse is None:
         lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
-    bsm_paged_attention(q, cache, page_table, lens, scale, out, lse, window,
-                        softcap, alibi_slopes, stream)
+    _paged(q, cache, page_table, lens, scale, out, lse, window, softcap,
+           alibi_slopes, stream, None, (tree, n_new) if drafts else None)
     return out, lse
 
 

@@ -1144,15 +1144,21 @@ size_t bsm_paged_attention_workspace_bytes(void) {
   return bsm::kPaWorkspaceBytes;
 }
 
-bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
-                               const int32_t* page_table, int64_t table_stride,
-                               int32_t max_pages, const int32_t* lens,
-                               int32_t B, int32_t H, int32_t T, float scale,
-                               int32_t window, const bsm_score_mod* mod,
-                               const bsm_tensor* out, float* lse,
-                               void* workspace, size_t workspace_bytes,
-                               void* stream) {
-  g_last_error.clear();
+namespace {
+// What bsm_paged_attention_tree has beside bsm_paged_attention.
+struct Drafts {
+  const int32_t* n_new;
+  const uint32_t* tree;
+  int64_t sb, st;
+};
+
+bsm_status paged(const bsm_tensor* q, const bsm_kv_cache* cache,
+                 const int32_t* page_table, int64_t table_stride,
+                 int32_t max_pages, const int32_t* lens, int32_t B, int32_t H,
+                 int32_t T, float scale, int32_t window,
+                 const bsm_score_mod* mod, const Drafts* drafts,
+                 const bsm_tensor* out, float* lse, void* workspace,
+                 size_t workspace_bytes, void* stream) {
   bsm_status s = check_cache(cache, table_stride, max_pages, B, T);
   if (s != BSM_OK) return s;
   if (H < 0 || (cache->H_kv == 0 ? H != 0 : H % cache->H_kv != 0))
@@ -1215,10 +1221,62 @@ bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
   p.o_sh = out->strides[1];
   p.o_ss = out->strides[2];
   p.lse = lse;
-  const cudaError_t e =
-      bsm::launch_paged_attention(p, num_sms, static_cast<cudaStream_t>(stream));
+  const auto st = static_cast<cudaStream_t>(stream);
+  p.n_new = nullptr;
+  p.tree = nullptr;
+  p.tree_sb = p.tree_st = 0;
+  if (drafts != nullptr) {
+    p.n_new = drafts->n_new;
+    p.tree = drafts->tree;
+    p.tree_sb = drafts->sb;
+    p.tree_st = drafts->st;
+  }
+  const cudaError_t e = drafts != nullptr
+                            ? bsm::launch_paged_tree(p, num_sms, st)
+                            : bsm::launch_paged_attention(p, num_sms, st);
   if (e != cudaSuccess) return cuda_fail(e, "paged_attention launch");
   return BSM_OK;
+}
+}  // namespace
+
+bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
+                               const int32_t* page_table, int64_t table_stride,
+                               int32_t max_pages, const int32_t* lens,
+                               int32_t B, int32_t H, int32_t T, float scale,
+                               int32_t window, const bsm_score_mod* mod,
+                               const bsm_tensor* out, float* lse,
+                               void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  g_last_error.clear();
+  return paged(q, cache, page_table, table_stride, max_pages, lens, B, H, T,
+               scale, window, mod, nullptr, out, lse, workspace,
+               workspace_bytes, stream);
+}
+
+size_t bsm_paged_attention_tree_workspace_bytes(int32_t H, int32_t H_kv,
+                                                int32_t T, int32_t D) {
+  return bsm::kPaWorkspaceBytes;
+}
+
+bsm_status bsm_paged_attention_tree(
+    const bsm_tensor* q, const bsm_kv_cache* cache, const int32_t* page_table,
+    int64_t table_stride, int32_t max_pages, const int32_t* lens,
+    const int32_t* n_new, const uint32_t* tree, int64_t tree_stride_b,
+    int64_t tree_stride_t, int32_t B, int32_t H, int32_t T, float scale,
+    int32_t window, const bsm_score_mod* mod, const bsm_tensor* out,
+    float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (T > 1024 && tree != nullptr)
+    return fail(BSM_ERR_UNSUPPORTED, "more than 1024 drafts in a tree");
+  if (((reinterpret_cast<uintptr_t>(n_new) |
+        reinterpret_cast<uintptr_t>(tree)) & 3u) != 0)
+    return fail(BSM_ERR_INVALID_ARG, "n_new and tree must be 4-byte aligned");
+  if (tree_stride_b < 0 || tree_stride_t < 0)
+    return fail(BSM_ERR_INVALID_ARG, "tree strides must be >= 0");
+  const Drafts d = {n_new, tree, tree_stride_b, tree_stride_t};
+  return paged(q, cache, page_table, table_stride, max_pages, lens, B, H, T,
+               scale, window, mod, &d, out, lse, workspace, workspace_bytes,
+               stream);
 }
 
 bsm_status bsm_device_status(void* stream, int32_t* detail) {

@@ -570,20 +570,50 @@ __device__ __forceinline__ void write_row(const PagedParams& p, int b,
 // read.
 struct PaPlan {
   int len, lo;      // of one sequence: tokens, first visible one
+  int drafts;       // query tokens that are there: its last ones
   int first_group;  // of 16 tokens
   int n_groups, n_units;
   int n_cost;  // n_units + kPaRunCost, or 0 without units
 };
 
-__device__ __forceinline__ PaPlan plan_of(const PagedParams& p, int len) {
+template <bool TREE>
+__device__ __forceinline__ PaPlan plan_of(const PagedParams& p, int b) {
   PaPlan s;
-  s.len = min(max(len, 0), p.max_pages * p.page_size);
-  s.lo = p.window > 0 ? max(0, s.len - p.T - p.window + 1) : 0;
+  s.len = min(max(p.lens[b], 0), p.max_pages * p.page_size);
+  s.drafts = p.T;
+  if (TREE) {
+    s.drafts = min(p.T, s.len);
+    if (p.n_new != nullptr) s.drafts = min(max(p.n_new[b], 0), s.drafts);
+  }
+  s.lo = p.window > 0 ? max(0, s.len - s.drafts - p.window + 1) : 0;
   s.first_group = s.lo / kPaGroup;
   s.n_groups = (s.len + kPaGroup - 1) / kPaGroup - s.first_group;
   s.n_units = (s.n_groups + kPaWarps - 1) / kPaWarps;
+  if (TREE && s.drafts == 0) s.n_groups = s.n_units = 0;
   s.n_cost = s.n_units > 0 ? s.n_units + kPaRunCost : 0;
   return s;
+}
+
+// Drafted tokens.  Draft t of a sequence with n of them lies n - t places
+// before its end; it sees every token before the drafts, and draft j where bit
+// j of its row is set (without a tree: j <= t).  Bits of drafts that are not
+// there count as clear.  Its depth, which gives its position behind the tokens
+// before the drafts, is the number of drafts it sees, less itself; -1: it sees
+// none, and its row is empty.
+__device__ __forceinline__ uint32_t draft_bits(const PagedParams& p, int b,
+                                               int t, int word, int n) {
+  const int left = (p.tree != nullptr ? n : min(n, t + 1)) - 32 * word;
+  const uint32_t there = left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1u;
+  return p.tree == nullptr
+             ? there
+             : p.tree[b * p.tree_sb + t * p.tree_st + word] & there;
+}
+__device__ __forceinline__ int draft_depth(const PagedParams& p, int b, int t,
+                                           int n) {
+  if (p.tree == nullptr) return t;
+  int seen = 0;
+  for (int w = 0; w * 32 < n; ++w) seen += __popc(draft_bits(p, b, t, w, n));
+  return seen - 1;
 }
 
 // a * b / c, in 32 bits where that is enough (a 64-bit division takes some
@@ -604,16 +634,18 @@ struct PaScan {
 
 // One warp's scan of the lengths, every warp on its own (no barrier): lane i
 // takes `chunk` sequences in order.  n: its sequences' units.
+template <bool TREE>
 __device__ __forceinline__ int lane_units(const PagedParams& p, int chunk,
                                           int64_t* n) {
   const int b0 = (threadIdx.x % 32) * chunk;
   int64_t sum = 0;
   for (int i = 0; i < chunk; ++i)
-    if (b0 + i < p.B) sum += plan_of(p, p.lens[b0 + i]).n_cost;
+    if (b0 + i < p.B) sum += plan_of<TREE>(p, b0 + i).n_cost;
   *n = sum;
   return b0;
 }
 
+template <bool TREE>
 __device__ __forceinline__ PaScan scan_before(const PagedParams& p, int seq) {
   const int chunk = (p.B + 31) / 32;
   int64_t all = 0, head = 0;
@@ -621,7 +653,7 @@ __device__ __forceinline__ PaScan scan_before(const PagedParams& p, int seq) {
   for (int i = 0; i < chunk; ++i) {
     const int b = i * 32 + threadIdx.x % 32;
     if (b < p.B) {
-      const int n = plan_of(p, p.lens[b]).n_cost;
+      const int n = plan_of<TREE>(p, b).n_cost;
       all += n;
       if (b < seq) head += n;
     }
@@ -637,13 +669,13 @@ __device__ __forceinline__ PaScan scan_before(const PagedParams& p, int seq) {
 // Sums all units (of one item row) and finds the sequence that holds the unit
 // `u_of(total)` of `per` item rows per sequence: the b with start(b) <= u <
 // start(b + 1).  Whole warps; the same in every one.
-template <class F>
+template <bool TREE, class F>
 __device__ __forceinline__ int find_sequence(const PagedParams& p, int per,
                                              F&& u_of, int64_t* start) {
   const int lane = threadIdx.x % 32;
   const int chunk = (p.B + 31) / 32;
   int64_t n;
-  int b = lane_units(p, chunk, &n);
+  int b = lane_units<TREE>(p, chunk, &n);
   int64_t inc = n;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
@@ -659,7 +691,7 @@ __device__ __forceinline__ int find_sequence(const PagedParams& p, int per,
   if (lane == owner)
     for (;; ++b) {
       const int64_t m =
-          static_cast<int64_t>(plan_of(p, p.lens[b]).n_cost) * per;
+          static_cast<int64_t>(plan_of<TREE>(p, b).n_cost) * per;
       if (u < at + m) break;
       at += m;
     }
@@ -684,7 +716,7 @@ __device__ __forceinline__ int64_t busy_ctas(int64_t units, int64_t grid) {
 // rounding is 2^-11) and q, scaled by a power of two per row.
 // `part`: where to leave o [row][D], m and l of an item cut across CTAs, or
 // null to write the result.
-template <int D, int NT>
+template <int D, int NT, bool TREE>
 __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
                                            int b, const PaPlan& plan, int hkv,
                                            int row0, int g0, int g1,
@@ -699,6 +731,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
   // which -inf - m and m - m need no special case
   const float kLowest = __int_as_float(0xff7fffff);
   const int len = plan.len, lo = plan.lo, first_group = plan.first_group;
+  const int base = len - plan.drafts;  // tokens before the drafts (TREE)
 
   // the copies start first; the queries are loaded while they run
   const uint32_t ring = smem_u32(smem) + warp * kPaStages * C::kStage;
@@ -802,6 +835,12 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
       const bool live = rr < rows;
       q_mul[nt][i] = u * p.scale_x;
       pos[nt][i] = live ? len - p.T + rr % p.T : -1;
+      if (TREE) {
+        const int t = live ? rr % p.T : 0;
+        const int depth =
+            live && t < plan.drafts ? draft_depth(p, b, t, plan.drafts) : -1;
+        pos[nt][i] = depth >= 0 ? base + depth : -1;
+      }
       slope2[nt][i] = (p.mod.kind & kModBias) && live
                           ? p.mod.slopes[hkv * G + rr / p.T] *
                                 1.4426950408889634f
@@ -810,7 +849,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
   }
   if (NT > 1) __syncthreads();
   // a group none of whose tokens any live row masks
-  const int pos_min = len - p.T, pos_max = len - 1;
+  const int pos_min = TREE ? base - 1 : len - p.T, pos_max = len - 1;
 
   float o[NT][kSteps][4];
   float m[NT][2], l[NT][2];
@@ -933,6 +972,38 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
     // ---- logits in log2 units, mask, running maximum
     const bool inner = tok + kPaGroup - 1 <= pos_min &&
                        (p.window <= 0 || pos_max - tok < p.window);
+    // of drafts among the group: what each row sees of the lane's two tokens,
+    // and their distances, which depths give
+    bool hidden[NT][4];
+    if (TREE && !inner) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = tok + g + h * 8;
+        const bool draft = j >= base && j < len;
+        const int at =
+            draft && (p.window > 0 || (p.mod.kind & kModBias))
+                ? base + draft_depth(p, b, j - base, plan.drafts)
+                : j;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int rr = row0 + nt * 8 + 2 * t + c;
+            bool hide = j >= len || pos[nt][c] < 0;
+            if (draft && !hide)
+              hide = !(draft_bits(p, b, rr % p.T, (j - base) / 32,
+                                  plan.drafts) >> ((j - base) % 32) & 1u);
+            hidden[nt][2 * h + c] =
+                hide || (p.window > 0 && pos[nt][c] - at >= p.window);
+            if (draft && (p.mod.kind & kModBias))
+              s[nt][2 * h + c] = fmaf(
+                  slope2[nt][c],
+                  -fabsf(static_cast<float>(pos[nt][c] - at)) -
+                      (d[nt][c] + h * 8.f),
+                  s[nt][2 * h + c]);  // (less what is added below)
+          }
+      }
+    }
     bool grow = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -943,7 +1014,9 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
         if (p.mod.kind & kModBias)
           x = fmaf(slope2[nt][c], d[nt][c] + (i >> 1) * 8.f, x);
         if (!inner &&
-            (j > pos[nt][c] || (p.window > 0 && pos[nt][c] - j >= p.window)))
+            (TREE ? hidden[nt][i]
+                  : j > pos[nt][c] ||
+                        (p.window > 0 && pos[nt][c] - j >= p.window)))
           x = NEG_INF;
         s[nt][i] = x;
         grow = grow || !(x <= m[nt][c]);
@@ -1026,7 +1099,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
     // Where the rows see different tokens (T > 1 only), a NaN value that a
     // row does not see must not reach it as 0 * NaN: such elements are taken
     // out of V, and the rows that do see one get NaN there.
-    if (!inner && p.T > 1) {
+    if (!inner && (TREE || p.T > 1)) {
       uint32_t any = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -1042,8 +1115,9 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
             float f[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-              f[c] = j > pos[nt][c] ||
-                             (p.window > 0 && pos[nt][c] - j >= p.window)
+              f[c] = (TREE ? hidden[nt][2 * hh + c]
+                           : j > pos[nt][c] ||
+                                 (p.window > 0 && pos[nt][c] - j >= p.window))
                          ? 0.f
                          : 1.f;
             seen[nt][hh] = transpose8x8(pack_f16x2(f[0], f[1]));
@@ -1111,6 +1185,12 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
       for (int d = 4; d < 32; d *= 2)
         sum += __shfl_xor_sync(0xffffffffu, sum, d);
       const int r = nt * 8 + 2 * t + c;
+      if (TREE && pos[nt][c] < 0) {  // an empty row, whatever it gathered
+        sum = 0.f;
+        m[nt][c] = kLowest;
+#pragma unroll
+        for (int d = 0; d < kSteps; ++d) o[nt][d][c] = o[nt][d][c + 2] = 0.f;
+      }
       if (g == 0) {
         sm[warp * R + r] = m[nt][c];
         sl[warp * R + r] = sum;
@@ -1159,7 +1239,7 @@ constexpr int kPaPerSm = D == 64 ? 4 : 3;
 
 static_assert(kPaPerSm<64, 2> <= kPaMaxPerSm, "workspace");
 
-template <int D, int NT>
+template <int D, int NT, bool TREE>
 __global__ void __launch_bounds__(kPaThreads, kPaPerSm<D, NT>)
     paged_attention_kernel(const PagedParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -1172,10 +1252,13 @@ __global__ void __launch_bounds__(kPaThreads, kPaPerSm<D, NT>)
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < p.B; b += kPaThreads) {
       const int len = p.lens[b];
-      if (len != plan_of(p, len).len) record_bad_index(b, -1, len);
+      const PaPlan plan = plan_of<TREE>(p, b);
+      if (len != plan.len) record_bad_index(b, -1, len);
+      if (TREE && p.n_new != nullptr && p.n_new[b] != plan.drafts)
+        record_bad_index(b, -1, p.n_new[b]);
     }
   int64_t u = -1, end = -1, start;
-  int b = find_sequence(
+  int b = find_sequence<TREE>(
       p, per,
       [&](int64_t all) {
         const int64_t units = all * per;
@@ -1189,7 +1272,7 @@ __global__ void __launch_bounds__(kPaThreads, kPaPerSm<D, NT>)
       &start);
   if (b < 0) return;
   while (u < end) {
-    const PaPlan plan = plan_of(p, p.lens[b]);
+    const PaPlan plan = plan_of<TREE>(p, b);
     const int64_t row_cost = static_cast<int64_t>(plan.n_cost) * per;
     if (u >= start + row_cost) {
       start += row_cost;
@@ -1212,8 +1295,9 @@ __global__ void __launch_bounds__(kPaThreads, kPaPerSm<D, NT>)
       if (r0 > 0 || r1 < plan.n_units)  // slot 0: an earlier CTA has the start
         part = p.parts + (blockIdx.x * 2 + (r0 > 0 ? 0 : 1)) *
                              static_cast<int64_t>(8 * NT * (D + 2));
-      attend_run<D, NT>(p, smem, b, plan, item / tiles, item % tiles * 8 * NT,
-                        r0 * kPaWarps, min(r1 * kPaWarps, plan.n_groups), part);
+      attend_run<D, NT, TREE>(p, smem, b, plan, item / tiles,
+                              item % tiles * 8 * NT, r0 * kPaWarps,
+                              min(r1 * kPaWarps, plan.n_groups), part);
     }
     u += n;
   }
@@ -1222,7 +1306,7 @@ __global__ void __launch_bounds__(kPaThreads, kPaPerSm<D, NT>)
 // Joins the parts of the items that were cut and writes the rows of sequences
 // without tokens: a warp per query row, or (WIDE) a block, whose warps share
 // the parts.
-template <int D, int NT, bool WIDE>
+template <int D, int NT, bool WIDE, bool TREE>
 __global__ void __launch_bounds__(kPaThreads)
     paged_join_kernel(const PagedParams p, const int grid) {
   constexpr int R = 8 * NT, kPer = D / 32;
@@ -1233,9 +1317,9 @@ __global__ void __launch_bounds__(kPaThreads)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int r = WIDE ? blockIdx.x : blockIdx.x * kPaWarps + warp;
   const int rr = item % tiles * R + r;
-  const PaScan scan = scan_before(p, b);
+  const PaScan scan = scan_before<TREE>(p, b);
   const int64_t units = scan.all * per;
-  const int n = plan_of(p, p.lens[b]).n_units;
+  const int n = plan_of<TREE>(p, b).n_units;
   // every block waits for the attention grid, so that work after this kernel
   // on the stream sees what that grid wrote itself
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1324,10 +1408,10 @@ __global__ void __launch_bounds__(kPaThreads)
   write_row<kPer>(p, b, head, t, lane * kPer, base, sum, x);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool TREE>
 cudaError_t launch_paged(const PagedParams& p, int num_sms,
                          cudaStream_t stream) {
-  auto kern = paged_attention_kernel<D, NT>;
+  auto kern = paged_attention_kernel<D, NT, TREE>;
   cudaError_t e = cudaFuncSetAttribute(
       kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PaCfg<D, NT>::kSmem);
   if (e != cudaSuccess) return e;
@@ -1352,10 +1436,10 @@ cudaError_t launch_paged(const PagedParams& p, int num_sms,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return wide
-             ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, NT, true>, p, grid)
-             : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, NT, false>, p,
-                                  grid);
+  return wide ? cudaLaunchKernelEx(
+                    &cfg, paged_join_kernel<D, NT, true, TREE>, p, grid)
+              : cudaLaunchKernelEx(
+                    &cfg, paged_join_kernel<D, NT, false, TREE>, p, grid);
 }
 
 }  // namespace
@@ -1397,17 +1481,28 @@ cudaError_t launch_kv_append_rope(const AppendParams& p, const TurnParams& t,
                     : append_rope<64>(p, t, stream);
 }
 
-cudaError_t launch_paged_attention(const PagedParams& p, int num_sms,
-                                   cudaStream_t stream) {
+template <bool TREE>
+static cudaError_t launch_rows(const PagedParams& p, int num_sms,
+                               cudaStream_t stream) {
   // one tile of 8 query rows, or two where the group and the tokens fill them
   const bool two = static_cast<int64_t>(p.H / p.H_kv) * p.T > 8;
   if (p.D == 128)
-    return two ? launch_paged<128, 2>(p, num_sms, stream)
-               : launch_paged<128, 1>(p, num_sms, stream);
+    return two ? launch_paged<128, 2, TREE>(p, num_sms, stream)
+               : launch_paged<128, 1, TREE>(p, num_sms, stream);
   if (p.D == 64)
-    return two ? launch_paged<64, 2>(p, num_sms, stream)
-               : launch_paged<64, 1>(p, num_sms, stream);
+    return two ? launch_paged<64, 2, TREE>(p, num_sms, stream)
+               : launch_paged<64, 1, TREE>(p, num_sms, stream);
   return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_paged_attention(const PagedParams& p, int num_sms,
+                                   cudaStream_t stream) {
+  return launch_rows<false>(p, num_sms, stream);
+}
+
+cudaError_t launch_paged_tree(const PagedParams& p, int num_sms,
+                              cudaStream_t stream) {
+  return launch_rows<true>(p, num_sms, stream);
 }
 
 cudaError_t read_cache_error(int32_t out[4]) {

@@ -214,6 +214,12 @@ struct PagedParams {
   int64_t o_sb, o_sh, o_ss;
   float* lse;  // [B][H][T] or null
   float* parts;  // workspace: parts of the items cut across CTAs
+  // drafted tokens (bsm_paged_attention_tree): how many of a sequence's last
+  // tokens are drafts, or null (T), and the bits of the drafts that each sees,
+  // tree[b * tree_sb + t * tree_st + word], or null (those up to itself)
+  const int32_t* n_new;
+  const uint32_t* tree;
+  int64_t tree_sb, tree_st;
 };
 // The workspace: for up to kPaMaxSms SMs with kPaMaxPerSm CTAs each, two parts
 // per CTA: o, m and l of up to 16 query rows.
@@ -231,6 +237,8 @@ cudaError_t launch_norm_rope_bwd(NormRopeParams& p, int num_sms,
                                  cudaStream_t stream);
 cudaError_t launch_paged_attention(const PagedParams& p, int num_sms,
                                    cudaStream_t stream);
+cudaError_t launch_paged_tree(const PagedParams& p, int num_sms,
+                              cudaStream_t stream);
 // Reads and clears the device error record of the cache kernels.
 cudaError_t read_cache_error(int32_t out[4]);
 cudaError_t launch_mask_info(const MaskInfoParams& p, cudaStream_t stream);

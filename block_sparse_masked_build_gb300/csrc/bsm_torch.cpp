@@ -35,6 +35,8 @@ decltype(&bsm_splash_fwd_mod) f_splash_fwd_mod;
 decltype(&bsm_splash_bwd_mod) f_splash_bwd_mod;
 decltype(&bsm_kv_append) f_kv_append;
 decltype(&bsm_paged_attention) f_paged_attention;
+decltype(&bsm_paged_attention_tree) f_paged_tree;
+decltype(&bsm_paged_attention_tree_workspace_bytes) f_paged_tree_bytes;
 decltype(&bsm_kv_append_rope) f_kv_append_rope;
 decltype(&bsm_norm_rope) f_norm_rope;
 decltype(&bsm_norm_rope_bwd) f_norm_rope_bwd;
@@ -274,7 +276,7 @@ at::Tensor workspace(int kind, size_t bytes, const at::Device& dev,
   using Key = std::pair<std::pair<int, int>, void*>;
   static auto* kept = new std::map<Key, at::Tensor>();
   at::Tensor& t = (*kept)[Key({kind, dev.index()}, stream)];
-  if (!t.defined())
+  if (!t.defined() || t.nbytes() < bytes)
     t = empty_on({static_cast<int64_t>(bytes)}, at::kByte, dev);
   return t;
 }
@@ -735,19 +737,38 @@ PyObject* py_kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The drafts' bits: int32 words [B, T, W] or [T, W].
+void check_tree(const at::Tensor& t, int64_t B, int64_t T,
+                const at::Device& dev) {
+  const int64_t d = t.dim(), words = (T + 31) / 32;
+  if ((t.scalar_type() != at::kInt && t.scalar_type() != at::kUInt32) ||
+      (d != 2 && d != 3) || (d == 3 && t.size(0) != B) || t.size(d - 2) != T ||
+      t.size(d - 1) < words || (words > 1 && t.stride(d - 1) != 1) ||
+      t.device() != dev)
+    value_error("tree must be an int32 tensor [" + std::to_string(B) + ", " +
+                std::to_string(T) + ", " + std::to_string(words) +
+                "] (the batch may be left out) with contiguous rows, beside "
+                "the cache");
+}
+
 // paged_attention(k_pages, v_pages, k_scale, v_scale, page_table, lens, q,
-// scale or None, window, softcap, slopes, out, lse, want_lse, stream) ->
-// (out, lse)
+// scale or None, window, softcap, slopes, out, lse, want_lse, stream), and
+// behind them, for drafted tokens: tree, n_new -> (out, lse)
 PyObject* py_paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    expect(n, 15);
+    if (n != 17) expect(n, 15);
     const bsm_kv_cache c = cache_of(a);
     const at::Device dev = tensor(a[0], "k_pages").device();
     const at::Tensor &table = tensor(a[4], "page_table"),
                      &lens = tensor(a[5], "lens"), &q = tensor(a[6], "q");
     if (q.dim() != 4) value_error("q must be [B, H, T, D]");
     const int64_t B = q.size(0), H = q.size(1), T = q.size(2);
-    check_table(dev, table, B, lens, at::Tensor());
+    const at::Tensor tree =
+        n == 17 ? tensor_or_none(a[15], "tree") : at::Tensor();
+    const at::Tensor n_new =
+        n == 17 ? tensor_or_none(a[16], "n_new") : at::Tensor();
+    check_table(dev, table, B, lens, n_new);
+    if (tree.defined()) check_tree(tree, B, T, dev);
     const bsm_tensor qt = token_view(q, B, H, T, c.D, dev, "q");
     OnDevice on(dev, a[14]);
     at::Tensor out = tensor_or_none(a[11], "out");
@@ -769,13 +790,27 @@ PyObject* py_paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float scale = static_cast<float>(
         a[7] == Py_None ? 1.0 / std::sqrt(static_cast<double>(c.D))
                         : number(a[7]));
-    const at::Tensor ws = workspace(1, paged_workspace_bytes, dev, on.stream);
-    check_status(f_paged_attention(
-        &qt, &c, data<const int32_t>(table), table.stride(0),
-        static_cast<int32_t>(table.size(1)), data<const int32_t>(lens),
-        static_cast<int32_t>(B), static_cast<int32_t>(H),
-        static_cast<int32_t>(T), scale, int32(a[8]), &mod, &ot,
-        data<float>(lse), data<void>(ws), bytes_of(ws), on.stream));
+    const int32_t b = static_cast<int32_t>(B), h = static_cast<int32_t>(H),
+                  t = static_cast<int32_t>(T);
+    const int32_t max_pages = static_cast<int32_t>(table.size(1));
+    if (n == 17) {
+      const at::Tensor ws = workspace(
+          3, f_paged_tree_bytes(h, c.H_kv, t, c.D), dev, on.stream);
+      check_status(f_paged_tree(
+          &qt, &c, data<const int32_t>(table), table.stride(0), max_pages,
+          data<const int32_t>(lens), data<const int32_t>(n_new),
+          data<const uint32_t>(tree),
+          tree.defined() && tree.dim() == 3 ? tree.stride(0) : 0,
+          tree.defined() ? tree.stride(tree.dim() - 2) : 0, b, h, t, scale,
+          int32(a[8]), &mod, &ot, data<float>(lse), data<void>(ws),
+          bytes_of(ws), on.stream));
+    } else {
+      const at::Tensor ws = workspace(1, paged_workspace_bytes, dev, on.stream);
+      check_status(f_paged_attention(
+          &qt, &c, data<const int32_t>(table), table.stride(0), max_pages,
+          data<const int32_t>(lens), b, h, t, scale, int32(a[8]), &mod, &ot,
+          data<float>(lse), data<void>(ws), bytes_of(ws), on.stream));
+    }
     PyObject* r = PyTuple_New(2);
     PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(out)));
     if (lse.defined()) {
@@ -811,6 +846,8 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     set(f_bwd_mod_workspace_bytes, "bsm_splash_bwd_mod_workspace_bytes");
     set(f_kv_append, "bsm_kv_append");
     set(f_paged_attention, "bsm_paged_attention");
+    set(f_paged_tree, "bsm_paged_attention_tree");
+    set(f_paged_tree_bytes, "bsm_paged_attention_tree_workspace_bytes");
     set(f_kv_append_rope, "bsm_kv_append_rope");
     set(f_norm_rope, "bsm_norm_rope");
     set(f_norm_rope_bwd, "bsm_norm_rope_bwd");

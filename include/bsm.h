@@ -501,6 +501,35 @@ bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
  * parts of rows whose keys are split over several CTAs. */
 size_t bsm_paged_attention_workspace_bytes(void);
 
+/* bsm_paged_attention where the queries are drafted tokens that form a tree
+ * (speculative decoding: several guesses of how a sequence goes on, answered
+ * at once).  The last n = n_new[b] tokens of sequence b are drafts (append
+ * them first, in the tree's order); query t < n is draft t.  It sees every
+ * token before the drafts, and draft j where bit j % 32 of word
+ *     tree[b * tree_stride_b + t * tree_stride_t + j / 32]
+ * is set: its ancestors' bits and its own.  Bits from n on are not looked at.
+ *   n_new   device int32 [B], or NULL: min(T, lens[b]) each
+ *   tree    device, rows of ceil(T / 32) words (a batch stride of 0 gives all
+ *           sequences one tree), T <= 1024; or NULL: draft t sees the drafts j
+ *           <= t, as one guess that goes on for n tokens
+ * A draft's position is lens[b] - n plus its depth, which is the number of bits
+ * set in its row, less one; a window and a bias go by these positions (the
+ * distance is taken without its sign).  A row with no bits set sees nothing,
+ * and so do the rows t >= n: out = 0 and lse = -inf.  n_new[b] outside [0,
+ * min(T, lens[b])] is cut to it and reported by bsm_device_status; everything
+ * else as in bsm_paged_attention.
+ *   workspace  >= bsm_paged_attention_tree_workspace_bytes(H, H_kv, T, D) */
+bsm_status bsm_paged_attention_tree(
+    const bsm_tensor* q, const bsm_kv_cache* cache, const int32_t* page_table,
+    int64_t table_stride, int32_t max_pages, const int32_t* lens,
+    const int32_t* n_new, const uint32_t* tree, int64_t tree_stride_b,
+    int64_t tree_stride_t, int32_t B, int32_t H, int32_t T, float scale,
+    int32_t window, const bsm_score_mod* mod, const bsm_tensor* out,
+    float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+size_t bsm_paged_attention_tree_workspace_bytes(int32_t H, int32_t H_kv,
+                                                int32_t T, int32_t D);
+
 /* Rotation of a head's row by its position (no counterpart on the pages): of
  * the row's first `dim` elements the pairs (x[i], x[i + dim / 2]), or with
  * `interleaved` (x[2 i], x[2 i + 1]), i < dim / 2, turn by the angle
