@@ -1184,16 +1184,20 @@ bsm_status paged(const bsm_tensor* q, const bsm_kv_cache* cache,
     return fail(BSM_ERR_UNSUPPORTED, "too many query rows");
   if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
     return fail(BSM_ERR_INVALID_ARG, "lse must be 4-byte aligned");
-  if (workspace == nullptr || workspace_bytes < bsm::kPaWorkspaceBytes ||
-      !aligned16(workspace))
+  const bool tc = drafts != nullptr && bsm::tree_tiles(rows) > 0;
+  const size_t need = drafts != nullptr
+                          ? bsm::tree_workspace_bytes(rows, cache->D)
+                          : bsm::kPaWorkspaceBytes;
+  if (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))
     return fail(BSM_ERR_INVALID_ARG,
-                "workspace must be >= bsm_paged_attention_workspace_bytes() "
-                "bytes, 16-byte aligned");
+                std::string("workspace must be >= bsm_paged_attention") +
+                    (drafts != nullptr ? "_tree" : "") +
+                    "_workspace_bytes() bytes, 16-byte aligned");
   int num_sms = 0;
   s = check_device(&num_sms);
   if (s != BSM_OK) return s;
-  if (num_sms > bsm::kPaMaxSms)
-    return fail(BSM_ERR_UNSUPPORTED, "more than 256 SMs");
+  if (num_sms > (tc ? bsm::kTreeMaxSms : bsm::kPaMaxSms))
+    return fail(BSM_ERR_UNSUPPORTED, "too many SMs");
   p.parts = static_cast<float*>(workspace);
   p.k = static_cast<const uint8_t*>(cache->k);
   p.v = static_cast<const uint8_t*>(cache->v);
@@ -1231,9 +1235,10 @@ bsm_status paged(const bsm_tensor* q, const bsm_kv_cache* cache,
     p.tree_sb = drafts->sb;
     p.tree_st = drafts->st;
   }
-  const cudaError_t e = drafts != nullptr
-                            ? bsm::launch_paged_tree(p, num_sms, st)
-                            : bsm::launch_paged_attention(p, num_sms, st);
+  const cudaError_t e =
+      tc ? bsm::launch_tree_tc(p, num_sms, wait_timeout_ns(), st)
+      : drafts != nullptr ? bsm::launch_paged_tree(p, num_sms, st)
+                          : bsm::launch_paged_attention(p, num_sms, st);
   if (e != cudaSuccess) return cuda_fail(e, "paged_attention launch");
   return BSM_OK;
 }
@@ -1255,7 +1260,8 @@ bsm_status bsm_paged_attention(const bsm_tensor* q, const bsm_kv_cache* cache,
 
 size_t bsm_paged_attention_tree_workspace_bytes(int32_t H, int32_t H_kv,
                                                 int32_t T, int32_t D) {
-  return bsm::kPaWorkspaceBytes;
+  if (H < 0 || H_kv <= 0 || T < 0) return 0;
+  return bsm::tree_workspace_bytes(static_cast<int64_t>(H / H_kv) * T, D);
 }
 
 bsm_status bsm_paged_attention_tree(
@@ -1282,16 +1288,21 @@ bsm_status bsm_paged_attention_tree(
 bsm_status bsm_device_status(void* stream, int32_t* detail) {
   g_last_error.clear();
   int32_t rec[4] = {0, 0, 0, 0}, brec[4] = {0, 0, 0, 0};
-  int32_t crec[4] = {0, 0, 0, 0};
+  int32_t crec[4] = {0, 0, 0, 0}, trec[4] = {0, 0, 0, 0};
   cudaError_t e = bsm::read_device_error(rec, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "device status");
   e = bsm::read_bwd_error(brec);
   if (e != cudaSuccess) return cuda_fail(e, "device status");
   if (rec[0] == 0 && brec[0] != 0) std::memcpy(rec, brec, sizeof(rec));
+  // (of timeouts or bad indices; the first is reported)
+  if (rec[0] == 0) e = bsm::read_tree_error(trec);
+  if (e != cudaSuccess) return cuda_fail(e, "device status");
+  if (trec[0] == 1) std::memcpy(rec, trec, sizeof(rec));
   // read, and so cleared, only where no timeout is reported before it: else
   // the next call reports it
   if (rec[0] == 0) e = bsm::read_cache_error(crec);
   if (e != cudaSuccess) return cuda_fail(e, "device status");
+  if (crec[0] == 0 && trec[0] == 2) std::memcpy(crec, trec, sizeof(crec));
   if (crec[0] != 0) {
     if (detail != nullptr) std::memcpy(detail, crec, sizeof(crec));
     return fail(BSM_ERR_INVALID_ARG,

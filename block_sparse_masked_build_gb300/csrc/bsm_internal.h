@@ -239,6 +239,16 @@ cudaError_t launch_paged_attention(const PagedParams& p, int num_sms,
                                    cudaStream_t stream);
 cudaError_t launch_paged_tree(const PagedParams& p, int num_sms,
                               cudaStream_t stream);
+// The same for many query rows, on the tensor core: tiles of 128 query rows
+// that a CTA takes at once (0: too few rows, launch_paged_tree serves them),
+// its workspace (for up to kTreeMaxSms SMs) and launch.
+constexpr int kTreeMaxSms = 160;
+int tree_tiles(int64_t rows);
+size_t tree_workspace_bytes(int64_t rows, int D);
+cudaError_t launch_tree_tc(const PagedParams& p, int num_sms,
+                           uint64_t timeout_ns, cudaStream_t stream);
+// Reads and clears its device error record.
+cudaError_t read_tree_error(int32_t out[4]);
 // Reads and clears the device error record of the cache kernels.
 cudaError_t read_cache_error(int32_t out[4]);
 cudaError_t launch_mask_info(const MaskInfoParams& p, cudaStream_t stream);
