@@ -335,99 +335,81 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Converts them into the f16 tile at `tile`: rows of 64 elements (128 bytes)
-// per token, two such blocks at D = 128, in the 128-byte swizzle.  Tokens that
-// are no sequence's become zeros, and so do NaN codes of values, which are
-// noted: a row that does not see them must not meet 0 * NaN.
-template <int D, bool V>
-__device__ __forceinline__ void store_codes(const PagedParams& p, TcCtl* c,
+// What a step that is not plain needs before its codes are converted: tokens
+// that are no sequence's become zeros, and so do NaN codes of values, which are
+// noted, as a row that does not see them must not meet 0 * NaN; and the
+// positions of its columns.
+template <int D>
+__device__ __forceinline__ void clean_codes(const PagedParams& p, TcCtl* c,
                                             const TcStep& s, uint32_t step,
-                                            TcLoad<D>& l, uint32_t tile) {
-  constexpr int kPer = D / 16;  // pieces of a token's row
+                                            bool values, TcLoad<D>& l) {
+  constexpr int kPer = D / 16, kRows = 128 / kPer;
   const int i = threadIdx.x % 128;
   const int piece = i % kPer, row = i / kPer;
-  constexpr int kRows = 128 / kPer;
-  if (!s.plain) {
-#pragma unroll
-    for (int k = 0; k < TcLoad<D>::kPieces; ++k) {
-      const int tr = row + k * kRows, tok = s.tok0 + tr;
-      if (tok < s.lo || tok >= s.len) l.x[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (V) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(&l.x[k]);
-        uint32_t found = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t n = nan_codes(w[j]) >> 7;  // one bit per byte
-          w[j] &= ~(n * 0xffu);
-          // the four bits 0, 8, 16, 24 next to each other
-          found |= ((n * 0x00204081u >> 21) & 0xfu) << (4 * j);
-        }
-        c->nan[step % 4][tr][piece] = static_cast<uint16_t>(found);
-        if (found != 0) c->nan_step[step % 4] = step + 1;
-      }
-    }
-    if (V && (p.window > 0 || (p.mod.kind & kModBias))) {
-      const int tok = s.tok0 + i, base = s.len - s.n;
-      c->pos[step % 4][i] =
-          tok >= base && tok < s.len
-              ? base + draft_depth(p, s.b, tok - base, s.n)
-              : tok;
-    }
-  }
-  // (lanes of the upper block store their second half first: eight lanes then
-  // touch eight different 16-byte columns)
-  const uint32_t flip = D == 128 ? piece >> 2 : 0u;
 #pragma unroll
   for (int k = 0; k < TcLoad<D>::kPieces; ++k) {
-    const int tr = row + k * kRows;
-    const uint32_t w[4] = {l.x[k].x, l.x[k].y, l.x[k].z, l.x[k].w};
-    uint32_t h[8];
+    const int tr = row + k * kRows, tok = s.tok0 + tr;
+    if (tok < s.lo || tok >= s.len) l.x[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (values) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(&l.x[k]);
+      uint32_t found = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      h[2 * j] = e4m3x2_to_f16x2(w[j]);
-      h[2 * j + 1] = e4m3x2_to_f16x2_hi(w[j]);
-    }
-    if (V) {
-      const float m = s.v_mul[min(tr / kPaGroup, s.groups - 1)];
-      if (m != 1.f) {
-        const uint32_t mm = pack_f16x2(m, m);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = hmul2(h[j], mm);
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t n = nan_codes(w[j]) >> 7;  // one bit per byte
+        w[j] &= ~(n * 0xffu);
+        // the four bits 0, 8, 16, 24 next to each other
+        found |= ((n * 0x00204081u >> 21) & 0xfu) << (4 * j);
       }
+      c->nan[step % 4][tr][piece] = static_cast<uint16_t>(found);
+      if (found != 0) c->nan_step[step % 4] = step + 1;
     }
-    const uint32_t line = tile + (D == 128 ? (piece >> 2) * (kTcTokens * 128) : 0) +
-                          tr * 128;
-    const uint32_t c0 = (2 * piece) & 7, sw = tr & 7;
-    const uint32_t a = line + (((c0 | flip) ^ sw) << 4);
-    const uint32_t b = line + (((c0 | (flip ^ 1)) ^ sw) << 4);
-    const bool f = flip != 0;
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a),
-                 "r"(f ? h[4] : h[0]), "r"(f ? h[5] : h[1]),
-                 "r"(f ? h[6] : h[2]), "r"(f ? h[7] : h[3])
-                 : "memory");
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(b),
-                 "r"(f ? h[0] : h[4]), "r"(f ? h[1] : h[5]),
-                 "r"(f ? h[2] : h[6]), "r"(f ? h[3] : h[7])
-                 : "memory");
+  }
+  if (values && (p.window > 0 || (p.mod.kind & kModBias))) {
+    const int tok = s.tok0 + i, base = s.len - s.n;
+    c->pos[step % 4][i] = tok >= base && tok < s.len
+                              ? base + draft_depth(p, s.b, tok - base, s.n)
+                              : tok;
   }
 }
 
-// One half of a step (its keys, or its values) into the ring.
-template <int D, int R, bool V>
-__device__ __forceinline__ bool convert_half(const TcParams& t, TcCtl* c,
-                                             uint32_t kv, uint32_t step,
-                                             TcLoad<D>& l) {
-  using C = TcCfg<D, R>;
-  const uint32_t h = 2 * step + (V ? 1 : 0);
-  const uint32_t slot = h % C::kSlots;
-  if (!tc_wait(t, c, &c->kv_empty[slot], ((h / C::kSlots) & 1) ^ 1,
-               kRoleConvert, V))
-    return false;
-  store_codes<D, V>(t.p, c, c->steps[step % kTcSteps], step, l,
-                    kv + slot * C::kTile);
-  fence_proxy_async();
-  warp_arrive(&c->kv_full[slot]);
-  return true;
+template <int OFF>
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y,
+                                       uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0+%5], {%1, %2, %3, %4};" ::"r"(a), "r"(x),
+               "r"(y), "r"(z), "r"(w), "n"(OFF)
+               : "memory");
+}
+
+// Piece K of a thread and the ones behind it into the f16 tile (see
+// convert_role); a, b: where the two halves of piece 0 go.
+template <int D, int K>
+__device__ __forceinline__ void store_codes(const TcStep& s, bool values,
+                                            bool flip, uint32_t a, uint32_t b,
+                                            const TcLoad<D>& l) {
+  constexpr int kRows = 2048 / D;
+  const uint32_t w[4] = {l.x[K].x, l.x[K].y, l.x[K].z, l.x[K].w};
+  uint32_t h[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    h[2 * j] = e4m3x2_to_f16x2(w[j]);
+    h[2 * j + 1] = e4m3x2_to_f16x2_hi(w[j]);
+  }
+  if (values) {
+    const int g = D == 128 ? K : 2 * K + threadIdx.x % 128 / 64;
+    const float m = s.v_mul[g];
+    if (m != 1.f) {
+      const uint32_t mm = pack_f16x2(m, m);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = hmul2(h[j], mm);
+    }
+  }
+  constexpr int off = K * kRows * 128;
+  sts128<off>(a, flip ? h[4] : h[0], flip ? h[5] : h[1], flip ? h[6] : h[2],
+              flip ? h[7] : h[3]);
+  sts128<off>(b, flip ? h[0] : h[4], flip ? h[1] : h[5], flip ? h[2] : h[6],
+              flip ? h[3] : h[7]);
+  if constexpr (K + 1 < TcLoad<D>::kPieces)
+    store_codes<D, K + 1>(s, values, flip, a, b, l);
 }
 
 __device__ __forceinline__ bool wait_step(const TcParams& t, TcCtl* c,
@@ -436,45 +418,64 @@ __device__ __forceinline__ bool wait_step(const TcParams& t, TcCtl* c,
                  role, 9);
 }
 
-// The keys or the values of every step (one tile of rows: a warpgroup each).
-template <int D, bool V>
-__device__ __forceinline__ void convert_role1(const TcParams& t, TcCtl* c,
-                                              uint32_t kv) {
-  const uint8_t* pages = V ? t.p.v : t.p.k;
-  TcLoad<D> a, b;
-  uint32_t step = 0;
-  // `now` holds step's codes; the next step's go into `then`
-  auto turn = [&](TcLoad<D>& now, TcLoad<D>& then) {
-    if (!wait_step(t, c, step + 1, kRoleConvert)) return false;
-    const bool more = c->steps[(step + 1) % kTcSteps].groups != 0;
-    if (more) load_codes<D>(c->steps[(step + 1) % kTcSteps], pages, then);
-    if (!convert_half<D, 1, V>(t, c, kv, step, now)) return false;
-    warp_arrive(&c->step_empty[step % kTcSteps]);
-    ++step;
-    return more;
-  };
+// A converter warpgroup: with one tile of rows the keys (which = 0) or the
+// values (1) of every step, with two tiles both in turn.  The codes of the half
+// step after the one in hand are on their way meanwhile.  (One copy of the code
+// for keys and values, as the roles together must fit the SM's instruction
+// cache: with a copy for each, unrolled by two, and the MMAs unrolled, the
+// kernel waited for instructions, 373 us on 32 sequences of 300-12000 tokens
+// and 16 drafts.)
+//
+// Tiles are rows of 64 elements (128 bytes) per token, two such blocks at D =
+// 128, in the 128-byte swizzle.  Lanes of the upper block store their second
+// half first: eight lanes then touch eight different 16-byte columns.
+template <int D, int R>
+__device__ __forceinline__ void convert_role(const TcParams& t, TcCtl* c,
+                                             uint32_t kv, int which) {
+  using C = TcCfg<D, R>;
+  constexpr int kPer = D / 16;
+  const int i = threadIdx.x % 128, piece = i % kPer;
+  const uint32_t row = i / kPer;
+  const bool flip = D == 128 && piece >= 4;
+  const uint32_t line =
+      kv + (D == 128 ? (piece >> 2) * (kTcTokens * 128) : 0) + row * 128;
+  const uint32_t chunk = ((2 * piece) & 7) | (flip ? 1u : 0u);
+  const uint32_t at_a = line + ((chunk ^ (row & 7)) << 4);
+  const uint32_t at_b = line + ((chunk ^ 1u ^ (row & 7)) << 4);
+  bool values = which != 0;
+  TcLoad<D> now, next;
   if (!wait_step(t, c, 0, kRoleConvert) || c->steps[0].groups == 0) return;
-  load_codes<D>(c->steps[0], pages, a);
-  while (turn(a, b) && turn(b, a)) {
-  }
-}
-
-// Both in turn (two tiles of rows: one warpgroup).
-template <int D>
-__device__ __forceinline__ void convert_role2(const TcParams& t, TcCtl* c,
-                                              uint32_t kv) {
-  TcLoad<D> a, b;
-  if (!wait_step(t, c, 0, kRoleConvert) || c->steps[0].groups == 0) return;
-  load_codes<D>(c->steps[0], t.p.k, a);
-  for (uint32_t step = 0;; ++step) {
-    load_codes<D>(c->steps[step % kTcSteps], t.p.v, b);
-    if (!convert_half<D, 2, false>(t, c, kv, step, a)) return;
-    if (!wait_step(t, c, step + 1, kRoleConvert)) return;
-    const bool more = c->steps[(step + 1) % kTcSteps].groups != 0;
-    if (more) load_codes<D>(c->steps[(step + 1) % kTcSteps], t.p.k, a);
-    if (!convert_half<D, 2, true>(t, c, kv, step, b)) return;
-    warp_arrive(&c->step_empty[step % kTcSteps]);
+  load_codes<D>(c->steps[0], values ? t.p.v : t.p.k, now);
+#pragma unroll 1
+  for (uint32_t step = 0;;) {
+    // the half step behind this one
+    uint32_t step2 = step;
+    bool values2 = values, more = true;
+    if (R == 2) values2 = !values;
+    if (R == 1 || values) {
+      ++step2;
+      if (!wait_step(t, c, step2, kRoleConvert)) return;
+      more = c->steps[step2 % kTcSteps].groups != 0;
+    }
+    if (more)
+      load_codes<D>(c->steps[step2 % kTcSteps], values2 ? t.p.v : t.p.k, next);
+    const TcStep& s = c->steps[step % kTcSteps];
+    const uint32_t h = 2 * step + (values ? 1 : 0);
+    const uint32_t slot = h % C::kSlots;
+    if (!tc_wait(t, c, &c->kv_empty[slot], ((h / C::kSlots) & 1) ^ 1,
+                 kRoleConvert, values))
+      return;
+    if (__builtin_expect(!s.plain, 0))
+      clean_codes<D>(t.p, c, s, step, values, now);
+    store_codes<D, 0>(s, values, flip, at_a + slot * C::kTile,
+                      at_b + slot * C::kTile, now);
+    fence_proxy_async();
+    warp_arrive(&c->kv_full[slot]);
+    if (R == 1 || values) warp_arrive(&c->step_empty[step % kTcSteps]);
     if (!more) return;
+    now = next;
+    step = step2;
+    values = values2;
   }
 }
 
@@ -497,8 +498,8 @@ __device__ __forceinline__ void mma_role(const TcParams& t, TcCtl* c,
   const uint64_t dv = sdesc_sw128(smem + C::kOffKv, kTcTokens * 128, 1024);
   bool ok = true;
   uint32_t runs = 0;  // begun
-  int groups[2] = {0, 0};  // of the step and of the one before
-  bool first[2] = {false, false};
+  int groups = 0, groups_before = 0;  // of the step and of the one before
+  bool first = false, first_before = false;
   // buffer of tile r at a step, and how often it was used before
   auto buf = [](uint32_t step, int r) { return R == 2 ? r : int(step & 1); };
   auto use = [](uint32_t step) { return R == 2 ? step : step >> 1; };
@@ -506,75 +507,70 @@ __device__ __forceinline__ void mma_role(const TcParams& t, TcCtl* c,
     return tc_wait(t, c, &c->kv_full[h % C::kSlots], (h / C::kSlots) & 1,
                    kRoleMma, 2);
   };
-  auto issue_s = [&](uint32_t step, int r) {
-    const uint64_t a = dq + r * kUnits;
-    const uint64_t b = dk + (2 * step) % C::kSlots * kUnits;
-    const uint32_t idesc = idesc_f16(groups[0] * kPaGroup, false);
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const uint32_t off = (k >> 2) * (kTcTokens * 128 / 16) + (k & 3) * 2;
-      mma_ss_elect(tmem + buf(step, r) * 128, a + off, b + off, idesc, k > 0);
-    }
-    mma_commit_elect(&c->s_full[buf(step, r)]);
-  };
-  // O_r (+)= P_r V of the step before `step`
-  auto issue_pv = [&](uint32_t step, int r) {
-    const uint32_t s = step - 1, h = 2 * s + 1;
-    const int bf = buf(s, r);
-    if (!tc_wait(t, c, &c->p_full[bf], use(s) & 1, kRoleMma, 3)) return false;
-    // run k (k = runs - 1 here) finds O free when k runs were written out
-    if (first[1] && !tc_wait(t, c, &c->o_free[r], runs & 1, kRoleMma, 4))
-      return false;
-    tc_fence_after();
-    const uint64_t b = dv + h % C::kSlots * kUnits;
-    constexpr uint32_t idesc = idesc_f16(D, true);
-#pragma unroll
-    for (int k = 0; k < kTcGroups; ++k)
-      if (k < groups[1])
-        mma_ts_elect(tmem + 256 + r * 128, tmem + bf * 128 + k * 8,
-                     b + k * (kPaGroup * 128 / 16), idesc,
-                     k > 0 || !first[1]);
-    mma_commit_elect(&c->pv_done[r]);
-    return true;
-  };
+#pragma unroll 1
   for (uint32_t step = 0; ok; ++step) {
     ok = wait_step(t, c, step, kRoleMma);
     if (!ok) break;
     const TcStep& s = c->steps[step % kTcSteps];
-    groups[1] = groups[0];
-    first[1] = first[0];
-    groups[0] = s.groups;
-    first[0] = s.first != 0;
-    const bool more = groups[0] != 0;
+    groups_before = groups;
+    first_before = first;
+    groups = s.groups;
+    first = s.first != 0;
+    const bool more = groups != 0;
     warp_arrive(&c->step_empty[step % kTcSteps]);
-    if (more) ok = wait_kv(2 * step);
     // One tile: S goes ahead of the P V before it, in the other buffer, while
     // that P is in the making.  Two tiles share the steps' S and P in turn: S
     // goes behind the P V that reads its columns (MMAs of one thread run in
     // the order they were issued).  A run's first S waits for its query, which
     // the rows load when the run before is written out.
-    const bool ahead = R == 1 && !first[0];
-    if (ok && more && ahead) {
-      tc_fence_after();
-      issue_s(step, 0);
-    }
-    if (ok && step > 0) ok = wait_kv(2 * step - 1);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (ok && step > 0) ok = issue_pv(step, r);
-      if (ok && more && !ahead) {
-        if (first[0])
+    const bool ahead = R == 1 && !first;
+#pragma unroll 1
+    for (int turn = 0; turn < 2 * R; ++turn) {
+      const int r = turn >> 1;
+      if (((turn & 1) != 0) != ahead) {  // S_r = Q_r K^T
+        if (!more) continue;
+        if (r == 0) ok = wait_kv(2 * step);
+        if (ok && first)
           ok = tc_wait(t, c, &c->q_full[r], runs & 1, kRoleMma, 1);
         if (!ok) break;
         tc_fence_after();
-        issue_s(step, r);
+        const uint64_t a = dq + r * kUnits;
+        const uint64_t b = dk + (2 * step) % C::kSlots * kUnits;
+        const uint32_t idesc = idesc_f16(groups * kPaGroup, false);
+        const uint32_t d = tmem + buf(step, r) * 128;
+#pragma unroll 2
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * (kTcTokens * 128 / 16) + (k & 3) * 2;
+          mma_ss_elect(d, a + off, b + off, idesc, k > 0);
+        }
+        mma_commit_elect(&c->s_full[buf(step, r)]);
+        if (r == R - 1)
+          mma_commit_elect(&c->kv_empty[(2 * step) % C::kSlots]);
+      } else {  // O_r (+)= P_r V of the step before
+        if (step == 0) continue;
+        const uint32_t before = step - 1, h = 2 * before + 1;
+        const int bf = buf(before, r);
+        if (r == 0) ok = wait_kv(h);
+        if (ok)
+          ok = tc_wait(t, c, &c->p_full[bf], use(before) & 1, kRoleMma, 3);
+        // run k (k = runs - 1 here) finds O free when k runs were written out
+        if (ok && first_before)
+          ok = tc_wait(t, c, &c->o_free[r], runs & 1, kRoleMma, 4);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t b = dv + h % C::kSlots * kUnits;
+        constexpr uint32_t idesc = idesc_f16(D, true);
+#pragma unroll 2
+        for (int k = 0; k < groups_before; ++k)
+          mma_ts_elect(tmem + 256 + r * 128, tmem + bf * 128 + k * 8,
+                       b + k * (kPaGroup * 128 / 16), idesc,
+                       k > 0 || !first_before);
+        mma_commit_elect(&c->pv_done[r]);
+        if (r == R - 1) mma_commit_elect(&c->kv_empty[h % C::kSlots]);
       }
     }
-    if (!ok) break;
-    if (step > 0) mma_commit_elect(&c->kv_empty[(2 * step - 1) % C::kSlots]);
     if (!more) break;
-    mma_commit_elect(&c->kv_empty[(2 * step) % C::kSlots]);
-    if (first[0]) ++runs;
+    if (first) ++runs;
   }
   // every MMA issued above has completed once this arrives
   __syncwarp();
@@ -754,7 +750,7 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
     const uint32_t use = R == 2 ? step : step >> 1;
     const uint32_t s_addr = tmem + lane_off + buf * 128;
     uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-    if (!s.plain) {
+    if (__builtin_expect(!s.plain, 0)) {
       // positions and NaN codes come with the values
       const uint32_t h = 2 * step + 1;
       if (!tc_wait(tp, c, &c->kv_full[h % C::kSlots], (h / C::kSlots) & 1,
@@ -821,7 +817,7 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
         }
       }
     }
-    if (!s.plain) {
+    if (__builtin_expect(!s.plain, 0)) {
 #pragma unroll
       for (int j = 0; j < kTcTokens; ++j)
         if (!(keep[j / 32] >> (j % 32) & 1u)) x[j] = NEG_INF;
@@ -1006,15 +1002,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       plan_role<D, R>(t, c);
     else if (warp == 1)
       mma_role<D, R>(t, c, base, tmem);
-  } else if (wg == 1) {
+  } else if (wg == 1 || (R == 1 && wg == 3)) {
     setmaxnreg_dec<C::kRegsConvert>();
-    if (R == 1)
-      convert_role1<D, false>(t, c, base + C::kOffKv);
-    else
-      convert_role2<D>(t, c, base + C::kOffKv);
-  } else if (wg == 3 && R == 1) {
-    setmaxnreg_dec<C::kRegsConvert>();
-    convert_role1<D, true>(t, c, base + C::kOffKv);
+    convert_role<D, R>(t, c, base + C::kOffKv, wg >> 1);
   } else {
     setmaxnreg_inc<C::kRegsScore>();
     score_role<D, R, MOD>(t, c, base, tmem, wg - 2);
