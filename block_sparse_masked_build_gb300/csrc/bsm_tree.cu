@@ -5,26 +5,30 @@
 // on the 5th-generation tensor core, 128 rows to a tile, one tile (R = 1) or
 // two (R = 2) per CTA, 128 tokens at a time.
 //
-// The tensor core's operands are f16, which holds every e4m3 value: codes go
-// from global memory through registers, where they are converted, into tiles
-// of shared memory; a key's scale multiplies its column of S, a value's scale
-// its tokens' rows of V.  Per 128 tokens and head dim 128 an SM reads 32 KB
-// (1400 cycles at its share of the memory's rate), converts 32768 elements, and
-// per tile of rows spends 1024 cycles on the tensor core and as many on the
+// The tensor core's operands are f16, which holds every e4m3 value: codes come
+// by bulk copies into a ring of shared memory and are converted from there into
+// f16 tiles; a key's scale multiplies its column of S, a value's scale its
+// token's row of V.  Per 128 tokens and head dim 128 an SM reads 32 KB (1400
+// cycles at its share of the memory's rate), converts 32768 elements, and per
+// tile of rows spends 1024 cycles on the tensor core and as many on the
 // exponentials: one tile is bound by memory, two by the tensor core and the
 // exponentials.
 //
-// Roles (512 threads, four warpgroups, registers shared out by setmaxnreg):
+// Roles (512 threads, four warpgroups):
 //   warp 0      deals the CTA's runs out in steps of up to 8 groups of 16
-//               tokens: looks up pages and scales, up to 8 steps ahead.
+//               tokens: looks up pages and scales, and starts the copies of
+//               the codes, up to two steps ahead of their conversion.
 //   warp 1      issues the MMAs (and owns the 512 TMEM columns).
 //   converters  warpgroup 1, and with one tile of rows warpgroup 3 as well (one
-//               takes the keys then, the other the values): the next 128
-//               tokens' codes are on their way into registers while these are
-//               converted.
+//               takes the keys then, the other the values).
 //   score       warpgroup 2 (and 3 with two tiles): one thread per query row,
 //               its TMEM lane: mask, running maximum, exponentials, P back to
 //               TMEM over S, and at a run's end the row's result.
+// The roles' loops are kept short, one copy of each and 32 columns of a row at
+// a time: together they must stay in the SM's instruction cache.  (With 128
+// columns unrolled and codes on their way in registers, a third of all
+// instruction fetches went past it: 32 sequences of 300-12000 tokens with up to
+// 16 drafts took 250 us.)
 // TMEM columns: S and P [0, 128) and [128, 256), by turns with one tile, one
 // for each of two; O [256, 256 + D), of a second tile from 384 on.
 //
@@ -67,15 +71,27 @@ struct TcDeal {
 template <int D, int R>
 struct TcCfg {
   static constexpr int kTile = kTcTokens * D * 2;  // Q, K or V in f16
-  // K and V tiles in turn: what fits beside Q, with two steps at least
-  static constexpr int kSlots = R == 1 ? 5 : 4;
+  static constexpr int kCodes = kTcTokens * D;     // K or V in e4m3
+  // Rings of tiles and of codes, by half steps h: 2 step (keys), 2 step + 1
+  // (values).  One converter fills them in turn; of two, which may be steps
+  // apart, each has its own slots, so that a slot's phases are waited for in
+  // order: two for the keys' tiles, as S goes ahead, one for the values'.
+  static constexpr int kSlots = 3, kStages = R == 1 ? 4 : 3;
+  static __device__ __forceinline__ uint32_t slot(uint32_t h) {
+    return R == 2 ? h % 3 : h % 2 ? 2 : h / 2 % 2;
+  }
+  static __device__ __forceinline__ uint32_t slot_use(uint32_t h) {
+    return R == 2 ? h / 3 : h % 2 ? h / 2 : h / 4;
+  }
+  static __device__ __forceinline__ uint32_t stage(uint32_t h) {
+    return R == 2 ? h % 3 : h % 4;
+  }
+  static __device__ __forceinline__ uint32_t stage_use(uint32_t h) {
+    return R == 2 ? h / 3 : h / 4;
+  }
   static constexpr int kOffKv = R * kTile;
-  static constexpr int kOffCtl = kOffKv + kSlots * kTile;
-  // registers per thread: warpgroup 0, converters, score
-  static constexpr uint32_t kRegsPlan = 64, kRegsConvert = R == 1 ? 120 : 96,
-                            kRegsScore = R == 1 ? 208 : 176;
-  static_assert(kRegsPlan + (3 - R) * kRegsConvert + R * kRegsScore <= 512,
-                "register file");
+  static constexpr int kOffCodes = kOffKv + kSlots * kTile;
+  static constexpr int kOffCtl = kOffCodes + kStages * kCodes;
 };
 
 // Up to 128 tokens of a run, newest step first.
@@ -91,23 +107,25 @@ struct TcStep {
   int32_t pad;
   float k_scale[kTcGroups];
   float v_mul[kTcGroups];      // scale / v_ref
-  int64_t off[kTcGroups];      // of the group's codes; -1: page out of range
+  int32_t valid[kTcGroups];    // 0: the group's page is out of range
 };
 
 struct TcCtl {
   uint64_t step_full[kTcSteps], step_empty[kTcSteps];
-  uint64_t kv_full[5], kv_empty[5];
+  uint64_t code_full[5], code_empty[5];
+  uint64_t kv_full[3], kv_empty[3];
   uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], o_free[2], mma_done;
   uint32_t tmem;
   int abort;
   TcStep steps[kTcSteps];
-  // of steps that are not plain, by step modulo 4: columns' positions, and the
+  // of steps that are not plain, by step modulo 2: columns' positions, and the
   // NaN codes of V (16 dims per entry), with the step's number + 1 where there
-  // are any.  A slot is written again four steps later, when the tensor core
-  // has long taken the P that the rows made with it.
-  int32_t pos[4][kTcTokens];
-  uint16_t nan[4][kTcTokens][8];
-  uint32_t nan_step[4];
+  // are any.  They are written with V's tile, whose slot comes free when the
+  // tensor core has taken P of the step before the last: the rows are done with
+  // that one's.
+  int32_t pos[2][kTcTokens];
+  uint16_t nan[2][kTcTokens][8];
+  uint32_t nan_step[2];
 };
 
 struct TcParams {
@@ -123,14 +141,26 @@ __device__ __forceinline__ void tc_record(int code, int a, int b, int c) {
   }
 }
 
-// Warp-wide bounded wait (see mbar_wait), alike in every lane.
+// Warp-wide bounded wait, alike in every lane: as mbar_wait, in fewer
+// instructions (the clock is looked at after every 256 tries that ran out).
 __device__ __forceinline__ bool tc_wait(const TcParams& t, TcCtl* c,
                                         uint64_t* bar, uint32_t parity,
                                         int role, int phase) {
-  const bool ok = __all_sync(
-      0xffffffffu, mbar_wait(bar, parity, &c->abort, t.timeout_ns));
-  if (!ok && threadIdx.x % 32 == 0) tc_record(1, blockIdx.x, role, phase);
-  return ok;
+  uint64_t t0 = 0;
+  bool ok;
+#pragma unroll 1
+  for (uint32_t it = 1; !(ok = mbar_try_wait(bar, parity)); ++it)
+    if ((it & 255u) == 0u) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (*static_cast<volatile int*>(&c->abort) != 0) break;
+      if (now - t0 > t.timeout_ns || it > (1u << 30)) {
+        c->abort = 1;
+        if (threadIdx.x % 32 == 0) tc_record(1, blockIdx.x, role, phase);
+        break;
+      }
+    }
+  return __all_sync(0xffffffffu, ok);
 }
 
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
@@ -153,35 +183,55 @@ __device__ __forceinline__ bool near_scale(float s, float ref) {
   return r >= 0x1p-10f && r <= 0x1p6f;
 }
 
+// 16 tokens' codes from global memory to shared memory, arriving on `bar`.
+__device__ __forceinline__ void copy_codes(uint32_t dst, const uint8_t* src,
+                                           uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // One run: groups [g0, g1) of its sequence's plan.
 template <int D, int R>
-__device__ __forceinline__ bool plan_run(const TcParams& t, TcCtl* c, int b,
+__device__ __forceinline__ bool plan_run(const TcParams& t, TcCtl* c,
+                                         uint32_t codes, int b,
                                          const PaPlan& plan, int hkv, int row0,
                                          int g0, int g1, int part,
-                                         uint32_t& step) {
+                                         uint32_t& step, uint32_t& copied) {
+  using C = TcCfg<D, R>;
   const PagedParams& p = t.p;
   const int lane = threadIdx.x % 32;
   const int* table = p.table + static_cast<int64_t>(b) * p.table_stride;
   const int base = plan.len - plan.drafts;
-  float ref = 0.f;
-  for (int top = g1; top > g0; top -= 32) {  // lane i: group top - 1 - i
+  // lane i has group top - 1 - i of the 32 in hand; the pages of the 32 behind
+  // them are looked up meanwhile
+  auto page_of = [&](int top) {
     const int g = top - 1 - lane;
+    return g >= g0 ? table[(plan.first_group + g) >> (p.page_shift - 4)] : -1;
+  };
+  int next_pid = page_of(g1);
+  float ref = 0.f;
+#pragma unroll 1
+  for (int top = g1; top > g0; top -= 32) {
+    const int g = top - 1 - lane, pid = next_pid;
     const int tok = (plan.first_group + g) * kPaGroup;
     float ks = 0.f, vs = 0.f;
     int64_t off = -1;
     if (g >= g0) {
-      const int slot = tok >> p.page_shift;
-      const int pid = table[slot];
       if (static_cast<uint32_t>(pid) < static_cast<uint32_t>(p.num_pages)) {
         const int64_t block = static_cast<int64_t>(pid) * p.H_kv + hkv;
         ks = p.k_scale[block];
         vs = p.v_scale[block];
         off = ((block << p.page_shift) + (tok & (p.page_size - 1))) * D;
       } else {
-        tc_record(2, b, slot, pid);
+        tc_record(2, b, tok >> p.page_shift, pid);
       }
     }
+    next_pid = page_of(top - 32);
     const int here = min(32, top - g0);
+#pragma unroll 1
     for (int at = 0; at < here;) {
       int n = min(kTcGroups, here - at);
       const bool mine = lane >= at && lane < at + n && off >= 0;
@@ -194,26 +244,27 @@ __device__ __forceinline__ bool plan_run(const TcParams& t, TcCtl* c, int b,
         far &= ~(1u << (__ffs(some) - 1));
       }
       if (far != 0) n = __ffs(far) - 1 - at;
+      const bool ours = lane >= at && lane < at + n;
       const uint32_t slot = step % kTcSteps;
       if (!tc_wait(t, c, &c->step_empty[slot], ((step / kTcSteps) & 1) ^ 1,
                    kRolePlan, 0))
         return false;
       TcStep& s = c->steps[slot];
-      if (lane >= at && lane < at + n) {
-        const int i = at + n - 1 - lane;  // ascending tokens
+      const int i = at + n - 1 - lane;  // ascending tokens
+      if (ours) {
         s.k_scale[i] = ks;
         s.v_mul[i] = off >= 0 && ref != 0.f ? vs / ref : 0.f;
-        s.off[i] = off;
+        s.valid[i] = off >= 0;
       }
       const int tok0 = (plan.first_group + top - at - n) * kPaGroup;
-      const unsigned there = __ballot_sync(0xffffffffu, off >= 0);
+      const unsigned there = __ballot_sync(0xffffffffu, ours && off >= 0);
       if (lane == 0) {
         s.groups = n;
         s.tok0 = tok0;
         s.first = top == g1 && at == 0;
         s.last = top - at - n == g0;
         s.plain = n == kTcGroups && tok0 + kTcTokens <= base &&
-                  tok0 >= plan.lo && (there >> at & 0xffu) == 0xffu &&
+                  tok0 >= plan.lo && __popc(there) == kTcGroups &&
                   (p.window <= 0 || plan.len - 1 - tok0 < p.window);
         s.v_ref = ref != 0.f ? ref : 1.f;
         s.b = b;
@@ -225,6 +276,23 @@ __device__ __forceinline__ bool plan_run(const TcParams& t, TcCtl* c, int b,
         s.n = plan.drafts;
       }
       warp_arrive(&c->step_full[slot]);
+      // its keys' codes, then its values'
+#pragma unroll 1
+      for (int v = 0; v < 2; ++v) {
+        const uint32_t h = 2 * step + v, st = C::stage(h);
+        if (!tc_wait(t, c, &c->code_empty[st], (C::stage_use(h) & 1) ^ 1,
+                     kRolePlan, 1))
+          return false;
+        if (lane == 0)
+          mbar_arrive_expect_tx(&c->code_full[st],
+                                __popc(there) * (kPaGroup * D));
+        __syncwarp();
+        if (ours && off >= 0)
+          copy_codes(codes + st * C::kCodes + i * (kPaGroup * D),
+                     (v ? p.v : p.k) + off, kPaGroup * D, &c->code_full[st]);
+        __syncwarp();
+        ++copied;
+      }
       ++step;
       at += n;
     }
@@ -233,8 +301,10 @@ __device__ __forceinline__ bool plan_run(const TcParams& t, TcCtl* c, int b,
 }
 
 template <int D, int R>
-__device__ __forceinline__ void plan_role(const TcParams& t, TcCtl* c) {
+__device__ __forceinline__ void plan_role(const TcParams& t, TcCtl* c,
+                                          uint32_t codes) {
   using X = TcDeal;
+  using C = TcCfg<D, R>;
   const PagedParams& p = t.p;
   const int lane = threadIdx.x % 32;
   const int rows = p.H / p.H_kv * p.T;
@@ -262,7 +332,7 @@ __device__ __forceinline__ void plan_role(const TcParams& t, TcCtl* c) {
         return u;
       },
       &start);
-  uint32_t step = 0;
+  uint32_t step = 0, copied = 0;  // half steps whose copies were started
   bool ok = true;
   while (ok && b >= 0 && u < end) {
     const PaPlan plan = plan_of<X>(p, b);
@@ -284,49 +354,43 @@ __device__ __forceinline__ void plan_role(const TcParams& t, TcCtl* c) {
       int part = -1;
       if (r0 > 0 || r1 < plan.n_units)  // slot 0: an earlier CTA has the start
         part = blockIdx.x * 2 + (r0 > 0 ? 0 : 1);
-      ok = plan_run<D, R>(t, c, b, plan, item / tiles,
+      ok = plan_run<D, R>(t, c, codes, b, plan, item / tiles,
                           item % tiles * (R * kTcRows), r0 * kTcGroups,
-                          min(r1 * kTcGroups, plan.n_groups), part, step);
+                          min(r1 * kTcGroups, plan.n_groups), part, step, copied);
     }
     u += n;
   }
-  if (!ok) return;
   const uint32_t slot = step % kTcSteps;  // the end
-  if (!tc_wait(t, c, &c->step_empty[slot], ((step / kTcSteps) & 1) ^ 1,
-               kRolePlan, 1))
-    return;
-  if (lane == 0) c->steps[slot].groups = 0;
-  warp_arrive(&c->step_full[slot]);
+  if (ok && tc_wait(t, c, &c->step_empty[slot], ((step / kTcSteps) & 1) ^ 1,
+                    kRolePlan, 2)) {
+    if (lane == 0) c->steps[slot].groups = 0;
+    warp_arrive(&c->step_full[slot]);
+    return;  // (the converters wait for every copy)
+  }
+  // given up: the copies under way still land in this CTA's shared memory; the
+  // last into a stage completes its (copies into it - 1)th phase
+  if (lane == 0)
+    for (uint32_t st = 0; st < C::kStages; ++st)
+      if (copied > st)
+        mbar_wait_drain(&c->code_full[st], ((copied - 1 - st) / C::kStages) & 1,
+                        t.timeout_ns);
+  __syncwarp();
 }
 
 // -------------------------------------------------------------- converters
 
-// The codes of one step's keys or values on their way: the thread's 16-byte
-// pieces.  A group of 16 tokens is 16 D bytes in a row: at D = 128 a piece per
-// thread of the warpgroup, at 64 one per thread of half of it.
+// Which token's row, and which 16-byte piece of it, a thread has in 16 tokens (D
+// = 128) or 32 (64).  Eight lanes that load or store together have pieces of
+// two neighbouring tokens, one half of a row from each at D = 128: loads touch
+// 128 different bytes, and the swizzle puts their two f16 halves into eight
+// different 16-byte columns.
 template <int D>
-struct TcLoad {
-  static constexpr int kPieces = D / 16;
-  uint4 x[kPieces];
-};
-
+__device__ __forceinline__ int piece_of(int i) {
+  return D == 128 ? (i & 3) | ((i ^ (i >> 1)) & 4) : i & 3;
+}
 template <int D>
-__device__ __forceinline__ void load_codes(const TcStep& s,
-                                           const uint8_t* pages,
-                                           TcLoad<D>& l) {
-  const int i = threadIdx.x % 128;
-#pragma unroll
-  for (int k = 0; k < TcLoad<D>::kPieces; ++k) {
-    const int g = D == 128 ? k : 2 * k + i / 64;
-    const int at = D == 128 ? i : i % 64;
-    l.x[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (g < s.groups) {
-      const int64_t off = s.off[g];
-      if (off >= 0)
-        l.x[k] = __ldcs(
-            reinterpret_cast<const uint4*>(pages + off + at * 16));
-    }
-  }
+__device__ __forceinline__ int token_of(int i) {
+  return D == 128 ? (i >> 2 & 1) | (i >> 4 << 1) : i >> 2;
 }
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -335,81 +399,34 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// What a step that is not plain needs before its codes are converted: tokens
-// that are no sequence's become zeros, and so do NaN codes of values, which are
-// noted, as a row that does not see them must not meet 0 * NaN; and the
-// positions of its columns.
-template <int D>
-__device__ __forceinline__ void clean_codes(const PagedParams& p, TcCtl* c,
-                                            const TcStep& s, uint32_t step,
-                                            bool values, TcLoad<D>& l) {
-  constexpr int kPer = D / 16, kRows = 128 / kPer;
-  const int i = threadIdx.x % 128;
-  const int piece = i % kPer, row = i / kPer;
-#pragma unroll
-  for (int k = 0; k < TcLoad<D>::kPieces; ++k) {
-    const int tr = row + k * kRows, tok = s.tok0 + tr;
-    if (tok < s.lo || tok >= s.len) l.x[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (values) {
-      uint32_t* w = reinterpret_cast<uint32_t*>(&l.x[k]);
-      uint32_t found = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t n = nan_codes(w[j]) >> 7;  // one bit per byte
-        w[j] &= ~(n * 0xffu);
-        // the four bits 0, 8, 16, 24 next to each other
-        found |= ((n * 0x00204081u >> 21) & 0xfu) << (4 * j);
-      }
-      c->nan[step % 4][tr][piece] = static_cast<uint16_t>(found);
-      if (found != 0) c->nan_step[step % 4] = step + 1;
-    }
-  }
-  if (values && (p.window > 0 || (p.mod.kind & kModBias))) {
-    const int tok = s.tok0 + i, base = s.len - s.n;
-    c->pos[step % 4][i] = tok >= base && tok < s.len
-                              ? base + draft_depth(p, s.b, tok - base, s.n)
-                              : tok;
-  }
-}
-
-template <int OFF>
-__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y,
-                                       uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.b32 [%0+%5], {%1, %2, %3, %4};" ::"r"(a), "r"(x),
-               "r"(y), "r"(z), "r"(w), "n"(OFF)
-               : "memory");
-}
-
-// Piece K of a thread and the ones behind it into the f16 tile (see
-// convert_role); a, b: where the two halves of piece 0 go.
-template <int D, int K>
-__device__ __forceinline__ void store_codes(const TcStep& s, bool values,
-                                            bool flip, uint32_t a, uint32_t b,
-                                            const TcLoad<D>& l) {
-  constexpr int kRows = 2048 / D;
-  const uint32_t w[4] = {l.x[K].x, l.x[K].y, l.x[K].z, l.x[K].w};
-  uint32_t h[8];
+// What a step that is not plain needs before 16 codes of token tr are
+// converted: tokens that are no sequence's become zeros, and so do NaN codes of
+// values, which are noted, as a row that does not see them must not meet 0 *
+// NaN.
+__device__ __forceinline__ void clean_codes(TcCtl* c, const TcStep& s,
+                                            uint32_t step, bool values, int tr,
+                                            int piece, uint32_t* w) {
+  const int tok = s.tok0 + tr;
+  const bool there = tok >= s.lo && tok < s.len && s.valid[tr / kPaGroup] != 0;
+  uint32_t found = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    h[2 * j] = e4m3x2_to_f16x2(w[j]);
-    h[2 * j + 1] = e4m3x2_to_f16x2_hi(w[j]);
+    if (!there) w[j] = 0u;
+    const uint32_t n = nan_codes(w[j]) >> 7;  // one bit per byte
+    if (values) w[j] &= ~(n * 0xffu);
+    // the four bits 0, 8, 16, 24 next to each other
+    found |= ((n * 0x00204081u >> 21) & 0xfu) << (4 * j);
   }
-  if (values) {
-    const int g = D == 128 ? K : 2 * K + threadIdx.x % 128 / 64;
-    const float m = s.v_mul[g];
-    if (m != 1.f) {
-      const uint32_t mm = pack_f16x2(m, m);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] = hmul2(h[j], mm);
-    }
-  }
-  constexpr int off = K * kRows * 128;
-  sts128<off>(a, flip ? h[4] : h[0], flip ? h[5] : h[1], flip ? h[6] : h[2],
-              flip ? h[7] : h[3]);
-  sts128<off>(b, flip ? h[0] : h[4], flip ? h[1] : h[5], flip ? h[2] : h[6],
-              flip ? h[3] : h[7]);
-  if constexpr (K + 1 < TcLoad<D>::kPieces)
-    store_codes<D, K + 1>(s, values, flip, a, b, l);
+  if (!values) return;
+  c->nan[step % 2][tr][piece] = static_cast<uint16_t>(found);
+  if (found != 0) c->nan_step[step % 2] = step + 1;
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y,
+                                       uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x),
+               "r"(y), "r"(z), "r"(w)
+               : "memory");
 }
 
 __device__ __forceinline__ bool wait_step(const TcParams& t, TcCtl* c,
@@ -419,63 +436,84 @@ __device__ __forceinline__ bool wait_step(const TcParams& t, TcCtl* c,
 }
 
 // A converter warpgroup: with one tile of rows the keys (which = 0) or the
-// values (1) of every step, with two tiles both in turn.  The codes of the half
-// step after the one in hand are on their way meanwhile.  (One copy of the code
-// for keys and values, as the roles together must fit the SM's instruction
-// cache: with a copy for each, unrolled by two, and the MMAs unrolled, the
-// kernel waited for instructions, 373 us on 32 sequences of 300-12000 tokens
-// and 16 drafts.)
-//
-// Tiles are rows of 64 elements (128 bytes) per token, two such blocks at D =
-// 128, in the 128-byte swizzle.  Lanes of the upper block store their second
-// half first: eight lanes then touch eight different 16-byte columns.
+// values (1) of every step, with two tiles both in turn.  Tiles are rows of 64
+// elements (128 bytes) per token, two such blocks at D = 128, in the 128-byte
+// swizzle.
 template <int D, int R>
 __device__ __forceinline__ void convert_role(const TcParams& t, TcCtl* c,
-                                             uint32_t kv, int which) {
+                                             uint32_t kv, uint32_t codes,
+                                             int which) {
   using C = TcCfg<D, R>;
-  constexpr int kPer = D / 16;
-  const int i = threadIdx.x % 128, piece = i % kPer;
-  const uint32_t row = i / kPer;
-  const bool flip = D == 128 && piece >= 4;
-  const uint32_t line =
-      kv + (D == 128 ? (piece >> 2) * (kTcTokens * 128) : 0) + row * 128;
-  const uint32_t chunk = ((2 * piece) & 7) | (flip ? 1u : 0u);
+  const PagedParams& p = t.p;
+  const int i = threadIdx.x % 128, piece = piece_of<D>(i);
+  const uint32_t row = token_of<D>(i), chunk = (2 * piece) & 7;
+  const uint32_t line = kv + (piece >> 2) * (kTcTokens * 128) + row * 128;
   const uint32_t at_a = line + ((chunk ^ (row & 7)) << 4);
   const uint32_t at_b = line + ((chunk ^ 1u ^ (row & 7)) << 4);
-  bool values = which != 0;
-  TcLoad<D> now, next;
-  if (!wait_step(t, c, 0, kRoleConvert) || c->steps[0].groups == 0) return;
-  load_codes<D>(c->steps[0], values ? t.p.v : t.p.k, now);
+  const uint32_t from = codes + row * D + piece * 16;
+  constexpr int kRows = 2048 / D;  // tokens of the warpgroup at a time
 #pragma unroll 1
-  for (uint32_t step = 0;;) {
-    // the half step behind this one
-    uint32_t step2 = step;
-    bool values2 = values, more = true;
-    if (R == 2) values2 = !values;
-    if (R == 1 || values) {
-      ++step2;
-      if (!wait_step(t, c, step2, kRoleConvert)) return;
-      more = c->steps[step2 % kTcSteps].groups != 0;
-    }
-    if (more)
-      load_codes<D>(c->steps[step2 % kTcSteps], values2 ? t.p.v : t.p.k, next);
+  for (uint32_t h = which;; h += R == 1 ? 2 : 1) {
+    const uint32_t step = h / 2;
+    const bool values = h % 2 != 0;
+    if (!wait_step(t, c, step, kRoleConvert)) return;
     const TcStep& s = c->steps[step % kTcSteps];
-    const uint32_t h = 2 * step + (values ? 1 : 0);
-    const uint32_t slot = h % C::kSlots;
-    if (!tc_wait(t, c, &c->kv_empty[slot], ((h / C::kSlots) & 1) ^ 1,
-                 kRoleConvert, values))
+    const int tokens = s.groups * kPaGroup;
+    if (tokens == 0) return;
+    const uint32_t st = C::stage(h), slot = C::slot(h);
+    if (!tc_wait(t, c, &c->code_full[st], C::stage_use(h) & 1, kRoleConvert,
+                 0) ||
+        !tc_wait(t, c, &c->kv_empty[slot], (C::slot_use(h) & 1) ^ 1,
+                 kRoleConvert, 1))
       return;
-    if (__builtin_expect(!s.plain, 0))
-      clean_codes<D>(t.p, c, s, step, values, now);
-    store_codes<D, 0>(s, values, flip, at_a + slot * C::kTile,
-                      at_b + slot * C::kTile, now);
+    const bool plain = s.plain != 0;
+    uint32_t src = from + st * C::kCodes;
+    uint32_t dst_a = at_a + slot * C::kTile, dst_b = at_b + slot * C::kTile;
+#pragma unroll 2
+    for (int t0 = 0; t0 < tokens; t0 += kRows) {
+      // (at D = 64 half of the warpgroup may be past the last group)
+      if (D == 128 || t0 + static_cast<int>(row) < tokens) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(src)
+                     : "memory");
+        if (__builtin_expect(!plain, 0))
+          clean_codes(c, s, step, values, t0 + row, piece, w);
+        uint32_t x[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[2 * j] = e4m3x2_to_f16x2(w[j]);
+          x[2 * j + 1] = e4m3x2_to_f16x2_hi(w[j]);
+        }
+        if (values) {
+          const float m = s.v_mul[(t0 + row) / kPaGroup];
+          if (m != 1.f) {
+            const uint32_t mm = pack_f16x2(m, m);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = hmul2(x[j], mm);
+          }
+        }
+        sts128(dst_a, x[0], x[1], x[2], x[3]);
+        sts128(dst_b, x[4], x[5], x[6], x[7]);
+      }
+      src += 2048;
+      dst_a += kRows * 128;
+      dst_b += kRows * 128;
+    }
+    if (!plain && values && (p.window > 0 || (p.mod.kind & kModBias))) {
+      const int tok = s.tok0 + i, base = s.len - s.n;
+      c->pos[step % 2][i] = tok >= base && tok < s.len
+                                ? base + draft_depth(p, s.b, tok - base, s.n)
+                                : tok;
+    }
     fence_proxy_async();
-    warp_arrive(&c->kv_full[slot]);
-    if (R == 1 || values) warp_arrive(&c->step_empty[step % kTcSteps]);
-    if (!more) return;
-    now = next;
-    step = step2;
-    values = values2;
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) {
+      mbar_arrive(&c->code_empty[st]);
+      mbar_arrive(&c->kv_full[slot]);
+      if (R == 1 || values) mbar_arrive(&c->step_empty[step % kTcSteps]);
+    }
   }
 }
 
@@ -504,8 +542,8 @@ __device__ __forceinline__ void mma_role(const TcParams& t, TcCtl* c,
   auto buf = [](uint32_t step, int r) { return R == 2 ? r : int(step & 1); };
   auto use = [](uint32_t step) { return R == 2 ? step : step >> 1; };
   auto wait_kv = [&](uint32_t h) {
-    return tc_wait(t, c, &c->kv_full[h % C::kSlots], (h / C::kSlots) & 1,
-                   kRoleMma, 2);
+    return tc_wait(t, c, &c->kv_full[C::slot(h)], C::slot_use(h) & 1, kRoleMma,
+                   2);
   };
 #pragma unroll 1
   for (uint32_t step = 0; ok; ++step) {
@@ -535,17 +573,17 @@ __device__ __forceinline__ void mma_role(const TcParams& t, TcCtl* c,
         if (!ok) break;
         tc_fence_after();
         const uint64_t a = dq + r * kUnits;
-        const uint64_t b = dk + (2 * step) % C::kSlots * kUnits;
+        const uint64_t b = dk + C::slot(2 * step) * kUnits;
         const uint32_t idesc = idesc_f16(groups * kPaGroup, false);
         const uint32_t d = tmem + buf(step, r) * 128;
-#pragma unroll 2
+#pragma unroll 1
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k >> 2) * (kTcTokens * 128 / 16) + (k & 3) * 2;
           mma_ss_elect(d, a + off, b + off, idesc, k > 0);
         }
         mma_commit_elect(&c->s_full[buf(step, r)]);
         if (r == R - 1)
-          mma_commit_elect(&c->kv_empty[(2 * step) % C::kSlots]);
+          mma_commit_elect(&c->kv_empty[C::slot(2 * step)]);
       } else {  // O_r (+)= P_r V of the step before
         if (step == 0) continue;
         const uint32_t before = step - 1, h = 2 * before + 1;
@@ -558,15 +596,15 @@ __device__ __forceinline__ void mma_role(const TcParams& t, TcCtl* c,
           ok = tc_wait(t, c, &c->o_free[r], runs & 1, kRoleMma, 4);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t b = dv + h % C::kSlots * kUnits;
+        const uint64_t b = dv + C::slot(h) * kUnits;
         constexpr uint32_t idesc = idesc_f16(D, true);
-#pragma unroll 2
+#pragma unroll 1
         for (int k = 0; k < groups_before; ++k)
           mma_ts_elect(tmem + 256 + r * 128, tmem + bf * 128 + k * 8,
                        b + k * (kPaGroup * 128 / 16), idesc,
                        k > 0 || !first_before);
         mma_commit_elect(&c->pv_done[r]);
-        if (r == R - 1) mma_commit_elect(&c->kv_empty[h % C::kSlots]);
+        if (r == R - 1) mma_commit_elect(&c->kv_empty[C::slot(h)]);
       }
     }
     if (!more) break;
@@ -634,7 +672,7 @@ __device__ __forceinline__ uint32_t visible(const PagedParams& p,
   if (lo > 0) keep = lo >= 32 ? 0u : keep & (~0u << lo);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    if (2 * word + i < s.groups && s.off[2 * word + i] < 0)
+    if (2 * word + i < s.groups && s.valid[2 * word + i] == 0)
       keep &= ~(0xffffu << (16 * i));
   const int d0 = t0 - base;  // draft of the word's first column
   if (d0 > -32) {
@@ -652,26 +690,27 @@ __device__ __forceinline__ uint32_t visible(const PagedParams& p,
   return keep;
 }
 
-// cap * tanh(x / cap) of a row's scores S = q.k, in log2 units: polynomials
-// where the warp's scores allow them (|y| <= 0.5, <= 1.2), else exponentials.
+// cap * tanh(x / cap) of 32 of a row's scores S = q.k, in log2 units:
+// polynomials where the warp's scores allow them (|y| <= 0.5, <= 1.2), else
+// exponentials.
 __device__ __forceinline__ void cap_scores(const ScoreMod& m, float* s) {
   float a0 = 0.f, a1 = 0.f;
 #pragma unroll
-  for (int c = 0; c < kTcTokens; c += 4) {
+  for (int c = 0; c < 32; c += 4) {
     a0 = fmax3_abs_nan(a0, s[c], s[c + 1]);
     a1 = fmax3_abs_nan(a1, s[c + 2], s[c + 3]);
   }
   const float top = fmax3_abs_nan(a0, a1, a1);
   if (__all_sync(0xffffffffu, top <= m.poly_max)) {
 #pragma unroll
-    for (int c = 0; c < kTcTokens; c += 2) {
+    for (int c = 0; c < 32; c += 2) {
       float h0, h1;
       poly_sq2<4>(h0, h1, s[c], s[c + 1], m.poly);
       fmul2v(s[c], s[c + 1], s[c], s[c + 1], h0, h1);
     }
   } else if (__all_sync(0xffffffffu, top <= m.wide_max)) {
 #pragma unroll
-    for (int c = 0; c < kTcTokens; c += 2) {
+    for (int c = 0; c < 32; c += 2) {
       float h0, h1;
       poly_sq2<7>(h0, h1, s[c], s[c + 1], m.wide);
       fmul2v(s[c], s[c + 1], s[c], s[c + 1], h0, h1);
@@ -680,7 +719,7 @@ __device__ __forceinline__ void cap_scores(const ScoreMod& m, float* s) {
     // tanh(y) = 1 - 2 / (1 + e^(2 y)), off by 2^-23 of the cap
     const float k2 = -2.f * m.cap_log2;
 #pragma unroll
-    for (int c = 0; c < kTcTokens; ++c) {
+    for (int c = 0; c < 32; ++c) {
       const float y = s[c] * m.cap_e;
       float z = fmaf(k2, rcp_approx(ex2_approx(y) + 1.f), m.cap_log2);
       if (m.cap_log2 > 300.f) {  // where that would show in the logits
@@ -694,6 +733,39 @@ __device__ __forceinline__ void cap_scores(const ScoreMod& m, float* s) {
       s[c] = z;
     }
   }
+}
+
+// The largest of 32 columns, the first 16 times f0, the others times f1.
+__device__ __forceinline__ float max_of(const float* x, float f0, float f1) {
+  float m[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float* v = x + 16 * i;
+    const float a = fmax3(v[0], v[1], v[2]), b = fmax3(v[3], v[4], v[5]);
+    const float d = fmax3(v[6], v[7], v[8]), e = fmax3(v[9], v[10], v[11]);
+    m[i] = fmax3(fmax3(a, b, d), fmax3(e, v[12], v[13]), fmaxf(v[14], v[15]));
+  }
+  return fmaxf(m[0] * f0, m[1] * f1);
+}
+
+// P of 32 columns: 2^(x f + add), into P's columns at `to`, and their sums.
+__device__ __forceinline__ void weigh(const float* x, float f0, float f1,
+                                      float add, float* l, uint32_t to) {
+  uint32_t pk[16];
+#pragma unroll
+  for (int j = 0; j < 32; j += 4) {
+    const float f = j < 16 ? f0 : f1;
+    float x0, x1, x2, x3;
+    ffma2(x0, x1, x[j], x[j + 1], f, add);
+    ffma2(x2, x3, x[j + 2], x[j + 3], f, add);
+    const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+    const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
+    fadd2(l[0], l[1], l[0], l[1], p0, p1);
+    fadd2(l[2], l[3], l[2], l[3], p2, p3);
+    pk[j / 2] = pack_f16x2(p0, p1);
+    pk[j / 2 + 1] = pack_f16x2(p2, p3);
+  }
+  tmem_st16(to, pk);
 }
 
 template <int D, int R, bool MOD>
@@ -712,13 +784,13 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
   const bool capped = MOD && (p.mod.kind & kModCap);
   const bool biased = MOD && (p.mod.kind & kModBias);
   const bool negate = !capped && p.scale_x < 0.f;
-  uint32_t pv = 0;  // P tiles given to the tensor core
   // of the run
   float q_mul = 0.f, slope2 = 0.f, m_used = NEG_INF, l_sum = 0.f, ref = 1.f;
   int row = 0, tq = 0, pos = -1;
   uint32_t nans[D / 32];
   uint32_t run_pv = 0;
-  for (uint32_t step = 0;; ++step) {
+#pragma unroll 1
+  for (uint32_t step = 0;; ++step) {  // (pv_done's phases are the steps)
     if (!wait_step(tp, c, step, kRoleScore)) return;
     const TcStep& s = c->steps[step % kTcSteps];
     if (s.groups == 0) return;
@@ -749,89 +821,89 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
     const int buf = R == 2 ? t : static_cast<int>(step & 1);
     const uint32_t use = R == 2 ? step : step >> 1;
     const uint32_t s_addr = tmem + lane_off + buf * 128;
-    uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-    if (__builtin_expect(!s.plain, 0)) {
-      // positions and NaN codes come with the values
+    const bool plain = s.plain != 0;
+    if (!plain) {  // positions and NaN codes come with the values
       const uint32_t h = 2 * step + 1;
-      if (!tc_wait(tp, c, &c->kv_full[h % C::kSlots], (h / C::kSlots) & 1,
+      if (!tc_wait(tp, c, &c->kv_full[C::slot(h)], C::slot_use(h) & 1,
                    kRoleScore, 5))
         return;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        keep[w] = pos >= 0 ? visible(p, s, w, tq) : 0u;
-        if (p.window > 0)
-#pragma unroll 4
-          for (int j = 0; j < 32; ++j)
-            if (pos - c->pos[step % 4][32 * w + j] >= p.window)
-              keep[w] &= ~(1u << j);
-      }
-      if (c->nan_step[step % 4] == step + 1) {
-        // values that are NaN: a row that sees one has NaN in that place
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          for (uint32_t k = keep[w]; k != 0; k &= k - 1) {
-            const uint16_t* n = c->nan[step % 4][32 * w + __ffs(k) - 1];
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-              nans[i] |= *reinterpret_cast<const uint32_t*>(n + 2 * i);
-          }
-      }
     }
-    float f[kTcGroups];
-#pragma unroll
-    for (int g = 0; g < kTcGroups; ++g) f[g] = q_mul * s.k_scale[g];
     if (!tc_wait(tp, c, &c->s_full[buf], use & 1, kRoleScore, 1)) return;
     tc_fence_after();
-    uint32_t raw[kTcTokens];
-#pragma unroll
-    for (int q = 0; q < kTcTokens / 32; ++q)
-      tmem_ld32(s_addr + q * 32, raw + q * 32);
-    tmem_ld_wait();
-    float* x = reinterpret_cast<float*>(raw);
-    if (MOD || !s.plain) {
-#pragma unroll
-      for (int j = 0; j < kTcTokens; j += 2)
-        fmul2(x[j], x[j + 1], x[j], x[j + 1], f[j / kPaGroup]);
-#pragma unroll
-      for (int g = 0; g < kTcGroups; ++g) f[g] = 1.f;
-    }
-    if (MOD) {
-      // columns that are not seen may hold anything; 0 costs the cap nothing
-      if (!s.plain)
-#pragma unroll
-        for (int j = 0; j < kTcTokens; ++j)
-          if (!(keep[j / 32] >> (j % 32) & 1u)) x[j] = 0.f;
-      if (capped) cap_scores(p.mod, x);
-      if (biased) {
-        if (s.plain) {
-          const float d0 = static_cast<float>(s.tok0 - pos);
-#pragma unroll
-          for (int j = 0; j < kTcTokens; ++j)
-            x[j] = fmaf(slope2, d0 + static_cast<float>(j), x[j]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < kTcTokens; ++j)
-            x[j] = fmaf(-slope2,
-                        fabsf(static_cast<float>(pos - c->pos[step % 4][j])),
-                        x[j]);
-        }
-      }
-    }
-    if (__builtin_expect(!s.plain, 0)) {
-#pragma unroll
-      for (int j = 0; j < kTcTokens; ++j)
-        if (!(keep[j / 32] >> (j % 32) & 1u)) x[j] = NEG_INF;
-    }
-    // the running maximum
+    // ---- the largest score.  Scores that the scales alone do not give are
+    // written back as they are to be weighed.
     float top = NEG_INF;
+    if (!MOD && plain) {
 #pragma unroll
-    for (int g = 0; g < kTcGroups; ++g) {
-      const float* v = x + g * kPaGroup;
-      const float a = fmax3(v[0], v[1], v[2]), b = fmax3(v[3], v[4], v[5]);
-      const float d = fmax3(v[6], v[7], v[8]), e = fmax3(v[9], v[10], v[11]);
-      const float m = fmax3(fmax3(a, b, d), fmax3(e, v[12], v[13]),
-                            fmaxf(v[14], v[15]));
-      top = fmaxf(top, m * f[g]);
+      for (int h = 0; h < 2; ++h) {
+        float x[64];
+        tmem_ld32(s_addr + h * 64, reinterpret_cast<uint32_t*>(x));
+        tmem_ld32(s_addr + h * 64 + 32, reinterpret_cast<uint32_t*>(x + 32));
+        tmem_ld_wait();
+        const float a = max_of(x, s.k_scale[4 * h], s.k_scale[4 * h + 1]);
+        const float b =
+            max_of(x + 32, s.k_scale[4 * h + 2], s.k_scale[4 * h + 3]);
+        top = fmax3(top, a * q_mul, b * q_mul);
+      }
+    } else {
+#pragma unroll 1
+      for (int q = 0; q < kTcTokens / 32; ++q) {
+        uint32_t keep = ~0u;
+        if (!plain) {
+          keep = pos >= 0 ? visible(p, s, q, tq) : 0u;
+          const int* at = c->pos[step % 2] + 32 * q;
+          if (p.window > 0)
+#pragma unroll 1
+            for (int j = 0; j < 32; ++j)
+              if (pos - at[j] >= p.window) keep &= ~(1u << j);
+          if (c->nan_step[step % 2] == step + 1) {
+            // values that are NaN: a row that sees one has NaN in that place
+#pragma unroll 1
+            for (uint32_t k = keep; k != 0; k &= k - 1) {
+              const uint16_t* n = c->nan[step % 2][32 * q + __ffs(k) - 1];
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i)
+                nans[i] |= *reinterpret_cast<const uint32_t*>(n + 2 * i);
+            }
+          }
+        }
+        float x[32];
+        tmem_ld32(s_addr + q * 32, reinterpret_cast<uint32_t*>(x));
+        tmem_ld_wait();
+        const float f0 = q_mul * s.k_scale[2 * q];
+        const float f1 = q_mul * s.k_scale[2 * q + 1];
+#pragma unroll
+        for (int j = 0; j < 32; j += 2)
+          fmul2(x[j], x[j + 1], x[j], x[j + 1], j < 16 ? f0 : f1);
+        if (MOD) {
+          // columns that are not seen may hold anything; 0 costs the cap
+          // nothing
+          if (!plain)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!(keep >> j & 1u)) x[j] = 0.f;
+          if (capped) cap_scores(p.mod, x);
+          if (biased && plain) {
+            const float d0 = static_cast<float>(s.tok0 + 32 * q - pos);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              x[j] = fmaf(slope2, d0 + static_cast<float>(j), x[j]);
+          } else if (biased) {
+            const int* at = c->pos[step % 2] + 32 * q;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              x[j] = fmaf(-slope2, fabsf(static_cast<float>(pos - at[j])),
+                          x[j]);
+          }
+        }
+        if (!plain)
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (!(keep >> j & 1u)) x[j] = NEG_INF;
+        top = fmaxf(top, max_of(x, 1.f, 1.f));
+        tmem_st32(s_addr + q * 32, reinterpret_cast<uint32_t*>(x));
+      }
+      tmem_st_wait();
     }
     float scale_o = 1.f;
     if (top > m_used + kTcRescaleLog2) {
@@ -844,29 +916,29 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
       scale_o *= ref / s.v_ref;
       ref = s.v_ref;
     }
-    // 2^9 goes along with P and the sums
+    // ---- P; 2^9 goes along with it and the sums.  The next 32 columns are on
+    // their way while 32 are weighed (P's columns lie before theirs)
     const float add = m_used == NEG_INF ? kTcUpLog2 : kTcUpLog2 - m_used;
-    float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-#pragma unroll
-    for (int q = 0; q < kTcTokens / 32; ++q) {
-      uint32_t pk[16];
-#pragma unroll
-      for (int j = 32 * q; j < 32 * q + 32; j += 4) {
-        float x0, x1, x2, x3;
-        ffma2(x0, x1, x[j], x[j + 1], f[j / kPaGroup], add);
-        ffma2(x2, x3, x[j + 2], x[j + 3], f[j / kPaGroup], add);
-        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-        const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
-        fadd2(l0, l1, l0, l1, p0, p1);
-        fadd2(l2, l3, l2, l3, p2, p3);
-        pk[(j & 31) / 2] = pack_f16x2(p0, p1);
-        pk[(j & 31) / 2 + 1] = pack_f16x2(p2, p3);
+    const float fq = MOD || !plain ? 1.f : q_mul;
+    float l[4] = {0.f, 0.f, 0.f, 0.f};
+    {
+      float xa[32], xb[32];
+      auto scale = [&](int g) { return MOD || !plain ? 1.f : s.k_scale[g] * fq; };
+      tmem_ld32(s_addr, reinterpret_cast<uint32_t*>(xa));
+#pragma unroll 1
+      for (int q = 0; q < 4; q += 2) {
+        tmem_ld_wait();
+        tmem_ld32(s_addr + q * 32 + 32, reinterpret_cast<uint32_t*>(xb));
+        weigh(xa, scale(2 * q), scale(2 * q + 1), add, l, s_addr + q * 16);
+        tmem_ld_wait();
+        if (q == 0) tmem_ld32(s_addr + 64, reinterpret_cast<uint32_t*>(xa));
+        weigh(xb, scale(2 * q + 2), scale(2 * q + 3), add, l,
+              s_addr + q * 16 + 16);
       }
-      tmem_st16(s_addr + q * 16, pk);
     }
-    l_sum += (l0 + l1) + (l2 + l3);
+    l_sum += (l[0] + l[1]) + (l[2] + l[3]);
     if (__any_sync(0xffffffffu, scale_o != 1.f) && run_pv > 0) {
-      if (!tc_wait(tp, c, &c->pv_done[t], (pv - 1) & 1, kRoleScore, 2)) return;
+      if (!tc_wait(tp, c, &c->pv_done[t], (step - 1) & 1, kRoleScore, 2)) return;
       tc_fence_after();
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
@@ -882,14 +954,13 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
     tmem_st_wait();
     tc_fence_before();
     mbar_arrive(&c->p_full[buf]);
-    ++pv;
     ++run_pv;
     if (!s.last) {
       warp_arrive(&c->step_empty[step % kTcSteps]);
       continue;
     }
     // ---- the row's result, or its part of it
-    if (!tc_wait(tp, c, &c->pv_done[t], (pv - 1) & 1, kRoleScore, 3)) return;
+    if (!tc_wait(tp, c, &c->pv_done[t], step & 1, kRoleScore, 3)) return;
     tc_fence_after();
     const int b = s.b, head = s.hkv * G + (row < rows ? row : 0) / p.T;
     const bool there = pos >= 0;  // else an empty row, whatever it gathered
@@ -958,9 +1029,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     paged_tree_kernel(const __grid_constant__ TcParams t) {
   using C = TcCfg<D, R>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-      ~static_cast<uintptr_t>(1023));
+  // (by an offset, so that the compiler knows it for shared memory)
+  uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
   TcCtl* c = reinterpret_cast<TcCtl*>(smem + C::kOffCtl);
   const int warp = threadIdx.x / 32, wg = threadIdx.x / 128;
   // the join kernel may be scheduled once every CTA here runs; it waits for
@@ -971,6 +1041,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int i = 0; i < kTcSteps; ++i) {
       mbar_init(&c->step_full[i], 1);
       mbar_init(&c->step_empty[i], kConvertWarps + 1 + kScoreWarps);
+    }
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&c->code_full[i], 1);
+      mbar_init(&c->code_empty[i], 4);
     }
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&c->kv_full[i], 4);
@@ -985,7 +1059,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     mbar_init(&c->mma_done, 1);
     c->abort = 0;
-    for (int i = 0; i < 4; ++i) c->nan_step[i] = 0;
+    c->nan_step[0] = c->nan_step[1] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -997,16 +1071,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_after();
   const uint32_t tmem = c->tmem, base = smem_u32(smem);
   if (wg == 0) {
-    setmaxnreg_dec<C::kRegsPlan>();
     if (warp == 0)
-      plan_role<D, R>(t, c);
+      plan_role<D, R>(t, c, base + C::kOffCodes);
     else if (warp == 1)
       mma_role<D, R>(t, c, base, tmem);
   } else if (wg == 1 || (R == 1 && wg == 3)) {
-    setmaxnreg_dec<C::kRegsConvert>();
-    convert_role<D, R>(t, c, base + C::kOffKv, wg >> 1);
+    convert_role<D, R>(t, c, base + C::kOffKv, base + C::kOffCodes, wg >> 1);
   } else {
-    setmaxnreg_inc<C::kRegsScore>();
     score_role<D, R, MOD>(t, c, base, tmem, wg - 2);
   }
   tc_fence_before();
@@ -1021,13 +1092,7 @@ cudaError_t launch_tc(const TcParams& t, int num_sms, cudaStream_t stream) {
   auto kern = paged_tree_kernel<D, R, MOD>;
   constexpr int smem = C::kOffCtl + static_cast<int>(sizeof(TcCtl)) + 1024;
   static_assert(smem <= 232448, "shared memory budget");
-  // the registers that the roles take sum up to those of the launch
-  cudaFuncAttributes a;
-  cudaError_t e = cudaFuncGetAttributes(&a, kern);
-  if (e != cudaSuccess) return e;
-  if (a.numRegs * 4 < static_cast<int>(C::kRegsPlan + (3 - R) * C::kRegsConvert +
-                                       R * C::kRegsScore))
-    return cudaErrorLaunchOutOfResources;
+  cudaError_t e;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            smem);
   if (e != cudaSuccess) return e;
