@@ -7,8 +7,8 @@
 //
 // The tensor core's operands are f16, which holds every e4m3 value: codes come
 // by bulk copies into a ring of shared memory and are converted from there into
-// f16 tiles; a key's scale multiplies its column of S, a value's scale its
-// token's row of V.  Per 128 tokens and head dim 128 an SM reads 32 KB (1400
+// f16 tiles; a key's scale multiplies its column of S, a value's scale that of
+// P.  Per 128 tokens and head dim 128 an SM reads 32 KB (1400
 // cycles at its share of the memory's rate), converts 32768 elements, and per
 // tile of rows spends 1024 cycles on the tensor core and as many on the
 // exponentials: one tile is bound by memory, two by the tensor core and the
@@ -57,9 +57,9 @@ constexpr uint32_t kTcTmem = 512;
 constexpr int kTreeFewRows = 16;  // see tree_tiles
 constexpr int kRolePlan = 1, kRoleMma = 2, kRoleConvert = 3, kRoleScore = 4;
 // P is scaled by 2^9 before it becomes f16, whose smallest number is 2^-24: a
-// key's weight is lost below 2^-34 of the largest (as in the attention of
-// single tokens).  The reference m may lie up to 2^6 below the running maximum
-// before O is rescaled; 2^15 still fits f16.
+// key's weight is lost below 2^-33 of the largest, with the least of the values'
+// scales (2^-6) below 2^-27.  The reference m may lie up to 2^6 below the running
+// maximum before O is rescaled; 2^15 still fits f16.
 constexpr float kTcUpLog2 = 9.f, kTcRescaleLog2 = 6.f;
 
 // The deal: a unit is a full step.
@@ -100,13 +100,14 @@ struct TcStep {
   int32_t tok0;
   int32_t first, last;  // of its run
   int32_t plain;     // 8 groups, and every row sees every token
-  float v_ref;       // V's tile, and so O, is in units of this scale
+  float v_ref;       // O is in units of this scale
   // of the run
   int32_t b, hkv, row0, part;  // part: -1 whole, else its slot in the workspace
   int32_t len, lo, n;          // tokens, first visible one, drafts
   int32_t pad;
   float k_scale[kTcGroups];
-  float v_mul[kTcGroups];      // scale / v_ref
+  float v_log2[kTcGroups];     // log2(scale / v_ref)
+  float v_inv[kTcGroups];      // v_ref / scale
   int32_t valid[kTcGroups];    // 0: the group's page is out of range
 };
 
@@ -141,26 +142,43 @@ __device__ __forceinline__ void tc_record(int code, int a, int b, int c) {
   }
 }
 
-// Warp-wide bounded wait, alike in every lane: as mbar_wait, in fewer
-// instructions (the clock is looked at after every 256 tries that ran out).
-__device__ __forceinline__ bool tc_wait(const TcParams& t, TcCtl* c,
-                                        uint64_t* bar, uint32_t parity,
-                                        int role, int phase) {
+// Bounded wait of a whole warp, alike in every lane: as mbar_wait, with the
+// clock looked at after every 256 tries that ran out.  One copy, called, as it
+// stands in every role's loop.
+__device__ __noinline__ bool tc_wait_at(uint32_t bar, uint32_t parity,
+                                        volatile int* abort, uint64_t limit,
+                                        int where) {
   uint64_t t0 = 0;
-  bool ok;
+  uint32_t ok;
 #pragma unroll 1
-  for (uint32_t it = 1; !(ok = mbar_try_wait(bar, parity)); ++it)
+  for (uint32_t it = 1;; ++it) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) break;
     if ((it & 255u) == 0u) {
       const uint64_t now = globaltimer_ns();
       if (t0 == 0) t0 = now;
-      if (*static_cast<volatile int*>(&c->abort) != 0) break;
-      if (now - t0 > t.timeout_ns || it > (1u << 30)) {
-        c->abort = 1;
-        if (threadIdx.x % 32 == 0) tc_record(1, blockIdx.x, role, phase);
+      if (*abort != 0) break;
+      if (now - t0 > limit || it > (1u << 30)) {
+        *abort = 1;
+        if (threadIdx.x % 32 == 0)
+          tc_record(1, blockIdx.x, where >> 4, where & 15);
         break;
       }
     }
+  }
   return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool tc_wait(const TcParams& t, TcCtl* c,
+                                        uint64_t* bar, uint32_t parity,
+                                        int role, int phase) {
+  return tc_wait_at(smem_u32(bar), parity, &c->abort, t.timeout_ns,
+                    role * 16 + phase);
 }
 
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
@@ -174,13 +192,14 @@ __device__ __forceinline__ float pow2(int e) {
 
 // ----------------------------------------------------------------- planner
 
-// Value scales of a step lie within these factors of its unit: a code times
-// the ratio is then exact in f16 (for ratios that are powers of two), 2^-19 its
-// smallest and 448 * 2^6 its largest number.  Pages further apart go in steps
-// of their own, between which O moves to the other unit.
+// Value scales go along with P: its column is multiplied by scale / v_ref, at
+// most 1 and no less than 2^-6, which its f16 stands (see kTcUpLog2), and the
+// row sums are of P over that factor.  Pages further apart go in steps of their
+// own, between which O moves to the other unit.  A unit leaves room for scales
+// that are four times that of the first page.
 __device__ __forceinline__ bool near_scale(float s, float ref) {
   const float r = s / ref;
-  return r >= 0x1p-10f && r <= 0x1p6f;
+  return r >= 0x1p-6f && r <= 1.f;
 }
 
 // 16 tokens' codes from global memory to shared memory, arriving on `bar`.
@@ -238,7 +257,7 @@ __device__ __forceinline__ bool plan_run(const TcParams& t, TcCtl* c,
       const unsigned some = __ballot_sync(0xffffffffu, mine);
       unsigned far = __ballot_sync(0xffffffffu, mine && !near_scale(vs, ref));
       if (far & (1u << at) || (ref == 0.f && some != 0)) {
-        ref = __shfl_sync(0xffffffffu, vs, __ffs(some) - 1);
+        ref = 4.f * __shfl_sync(0xffffffffu, vs, __ffs(some) - 1);
         far = __ballot_sync(0xffffffffu, mine && !near_scale(vs, ref));
         // (a scale that is near nothing, itself included, goes alone)
         far &= ~(1u << (__ffs(some) - 1));
@@ -253,8 +272,14 @@ __device__ __forceinline__ bool plan_run(const TcParams& t, TcCtl* c,
       const int i = at + n - 1 - lane;  // ascending tokens
       if (ours) {
         s.k_scale[i] = ks;
-        s.v_mul[i] = off >= 0 && ref != 0.f ? vs / ref : 0.f;
+        const float mul = off >= 0 && ref != 0.f ? vs / ref : 1.f;
+        s.v_log2[i] = log2f(mul);
+        s.v_inv[i] = 1.f / mul;
         s.valid[i] = off >= 0;
+      }
+      if (lane >= n && lane < kTcGroups) {  // their columns weigh 0
+        s.k_scale[lane] = s.v_log2[lane] = 0.f;
+        s.v_inv[lane] = 1.f;
       }
       const int tok0 = (plan.first_group + top - at - n) * kPaGroup;
       const unsigned there = __ballot_sync(0xffffffffu, ours && off >= 0);
@@ -393,12 +418,6 @@ __device__ __forceinline__ int token_of(int i) {
   return D == 128 ? (i >> 2 & 1) | (i >> 4 << 1) : i >> 2;
 }
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // What a step that is not plain needs before 16 codes of token tr are
 // converted: tokens that are no sequence's become zeros, and so do NaN codes of
 // values, which are noted, as a row that does not see them must not meet 0 *
@@ -427,6 +446,20 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y,
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x),
                "r"(y), "r"(z), "r"(w)
                : "memory");
+}
+
+__device__ __forceinline__ void lds128(uint32_t w[4], uint32_t a) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(a));
+}
+// 16 codes as f16, the first eight at a, the others at b.
+__device__ __forceinline__ void store_codes(const uint32_t w[4], uint32_t a,
+                                            uint32_t b) {
+  sts128(a, e4m3x2_to_f16x2(w[0]), e4m3x2_to_f16x2_hi(w[0]),
+         e4m3x2_to_f16x2(w[1]), e4m3x2_to_f16x2_hi(w[1]));
+  sts128(b, e4m3x2_to_f16x2(w[2]), e4m3x2_to_f16x2_hi(w[2]),
+         e4m3x2_to_f16x2(w[3]), e4m3x2_to_f16x2_hi(w[3]));
 }
 
 __device__ __forceinline__ bool wait_step(const TcParams& t, TcCtl* c,
@@ -467,39 +500,26 @@ __device__ __forceinline__ void convert_role(const TcParams& t, TcCtl* c,
                  kRoleConvert, 1))
       return;
     const bool plain = s.plain != 0;
-    uint32_t src = from + st * C::kCodes;
-    uint32_t dst_a = at_a + slot * C::kTile, dst_b = at_b + slot * C::kTile;
-#pragma unroll 2
-    for (int t0 = 0; t0 < tokens; t0 += kRows) {
-      // (at D = 64 half of the warpgroup may be past the last group)
-      if (D == 128 || t0 + static_cast<int>(row) < tokens) {
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(src)
-                     : "memory");
-        if (__builtin_expect(!plain, 0))
-          clean_codes(c, s, step, values, t0 + row, piece, w);
-        uint32_t x[8];
+    const uint32_t src = from + st * C::kCodes;
+    const uint32_t dst_a = at_a + slot * C::kTile,
+                   dst_b = at_b + slot * C::kTile;
+    constexpr int kPieces = D / 16;
+    uint32_t w[kPieces][4];
+    if (plain) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[2 * j] = e4m3x2_to_f16x2(w[j]);
-          x[2 * j + 1] = e4m3x2_to_f16x2_hi(w[j]);
-        }
-        if (values) {
-          const float m = s.v_mul[(t0 + row) / kPaGroup];
-          if (m != 1.f) {
-            const uint32_t mm = pack_f16x2(m, m);
+      for (int k = 0; k < kPieces; ++k) lds128(w[k], src + k * 2048);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = hmul2(x[j], mm);
-          }
-        }
-        sts128(dst_a, x[0], x[1], x[2], x[3]);
-        sts128(dst_b, x[4], x[5], x[6], x[7]);
+      for (int k = 0; k < kPieces; ++k)
+        store_codes(w[k], dst_a + k * (kRows * 128), dst_b + k * (kRows * 128));
+    } else {
+#pragma unroll 1
+      for (int k = 0; k * kRows < tokens; ++k) {
+        const int tr = k * kRows + static_cast<int>(row);
+        if (tr >= tokens) break;  // (D = 64, half of the warpgroup)
+        lds128(w[0], src + k * 2048);
+        clean_codes(c, s, step, values, tr, piece, w[0]);
+        store_codes(w[0], dst_a + k * (kRows * 128), dst_b + k * (kRows * 128));
       }
-      src += 2048;
-      dst_a += kRows * 128;
-      dst_b += kRows * 128;
     }
     if (!plain && values && (p.window > 0 || (p.mod.kind & kModBias))) {
       const int tok = s.tok0 + i, base = s.len - s.n;
@@ -576,7 +596,7 @@ __device__ __forceinline__ void mma_role(const TcParams& t, TcCtl* c,
         const uint64_t b = dk + C::slot(2 * step) * kUnits;
         const uint32_t idesc = idesc_f16(groups * kPaGroup, false);
         const uint32_t d = tmem + buf(step, r) * 128;
-#pragma unroll 1
+#pragma unroll 2
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k >> 2) * (kTcTokens * 128 / 16) + (k & 3) * 2;
           mma_ss_elect(d, a + off, b + off, idesc, k > 0);
@@ -598,7 +618,7 @@ __device__ __forceinline__ void mma_role(const TcParams& t, TcCtl* c,
         tc_fence_after();
         const uint64_t b = dv + C::slot(h) * kUnits;
         constexpr uint32_t idesc = idesc_f16(D, true);
-#pragma unroll 1
+#pragma unroll 2
         for (int k = 0; k < groups_before; ++k)
           mma_ts_elect(tmem + 256 + r * 128, tmem + bf * 128 + k * 8,
                        b + k * (kPaGroup * 128 / 16), idesc,
@@ -748,24 +768,32 @@ __device__ __forceinline__ float max_of(const float* x, float f0, float f1) {
   return fmaxf(m[0] * f0, m[1] * f1);
 }
 
-// P of 32 columns: 2^(x f + add), into P's columns at `to`, and their sums.
-__device__ __forceinline__ void weigh(const float* x, float f0, float f1,
-                                      float add, float* l, uint32_t to) {
+// P of 32 columns, 2^(x f + add) times their values' scales, into P's columns at
+// `to`; returns the sum without the scales.  f, add, inv: of either 16 columns.
+__device__ __forceinline__ float weigh(const float* x, const float* f,
+                                       const float* add, const float* inv,
+                                       uint32_t to) {
   uint32_t pk[16];
+  float sum = 0.f;
 #pragma unroll
-  for (int j = 0; j < 32; j += 4) {
-    const float f = j < 16 ? f0 : f1;
-    float x0, x1, x2, x3;
-    ffma2(x0, x1, x[j], x[j + 1], f, add);
-    ffma2(x2, x3, x[j + 2], x[j + 3], f, add);
-    const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-    const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
-    fadd2(l[0], l[1], l[0], l[1], p0, p1);
-    fadd2(l[2], l[3], l[2], l[3], p2, p3);
-    pk[j / 2] = pack_f16x2(p0, p1);
-    pk[j / 2 + 1] = pack_f16x2(p2, p3);
+  for (int g = 0; g < 2; ++g) {
+    float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+    for (int j = 16 * g; j < 16 * g + 16; j += 4) {
+      float x0, x1, x2, x3;
+      ffma2(x0, x1, x[j], x[j + 1], f[g], add[g]);
+      ffma2(x2, x3, x[j + 2], x[j + 3], f[g], add[g]);
+      const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+      const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
+      fadd2(l0, l1, l0, l1, p0, p1);
+      fadd2(l2, l3, l2, l3, p2, p3);
+      pk[j / 2] = pack_f16x2(p0, p1);
+      pk[j / 2 + 1] = pack_f16x2(p2, p3);
+    }
+    sum = fmaf((l0 + l1) + (l2 + l3), inv[g], sum);
   }
   tmem_st16(to, pk);
+  return sum;
 }
 
 template <int D, int R, bool MOD>
@@ -920,23 +948,28 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
     // their way while 32 are weighed (P's columns lie before theirs)
     const float add = m_used == NEG_INF ? kTcUpLog2 : kTcUpLog2 - m_used;
     const float fq = MOD || !plain ? 1.f : q_mul;
-    float l[4] = {0.f, 0.f, 0.f, 0.f};
     {
       float xa[32], xb[32];
-      auto scale = [&](int g) { return MOD || !plain ? 1.f : s.k_scale[g] * fq; };
+      auto weigh32 = [&](const float* x, int q) {
+        const float2 ks = *reinterpret_cast<const float2*>(&s.k_scale[2 * q]);
+        const float2 vl = *reinterpret_cast<const float2*>(&s.v_log2[2 * q]);
+        const float2 vi = *reinterpret_cast<const float2*>(&s.v_inv[2 * q]);
+        const float f[2] = {MOD || !plain ? 1.f : ks.x * fq,
+                            MOD || !plain ? 1.f : ks.y * fq};
+        const float a[2] = {add + vl.x, add + vl.y}, i[2] = {vi.x, vi.y};
+        l_sum += weigh(x, f, a, i, s_addr + q * 16);
+      };
       tmem_ld32(s_addr, reinterpret_cast<uint32_t*>(xa));
 #pragma unroll 1
       for (int q = 0; q < 4; q += 2) {
         tmem_ld_wait();
         tmem_ld32(s_addr + q * 32 + 32, reinterpret_cast<uint32_t*>(xb));
-        weigh(xa, scale(2 * q), scale(2 * q + 1), add, l, s_addr + q * 16);
+        weigh32(xa, q);
         tmem_ld_wait();
         if (q == 0) tmem_ld32(s_addr + 64, reinterpret_cast<uint32_t*>(xa));
-        weigh(xb, scale(2 * q + 2), scale(2 * q + 3), add, l,
-              s_addr + q * 16 + 16);
+        weigh32(xb, q + 1);
       }
     }
-    l_sum += (l[0] + l[1]) + (l[2] + l[3]);
     if (__any_sync(0xffffffffu, scale_o != 1.f) && run_pv > 0) {
       if (!tc_wait(tp, c, &c->pv_done[t], (step - 1) & 1, kRoleScore, 2)) return;
       tc_fence_after();
