@@ -16,8 +16,9 @@
 //
 // Roles (512 threads, four warpgroups):
 //   warp 0      deals the CTA's runs out in steps of up to 8 groups of 16
-//               tokens: looks up pages and scales, and starts the copies of
-//               the codes, up to two steps ahead of their conversion.
+//               tokens: looks up pages and scales, up to 8 steps ahead.
+//   warps 2, 3  start the copies of the keys' and of the values' codes, up to
+//               two steps ahead of their conversion.
 //   warp 1      issues the MMAs (and owns the 512 TMEM columns).
 //   converters  warpgroup 1, and with one tile of rows warpgroup 3 as well (one
 //               takes the keys then, the other the values).
@@ -34,6 +35,7 @@
 //
 // A step's tokens go from a run's end to its start: the drafts come first, and
 // with a bias that falls with the distance the maximum is met early.
+#include <cstddef>
 #include <cstdint>
 
 #include "bsm_internal.h"
@@ -55,7 +57,8 @@ constexpr int kTcGroups = kTcTokens / kPaGroup;
 constexpr int kTcSteps = 8;     // ring of steps
 constexpr uint32_t kTcTmem = 512;
 constexpr int kTreeFewRows = 16;  // see tree_tiles
-constexpr int kRolePlan = 1, kRoleMma = 2, kRoleConvert = 3, kRoleScore = 4;
+constexpr int kRolePlan = 1, kRoleMma = 2, kRoleConvert = 3, kRoleScore = 4,
+              kRoleLoad = 5;
 // P is scaled by 2^9 before it becomes f16, whose smallest number is 2^-24: a
 // key's weight is lost below 2^-33 of the largest, with the least of the values'
 // scales (2^-6) below 2^-27.  The reference m may lie up to 2^6 below the running
@@ -95,7 +98,7 @@ struct TcCfg {
 };
 
 // Up to 128 tokens of a run, newest step first.
-struct TcStep {
+struct alignas(16) TcStep {  // (its arrays are read 16 bytes at a time)
   int32_t groups;    // 1 .. 8 groups of 16 tokens from tok0 on; 0: the end
   int32_t tok0;
   int32_t first, last;  // of its run
@@ -104,12 +107,15 @@ struct TcStep {
   // of the run
   int32_t b, hkv, row0, part;  // part: -1 whole, else its slot in the workspace
   int32_t len, lo, n;          // tokens, first visible one, drafts
-  int32_t pad;
+  int32_t pad[3];
   float k_scale[kTcGroups];
   float v_log2[kTcGroups];     // log2(scale / v_ref)
   float v_inv[kTcGroups];      // v_ref / scale
-  int32_t valid[kTcGroups];    // 0: the group's page is out of range
+  int64_t off[kTcGroups];      // of the group's codes; -1: page out of range
 };
+
+static_assert(offsetof(TcStep, k_scale) % 16 == 0 && sizeof(TcStep) % 16 == 0,
+              "alignment");
 
 struct TcCtl {
   uint64_t step_full[kTcSteps], step_empty[kTcSteps];
@@ -196,30 +202,19 @@ __device__ __forceinline__ float pow2(int e) {
 // most 1 and no less than 2^-6, which its f16 stands (see kTcUpLog2), and the
 // row sums are of P over that factor.  Pages further apart go in steps of their
 // own, between which O moves to the other unit.  A unit leaves room for scales
-// that are four times that of the first page.
-__device__ __forceinline__ bool near_scale(float s, float ref) {
-  const float r = s / ref;
-  return r >= 0x1p-6f && r <= 1.f;
-}
-
-// 16 tokens' codes from global memory to shared memory, arriving on `bar`.
-__device__ __forceinline__ void copy_codes(uint32_t dst, const uint8_t* src,
-                                           uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
+// that are four times that of the first page.  (All in log2: of a scale of 0,
+// which no page that holds tokens has, -inf, as a unit 2^-126.)
+__device__ __forceinline__ bool near_scale(float log2_scale, float log2_ref) {
+  const float r = log2_scale - log2_ref;
+  return r >= -6.f && r <= 0.f;
 }
 
 // One run: groups [g0, g1) of its sequence's plan.
 template <int D, int R>
 __device__ __forceinline__ bool plan_run(const TcParams& t, TcCtl* c,
-                                         uint32_t codes, int b,
-                                         const PaPlan& plan, int hkv, int row0,
-                                         int g0, int g1, int part,
-                                         uint32_t& step, uint32_t& copied) {
-  using C = TcCfg<D, R>;
+                                         int b, const PaPlan& plan, int hkv,
+                                         int row0, int g0, int g1, int part,
+                                         uint32_t& step) {
   const PagedParams& p = t.p;
   const int lane = threadIdx.x % 32;
   const int* table = p.table + static_cast<int64_t>(b) * p.table_stride;
@@ -231,12 +226,12 @@ __device__ __forceinline__ bool plan_run(const TcParams& t, TcCtl* c,
     return g >= g0 ? table[(plan.first_group + g) >> (p.page_shift - 4)] : -1;
   };
   int next_pid = page_of(g1);
-  float ref = 0.f;
+  float ref = 0.f, log2_ref = 0.f;  // 0: none yet
 #pragma unroll 1
   for (int top = g1; top > g0; top -= 32) {
     const int g = top - 1 - lane, pid = next_pid;
     const int tok = (plan.first_group + g) * kPaGroup;
-    float ks = 0.f, vs = 0.f;
+    float ks = 0.f, vs = 1.f;
     int64_t off = -1;
     if (g >= g0) {
       if (static_cast<uint32_t>(pid) < static_cast<uint32_t>(p.num_pages)) {
@@ -249,18 +244,22 @@ __device__ __forceinline__ bool plan_run(const TcParams& t, TcCtl* c,
       }
     }
     next_pid = page_of(top - 32);
+    const float lv = log2f(vs), rv = 1.f / vs;
     const int here = min(32, top - g0);
 #pragma unroll 1
     for (int at = 0; at < here;) {
       int n = min(kTcGroups, here - at);
       const bool mine = lane >= at && lane < at + n && off >= 0;
       const unsigned some = __ballot_sync(0xffffffffu, mine);
-      unsigned far = __ballot_sync(0xffffffffu, mine && !near_scale(vs, ref));
+      unsigned far = __ballot_sync(
+          0xffffffffu, mine && (ref == 0.f || !near_scale(lv, log2_ref)));
       if (far & (1u << at) || (ref == 0.f && some != 0)) {
-        ref = 4.f * __shfl_sync(0xffffffffu, vs, __ffs(some) - 1);
-        far = __ballot_sync(0xffffffffu, mine && !near_scale(vs, ref));
+        const int one = __ffs(some) - 1;
+        ref = fmaxf(4.f * __shfl_sync(0xffffffffu, vs, one), 0x1p-126f);
+        log2_ref = log2f(ref);
+        far = __ballot_sync(0xffffffffu, mine && !near_scale(lv, log2_ref));
         // (a scale that is near nothing, itself included, goes alone)
-        far &= ~(1u << (__ffs(some) - 1));
+        far &= ~(1u << one);
       }
       if (far != 0) n = __ffs(far) - 1 - at;
       const bool ours = lane >= at && lane < at + n;
@@ -272,10 +271,9 @@ __device__ __forceinline__ bool plan_run(const TcParams& t, TcCtl* c,
       const int i = at + n - 1 - lane;  // ascending tokens
       if (ours) {
         s.k_scale[i] = ks;
-        const float mul = off >= 0 && ref != 0.f ? vs / ref : 1.f;
-        s.v_log2[i] = log2f(mul);
-        s.v_inv[i] = 1.f / mul;
-        s.valid[i] = off >= 0;
+        s.v_log2[i] = off >= 0 ? lv - log2_ref : 0.f;
+        s.v_inv[i] = off >= 0 ? rv * ref : 1.f;
+        s.off[i] = off;
       }
       if (lane >= n && lane < kTcGroups) {  // their columns weigh 0
         s.k_scale[lane] = s.v_log2[lane] = 0.f;
@@ -301,23 +299,6 @@ __device__ __forceinline__ bool plan_run(const TcParams& t, TcCtl* c,
         s.n = plan.drafts;
       }
       warp_arrive(&c->step_full[slot]);
-      // its keys' codes, then its values'
-#pragma unroll 1
-      for (int v = 0; v < 2; ++v) {
-        const uint32_t h = 2 * step + v, st = C::stage(h);
-        if (!tc_wait(t, c, &c->code_empty[st], (C::stage_use(h) & 1) ^ 1,
-                     kRolePlan, 1))
-          return false;
-        if (lane == 0)
-          mbar_arrive_expect_tx(&c->code_full[st],
-                                __popc(there) * (kPaGroup * D));
-        __syncwarp();
-        if (ours && off >= 0)
-          copy_codes(codes + st * C::kCodes + i * (kPaGroup * D),
-                     (v ? p.v : p.k) + off, kPaGroup * D, &c->code_full[st]);
-        __syncwarp();
-        ++copied;
-      }
       ++step;
       at += n;
     }
@@ -326,10 +307,8 @@ __device__ __forceinline__ bool plan_run(const TcParams& t, TcCtl* c,
 }
 
 template <int D, int R>
-__device__ __forceinline__ void plan_role(const TcParams& t, TcCtl* c,
-                                          uint32_t codes) {
+__device__ __forceinline__ void plan_role(const TcParams& t, TcCtl* c) {
   using X = TcDeal;
-  using C = TcCfg<D, R>;
   const PagedParams& p = t.p;
   const int lane = threadIdx.x % 32;
   const int rows = p.H / p.H_kv * p.T;
@@ -357,7 +336,7 @@ __device__ __forceinline__ void plan_role(const TcParams& t, TcCtl* c,
         return u;
       },
       &start);
-  uint32_t step = 0, copied = 0;  // half steps whose copies were started
+  uint32_t step = 0;
   bool ok = true;
   while (ok && b >= 0 && u < end) {
     const PaPlan plan = plan_of<X>(p, b);
@@ -379,26 +358,80 @@ __device__ __forceinline__ void plan_role(const TcParams& t, TcCtl* c,
       int part = -1;
       if (r0 > 0 || r1 < plan.n_units)  // slot 0: an earlier CTA has the start
         part = blockIdx.x * 2 + (r0 > 0 ? 0 : 1);
-      ok = plan_run<D, R>(t, c, codes, b, plan, item / tiles,
+      ok = plan_run<D, R>(t, c, b, plan, item / tiles,
                           item % tiles * (R * kTcRows), r0 * kTcGroups,
-                          min(r1 * kTcGroups, plan.n_groups), part, step, copied);
+                          min(r1 * kTcGroups, plan.n_groups), part, step);
     }
     u += n;
   }
   const uint32_t slot = step % kTcSteps;  // the end
-  if (ok && tc_wait(t, c, &c->step_empty[slot], ((step / kTcSteps) & 1) ^ 1,
-                    kRolePlan, 2)) {
-    if (lane == 0) c->steps[slot].groups = 0;
-    warp_arrive(&c->step_full[slot]);
-    return;  // (the converters wait for every copy)
+  if (!ok || !tc_wait(t, c, &c->step_empty[slot], ((step / kTcSteps) & 1) ^ 1,
+                      kRolePlan, 2))
+    return;
+  if (lane == 0) c->steps[slot].groups = 0;
+  warp_arrive(&c->step_full[slot]);
+}
+
+// ------------------------------------------------------------------- loader
+
+__device__ __forceinline__ bool wait_step(const TcParams& t, TcCtl* c,
+                                          uint32_t step, int role) {
+  return tc_wait(t, c, &c->step_full[step % kTcSteps], (step / kTcSteps) & 1,
+                 role, 9);
+}
+
+// Copies the codes of every step's keys (which = 0) or values (1): one bulk copy
+// for groups that follow each other in a page.
+template <int D, int R>
+__device__ __forceinline__ void load_role(const TcParams& t, TcCtl* c,
+                                          uint32_t codes, int which) {
+  using C = TcCfg<D, R>;
+  constexpr int kBytes = kPaGroup * D;
+  const uint8_t* pages = which ? t.p.v : t.p.k;
+  const int lane = threadIdx.x % 32;
+  uint32_t step = 0;  // so many copied
+  bool ok;
+#pragma unroll 1
+  for (;; ++step) {
+    ok = wait_step(t, c, step, kRoleLoad);
+    if (!ok) break;
+    const TcStep& s = c->steps[step % kTcSteps];
+    const int groups = s.groups;
+    if (groups == 0) break;
+    const int64_t off = lane < groups ? s.off[lane] : -1;
+    warp_arrive(&c->step_empty[step % kTcSteps]);
+    const int64_t before = __shfl_up_sync(0xffffffffu, off, 1);
+    const unsigned there = __ballot_sync(0xffffffffu, off >= 0);
+    const unsigned starts = __ballot_sync(
+        0xffffffffu,
+        off >= 0 && (lane == 0 || before < 0 || before + kBytes != off));
+    const uint32_t h = 2 * step + which, st = C::stage(h);
+    ok = tc_wait(t, c, &c->code_empty[st], (C::stage_use(h) & 1) ^ 1, kRoleLoad,
+                 which);
+    if (!ok) break;
+    if (lane == 0)
+      mbar_arrive_expect_tx(&c->code_full[st], __popc(there) * kBytes);
+    __syncwarp();
+    if (starts >> lane & 1u) {
+      // up to the next start or the next page that is not there
+      const unsigned ends = (starts | ~there) >> lane >> 1;
+      const int n = ends != 0 ? __ffs(ends) : 32;
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+          "[%0], [%1], %2, [%3];" ::"r"(codes + st * C::kCodes + lane * kBytes),
+          "l"(pages + off), "r"(n * kBytes), "r"(smem_u32(&c->code_full[st]))
+          : "memory");
+    }
+    __syncwarp();
   }
-  // given up: the copies under way still land in this CTA's shared memory; the
-  // last into a stage completes its (copies into it - 1)th phase
-  if (lane == 0)
-    for (uint32_t st = 0; st < C::kStages; ++st)
-      if (copied > st)
-        mbar_wait_drain(&c->code_full[st], ((copied - 1 - st) / C::kStages) & 1,
-                        t.timeout_ns);
+  // Given up: the copies under way still land in this CTA's shared memory.  (At
+  // the end the converters have waited for every copy.)
+  if (!ok && lane == 0)
+    for (uint32_t i = 1; i <= C::kStages && i <= step; ++i) {
+      const uint32_t h = 2 * (step - i) + which;
+      mbar_wait_drain(&c->code_full[C::stage(h)], C::stage_use(h) & 1,
+                      t.timeout_ns);
+    }
   __syncwarp();
 }
 
@@ -426,7 +459,7 @@ __device__ __forceinline__ void clean_codes(TcCtl* c, const TcStep& s,
                                             uint32_t step, bool values, int tr,
                                             int piece, uint32_t* w) {
   const int tok = s.tok0 + tr;
-  const bool there = tok >= s.lo && tok < s.len && s.valid[tr / kPaGroup] != 0;
+  const bool there = tok >= s.lo && tok < s.len && s.off[tr / kPaGroup] >= 0;
   uint32_t found = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -460,12 +493,6 @@ __device__ __forceinline__ void store_codes(const uint32_t w[4], uint32_t a,
          e4m3x2_to_f16x2(w[1]), e4m3x2_to_f16x2_hi(w[1]));
   sts128(b, e4m3x2_to_f16x2(w[2]), e4m3x2_to_f16x2_hi(w[2]),
          e4m3x2_to_f16x2(w[3]), e4m3x2_to_f16x2_hi(w[3]));
-}
-
-__device__ __forceinline__ bool wait_step(const TcParams& t, TcCtl* c,
-                                          uint32_t step, int role) {
-  return tc_wait(t, c, &c->step_full[step % kTcSteps], (step / kTcSteps) & 1,
-                 role, 9);
 }
 
 // A converter warpgroup: with one tile of rows the keys (which = 0) or the
@@ -596,7 +623,7 @@ __device__ __forceinline__ void mma_role(const TcParams& t, TcCtl* c,
         const uint64_t b = dk + C::slot(2 * step) * kUnits;
         const uint32_t idesc = idesc_f16(groups * kPaGroup, false);
         const uint32_t d = tmem + buf(step, r) * 128;
-#pragma unroll 2
+#pragma unroll 1
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k >> 2) * (kTcTokens * 128 / 16) + (k & 3) * 2;
           mma_ss_elect(d, a + off, b + off, idesc, k > 0);
@@ -618,7 +645,7 @@ __device__ __forceinline__ void mma_role(const TcParams& t, TcCtl* c,
         tc_fence_after();
         const uint64_t b = dv + C::slot(h) * kUnits;
         constexpr uint32_t idesc = idesc_f16(D, true);
-#pragma unroll 2
+#pragma unroll 1
         for (int k = 0; k < groups_before; ++k)
           mma_ts_elect(tmem + 256 + r * 128, tmem + bf * 128 + k * 8,
                        b + k * (kPaGroup * 128 / 16), idesc,
@@ -692,7 +719,7 @@ __device__ __forceinline__ uint32_t visible(const PagedParams& p,
   if (lo > 0) keep = lo >= 32 ? 0u : keep & (~0u << lo);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    if (2 * word + i < s.groups && s.valid[2 * word + i] == 0)
+    if (2 * word + i < s.groups && s.off[2 * word + i] < 0)
       keep &= ~(0xffffu << (16 * i));
   const int d0 = t0 - base;  // draft of the word's first column
   if (d0 > -32) {
@@ -862,16 +889,15 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
     // written back as they are to be weighed.
     float top = NEG_INF;
     if (!MOD && plain) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
+#pragma unroll 1
+      for (int q = 0; q < 4; q += 2) {
         float x[64];
-        tmem_ld32(s_addr + h * 64, reinterpret_cast<uint32_t*>(x));
-        tmem_ld32(s_addr + h * 64 + 32, reinterpret_cast<uint32_t*>(x + 32));
+        tmem_ld32(s_addr + q * 32, reinterpret_cast<uint32_t*>(x));
+        tmem_ld32(s_addr + q * 32 + 32, reinterpret_cast<uint32_t*>(x + 32));
+        const float4 ks = *reinterpret_cast<const float4*>(&s.k_scale[2 * q]);
         tmem_ld_wait();
-        const float a = max_of(x, s.k_scale[4 * h], s.k_scale[4 * h + 1]);
-        const float b =
-            max_of(x + 32, s.k_scale[4 * h + 2], s.k_scale[4 * h + 3]);
-        top = fmax3(top, a * q_mul, b * q_mul);
+        top = fmax3(top, max_of(x, ks.x, ks.y) * q_mul,
+                    max_of(x + 32, ks.z, ks.w) * q_mul);
       }
     } else {
 #pragma unroll 1
@@ -949,8 +975,14 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
     const float add = m_used == NEG_INF ? kTcUpLog2 : kTcUpLog2 - m_used;
     const float fq = MOD || !plain ? 1.f : q_mul;
     {
-      float xa[32], xb[32];
-      auto weigh32 = [&](const float* x, int q) {
+      float x[32], next[32];
+      tmem_ld32(s_addr, reinterpret_cast<uint32_t*>(x));
+      tmem_ld_wait();
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        // (the last turn loads the last columns again)
+        tmem_ld32(s_addr + min(q + 1, 3) * 32,
+                  reinterpret_cast<uint32_t*>(next));
         const float2 ks = *reinterpret_cast<const float2*>(&s.k_scale[2 * q]);
         const float2 vl = *reinterpret_cast<const float2*>(&s.v_log2[2 * q]);
         const float2 vi = *reinterpret_cast<const float2*>(&s.v_inv[2 * q]);
@@ -958,16 +990,9 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
                             MOD || !plain ? 1.f : ks.y * fq};
         const float a[2] = {add + vl.x, add + vl.y}, i[2] = {vi.x, vi.y};
         l_sum += weigh(x, f, a, i, s_addr + q * 16);
-      };
-      tmem_ld32(s_addr, reinterpret_cast<uint32_t*>(xa));
-#pragma unroll 1
-      for (int q = 0; q < 4; q += 2) {
         tmem_ld_wait();
-        tmem_ld32(s_addr + q * 32 + 32, reinterpret_cast<uint32_t*>(xb));
-        weigh32(xa, q);
-        tmem_ld_wait();
-        if (q == 0) tmem_ld32(s_addr + 64, reinterpret_cast<uint32_t*>(xa));
-        weigh32(xb, q + 1);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = next[j];
       }
     }
     if (__any_sync(0xffffffffu, scale_o != 1.f) && run_pv > 0) {
@@ -1073,7 +1098,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kTcSteps; ++i) {
       mbar_init(&c->step_full[i], 1);
-      mbar_init(&c->step_empty[i], kConvertWarps + 1 + kScoreWarps);
+      mbar_init(&c->step_empty[i], 3 + kConvertWarps + kScoreWarps);
     }
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&c->code_full[i], 1);
@@ -1105,9 +1130,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t tmem = c->tmem, base = smem_u32(smem);
   if (wg == 0) {
     if (warp == 0)
-      plan_role<D, R>(t, c, base + C::kOffCodes);
+      plan_role<D, R>(t, c);
     else if (warp == 1)
       mma_role<D, R>(t, c, base, tmem);
+    else
+      load_role<D, R>(t, c, base + C::kOffCodes, warp - 2);
   } else if (wg == 1 || (R == 1 && wg == 3)) {
     convert_role<D, R>(t, c, base + C::kOffKv, base + C::kOffCodes, wg >> 1);
   } else {
