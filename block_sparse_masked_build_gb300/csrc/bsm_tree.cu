@@ -17,9 +17,9 @@
 // Roles (512 threads, four warpgroups):
 //   warp 0      deals the CTA's runs out in steps of up to 8 groups of 16
 //               tokens: looks up pages and scales, up to 8 steps ahead.
-//   warps 2, 3  start the copies of the keys' and of the values' codes, up to
-//               two steps ahead of their conversion.
-//   warp 1      issues the MMAs (and owns the 512 TMEM columns).
+//   warp 3      starts the copies of the codes, up to two steps ahead of their
+//               conversion.
+//   warps 1, 2  issue the MMAs (warp 1 owns the 512 TMEM columns).
 //   converters  warpgroup 1, and with one tile of rows warpgroup 3 as well (one
 //               takes the keys then, the other the values).
 //   score       warpgroup 2 (and 3 with two tiles): one thread per query row,
@@ -121,7 +121,7 @@ struct TcCtl {
   uint64_t step_full[kTcSteps], step_empty[kTcSteps];
   uint64_t code_full[5], code_empty[5];
   uint64_t kv_full[3], kv_empty[3];
-  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], o_free[2], mma_done;
+  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], o_free[2], mma_done[2];
   uint32_t tmem;
   int abort;
   TcStep steps[kTcSteps];
@@ -380,34 +380,37 @@ __device__ __forceinline__ bool wait_step(const TcParams& t, TcCtl* c,
                  role, 9);
 }
 
-// Copies the codes of every step's keys (which = 0) or values (1): one bulk copy
-// for groups that follow each other in a page.
+// Copies the codes of every step's keys and then its values: one bulk copy for
+// groups that follow each other in a page.
 template <int D, int R>
 __device__ __forceinline__ void load_role(const TcParams& t, TcCtl* c,
-                                          uint32_t codes, int which) {
+                                          uint32_t codes) {
   using C = TcCfg<D, R>;
   constexpr int kBytes = kPaGroup * D;
-  const uint8_t* pages = which ? t.p.v : t.p.k;
   const int lane = threadIdx.x % 32;
-  uint32_t step = 0;  // so many copied
-  bool ok;
+  uint32_t h = 0;  // half steps copied
+  int64_t off = -1;
+  bool ok = true;
 #pragma unroll 1
-  for (;; ++step) {
-    ok = wait_step(t, c, step, kRoleLoad);
-    if (!ok) break;
-    const TcStep& s = c->steps[step % kTcSteps];
-    const int groups = s.groups;
-    if (groups == 0) break;
-    const int64_t off = lane < groups ? s.off[lane] : -1;
-    warp_arrive(&c->step_empty[step % kTcSteps]);
+  for (;; ++h) {
+    if (h % 2 == 0) {
+      const uint32_t step = h / 2;
+      ok = wait_step(t, c, step, kRoleLoad);
+      if (!ok) break;
+      const TcStep& s = c->steps[step % kTcSteps];
+      const int groups = s.groups;
+      if (groups == 0) break;
+      off = lane < groups ? s.off[lane] : -1;
+      warp_arrive(&c->step_empty[step % kTcSteps]);
+    }
     const int64_t before = __shfl_up_sync(0xffffffffu, off, 1);
     const unsigned there = __ballot_sync(0xffffffffu, off >= 0);
     const unsigned starts = __ballot_sync(
         0xffffffffu,
         off >= 0 && (lane == 0 || before < 0 || before + kBytes != off));
-    const uint32_t h = 2 * step + which, st = C::stage(h);
+    const uint32_t st = C::stage(h);
     ok = tc_wait(t, c, &c->code_empty[st], (C::stage_use(h) & 1) ^ 1, kRoleLoad,
-                 which);
+                 0);
     if (!ok) break;
     if (lane == 0)
       mbar_arrive_expect_tx(&c->code_full[st], __popc(there) * kBytes);
@@ -419,7 +422,8 @@ __device__ __forceinline__ void load_role(const TcParams& t, TcCtl* c,
       asm volatile(
           "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
           "[%0], [%1], %2, [%3];" ::"r"(codes + st * C::kCodes + lane * kBytes),
-          "l"(pages + off), "r"(n * kBytes), "r"(smem_u32(&c->code_full[st]))
+          "l"((h % 2 ? t.p.v : t.p.k) + off), "r"(n * kBytes),
+          "r"(smem_u32(&c->code_full[st]))
           : "memory");
     }
     __syncwarp();
@@ -427,11 +431,9 @@ __device__ __forceinline__ void load_role(const TcParams& t, TcCtl* c,
   // Given up: the copies under way still land in this CTA's shared memory.  (At
   // the end the converters have waited for every copy.)
   if (!ok && lane == 0)
-    for (uint32_t i = 1; i <= C::kStages && i <= step; ++i) {
-      const uint32_t h = 2 * (step - i) + which;
-      mbar_wait_drain(&c->code_full[C::stage(h)], C::stage_use(h) & 1,
-                      t.timeout_ns);
-    }
+    for (uint32_t i = 1; i <= C::kStages && i <= h; ++i)
+      mbar_wait_drain(&c->code_full[C::stage(h - i)],
+                      C::stage_use(h - i) & 1, t.timeout_ns);
   __syncwarp();
 }
 
@@ -521,10 +523,17 @@ __device__ __forceinline__ void convert_role(const TcParams& t, TcCtl* c,
     const int tokens = s.groups * kPaGroup;
     if (tokens == 0) return;
     const uint32_t st = C::stage(h), slot = C::slot(h);
+    // the tile is free again when the MMA that read it is done: with one tile
+    // of rows S of the step before the last, or P V of the step before
+    uint64_t* free_at = &c->kv_empty[slot];
+    uint32_t uses = C::slot_use(h);
+    if (R == 1 && step > 0) {
+      free_at = values ? &c->pv_done[(step - 1) & 1] : &c->s_full[step & 1];
+      uses = values ? ((step - 1) >> 1) + 1 : step >> 1;
+    }
     if (!tc_wait(t, c, &c->code_full[st], C::stage_use(h) & 1, kRoleConvert,
                  0) ||
-        !tc_wait(t, c, &c->kv_empty[slot], (C::slot_use(h) & 1) ^ 1,
-                 kRoleConvert, 1))
+        !tc_wait(t, c, free_at, (uses & 1) ^ 1, kRoleConvert, 1))
       return;
     const bool plain = s.plain != 0;
     const uint32_t src = from + st * C::kCodes;
@@ -573,21 +582,51 @@ __device__ __forceinline__ constexpr uint32_t idesc_f16(int N, bool mn_major) {
          (static_cast<uint32_t>(kTcRows >> 4) << 24);
 }
 
+// S (128 rows x 16 groups tokens) = Q K^T, by descriptors of the two tiles.
+template <int D>
+__device__ __forceinline__ void issue_s(uint32_t d, uint64_t q, uint64_t k,
+                                        int groups) {
+  const uint32_t idesc = idesc_f16(groups * kPaGroup, false);
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    const uint32_t off = (i >> 2) * (kTcTokens * 128 / 16) + (i & 3) * 2;
+    mma_ss_elect(d, q + off, k + off, idesc, i > 0);
+  }
+}
+
+// O (+)= P V over `groups` groups; first: O's first.
+template <int D>
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t p, uint64_t v,
+                                         int groups, bool first) {
+  constexpr uint32_t idesc = idesc_f16(D, true);
+#pragma unroll
+  for (int i = 0; i < kTcGroups; ++i)
+    if (i < groups)
+      mma_ts_elect(d, p + i * 8, v + i * (kPaGroup * 128 / 16), idesc,
+                   i > 0 || !first);
+}
+
+// Two warps issue MMAs (one warp alone, whose waits and commits no other work
+// covered, took 3300 cycles for a step's S and P V).  With one tile of rows warp
+// 0 issues every S and warp 1 every P V; with two, each its tile's: S_t goes
+// behind the P V that reads its columns, as MMAs of one thread run in the order
+// they were issued.  A run's first S waits for its query, its first P V for O,
+// until the rows of the run before are written out.
 template <int D, int R>
 __device__ __forceinline__ void mma_role(const TcParams& t, TcCtl* c,
-                                         uint32_t smem, uint32_t tmem) {
+                                         uint32_t smem, uint32_t tmem,
+                                         const int w) {
   using C = TcCfg<D, R>;
   constexpr uint32_t kUnits = C::kTile >> 4;
-  const uint64_t dq = sdesc_sw128(smem, 16, 1024);
+  const int tile = R == 2 ? w : 0;
+  const uint64_t dq = sdesc_sw128(smem, 16, 1024) + tile * kUnits;
   const uint64_t dk = sdesc_sw128(smem + C::kOffKv, 16, 1024);
   const uint64_t dv = sdesc_sw128(smem + C::kOffKv, kTcTokens * 128, 1024);
-  bool ok = true;
+  const uint32_t o_acc = tmem + 256 + tile * 128;
   uint32_t runs = 0;  // begun
-  int groups = 0, groups_before = 0;  // of the step and of the one before
-  bool first = false, first_before = false;
-  // buffer of tile r at a step, and how often it was used before
-  auto buf = [](uint32_t step, int r) { return R == 2 ? r : int(step & 1); };
-  auto use = [](uint32_t step) { return R == 2 ? step : step >> 1; };
+  int groups_before = 0;
+  bool first_before = false;
+  bool ok = true;
   auto wait_kv = [&](uint32_t h) {
     return tc_wait(t, c, &c->kv_full[C::slot(h)], C::slot_use(h) & 1, kRoleMma,
                    2);
@@ -597,70 +636,71 @@ __device__ __forceinline__ void mma_role(const TcParams& t, TcCtl* c,
     ok = wait_step(t, c, step, kRoleMma);
     if (!ok) break;
     const TcStep& s = c->steps[step % kTcSteps];
-    groups_before = groups;
-    first_before = first;
-    groups = s.groups;
-    first = s.first != 0;
+    const int groups = s.groups;
+    const bool first = s.first != 0;
     const bool more = groups != 0;
     warp_arrive(&c->step_empty[step % kTcSteps]);
-    // One tile: S goes ahead of the P V before it, in the other buffer, while
-    // that P is in the making.  Two tiles share the steps' S and P in turn: S
-    // goes behind the P V that reads its columns (MMAs of one thread run in
-    // the order they were issued).  A run's first S waits for its query, which
-    // the rows load when the run before is written out.
-    const bool ahead = R == 1 && !first;
-#pragma unroll 1
-    for (int turn = 0; turn < 2 * R; ++turn) {
-      const int r = turn >> 1;
-      if (((turn & 1) != 0) != ahead) {  // S_r = Q_r K^T
-        if (!more) continue;
-        if (r == 0) ok = wait_kv(2 * step);
+    if (R == 1) {
+      if (!more) break;
+      const uint32_t buf = step & 1, use = step >> 1;
+      const uint32_t s_acc = tmem + buf * 128;
+      const uint32_t h = 2 * step + w;
+      ok = wait_kv(h);
+      if (w == 0) {
+        // the buffer's P is used up
+        if (ok && step > 1)
+          ok = tc_wait(t, c, &c->pv_done[buf], (use - 1) & 1, kRoleMma, 5);
+        if (ok && first) ok = tc_wait(t, c, &c->q_full[0], runs & 1, kRoleMma, 1);
+      } else {
+        if (ok) ok = tc_wait(t, c, &c->p_full[buf], use & 1, kRoleMma, 3);
         if (ok && first)
-          ok = tc_wait(t, c, &c->q_full[r], runs & 1, kRoleMma, 1);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t a = dq + r * kUnits;
-        const uint64_t b = dk + C::slot(2 * step) * kUnits;
-        const uint32_t idesc = idesc_f16(groups * kPaGroup, false);
-        const uint32_t d = tmem + buf(step, r) * 128;
-#pragma unroll 1
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * (kTcTokens * 128 / 16) + (k & 3) * 2;
-          mma_ss_elect(d, a + off, b + off, idesc, k > 0);
-        }
-        mma_commit_elect(&c->s_full[buf(step, r)]);
-        if (r == R - 1)
-          mma_commit_elect(&c->kv_empty[C::slot(2 * step)]);
-      } else {  // O_r (+)= P_r V of the step before
-        if (step == 0) continue;
-        const uint32_t before = step - 1, h = 2 * before + 1;
-        const int bf = buf(before, r);
-        if (r == 0) ok = wait_kv(h);
-        if (ok)
-          ok = tc_wait(t, c, &c->p_full[bf], use(before) & 1, kRoleMma, 3);
-        // run k (k = runs - 1 here) finds O free when k runs were written out
-        if (ok && first_before)
-          ok = tc_wait(t, c, &c->o_free[r], runs & 1, kRoleMma, 4);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t b = dv + C::slot(h) * kUnits;
-        constexpr uint32_t idesc = idesc_f16(D, true);
-#pragma unroll 1
-        for (int k = 0; k < groups_before; ++k)
-          mma_ts_elect(tmem + 256 + r * 128, tmem + bf * 128 + k * 8,
-                       b + k * (kPaGroup * 128 / 16), idesc,
-                       k > 0 || !first_before);
-        mma_commit_elect(&c->pv_done[r]);
-        if (r == R - 1) mma_commit_elect(&c->kv_empty[C::slot(h)]);
+          ok = tc_wait(t, c, &c->o_free[0], (runs & 1) ^ 1, kRoleMma, 4);
       }
+      if (!ok) break;
+      runs += first;
+      tc_fence_after();
+      if (w == 0) {
+        issue_s<D>(s_acc, dq, dk + C::slot(h) * kUnits, groups);
+        mma_commit_elect(&c->s_full[buf]);
+      } else {
+        issue_pv<D>(o_acc, s_acc, dv + C::slot(h) * kUnits, groups, first);
+        mma_commit_elect(&c->pv_done[buf]);
+      }
+    } else {
+      const uint32_t s_acc = tmem + tile * 128;
+      if (step > 0) {
+        const uint32_t h = 2 * step - 1;
+        ok = wait_kv(h) &&
+             tc_wait(t, c, &c->p_full[tile], (step - 1) & 1, kRoleMma, 3);
+        // run k (k = runs - 1) finds O free when k runs were written out
+        if (ok && first_before)
+          ok = tc_wait(t, c, &c->o_free[tile], runs & 1, kRoleMma, 4);
+        if (!ok) break;
+        tc_fence_after();
+        issue_pv<D>(o_acc, s_acc, dv + C::slot(h) * kUnits, groups_before,
+                    first_before);
+        mma_commit_elect(&c->pv_done[tile]);
+        mma_commit_elect(&c->kv_empty[C::slot(h)]);
+      }
+      if (!more) break;
+      ok = wait_kv(2 * step);
+      if (ok && first)
+        ok = tc_wait(t, c, &c->q_full[tile], runs & 1, kRoleMma, 1);
+      if (!ok) break;
+      runs += first;
+      tc_fence_after();
+      issue_s<D>(s_acc, dq, dk + C::slot(2 * step) * kUnits, groups);
+      mma_commit_elect(&c->s_full[tile]);
+      mma_commit_elect(&c->kv_empty[C::slot(2 * step)]);
+      groups_before = groups;
+      first_before = first;
     }
-    if (!more) break;
-    if (first) ++runs;
   }
   // every MMA issued above has completed once this arrives
   __syncwarp();
-  mma_commit_elect(&c->mma_done);
-  if (threadIdx.x % 32 == 0 && !mbar_wait_drain(&c->mma_done, 0, t.timeout_ns))
+  mma_commit_elect(&c->mma_done[w]);
+  if (threadIdx.x % 32 == 0 &&
+      !mbar_wait_drain(&c->mma_done[w], 0, t.timeout_ns))
     tc_record(1, blockIdx.x, kRoleMma, 8);
   __syncwarp();
 }
@@ -844,8 +884,13 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
   int row = 0, tq = 0, pos = -1;
   uint32_t nans[D / 32];
   uint32_t run_pv = 0;
+  auto wait_pv = [&](uint32_t step, int phase) {  // a step's P V is done
+    return R == 2 ? tc_wait(tp, c, &c->pv_done[t], step & 1, kRoleScore, phase)
+                  : tc_wait(tp, c, &c->pv_done[step & 1], step >> 1 & 1,
+                            kRoleScore, phase);
+  };
 #pragma unroll 1
-  for (uint32_t step = 0;; ++step) {  // (pv_done's phases are the steps)
+  for (uint32_t step = 0;; ++step) {
     if (!wait_step(tp, c, step, kRoleScore)) return;
     const TcStep& s = c->steps[step % kTcSteps];
     if (s.groups == 0) return;
@@ -996,7 +1041,7 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
       }
     }
     if (__any_sync(0xffffffffu, scale_o != 1.f) && run_pv > 0) {
-      if (!tc_wait(tp, c, &c->pv_done[t], (step - 1) & 1, kRoleScore, 2)) return;
+      if (!wait_pv(step - 1, 2)) return;
       tc_fence_after();
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
@@ -1018,7 +1063,7 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
       continue;
     }
     // ---- the row's result, or its part of it
-    if (!tc_wait(tp, c, &c->pv_done[t], step & 1, kRoleScore, 3)) return;
+    if (!wait_pv(step, 3)) return;
     tc_fence_after();
     const int b = s.b, head = s.hkv * G + (row < rows ? row : 0) / p.T;
     const bool there = pos >= 0;  // else an empty row, whatever it gathered
@@ -1106,7 +1151,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&c->kv_full[i], 4);
-      mbar_init(&c->kv_empty[i], 1);
+      mbar_init(&c->kv_empty[i], 2);  // two tiles of rows
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c->q_full[i], kTcRows);
@@ -1114,8 +1159,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&c->p_full[i], kTcRows);
       mbar_init(&c->pv_done[i], 1);
       mbar_init(&c->o_free[i], kTcRows);
+      mbar_init(&c->mma_done[i], 1);
     }
-    mbar_init(&c->mma_done, 1);
     c->abort = 0;
     c->nan_step[0] = c->nan_step[1] = 0;
     fence_mbar_init();
@@ -1131,10 +1176,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (wg == 0) {
     if (warp == 0)
       plan_role<D, R>(t, c);
-    else if (warp == 1)
-      mma_role<D, R>(t, c, base, tmem);
+    else if (warp == 3)
+      load_role<D, R>(t, c, base + C::kOffCodes);
     else
-      load_role<D, R>(t, c, base + C::kOffCodes, warp - 2);
+      mma_role<D, R>(t, c, base, tmem, warp - 1);
   } else if (wg == 1 || (R == 1 && wg == 3)) {
     convert_role<D, R>(t, c, base + C::kOffKv, base + C::kOffCodes, wg >> 1);
   } else {
