@@ -20,11 +20,11 @@
 //   warp 3      starts the copies of the codes, up to two steps ahead of their
 //               conversion.
 //   warps 1, 2  issue the MMAs (warp 1 owns the 512 TMEM columns).
-//   converters  warpgroup 1, and with one tile of rows warpgroup 3 as well (one
-//               takes the keys then, the other the values).
-//   score       warpgroup 2 (and 3 with two tiles): one thread per query row,
-//               its TMEM lane: mask, running maximum, exponentials, P back to
-//               TMEM over S, and at a run's end the row's result.
+//   converter   warpgroup 1.
+//   score       warpgroups 2 and 3: one thread per query row, its TMEM lane, or
+//               with one tile two, each with half of the columns: mask, running
+//               maximum, exponentials, P back to TMEM over S, and at a run's
+//               end the row's result.
 // The roles' loops are kept short, one copy of each and 32 columns of a row at
 // a time: together they must stay in the SM's instruction cache.  (With 128
 // columns unrolled and codes on their way in registers, a third of all
@@ -75,23 +75,22 @@ template <int D, int R>
 struct TcCfg {
   static constexpr int kTile = kTcTokens * D * 2;  // Q, K or V in f16
   static constexpr int kCodes = kTcTokens * D;     // K or V in e4m3
-  // Rings of tiles and of codes, by half steps h: 2 step (keys), 2 step + 1
-  // (values).  One converter fills them in turn; of two, which may be steps
-  // apart, each has its own slots, so that a slot's phases are waited for in
-  // order: two for the keys' tiles, as S goes ahead, one for the values'.
-  static constexpr int kSlots = 3, kStages = R == 1 ? 4 : 3;
-  static __device__ __forceinline__ uint32_t slot(uint32_t h) {
-    return R == 2 ? h % 3 : h % 2 ? 2 : h / 2 % 2;
-  }
+  // Rings of tiles and of codes, by half steps: 2 step (keys), 2 step + 1
+  // (values); 208 KB with Q at D = 128.
+  static constexpr int kSlots = 3, kStages = R == 1 ? 5 : 3;
+  static __device__ __forceinline__ uint32_t slot(uint32_t h) { return h % 3; }
   static __device__ __forceinline__ uint32_t slot_use(uint32_t h) {
-    return R == 2 ? h / 3 : h % 2 ? h / 2 : h / 4;
+    return h / 3;
   }
   static __device__ __forceinline__ uint32_t stage(uint32_t h) {
-    return R == 2 ? h % 3 : h % 4;
+    return h % kStages;
   }
   static __device__ __forceinline__ uint32_t stage_use(uint32_t h) {
-    return R == 2 ? h / 3 : h / 4;
+    return h / kStages;
   }
+  // threads that share a row: with one tile the two score warpgroups take half
+  // of its columns each
+  static constexpr int kRowThreads = R == 1 ? 2 : 1;
   static constexpr int kOffKv = R * kTile;
   static constexpr int kOffCodes = kOffKv + kSlots * kTile;
   static constexpr int kOffCtl = kOffCodes + kStages * kCodes;
@@ -133,6 +132,10 @@ struct TcCtl {
   int32_t pos[2][kTcTokens];
   uint16_t nan[2][kTcTokens][8];
   uint32_t nan_step[2];
+  // one tile of rows: what a row's two threads tell each other, [half][row]
+  uint64_t meet[4];  // by TMEM lane quarter
+  float pair[2][2][kTcRows];
+  uint32_t pair_nan[2][4][kTcRows];
 };
 
 struct TcParams {
@@ -497,14 +500,12 @@ __device__ __forceinline__ void store_codes(const uint32_t w[4], uint32_t a,
          e4m3x2_to_f16x2(w[3]), e4m3x2_to_f16x2_hi(w[3]));
 }
 
-// A converter warpgroup: with one tile of rows the keys (which = 0) or the
-// values (1) of every step, with two tiles both in turn.  Tiles are rows of 64
-// elements (128 bytes) per token, two such blocks at D = 128, in the 128-byte
+// The converter warpgroup: every step's keys, then its values.  Tiles are rows of
+// 64 elements (128 bytes) per token, two such blocks at D = 128, in the 128-byte
 // swizzle.
 template <int D, int R>
 __device__ __forceinline__ void convert_role(const TcParams& t, TcCtl* c,
-                                             uint32_t kv, uint32_t codes,
-                                             int which) {
+                                             uint32_t kv, uint32_t codes) {
   using C = TcCfg<D, R>;
   const PagedParams& p = t.p;
   const int i = threadIdx.x % 128, piece = piece_of<D>(i);
@@ -515,7 +516,7 @@ __device__ __forceinline__ void convert_role(const TcParams& t, TcCtl* c,
   const uint32_t from = codes + row * D + piece * 16;
   constexpr int kRows = 2048 / D;  // tokens of the warpgroup at a time
 #pragma unroll 1
-  for (uint32_t h = which;; h += R == 1 ? 2 : 1) {
+  for (uint32_t h = 0;; ++h) {
     const uint32_t step = h / 2;
     const bool values = h % 2 != 0;
     if (!wait_step(t, c, step, kRoleConvert)) return;
@@ -523,17 +524,10 @@ __device__ __forceinline__ void convert_role(const TcParams& t, TcCtl* c,
     const int tokens = s.groups * kPaGroup;
     if (tokens == 0) return;
     const uint32_t st = C::stage(h), slot = C::slot(h);
-    // the tile is free again when the MMA that read it is done: with one tile
-    // of rows S of the step before the last, or P V of the step before
-    uint64_t* free_at = &c->kv_empty[slot];
-    uint32_t uses = C::slot_use(h);
-    if (R == 1 && step > 0) {
-      free_at = values ? &c->pv_done[(step - 1) & 1] : &c->s_full[step & 1];
-      uses = values ? ((step - 1) >> 1) + 1 : step >> 1;
-    }
     if (!tc_wait(t, c, &c->code_full[st], C::stage_use(h) & 1, kRoleConvert,
                  0) ||
-        !tc_wait(t, c, free_at, (uses & 1) ^ 1, kRoleConvert, 1))
+        !tc_wait(t, c, &c->kv_empty[slot], (C::slot_use(h) & 1) ^ 1,
+                 kRoleConvert, 1))
       return;
     const bool plain = s.plain != 0;
     const uint32_t src = from + st * C::kCodes;
@@ -568,7 +562,7 @@ __device__ __forceinline__ void convert_role(const TcParams& t, TcCtl* c,
     if (threadIdx.x % 32 == 0) {
       mbar_arrive(&c->code_empty[st]);
       mbar_arrive(&c->kv_full[slot]);
-      if (R == 1 || values) mbar_arrive(&c->step_empty[step % kTcSteps]);
+      if (values) mbar_arrive(&c->step_empty[step % kTcSteps]);
     }
   }
 }
@@ -662,9 +656,11 @@ __device__ __forceinline__ void mma_role(const TcParams& t, TcCtl* c,
       if (w == 0) {
         issue_s<D>(s_acc, dq, dk + C::slot(h) * kUnits, groups);
         mma_commit_elect(&c->s_full[buf]);
+        mma_commit_elect(&c->kv_empty[C::slot(h)]);
       } else {
         issue_pv<D>(o_acc, s_acc, dv + C::slot(h) * kUnits, groups, first);
         mma_commit_elect(&c->pv_done[buf]);
+        mma_commit_elect(&c->kv_empty[C::slot(h)]);
       }
     } else {
       const uint32_t s_acc = tmem + tile * 128;
@@ -710,9 +706,11 @@ __device__ __forceinline__ void mma_role(const TcParams& t, TcCtl* c,
 // A row's query into its tile: f16, scaled so that the row's largest magnitude
 // becomes [1, 2) (f16 then keeps bf16's 8 bits of every element above 2^-17 of
 // it, and 2^-25 of it of the rest).  Returns the factor that undoes it.
+// (Pieces [i0, i1) of 8 elements are stored.)
 template <int D>
-__device__ __forceinline__ float load_query(const uint16_t* src, bool live,
-                                            bool negate, uint32_t tile, int r) {
+__device__ __noinline__ float load_query(const uint16_t* src, bool live,
+                                         bool negate, uint32_t tile, int r,
+                                         int i0, int i1) {
   uint32_t w[D / 2];
   uint32_t top = 0;
 #pragma unroll
@@ -732,6 +730,7 @@ __device__ __forceinline__ float load_query(const uint16_t* src, bool live,
   const float down = negate ? -pow2(-e) : pow2(-e);
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) {
+    if (i < i0 || i >= i1) continue;
     uint32_t h[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -863,48 +862,159 @@ __device__ __forceinline__ float weigh(const float* x, const float* f,
   return sum;
 }
 
+// The scores of a step that its scales alone do not give (32-column pieces [q0,
+// q1)), written back as they are to be weighed; returns the largest.  Out of
+// line, as most steps are plain and the score loop is to stay short.
+template <int D>
+struct NanPlaces {  // dims in which a row sees a NaN value
+  uint32_t w[D / 32];
+};
+
+template <int D, bool MOD>
+__device__ __noinline__ float modified_scores(const PagedParams& p, TcCtl* c,
+                                              const TcStep& s, uint32_t step,
+                                              uint32_t s_addr, int q0, int q1,
+                                              float q_mul, float slope2,
+                                              int pos, int tq,
+                                              NanPlaces<D>* nans) {
+  const float NEG_INF = __int_as_float(0xff800000);
+  const bool plain = s.plain != 0;
+  const bool capped = MOD && (p.mod.kind & kModCap);
+  const bool biased = MOD && (p.mod.kind & kModBias);
+  float top = NEG_INF;
+#pragma unroll 1
+  for (int q = q0; q < q1; ++q) {
+    uint32_t keep = ~0u;
+    if (!plain) {
+      keep = pos >= 0 ? visible(p, s, q, tq) : 0u;
+      const int* at = c->pos[step % 2] + 32 * q;
+      if (p.window > 0)
+#pragma unroll 1
+        for (int j = 0; j < 32; ++j)
+          if (pos - at[j] >= p.window) keep &= ~(1u << j);
+      if (c->nan_step[step % 2] == step + 1) {
+        // values that are NaN: a row that sees one has NaN in that place
+#pragma unroll 1
+        for (uint32_t k = keep; k != 0; k &= k - 1) {
+          const uint16_t* n = c->nan[step % 2][32 * q + __ffs(k) - 1];
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+            nans->w[i] |= *reinterpret_cast<const uint32_t*>(n + 2 * i);
+        }
+      }
+    }
+    float x[32];
+    tmem_ld32(s_addr + q * 32, reinterpret_cast<uint32_t*>(x));
+    tmem_ld_wait();
+    const float f0 = q_mul * s.k_scale[2 * q];
+    const float f1 = q_mul * s.k_scale[2 * q + 1];
+#pragma unroll
+    for (int j = 0; j < 32; j += 2)
+      fmul2(x[j], x[j + 1], x[j], x[j + 1], j < 16 ? f0 : f1);
+    if (MOD) {
+      // columns that are not seen may hold anything; 0 costs the cap
+      // nothing
+      if (!plain)
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (!(keep >> j & 1u)) x[j] = 0.f;
+      if (capped) cap_scores(p.mod, x);
+      if (biased && plain) {
+        const float d0 = static_cast<float>(s.tok0 + 32 * q - pos);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          x[j] = fmaf(slope2, d0 + static_cast<float>(j), x[j]);
+      } else if (biased) {
+        const int* at = c->pos[step % 2] + 32 * q;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          x[j] = fmaf(-slope2, fabsf(static_cast<float>(pos - at[j])),
+                      x[j]);
+      }
+    }
+    if (!plain)
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (!(keep >> j & 1u)) x[j] = NEG_INF;
+    top = fmaxf(top, max_of(x, 1.f, 1.f));
+    tmem_st32(s_addr + q * 32, reinterpret_cast<uint32_t*>(x));
+  }
+  tmem_st_wait();
+  return top;
+}
+
+// The rows' warpgroups: one of each tile, or, with one tile, one of each half of
+// a step's columns (and of O's): a row's two threads then tell each other their
+// maxima.
 template <int D, int R, bool MOD>
 __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
                                            uint32_t smem, uint32_t tmem,
-                                           const int t) {
+                                           const int w) {
   using C = TcCfg<D, R>;
   const PagedParams& p = tp.p;
+  const int tile = R == 2 ? w : 0, half = R == 1 ? w : 0;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int quarter = warp % 4;
   const int r = quarter * 32 + lane;
   const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-  const uint32_t o_addr = tmem + lane_off + 256 + t * 128;
+  constexpr int kDims = D / C::kRowThreads;  // of O that a thread scales, writes
+  const uint32_t o_addr = tmem + lane_off + 256 + tile * 128 + half * kDims;
   const float NEG_INF = __int_as_float(0xff800000);
   const int G = p.H / p.H_kv, rows = G * p.T;
   const bool capped = MOD && (p.mod.kind & kModCap);
   const bool biased = MOD && (p.mod.kind & kModBias);
   const bool negate = !capped && p.scale_x < 0.f;
+  uint32_t meets = 0;
+  // Tells the row's other thread x, and the NaN places if any are given, and
+  // waits for its.
+  auto exchange = [&](float& x, const NanPlaces<D>* nans, float* other) {
+    c->pair[meets & 1][half][r] = x;
+    if (nans != nullptr)
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) c->pair_nan[half][i][r] = nans->w[i];
+    warp_arrive(&c->meet[quarter]);
+    const bool ok =
+        tc_wait(tp, c, &c->meet[quarter], meets & 1, kRoleScore, 6);
+    *other = c->pair[meets & 1][half ^ 1][r];
+    ++meets;
+    return ok;
+  };
+  auto wait_pv = [&](uint32_t step, int phase) {  // a step's P V is done
+    return R == 2
+               ? tc_wait(tp, c, &c->pv_done[tile], step & 1, kRoleScore, phase)
+               : tc_wait(tp, c, &c->pv_done[step & 1], step >> 1 & 1,
+                         kRoleScore, phase);
+  };
+  // the run's query into its tile; the tile's S before must be done
+  auto start_query = [&](const TcStep& s) {
+    const int at = s.row0 + tile * kTcRows + r;
+    const bool live = at < rows;
+    const int head = s.hkv * G + (live ? at / p.T : 0);
+    const float up = load_query<D>(
+        p.q + s.b * p.q_sb + head * p.q_sh + (live ? at % p.T : 0) * p.q_ss,
+        live, negate, smem + tile * C::kTile, r, half * (kDims / 8),
+        (half + 1) * (kDims / 8));
+    fence_proxy_async();
+    mbar_arrive(&c->q_full[tile]);
+    return up;
+  };
   // of the run
   float q_mul = 0.f, slope2 = 0.f, m_used = NEG_INF, l_sum = 0.f, ref = 1.f;
   int row = 0, tq = 0, pos = -1;
-  uint32_t nans[D / 32];
+  NanPlaces<D> nans;
   uint32_t run_pv = 0;
-  auto wait_pv = [&](uint32_t step, int phase) {  // a step's P V is done
-    return R == 2 ? tc_wait(tp, c, &c->pv_done[t], step & 1, kRoleScore, phase)
-                  : tc_wait(tp, c, &c->pv_done[step & 1], step >> 1 & 1,
-                            kRoleScore, phase);
-  };
+  float up = 0.f;  // of the next run's query, which is loaded ahead
 #pragma unroll 1
   for (uint32_t step = 0;; ++step) {
     if (!wait_step(tp, c, step, kRoleScore)) return;
     const TcStep& s = c->steps[step % kTcSteps];
     if (s.groups == 0) return;
     if (s.first) {
-      row = s.row0 + t * kTcRows + r;
+      if (step == 0) up = start_query(s);
+      row = s.row0 + tile * kTcRows + r;
       const bool live = row < rows;
-      const int at = live ? row : 0;
-      const int head = s.hkv * G + at / p.T;
-      tq = at % p.T;
-      const float up = load_query<D>(
-          p.q + s.b * p.q_sb + head * p.q_sh + tq * p.q_ss, live, negate,
-          smem + t * C::kTile, r);
-      fence_proxy_async();
-      mbar_arrive(&c->q_full[t]);
+      tq = live ? row % p.T : 0;
+      const int head = s.hkv * G + (live ? row / p.T : 0);
       // with a cap: to S itself; else to log2 units
       q_mul = capped ? up : up * fabsf(p.scale_x);
       slope2 = biased ? p.mod.slopes[head] * 1.4426950408889634f : 0.f;
@@ -916,9 +1026,9 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
       ref = s.v_ref;
       run_pv = 0;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) nans[i] = 0u;
+      for (int i = 0; i < D / 32; ++i) nans.w[i] = 0u;
     }
-    const int buf = R == 2 ? t : static_cast<int>(step & 1);
+    const int buf = R == 2 ? tile : static_cast<int>(step & 1);
     const uint32_t use = R == 2 ? step : step >> 1;
     const uint32_t s_addr = tmem + lane_off + buf * 128;
     const bool plain = s.plain != 0;
@@ -932,77 +1042,42 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
     tc_fence_after();
     // ---- the largest score.  Scores that the scales alone do not give are
     // written back as they are to be weighed.
+    const bool scaled = MOD || !plain;
     float top = NEG_INF;
-    if (!MOD && plain) {
+    if (scaled)
+      top = modified_scores<D, MOD>(p, c, s, step, s_addr, 2 * half,
+                                    R == 1 ? 2 * half + 2 : 4, q_mul, slope2,
+                                    pos, tq, &nans);
+    float xa[32], xb[32];
+    float f[4];  // the scales of xa's and xb's groups
+    auto load_scales = [&](int q) {
+      const float4 ks = *reinterpret_cast<const float4*>(&s.k_scale[2 * q]);
+      f[0] = scaled ? 1.f : ks.x * q_mul, f[1] = scaled ? 1.f : ks.y * q_mul;
+      f[2] = scaled ? 1.f : ks.z * q_mul, f[3] = scaled ? 1.f : ks.w * q_mul;
+    };
+    if (R == 1) {  // this thread's columns stay in registers
+      const uint32_t at = s_addr + half * 64;
+      tmem_ld32(at, reinterpret_cast<uint32_t*>(xa));
+      tmem_ld32(at + 32, reinterpret_cast<uint32_t*>(xb));
+      load_scales(2 * half);
+      tmem_ld_wait();
+      if (!scaled)
+        top = fmaxf(max_of(xa, f[0], f[1]), max_of(xb, f[2], f[3]));
+      // (and P may now be written over all of S)
+      tc_fence_before();
+      float other;
+      if (!exchange(top, nullptr, &other)) return;
+      tc_fence_after();
+      top = fmaxf(top, other);
+    } else if (!scaled) {
 #pragma unroll 1
       for (int q = 0; q < 4; q += 2) {
-        float x[64];
-        tmem_ld32(s_addr + q * 32, reinterpret_cast<uint32_t*>(x));
-        tmem_ld32(s_addr + q * 32 + 32, reinterpret_cast<uint32_t*>(x + 32));
-        const float4 ks = *reinterpret_cast<const float4*>(&s.k_scale[2 * q]);
+        tmem_ld32(s_addr + q * 32, reinterpret_cast<uint32_t*>(xa));
+        tmem_ld32(s_addr + q * 32 + 32, reinterpret_cast<uint32_t*>(xb));
+        load_scales(q);
         tmem_ld_wait();
-        top = fmax3(top, max_of(x, ks.x, ks.y) * q_mul,
-                    max_of(x + 32, ks.z, ks.w) * q_mul);
+        top = fmax3(top, max_of(xa, f[0], f[1]), max_of(xb, f[2], f[3]));
       }
-    } else {
-#pragma unroll 1
-      for (int q = 0; q < kTcTokens / 32; ++q) {
-        uint32_t keep = ~0u;
-        if (!plain) {
-          keep = pos >= 0 ? visible(p, s, q, tq) : 0u;
-          const int* at = c->pos[step % 2] + 32 * q;
-          if (p.window > 0)
-#pragma unroll 1
-            for (int j = 0; j < 32; ++j)
-              if (pos - at[j] >= p.window) keep &= ~(1u << j);
-          if (c->nan_step[step % 2] == step + 1) {
-            // values that are NaN: a row that sees one has NaN in that place
-#pragma unroll 1
-            for (uint32_t k = keep; k != 0; k &= k - 1) {
-              const uint16_t* n = c->nan[step % 2][32 * q + __ffs(k) - 1];
-#pragma unroll
-              for (int i = 0; i < D / 32; ++i)
-                nans[i] |= *reinterpret_cast<const uint32_t*>(n + 2 * i);
-            }
-          }
-        }
-        float x[32];
-        tmem_ld32(s_addr + q * 32, reinterpret_cast<uint32_t*>(x));
-        tmem_ld_wait();
-        const float f0 = q_mul * s.k_scale[2 * q];
-        const float f1 = q_mul * s.k_scale[2 * q + 1];
-#pragma unroll
-        for (int j = 0; j < 32; j += 2)
-          fmul2(x[j], x[j + 1], x[j], x[j + 1], j < 16 ? f0 : f1);
-        if (MOD) {
-          // columns that are not seen may hold anything; 0 costs the cap
-          // nothing
-          if (!plain)
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!(keep >> j & 1u)) x[j] = 0.f;
-          if (capped) cap_scores(p.mod, x);
-          if (biased && plain) {
-            const float d0 = static_cast<float>(s.tok0 + 32 * q - pos);
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              x[j] = fmaf(slope2, d0 + static_cast<float>(j), x[j]);
-          } else if (biased) {
-            const int* at = c->pos[step % 2] + 32 * q;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              x[j] = fmaf(-slope2, fabsf(static_cast<float>(pos - at[j])),
-                          x[j]);
-          }
-        }
-        if (!plain)
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (!(keep >> j & 1u)) x[j] = NEG_INF;
-        top = fmaxf(top, max_of(x, 1.f, 1.f));
-        tmem_st32(s_addr + q * 32, reinterpret_cast<uint32_t*>(x));
-      }
-      tmem_st_wait();
     }
     float scale_o = 1.f;
     if (top > m_used + kTcRescaleLog2) {
@@ -1015,36 +1090,34 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
       scale_o *= ref / s.v_ref;
       ref = s.v_ref;
     }
-    // ---- P; 2^9 goes along with it and the sums.  The next 32 columns are on
-    // their way while 32 are weighed (P's columns lie before theirs)
+    // ---- P; 2^9 goes along with it and the sums
     const float add = m_used == NEG_INF ? kTcUpLog2 : kTcUpLog2 - m_used;
-    const float fq = MOD || !plain ? 1.f : q_mul;
-    {
-      float x[32], next[32];
-      tmem_ld32(s_addr, reinterpret_cast<uint32_t*>(x));
-      tmem_ld_wait();
+    auto weigh64 = [&](int q) {  // xa, xb: pieces q, q + 1
+      const float4 vl = *reinterpret_cast<const float4*>(&s.v_log2[2 * q]);
+      const float4 vi = *reinterpret_cast<const float4*>(&s.v_inv[2 * q]);
+      const float a[4] = {add + vl.x, add + vl.y, add + vl.z, add + vl.w};
+      const float i[4] = {vi.x, vi.y, vi.z, vi.w};
+      l_sum += weigh(xa, f, a, i, s_addr + q * 16);
+      l_sum += weigh(xb, f + 2, a + 2, i + 2, s_addr + q * 16 + 16);
+    };
+    if (R == 1) {
+      weigh64(2 * half);
+    } else {
+      // (P's columns lie before the next ones to be read)
 #pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        // (the last turn loads the last columns again)
-        tmem_ld32(s_addr + min(q + 1, 3) * 32,
-                  reinterpret_cast<uint32_t*>(next));
-        const float2 ks = *reinterpret_cast<const float2*>(&s.k_scale[2 * q]);
-        const float2 vl = *reinterpret_cast<const float2*>(&s.v_log2[2 * q]);
-        const float2 vi = *reinterpret_cast<const float2*>(&s.v_inv[2 * q]);
-        const float f[2] = {MOD || !plain ? 1.f : ks.x * fq,
-                            MOD || !plain ? 1.f : ks.y * fq};
-        const float a[2] = {add + vl.x, add + vl.y}, i[2] = {vi.x, vi.y};
-        l_sum += weigh(x, f, a, i, s_addr + q * 16);
+      for (int q = 0; q < 4; q += 2) {
+        tmem_ld32(s_addr + q * 32, reinterpret_cast<uint32_t*>(xa));
+        tmem_ld32(s_addr + q * 32 + 32, reinterpret_cast<uint32_t*>(xb));
+        load_scales(q);
         tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = next[j];
+        weigh64(q);
       }
     }
     if (__any_sync(0xffffffffu, scale_o != 1.f) && run_pv > 0) {
       if (!wait_pv(step - 1, 2)) return;
       tc_fence_after();
 #pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
+      for (int q = 0; q < kDims / 32; ++q) {
         uint32_t o[32];
         tmem_ld32(o_addr + q * 32, o);
         tmem_ld_wait();
@@ -1062,44 +1135,55 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
       warp_arrive(&c->step_empty[step % kTcSteps]);
       continue;
     }
-    // ---- the row's result, or its part of it
+    // ---- the row's result, or its part of it; the next run's query first, as
+    // its S may then go ahead
+    const int b = s.b, head = s.hkv * G + (row < rows ? row : 0) / p.T;
+    const int part_at = s.part;
+    warp_arrive(&c->step_empty[step % kTcSteps]);
+    if (!wait_step(tp, c, step + 1, kRoleScore)) return;
+    if (c->steps[(step + 1) % kTcSteps].groups != 0)
+      up = start_query(c->steps[(step + 1) % kTcSteps]);
+    const bool there = pos >= 0;  // else an empty row, whatever it gathered
+    float sum = there ? l_sum * pow2(-static_cast<int>(kTcUpLog2)) : 0.f;
+    if (R == 1) {
+      float other;
+      if (!exchange(sum, &nans, &other)) return;
+      sum += other;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) nans.w[i] |= c->pair_nan[half ^ 1][i][r];
+    }
     if (!wait_pv(step, 3)) return;
     tc_fence_after();
-    const int b = s.b, head = s.hkv * G + (row < rows ? row : 0) / p.T;
-    const bool there = pos >= 0;  // else an empty row, whatever it gathered
-    if (!there) l_sum = 0.f;
-    const float unit = there ? ref * pow2(-static_cast<int>(kTcUpLog2)) : 0.f;
-    const float sum = l_sum * pow2(-static_cast<int>(kTcUpLog2));
+    const float unit = ref * pow2(-static_cast<int>(kTcUpLog2));
     const float inv = sum != 0.f ? 1.f / sum : 0.f;
     constexpr int kPartRows = R * kTcRows;
-    float* part = s.part < 0 ? nullptr
-                             : p.parts + static_cast<int64_t>(s.part) *
-                                             (kPartRows * (D + 2));
-    const int in_part = t * kTcRows + r;
+    float* part = part_at < 0 ? nullptr
+                              : p.parts + static_cast<int64_t>(part_at) *
+                                              (kPartRows * (D + 2));
+    const int in_part = tile * kTcRows + r;
 #pragma unroll 1
-    for (int q = 0; q < D / 32; ++q) {
-      uint32_t raw_o[32];
-      tmem_ld32(o_addr + q * 32, raw_o);
+    for (int q = 0; q < kDims / 32; ++q) {
+      const int dim = half * kDims + q * 32;
+      float o[32];
+      tmem_ld32(o_addr + q * 32, reinterpret_cast<uint32_t*>(o));
       tmem_ld_wait();
       uint32_t nan = 0;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) nan = i == q ? nans[i] : nan;
-      float* o = reinterpret_cast<float*>(raw_o);
+      for (int i = 0; i < D / 32; ++i) nan = i * 32 == dim ? nans.w[i] : nan;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        o[j] = there ? o[j] * unit : 0.f;
-        if (nan >> j & 1u) o[j] = __int_as_float(0x7fffffff);
-      }
+      for (int j = 0; j < 32; ++j) o[j] = there ? o[j] * unit : 0.f;
+      if (nan != 0)
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (nan >> j & 1u) o[j] = __int_as_float(0x7fffffff);
       if (row >= rows) continue;
-      if (part != nullptr) {
-        float* dst = part + in_part * D + q * 32;
+      if (part != nullptr) {  // [dim][row]: a warp's rows lie side by side
+        float* dst = part + dim * kPartRows + in_part;
 #pragma unroll
-        for (int j = 0; j < 32; j += 4)
-          *reinterpret_cast<float4*>(dst + j) =
-              make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+        for (int j = 0; j < 32; ++j) dst[j * kPartRows] = o[j];
       } else {
-        uint16_t* dst = p.out + b * p.o_sb + head * p.o_sh + tq * p.o_ss +
-                        q * 32;
+        uint16_t* dst =
+            p.out + b * p.o_sb + head * p.o_sh + tq * p.o_ss + dim;
 #pragma unroll
         for (int j = 0; j < 32; j += 8)
           st_global_v4(dst + j, pack_bf16x2(o[j] * inv, o[j + 1] * inv),
@@ -1109,8 +1193,8 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
       }
     }
     tc_fence_before();
-    mbar_arrive(&c->o_free[t]);
-    if (row < rows) {
+    mbar_arrive(&c->o_free[tile]);
+    if (row < rows && half == 0) {
       // (a row without a key in this part: the join's lowest reference)
       const float base = there && m_used != NEG_INF
                              ? m_used
@@ -1123,8 +1207,107 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
             sum != 0.f ? (base + log2f(sum)) * 0.6931471805599453f : NEG_INF;
       }
     }
-    warp_arrive(&c->step_empty[step % kTcSteps]);
   }
+}
+
+// Joins the parts of items that were cut, and writes the rows of sequences
+// without drafts: 32 rows per block, a lane each, a quarter of the dims per
+// warp.  Parts lie [dim][row], so a warp reads its rows' elements of a dim at
+// once.  The weights of up to kJoinParts parts are worked out first, so that the
+// parts' loads wait for nothing.
+constexpr int kJoinParts = 32;
+
+template <int D, int R>
+__global__ void __launch_bounds__(128)
+    tree_join_kernel(const PagedParams p, const int grid) {
+  using X = TcDeal;
+  constexpr int kRows = R * kTcRows, kPer = D / 4;
+  __shared__ float weight[kJoinParts][32], total[32];
+  const int rows = p.H / p.H_kv * p.T;
+  const int tiles = (rows + kRows - 1) / kRows;
+  const int per = p.H_kv * tiles;
+  const int b = blockIdx.z, item = blockIdx.y;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int r = blockIdx.x * 32 + lane;
+  const int rr = item % tiles * kRows + r;
+  const PaScan scan = scan_before<X>(p, b);
+  const int64_t units = scan.all * per;
+  const int n = plan_of<X>(p, b).n_units;
+  // every block waits for the attention grid, so that work after this kernel
+  // on the stream sees what that grid wrote itself
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int64_t c0 = 0, c1 = -1;
+  if (n > 0) {
+    const int64_t busy = busy_ctas<X>(units, grid);
+    // the CTAs that hold its first and last unit
+    const int64_t u0 = scan.before * per +
+                       static_cast<int64_t>(item) * (n + X::kRunCost) +
+                       X::kRunCost;
+    auto cta_of = [&](int64_t u) {  // the last c with c * units / busy <= u
+      const int64_t c = mul_div(u + 1, busy, units);
+      return c - (c * units == (u + 1) * busy);
+    };
+    c0 = cta_of(u0), c1 = cta_of(u0 + n - 1);
+    if (c0 == c1) return;  // whole in one CTA, which wrote it
+  }
+  const bool live = rr < rows && r < kRows;
+  constexpr int64_t kPart = kRows * (D + 2);
+  // the first CTA leaves its part in slot 1
+  auto part_of = [&](int64_t c) {
+    return p.parts + (c * 2 + (c == c0 ? 1 : 0)) * kPart + (live ? r : 0);
+  };
+  float base = __int_as_float(0xff7fffff);  // as every part's before a key
+#pragma unroll 4
+  for (int64_t c = c0 + warp; c <= c1; c += 4)
+    base = fmaxf(base, part_of(c)[kRows * D]);
+  weight[warp][lane] = base;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) base = fmaxf(base, weight[i][lane]);
+  float sum = 0.f, x[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) x[i] = 0.f;
+  for (int64_t first = c0; first <= c1; first += kJoinParts) {
+    const int m = static_cast<int>(
+        min(c1 - first + 1, static_cast<int64_t>(kJoinParts)));
+    __syncthreads();
+#pragma unroll 4
+    for (int i = warp; i < m; i += 4) {
+      const float* part = part_of(first + i) + kRows * D;
+      const float f = ex2_approx(part[0] - base);
+      weight[i][lane] = f;
+      sum = fmaf(part[kRows], f, sum);
+    }
+    __syncthreads();
+#pragma unroll 2
+    for (int j = 0; j < m; ++j) {
+      const float* part = part_of(first + j) + warp * kPer * kRows;
+      const float f = weight[j][lane];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) x[i] = fmaf(part[i * kRows], f, x[i]);
+    }
+  }
+  // the warps' sums, in their order
+  for (int i = 0; i < 4; ++i) {
+    __syncthreads();
+    if (warp == i) total[lane] = i == 0 ? sum : total[lane] + sum;
+  }
+  __syncthreads();
+  sum = total[lane];
+  if (!live) return;
+  const int head = item / tiles * (p.H / p.H_kv) + rr / p.T, t = rr % p.T;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  uint16_t* dst = p.out + b * p.o_sb + head * p.o_sh + t * p.o_ss + warp * kPer;
+#pragma unroll
+  for (int i = 0; i < kPer; i += 8)
+    st_global_v4(dst + i, pack_bf16x2(x[i] * inv, x[i + 1] * inv),
+                 pack_bf16x2(x[i + 2] * inv, x[i + 3] * inv),
+                 pack_bf16x2(x[i + 4] * inv, x[i + 5] * inv),
+                 pack_bf16x2(x[i + 6] * inv, x[i + 7] * inv));
+  if (warp == 0 && p.lse != nullptr)
+    p.lse[(static_cast<int64_t>(b) * p.H + head) * p.T + t] =
+        sum != 0.f ? (base + log2f(sum)) * 0.6931471805599453f
+                   : __int_as_float(0xff800000);
 }
 
 template <int D, int R, bool MOD>
@@ -1139,7 +1322,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // the join kernel may be scheduled once every CTA here runs; it waits for
   // this grid's end before it reads the parts
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  constexpr int kConvertWarps = 4 * (3 - R), kScoreWarps = 4 * R;
+  constexpr int kConvertWarps = 4, kScoreWarps = 8;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kTcSteps; ++i) {
       mbar_init(&c->step_full[i], 1);
@@ -1151,16 +1334,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&c->kv_full[i], 4);
-      mbar_init(&c->kv_empty[i], 2);  // two tiles of rows
+      mbar_init(&c->kv_empty[i], R);  // MMAs that read a tile
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&c->q_full[i], kTcRows);
+      mbar_init(&c->q_full[i], kTcRows * C::kRowThreads);
       mbar_init(&c->s_full[i], 1);
-      mbar_init(&c->p_full[i], kTcRows);
+      mbar_init(&c->p_full[i], kTcRows * C::kRowThreads);
       mbar_init(&c->pv_done[i], 1);
-      mbar_init(&c->o_free[i], kTcRows);
+      mbar_init(&c->o_free[i], kTcRows * C::kRowThreads);
       mbar_init(&c->mma_done[i], 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&c->meet[i], 2);
     c->abort = 0;
     c->nan_step[0] = c->nan_step[1] = 0;
     fence_mbar_init();
@@ -1180,8 +1364,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       load_role<D, R>(t, c, base + C::kOffCodes);
     else
       mma_role<D, R>(t, c, base, tmem, warp - 1);
-  } else if (wg == 1 || (R == 1 && wg == 3)) {
-    convert_role<D, R>(t, c, base + C::kOffKv, base + C::kOffCodes, wg >> 1);
+  } else if (wg == 1) {
+    convert_role<D, R>(t, c, base + C::kOffKv, base + C::kOffCodes);
   } else {
     score_role<D, R, MOD>(t, c, base, tmem, wg - 2);
   }
@@ -1204,7 +1388,19 @@ cudaError_t launch_tc(const TcParams& t, int num_sms, cudaStream_t stream) {
   kern<<<num_sms, kTcThreads, smem, stream>>>(t);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_join<TcDeal, D, R * kTcRows>(t.p, num_sms, num_sms, stream);
+  const int rows = t.p.H / t.p.H_kv * t.p.T;
+  const int tiles = (rows + R * kTcRows - 1) / (R * kTcRows);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((min(rows, R * kTcRows) + 31) / 32, t.p.H_kv * tiles,
+                     t.p.B);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_join_kernel<D, R>, t.p, num_sms);
 }
 
 template <int D, int R>
