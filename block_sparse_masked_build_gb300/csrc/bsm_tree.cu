@@ -77,10 +77,14 @@ struct TcCfg {
   static constexpr int kCodes = kTcTokens * D;     // K or V in e4m3
   // Rings of tiles and of codes, by half steps: 2 step (keys), 2 step + 1
   // (values); 208 KB with Q at D = 128.
-  static constexpr int kSlots = 3, kStages = R == 1 ? 5 : 3;
-  static __device__ __forceinline__ uint32_t slot(uint32_t h) { return h % 3; }
+  // (With three tiles beside one of rows, keys would wait for the P V two steps
+  // back, and S could not go ahead.)
+  static constexpr int kSlots = R == 1 ? 4 : 3, kStages = 3;
+  static __device__ __forceinline__ uint32_t slot(uint32_t h) {
+    return h % kSlots;
+  }
   static __device__ __forceinline__ uint32_t slot_use(uint32_t h) {
-    return h / 3;
+    return h / kSlots;
   }
   static __device__ __forceinline__ uint32_t stage(uint32_t h) {
     return h % kStages;
@@ -118,8 +122,8 @@ static_assert(offsetof(TcStep, k_scale) % 16 == 0 && sizeof(TcStep) % 16 == 0,
 
 struct TcCtl {
   uint64_t step_full[kTcSteps], step_empty[kTcSteps];
-  uint64_t code_full[5], code_empty[5];
-  uint64_t kv_full[3], kv_empty[3];
+  uint64_t code_full[3], code_empty[3];
+  uint64_t kv_full[4], kv_empty[4];
   uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], o_free[2], mma_done[2];
   uint32_t tmem;
   int abort;
@@ -1211,24 +1215,25 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
 }
 
 // Joins the parts of items that were cut, and writes the rows of sequences
-// without drafts: 32 rows per block, a lane each, a quarter of the dims per
-// warp.  Parts lie [dim][row], so a warp reads its rows' elements of a dim at
-// once.  The weights of up to kJoinParts parts are worked out first, so that the
-// parts' loads wait for nothing.
-constexpr int kJoinParts = 32;
+// without drafts: 32 rows (a lane each) and 16 dims per block, whose warps share
+// the parts.  Parts lie [dim][row], so a warp reads its rows' elements of a dim
+// at once; all loads of a part are on their way together.
+constexpr int kJoinDims = 16, kJoinWarps = 4;
 
 template <int D, int R>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(32 * kJoinWarps)
     tree_join_kernel(const PagedParams p, const int grid) {
   using X = TcDeal;
-  constexpr int kRows = R * kTcRows, kPer = D / 4;
-  __shared__ float weight[kJoinParts][32], total[32];
+  constexpr int kRows = R * kTcRows;
+  __shared__ float top[kJoinWarps][32], total[kJoinWarps][32];
+  __shared__ float part_x[kJoinWarps][kJoinDims][32];
   const int rows = p.H / p.H_kv * p.T;
   const int tiles = (rows + kRows - 1) / kRows;
   const int per = p.H_kv * tiles;
   const int b = blockIdx.z, item = blockIdx.y;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int r = blockIdx.x * 32 + lane;
+  const int dim = blockIdx.x % (D / kJoinDims) * kJoinDims;
+  const int r = blockIdx.x / (D / kJoinDims) * 32 + lane;
   const int rr = item % tiles * kRows + r;
   const PaScan scan = scan_before<X>(p, b);
   const int64_t units = scan.all * per;
@@ -1256,57 +1261,58 @@ __global__ void __launch_bounds__(128)
   auto part_of = [&](int64_t c) {
     return p.parts + (c * 2 + (c == c0 ? 1 : 0)) * kPart + (live ? r : 0);
   };
+  // a running maximum over this warp's parts
   float base = __int_as_float(0xff7fffff);  // as every part's before a key
-#pragma unroll 4
-  for (int64_t c = c0 + warp; c <= c1; c += 4)
-    base = fmaxf(base, part_of(c)[kRows * D]);
-  weight[warp][lane] = base;
-  __syncthreads();
+  float sum = 0.f, x[kJoinDims];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) base = fmaxf(base, weight[i][lane]);
-  float sum = 0.f, x[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) x[i] = 0.f;
-  for (int64_t first = c0; first <= c1; first += kJoinParts) {
-    const int m = static_cast<int>(
-        min(c1 - first + 1, static_cast<int64_t>(kJoinParts)));
-    __syncthreads();
-#pragma unroll 4
-    for (int i = warp; i < m; i += 4) {
-      const float* part = part_of(first + i) + kRows * D;
-      const float f = ex2_approx(part[0] - base);
-      weight[i][lane] = f;
-      sum = fmaf(part[kRows], f, sum);
-    }
-    __syncthreads();
+  for (int i = 0; i < kJoinDims; ++i) x[i] = 0.f;
 #pragma unroll 2
-    for (int j = 0; j < m; ++j) {
-      const float* part = part_of(first + j) + warp * kPer * kRows;
-      const float f = weight[j][lane];
+  for (int64_t c = c0 + warp; c <= c1; c += kJoinWarps) {
+    const float* part = part_of(c);
+    float y[kJoinDims];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) x[i] = fmaf(part[i * kRows], f, x[i]);
-    }
+    for (int i = 0; i < kJoinDims; ++i) y[i] = part[(dim + i) * kRows];
+    const float m = part[kRows * D], l = part[kRows * D + kRows];
+    const float to = fmaxf(base, m);
+    const float f0 = ex2_approx(base - to), f1 = ex2_approx(m - to);
+    base = to;
+    sum = fmaf(l, f1, sum * f0);
+#pragma unroll
+    for (int i = 0; i < kJoinDims; ++i) x[i] = fmaf(y[i], f1, x[i] * f0);
   }
-  // the warps' sums, in their order
-  for (int i = 0; i < 4; ++i) {
-    __syncthreads();
-    if (warp == i) total[lane] = i == 0 ? sum : total[lane] + sum;
-  }
+  top[warp][lane] = base;
   __syncthreads();
-  sum = total[lane];
-  if (!live) return;
-  const int head = item / tiles * (p.H / p.H_kv) + rr / p.T, t = rr % p.T;
-  const float inv = sum != 0.f ? 1.f / sum : 0.f;
-  uint16_t* dst = p.out + b * p.o_sb + head * p.o_sh + t * p.o_ss + warp * kPer;
+  float all = base;
 #pragma unroll
-  for (int i = 0; i < kPer; i += 8)
-    st_global_v4(dst + i, pack_bf16x2(x[i] * inv, x[i + 1] * inv),
-                 pack_bf16x2(x[i + 2] * inv, x[i + 3] * inv),
-                 pack_bf16x2(x[i + 4] * inv, x[i + 5] * inv),
-                 pack_bf16x2(x[i + 6] * inv, x[i + 7] * inv));
-  if (warp == 0 && p.lse != nullptr)
+  for (int i = 0; i < kJoinWarps; ++i) all = fmaxf(all, top[i][lane]);
+  const float f = ex2_approx(base - all);
+  total[warp][lane] = sum * f;
+#pragma unroll
+  for (int i = 0; i < kJoinDims; ++i) part_x[warp][i][lane] = x[i] * f;
+  __syncthreads();
+  if (warp > 0 || !live) return;
+  sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kJoinWarps; ++i) sum += total[i][lane];
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int i = 0; i < kJoinDims; ++i) {
+    x[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) x[i] += part_x[w][i][lane];
+    x[i] *= inv;
+  }
+  const int head = item / tiles * (p.H / p.H_kv) + rr / p.T, t = rr % p.T;
+  uint16_t* dst = p.out + b * p.o_sb + head * p.o_sh + t * p.o_ss + dim;
+#pragma unroll
+  for (int i = 0; i < kJoinDims; i += 8)
+    st_global_v4(dst + i, pack_bf16x2(x[i], x[i + 1]),
+                 pack_bf16x2(x[i + 2], x[i + 3]),
+                 pack_bf16x2(x[i + 4], x[i + 5]),
+                 pack_bf16x2(x[i + 6], x[i + 7]));
+  if (dim == 0 && p.lse != nullptr)
     p.lse[(static_cast<int64_t>(b) * p.H + head) * p.T + t] =
-        sum != 0.f ? (base + log2f(sum)) * 0.6931471805599453f
+        sum != 0.f ? (all + log2f(sum)) * 0.6931471805599453f
                    : __int_as_float(0xff800000);
 }
 
@@ -1391,9 +1397,9 @@ cudaError_t launch_tc(const TcParams& t, int num_sms, cudaStream_t stream) {
   const int rows = t.p.H / t.p.H_kv * t.p.T;
   const int tiles = (rows + R * kTcRows - 1) / (R * kTcRows);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((min(rows, R * kTcRows) + 31) / 32, t.p.H_kv * tiles,
-                     t.p.B);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3((min(rows, R * kTcRows) + 31) / 32 * (D / kJoinDims),
+                     t.p.H_kv * tiles, t.p.B);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
