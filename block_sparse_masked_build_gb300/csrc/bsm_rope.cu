@@ -113,7 +113,7 @@ __device__ __forceinline__ void job_turns(const TurnParams& t,
                                           const LanePart& part, const Job& j,
                                           float* c, float* s) {
   if (MODE != kPlain && part.freq >= 0)
-    turns_of<8>(t.rope, steps, part.freq,
+    turns_of<8>(t.rope, steps + part.freq, part.freq,
                 t.pos == nullptr ? nullptr
                                  : t.pos + j.b * t.pos_sb + j.s * t.pos_ss,
                 t.pos_sa, j.s, c, s);

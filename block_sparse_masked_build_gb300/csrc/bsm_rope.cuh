@@ -23,7 +23,8 @@ __device__ __forceinline__ void turn_of(uint64_t step, int32_t position,
   __sincosf(a, s, c);
 }
 
-// Of N frequencies from f on; pos: the token's first axis.
+// Of N frequencies from f on, whose steps the caller holds; pos: the token's
+// first axis.
 template <int N>
 __device__ __forceinline__ void turns_of(const bsm_rope& rope,
                                          const uint64_t* steps, int f,
@@ -32,11 +33,11 @@ __device__ __forceinline__ void turns_of(const bsm_rope& rope,
   if (pos == nullptr || rope.axes == 1) {
     const int32_t at = pos == nullptr ? index : *pos;
 #pragma unroll
-    for (int i = 0; i < N; ++i) turn_of(steps[f + i], at, &c[i], &s[i]);
+    for (int i = 0; i < N; ++i) turn_of(steps[i], at, &c[i], &s[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      turn_of(steps[f + i], pos[rope.axis[f + i] * axis_stride], &c[i], &s[i]);
+      turn_of(steps[i], pos[rope.axis[f + i] * axis_stride], &c[i], &s[i]);
   }
 }
 

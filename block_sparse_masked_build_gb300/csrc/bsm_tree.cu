@@ -56,7 +56,10 @@ constexpr int kTcTokens = 128;  // of a full step
 constexpr int kTcGroups = kTcTokens / kPaGroup;
 constexpr int kTcSteps = 8;     // ring of steps
 constexpr uint32_t kTcTmem = 512;
-constexpr int kTreeFewRows = 16;  // see tree_tiles
+// Up to so many query rows per key/value head go to the kernel of single tokens,
+// which reads the cache once for each 16: 32 sequences of 300-12000 tokens with 8
+// rows took it 94 us (this one 167), with 16 142 (170), with 24 246 (172).
+constexpr int kTreeFewRows = 16;
 constexpr int kRolePlan = 1, kRoleMma = 2, kRoleConvert = 3, kRoleScore = 4,
               kRoleLoad = 5;
 // P is scaled by 2^9 before it becomes f16, whose smallest number is 2^-24: a
@@ -68,7 +71,7 @@ constexpr float kTcUpLog2 = 9.f, kTcRescaleLog2 = 6.f;
 // The deal: a unit is a full step.
 struct TcDeal {
   static constexpr bool kTree = true;
-  static constexpr int kUnit = kTcGroups, kRunCost = 3, kLeast = 1;
+  static constexpr int kUnit = kTcGroups, kRunCost = 6, kLeast = 1;
 };
 
 template <int D, int R>
@@ -190,6 +193,16 @@ __device__ __noinline__ bool tc_wait_at(uint32_t bar, uint32_t parity,
 __device__ __forceinline__ bool tc_wait(const TcParams& t, TcCtl* c,
                                         uint64_t* bar, uint32_t parity,
                                         int role, int phase) {
+  // (a call costs some 150 cycles: most phases are over already)
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  if (__all_sync(0xffffffffu, ok)) return true;
   return tc_wait_at(smem_u32(bar), parity, &c->abort, t.timeout_ns,
                     role * 16 + phase);
 }
@@ -233,6 +246,16 @@ __device__ __forceinline__ bool plan_run(const TcParams& t, TcCtl* c,
     return g >= g0 ? table[(plan.first_group + g) >> (p.page_shift - 4)] : -1;
   };
   int next_pid = page_of(g1);
+  // the run's query into L2, for the rows that will load it at its start
+  for (int i = lane; i < R * kTcRows; i += 32)
+    if (row0 + i < p.H / p.H_kv * p.T) {
+      const uint16_t* q = p.q + b * p.q_sb +
+                          (hkv * (p.H / p.H_kv) + (row0 + i) / p.T) * p.q_sh +
+                          (row0 + i) % p.T * p.q_ss;
+#pragma unroll
+      for (int j = 0; j < D; j += 64)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(q + j));
+    }
   float ref = 0.f, log2_ref = 0.f;  // 0: none yet
 #pragma unroll 1
   for (int top = g1; top > g0; top -= 32) {
@@ -712,7 +735,7 @@ __device__ __forceinline__ void mma_role(const TcParams& t, TcCtl* c,
 // it, and 2^-25 of it of the rest).  Returns the factor that undoes it.
 // (Pieces [i0, i1) of 8 elements are stored.)
 template <int D>
-__device__ __noinline__ float load_query(const uint16_t* src, bool live,
+__device__ __forceinline__ float load_query(const uint16_t* src, bool live,
                                          bool negate, uint32_t tile, int r,
                                          int i0, int i1) {
   uint32_t w[D / 2];
