@@ -198,18 +198,20 @@ __global__ void __launch_bounds__(kAppendThreads, NCH <= 8 ? 8 : 4)
 }
 
 // The same with the keys normalised and rotated first, in f32 from the load to
-// the rounding to e4m3.  A token's row lies in D / 8 neighbouring lanes, eight
-// elements each; the partner of a lane's elements is in the lane half a
-// rotation away (or, for neighbouring pairs, in the lane itself), which is the
-// one exchange beside the norm's sum.  A thread's pieces are all of one place
-// in the row, so it reads its weights and frequencies once.
+// the rounding to e4m3.  A token's row lies in D / 16 neighbouring lanes,
+// sixteen elements each, the two elements of a rotated pair in one lane: the
+// only exchange is the norm's sum.  (With eight elements a lane, partners
+// exchanged and every angle worked out twice, 8 prompts of 500-2048 tokens, 8
+// heads of 128, took 38 us; now 28, and 64 sequences' one token each 8 instead of
+// 12.)  The prompts' 63 MB would take 9 us: bound by the chain of loads and the
+// block's maximum between them and the stores, with 24 warps per SM.
 constexpr int kTurnThreads = 256;
 
 template <int D, int NCH>
-__global__ void __launch_bounds__(kTurnThreads, 2)
+__global__ void __launch_bounds__(kTurnThreads, NCH > 2 ? 2 : 3)
     kv_append_rope_kernel(const AppendParams p,
                           const __grid_constant__ TurnParams turn) {
-  constexpr int kPer = D / 8;  // pieces of a token's row
+  constexpr int kPer = D / 16;  // lanes of a token's row
   const int b = blockIdx.z;
   const int h = blockIdx.y >> 1;
   const bool is_v = blockIdx.y & 1;
@@ -227,108 +229,98 @@ __global__ void __launch_bounds__(kTurnThreads, 2)
   const int hi = min(len + n - tok0, p.page_size);
   if (lo >= hi) return;
   const int pid = p.table[static_cast<int64_t>(b) * p.table_stride + slot];
-  const int piece = threadIdx.x % kPer, row0 = threadIdx.x / kPer;
+  const bsm_rope& rope = turn.rope;
+  const bool pairs = rope.interleaved != 0;
+  const int row0 = threadIdx.x / kPer;
   constexpr int kRows = kTurnThreads / kPer;  // rows of one step
+  const LanePart part =
+      lane_part(threadIdx.x % kPer, rope.dim, !pairs);
   const uint16_t* src = is_v ? p.v_new : p.k_new;
   const int64_t sb = is_v ? p.v_sb : p.k_sb, sh = is_v ? p.v_sh : p.k_sh,
                 ss = is_v ? p.v_ss : p.k_ss;
-  src += b * sb + h * sh + piece * 8;
-  uint4 raw[NCH];
+  src += b * sb + h * sh;
+  uint4 raw[NCH][2];
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int tok = row0 + i * kRows;
-    raw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (tok >= lo && tok < hi)
-      raw[i] = *reinterpret_cast<const uint4*>(src + (tok0 + tok - len) * ss);
+    raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (tok >= lo && tok < hi) {
+      const uint16_t* row = src + (tok0 + tok - len) * ss;
+      raw[i][0] = *reinterpret_cast<const uint4*>(row + part.at0);
+      raw[i][1] = *reinterpret_cast<const uint4*>(row + part.at1);
+    }
   }
-  // the rotation of this thread's place in the row
-  const bsm_rope& rope = turn.rope;
-  const int half = rope.dim / 16;  // pieces of half a rotation
-  const bool turned = !is_v && piece < 2 * half;
-  const bool pairs = rope.interleaved != 0;
-  const int lane = threadIdx.x % 32;
-  const int partner = turned && !pairs
-                          ? (piece < half ? lane + half : lane - half)
-                          : lane;
-  const int freq = pairs ? piece * 4 : (piece < half ? piece : piece - half) * 8;
-  // its steps in registers: every piece of the thread turns by the same ones
-  // (read from the parameters piece by piece, where lanes of a warp want
-  // different words, 8 prompts of 500-2048 tokens took 49 us)
-  __shared__ uint64_t all_steps[64];
-  uint64_t steps[8];
-  if (!is_v && rope.dim != 0) {
-    if (threadIdx.x < 64) all_steps[threadIdx.x] = rope.step[threadIdx.x];
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 8; ++e) steps[e] = turned ? all_steps[(freq + e) & 63] : 0;
+  // steps and weights in shared memory while the elements are on their way
+  // (read from the parameters, where lanes of a warp want different words, the
+  // steps cost 11 us of 49 on those prompts)
+  __shared__ __align__(16) uint64_t steps[64];
+  __shared__ __align__(16) float weights[D];
+  if (!is_v) {
+    if (threadIdx.x < 64) steps[threadIdx.x] = rope.step[threadIdx.x];
+    if (turn.norm && threadIdx.x >= 128 && threadIdx.x < 128 + D / 8)
+      weights_of(turn.k_weight, turn.weights_bf16, (threadIdx.x - 128) * 8,
+                 weights + (threadIdx.x - 128) * 8);
   }
-  float w[8];
-  if (!is_v && turn.norm)
-    weights_of(turn.k_weight, turn.weights_bf16, piece * 8, w);
   if (pid < 0 || pid >= p.num_pages) {
     if (threadIdx.x == 0) record_bad_index(b, slot, pid);
     return;
   }
   const int64_t block = static_cast<int64_t>(pid) * p.H_kv + h;
-  uint8_t* dst = (is_v ? p.v : p.k) + block * p.page_size * p.D + piece * 8;
+  uint8_t* dst = (is_v ? p.v : p.k) + block * p.page_size * p.D;
   float* scale_at = (is_v ? p.v_scale : p.k_scale) + block;
   const float was = lo > 0 ? *scale_at : 0.f;
-  float x[NCH][8];
+  __syncthreads();
+  float x[NCH][16];
   float top = 0.f;  // the largest finite magnitude
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    unpack_bf16x8(raw[i], x[i]);
+    unpack_bf16x8(raw[i][0], x[i]);
+    unpack_bf16x8(raw[i][1], x[i] + 8);
     const int tok = row0 + i * kRows;
     const bool fresh = tok >= lo && tok < hi;
-    // (whole warps: the lanes exchange elements)
+    // (whole warps: the lanes add up their squares)
     if (!is_v && __any_sync(0xffffffffu, fresh)) {
       if (turn.norm) {
         float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(x[i][e], x[i][e], sum);
+        for (int e = 0; e < 16; ++e) sum = fmaf(x[i][e], x[i][e], sum);
 #pragma unroll
         for (int d = 1; d < kPer; d *= 2)
           sum += __shfl_xor_sync(0xffffffffu, sum, d);
         const float r = rsqrtf(fmaf(sum, 1.f / D, turn.eps));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] *= r * w[e];
+        for (int e = 0; e < 16; ++e)
+          x[i][e] *= r * weights[(e < 8 ? part.at0 : part.at1 - 8) + e];
       }
-      if (rope.dim != 0) {
+      if (part.freq >= 0 && fresh) {
         const int t = tok0 + tok - len;
-        const int32_t* pos = turn.pos != nullptr && fresh
-                                 ? turn.pos + b * turn.pos_sb + t * turn.pos_ss
-                                 : nullptr;
+        const int32_t* pos =
+            turn.pos != nullptr
+                ? turn.pos + b * turn.pos_sb + t * turn.pos_ss
+                : nullptr;
         float c[8], s[8];
+        turns_of<8>(rope, steps + part.freq, part.freq, pos, turn.pos_sa,
+                    tok0 + tok, c, s);
         if (pairs) {
-          if (turned && fresh) {
-            turns_of<4>(rope, steps, freq, pos, turn.pos_sa, tok0 + tok, c,
-                        s);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float u = x[i][2 * e], v = x[i][2 * e + 1];
-              x[i][2 * e] = u * c[e] - v * s[e];
-              x[i][2 * e + 1] = v * c[e] + u * s[e];
-            }
+          for (int e = 0; e < 8; ++e) {
+            const float u = x[i][2 * e], v = x[i][2 * e + 1];
+            x[i][2 * e] = u * c[e] - v * s[e];
+            x[i][2 * e + 1] = v * c[e] + u * s[e];
           }
         } else {
-          float other[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            other[e] = __shfl_sync(0xffffffffu, x[i][e], partner);
-          if (turned && fresh) {
-            turns_of<8>(rope, steps, freq, pos, turn.pos_sa, tok0 + tok, c,
-                        s);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              x[i][e] = x[i][e] * c[e] +
-                        other[e] * (piece < half ? -s[e] : s[e]);
+          for (int e = 0; e < 8; ++e) {
+            const float u = x[i][e], v = x[i][8 + e];
+            x[i][e] = u * c[e] - v * s[e];
+            x[i][8 + e] = v * c[e] + u * s[e];
           }
         }
       }
     }
     if (fresh) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < 16; ++e) {
         const float a = fabsf(x[i][e]);
         top = fmaxf(top, a < __int_as_float(0x7f800000) ? a : 0.f);
       }
@@ -337,7 +329,7 @@ __global__ void __launch_bounds__(kTurnThreads, 2)
   __shared__ uint32_t warp_top[kTurnThreads / 32];
   const uint32_t mine =
       __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-  if (lane == 0) warp_top[threadIdx.x / 32] = mine;
+  if (threadIdx.x % 32 == 0) warp_top[threadIdx.x / 32] = mine;
   __syncthreads();  // (and every thread has read the old scale)
   uint32_t most = 0;
 #pragma unroll
@@ -348,23 +340,28 @@ __global__ void __launch_bounds__(kTurnThreads, 2)
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int tok = row0 + i * kRows;
-    uint2* at = reinterpret_cast<uint2*>(dst + tok * D);
-    if (tok >= lo && tok < hi) {
-      *at = make_uint2(f32x4_to_e4m3(x[i][0] * inv, x[i][1] * inv,
-                                     x[i][2] * inv, x[i][3] * inv),
-                       f32x4_to_e4m3(x[i][4] * inv, x[i][5] * inv,
-                                     x[i][6] * inv, x[i][7] * inv));
-    } else if (tok < lo && scale > was) {
-      const float ratio = was * inv;
-      const uint2 q = *at;
-      uint32_t r[2] = {q.x, q.y};
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t f0 = e4m3x2_to_f16x2(r[j]), f1 = e4m3x2_to_f16x2_hi(r[j]);
-        r[j] = f32x4_to_e4m3(f16_lo(f0) * ratio, f16_hi(f0) * ratio,
-                             f16_lo(f1) * ratio, f16_hi(f1) * ratio);
+    for (int k = 0; k < 2; ++k) {
+      const float* y = x[i] + 8 * k;
+      uint2* at =
+          reinterpret_cast<uint2*>(dst + tok * D + (k ? part.at1 : part.at0));
+      if (tok >= lo && tok < hi) {
+        *at = make_uint2(
+            f32x4_to_e4m3(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+            f32x4_to_e4m3(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+      } else if (tok < lo && scale > was) {
+        const float ratio = was * inv;
+        const uint2 q = *at;
+        uint32_t r[2] = {q.x, q.y};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t f0 = e4m3x2_to_f16x2(r[j]),
+                         f1 = e4m3x2_to_f16x2_hi(r[j]);
+          r[j] = f32x4_to_e4m3(f16_lo(f0) * ratio, f16_hi(f0) * ratio,
+                               f16_lo(f1) * ratio, f16_hi(f1) * ratio);
+        }
+        *at = make_uint2(r[0], r[1]);
       }
-      *at = make_uint2(r[0], r[1]);
     }
   }
   if (threadIdx.x == 0) *scale_at = scale;
@@ -1151,13 +1148,12 @@ static cudaError_t append_rope(const AppendParams& p, const TurnParams& t,
                                cudaStream_t stream) {
   const int slots = (p.T + p.page_size - 2) / p.page_size + 1;
   const dim3 grid(slots, 2 * p.H_kv, p.B);
-  // steps of the block over a page's pieces (half a step: page 16 at D = 64)
-  switch (p.page_size * D / (8 * kTurnThreads)) {
+  // steps of the block over a page's pieces (the smallest pages: part of one)
+  switch (p.page_size * D / (16 * kTurnThreads)) {
     case 0:
     case 1: kv_append_rope_kernel<D, 1><<<grid, kTurnThreads, 0, stream>>>(p, t); break;
     case 2: kv_append_rope_kernel<D, 2><<<grid, kTurnThreads, 0, stream>>>(p, t); break;
     case 4: kv_append_rope_kernel<D, 4><<<grid, kTurnThreads, 0, stream>>>(p, t); break;
-    case 8: kv_append_rope_kernel<D, 8><<<grid, kTurnThreads, 0, stream>>>(p, t); break;
     default: return cudaErrorInvalidValue;
   }
   return cudaGetLastError();

@@ -24,25 +24,8 @@ namespace bsm {
 namespace {
 
 constexpr int kFwdThreads = 128, kBwdThreads = 256;
-enum { kPlain = 0, kHalves = 1, kPairs = 2 };  // MODE: how elements are paired
-
-// Where a lane's 16 elements lie and which frequencies turn them.
-struct LanePart {
-  int at0, at1;  // its first eight elements, and the other eight
-  int freq;      // frequencies freq .. freq + 7; -1: not turned
-};
-
-// Halves: lane l of dim / 16 holds elements 8 l .. and dim / 2 + 8 l ..;
-// neighbouring pairs, and what is not turned: 16 elements in a row.
-template <int MODE>
-__device__ __forceinline__ LanePart lane_part(int l, int dim) {
-  LanePart p;
-  const bool turned = MODE != kPlain && l < dim / 16;
-  p.freq = turned ? 8 * l : -1;
-  p.at0 = MODE == kHalves && turned ? 8 * l : 16 * l;
-  p.at1 = MODE == kHalves && turned ? dim / 2 + 8 * l : 16 * l + 8;
-  return p;
-}
+// MODE: how elements are paired
+enum { kPlain = 0, kHalves = 1, kPairs = 2 };
 
 // Pair i of a lane's 16 elements, turned by +angle (or -angle).
 template <int MODE, bool BACK>
@@ -87,9 +70,24 @@ __device__ __forceinline__ uint16_t* row_at(const RowView& v, const Job& j) {
   return v.data + j.b * v.sb + j.head * v.sh + j.s * v.ss;
 }
 
-__device__ __forceinline__ uint4 load8(const uint16_t* p, bool live) {
-  return live ? __ldcs(reinterpret_cast<const uint4*>(p))
-              : make_uint4(0u, 0u, 0u, 0u);
+// Rows on their way: a thread's 16 elements of kAhead rows to come, copied to
+// its own places in shared memory, so that they take no registers (loads of the
+// next row alone into registers left the forward pass at 67 % of the copy
+// bandwidth, the backward one at 71 %).  One place more than rows on their way:
+// a place is filled when the row read from it has been used.
+constexpr int kAhead = 3, kPlaces = kAhead + 1;
+
+__device__ __forceinline__ void fetch8(uint4* place, const uint16_t* p) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   smem_u32(place)),
+               "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void fetch_end() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void fetch_wait() {  // for the oldest of kAhead
+  asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
 }
 
 __device__ __forceinline__ void store8(uint16_t* p, const float* v) {
@@ -135,11 +133,21 @@ __global__ void __launch_bounds__(kFwdThreads)
   if (which) chunk -= p.chunks[0];
   Job j = job_of(p, which, live ? token : 0, chunk);
   if (!live) j.n = 0;
-  const LanePart part = lane_part<MODE>(threadIdx.x % L, p.turn.rope.dim);
+  const LanePart part =
+      lane_part(threadIdx.x % L, p.turn.rope.dim, MODE == kHalves);
   const uint16_t* src = row_at(p.x[which], j);
   uint16_t* dst = row_at(p.out[which], j);
   const int64_t src_sh = p.x[which].sh, dst_sh = p.out[which].sh;
-  uint4 x0 = load8(src + part.at0, 0 < j.n), x1 = load8(src + part.at1, 0 < j.n);
+  __shared__ uint4 rows[kPlaces][2][kFwdThreads];
+  auto fetch = [&](int i) {  // (a row that is not there leaves its place as is)
+    if (i < j.n) {
+      fetch8(&rows[i % kPlaces][0][threadIdx.x], src + part.at0);
+      fetch8(&rows[i % kPlaces][1][threadIdx.x], src + part.at1);
+    }
+    fetch_end();
+    src += src_sh;
+  };
+  for (int i = 0; i < kAhead; ++i) fetch(i);
   float w[16], c[8], s[8];
   if (NORM) {
     const void* wt = which ? p.turn.k_weight : p.turn.q_weight;
@@ -150,11 +158,10 @@ __global__ void __launch_bounds__(kFwdThreads)
   const int trips = max(p.per[0], p.per[1]);  // the same in a whole warp
   for (int i = 0; i < trips; ++i) {
     float v[16];
-    unpack_bf16x8(x0, v);
-    unpack_bf16x8(x1, v + 8);
-    src += src_sh;
-    x0 = load8(src + part.at0, i + 1 < j.n);
-    x1 = load8(src + part.at1, i + 1 < j.n);
+    fetch_wait();
+    fetch(i + kAhead);
+    unpack_bf16x8(rows[i % kPlaces][0][threadIdx.x], v);
+    unpack_bf16x8(rows[i % kPlaces][1][threadIdx.x], v + 8);
     if (NORM) {
       float sum = 0.f;
 #pragma unroll
@@ -180,14 +187,17 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
     norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int L = D / 16, kGroups = kBwdThreads / L;
   __shared__ uint64_t steps[64];
-  __shared__ float sums[NORM ? kGroups * D : 1];
+  constexpr int kParts = NORM ? 4 : 2;  // of 8 elements: gradient, row
+  extern __shared__ __align__(16) uint4 rows[];  // [kPlaces][kParts][threads]
+  float* sums = reinterpret_cast<float*>(rows);  // at the end: [kGroups][D]
   // the sums' kernel may be scheduled; it waits for this grid's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   load_steps<MODE>(p.turn, steps);
   const int which = static_cast<int>(blockIdx.x) >= p.blocks[0];
   const uint32_t block = blockIdx.x - (which ? p.blocks[0] : 0);
   const int group = threadIdx.x / L;
-  const LanePart part = lane_part<MODE>(threadIdx.x % L, p.turn.rope.dim);
+  const LanePart part =
+      lane_part(threadIdx.x % L, p.turn.rope.dim, MODE == kHalves);
   float w[16], acc[16], c[8], s[8];
   if (NORM) {
     const void* wt = which ? p.turn.k_weight : p.turn.q_weight;
@@ -199,36 +209,62 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
   const uint32_t chunks = p.chunks[which];
   const uint32_t jobs = static_cast<uint32_t>(p.B) * p.S * chunks;
   const uint32_t stride = p.blocks[which] * kGroups;
+  const int per = p.per[which];
   const int64_t x_sh = p.x[which].sh, g_sh = p.g[which].sh,
                 o_sh = p.out[which].sh;
-  for (uint32_t base = block * kGroups; base < jobs; base += stride) {
+  auto job_at = [&](uint32_t base) {
     const uint32_t job = base + group;
     const uint32_t token = job / chunks;
     Job j = job_of(p, which, job < jobs ? token : 0, job - token * chunks);
     if (job >= jobs) j.n = 0;
-    const uint16_t* x = NORM ? row_at(p.x[which], j) : nullptr;
-    const uint16_t* g = row_at(p.g[which], j);
-    uint16_t* dst = row_at(p.out[which], j);
-    uint4 g0 = load8(g + part.at0, 0 < j.n), g1 = load8(g + part.at1, 0 < j.n);
-    uint4 x0, x1;
-    if (NORM) {
-      x0 = load8(x + part.at0, 0 < j.n);
-      x1 = load8(x + part.at1, 0 < j.n);
+    return j;
+  };
+  // the next row to fetch: row f_i of the job at f_base, across jobs
+  uint32_t f_base = block * kGroups;
+  int f_i = 0, f_n = 0, f_place = 0;
+  const uint16_t *f_x = nullptr, *f_g = nullptr;
+  auto fetch = [&] {
+    if (f_i == 0 && f_base < jobs) {
+      const Job j = job_at(f_base);
+      f_n = j.n;
+      f_g = row_at(p.g[which], j);
+      if (NORM) f_x = row_at(p.x[which], j);
     }
-    job_turns<MODE>(p.turn, steps, part, j, c, s);
-    for (int i = 0; i < p.per[which]; ++i) {
-      float h[16], v[16];
-      unpack_bf16x8(g0, h);
-      unpack_bf16x8(g1, h + 8);
-      g += g_sh;
-      g0 = load8(g + part.at0, i + 1 < j.n);
-      g1 = load8(g + part.at1, i + 1 < j.n);
+    if (f_base < jobs && f_i < f_n) {
+      uint4* place = rows + f_place * kParts * kBwdThreads + threadIdx.x;
+      fetch8(place, f_g + part.at0);
+      fetch8(place + kBwdThreads, f_g + part.at1);
+      f_g += g_sh;
       if (NORM) {
-        unpack_bf16x8(x0, v);
-        unpack_bf16x8(x1, v + 8);
-        x += x_sh;
-        x0 = load8(x + part.at0, i + 1 < j.n);
-        x1 = load8(x + part.at1, i + 1 < j.n);
+        fetch8(place + 2 * kBwdThreads, f_x + part.at0);
+        fetch8(place + 3 * kBwdThreads, f_x + part.at1);
+        f_x += x_sh;
+      }
+    }
+    fetch_end();
+    f_place = (f_place + 1) % kPlaces;
+    if (++f_i == per) {
+      f_i = 0;
+      f_base += stride;
+    }
+  };
+  for (int i = 0; i < kAhead; ++i) fetch();
+  int at = 0;
+  for (uint32_t base = block * kGroups; base < jobs; base += stride) {
+    const Job j = job_at(base);
+    uint16_t* dst = row_at(p.out[which], j);
+    job_turns<MODE>(p.turn, steps, part, j, c, s);
+    for (int i = 0; i < per; ++i) {
+      float h[16], v[16];
+      fetch_wait();
+      fetch();
+      const uint4* place = rows + at * kParts * kBwdThreads + threadIdx.x;
+      at = (at + 1) % kPlaces;
+      unpack_bf16x8(place[0], h);
+      unpack_bf16x8(place[kBwdThreads], h + 8);
+      if (NORM) {
+        unpack_bf16x8(place[2 * kBwdThreads], v);
+        unpack_bf16x8(place[3 * kBwdThreads], v + 8);
       }
       if (MODE != kPlain && part.freq >= 0) turn<MODE, true>(h, c, s);
       if (NORM) {
@@ -257,6 +293,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
     }
   }
   if (NORM && p.partial != nullptr) {
+    __syncthreads();  // (no row is on its way or being read)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       sums[group * D + part.at0 + e] = acc[e];
@@ -327,14 +364,24 @@ void launch_fwd(const NormRopeParams& p, cudaStream_t stream) {
         <<<grid, kFwdThreads, 0, stream>>>(p);
 }
 
+template <int D, int MODE, bool NORM>
+cudaError_t launch_bwd_as(const NormRopeParams& p, cudaStream_t stream) {
+  constexpr int kSmem = kPlaces * (NORM ? 4 : 2) * kBwdThreads * 16;
+  static_assert(!NORM || kBwdThreads / (D / 16) * D * 4 <= kSmem, "sums");
+  const cudaError_t e = cudaFuncSetAttribute(
+      norm_rope_bwd_kernel<D, MODE, NORM>,
+      cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  norm_rope_bwd_kernel<D, MODE, NORM>
+      <<<p.blocks[0] + p.blocks[1], kBwdThreads, kSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
 template <int D, int MODE>
-void launch_bwd(const NormRopeParams& p, cudaStream_t stream) {
-  const unsigned grid = p.blocks[0] + p.blocks[1];
-  if (p.turn.norm)
-    norm_rope_bwd_kernel<D, MODE, true><<<grid, kBwdThreads, 0, stream>>>(p);
-  else if (MODE != kPlain)
-    norm_rope_bwd_kernel<D, MODE, MODE == kPlain>
-        <<<grid, kBwdThreads, 0, stream>>>(p);
+cudaError_t launch_bwd(const NormRopeParams& p, cudaStream_t stream) {
+  if (p.turn.norm) return launch_bwd_as<D, MODE, true>(p, stream);
+  // (neither norm nor rotation: refused before)
+  return launch_bwd_as<D, MODE == kPlain ? kHalves : MODE, false>(p, stream);
 }
 
 }  // namespace
@@ -371,17 +418,17 @@ cudaError_t launch_norm_rope_bwd(NormRopeParams& p, int num_sms,
   const bool dw = p.dw[0] != nullptr || p.dw[1] != nullptr;
   if (!dw) p.partial = nullptr;
   const int mode = mode_of(p);
+  cudaError_t e = cudaSuccess;
   if (p.blocks[0] + p.blocks[1] == 0)
     ;  // no rows: sums of nothing below
   else if (p.D == 128)
-    mode == kPlain    ? launch_bwd<128, kPlain>(p, stream)
-    : mode == kHalves ? launch_bwd<128, kHalves>(p, stream)
-                      : launch_bwd<128, kPairs>(p, stream);
+    e = mode == kPlain    ? launch_bwd<128, kPlain>(p, stream)
+        : mode == kHalves ? launch_bwd<128, kHalves>(p, stream)
+                          : launch_bwd<128, kPairs>(p, stream);
   else
-    mode == kPlain    ? launch_bwd<64, kPlain>(p, stream)
-    : mode == kHalves ? launch_bwd<64, kHalves>(p, stream)
-                      : launch_bwd<64, kPairs>(p, stream);
-  const cudaError_t e = cudaGetLastError();
+    e = mode == kPlain    ? launch_bwd<64, kPlain>(p, stream)
+        : mode == kHalves ? launch_bwd<64, kHalves>(p, stream)
+                          : launch_bwd<64, kPairs>(p, stream);
   if (e != cudaSuccess || !dw) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * p.D / 32);

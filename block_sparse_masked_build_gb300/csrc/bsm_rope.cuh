@@ -16,11 +16,33 @@ namespace bsm {
 // size 1.
 __device__ __forceinline__ void turn_of(uint64_t step, int32_t position,
                                         float* c, float* s) {
-  const uint64_t turns =
-      static_cast<uint64_t>(static_cast<int64_t>(position)) * step;
-  const float a = static_cast<float>(static_cast<int32_t>(turns >> 32)) *
+  // (the product's upper half in 32 bits: a negative position is 2^32 less
+  // than its bits)
+  const uint32_t p = static_cast<uint32_t>(position);
+  const uint32_t lo = static_cast<uint32_t>(step);
+  const uint32_t turns = __umulhi(p, lo) + p * static_cast<uint32_t>(step >> 32) -
+                         (position < 0 ? lo : 0u);
+  const float a = static_cast<float>(static_cast<int32_t>(turns)) *
                   1.4629180792671596e-9f;  // 2 pi / 2^32
   __sincosf(a, s, c);
+}
+
+// Where a lane's 16 elements of a row lie, and which frequencies turn them: the
+// two elements of a pair lie in one lane.
+struct LanePart {
+  int at0, at1;  // its first eight elements, and the other eight
+  int freq;      // frequencies freq .. freq + 7; -1: not turned
+};
+
+// Halves: lane l of dim / 16 holds elements 8 l .. and dim / 2 + 8 l ..;
+// neighbouring pairs, and what is not turned: 16 elements in a row.
+__device__ __forceinline__ LanePart lane_part(int l, int dim, bool halves) {
+  LanePart p;
+  const bool turned = l < dim / 16;
+  p.freq = turned ? 8 * l : -1;
+  p.at0 = halves && turned ? 8 * l : 16 * l;
+  p.at1 = halves && turned ? dim / 2 + 8 * l : 16 * l + 8;
+  return p;
 }
 
 // Of N frequencies from f on, whose steps the caller holds; pos: the token's
