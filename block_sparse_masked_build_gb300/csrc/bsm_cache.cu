@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kAppendThreads, NCH <= 8 ? 8 : 4)
 constexpr int kTurnThreads = 256;
 
 template <int D, int NCH>
-__global__ void __launch_bounds__(kTurnThreads, NCH > 2 ? 2 : 3)
+__global__ void __launch_bounds__(kTurnThreads, NCH > 2 ? 2 : 4)
     kv_append_rope_kernel(const AppendParams p,
                           const __grid_constant__ TurnParams turn) {
   constexpr int kPer = D / 16;  // lanes of a token's row
@@ -290,7 +290,12 @@ __global__ void __launch_bounds__(kTurnThreads, NCH > 2 ? 2 : 3)
         const float r = rsqrtf(fmaf(sum, 1.f / D, turn.eps));
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          x[i][e] *= r * weights[(e < 8 ? part.at0 : part.at1 - 8) + e];
+          x[i][e] *= r;  // (and then the weight, as in norm_rope)
+        if (turn.k_weight != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            x[i][e] *= weights[(e < 8 ? part.at0 : part.at1 - 8) + e];
+        }
       }
       if (part.freq >= 0 && fresh) {
         const int t = tok0 + tok - len;
@@ -298,22 +303,19 @@ __global__ void __launch_bounds__(kTurnThreads, NCH > 2 ? 2 : 3)
             turn.pos != nullptr
                 ? turn.pos + b * turn.pos_sb + t * turn.pos_ss
                 : nullptr;
-        float c[8], s[8];
-        turns_of<8>(rope, steps + part.freq, part.freq, pos, turn.pos_sa,
-                    tok0 + tok, c, s);
-        if (pairs) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 8; ++e) {
+          float c, s;
+          turns_of<1>(rope, steps + part.freq + e, part.freq + e, pos,
+                      turn.pos_sa, tok0 + tok, &c, &s);
+          if (pairs) {
             const float u = x[i][2 * e], v = x[i][2 * e + 1];
-            x[i][2 * e] = u * c[e] - v * s[e];
-            x[i][2 * e + 1] = v * c[e] + u * s[e];
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
+            x[i][2 * e] = u * c - v * s;
+            x[i][2 * e + 1] = v * c + u * s;
+          } else {
             const float u = x[i][e], v = x[i][8 + e];
-            x[i][e] = u * c[e] - v * s[e];
-            x[i][8 + e] = v * c[e] + u * s[e];
+            x[i][e] = u * c - v * s;
+            x[i][8 + e] = v * c + u * s;
           }
         }
       }

@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kFwdThreads)
       for (int e = 0; e < 16; ++e) sum = fmaf(v[e], v[e], sum);
       const float r = rsqrtf(fmaf(row_sum<D>(sum), 1.f / D, p.turn.eps));
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] *= r * w[e];
+      for (int e = 0; e < 16; ++e) v[e] = v[e] * r * w[e];
     }
     if (MODE != kPlain && part.freq >= 0) turn<MODE, false>(v, c, s);
     if (i < j.n) {

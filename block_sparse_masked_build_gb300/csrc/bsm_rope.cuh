@@ -9,22 +9,38 @@
 namespace bsm {
 
 // cos and sin of position * step turns.  The product modulo 2^64 drops whole
-// turns exactly; its upper half is a signed fraction of a turn in [-1/2, 1/2),
-// whose angle __sincosf takes within its bound for [-pi, pi] (2^-21.2
-// absolute); with the roundings of the angle itself (3 of 2^-25 of at most pi)
-// that is less than 2^-20, eleven bits below bf16's half step of a result of
-// size 1.
+// turns exactly; its upper half, to the nearest quarter turn, leaves an angle in
+// [-pi/4, pi/4), a + low with 2 pi / 2^32 as a sum of two f32, so that what it
+// is off by is the integer's rounding, 2^-24 of at most pi / 4.  The Taylor series
+// are summed to a^9 and a^8 (they leave out at most (pi/4)^11 / 11! < 2^-29 and
+// (pi/4)^10 / 10! < 2^-25) and moved by low.  With the sums' own roundings that
+// is less than 2^-23.  (__sincosf, within 2^-20, moved enough keys to the
+// neighbouring e4m3 value to be seen in a cache's error.)
 __device__ __forceinline__ void turn_of(uint64_t step, int32_t position,
                                         float* c, float* s) {
-  // (the product's upper half in 32 bits: a negative position is 2^32 less
-  // than its bits)
-  const uint32_t p = static_cast<uint32_t>(position);
-  const uint32_t lo = static_cast<uint32_t>(step);
-  const uint32_t turns = __umulhi(p, lo) + p * static_cast<uint32_t>(step >> 32) -
-                         (position < 0 ? lo : 0u);
-  const float a = static_cast<float>(static_cast<int32_t>(turns)) *
-                  1.4629180792671596e-9f;  // 2 pi / 2^32
-  __sincosf(a, s, c);
+  const uint64_t turns =
+      static_cast<uint64_t>(static_cast<int64_t>(position)) * step;
+  const uint32_t t = static_cast<uint32_t>(turns >> 32);
+  const uint32_t q = t + 0x20000000u;  // the nearest quarter in its two top bits
+  const float r = static_cast<float>(static_cast<int32_t>(t - (q & 0xc0000000u)));
+  constexpr float kTurn = 1.462918119976564e-09f, kTurnLow = -4.070940267922164e-17f;
+  const float a = r * kTurn;
+  const float low = fmaf(r, kTurnLow, fmaf(r, kTurn, -a));
+  const float z = a * a;
+  float sn = fmaf(z, 1.f / 362880.f, -1.f / 5040.f);
+  sn = fmaf(sn, z, 1.f / 120.f);
+  sn = fmaf(sn, z, -1.f / 6.f);
+  float cs = fmaf(z, 1.f / 40320.f, -1.f / 720.f);
+  cs = fmaf(cs, z, 1.f / 24.f);
+  cs = fmaf(cs, z, -0.5f);
+  // + low cos a and - low sin a, to the terms that count; the small parts first
+  sn = a + fmaf(sn * z, a, fmaf(-0.5f * z, low, low));
+  cs = 1.f + fmaf(cs, z, -low * a);
+  const bool odd = q & 0x40000000u;  // a quarter turn exchanges them
+  const float x = odd ? sn : cs, y = odd ? cs : sn;
+  *c = __uint_as_float(__float_as_uint(x) ^
+                       ((q + 0x40000000u) & 0x80000000u));
+  *s = __uint_as_float(__float_as_uint(y) ^ (q & 0x80000000u));
 }
 
 // Where a lane's 16 elements of a row lie, and which frequencies turn them: the
