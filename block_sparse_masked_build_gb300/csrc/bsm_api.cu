@@ -1294,15 +1294,15 @@ bsm_status bsm_device_status(void* stream, int32_t* detail) {
   e = bsm::read_bwd_error(brec);
   if (e != cudaSuccess) return cuda_fail(e, "device status");
   if (rec[0] == 0 && brec[0] != 0) std::memcpy(rec, brec, sizeof(rec));
-  // (of timeouts or bad indices; the first is reported)
-  if (rec[0] == 0) e = bsm::read_tree_error(trec);
+  if (rec[0] == 0) e = bsm::read_tree_error(1, trec);
   if (e != cudaSuccess) return cuda_fail(e, "device status");
-  if (trec[0] == 1) std::memcpy(rec, trec, sizeof(rec));
+  if (trec[0] != 0) std::memcpy(rec, trec, sizeof(rec));
   // read, and so cleared, only where no timeout is reported before it: else
   // the next call reports it
   if (rec[0] == 0) e = bsm::read_cache_error(crec);
   if (e != cudaSuccess) return cuda_fail(e, "device status");
-  if (crec[0] == 0 && trec[0] == 2) std::memcpy(crec, trec, sizeof(crec));
+  if (rec[0] == 0 && crec[0] == 0) e = bsm::read_tree_error(2, crec);
+  if (e != cudaSuccess) return cuda_fail(e, "device status");
   if (crec[0] != 0) {
     if (detail != nullptr) std::memcpy(detail, crec, sizeof(crec));
     return fail(BSM_ERR_INVALID_ARG,

@@ -248,7 +248,7 @@ size_t tree_workspace_bytes(int64_t rows, int D);
 cudaError_t launch_tree_tc(const PagedParams& p, int num_sms,
                            uint64_t timeout_ns, cudaStream_t stream);
 // Reads and clears its device error record.
-cudaError_t read_tree_error(int32_t out[4]);
+cudaError_t read_tree_error(int code, int32_t out[4]);
 // Reads and clears the device error record of the cache kernels.
 cudaError_t read_cache_error(int32_t out[4]);
 cudaError_t launch_mask_info(const MaskInfoParams& p, cudaStream_t stream);

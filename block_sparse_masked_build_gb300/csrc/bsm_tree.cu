@@ -44,9 +44,9 @@
 
 namespace bsm {
 
-// Error record: [0] code (1: a wait gave up, then block, role, phase; 2: a
-// page table or length out of range, then sequence, page slot, value).
-__device__ int g_tree_error[4];
+// Error records, the first of each kind: code 1 (a wait gave up), block, role,
+// phase; code 2 (a page table or length out of range), sequence, page slot, value.
+__device__ int g_tree_error[2][4];
 
 namespace {
 
@@ -151,10 +151,11 @@ struct TcParams {
 };
 
 __device__ __forceinline__ void tc_record(int code, int a, int b, int c) {
-  if (atomicCAS(&g_tree_error[0], 0, code) == 0) {
-    g_tree_error[1] = a;
-    g_tree_error[2] = b;
-    g_tree_error[3] = c;
+  int* rec = g_tree_error[code - 1];
+  if (atomicCAS(&rec[0], 0, code) == 0) {
+    rec[1] = a;
+    rec[2] = b;
+    rec[3] = c;
   }
 }
 
@@ -1463,11 +1464,12 @@ cudaError_t launch_tree_tc(const PagedParams& p, int num_sms,
                     : launch_mod<64, 2>(t, num_sms, stream);
 }
 
-cudaError_t read_tree_error(int32_t out[4]) {
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_tree_error, 4 * sizeof(int32_t));
+cudaError_t read_tree_error(int code, int32_t out[4]) {
+  const size_t bytes = 4 * sizeof(int32_t), at = (code - 1) * bytes;
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_tree_error, bytes, at);
   if (e != cudaSuccess) return e;
   const int32_t zero[4] = {0, 0, 0, 0};
-  return cudaMemcpyToSymbol(g_tree_error, zero, 4 * sizeof(int32_t));
+  return cudaMemcpyToSymbol(g_tree_error, zero, bytes, at);
 }
 
 }  // namespace bsm
