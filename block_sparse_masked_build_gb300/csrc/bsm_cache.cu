@@ -200,11 +200,14 @@ __global__ void __launch_bounds__(kAppendThreads, NCH <= 8 ? 8 : 4)
 // The same with the keys normalised and rotated first, in f32 from the load to
 // the rounding to e4m3.  A token's row lies in D / 16 neighbouring lanes,
 // sixteen elements each, the two elements of a rotated pair in one lane: the
-// only exchange is the norm's sum.  (With eight elements a lane, partners
-// exchanged and every angle worked out twice, 8 prompts of 500-2048 tokens, 8
-// heads of 128, took 38 us; now 28, and 64 sequences' one token each 8 instead of
-// 12.)  The prompts' 63 MB would take 9 us: bound by the chain of loads and the
-// block's maximum between them and the stores, with 24 warps per SM.
+// only exchange is the norm's sum.  8 prompts of 500-2048 tokens, 8 heads of 128:
+// 31 us (eight elements a lane, partners exchanged and every angle worked out
+// twice, took 7 us more at the same angles' cost); one token for each of 64
+// sequences 10, 20-48 drafts for 16 of them 9.  The prompts' 63 MB would take 9
+// us: bound by instructions, which issue in 67 % of the cycles, half of them the
+// angles'.  Working these out once for two or four heads of a page (35-38 us: a
+// block's heads then wait one after another) or ahead of the elements into
+// shared memory (32) gained nothing, nor did blocks of 512 threads (36).
 constexpr int kTurnThreads = 256;
 
 template <int D, int NCH>

