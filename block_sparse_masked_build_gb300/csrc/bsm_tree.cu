@@ -33,12 +33,13 @@
 // TMEM columns: S and P [0, 128) and [128, 256), by turns with one tile, one
 // for each of two; O [256, 256 + D), of a second tile from 384 on.
 //
-// Measured (32/8 heads of 128): 32 sequences of 300-12000 tokens, 7-16 drafts, one
-// tile, 149-156 us (2.7 TB/s: the conversion and the chain from S over the softmax
-// to P take ~2300 cycles per 128 tokens, the tensor pipe is active in 28 %); 16
-// sequences of 2000-12000 tokens, 64 drafts, two tiles, 152-179 us (650-780
-// TFLOP/s, ~5000 cycles per 128 tokens); 2 sequences of 100000-131072, 25 drafts, 153-164
-// us, with capped scores, which pass through registers once more, 243-264.
+// Measured (32/8 heads of 128): 32 sequences of 300-12000 tokens, 7-16 drafts,
+// one tile, 149-156 us (2.7 TB/s: the conversion and the chain from S over the
+// softmax to P take ~2300 cycles per 128 tokens, the tensor pipe is active in 28
+// %); 16 sequences of 2000-12000 tokens, 64 drafts, two tiles, 152-179 us
+// (650-780 TFLOP/s, ~5000 cycles per 128 tokens); 2 sequences of 100000-131072
+// tokens, 25 drafts, 153-164 us, with capped scores, which pass through registers
+// once more, 243-264.
 //
 // A step's tokens go from a run's end to its start: the drafts come first, and
 // with a bias that falls with the distance the maximum is met early.
@@ -1448,6 +1449,8 @@ cudaError_t launch_mod(const TcParams& t, int num_sms, cudaStream_t stream) {
 
 }  // namespace
 
+// Tiles of rows that a CTA works on: what does not fit one takes two at a time,
+// for which each code is copied and converted once.
 int tree_tiles(int64_t rows) {
   return rows <= kTreeFewRows ? 0 : rows <= kTcRows ? 1 : 2;
 }
