@@ -2,7 +2,7 @@
 against fp64.
 
 Tolerances.  The result is rounded to bf16 once (half a step, 2^-8 relative).
-Before that everything is f32: cosines and sines are off by 2^-20 of the pair's
+Before that everything is f32: cosines and sines are off by at most 2^-20 of the pair's
 length, the norm's factor, the weight and the products by a few 2^-24, the sum
 of up to 128 squares or products by at most 128 * 2^-24 of the sum of
 magnitudes: together less than 2^-16 of the element's size as the reference
@@ -299,3 +299,33 @@ def test_layer(both):  # noqa: F811
         for t, w in zip(got, (y.detach(), *want)):
             err = (t.double().cpu() - w).abs().max()
             assert float(err) <= 2e-2 * float(w.abs().max())
+
+
+@pytest.mark.parametrize("case", [
+    (1, 13, 3, 5003, 64, 64, False, 1, True, torch.bfloat16, 9),
+    (2, 5, 2, 3001, 128, 64, True, 2, True, torch.float32, 0),
+    (1, 9, 1, 8195, 64, 32, False, 1, False, None, 70000)])
+def test_many_rows(case):
+    """Several heads of a token for a group of lanes, unevenly, and several
+    tokens one after another in the backward; the forward also in place."""
+    d = _case(*case)
+    g = torch.Generator().manual_seed(4)
+    gq, gk = (torch.randn(d[n].shape, generator=g).bfloat16() for n in "qk")
+    args = _args(d)
+    q, k = d["q"].cuda(), d["k"].cuda()
+    x = (q, k) if d["eps"] is not None else ()
+    got = bsm.norm_rope_bwd(gq.cuda(), gk.cuda(), *x, **args)
+    res = bsm.norm_rope(q, k, **args)
+    for i, n in ((0, "q"), (1, "k")):
+        w = d[n + "w"]
+        near(res[i], *ref.forward(d[n], w, d["eps"], d["angle"], d["inter"]),
+             n)
+        dx, size, dw, dsize = ref.backward((gq, gk)[i], d[n], w, d["eps"],
+                                           d["angle"], d["inter"])
+        near(got[i], dx, size, "d" + n)
+        if w is not None:
+            err = (got[2 + i].double().cpu() - dw).abs()
+            assert bool((err <= 2.0 ** -13 * dsize).all()), n
+    bsm.norm_rope(q, k, out=q, k_out=k, **args)
+    assert torch.equal(q, res[0]) and torch.equal(k, res[1])
+    assert bsm.bsm_device_status()[0] == 0
