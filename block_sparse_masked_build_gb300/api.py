@@ -597,7 +597,7 @@ class Rope:
     are exact however far the position.  Made once and kept; it holds no
     device memory."""
 
-    __slots__ = ("_struct", "_address")
+    __slots__ = ("_struct",)
 
     def __init__(self, dim: int, base: float = 10000.0, *, inv_freq=None,
                  axes=None, interleaved: bool = False):
@@ -615,7 +615,6 @@ class Rope:
             self._struct, dim, bool(interleaved),
             (ctypes.c_double * half)(*freq), (ctypes.c_int32 * half)(*axis),
             max(axis, default=0) + 1))
-        self._address = ctypes.addressof(self._struct)
 
     dim = property(lambda self: self._struct.dim)
     axes = property(lambda self: self._struct.axes)
@@ -627,7 +626,8 @@ def _rope_address(rope) -> int:
         return 0
     if not isinstance(rope, Rope):
         raise TypeError("rope must be a Rope")
-    return rope._address
+    # (not kept: a copied or unpickled Rope has a struct of its own)
+    return ctypes.addressof(rope._struct)
 
 
 def _check_rows(t, shape, dev, name: str) -> None:
