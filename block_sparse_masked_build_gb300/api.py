@@ -593,8 +593,9 @@ class Rope:
     (x[i], x[i + dim / 2]) or with ``interleaved`` (x[2 i], x[2 i + 1]), turns
     by position * inv_freq[i], where inv_freq is given ([dim / 2] numbers) or
     base^(-2 i / dim).  With ``axes`` ([dim / 2] whole numbers from 0 to 3) a
-    position has several numbers, and pair i goes by number axes[i].  Angles
-    are exact however far the position.  Made once and kept; it holds no
+    position has several numbers, and pair i goes by number axes[i].  inv_freq
+    is taken as it is in float64; cosines and sines of its product with any
+    int32 position are off by less than 2^-23.  Made once and kept; it holds no
     device memory."""
 
     __slots__ = ("_struct",)

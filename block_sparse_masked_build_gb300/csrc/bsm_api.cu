@@ -924,6 +924,23 @@ bsm_status bsm_splash_bwd_mod(const bsm_tensor* q, const bsm_tensor* k,
   return BSM_OK;
 }
 
+namespace {
+// freq / (2 pi) turns, |freq| <= 64, without the whole ones, in units of 2^-64 and
+// off by half of one: the product with 1 / (2 pi) in two f64 (either alone would
+// leave 53 bits, which 2^31 positions multiply to an error of 2^-21 and, at a
+// frequency of 64, 2^-17).
+uint64_t turn_step(double freq) {
+  constexpr double kHigh = 0.15915494309189535, kLow = -9.839338337591243e-18;
+  const double high = freq * kHigh;
+  const double low = std::fma(freq, kHigh, -high) + freq * kLow;
+  const double units = std::ldexp(high, 64);  // below 2^68
+  const __int128 whole = static_cast<__int128>(units);
+  const double rest =
+      (units - static_cast<double>(whole)) + std::ldexp(low, 64);
+  return static_cast<uint64_t>(whole + std::llrint(rest));
+}
+}  // namespace
+
 bsm_status bsm_rope_init(bsm_rope* rope, int32_t dim, int32_t interleaved,
                          const double* inv_freq, const int32_t* axis,
                          int32_t axes) {
@@ -946,11 +963,7 @@ bsm_status bsm_rope_init(bsm_rope* rope, int32_t dim, int32_t interleaved,
     if (a < 0 || a >= axes)
       return fail(BSM_ERR_INVALID_ARG, "axis must be within [0, axes)");
     r.axis[i] = static_cast<uint8_t>(a);
-    // whole turns dropped, in units of 2^-64 (2^64 itself, which a fraction
-    // next to 1 rounds to, is 0 turns)
-    const double turns = inv_freq[i] * 0.15915494309189535;
-    const double part = std::ldexp(turns - std::floor(turns), 64);
-    r.step[i] = part < 0x1p64 ? static_cast<uint64_t>(part) : 0;
+    r.step[i] = turn_step(inv_freq[i]);
   }
   *rope = r;
   return BSM_OK;

@@ -538,9 +538,10 @@ size_t bsm_paged_attention_tree_workspace_bytes(int32_t H, int32_t H_kv,
  * the elements behind them stay as they are.  A position has `axes` numbers
  * (time, height, width, ...); frequency i goes by the one axis[i] names.
  * Filled by bsm_rope_init, plain data, copied by the calls that take it.
- * step[i] is inv_freq[i] / (2 pi) turns in units of 2^-64, so that position *
- * step[i] modulo 2^64 is the angle without its whole turns, however far the
- * position: cosines and sines are off by less than 2^-23. */
+ * step[i] is inv_freq[i] / (2 pi) turns in units of 2^-64, rounded to the
+ * nearest, so that position * step[i] modulo 2^64 is the angle without its whole
+ * turns, off by at most 2^-34 turns at the farthest position: cosines and sines
+ * are off by less than 2^-23 at every position and frequency. */
 typedef struct bsm_rope {
   int32_t dim, interleaved, axes, reserved;
   uint64_t step[64];
