@@ -563,6 +563,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
     if (static_cast<uint32_t>(pid) < static_cast<uint32_t>(p.num_pages))
       return pid;
     if (lane == 0) record_bad_index(b, slot, pid);
+    __syncwarp();  // (matrix instructions are a whole warp's, here as below)
     return -1;
   };
   auto issue = [&](int k, int st, int pid) {
@@ -814,6 +815,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
                   s[nt][2 * h + c]);  // (less what is added below)
           }
       }
+      __syncwarp();
     }
     bool grow = false;
 #pragma unroll
@@ -852,6 +854,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
             }
           }
         }
+      __syncwarp();
     }
     // ---- the value scale: o is kept in units of v_ref / kPUp, and a
     // group's scale multiplies p while it is within 2^6 of v_ref; past that o
@@ -960,6 +963,7 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
             }
           }
         }
+        __syncwarp();
       }
     }
 #pragma unroll

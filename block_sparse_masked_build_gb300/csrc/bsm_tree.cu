@@ -225,6 +225,9 @@ __device__ __forceinline__ float pow2(int e) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+// (Loads and stores of TMEM and the MMAs' elections are a whole warp's at once: a
+// __syncwarp stands between them and what lanes do apart.)
+
 // ----------------------------------------------------------------- planner
 
 // Value scales go along with P: its column is multiplied by scale / v_ref, at
@@ -938,6 +941,7 @@ __device__ __noinline__ float modified_scores(const PagedParams& p, TcCtl* c,
             nans->w[i] |= *reinterpret_cast<const uint32_t*>(n + 2 * i);
         }
       }
+      __syncwarp();  // (what the lanes did differs)
     }
     float x[32];
     tmem_ld32(s_addr + q * 32, reinterpret_cast<uint32_t*>(x));
@@ -1063,6 +1067,7 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
       run_pv = 0;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) nans.w[i] = 0u;
+      __syncwarp();
     }
     const int buf = R == 2 ? tile : static_cast<int>(step & 1);
     const uint32_t use = R == 2 ? step : step >> 1;
@@ -1115,13 +1120,11 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
         top = fmax3(top, max_of(xa, f[0], f[1]), max_of(xb, f[2], f[3]));
       }
     }
-    float scale_o = 1.f;
-    if (top > m_used + kTcRescaleLog2) {
-      const float alpha = ex2_approx(m_used - top);  // 0 from -inf
-      l_sum *= alpha;
-      scale_o = alpha;
-      m_used = top;
-    }
+    // (selected, not branched on: the lanes stay together)
+    const bool up_now = top > m_used + kTcRescaleLog2;
+    float scale_o = up_now ? ex2_approx(m_used - top) : 1.f;  // 0 from -inf
+    l_sum *= scale_o;
+    m_used = up_now ? top : m_used;
     if (s.v_ref != ref) {
       scale_o *= ref / s.v_ref;
       ref = s.v_ref;
@@ -1212,8 +1215,8 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
 #pragma unroll
         for (int j = 0; j < 32; ++j)
           if (nan >> j & 1u) o[j] = __int_as_float(0x7fffffff);
-      if (row >= rows) continue;
-      if (part != nullptr) {  // [dim][row]: a warp's rows lie side by side
+      if (row >= rows) {  // none
+      } else if (part != nullptr) {  // [dim][row]: a warp's rows lie side by side
         float* dst = part + dim * kPartRows + in_part;
 #pragma unroll
         for (int j = 0; j < 32; ++j) dst[j * kPartRows] = o[j];
@@ -1227,6 +1230,7 @@ __device__ __forceinline__ void score_role(const TcParams& tp, TcCtl* c,
                        pack_bf16x2(o[j + 4] * inv, o[j + 5] * inv),
                        pack_bf16x2(o[j + 6] * inv, o[j + 7] * inv));
       }
+      __syncwarp();  // (the next piece is the whole warp's to load)
     }
     tc_fence_before();
     mbar_arrive(&c->o_free[tile]);
