@@ -355,6 +355,19 @@ bsm_status check_rows(int32_t B, int32_t H, int32_t H_kv, int32_t S,
   return BSM_OK;
 }
 
+// A result that begins where its input does must lie as that does, or rows are
+// written that are still to be read.
+bsm_status check_in_place(const bsm_tensor* in, const bsm_tensor* out,
+                          int64_t B, int64_t heads, int64_t S,
+                          const char* name) {
+  const int64_t sizes[3] = {B, heads, S};
+  for (int d = 0; d < 3 && in->data == out->data; ++d)
+    if (sizes[d] > 1 && in->strides[d] != out->strides[d])
+      return fail(BSM_ERR_INVALID_ARG,
+                  std::string(name) + " in place must have its input's strides");
+  return BSM_OK;
+}
+
 bsm::RowView row_view(const bsm_tensor* t) {
   if (t == nullptr) return bsm::RowView{nullptr, 0, 0, 0};
   return bsm::RowView{static_cast<uint16_t*>(t->data), t->strides[0],
@@ -987,10 +1000,12 @@ bsm_status bsm_norm_rope(const bsm_tensor* q, const bsm_tensor* k, int32_t B,
   if (H > 0) {
     s = check_view(q, B, H, S, "q");
     if (s == BSM_OK) s = check_view(q_out, B, H, S, "q_out");
+    if (s == BSM_OK) s = check_in_place(q, q_out, B, H, S, "q_out");
   }
   if (s == BSM_OK && H_kv > 0) {
     s = check_view(k, B, H_kv, S, "k");
     if (s == BSM_OK) s = check_view(k_out, B, H_kv, S, "k_out");
+    if (s == BSM_OK) s = check_in_place(k, k_out, B, H_kv, S, "k_out");
   }
   int num_sms = 0;
   if (s == BSM_OK) s = check_device(&num_sms);
@@ -1052,6 +1067,10 @@ bsm_status bsm_norm_rope_bwd(const bsm_tensor* gq, const bsm_tensor* gk,
     for (int j = 0; j < (norm != nullptr ? 3 : 2) && (i ? H_kv : H) > 0; ++j)
       if (s == BSM_OK)
         s = check_view(views[i][j], B, i ? H_kv : H, S, names[i][j]);
+  for (int i = 0; i < 2 && rows && s == BSM_OK; ++i)
+    if ((i ? H_kv : H) > 0)
+      s = check_in_place(views[i][0], views[i][1], B, i ? H_kv : H, S,
+                         names[i][1]);
   int num_sms = 0;
   if (s == BSM_OK) s = check_device(&num_sms);
   if (s != BSM_OK) return s;

@@ -579,8 +579,8 @@ typedef struct bsm_head_norm {
  * given).  Computed in f32 and rounded to bf16 once.
  *   q, q_out  device bf16 [B][H][S][D]; k, k_out [B][H_kv][S][D], or both NULL
  *             with H_kv = 0; D 64 or 128, rope->dim <= D.  q_out may be q
- *             itself (the same memory and strides), and k_out k; no other
- *             overlap is allowed
+ *             itself (the same memory and strides: others are refused), and k_out
+ *             k; no other overlap is allowed
  *   pos       NULL: token indices
  * One launch on `stream`. */
 bsm_status bsm_norm_rope(const bsm_tensor* q, const bsm_tensor* k, int32_t B,

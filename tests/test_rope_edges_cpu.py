@@ -1,4 +1,5 @@
-"""Rotations without a GPU: copies of a Rope, and the turns it holds."""
+"""Rotations without a GPU: copies of a Rope, the turns it holds, and results in
+place of their inputs."""
 
 import copy
 import ctypes
@@ -9,8 +10,8 @@ from decimal import Decimal, localcontext
 import pytest
 
 import block_sparse_masked_build_gb300 as bsm
-from block_sparse_masked_build_gb300 import api
-from block_sparse_masked_build_gb300._lib import RopeStruct
+from block_sparse_masked_build_gb300 import _lib, api
+from block_sparse_masked_build_gb300._lib import I64x3, RopeStruct, TensorView
 
 
 @pytest.mark.parametrize("again", [
@@ -47,3 +48,37 @@ def test_steps_to_their_last_bit(freq):
         off = abs((Decimal(got) - want) % 2 ** 64)
         off = min(off, 2 ** 64 - off)
     assert off <= Decimal("0.5001"), off
+
+
+def _view(data, *strides):
+    return ctypes.byref(TensorView(data, I64x3(*strides)))
+
+
+@pytest.mark.parametrize("which", ["q", "k"])
+@pytest.mark.parametrize("backward", [False, True])
+def test_in_place_needs_the_inputs_strides(which, backward):
+    """Rows written over an input that lies otherwise in the same memory would
+    be read again."""
+    lib = _lib.lib()
+    rope = bsm.Rope(64)._struct
+    # [B, S, H, D] and [B, H, S, D] in one memory; the others apart
+    a, b = (4096, 64, 512), (4096, 512, 64)
+    kw = dict(q=_view(0x500000, *a), qo=_view(0x600000, *a),
+              k=_view(0x700000, *a), ko=_view(0x800000, *a))
+    kw[which] = _view(0x900000, *a)
+    kw[which + "o"] = _view(0x900000, *b)
+
+    def call(B=2, H=8, S=8):
+        more = (B, H, H, S, 64, None, rope, None)
+        if backward:
+            return lib.bsm_norm_rope_bwd(
+                kw["q"], kw["k"], None, None, *more, kw["qo"], kw["ko"], None,
+                None, None, 0, None)
+        return lib.bsm_norm_rope(kw["q"], kw["k"], *more, kw["qo"], kw["ko"],
+                                 None)
+
+    assert call() == _lib.BSM_ERR_INVALID_ARG
+    assert "strides" in _lib.last_error() and "in place" in _lib.last_error()
+    kw[which + "o"] = _view(0x900000, 4096, 64, 1024)
+    assert call() == _lib.BSM_ERR_INVALID_ARG and "place" in _lib.last_error()
+    assert call(S=0) == 0
