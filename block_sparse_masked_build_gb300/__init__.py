@@ -33,6 +33,7 @@ from .api import (  # noqa: F401
     bsm_paged_attention_tree,
     bsm_paged_attention_tree_workspace_bytes,
     bsm_paged_attention_workspace_bytes,
+    bsm_selftest_tree_timeout,
     bsm_selftest_wait_timeout,
     bsm_splash_bwd,
     bsm_splash_bwd_mod_workspace_bytes,

@@ -213,6 +213,8 @@ def _declare(lib):
     lib.bsm_device_status.argtypes = [c.c_void_p, c.POINTER(c.c_int32)]
     lib.bsm_selftest_wait_timeout.restype = c.c_int
     lib.bsm_selftest_wait_timeout.argtypes = [c.c_int64, c.c_void_p]
+    lib.bsm_selftest_tree_timeout.restype = c.c_int
+    lib.bsm_selftest_tree_timeout.argtypes = [c.c_int64, c.c_void_p]
     lib.bsm_debug_set_trace.restype = c.c_int
     lib.bsm_debug_set_trace.argtypes = [c.c_void_p, c.c_size_t]
     lib.bsm_debug_fwd_grid.restype = c.c_int32

@@ -878,6 +878,11 @@ def bsm_selftest_wait_timeout(timeout_ns: int, stream=None) -> None:
                                                 _stream_handle(stream)))
 
 
+def bsm_selftest_tree_timeout(timeout_ns: int, stream=None) -> None:
+    _check(_lib.lib().bsm_selftest_tree_timeout(int(timeout_ns),
+                                                _stream_handle(stream)))
+
+
 def bsm_debug_set_trace(buffer) -> None:
     """Trace the following forward launches into ``buffer`` (a CUDA tensor,
     16-byte aligned) or switch tracing off with None."""

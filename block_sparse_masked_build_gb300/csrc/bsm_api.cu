@@ -1353,16 +1353,27 @@ bsm_status bsm_device_status(void* stream, int32_t* detail) {
   return BSM_OK;
 }
 
-bsm_status bsm_selftest_wait_timeout(int64_t timeout_ns, void* stream) {
+namespace {
+bsm_status selftest(cudaError_t (*launch)(uint64_t, cudaStream_t),
+                    int64_t timeout_ns, void* stream) {
   g_last_error.clear();
   if (timeout_ns < 1000 || timeout_ns > 10000000000LL)
     return fail(BSM_ERR_INVALID_ARG, "timeout_ns must be in [1e3, 1e10]");
   bsm_status s = check_device(nullptr);
   if (s != BSM_OK) return s;
-  cudaError_t e = bsm::launch_wait_selftest(static_cast<uint64_t>(timeout_ns),
-                                            static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch(static_cast<uint64_t>(timeout_ns),
+                               static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "self-test launch");
   return BSM_OK;
+}
+}  // namespace
+
+bsm_status bsm_selftest_wait_timeout(int64_t timeout_ns, void* stream) {
+  return selftest(bsm::launch_wait_selftest, timeout_ns, stream);
+}
+
+bsm_status bsm_selftest_tree_timeout(int64_t timeout_ns, void* stream) {
+  return selftest(bsm::launch_tree_selftest, timeout_ns, stream);
 }
 
 bsm_status bsm_debug_set_trace(void* buffer, size_t bytes) {

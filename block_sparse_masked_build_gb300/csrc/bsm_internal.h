@@ -247,6 +247,8 @@ int tree_tiles(int64_t rows);
 size_t tree_workspace_bytes(int64_t rows, int D);
 cudaError_t launch_tree_tc(const PagedParams& p, int num_sms,
                            uint64_t timeout_ns, cudaStream_t stream);
+// One block whose roles wait for steps that never come.
+cudaError_t launch_tree_selftest(uint64_t timeout_ns, cudaStream_t stream);
 // Reads and clears its device error record.
 cudaError_t read_tree_error(int code, int32_t out[4]);
 // Reads and clears the device error record of the cache kernels.

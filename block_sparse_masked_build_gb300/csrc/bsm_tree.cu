@@ -156,6 +156,7 @@ struct TcCtl {
 struct TcParams {
   PagedParams p;
   uint64_t timeout_ns;
+  int32_t no_plan;  // self test: nothing is dealt out, and the other roles give up
 };
 
 __device__ __forceinline__ void tc_record(int code, int a, int b, int c) {
@@ -1400,12 +1401,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_after();
   const uint32_t tmem = c->tmem, base = smem_u32(smem);
   if (wg == 0) {
-    if (warp == 0)
-      plan_role<D, R>(t, c);
-    else if (warp == 3)
+    if (warp == 3) {
       load_role<D, R>(t, c, base + C::kOffCodes);
-    else
+    } else if (warp > 0) {
       mma_role<D, R>(t, c, base, tmem, warp - 1);
+    } else if (!t.no_plan) {
+      plan_role<D, R>(t, c);
+    }
   } else if (wg == 1) {
     convert_role<D, R>(t, c, base + C::kOffKv, base + C::kOffCodes);
   } else {
@@ -1418,7 +1420,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 template <int D, int R, bool MOD>
-cudaError_t launch_tc(const TcParams& t, int num_sms, cudaStream_t stream) {
+cudaError_t launch_attend(const TcParams& t, int grid, cudaStream_t stream) {
   using C = TcCfg<D, R>;
   auto kern = paged_tree_kernel<D, R, MOD>;
   constexpr int smem = C::kOffCtl + static_cast<int>(sizeof(TcCtl)) + 1024;
@@ -1427,8 +1429,13 @@ cudaError_t launch_tc(const TcParams& t, int num_sms, cudaStream_t stream) {
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            smem);
   if (e != cudaSuccess) return e;
-  kern<<<num_sms, kTcThreads, smem, stream>>>(t);
-  e = cudaGetLastError();
+  kern<<<grid, kTcThreads, smem, stream>>>(t);
+  return cudaGetLastError();
+}
+
+template <int D, int R, bool MOD>
+cudaError_t launch_tc(const TcParams& t, int num_sms, cudaStream_t stream) {
+  const cudaError_t e = launch_attend<D, R, MOD>(t, num_sms, stream);
   if (e != cudaSuccess) return e;
   const int rows = t.p.H / t.p.H_kv * t.p.T;
   const int tiles = (rows + R * kTcRows - 1) / (R * kTcRows);
@@ -1470,12 +1477,22 @@ cudaError_t launch_tree_tc(const PagedParams& p, int num_sms,
   TcParams t;
   t.p = p;
   t.timeout_ns = timeout_ns;
+  t.no_plan = 0;
   const int tiles = tree_tiles(static_cast<int64_t>(p.H / p.H_kv) * p.T);
   if (p.D == 128)
     return tiles == 1 ? launch_mod<128, 1>(t, num_sms, stream)
                       : launch_mod<128, 2>(t, num_sms, stream);
   return tiles == 1 ? launch_mod<64, 1>(t, num_sms, stream)
                     : launch_mod<64, 2>(t, num_sms, stream);
+}
+
+cudaError_t launch_tree_selftest(uint64_t timeout_ns, cudaStream_t stream) {
+  TcParams t = {};  // (no role gets to a pointer: each waits for its first step)
+  t.p.H = t.p.H_kv = t.p.T = 1;
+  t.p.D = 64;
+  t.timeout_ns = timeout_ns;
+  t.no_plan = 1;
+  return launch_attend<64, 1, false>(t, 1, stream);
 }
 
 cudaError_t read_tree_error(int code, int32_t out[4]) {

@@ -641,6 +641,10 @@ bsm_status bsm_device_status(void* stream, int32_t* detail);
  * bsm_device_status() then returns BSM_ERR_DEVICE_TIMEOUT. */
 bsm_status bsm_selftest_wait_timeout(int64_t timeout_ns, void* stream);
 
+/* The same of bsm_paged_attention_tree's kernel: one block of it whose roles
+ * wait for work that is never dealt out, give up and return. */
+bsm_status bsm_selftest_tree_timeout(int64_t timeout_ns, void* stream);
+
 /* Tracing (diagnostics).  With a non-NULL device buffer, every following
  * bsm_splash_fwd launch records timestamped events into it: the buffer is
  * split evenly over the launch's CTAs (see bsm_debug_fwd_grid) into
