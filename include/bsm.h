@@ -513,8 +513,10 @@ size_t bsm_paged_attention_workspace_bytes(void);
  *           sequences one tree), T <= 1024; or NULL: draft t sees the drafts j
  *           <= t, as one guess that goes on for n tokens
  * A draft's position is lens[b] - n plus its depth, which is the number of bits
- * set in its row, less one; a window and a bias go by these positions (the
- * distance is taken without its sign).  A row with no bits set sees nothing,
+ * set in its row, less one; a window and a bias go by these positions.  (Bits
+ * that are no tree's may show a row, at position p, a draft of a later position j:
+ * a window keeps it, as it keeps every p - j < window, and a bias takes the distance
+ * without its sign, slope |p - j|.)  A row with no bits set sees nothing,
  * and so do the rows t >= n: out = 0 and lse = -inf.  n_new[b] outside [0,
  * min(T, lens[b])] is cut to it and reported by bsm_device_status; everything
  * else as in bsm_paged_attention.

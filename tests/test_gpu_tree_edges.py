@@ -68,3 +68,16 @@ def test_any_bits(H, T):
     g = torch.Generator().manual_seed(T)
     d["bits"] = torch.rand(2, T, T, generator=g) < 0.3
     _same(_run(d), _want(d))
+
+
+@pytest.mark.parametrize("window", [1, 3])
+@pytest.mark.parametrize("H,T", [(8, 2), (8, 40), (8, 70)])
+def test_any_bits_and_a_window(H, T, window):
+    """A later position than the row's is within every window."""
+    d = _case(64, 128, H, 2, T, [300, 90], [T, T - 1], window, 0.0, True, True)
+    g = torch.Generator().manual_seed(T)
+    d["bits"] = torch.rand(2, T, T, generator=g) < 0.3
+    depth = d["bits"].sum(-1) - 1
+    later = d["bits"] & (depth[:, None, :] - depth[:, :, None] >= window)
+    assert T == 2 or bool(later.any())
+    _same(_run(d), _want(d))
