@@ -72,15 +72,17 @@ __device__ __forceinline__ void write_row(const PagedParams& p, int b,
                    : __int_as_float(0xff800000);
 }
 
-// How the tokens are dealt out.  An item is (sequence, key/value head, tile of
-// 8 NT query rows); its work is its sequence's visible tokens in units of 64
-// (a group of 16 for each warp).  All units of all items, in order, are cut
-// into equal runs, one per CTA, so that unequal lengths and few long
-// sequences load every SM alike.  An item counts kPaRunCost units more than
-// it has, before its first: what starting and ending a run costs (64
-// sequences of 300-12000 tokens: 160 us without, 140 with).  A CTA may start and end inside an item;
-// then it leaves its part (o, m, l) in the workspace and the join kernel adds
-// the parts up.  The cut depends on the lengths alone, which both kernels
+// How the tokens are dealt out; X is a kernel's deal.  An item is (sequence,
+// key/value head, tile of query rows: 8 or 16 in the kernel of few rows, 128 or
+// 256 in the trees'); its work is its sequence's visible tokens in units of
+// X::kUnit groups (64 tokens, a group for each warp; the trees' 128, a full
+// step).  All units of all items, in order, are cut into equal runs, one per CTA,
+// so that unequal lengths and few long sequences load every SM alike.  An item
+// counts X::kRunCost units more than it has, before its first: what starting and
+// ending a run costs (the kernel of few rows, 64 sequences of 300-12000 tokens:
+// 160 us without, 140 with).  A CTA may start and end inside an item; then it
+// leaves its part (o, m, l) in the workspace and a join kernel adds the parts up.
+// The cut depends on the lengths and numbers of drafts alone, which both kernels
 // read.
 struct PaPlan {
   int len, lo;      // of one sequence: tokens, first visible one
@@ -213,8 +215,9 @@ __device__ __forceinline__ int find_sequence(const PagedParams& p, int per,
   return __shfl_sync(0xffffffffu, b, owner);
 }
 
-// CTAs that get work: at least kLeast (two) units each, so that a CTA's first loads
-// and its join are spread over more than one round of groups.
+// CTAs that get work: at least X::kLeast units each (two in the kernel of few
+// rows, so that a CTA's first loads and its join are spread over more than one
+// round of groups; one of the trees', which are twice as long).
 template <class X>
 __device__ __forceinline__ int64_t busy_ctas(int64_t units, int64_t grid) {
   const int64_t n = (units + X::kLeast - 1) / X::kLeast;

@@ -529,6 +529,7 @@ bsm_status bsm_paged_attention_tree(
     int32_t window, const bsm_score_mod* mod, const bsm_tensor* out,
     float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Bytes of its workspace (0 for H < 0, H_kv <= 0 or T < 0). */
 size_t bsm_paged_attention_tree_workspace_bytes(int32_t H, int32_t H_kv,
                                                 int32_t T, int32_t D);
 
