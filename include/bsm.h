@@ -484,6 +484,9 @@ bsm_status bsm_kv_append(const bsm_kv_cache* cache, const int32_t* page_table,
  *   workspace   device, >= bsm_paged_attention_workspace_bytes() bytes,
  *               16-byte aligned; its contents do not matter.  Two calls that
  *               may run at once need separate ones
+ * A key's weight goes to the values as f16: it is off by up to 2^-11 of itself,
+ * or 2^-28 of the row's largest weight where that is more (the logsumexp has the
+ * whole weights).
  * A row that sees no key (lens[b] = 0, or T > lens[b]) gets out = 0 and lse =
  * -inf.  On the device, a length outside [0, max_pages * page_size] is cut to
  * it, tokens of a page outside [0, num_pages) count as masked, and both are

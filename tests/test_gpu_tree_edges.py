@@ -5,7 +5,7 @@ test_gpu_tree.py)."""
 import pytest
 import torch
 
-import block_sparse_masked_build_gb300 as bsm  # noqa: F401  (builds)
+import block_sparse_masked_build_gb300 as bsm
 from test_gpu_kv_cache import check, status
 from test_gpu_tree import _case, _run, _want
 
@@ -81,3 +81,42 @@ def test_any_bits_and_a_window(H, T, window):
     later = d["bits"] & (depth[:, None, :] - depth[:, :, None] >= window)
     assert T == 2 or bool(later.any())
     _same(_run(d), _want(d))
+
+
+@pytest.mark.parametrize("drafts", [False, True])
+@pytest.mark.parametrize("D,G", [(64, 8), (128, 40), (128, 200)])
+def test_weights_far_below_the_largest(D, G, drafts):
+    """A row's first key weighs 1 and has values of 0, its second 2^-w with
+    values of 1 (in units whose scale is 1/64 to 4 of the first's): what is left
+    of 2^-w is within 2^-28, beside f16's 2^-11 and bf16's 2^-8 of itself."""
+    page = 16
+    w = torch.arange(G).double() * 40 / G
+    q = torch.zeros(1, G, 1, D)
+    q[0, :, 0, 0] = w * 0.6931471805599453
+    q = q.bfloat16()
+    k = torch.zeros(2, 1, page, D)
+    k[0, :, 0, 0] = 1.0
+    v = torch.zeros(2, 1, page, D)
+    v[1, :, 0] = 1.0
+    ones = torch.ones(2, 1)
+    table = torch.tensor([[0, 1]], dtype=torch.int32)
+    lens = torch.tensor([page + 1], dtype=torch.int32)
+    k[0, :, 1:, 0] = -448.0  # the keys between the two: next to no weight
+    more = dict(tree=torch.ones(1, 1, dtype=torch.int32).cuda()) if drafts \
+        else {}
+    for unit in (2.0 ** -6, 1.0, 4.0):
+        vs = ones.clone()
+        vs[1] = unit
+        cache = bsm.KVCache(*[t.cuda() for t in (
+            k.to(torch.float8_e4m3fn), v.to(torch.float8_e4m3fn), ones, vs)])
+        out, lse = bsm.paged_attention(q.cuda(), cache, table.cuda(),
+                                       lens.cuda(), scale=1.0, **more)
+        x = q[0, :, 0, 0].double()
+        total = 1 + torch.exp(-x) + 15 * torch.exp(-449 * x)
+        want = (torch.exp(-x) / total * unit)[:, None]
+        err = (out[0, :, 0].double().cpu() - want).abs()
+        tol = want * (2.0 ** -8 * (1 + 2.0 ** -7) + 2.0 ** -10) \
+            + 2.0 ** -28 * unit
+        assert bool((err <= tol).all()), float((err - tol).max())
+        rel = (lse[0, :, 0].double().cpu() - x - torch.log(total)).abs()
+        assert float(rel.max()) <= 1e-4
