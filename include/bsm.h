@@ -571,7 +571,9 @@ typedef struct bsm_positions {
 
 /* Root-mean-square norm of each head's row: x -> w x / sqrt(mean(x^2) + eps),
  * w of the queries' rows and of the keys' ([D], device, f32, or bf16 with
- * weights_bf16; NULL = ones); eps >= 0.  Sums are f32: |x| up to 2^59. */
+ * weights_bf16; NULL = ones); eps >= 0.  Sums are f32: |x| up to 2^59 and, where
+ * eps does not outweigh it (as 0 does not), a row's largest from 2^-59 on.  A row
+ * of zeros with an eps of 0 is NaN, as the formula is. */
 typedef struct bsm_head_norm {
   const void* q_weight;
   const void* k_weight;
