@@ -843,18 +843,17 @@ __device__ __forceinline__ void attend_run(const PagedParams& p, uint8_t* smem,
 #pragma unroll
           for (int d = 4; d < 32; d *= 2)
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-          if (mx > m[nt][c]) {
-            const float alpha = ex2_approx(m[nt][c] - mx);  // 0 from -inf
-            m[nt][c] = mx;
-            l[nt][c] *= alpha;
+          // (selected, not branched on: the lanes stay together)
+          const bool more = mx > m[nt][c];
+          const float alpha = more ? ex2_approx(m[nt][c] - mx) : 1.f;
+          m[nt][c] = more ? mx : m[nt][c];
+          l[nt][c] *= alpha;
 #pragma unroll
-            for (int d = 0; d < kSteps; ++d) {
-              o[nt][d][c] *= alpha;
-              o[nt][d][c + 2] *= alpha;
-            }
+          for (int d = 0; d < kSteps; ++d) {
+            o[nt][d][c] *= alpha;
+            o[nt][d][c + 2] *= alpha;
           }
         }
-      __syncwarp();
     }
     // ---- the value scale: o is kept in units of v_ref / kPUp, and a
     // group's scale multiplies p while it is within 2^6 of v_ref; past that o
