@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kAppendThreads, NCH <= 8 ? 8 : 4)
 // the rounding to e4m3.  A token's row lies in D / 16 neighbouring lanes,
 // sixteen elements each, the two elements of a rotated pair in one lane: the
 // only exchange is the norm's sum.  8 prompts of 500-2048 tokens, 8 heads of 128:
-// 31 us (eight elements a lane, partners exchanged and every angle worked out
+// 27-35 us (eight elements a lane, partners exchanged and every angle worked out
 // twice, took 7 us more at the same angles' cost); one token for each of 64
 // sequences 10, 20-48 drafts for 16 of them 9.  The prompts' 63 MB would take 9
 // us: bound by instructions, which issue in 67 % of the cycles, half of them the

@@ -15,9 +15,14 @@
 // Bound by memory: 4 bytes per element forward, 6 backward.  Measured, norm and
 // rotation: a prompt of 8192 tokens, 32/8 heads of 128, 30.5 us (5.5 TB/s of a
 // copy's 6.8); 2 x 16 heads of 8192 tokens, queries and keys, forward and
-// backward 117 us (5.7 TB/s); one token for 8 sequences 7.5 us, the launch and a
-// round trip.  Instructions issue in two thirds of the cycles, the most of what
+// backward 117 us (5.7 TB/s); one token for 8 sequences 7.5-11 us, the launch and
+// a round trip.  Instructions issue in two thirds of the cycles, the most of what
 // is left between these and the copy's rate.
+// With few key heads lanes idle: a token's groups of queries and of keys share a
+// warp and run the longer of their counts, and the backward's key blocks have a
+// job's angles for one head each.  8192 tokens, 4 x 8/1 heads: forward 64 % of the
+// copy's rate, backward 58 %; 2 x 16/2: 77 and 71 %; 32/8: 84 and 86 %.  Rotation
+// alone: 80-90 % forward, 59 (8/1) to 84 % (16/16) backward.
 #include <algorithm>
 #include <cstdint>
 

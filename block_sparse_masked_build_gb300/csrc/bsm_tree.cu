@@ -33,13 +33,14 @@
 // TMEM columns: S and P [0, 128) and [128, 256), by turns with one tile, one
 // for each of two; O [256, 256 + D), of a second tile from 384 on.
 //
-// Measured (32/8 heads of 128): 32 sequences of 300-12000 tokens, 7-16 drafts,
-// one tile, 149-156 us (2.7 TB/s: the conversion and the chain from S over the
-// softmax to P take ~2300 cycles per 128 tokens, the tensor pipe is active in 28
-// %); 16 sequences of 2000-12000 tokens, 64 drafts, two tiles, 152-179 us
-// (650-780 TFLOP/s, ~5000 cycles per 128 tokens); 2 sequences of 100000-131072
-// tokens, 25 drafts, 153-164 us, with capped scores, which pass through registers
-// once more, 243-264.
+// Measured over several boxes (32/8 heads of 128): 32 sequences of 300-12000
+// tokens, 7-16 drafts, one tile, 149-171 us (2.4-2.7 TB/s: the conversion and the
+// chain from S over the softmax to P take ~2300 cycles per 128 tokens, the tensor
+// pipe is active in 28-31 %); 16 sequences of 2000-12000 tokens, 64 drafts, two
+// tiles, 152-179 us (650-780 TFLOP/s, ~5000 cycles per 128 tokens); 2 sequences of
+// 100000-131072 tokens, 25 drafts, 144-164 us, with capped scores, which pass
+// through registers once more, 243-264.  A bias costs as much as a cap: the first
+// two 235 and 224 (cap 50: 271 and 266), on a box where they took 168 and 167.
 //
 // A step's tokens go from a run's end to its start: the drafts come first, and
 // with a bias that falls with the distance the maximum is met early.
@@ -66,7 +67,8 @@ constexpr int kTcSteps = 8;     // ring of steps
 constexpr uint32_t kTcTmem = 512;
 // Up to so many query rows per key/value head go to the kernel of single tokens,
 // which reads the cache once for each 16: 32 sequences of 300-12000 tokens with 8
-// rows took it 94 us (this one 167), with 16 142 (170), with 24 246 (172).
+// rows took it 94 us (this one 167), with 16 130 (170), with 24 246 (172).  (One
+// sequence of 2000 tokens with 32 rows: 21.9 us, this one 24.4.)
 constexpr int kTreeFewRows = 16;
 constexpr int kRolePlan = 1, kRoleMma = 2, kRoleConvert = 3, kRoleScore = 4,
               kRoleLoad = 5;
