@@ -602,15 +602,24 @@ class Rope:
 
     def __init__(self, dim: int, base: float = 10000.0, *, inv_freq=None,
                  axes=None, interleaved: bool = False):
-        dim = int(dim)
+        def whole(x):
+            if int(x) != x:
+                raise ValueError("dim and axes must be whole numbers")
+            return int(x)
+
+        dim = whole(dim)
+        if not 0 < dim <= 128:  # (ahead of the lists of that size)
+            raise ValueError("dim must be a multiple of 16 from 16 to 128")
         half = dim // 2
         if inv_freq is None:
             inv_freq = [float(base) ** (-2.0 * i / dim) for i in range(half)]
         freq = [float(f) for f in inv_freq]
-        axis = [0] * half if axes is None else [int(i) for i in axes]
+        axis = [0] * half if axes is None else [whole(i) for i in axes]
         if len(freq) != half or len(axis) != half:
             raise ValueError(f"inv_freq and axes must have dim / 2 = {half} "
                              "elements")
+        if not all(0 <= a <= 3 for a in axis):
+            raise ValueError("axes must be from 0 to 3")
         self._struct = RopeStruct()
         _check(_lib.lib().bsm_rope_init(
             self._struct, dim, bool(interleaved),

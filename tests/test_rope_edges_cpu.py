@@ -1,5 +1,5 @@
-"""Rotations without a GPU: copies of a Rope, the turns it holds, and results in
-place of their inputs."""
+"""Rotations without a GPU: copies of a Rope, the turns it holds, what it refuses,
+and results in place of their inputs."""
 
 import copy
 import ctypes
@@ -8,6 +8,7 @@ import pickle
 from decimal import Decimal, localcontext
 
 import pytest
+import torch
 
 import block_sparse_masked_build_gb300 as bsm
 from block_sparse_masked_build_gb300 import _lib, api
@@ -82,3 +83,21 @@ def test_in_place_needs_the_inputs_strides(which, backward):
     kw[which + "o"] = _view(0x900000, 4096, 64, 1024)
     assert call() == _lib.BSM_ERR_INVALID_ARG and "place" in _lib.last_error()
     assert call(S=0) == 0
+
+
+@pytest.mark.parametrize("args", [
+    dict(dim=1 << 40), dict(dim=-64), dict(dim=0), dict(dim=144),
+    dict(dim=64.5), dict(dim=64, axes=[0.5] * 32),
+    dict(dim=64, axes=[0, 1.25] * 16), dict(dim=64, axes=[1 << 32] * 32),
+    dict(dim=64, axes=[-1] * 32)])
+def test_sizes_and_axes_that_are_none(args):
+    """Refused before anything of that size is made, and not cut to whole
+    numbers."""
+    with pytest.raises((ValueError, bsm.BsmError)):
+        bsm.Rope(**args)
+
+
+def test_whole_numbers_of_any_type():
+    r = bsm.Rope(64.0, axes=torch.tensor([0.0, 1.0] * 16))
+    assert (r.dim, r.axes) == (64, 2)
+    assert bytes(r._struct) == bytes(bsm.Rope(64, axes=[0, 1] * 16)._struct)
